@@ -323,6 +323,99 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
                        int D, uint16_t* y, void* stream);
 
 /* ----------------------------------------------------------------------------
+ * Paged key/value cache held in 4 bits, and the attention of new tokens over
+ * it: the serving form of the causal attention above. Rows are tokens packed
+ * request by request ([N][heads][D]); a request's cached tokens live in pages
+ * of page_size tokens named by its row of a block table, in the order they
+ * were appended. A dropped key (QK-sparse attention, scfa_qk_select) is
+ * simply not cached: every cached token of a request precedes its later
+ * tokens, so the causal mask of a query token is one number, vis: the count of
+ * the request's cached tokens it sees, itself included when it was kept.
+ *
+ * Types: bf16 or fp16 rows (SCFA_DTYPE_*), D = 64 or 128, page_size 16, 32,
+ * 64, 128 or 256. Row tensors of N tokens take a stride in elements per token
+ * and per head (channels contiguous, strides multiples of 8, pointers 16-byte
+ * aligned), so views of a fused projection need no copy. n_pages * page_size
+ * and N are below 2^31; byte offsets are 64-bit.
+ *
+ * The cache is a uint8 array [n_pages][Hkv][scfa_cache4_page_bytes], 16-byte
+ * aligned. A group is 32 consecutive channels of one row of K or V and holds
+ * codes c in -7..7 and a scale s: value = c s.
+ *   a = max |x| of the group (a NaN counts as 0); s = min(a / 7, 9216) rounded
+ *   to four significant bits (ties to even), at least 2^-15; c = x / s rounded
+ *   to the nearest whole number (ties to even), within -7..7; NaN gives 0. So
+ *   |value| <= 64512, larger magnitudes saturate, and c s has at most seven
+ *   significant bits: every value is exact in bf16 and in fp16.
+ *   The scale is one byte b: s = (1 + (b & 7) / 8) 2^((b >> 3) - 15); a code
+ *   is stored as c + 8 in four bits. Every byte pattern is a finite value, so
+ *   what earlier requests left in a page can not spoil a sum it is masked from.
+ * A page of one head is a run of tiles of 16 tokens; with G = D / 32 a tile is
+ *   K codes  [16 tokens][4 j][G g] 32-bit words: channels 32 g + 8 j + i, the
+ *            channel i = 0 2 4 6 1 3 5 7 in bits 0-3, 4-7, ..., 28-31;
+ *   V codes  [2 u][8 r][4 w][2 b][G g] 16-bit words: token 8 u + 2 w + b,
+ *            channels 32 g + 4 r + i, i = 0..3 in bits 0-3, ..., 12-15;
+ *   K scales [16 tokens][G], V scales [16 tokens][G], one byte each:
+ * the order in which the attention's matrix instructions take them.
+ *
+ * scfa_cache4_plan: block tables and slots of the next step. len [R]: cached
+ *   tokens of each request; new_len [R]: its new tokens (0 allowed); keep [N]
+ *   uint8 or NULL: nonzero = the token's key and value are cached; free_pages
+ *   [n_pages]: a stack of free page ids, n_free [1] its height; table
+ *   [R][max_pages]: the page of every page_size cached tokens. Pages are taken
+ *   from the top of the stack, request by request, and written behind a
+ *   request's pages in table, the rest of which is left as it is. Outputs:
+ *   q_start [R + 1], the sums of new_len; for the tokens below q_start[R]
+ *   slot = page * page_size + place in it (-1: dropped) and vis, for those
+ *   up to N -1 and 0; len_out [R] and n_free_out [1], which may be len and
+ *   n_free themselves. A request is released by pushing its pages on the stack and setting its
+ *   len to 0. The status word reads SCFA_ERR_INVALID for a negative length,
+ *   sum(new_len) > N, more than max_pages pages in a request, or n_free
+ *   outside [0, n_pages], SCFA_ERR_WORKSPACE when there are too few free
+ *   pages: then nothing is taken, table, len and n_free stay, and q_start and vis are
+ *   all 0 and slot all -1. A page id outside [0, n_pages) gives slots of
+ *   -1 and SCFA_ERR_INVALID.
+ * scfa_cache4_append: quantises the rows k, v [N][Hkv][D] into their slots.
+ *   A slot outside [0, n_pages * page_size) is skipped. Slots must be
+ *   distinct.
+ * scfa_cache4_read: k, v [N][Hkv][D] = the values of the slots' rows (zero
+ *   rows for a slot outside the cache).
+ * scfa_cache4_attn: for each token t of request r, q_start[r] <= t <
+ *   q_start[r + 1], and query head h, over the first vis[t] cached tokens of r
+ *   (head h / (Hq / Hkv)): o = softmax(scale q K^T) V, lse = its natural-log
+ *   denominator; vis[t] = 0 gives o = 0, lse = -inf. vis must not decrease
+ *   within a request. q, o [N][Hq][D], lse [N][Hq] fp32; Hq a multiple of
+ *   Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
+ *   outside [0, n_pages) within a request's visible pages is skipped, its
+ *   keys masked, and raises SCFA_ERR_INVALID in the status word.
+ *   flags: SCFA_FLAG_DEBUG_SYNC, SCFA_FLAG_DEBUG_STALL.
+ * ------------------------------------------------------------------------- */
+enum { SCFA_DTYPE_BF16 = 0, SCFA_DTYPE_F16 = 1 };
+
+/* bytes of one page of one head: page_size * (D + D / 16); 0 on bad sizes */
+size_t scfa_cache4_page_bytes(int page_size, int D);
+size_t scfa_cache4_plan_workspace_size(int N, int R);
+size_t scfa_cache4_attn_workspace_size(int N, int R, int Hq, int Hkv, int D);
+scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const uint8_t* keep,
+                             const int32_t* free_pages, const int32_t* n_free, int32_t* table,
+                             int N, int R, int max_pages, int page_size, int n_pages,
+                             int32_t* len_out, int32_t* n_free_out, int32_t* q_start,
+                             int32_t* slot, int32_t* vis, void* ws, size_t ws_bytes, void* stream);
+scfa_status scfa_cache4_append(const uint16_t* k, long long k_token, long long k_head,
+                               const uint16_t* v, long long v_token, long long v_head,
+                               const int32_t* slot, int N, int Hkv, int D, int dtype,
+                               uint8_t* cache, int page_size, int n_pages, void* stream);
+scfa_status scfa_cache4_read(const uint8_t* cache, int page_size, int n_pages, const int32_t* slot,
+                             int N, int Hkv, int D, int dtype,
+                             uint16_t* k, long long k_token, long long k_head,
+                             uint16_t* v, long long v_token, long long v_head, void* stream);
+scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_head,
+                             const uint8_t* cache, int page_size, int n_pages,
+                             const int32_t* table, int max_pages, const int32_t* q_start,
+                             const int32_t* vis, int N, int R, int Hq, int Hkv, int D, float scale,
+                             int dtype, uint16_t* o, long long o_token, long long o_head, float* lse,
+                             void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ----------------------------------------------------------------------------
  * Tile metadata and the live-tile work list (page section "SCFA 解决方案":
  * tile pruning of part 1, bucket and causal pruning of part 2). Normally run
  * inside the attention calls; exposed for inspection and tests. Writes into

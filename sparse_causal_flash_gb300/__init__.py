@@ -23,6 +23,7 @@ MODE_DENSE, MODE_QK, MODE_HASH = 0, 1, 2
 FLAG_NO_PRUNE, FLAG_VALIDATE, FLAG_DEBUG_SYNC, FLAG_REUSE_TILES, FLAG_ORIGINAL_ORDER = 1, 2, 4, 8, 16
 FLAG_KEEP_O32, FLAG_DEBUG_STALL, FLAG_GATHER_Q, FLAG_GATHER_KV = 32, 64, 128, 256
 TILE = 128
+DTYPE_BF16, DTYPE_F16 = 0, 1
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "workspace", 4: "CUDA error", 5: "device timeout"}
 
 
@@ -37,6 +38,7 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
 _U = ctypes.c_uint
+_L = ctypes.c_longlong
 
 _SIGS = {
     "scfa_status_string": ([_I], ctypes.c_char_p),
@@ -67,6 +69,14 @@ _SIGS = {
     "scfa_count_pairs": ([_I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _S, _P, _P], _I),
     "scfa_count_chunked_pairs": ([_P, _P, _P, _P, _I, _I, _I, _I, _P, _P], _I),
     "scfa_set_kernel_events": ([_I, _P, _P], _I),
+    "scfa_cache4_page_bytes": ([_I, _I], _S),
+    "scfa_cache4_plan_workspace_size": ([_I, _I], _S),
+    "scfa_cache4_attn_workspace_size": ([_I, _I, _I, _I, _I], _S),
+    "scfa_cache4_plan": ([_P] * 6 + [_I] * 5 + [_P] * 6 + [_S, _P], _I),
+    "scfa_cache4_append": ([_P, _L, _L, _P, _L, _L, _P, _I, _I, _I, _I, _P, _I, _I, _P], _I),
+    "scfa_cache4_read": ([_P, _I, _I, _P, _I, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P], _I),
+    "scfa_cache4_attn": ([_P, _L, _L, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _L, _L, _P, _P, _S,
+                          _U, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -279,6 +289,127 @@ def lsh_unsort(y_sorted, perm, y, stream=None):
     B, H, T, D = y.shape
     _check("lsh_unsort", _lib.lsh_unsort(_ptr(y_sorted), _ptr(perm), B, H, T, y_sorted.shape[2], D, _ptr(y),
                                          _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged 4-bit cache
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def cache4_page_bytes(page_size, D) -> int:
+    """Bytes of one page of one head; the cache is uint8 [n_pages, Hkv, this]."""
+    return int(_lib.scfa_cache4_page_bytes(int(page_size), int(D)))
+
+
+def cache4_plan_workspace_size(N, R) -> int:
+    return int(_lib.scfa_cache4_plan_workspace_size(int(N), int(R)))
+
+
+def cache4_attn_workspace_size(N, R, Hq, Hkv, D) -> int:
+    return int(_lib.scfa_cache4_attn_workspace_size(int(N), int(R), int(Hq), int(Hkv), int(D)))
+
+
+def _ints(name, device, **tensors):
+    for key, (t, n) in tensors.items():
+        if t.dtype != torch.int32 or t.device != device or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name}: {key} must be a contiguous int32 tensor of {n} on {device}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+
+
+def _rows4(name, key, t, shape, dtype, device):
+    """Strides per token and head of a row tensor [N, heads, D]."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or (t.stride(2) != 1):
+        raise ValueError(f"{name}: {key} must be {dtype} {tuple(shape)} on {device} with contiguous channels, got "
+                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+    # the stride of an axis of one is never used, and may be anything
+    return (t.stride(0) if shape[0] > 1 else 0), (t.stride(1) if shape[1] > 1 else 0)
+
+
+def _cache4(name, cache, page_size, D):
+    """(pages, key heads) of a cache tensor."""
+    if (cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 3 or not cache.is_contiguous()
+            or cache.shape[2] != page_size * (D + D // 16)):
+        raise ValueError(f"{name}: cache must be a contiguous CUDA uint8 tensor [pages, heads, "
+                         f"{page_size * (D + D // 16)}], got {cache.dtype} {tuple(cache.shape)} on {cache.device}")
+    return cache.shape[0], cache.shape[1]
+
+
+def _launch(fn, device, stream, *args):
+    """Call a C entry point whose last argument is the stream, with `device` current."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(fn, device, stream, *args)
+    st = torch.cuda.current_stream(device) if stream is None else stream
+    _check(fn, getattr(_lib, fn)(*args, st.cuda_stream))
+
+
+def scfa_cache4_plan(len_, new_len, keep, free_pages, n_free, table, page_size, n_pages, len_out, n_free_out, q_start,
+                     slot, vis, ws, stream=None):
+    """Block tables and slots of the next step (all int32 CUDA tensors; keep
+    [N] uint8 or None): len_, new_len, len_out [R]; free_pages [n_pages];
+    n_free, n_free_out [1]; table [R, max_pages]; q_start [R + 1]; slot, vis
+    [N]. len_out / n_free_out may be len_ / n_free."""
+    R, N, dev = len_.numel(), slot.numel(), table.device
+    if not table.is_cuda or table.dim() != 2:
+        raise ValueError(f"scfa_cache4_plan: table must be a CUDA tensor [R, max_pages], got {tuple(table.shape)}")
+    _ints("scfa_cache4_plan", dev, len=(len_, R), new_len=(new_len, R), free_pages=(free_pages, n_pages),
+          n_free=(n_free, 1), table=(table, R * table.shape[1]), len_out=(len_out, R), n_free_out=(n_free_out, 1),
+          q_start=(q_start, R + 1), slot=(slot, N), vis=(vis, N))
+    if keep is not None and (keep.dtype != torch.uint8 or keep.device != dev or keep.numel() != N
+                             or not keep.is_contiguous()):
+        raise ValueError(f"scfa_cache4_plan: keep must be a contiguous uint8 tensor of {N} on {dev}")
+    _launch("scfa_cache4_plan", dev, stream, len_.data_ptr(), new_len.data_ptr(),
+            None if keep is None else keep.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), table.data_ptr(), N, R,
+            table.shape[1], page_size, n_pages, len_out.data_ptr(), n_free_out.data_ptr(), q_start.data_ptr(),
+            slot.data_ptr(), vis.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def scfa_cache4_append(k, v, slot, cache, page_size, stream=None):
+    """Quantise the rows k, v [N, Hkv, D] (bf16 or fp16; any token and head
+    strides that are multiples of 8) into their slots of the cache."""
+    N, H, D = k.shape
+    P, Hkv = _cache4("scfa_cache4_append", cache, page_size, D)
+    dev = cache.device
+    dt = _DTYPES.get(k.dtype, -1)
+    shape = (N, Hkv, D)
+    kt, kh = _rows4("scfa_cache4_append", "k", k, shape, k.dtype, dev)
+    vt, vh = _rows4("scfa_cache4_append", "v", v, shape, k.dtype, dev)
+    _ints("scfa_cache4_append", dev, slot=(slot, N))
+    _launch("scfa_cache4_append", dev, stream, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slot.data_ptr(), N, Hkv, D,
+            dt, cache.data_ptr(), page_size, P)
+
+
+def scfa_cache4_read(cache, page_size, slot, k_out, v_out, stream=None):
+    """k_out, v_out [N, Hkv, D] = the values of the slots' rows (zero rows for slots outside the cache)."""
+    N, H, D = k_out.shape
+    P, Hkv = _cache4("scfa_cache4_read", cache, page_size, D)
+    dev = cache.device
+    dt = _DTYPES.get(k_out.dtype, -1)
+    shape = (N, Hkv, D)
+    kt, kh = _rows4("scfa_cache4_read", "k_out", k_out, shape, k_out.dtype, dev)
+    vt, vh = _rows4("scfa_cache4_read", "v_out", v_out, shape, k_out.dtype, dev)
+    _ints("scfa_cache4_read", dev, slot=(slot, N))
+    _launch("scfa_cache4_read", dev, stream, cache.data_ptr(), page_size, P, slot.data_ptr(), N, Hkv, D, dt,
+            k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh)
+
+
+def scfa_cache4_attn(q, cache, page_size, table, q_start, vis, scale, o, lse, ws, flags=0, stream=None):
+    """Attention of the new tokens q [N, Hq, D] over their requests' cached
+    tokens: token t of request r (q_start[r] <= t < q_start[r + 1]) sees the
+    first vis[t] of them. o [N, Hq, D], lse [N, Hq] fp32."""
+    N, Hq, D = q.shape
+    P, Hkv = _cache4("scfa_cache4_attn", cache, page_size, D)
+    dev = cache.device
+    dt = _DTYPES.get(q.dtype, -1)
+    shape = (N, Hq, D)
+    qt, qh = _rows4("scfa_cache4_attn", "q", q, shape, q.dtype, dev)
+    ot, oh = _rows4("scfa_cache4_attn", "o", o, shape, q.dtype, dev)
+    R, mp = table.shape
+    _ints("scfa_cache4_attn", dev, table=(table, R * mp), q_start=(q_start, R + 1), vis=(vis, N))
+    if lse.dtype != torch.float32 or lse.device != dev or lse.shape != (N, Hq) or not lse.is_contiguous():
+        raise ValueError(f"scfa_cache4_attn: lse must be a contiguous fp32 tensor ({N}, {Hq}) on {dev}")
+    _launch("scfa_cache4_attn", dev, stream, q.data_ptr(), qt, qh, cache.data_ptr(), page_size, P, table.data_ptr(), mp,
+            q_start.data_ptr(), vis.data_ptr(), N, R, Hq, Hkv, D, scale, dt, o.data_ptr(), ot, oh, lse.data_ptr(),
+            ws.data_ptr(), ws.numel(), flags)
 
 
 # ---------------------------------------------------------------- tiles

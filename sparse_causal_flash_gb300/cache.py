@@ -1,0 +1,102 @@
+"""Serving steps over the paged 4-bit key/value cache, composed from C-ABI calls.
+
+KVCache4 owns the pages, block tables and workspaces of a fixed number of
+request rows; step() plans the new tokens' slots on the GPU, quantises their
+keys and values into the pages and attends over what each token sees. Nothing
+is read back on the host, so a step can be captured as one CUDA graph and
+replayed for as long as its inputs keep their shapes. Keys dropped by a keep
+mask (QK-sparse attention) take no room: the cache holds the kept ones.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (cache4_attn_workspace_size, cache4_page_bytes, cache4_plan_workspace_size, scfa_cache4_append,
+               scfa_cache4_attn, scfa_cache4_plan, scfa_cache4_read, scfa_get_device_status, workspace)
+
+
+class KVCache4:
+    """Pages, tables and the launch sequence of serving steps for R request rows."""
+
+    def __init__(self, R: int, n_pages: int, Hq: int, Hkv: int, D: int, max_len: int, max_tokens: int,
+                 page_size: int = 64, dtype=torch.bfloat16, device="cuda"):
+        """R request rows share n_pages pages of page_size tokens; a request
+        caches at most max_len tokens, a step brings at most max_tokens new
+        ones over all requests."""
+        nbytes = cache4_page_bytes(page_size, D)
+        if nbytes == 0:
+            raise ValueError(f"KVCache4: head dimension {D} or page size {page_size} is not supported")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"KVCache4: rows are bf16 or fp16, not {dtype}")
+        if Hkv < 1 or Hq % Hkv != 0:
+            raise ValueError(f"KVCache4: {Hq} query heads are no multiple of {Hkv} key heads")
+        dev = torch.device(device)
+        self.device, self.dtype = dev, dtype
+        self.R, self.n_pages, self.Hq, self.Hkv, self.D, self.page_size = R, n_pages, Hq, Hkv, D, page_size
+        self.max_len, self.max_tokens = max_len, max_tokens
+        max_pages = -(-max_len // page_size)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.cache = torch.zeros((n_pages, Hkv, nbytes), dtype=torch.uint8, device=dev)
+        self.len = torch.zeros(R, **i32)
+        self.table = torch.full((R, max_pages), -1, **i32)
+        # a stack: page 0 on top
+        self.free = torch.arange(n_pages - 1, -1, -1, **i32)
+        self.n_free = torch.full((1,), n_pages, **i32)
+        self.q_start = torch.zeros(R + 1, **i32)
+        self.slot = torch.empty(max_tokens, **i32)
+        self.vis = torch.empty(max_tokens, **i32)
+        self.o = torch.zeros((max_tokens, Hq, D), dtype=dtype, device=dev)
+        self.lse = torch.zeros((max_tokens, Hq), dtype=torch.float32, device=dev)
+        self.ws_plan = workspace(cache4_plan_workspace_size(max_tokens, R), dev)
+        self.ws_attn = workspace(cache4_attn_workspace_size(max_tokens, R, Hq, Hkv, D), dev)
+
+    def step(self, q, k, v, new_len, scale, keep=None, stream=None):
+        """One serving step: new_len [R] int32 new tokens of each request, packed
+        request by request in q [N, Hq, D], k, v [N, Hkv, D] (N at most
+        max_tokens; the sum of new_len may be smaller), keep [N] uint8 or
+        None. Returns views of o [N, Hq, D] and lse [N, Hq], whose rows from
+        the sum of new_len on are left as they were. A step that does not fit
+        (status()) caches nothing and computes nothing."""
+        N = q.shape[0]
+        if N > self.max_tokens:
+            raise ValueError(f"KVCache4.step: {N} token rows, room for {self.max_tokens}")
+        slot, vis, o, lse = self.slot[:N], self.vis[:N], self.o[:N], self.lse[:N]
+        scfa_cache4_plan(self.len, new_len, keep, self.free, self.n_free, self.table, self.page_size, self.n_pages,
+                         self.len, self.n_free, self.q_start, slot, vis, self.ws_plan, stream)
+        scfa_cache4_append(k, v, slot, self.cache, self.page_size, stream)
+        scfa_cache4_attn(q, self.cache, self.page_size, self.table, self.q_start, vis, scale, o, lse, self.ws_attn, 0,
+                         stream)
+        return o, lse
+
+    def capture(self, q, k, v, new_len, scale, keep=None):
+        """The step on these input tensors as a CUDA graph; each replay() is
+        one more step. They must stay alive and in place. Nothing is run: the
+        cache is as before."""
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.device(self.device), torch.cuda.graph(g):
+            self.step(q, k, v, new_len, scale, keep)
+        return g
+
+    def rows(self, request: int):
+        """(k, v) [tokens, Hkv, D]: the values the cache holds of a request (reads its length back)."""
+        n = int(self.len[request])
+        shape = (max(n, 1), self.Hkv, self.D)
+        k = torch.empty(shape, dtype=self.dtype, device=self.device)
+        v = torch.empty(shape, dtype=self.dtype, device=self.device)
+        t = torch.arange(max(n, 1), dtype=torch.int32, device=self.device)
+        slot = self.table[request, t // self.page_size] * self.page_size + t % self.page_size
+        scfa_cache4_read(self.cache, self.page_size, slot, k, v)
+        return k[:n], v[:n]
+
+    def release(self, request: int):
+        """Give a request's pages back (reads its length back); its row is free for another."""
+        n = -(-int(self.len[request]) // self.page_size)
+        have = int(self.n_free)
+        self.free[have:have + n] = self.table[request, :n]
+        self.n_free += n
+        self.len[request] = 0
+
+    def status(self) -> int:
+        """Status of the last step: 0, or the first error of its plan, then of its attention (synchronises)."""
+        with torch.cuda.device(self.device):
+            return scfa_get_device_status(self.ws_plan) or scfa_get_device_status(self.ws_attn)

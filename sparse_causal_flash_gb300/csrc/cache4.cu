@@ -1,0 +1,432 @@
+// The paged 4-bit key/value cache: page planning, quantising append and read.
+#include <climits>
+
+#include "cache4.cuh"
+#include "internal.h"
+
+namespace scfa {
+namespace {
+
+// ---------------------------------------------------------------- plan
+// Per request, between the request scan and the token fill.
+struct PlanReq {
+  int32_t len;    // cached tokens before this step
+  int32_t first;  // kept tokens of all requests before this one
+  int32_t kept;   // kept new tokens
+  int32_t taken;  // pages taken by the requests before this one
+};
+struct PlanArgs {
+  const int32_t *len, *new_len;
+  const uint8_t* keep;
+  const int32_t *free_pages, *n_free;
+  int32_t* table;
+  int N, R, max_pages, page_size, n_pages;
+  int32_t *len_out, *n_free_out, *q_start, *slot, *vis;
+  int* status;
+  int32_t* free_before;  // n_free as it was (n_free_out may be n_free)
+  PlanReq* req;
+};
+
+// exclusive sum over the block; *total gets the sum. `part`: 33 entries.
+__device__ __forceinline__ long long block_excl(long long x, long long* part, long long* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  long long s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  if (lane == 31) part[w] = s;
+  __syncthreads();
+  if (w == 0) {
+    long long p = lane < nw ? part[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += y;
+    }
+    part[lane] = p;
+  }
+  __syncthreads();
+  const long long before = w > 0 ? part[w - 1] : 0;
+  *total = part[nw - 1];
+  __syncthreads();
+  return before + s - x;
+}
+
+// Slot, vis and a fresh table entry of token t. vis[t] holds the number of
+// kept tokens before t when there is a keep mask.
+__device__ __forceinline__ void plan_token(const PlanArgs& a, int t) {
+  const int total = a.q_start[a.R];
+  if (t >= total) {
+    a.slot[t] = -1;
+    a.vis[t] = 0;
+    return;
+  }
+  int lo = 0, hi = a.R;  // the last request that starts at or before t and is not empty
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_start[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const PlanReq q = a.req[lo];
+  const bool keep = a.keep == nullptr || a.keep[t] != 0;
+  const int upto = a.keep == nullptr ? t : a.vis[t];
+  const int pos = q.len + upto - q.first;
+  int slot = -1;
+  if (keep) {
+    const int pg = pos / a.page_size, have = (q.len + a.page_size - 1) / a.page_size;
+    const long long row = static_cast<long long>(lo) * a.max_pages;
+    int page;
+    if (pg < have) {
+      page = a.table[row + pg];
+    } else {
+      page = a.free_pages[*a.free_before - 1 - (q.taken + pg - have)];
+      if (pos % a.page_size == 0) a.table[row + pg] = page;
+    }
+    if (page >= 0 && page < a.n_pages) slot = page * a.page_size + pos % a.page_size;
+    else raise_status(a.status, SCFA_ERR_INVALID);
+  }
+  a.slot[t] = slot;
+  a.vis[t] = pos + (keep ? 1 : 0);
+}
+
+// One CTA: kept-token prefix, sums over the requests, the checks, the new
+// state; with fill also the tokens (few of them). Latency bound: the requests
+// and tokens of a decode step fit one CTA's threads once.
+__global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
+  __shared__ long long part[33];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  if (tid == 0) s_bad = 0;
+  long long kept_all = 0;
+  if (a.keep != nullptr) {
+    for (int base = 0; base < a.N; base += nt) {
+      const int t = base + tid;
+      const int k = t < a.N && a.keep[t] != 0;
+      long long sum;
+      const long long before = block_excl(k, part, &sum);
+      if (t < a.N) a.vis[t] = static_cast<int32_t>(kept_all + before);
+      kept_all += sum;
+    }
+  }
+  __syncthreads();
+  const int n_free = *a.n_free;
+  long long tokens = 0, taken = 0;
+  for (int base = 0; base < a.R; base += nt) {
+    const int r = base + tid;
+    const bool in = r < a.R;
+    const int len = in ? a.len[r] : 0, n = in ? a.new_len[r] : 0;
+    bool bad = len < 0 || n < 0;
+    long long sum;
+    const long long start = tokens + block_excl(bad ? 0 : n, part, &sum);
+    tokens += sum;
+    const long long end = start + (bad ? 0 : n);
+    long long first = start, last = end;
+    if (a.keep != nullptr) {
+      first = start < a.N ? a.vis[start] : kept_all;
+      last = end < a.N ? a.vis[end] : kept_all;
+    }
+    const long long kept = last - first;
+    const long long have = (static_cast<long long>(len) + a.page_size - 1) / a.page_size;
+    const long long then = (len + kept + a.page_size - 1) / a.page_size;
+    bad = bad || end > a.N || then > a.max_pages;
+    const long long before = taken + block_excl(bad ? 0 : then - have, part, &sum);
+    taken += sum;
+    if (in) {
+      a.req[r] = {len, static_cast<int32_t>(first), static_cast<int32_t>(kept), static_cast<int32_t>(before)};
+      a.q_start[r] = static_cast<int32_t>(start);
+      if (bad) s_bad = 1;
+    }
+  }
+  __syncthreads();
+  int err = SCFA_OK;
+  if (s_bad || n_free < 0 || n_free > a.n_pages || tokens > a.N) err = SCFA_ERR_INVALID;
+  else if (taken > n_free) err = SCFA_ERR_WORKSPACE;
+  for (int r = tid; r < a.R; r += nt) {
+    const PlanReq q = a.req[r];
+    a.len_out[r] = q.len + (err == SCFA_OK ? q.kept : 0);
+    if (err != SCFA_OK) a.q_start[r] = 0;
+  }
+  if (tid == 0) {
+    a.q_start[a.R] = err == SCFA_OK ? static_cast<int32_t>(tokens) : 0;
+    *a.free_before = n_free;
+    *a.n_free_out = n_free - (err == SCFA_OK ? static_cast<int32_t>(taken) : 0);
+    *a.status = err;
+  }
+  if (!fill) return;
+  __syncthreads();
+  for (int t = tid; t < a.N; t += nt) plan_token(a, t);
+}
+
+__global__ void __launch_bounds__(256) plan_fill_kernel(PlanArgs a) {
+  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (t < a.N) plan_token(a, static_cast<int>(t));
+}
+
+// ---------------------------------------------------------------- append / read
+struct RowArgs {
+  const uint16_t *k, *v;
+  uint16_t *k_out, *v_out;
+  long long kt, kh, vt, vh;  // strides per token and head
+  const int32_t* slot;
+  long long rows;  // N * Hkv
+  int Hkv, page_size, log_ps;
+  long long slots;  // slots of the cache
+  uint8_t* cache;
+};
+
+// Eight threads per row (one token of one head): HBM bound, the rows read
+// once and the codes written once. Thread i quantises D / 8 consecutive
+// channels of K (D / 64 words) and the channels 32 g + 4 i + 0..3 of V, which
+// is how the tile groups them, so every store is a whole word.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) append_kernel(RowArgs a) {
+  using L = C4<D>;
+  constexpr int W = D / 64;  // K words per thread
+  constexpr int G = L::kG;
+  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const int i = threadIdx.x & 7;
+  const bool in = row < a.rows;
+  const long long tok = in ? row / a.Hkv : 0;
+  const int head = static_cast<int>(in ? row - tok * a.Hkv : 0);
+  const long long slot = in ? a.slot[tok] : -1;
+  const bool live = slot >= 0 && slot < a.slots;
+  // every thread stays for the shuffles
+  uint32_t kw[4 * W], vw[2 * G];
+#pragma unroll
+  for (int x = 0; x < 4 * W; ++x) kw[x] = 0;
+#pragma unroll
+  for (int x = 0; x < 2 * G; ++x) vw[x] = 0;
+  if (live) {
+    const uint4* ks = reinterpret_cast<const uint4*>(a.k + tok * a.kt + head * a.kh + i * (8 * W));
+#pragma unroll
+    for (int x = 0; x < W; ++x) {
+      const uint4 u = ks[x];
+      kw[4 * x] = u.x, kw[4 * x + 1] = u.y, kw[4 * x + 2] = u.z, kw[4 * x + 3] = u.w;
+    }
+    const uint16_t* vs = a.v + tok * a.vt + head * a.vh + 4 * i;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint2 u = *reinterpret_cast<const uint2*>(vs + 32 * g);
+      vw[2 * g] = u.x, vw[2 * g + 1] = u.y;
+    }
+  }
+  float amax = 0.f;  // fmaxf leaves a NaN out
+#pragma unroll
+  for (int x = 0; x < 4 * W; ++x) {
+    const float2 f = c4_unpack<F16>(kw[x]);
+    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  // a group of 32 channels lies in 32 / (D / 8) threads
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  if (W == 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  float vmax[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const float2 f = c4_unpack<F16>(vw[2 * g]), h = c4_unpack<F16>(vw[2 * g + 1]);
+    vmax[g] = fmaxf(fmaxf(fmaxf(0.f, fabsf(f.x)), fabsf(f.y)), fmaxf(fabsf(h.x), fabsf(h.y)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) vmax[g] = fmaxf(vmax[g], __shfl_xor_sync(0xffffffffu, vmax[g], o));
+  }
+  if (!live) return;
+  const int at = static_cast<int>(slot & (a.page_size - 1)), t = at & 15;
+  uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, head, a.page_size, at, L::kTileBytes);
+  const uint32_t kb = c4_scale_byte(amax);
+  const float ksc = c4_scale(kb);
+#pragma unroll
+  for (int x = 0; x < W; ++x) {
+    const int word = i * W + x, g = word >> 2, j = word & 3;
+    uint32_t c = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {  // channels 2 y and 2 y + 1 of the word
+      const float2 f = c4_unpack<F16>(kw[4 * x + y]);
+      c |= c4_code(f.x, ksc) << (4 * y) | c4_code(f.y, ksc) << (4 * y + 16);
+    }
+    *reinterpret_cast<uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4) = c;
+    if (j == 0) tile[L::kKScales + t * G + g] = static_cast<uint8_t>(kb);
+  }
+  uint32_t piece[G / 2];
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const uint32_t b = c4_scale_byte(vmax[g]);
+    const float s = c4_scale(b);
+    const float2 f = c4_unpack<F16>(vw[2 * g]), h = c4_unpack<F16>(vw[2 * g + 1]);
+    const uint32_t c = c4_code(f.x, s) | c4_code(f.y, s) << 4 | c4_code(h.x, s) << 8 | c4_code(h.y, s) << 12;
+    if (g & 1) piece[g / 2] |= c << 16;
+    else piece[g / 2] = c;
+    if (i == g) tile[L::kVScales + t * G + g] = static_cast<uint8_t>(b);
+  }
+#pragma unroll
+  for (int x = 0; x < G / 2; ++x) *reinterpret_cast<uint32_t*>(tile + L::v_piece(t, i) + 4 * x) = piece[x];
+}
+
+// The reverse, with the same threads: a thread writes the channels it read
+// there.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) read_kernel(RowArgs a) {
+  using L = C4<D>;
+  constexpr int W = D / 64;
+  constexpr int G = L::kG;
+  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const int i = threadIdx.x & 7;
+  if (row >= a.rows) return;
+  const long long tok = row / a.Hkv;
+  const int head = static_cast<int>(row - tok * a.Hkv);
+  const long long slot = a.slot[tok];
+  uint16_t* ko = a.k_out + tok * a.kt + head * a.kh + i * (8 * W);
+  uint16_t* vo = a.v_out + tok * a.vt + head * a.vh + 4 * i;
+  if (slot < 0 || slot >= a.slots) {
+#pragma unroll
+    for (int x = 0; x < W; ++x) reinterpret_cast<uint4*>(ko)[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int g = 0; g < G; ++g) *reinterpret_cast<uint2*>(vo + 32 * g) = make_uint2(0u, 0u);
+    return;
+  }
+  const int at = static_cast<int>(slot & (a.page_size - 1)), t = at & 15;
+  const uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, head, a.page_size, at, L::kTileBytes);
+#pragma unroll
+  for (int x = 0; x < W; ++x) {
+    const int word = i * W + x, g = word >> 2, j = word & 3;
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4);
+    const float s = c4_scale(tile[L::kKScales + t * G + g]);
+    uint32_t w[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      w[y] = c4_pack<F16>(static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8) * s,
+                          static_cast<float>(static_cast<int>(c >> (4 * y + 16) & 15u) - 8) * s);
+    reinterpret_cast<uint4*>(ko)[x] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + L::v_piece(t, i) + 2 * g);
+    const float s = c4_scale(tile[L::kVScales + t * G + g]);
+    float f[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) f[y] = static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8) * s;
+    *reinterpret_cast<uint2*>(vo + 32 * g) = make_uint2(c4_pack<F16>(f[0], f[1]), c4_pack<F16>(f[2], f[3]));
+  }
+}
+
+constexpr int kPlanOneCta = 4096;  // tokens one CTA fills itself
+
+struct PlanWs {
+  size_t free_before = sizeof(WsHeader), req = sizeof(WsHeader) + 256, total = 0;
+};
+bool plan_ws_layout(int N, int R, PlanWs* w) {
+  if (N < 1 || R < 1) return false;
+  w->total = align_up(w->req + sizeof(PlanReq) * static_cast<size_t>(R), 256);
+  return true;
+}
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// sizes and pointers common to append and read
+scfa_status check_rows(const void* k, long long kt, long long kh, const void* v, long long vt, long long vh,
+                       const int32_t* slot, int N, int Hkv, int D, int dtype, const void* cache, int page_size,
+                       int n_pages) {
+  if (!k || !v || !slot || !cache) return SCFA_ERR_INVALID;
+  if (N < 1 || Hkv < 1 || n_pages < 1) return SCFA_ERR_INVALID;
+  if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(n_pages) * page_size >= (1ll << 31)) return SCFA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache)) return SCFA_ERR_INVALID;
+  if ((kt | kh | vt | vh) & 7) return SCFA_ERR_INVALID;
+  return SCFA_OK;
+}
+
+RowArgs row_args(long long kt, long long kh, long long vt, long long vh, const int32_t* slot, int N, int Hkv,
+                 int page_size, int n_pages, const uint8_t* cache) {
+  RowArgs a = {};
+  a.kt = kt, a.kh = kh, a.vt = vt, a.vh = vh;
+  a.slot = slot;
+  a.rows = static_cast<long long>(N) * Hkv;
+  a.Hkv = Hkv;
+  a.page_size = page_size;
+  while ((1 << a.log_ps) < page_size) ++a.log_ps;
+  a.slots = static_cast<long long>(n_pages) * page_size;
+  a.cache = const_cast<uint8_t*>(cache);
+  return a;
+}
+
+}  // namespace
+}  // namespace scfa
+
+using namespace scfa;
+
+extern "C" {
+
+size_t scfa_cache4_page_bytes(int page_size, int D) {
+  if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return 0;
+  return static_cast<size_t>(page_size) * (D + D / 16);
+}
+
+size_t scfa_cache4_plan_workspace_size(int N, int R) {
+  PlanWs w;
+  return plan_ws_layout(N, R, &w) ? w.total : 0;
+}
+
+scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const uint8_t* keep,
+                             const int32_t* free_pages, const int32_t* n_free, int32_t* table, int N, int R,
+                             int max_pages, int page_size, int n_pages, int32_t* len_out, int32_t* n_free_out,
+                             int32_t* q_start, int32_t* slot, int32_t* vis, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (!len || !new_len || !free_pages || !n_free || !table || !len_out || !n_free_out || !q_start || !slot || !vis ||
+      !ws)
+    return SCFA_ERR_INVALID;
+  if (N < 1 || R < 1 || max_pages < 1 || n_pages < 1) return SCFA_ERR_INVALID;
+  if (!c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
+      static_cast<long long>(max_pages) * page_size >= (1ll << 31))
+    return SCFA_ERR_UNSUPPORTED;
+  PlanWs w;
+  plan_ws_layout(N, R, &w);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total) return SCFA_ERR_WORKSPACE;
+  char* p = static_cast<char*>(ws);
+  const PlanArgs a = {len, new_len, keep, free_pages, n_free, table, N, R, max_pages, page_size, n_pages,
+                      len_out, n_free_out, q_start, slot, vis, reinterpret_cast<int*>(p),
+                      reinterpret_cast<int32_t*>(p + w.free_before), reinterpret_cast<PlanReq*>(p + w.req)};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int fill = N <= kPlanOneCta;
+  const int most = (fill || keep) && N > R ? N : R;  // items of the longest loop
+  const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
+  plan_kernel<<<1, threads, 0, st>>>(a, fill);
+  if (!fill) plan_fill_kernel<<<(N + 255) / 256, 256, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
+scfa_status scfa_cache4_append(const uint16_t* k, long long k_token, long long k_head, const uint16_t* v,
+                               long long v_token, long long v_head, const int32_t* slot, int N, int Hkv, int D,
+                               int dtype, uint8_t* cache, int page_size, int n_pages, void* stream) {
+  const scfa_status s =
+      check_rows(k, k_token, k_head, v, v_token, v_head, slot, N, Hkv, D, dtype, cache, page_size, n_pages);
+  if (s != SCFA_OK) return s;
+  RowArgs a = row_args(k_token, k_head, v_token, v_head, slot, N, Hkv, page_size, n_pages, cache);
+  a.k = k, a.v = v;
+  const long long grid = (a.rows + 31) / 32;
+  if (grid > INT_MAX) return SCFA_ERR_UNSUPPORTED;
+  const bool h = dtype == SCFA_DTYPE_F16;
+  auto kern = D == 64 ? (h ? append_kernel<64, true> : append_kernel<64, false>)
+                      : (h ? append_kernel<128, true> : append_kernel<128, false>);
+  kern<<<static_cast<int>(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
+scfa_status scfa_cache4_read(const uint8_t* cache, int page_size, int n_pages, const int32_t* slot, int N, int Hkv,
+                             int D, int dtype, uint16_t* k, long long k_token, long long k_head, uint16_t* v,
+                             long long v_token, long long v_head, void* stream) {
+  const scfa_status s =
+      check_rows(k, k_token, k_head, v, v_token, v_head, slot, N, Hkv, D, dtype, cache, page_size, n_pages);
+  if (s != SCFA_OK) return s;
+  RowArgs a = row_args(k_token, k_head, v_token, v_head, slot, N, Hkv, page_size, n_pages, cache);
+  a.k_out = k, a.v_out = v;
+  const long long grid = (a.rows + 31) / 32;
+  if (grid > INT_MAX) return SCFA_ERR_UNSUPPORTED;
+  const bool h = dtype == SCFA_DTYPE_F16;
+  auto kern = D == 64 ? (h ? read_kernel<64, true> : read_kernel<64, false>)
+                      : (h ? read_kernel<128, true> : read_kernel<128, false>);
+  kern<<<static_cast<int>(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,470 @@
+"""Parity of the paged 4-bit cache on the GPU against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache4 as oc
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def scfa():
+    import sparse_causal_flash_gb300 as s
+    s.load()
+    return s
+
+
+def i32(x, dev="cuda"):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).to(dev)
+
+
+def dbl(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rand(seed, shape, dt=BF, spread=0.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    if spread:
+        x = x * torch.exp(spread * torch.randn(shape[:-1] + (1,), generator=g))
+    return x.to(dt)
+
+
+def noise_cache(seed, P, H, D, ps):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(0, 256, (P, H, ps * (D + D // 16)), generator=g, dtype=torch.uint8).cuda()
+
+
+# ---------------------------------------------------------------- plan
+def run_plan(scfa, length, new, keep, free, n_free, table, N, ps, P, in_place=False):
+    R = len(length)
+    ln, nf, tb = i32(length), i32([n_free]), i32(table)
+    fr = i32(list(free) + [-1] * (P - len(free)))
+    lo, fo = (ln, nf) if in_place else (torch.full_like(ln, -7), torch.full_like(nf, -7))
+    qs, slot, vis = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for n in (R + 1, N, N))
+    ws = scfa.workspace(scfa.cache4_plan_workspace_size(N, R))
+    kp = None if keep is None else torch.as_tensor(np.asarray(keep), dtype=torch.uint8).cuda()
+    scfa.scfa_cache4_plan(ln, i32(new), kp, fr, nf, tb, ps, P, lo, fo, qs, slot, vis, ws)
+    st = scfa.scfa_get_device_status(ws)
+    return st, dict(table=tb, len=lo, n_free=fo, q_start=qs, slot=slot, vis=vis)
+
+
+def plan_problem(seed, R, lo, hi, n_hi, ps, slack=4):
+    g = np.random.default_rng(seed)
+    length, new = g.integers(lo, hi + 1, R), g.integers(0, n_hi + 1, R)
+    mp = max(1, -(-(hi + n_hi) // ps))
+    P = int(sum(-(-(int(a) + n_hi) // ps) for a in length)) + slack
+    order = g.permutation(P)
+    table, at = np.full((R, mp), -1), 0
+    for r in range(R):
+        n = -(-int(length[r]) // ps)
+        table[r, :n] = order[at:at + n]
+        at += n
+    return length, new, order[at:].tolist(), table, P
+
+
+@pytest.mark.parametrize("R,lo,hi,n_hi,ps,pad,drop", [
+    (1, 0, 0, 1, 16, 0, None), (1, 15, 15, 1, 16, 3, None), (5, 0, 40, 9, 16, 2, 0.5), (33, 0, 300, 1, 64, 7, None),
+    (64, 1, 5000, 1, 32, 0, None), (7, 0, 100, 200, 16, 5, 0.3), (3, 0, 10, 3000, 256, 1, 0.8), (2, 5, 9, 2600, 16, 0, None),
+    (1500, 0, 50, 2, 16, 9, 0.7), (1100, 0, 20, 9, 16, 40, 0.5), (40, 0, 64, 0, 16, 1, None), (12, 0, 64, 30, 16, 0, 0.0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_matches_the_oracle(scfa, R, lo, hi, n_hi, ps, pad, drop, in_place):
+    length, new, free, table, P = plan_problem(R * 7 + hi, R, lo, hi, n_hi, ps)
+    N = int(new.sum()) + pad or 1
+    keep = None if drop is None else (np.random.default_rng(3).random(N) < drop).astype(np.uint8) * 5
+    ref = oc.plan(length, new, keep, free, len(free), table, N, ps, P)
+    st, got = run_plan(scfa, length, new, keep, free, len(free), table, N, ps, P, in_place)
+    assert st == 0
+    for key, v in ref.items():
+        assert np.array_equal(got[key].cpu().numpy().reshape(np.shape(v)), v), key
+
+
+@pytest.mark.parametrize("length,new,n_free,N,code", [
+    ([3, -1], [1, 1], 4, 4, 1), ([3, 3], [1, -2], 4, 4, 1), ([3, 3], [3, 2], 4, 4, 1), ([31, 3], [2, 1], 4, 4, 1),
+    ([3, 40], [1, 1], 4, 4, 1), ([16, 16], [1, 1], 1, 4, 3), ([3, 3], [1, 1], -1, 4, 1), ([3, 3], [1, 1], 9, 4, 1),
+    ([2 ** 31 - 1, 3], [1, 1], 4, 4, 1), ([3, 3], [2 ** 31 - 1, 2 ** 31 - 1], 4, 4, 1)])
+@pytest.mark.parametrize("mask", [False, True])
+def test_plan_that_does_not_fit_changes_nothing(scfa, length, new, n_free, N, code, mask):
+    table = [[0, -1], [1, -1]]
+    keep = [1] * N if mask else None
+    st, got = run_plan(scfa, length, new, keep, [5, 4, 3, 2], n_free, table, N, 16, 8)
+    assert st == code
+    assert got["table"].tolist() == table and got["len"].tolist() == length and got["n_free"].tolist() == [n_free]
+    assert got["q_start"].tolist() == [0, 0, 0] and got["slot"].tolist() == [-1] * N and got["vis"].tolist() == [0] * N
+
+
+def test_plan_reports_page_ids_out_of_range(scfa):
+    st, got = run_plan(scfa, [3, 16], [1, 1], None, [1, 800], 2, [[-1, -1], [0, -1]], 2, 16, 8)
+    assert st == 1 and got["slot"].tolist() == [-1, -1] and got["vis"].tolist() == [4, 17]
+
+
+# ---------------------------------------------------------------- append / read
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,H,ps,strided", [(1, 1, 16, False), (3, 5, 16, True), (37, 2, 64, False), (129, 3, 256, True)])
+def test_append_then_read_matches_the_oracle(scfa, dt, D, N, H, ps, strided):
+    P = -(-N // ps) + 3
+    cache = noise_cache(N, P, H, D, ps)
+    before = cache.clone()
+    g = np.random.default_rng(N)
+    slot = g.permutation(P * ps)[:N]
+    if N > 3:
+        slot[1], slot[2] = -1, P * ps  # a dropped row and one outside the cache
+    kv = rand(N, (N, 2 * H + 3, D), dt, 2.0).cuda()
+    k, v = kv[:, 1:1 + H], kv[:, 2 + H:2 + 2 * H]
+    if not strided:
+        k, v = k.contiguous(), v.contiguous()
+    scfa.scfa_cache4_append(k, v, i32(slot), cache, ps)
+    out = torch.full((N, 2 * H, D), 3.0, dtype=dt, device="cuda")
+    ko, vo = (out[:, :H], out[:, H:]) if strided else (torch.full((N, H, D), 3.0, dtype=dt, device="cuda") for _ in "kv")
+    scfa.scfa_cache4_read(cache, ps, i32(slot), ko, vo)
+    live = ((slot >= 0) & (slot < P * ps))[:, None, None]
+    assert np.array_equal(dbl(ko), oc.values(dbl(k)) * live)
+    assert np.array_equal(dbl(vo), oc.values(dbl(v)) * live)
+    # the bytes are where the format puts them, and nothing else was written
+    flat, changed = cache.view(-1).cpu().numpy(), set()
+    for n in np.flatnonzero(live[:, 0, 0])[:4]:
+        for h in (0, H - 1):
+            assert np.array_equal(oc.row(flat, int(slot[n]), h, H, D, ps, False), oc.values(dbl(k[n, h])))
+            assert np.array_equal(oc.row(flat, int(slot[n]), h, H, D, ps, True), oc.values(dbl(v[n, h])))
+    for n in np.flatnonzero(live[:, 0, 0]):
+        for h in range(H):
+            for ch in range(D):
+                for is_v in (False, True):
+                    at, _, sc = oc.addresses(int(slot[n]), h, ch, H, D, ps, is_v)
+                    changed |= {at, sc}
+    rest = np.ones(flat.size, bool)
+    rest[list(changed)] = False
+    assert np.array_equal(flat[rest], before.view(-1).cpu().numpy()[rest])
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_append_at_the_borders(scfa, dt):
+    """Ties of scale and code, zeros, the smallest and largest numbers, NaN and infinities."""
+    D, H, ps = 64, 1, 16
+    top = 3e38 if dt is BF else 65504.0
+    rows = []
+    for m in range(128, 256):  # every significand of the largest magnitude, ties of the scale among them
+        rows.append([m / 16.0] + [(i + 0.5) * m / 112.0 for i in range(31)])
+    for s in (1.0, 1.125, 1.25, 1.875, 2.0 ** -15, 1.5 * 2.0 ** -10):  # ties of the code
+        rows.append([7 * s] + [(i / 2.0 - 7.5) * s for i in range(31)])
+    rows += [[0.0] * 32, [-0.0] * 32, [float("nan")] * 32, [float("inf"), 1.0, float("nan")] + [-3.0] * 29,
+             [-float("inf")] + [64512.0] * 31, [top] + [-top] * 31, [1e-6] * 32, [1.4e-5, 1.6e-5, -4e-5] + [0.0] * 29,
+             [5.9e-8] * 32, [64512.0, -65000.0] + [60000.0] * 30, [float("nan"), 7.0] + [0.5] * 30]
+    if len(rows) % 2:
+        rows.append([1.0] * 32)
+    x = torch.tensor(rows).to(dt).view(-1, 1, D).cuda()
+    N = x.shape[0]
+    cache = noise_cache(5, -(-N // ps), H, D, ps)
+    slot = torch.arange(N, dtype=torch.int32, device="cuda")
+    ko, vo = torch.empty_like(x), torch.empty_like(x)
+    scfa.scfa_cache4_append(x, x.flip(0), slot, cache, ps)
+    scfa.scfa_cache4_read(cache, ps, slot, ko, vo)
+    assert np.array_equal(dbl(ko), oc.values(dbl(x)))
+    assert np.array_equal(dbl(vo), oc.values(dbl(x.flip(0))))
+
+
+def test_append_and_read_past_32_bit_offsets(scfa):
+    """A cache of more than 2^32 bytes: rows at its far end."""
+    D, H, ps = 128, 8, 64
+    P = (1 << 32) // (H * ps * (D + D // 16)) + 9
+    cache = torch.zeros((P, H, ps * (D + D // 16)), dtype=torch.uint8, device="cuda")
+    slot = np.array([5, P * ps - 1, P * ps - 70, (P // 2) * ps + 3])
+    k, v = rand(1, (4, H, D)).cuda(), rand(2, (4, H, D)).cuda()
+    scfa.scfa_cache4_append(k, v, i32(slot), cache, ps)
+    ko, vo = torch.empty_like(k), torch.empty_like(v)
+    scfa.scfa_cache4_read(cache, ps, i32(slot), ko, vo)
+    assert np.array_equal(dbl(ko), oc.values(dbl(k))) and np.array_equal(dbl(vo), oc.values(dbl(v)))
+    # and attended over
+    table, qs, vis = i32([[P - 1, P - 2]]), i32([0, 1]), i32([ps + 1])
+    q, o, lse = rand(3, (1, H, D)).cuda(), torch.empty((1, H, D), dtype=BF, device="cuda"), torch.empty((1, H), device="cuda")
+    ws = scfa.workspace(scfa.cache4_attn_workspace_size(1, 1, H, H, D))
+    scfa.scfa_cache4_attn(q, cache, ps, table, qs, vis, 0.09, o, lse, ws)
+    assert scfa.scfa_get_device_status(ws) == 0
+    slots = np.concatenate([np.arange(ps) + (P - 1) * ps, [(P - 2) * ps]])
+    kk = torch.empty((ps + 1, H, D), dtype=BF, device="cuda")
+    vv = torch.empty_like(kk)
+    scfa.scfa_cache4_read(cache, ps, i32(slots), kk, vv)
+    check_rows(dbl(q), dbl(kk), dbl(vv), [ps + 1], 0.09, o, lse, BF)
+
+
+# ---------------------------------------------------------------- attention
+def check_rows(q, k, v, vis, scale, o, lse, dt):
+    """Rows q [n, Hq, D] over k, v [L, Hkv, D] (the exact values the cache holds).
+
+    Bounds. u8 = 2^-8 is half a bf16 step, uo half a step of the output type.
+    A weight p is rounded to bf16 before it meets V: at most u8 sum(p |v|) in
+    O. A score is a sum of D exact products kept as sums of q (c + 136) <= 144
+    |q| in fp32, each of the D / 8 + 2 accumulations off by at most 2^-23 of
+    144 sum |q| over its group: e = (D / 8 + 2) 2^-23 144 scale sum_g s_g
+    sum |q_g|, plus 2^-20 of a score for the products with the scales and the
+    change of base. Weights are then off by 2 e relative (numerator and
+    denominator), LSE by e; exp2 and the fp32 sums add 2^-18."""
+    uo, u8 = (2.0 ** -8 if dt is BF else 2.0 ** -11), 2.0 ** -8
+    o, lse = dbl(o), dbl(lse)
+    G, D = q.shape[1] // k.shape[1], q.shape[2]
+    for t in range(q.shape[0]):
+        for h in range(q.shape[1]):
+            n, hk = int(vis[t]), h // G
+            kk, vv = k[:n, hk], v[:n, hk]
+            ro, rl = oc.attention(q[t, h], kk, vv, scale)
+            if n == 0:
+                assert not o[t, h].any() and lse[t, h] == -np.inf
+                continue
+            # a group's scale is at most its largest value (the code of that is 7, or 0 in a zero group)
+            sg = np.abs(kk).reshape(n, -1, 32).max(-1) / 6 + 2.0 ** -15
+            qg = np.abs(q[t, h]).reshape(-1, 32).sum(-1)
+            s = np.abs(kk @ q[t, h] * scale).max()
+            e = (D / 8 + 2) * 2.0 ** -23 * 144 * scale * (sg @ qg).max() + 2.0 ** -20 * s
+            p = np.exp(kk @ q[t, h] * scale - rl)
+            a = p @ np.abs(vv)
+            assert abs(lse[t, h] - rl) <= e + 2.0 ** -18 * max(1.0, abs(rl)), (t, h, lse[t, h], rl)
+            err = np.abs(o[t, h] - ro)
+            tol = uo * np.abs(ro) + (u8 + 2 * e + 2.0 ** -18) * a + 2.0 ** -24
+            assert np.all(err <= tol), (t, h, n, float((err / tol).max()))
+
+
+def attn_problem(scfa, seed, lens, news, Hq, Hkv, D, ps, dt, extra=0, spread=0.3):
+    """Rows cached through append, their exact values, and everything attn takes."""
+    R = len(lens)
+    g = np.random.default_rng(seed)
+    have = [-(-n // ps) for n in lens]
+    P, mp = sum(have) + 4, max(1, max(have)) + 1
+    order = g.permutation(P)
+    table, at = np.full((R, mp), -1), 0
+    for r in range(R):
+        table[r, :have[r]] = order[at:at + have[r]]
+        at += have[r]
+    cache = noise_cache(seed, P, Hkv, D, ps)
+    rows = []
+    for r in range(R):
+        n = max(1, lens[r])
+        k, v = rand(seed + 2 * r, (n, Hkv, D), dt, spread).cuda(), rand(seed + 2 * r + 1, (n, Hkv, D), dt, spread).cuda()
+        if lens[r]:
+            pos = np.arange(n)
+            scfa.scfa_cache4_append(k, v, i32(table[r, pos // ps] * ps + pos % ps), cache, ps)
+        rows.append((oc.values(dbl(k))[:lens[r]], oc.values(dbl(v))[:lens[r]]))
+    q_start = np.concatenate([[0], np.cumsum(news)])
+    N = int(q_start[-1]) + extra
+    vis = np.full(max(N, 1), 10 ** 6)
+    for r in range(R):
+        vis[q_start[r]:q_start[r + 1]] = np.maximum(0, lens[r] - news[r] + 1 + np.arange(news[r]))
+    q = rand(seed + 999, (max(N, 1), Hq, D), dt).cuda()
+    return dict(q=q, cache=cache, ps=ps, table=i32(table), q_start=i32(q_start), vis=i32(vis), rows=rows, news=news,
+                scale=D ** -0.5, dt=dt)
+
+
+def run_attn(scfa, p, o=None, lse=None, stream=None):
+    N, Hq, D = p["q"].shape
+    o = torch.full((N, Hq, D), 77.0, dtype=p["dt"], device="cuda") if o is None else o
+    lse = torch.full((N, Hq), 77.0, device="cuda") if lse is None else lse
+    ws = scfa.workspace(scfa.cache4_attn_workspace_size(N, p["table"].shape[0], Hq, p["cache"].shape[1], D))
+    scfa.scfa_cache4_attn(p["q"], p["cache"], p["ps"], p["table"], p["q_start"], p["vis"], p["scale"], o, lse, ws, 0,
+                          stream)
+    return o, lse, ws
+
+
+def check_attn(scfa, p):
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    qs, vis = p["q_start"].tolist(), p["vis"].cpu().numpy()
+    for r, (k, v) in enumerate(p["rows"]):
+        a, b = qs[r], qs[r + 1]
+        check_rows(dbl(p["q"][a:b]), k, v, vis[a:b], p["scale"], o[a:b], lse[a:b], p["dt"])
+    assert torch.all(o[qs[-1]:] == 77.0) and torch.all(lse[qs[-1]:] == 77.0)  # rows behind the last request
+    return o, lse
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (8, 2), (12, 1), (20, 1), (40, 1)])
+def test_attn_single_tokens(scfa, dt, D, Hq, Hkv):
+    check_attn(scfa, attn_problem(scfa, Hq + D, [1, 0, 17, 64, 65, 300], [1] * 6, Hq, Hkv, D, 64, dt))
+
+
+@pytest.mark.parametrize("ps", [16, 32, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_page_sizes_and_ragged_tokens(scfa, ps, D):
+    check_attn(scfa, attn_problem(scfa, ps, [5, 0, 16, 255, 257, 40, 1], [5, 0, 3, 0, 9, 1, 1], 4, 2, D, ps, BF, extra=3))
+
+
+@pytest.mark.parametrize("lens,news,Hq,Hkv,D,dt", [
+    ([3001], [1], 8, 1, 128, BF), ([2049, 3, 700], [1, 1, 1], 16, 2, 64, HF), ([1500], [130], 4, 2, 128, BF),
+    ([70, 333, 64], [70, 65, 64], 6, 2, 64, BF), ([900, 33], [37, 33], 5, 1, 128, HF), ([0, 0], [3, 1], 4, 2, 64, BF),
+    ([130] * 70, [1] * 70, 8, 8, 64, BF), ([20] * 9, [16] * 9, 2, 1, 128, BF), ([4, 4], [9, 2], 2, 2, 64, BF)])
+def test_attn_shapes(scfa, lens, news, Hq, Hkv, D, dt):
+    check_attn(scfa, attn_problem(scfa, sum(lens), lens, news, Hq, Hkv, D, 16, dt))
+
+
+def test_attn_without_any_token(scfa):
+    p = attn_problem(scfa, 1, [5, 9], [0, 0], 4, 2, 64, 16, BF, extra=3)
+    check_attn(scfa, p)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+def test_attn_far_scores(scfa, dt):
+    """Scores far from zero, of both signs: the running maximum grows and the first keys hold next to nothing."""
+    p = attn_problem(scfa, 8, [400, 90], [1, 3], 4, 2, 64, 32, dt, spread=1.5)
+    p["scale"] = 0.9
+    p["q"] *= torch.linspace(-6, 6, p["q"].shape[0] * 4, device="cuda").view(-1, 4, 1).to(dt)
+    check_attn(scfa, p)
+
+
+def test_attn_strides_and_equal_bits(scfa):
+    p = attn_problem(scfa, 3, [100, 900, 33], [2, 1, 4], 8, 2, 128, 64, BF)
+    o, lse = check_attn(scfa, p)
+    wide = torch.zeros((7, 8 + 4, 128), dtype=BF, device="cuda")
+    wide[:, 2:10] = p["q"]
+    out = torch.full((7, 3, 8, 128), 5.0, dtype=BF, device="cuda")
+    o2, l2, _ = run_attn(scfa, {**p, "q": wide[:, 2:10]}, o=out[:, 1])
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert torch.all(out[:, 0] == 5.0) and torch.all(out[:, 2] == 5.0)
+    heads_first = torch.empty((8, 7, 128), dtype=BF, device="cuda").transpose(0, 1)
+    o3, _, _ = run_attn(scfa, {**p, "q": heads_first.copy_(p["q"])}, o=torch.empty_like(heads_first))
+    assert torch.equal(o, o3)
+
+
+def test_attn_on_a_side_stream_and_in_a_graph(scfa):
+    p = attn_problem(scfa, 4, [100, 900, 33, 2], [1] * 4, 8, 2, 64, 64, BF)
+    o, lse, _ = run_attn(scfa, p)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    o2, l2, _ = run_attn(scfa, p, stream=side)
+    side.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+    ws = scfa.workspace(scfa.cache4_attn_workspace_size(4, 4, 8, 2, 64))
+    outs = [(torch.zeros_like(o), torch.zeros_like(lse)) for _ in range(2)]
+    graphs = []
+    for a, b in outs:  # two graphs on one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            scfa.scfa_cache4_attn(p["q"], p["cache"], p["ps"], p["table"], p["q_start"], p["vis"], p["scale"], a, b, ws)
+        graphs.append(g)
+    for i in (0, 1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for a, b in outs:
+        assert torch.equal(o, a) and torch.equal(lse, b)
+    # longer answers on the same graph
+    p["vis"].sub_(1)
+    graphs[0].replay()
+    o3, l3, _ = run_attn(scfa, p)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], o3) and torch.equal(outs[0][1], l3)
+
+
+def test_attn_page_ids_out_of_range_are_masked_and_reported(scfa):
+    p = attn_problem(scfa, 5, [200, 90], [1, 2], 4, 2, 64, 16, BF)
+    P = p["cache"].shape[0]
+    p["table"][0, 3], p["table"][1, 0], p["table"][1, 5] = -5, P, 2 ** 30
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 1
+    for r, gone in ((0, {3}), (1, {0, 5})):
+        k, v = p["rows"][r]
+        sel = [i for i in range(len(k)) if i // 16 not in gone]
+        a, b = p["q_start"][r:r + 2].tolist()
+        for t in range(a, b):
+            n = sum(i < int(p["vis"][t]) for i in sel)
+            check_rows(dbl(p["q"][t:t + 1]), k[sel], v[sel], [n], p["scale"], o[t:t + 1], lse[t:t + 1], BF)
+    p["table"][0, 3] = p["table"][0, 2]
+    p["table"][1, 0] = p["table"][1, 5] = p["table"][1, 1]
+    _, _, ws2 = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws2) == 0
+
+
+def test_attn_page_id_out_of_range_for_all_keys(scfa):
+    p = attn_problem(scfa, 6, [10], [1], 2, 1, 64, 16, BF)
+    p["table"].fill_(-1)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 1
+    assert not o.any() and torch.all(lse == -torch.inf)
+
+
+def test_attn_wild_row_bounds(scfa):
+    """q_start and vis outside their ranges read and write nothing out of bounds."""
+    p = attn_problem(scfa, 7, [30, 30], [2, 2], 2, 1, 64, 16, BF)
+    p["vis"][3] = 2 ** 31 - 1  # more than the table has pages for: its pages past the end are -1
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 1
+    p["q_start"].copy_(i32([0, 2, 400]))
+    o, lse, ws = run_attn(scfa, p)
+    torch.cuda.synchronize()
+    p["q_start"].copy_(i32([-3, 2, 1]))
+    run_attn(scfa, p)
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- steps
+@pytest.mark.parametrize("dt,D,Hq,Hkv,ps", [(BF, 64, 12, 12, 64), (HF, 128, 8, 2, 16)])
+@pytest.mark.parametrize("drop", [None, 0.6])
+def test_steps_together(scfa, dt, D, Hq, Hkv, ps, drop):
+    """Prompts, then single tokens, a release and a new request, against a dense replay of everything cached."""
+    from sparse_causal_flash_gb300.cache import KVCache4
+    R, scale = 3, D ** -0.5
+    c = KVCache4(R, 24, Hq, Hkv, D, max_len=160, max_tokens=160, page_size=ps, dtype=dt)
+    held = [(np.zeros((0, Hkv, D)), np.zeros((0, Hkv, D))) for _ in range(R)]
+    g = np.random.default_rng(1)
+    for i, new in enumerate([[40, 0, 75], [1, 0, 1], [1, 33, 1], "release", [1, 1, 20], [4, 4, 0], [0, 0, 0]]):
+        if new == "release":
+            c.release(2)
+            held[2] = tuple(np.zeros((0, Hkv, D)) for _ in "kv")
+            assert sorted(c.free[:int(c.n_free)].tolist() + c.table[0, :-(-int(c.len[0]) // ps)].tolist()
+                          + c.table[1, :-(-int(c.len[1]) // ps)].tolist()) == list(range(24))
+            continue
+        N = sum(new) + 2
+        q = rand(50 + i, (N, Hq, D), dt).cuda()
+        kv = rand(90 + i, (N, 2 * Hkv, D), dt).cuda()
+        keep = None if drop is None else (g.random(N) < drop).astype(np.uint8)
+        o, lse = c.step(q, kv[:, :Hkv], kv[:, Hkv:], i32(new), scale,
+                        None if keep is None else torch.as_tensor(keep).cuda())
+        assert c.status() == 0
+        at = 0
+        for r in range(R):
+            k, v = held[r]
+            for t in range(at, at + new[r]):
+                if keep is None or keep[t]:
+                    k = np.concatenate([k, oc.values(dbl(kv[t:t + 1, :Hkv]))])
+                    v = np.concatenate([v, oc.values(dbl(kv[t:t + 1, Hkv:]))])
+                check_rows(dbl(q[t:t + 1]), k, v, [len(k)], scale, o[t:t + 1], lse[t:t + 1], dt)
+            held[r], at = (k, v), at + new[r]
+        assert c.len.tolist() == [len(k) for k, _ in held]
+    for r in range(R):
+        k, v = c.rows(r)
+        assert np.array_equal(dbl(k), held[r][0]) and np.array_equal(dbl(v), held[r][1])
+
+
+def test_captured_steps_equal_eager_ones(scfa):
+    from sparse_causal_flash_gb300.cache import KVCache4
+    R, Hq, Hkv, D = 5, 8, 2, 64
+    a, b = (KVCache4(R, 60, Hq, Hkv, D, max_len=96, max_tokens=300, page_size=16) for _ in "ab")
+    prompt = i32([30, 1, 50, 0, 17])
+    q, kv = rand(1, (98, Hq, D)).cuda(), rand(2, (98, 2 * Hkv, D)).cuda()
+    for c in (a, b):
+        c.step(q, kv[:, :Hkv], kv[:, Hkv:], prompt, 0.125)
+    q1, kv1, ones = torch.empty_like(q[:R]), torch.empty_like(kv[:R]), i32([1] * R)
+    g = b.capture(q1, kv1[:, :Hkv], kv1[:, Hkv:], ones, 0.125)
+    assert b.len.tolist() == a.len.tolist()
+    for i in range(20):
+        q1.copy_(rand(100 + i, (R, Hq, D)))
+        kv1.copy_(rand(200 + i, (R, 2 * Hkv, D)))
+        o, lse = a.step(q1, kv1[:, :Hkv], kv1[:, Hkv:], ones, 0.125)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, b.o[:R]) and torch.equal(lse, b.lse[:R])
+    assert a.len.tolist() == b.len.tolist() == [50, 21, 70, 20, 37]
+    assert torch.equal(a.cache, b.cache) and torch.equal(a.table, b.table)
+    assert a.status() == 0 and b.status() == 0
+
+
+def test_step_without_room_computes_nothing(scfa):
+    from sparse_causal_flash_gb300.cache import KVCache4
+    c = KVCache4(2, 3, 4, 2, 64, max_len=64, max_tokens=64, page_size=16)
+    q, kv = rand(1, (60, 4, 64)).cuda(), rand(2, (60, 4, 64)).cuda()
+    c.step(q[:40], kv[:40, :2], kv[:40, 2:], i32([20, 20]), 0.125)
+    assert c.status() == 3 and c.len.tolist() == [0, 0] and int(c.n_free) == 3
+    assert not c.o.any() and not c.cache.any()
+    c.step(q[:40], kv[:40, :2], kv[:40, 2:], i32([32, 8]), 0.125)
+    assert c.status() == 0 and c.len.tolist() == [32, 8] and int(c.n_free) == 0
