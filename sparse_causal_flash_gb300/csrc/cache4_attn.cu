@@ -1,5 +1,31 @@
 // Attention of new tokens over the paged 4-bit cache.
+//
+// One pass over the cached tokens with the running maximum and sum of the
+// softmax. An item is up to 8 * NT query rows (token, head) of one request
+// that share a key head; its tokens are walked in chunks of 128, and the
+// chunks of all items, in one long line, are cut into equal pieces, one per
+// CTA of a grid that fills the GPU: a ragged batch and one long request are
+// spread alike. An item that falls into several pieces leaves partial rows
+// (O, m, l in fp32), which a second kernel joins in a fixed order, so results
+// do not depend on scheduling.
+//
+// A CTA is a producer warp, which walks the block table and copies whole
+// tiles of the pages into a ring of shared-memory stages, and four warps that
+// each take two 16-token tiles of every chunk with their own m, l and O (they
+// meet once per item). The cached codes are the A operands: S^T = K Q^T and
+// O^T = V^T P^T with 16 keys or channels by 8 query rows by 16, so up to 8
+// rows cost what one does, and the page layout is the operand layout: no
+// shuffle between the copy and the MMA. The matrix instructions are the
+// warp-level ones: a decode step does 8 * rows flops per cached byte, far
+// below what any of them bounds.
+//   K: codes become 128 + (c + 8) in bf16 by one AND-OR (for fp16 queries the
+//      bits of c + 8 are read as a subnormal, (c + 8) 2^-24); the offset is
+//      taken off by starting the accumulator at -136 sum(q) (-8 2^-24 sum(q)),
+//      and the group's scale multiplies the fp32 sum.
+//   V: codes become c s in bf16 by one FMA (exact: seven significant bits);
+//      P is rounded to bf16, as in the training kernels.
 #include <climits>
+#include <cmath>
 
 #include "cache4.cuh"
 #include "internal.h"
@@ -7,102 +33,709 @@
 namespace scfa {
 namespace {
 
+constexpr int kCh = 128;             // tokens per chunk
+constexpr int kChTiles = kCh / kC4Tile;
+constexpr int kWarps = 4;            // compute warps
+constexpr int kTpw = kChTiles / kWarps;
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr float kNoMax = -1e30f;     // running maximum before any key (finite: differences stay defined)
+
+// Where the partial rows of a CTA go, and what it reports. One per CTA,
+// written by every call.
+struct C4Desc {
+  int err;     // SCFA_OK or the CTA's first error
+  int parts;   // > 0: an item begins here and ends `parts` CTAs later
+  int tok0, rows, row0, head;
+  int pad[2];
+};
+
 struct C4AttnArgs {
   const uint16_t* q;
   long long qt, qh;
   const uint8_t* cache;
-  int page_size, n_pages;
+  int page_size, log_ps, n_pages;
   const int32_t* table;
   int max_pages;
   const int32_t *q_start, *vis;
-  int N, R, Hq, Hkv;
-  float scale;
+  int N, R, Hq, Hkv, G;
+  float factor;  // score in log2 units = accumulated sum * factor
   uint16_t* o;
   long long ot, oh;
   float* lse;
   int* status;
+  C4Desc* desc;
+  float* part;  // [cta][2][rows][D]
+  float* ml;    // [cta][2][rows][2]
+  int stall;
 };
 
-// One CTA per (token, query head), 128 keys at a time: thread = key for the
-// scores, thread = channel for the values.
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) attn_simple_kernel(C4AttnArgs a) {
-  using L = C4<D>;
-  __shared__ float sq[D], sp[128], red[4];
-  __shared__ long long sbase[128];
-  const int tok = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, hk = h / (a.Hq / a.Hkv), tid = threadIdx.x;
-  if (tok >= a.q_start[a.R]) return;
-  int lo = 0, hi = a.R;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.q_start[mid] <= tok) lo = mid;
-    else hi = mid;
-  }
-  const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
-  const int vis = static_cast<int>(min(cap, static_cast<long long>(max(0, a.vis[tok]))));
-  if (tid < D / 2) {
-    const float2 f = c4_unpack<F16>(reinterpret_cast<const uint32_t*>(a.q + tok * a.qt + h * a.qh)[tid]);
-    sq[2 * tid] = f.x, sq[2 * tid + 1] = f.y;
-  }
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  __syncthreads();
-  for (int p0 = 0; p0 < vis; p0 += 128) {
-    const int pos = p0 + tid;
-    float s = -INFINITY;
-    sbase[tid] = -1;
-    if (pos < vis) {
-      const int page = a.table[static_cast<long long>(lo) * a.max_pages + pos / a.page_size];
-      if (page >= 0 && page < a.n_pages) {
-        const int at = pos % a.page_size, t = at & 15;
-        sbase[tid] = c4_tile_base(page, a.Hkv, hk, a.page_size, at, L::kTileBytes);
-        const uint8_t* tile = a.cache + sbase[tid];
-        s = 0.f;
-        for (int g = 0; g < L::kG; ++g) {
-          float x = 0.f;
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(tile + L::k_row(t) + (j * L::kG + g) * 4);
-            for (int y = 0; y < 8; ++y)
-              x += sq[32 * g + 8 * j + (y < 4 ? 2 * y : 2 * y - 7)] *
-                   static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8);
-          }
-          s += x * c4_scale(tile[L::kKScales + t * L::kG + g]);
-        }
-        s *= a.scale;
-      } else {
-        raise_status(a.status, SCFA_ERR_INVALID);
-      }
-    }
-    float x = s;
-    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    if ((tid & 31) == 0) red[tid >> 5] = x;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = expf(m - base);
-    sp[tid] = expf(s - base);
-    __syncthreads();
-    l *= f, o *= f, m = mn;
-    const int r = tid % 32 / 4, y = tid % 4, g = tid / 32;
-    for (int k = 0; k < 128; ++k) {
-      l += sp[k];
-      if (tid < D && sbase[k] >= 0) {
-        const uint8_t* tile = a.cache + sbase[k];
-        const int t = (p0 + k) & 15;
-        const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + L::v_piece(t, r) + 2 * g);
-        o += sp[k] * static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8) *
-             c4_scale(tile[L::kVScales + t * L::kG + g]);
-      }
-    }
-    __syncthreads();
-  }
-  if (tid < D) {
-    const float v = l > 0.f ? o / l : 0.f;
-    a.o[tok * a.ot + h * a.oh + tid] = static_cast<uint16_t>(c4_pack<F16>(v, 0.f) & 0xFFFFu);
-  }
-  if (tid == 0) a.lse[static_cast<long long>(tok) * a.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+// What a stage holds.
+struct C4Stage {
+  int tok0, rows, row0, head;  // first token of the request, its rows, first row of the item, key head
+  int base;                    // position of the chunk's first token
+  int tiles;                   // bit t: tile t was copied
+  int flags;
+  int pad;
+};
+enum { kFirst = 1, kLast = 2, kOpenStart = 4, kOpenEnd = 8 };
+
+template <int D, int NT>
+struct C4Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStageBytes = kChTiles * C4<D>::kTileBytes;
+  static constexpr int kCtas = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
+  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 6);
+  static constexpr int kPad = D + 4;  // floats per row of the warps' partial O (conflict-free float4 stores)
+  static constexpr bool kQSmem = NT > 2;
+  static constexpr size_t kPartBytes = sizeof(float) * kWarps * kRows * kPad;
+  static constexpr size_t kQBytes = kQSmem ? static_cast<size_t>(kWarps) * NT * (D / 32) * 32 * 16 : 0;
+  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kPartBytes + kQBytes;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// transpose of an 8 x 8 matrix of 16-bit values, one row per four lanes
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-__global__ void clear_status_kernel(int* status) { *status = SCFA_OK; }
+// bounded wait of a whole warp: its lanes go on, or give up, together
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+}
+
+// Row blocks of a request and the chunks of one of them.
+struct C4Req {
+  int tok0, rows, blocks;
+};
+template <int ROWS>
+__device__ __forceinline__ C4Req c4_request(const C4AttnArgs& a, int r) {
+  C4Req q;
+  // (indices are clamped: nothing is read out of bounds whatever q_start holds)
+  q.tok0 = min(max(a.q_start[r], 0), a.N);
+  const int end = min(max(a.q_start[r + 1], q.tok0), a.N);
+  q.rows = (end - q.tok0) * a.G;
+  q.blocks = (q.rows + ROWS - 1) / ROWS;
+  return q;
+}
+// tokens that the last row of block b sees (vis does not decrease within a request)
+template <int ROWS>
+__device__ __forceinline__ int c4_seen(const C4AttnArgs& a, const C4Req& q, int b) {
+  const int last = min((b + 1) * ROWS, q.rows) - 1;
+  const long long cap = static_cast<long long>(a.max_pages) << a.log_ps;
+  return static_cast<int>(min(cap, static_cast<long long>(max(0, a.vis[q.tok0 + last / a.G]))));
+}
+__device__ __forceinline__ int c4_chunks(int seen) { return max(1, (seen + kCh - 1) / kCh); }
+
+template <int D, bool F16, int NT>
+__global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_kernel(C4AttnArgs a) {
+  using L = C4<D>;
+  using C = C4Cfg<D, NT>;
+  constexpr int G = L::kG, ROWS = C::kRows, S = C::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[S], empty[S], mfull, mempty;
+  __shared__ C4Stage stage[S];
+  __shared__ float s_ml[kWarps][ROWS][2];
+  __shared__ long long s_sum[kWarps + 2];
+  __shared__ long long s_prefix;
+  __shared__ int s_req;
+  __shared__ volatile int abort_flag;
+  float* const s_part = reinterpret_cast<float*>(smem + static_cast<size_t>(S) * C::kStageBytes);
+
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  C4Desc* const desc = a.desc + blockIdx.x;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    mbar_init(&mfull, kWarps);
+    mbar_init(&mempty, kWarps);
+    fence_mbar_init();
+    abort_flag = 0;
+    s_req = -1;
+    desc->err = SCFA_OK;
+    desc->parts = 0;
+  }
+
+  // ---- chunks of all requests, and the request in which this CTA's piece begins
+  auto request_units = [&](int r) {
+    C4Req q = {0, 0, 0};
+    if (r < a.R) q = c4_request<ROWS>(a, r);
+    long long sum = 0;
+    if (q.blocks <= 4) {
+      for (int b = 0; b < q.blocks; ++b) sum += c4_chunks(c4_seen<ROWS>(a, q, b));
+    }
+    // requests of many blocks: the warp together
+    uint32_t big = __ballot_sync(0xffffffffu, q.blocks > 4);
+    while (big) {
+      const int src = __ffs(big) - 1;
+      big &= big - 1;
+      C4Req p;
+      p.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
+      p.rows = __shfl_sync(0xffffffffu, q.rows, src);
+      p.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
+      int x = 0;
+      for (int b = lane; b < p.blocks; b += 32) x += c4_chunks(c4_seen<ROWS>(a, p, b));
+      x = __reduce_add_sync(0xffffffffu, x);
+      if (lane == src) sum = x;
+    }
+    return sum * a.Hkv;
+  };
+  // inclusive sum over the block; *total gets the sum
+  auto block_incl = [&](long long x, long long* total) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_sum[w] = x;
+    __syncthreads();
+    long long all = 0;
+    for (int i = 0; i <= kWarps; ++i) {
+      if (i == w) x += all;
+      all += s_sum[i];
+    }
+    *total = all;
+    return x;
+  };
+  long long total = 0, mine = 0;
+  for (int base = 0; base < a.R; base += kThreads) {
+    long long sum;
+    mine = request_units(base + tid);
+    block_incl(mine, &sum);
+    total += sum;
+  }
+  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+  if (u0 >= u1) return;  // (the whole CTA)
+  long long before = 0;
+  for (int base = 0; base < a.R; base += kThreads) {
+    long long sum;
+    if (a.R > kThreads) mine = request_units(base + tid);
+    const long long upto = before + block_incl(mine, &sum);
+    if (u0 < upto && u0 >= upto - mine) {
+      s_req = base + tid;
+      s_prefix = upto - mine;
+    }
+    before += sum;
+    if (u0 < before) break;  // (uniform)
+  }
+  __syncthreads();
+  const int n_units = static_cast<int>(u1 - u0);
+
+  if (w == kWarps) {
+    // ================================================= producer
+    int r = s_req, b = 0, h, ch, seen;
+    C4Req q = c4_request<ROWS>(a, r);
+    long long rem = u0 - s_prefix;
+    for (;; b += 32) {  // the block: 32 at a time
+      const int mb = b + lane;
+      const int c = mb < q.blocks ? c4_chunks(c4_seen<ROWS>(a, q, mb)) : 0;
+      long long x = static_cast<long long>(c) * a.Hkv;
+      const long long own = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, rem < x);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        b += src;
+        rem -= __shfl_sync(0xffffffffu, x - own, src);
+        break;
+      }
+      rem -= __shfl_sync(0xffffffffu, x, 31);
+      if (b + 32 >= q.blocks) break;  // (does not happen: the piece begins in this request)
+    }
+    seen = c4_seen<ROWS>(a, q, b);
+    int chunks = c4_chunks(seen);
+    h = static_cast<int>(rem / chunks);
+    ch = static_cast<int>(rem % chunks);
+    bool first = true;  // of its item in this CTA
+
+    const int psub = min(a.page_size, kCh), npc = kCh / psub;
+    int have_r = -1, have_p = 0, page = -1;  // the 32 pieces whose pages the lanes hold
+    int issued = 0;
+    for (int u = 0; u < n_units; ++u) {
+      const int s = u % S;
+      if (u >= S && !wait_all(&empty[s], ((u / S) & 1) ^ 1, &abort_flag, &desc->err)) break;
+      // pages of this chunk
+      const int p0 = ch * npc;
+      if (have_r != r || p0 < have_p || p0 + npc > have_p + 32) {
+        have_r = r;
+        have_p = p0;
+        const long long tokpos = static_cast<long long>(p0 + lane) * psub;
+        page = -1;
+        if (tokpos < (static_cast<long long>(a.max_pages) << a.log_ps))
+          page = a.table[static_cast<long long>(r) * a.max_pages + (tokpos >> a.log_ps)];
+      }
+      const int pg = __shfl_sync(0xffffffffu, page, (p0 - have_p + lane) & 31);
+      const int n = min(kCh, seen - ch * kCh) - lane * psub;  // tokens of this lane's piece
+      int tiles = lane < npc && n > 0 ? (min(n, psub) + kC4Tile - 1) / kC4Tile : 0;
+      if (tiles > 0 && (pg < 0 || pg >= a.n_pages)) {
+        raise_status(&desc->err, SCFA_ERR_INVALID);
+        tiles = 0;
+      }
+      const uint32_t mask =
+          __reduce_or_sync(0xffffffffu, tiles > 0 ? ((1u << tiles) - 1u) << (lane * (psub / kC4Tile)) : 0u);
+      const uint32_t bytes = __popc(mask) * L::kTileBytes;
+      const bool last_chunk = ch + 1 == chunks;
+      if (lane == 0) {
+        C4Stage d;
+        d.tok0 = q.tok0;
+        d.rows = q.rows;
+        d.row0 = b * ROWS;
+        d.head = h;
+        d.base = ch * kCh;
+        d.tiles = static_cast<int>(mask);
+        const bool began = ch <= u, goes_on = !last_chunk && u + 1 == n_units;  // the item, in this piece
+        d.flags = (first ? kFirst : 0) | (last_chunk || goes_on ? kLast : 0) | (began ? 0 : kOpenStart) |
+                  (goes_on ? kOpenEnd : 0);
+        stage[s] = d;
+        if (goes_on && began) {
+          const long long last = u1 - 1 + (chunks - 1 - ch);  // the item's last unit
+          desc->parts = static_cast<int>(last / per - blockIdx.x);
+          desc->tok0 = q.tok0;
+          desc->rows = q.rows;
+          desc->row0 = b * ROWS;
+          desc->head = h;
+        }
+        if (!(a.stall && u == 0)) mbar_arrive_expect_tx(&full[s], bytes);
+      }
+      __syncwarp();
+      if (tiles > 0 && !(a.stall && u == 0)) {
+        const long long tok = static_cast<long long>(p0 + lane) * psub;
+        const uint8_t* src =
+            a.cache + c4_tile_base(pg, a.Hkv, h, a.page_size, static_cast<int>(tok & (a.page_size - 1)), L::kTileBytes);
+        bulk_load(smem + static_cast<size_t>(s) * C::kStageBytes + lane * (psub / kC4Tile) * L::kTileBytes, src,
+                  tiles * L::kTileBytes, &full[s]);
+      }
+      issued = u + 1;
+      // next chunk
+      first = false;
+      if (last_chunk) {
+        first = true;
+        ch = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          if (u + 1 < n_units) {
+            if (++b == q.blocks) {
+              b = 0;
+              do {
+                q = c4_request<ROWS>(a, ++r);
+              } while (q.blocks == 0 && r + 1 < a.R);
+            }
+            seen = c4_seen<ROWS>(a, q, b);
+            chunks = c4_chunks(seen);
+          }
+        }
+      } else {
+        ++ch;
+      }
+    }
+    // copies in flight land before the shared memory goes
+    for (int u = max(0, issued - S); u < issued; ++u)
+      if (!(a.stall && u == 0)) mbar_wait_drain(&full[u % S], (u / S) & 1, &desc->err);
+    return;
+  }
+
+  // =================================================== compute warps
+  const int r8 = lane >> 2, j = lane & 3;
+  uint4* const s_q = reinterpret_cast<uint4*>(smem + static_cast<size_t>(S) * C::kStageBytes + C::kPartBytes) +
+                     static_cast<size_t>(w) * NT * G * 32;
+  float O[NT][G][2][4];
+  uint32_t Q[C::kQSmem ? 1 : NT][G][4];
+  float x0[NT][G][2];  // accumulator start per group and column
+  float m[NT][2], l[NT][2];
+  int seen[NT][2], full_to = 0, items = 0;
+  for (int u = 0; u < n_units; ++u) {
+    const int s = u % S;
+    if (!wait_all(&full[s], (u / S) & 1, &abort_flag, &desc->err)) return;
+    const C4Stage d = stage[s];
+    if (d.flags & kFirst) {
+      int lo = INT_MAX;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = d.row0 + nt * 8 + r8;
+        const bool in = row < d.rows;
+        const int tok = row / a.G;
+        const uint16_t* qp = a.q + (d.tok0 + tok) * a.qt + (d.head * a.G + row - tok * a.G) * a.qh + 8 * j;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint4 v = in ? *reinterpret_cast<const uint4*>(qp + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+          const float2 f0 = c4_unpack<F16>(v.x), f1 = c4_unpack<F16>(v.y), f2 = c4_unpack<F16>(v.z),
+                       f3 = c4_unpack<F16>(v.w);
+          float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          sum *= F16 ? -8.f * 0x1p-24f : -136.f;
+          x0[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * j);
+          x0[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
+          if (C::kQSmem) {
+            s_q[(nt * G + g) * 32 + lane] = v;
+          } else {
+            Q[nt][g][0] = v.x, Q[nt][g][1] = v.y, Q[nt][g][2] = v.z, Q[nt][g][3] = v.w;
+          }
+          O[nt][g][0][0] = O[nt][g][0][1] = O[nt][g][0][2] = O[nt][g][0][3] = 0.f;
+          O[nt][g][1][0] = O[nt][g][1][1] = O[nt][g][1][2] = O[nt][g][1][3] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = d.row0 + nt * 8 + 2 * j + c;
+          seen[nt][c] = col < d.rows ? a.vis[d.tok0 + col / a.G] : INT_MAX;
+          lo = min(lo, seen[nt][c]);
+          m[nt][c] = kNoMax;
+          l[nt][c] = 0.f;
+        }
+      }
+      full_to = __reduce_min_sync(0xffffffffu, lo);
+      if (C::kQSmem) __syncwarp();
+    }
+    const int t0 = w * kTpw;
+    if ((d.tiles >> t0) & ((1 << kTpw) - 1)) {
+      const uint8_t* tile0 = smem + static_cast<size_t>(s) * C::kStageBytes + t0 * L::kTileBytes;
+      float x[kTpw][NT][4];
+      // ---- scores
+#pragma unroll
+      for (int i = 0; i < kTpw; ++i) {
+        const uint8_t* tile = tile0 + i * L::kTileBytes;
+        uint32_t kw[2][G], ks[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint8_t* p = tile + L::k_row(r8 + 8 * y) + j * 4 * G;
+          if (G == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            kw[y][0] = v.x, kw[y][1] = v.y, kw[y][G - 2] = v.z, kw[y][G - 1] = v.w;
+            ks[y] = *reinterpret_cast<const uint32_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            kw[y][0] = v.x, kw[y][1] = v.y;
+            ks[y] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint32_t magic = F16 ? 0u : 0x43004300u;
+          uint32_t A[2][4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            A[k][0] = ((kw[0][g] >> (8 * k)) & 0x000F000Fu) | magic;
+            A[k][1] = ((kw[1][g] >> (8 * k)) & 0x000F000Fu) | magic;
+            A[k][2] = ((kw[0][g] >> (8 * k + 4)) & 0x000F000Fu) | magic;
+            A[k][3] = ((kw[1][g] >> (8 * k + 4)) & 0x000F000Fu) | magic;
+          }
+          const float s0 = c4_scale((ks[0] >> (8 * g)) & 255u, 96u), s1 = c4_scale((ks[1] >> (8 * g)) & 255u, 96u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {x0[nt][g][0], x0[nt][g][1], x0[nt][g][0], x0[nt][g][1]};
+            uint4 qv;
+            if (C::kQSmem) qv = s_q[(nt * G + g) * 32 + lane];
+            else qv = make_uint4(Q[C::kQSmem ? 0 : nt][g][0], Q[C::kQSmem ? 0 : nt][g][1],
+                                 Q[C::kQSmem ? 0 : nt][g][2], Q[C::kQSmem ? 0 : nt][g][3]);
+            if (F16) {
+              mma_f16(acc, A[0], qv.x, qv.y);
+              mma_f16(acc, A[1], qv.z, qv.w);
+            } else {
+              mma_bf16(acc, A[0], qv.x, qv.y);
+              mma_bf16(acc, A[1], qv.z, qv.w);
+            }
+            x[i][nt][0] = fmaf(acc[0], s0, x[i][nt][0]);
+            x[i][nt][1] = fmaf(acc[1], s0, x[i][nt][1]);
+            x[i][nt][2] = fmaf(acc[2], s1, x[i][nt][2]);
+            x[i][nt][3] = fmaf(acc[3], s1, x[i][nt][3]);
+          }
+        }
+        const int key = d.base + (t0 + i) * kC4Tile + r8;
+        const bool there = (d.tiles >> (t0 + i)) & 1;
+        if (!there || key - r8 + kC4Tile > full_to) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!there || key + 8 * (e >> 1) >= seen[nt][e & 1]) x[i][nt][e] = -INFINITY;
+        }
+      }
+      // ---- softmax: the maximum moves only when a score exceeds it by 2^8
+      uint32_t P[kTpw][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < kTpw; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over |= fmaf(x[i][nt][e], a.factor, -m[nt][e & 1]) > 8.f;
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kTpw; ++i) mx = fmaxf(mx, fmaxf(x[i][nt][c], x[i][nt][c + 2]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(m[nt][c], mx * a.factor);
+            const float f = ex2_approx(m[nt][c] - mx);
+            m[nt][c] = mx;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) O[nt][g][t][c] *= f, O[nt][g][t][c + 2] *= f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTpw; ++i) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(x[i][nt][e], a.factor, -m[nt][e & 1]));
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
+          P[i][nt][0] = transpose8(pack_bf16x2(p[0], p[1]));
+          P[i][nt][1] = transpose8(pack_bf16x2(p[2], p[3]));
+        }
+      }
+      // ---- values
+#pragma unroll
+      for (int i = 0; i < kTpw; ++i) {
+        const uint8_t* tile = tile0 + i * L::kTileBytes;
+        uint32_t vw[2][2][G / 2];  // [keys 0-7 / 8-15][key 2 j + ..][groups 2 y, 2 y + 1]
+        uint32_t vs[2][2];         // scale bytes of those keys
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint8_t* p = tile + L::kVCodes + y * 4 * D + r8 * 16 * G + j * 4 * G;
+          const uint8_t* q = tile + L::kVScales + (8 * y + 2 * j) * G;
+          if (G == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            vw[y][0][0] = v.x, vw[y][0][G / 2 - 1] = v.y, vw[y][1][0] = v.z, vw[y][1][G / 2 - 1] = v.w;
+            const uint2 f = *reinterpret_cast<const uint2*>(q);
+            vs[y][0] = f.x, vs[y][1] = f.y;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            vw[y][0][0] = v.x, vw[y][1][0] = v.y;
+            const uint32_t f = *reinterpret_cast<const uint32_t*>(q);
+            vs[y][0] = f & 0xFFFFu, vs[y][1] = f >> 16;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          uint32_t A[2][4];  // channels 4 r + 2 t, + 1 of two m16 tiles
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t pair = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
+            // the two keys' scales times 2^-16, and -136 of them
+            const uint32_t sb = __byte_perm(vs[y][0], vs[y][1], g | g << 4 | (4 + g) << 8 | (4 + g) << 12);
+            const uint32_t sc = ((sb << 4) & 0x0FF00FF0u) | 0x30003000u;
+            const uint32_t off = mul_bf16x2(sc, 0xC308C308u);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              A[c >> 1][(c & 1) + 2 * y] = fma_bf16x2(((pair >> (4 * c)) & 0x000F000Fu) | 0x43004300u, sc, off);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(O[nt][g][0], A[0], P[i][nt][0], P[i][nt][1]);
+            mma_bf16(O[nt][g][1], A[1], P[i][nt][0], P[i][nt][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+
+    if (d.flags & kLast) {
+      // ---- the four warps' rows become one
+      if (items > 0 && !wait_all(&mempty, (items - 1) & 1, &abort_flag, &desc->err)) return;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float z = l[nt][c];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+          const int row = nt * 8 + 2 * j + c;
+          if (r8 == 0) s_ml[w][row][0] = m[nt][c], s_ml[w][row][1] = z;
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+            *reinterpret_cast<float4*>(s_part + (w * ROWS + row) * C::kPad + 32 * g + 4 * r8) =
+                make_float4(O[nt][g][0][c], O[nt][g][0][c + 2], O[nt][g][1][c], O[nt][g][1][c + 2]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mfull);
+      if (!wait_all(&mfull, items & 1, &abort_flag, &desc->err)) return;
+      constexpr int CPT = D / 16;  // channels per thread
+      const int ch0 = (tid & 15) * CPT;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = nt * 8 + (tid >> 4), grow = d.row0 + row;
+        if (grow < d.rows) {
+          float mt = s_ml[0][row][0];
+#pragma unroll
+          for (int i = 1; i < kWarps; ++i) mt = fmaxf(mt, s_ml[i][row][0]);
+          float lt = 0.f, o[CPT];
+#pragma unroll
+          for (int e = 0; e < CPT; ++e) o[e] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) {
+            const float f = ex2_approx(s_ml[i][row][0] - mt);
+            lt = fmaf(s_ml[i][row][1], f, lt);
+            const float* p = s_part + (i * ROWS + row) * C::kPad + ch0;
+#pragma unroll
+            for (int e = 0; e < CPT; e += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(p + e);
+              o[e] = fmaf(v.x, f, o[e]), o[e + 1] = fmaf(v.y, f, o[e + 1]);
+              o[e + 2] = fmaf(v.z, f, o[e + 2]), o[e + 3] = fmaf(v.w, f, o[e + 3]);
+            }
+          }
+          const bool tail = d.flags & kOpenStart, open = d.flags & kOpenEnd;
+          if (!tail && !open) {
+            const int tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
+            const float inv = lt > 0.f ? 0x1p16f / lt : 0.f;  // V's scales carried 2^-16
+            uint32_t z[CPT / 2];
+#pragma unroll
+            for (int e = 0; e < CPT; e += 2) z[e / 2] = c4_pack<F16>(o[e] * inv, o[e + 1] * inv);
+            uint16_t* op = a.o + tok * a.ot + head * a.oh + ch0;
+            if (CPT == 8) *reinterpret_cast<uint4*>(op) = make_uint4(z[0], z[1], z[CPT / 2 - 2], z[CPT / 2 - 1]);
+            else *reinterpret_cast<uint2*>(op) = make_uint2(z[0], z[1]);
+            if ((tid & 15) == 0)
+              a.lse[static_cast<long long>(tok) * a.Hq + head] =
+                  lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          } else {
+            const long long at = (static_cast<long long>(blockIdx.x) * 2 + (tail ? 0 : 1)) * ROWS + row;
+#pragma unroll
+            for (int e = 0; e < CPT; e += 4)
+              *reinterpret_cast<float4*>(a.part + at * D + ch0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            if ((tid & 15) == 0) a.ml[2 * at] = mt, a.ml[2 * at + 1] = lt;
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mempty);
+      ++items;
+    }
+  }
+}
+
+// Joins the partial rows of the items that were cut, in the order of their
+// chunks, and gathers the CTAs' errors. One CTA per piece: the one in which
+// the item begins.
+template <int D, bool F16, int ROWS>
+__global__ void __launch_bounds__(128) cache4_join_kernel(C4AttnArgs a, int n_desc) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    int err = 0;
+    for (int i = tid; i < n_desc; i += 128) err = max(err, a.desc[i].err);
+    err = __reduce_max_sync(0xffffffffu, err);
+    __shared__ int s_err[4];
+    if ((tid & 31) == 0) s_err[tid >> 5] = err;
+    __syncthreads();
+    if (tid == 0) *a.status = max(max(s_err[0], s_err[1]), max(s_err[2], s_err[3]));
+  }
+  const C4Desc d = a.desc[blockIdx.x];
+  if (d.parts <= 0) return;
+  constexpr int CPT = D / 16;
+  const int ch0 = (tid & 15) * CPT;
+  for (int row = tid >> 4; row < ROWS; row += 8) {
+    const int grow = d.row0 + row;
+    if (grow >= d.rows) break;
+    auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+    float mt = kNoMax;
+    for (int i = 0; i <= d.parts; ++i) mt = fmaxf(mt, a.ml[2 * at(i)]);
+    float lt = 0.f, o[CPT];
+#pragma unroll
+    for (int e = 0; e < CPT; ++e) o[e] = 0.f;
+    for (int i = 0; i <= d.parts; ++i) {
+      const long long p = at(i);
+      const float f = ex2_approx(a.ml[2 * p] - mt);
+      lt = fmaf(a.ml[2 * p + 1], f, lt);
+#pragma unroll
+      for (int e = 0; e < CPT; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(a.part + p * D + ch0 + e);
+        o[e] = fmaf(v.x, f, o[e]), o[e + 1] = fmaf(v.y, f, o[e + 1]);
+        o[e + 2] = fmaf(v.z, f, o[e + 2]), o[e + 3] = fmaf(v.w, f, o[e + 3]);
+      }
+    }
+    const int tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
+    const float inv = lt > 0.f ? 0x1p16f / lt : 0.f;
+    uint32_t z[CPT / 2];
+#pragma unroll
+    for (int e = 0; e < CPT; e += 2) z[e / 2] = c4_pack<F16>(o[e] * inv, o[e + 1] * inv);
+    uint16_t* op = a.o + tok * a.ot + head * a.oh + ch0;
+    if (CPT == 8) *reinterpret_cast<uint4*>(op) = make_uint4(z[0], z[1], z[CPT / 2 - 2], z[CPT / 2 - 1]);
+    else *reinterpret_cast<uint2*>(op) = make_uint2(z[0], z[1]);
+    if ((tid & 15) == 0)
+      a.lse[static_cast<long long>(tok) * a.Hq + head] =
+          lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+// Query rows of an item, 8 * NT: the average request's rows in as few passes
+// over its tokens as registers allow.
+int c4_nt(int N, int R, int G) {
+  const long long rows = (static_cast<long long>(N) + R - 1) / R * G;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+int c4_ctas(int nt) { return (nt == 1 ? 3 : nt == 2 ? 2 : 1) * num_sms(); }
+
+struct C4Ws {
+  size_t desc = 0, ml = 0, part = 0, total = 0;
+};
+// One size for every N and R, so that a workspace serves smaller steps too.
+C4Ws c4_ws(int D) {
+  C4Ws w;
+  size_t n = 0, rows = 0;
+  for (int nt = 1; nt <= 4; nt *= 2) {
+    const size_t c = c4_ctas(nt);
+    n = c > n ? c : n;
+    rows = c * 2 * 8 * nt > rows ? c * 2 * 8 * nt : rows;
+  }
+  w.desc = sizeof(WsHeader);
+  w.ml = align_up(w.desc + n * sizeof(C4Desc), 256);
+  w.part = align_up(w.ml + rows * 2 * sizeof(float), 256);
+  w.total = align_up(w.part + rows * D * sizeof(float), 256);
+  return w;
+}
+
+template <int D, bool F16, int NT>
+cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
+  using C = C4Cfg<D, NT>;
+  const int grid = c4_ctas(NT);
+  auto kern = cache4_attn_kernel<D, F16, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, C::kSmem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cache4_join_kernel<D, F16, C::kRows><<<grid, 128, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t launch_nt(int nt, const C4AttnArgs& a, cudaStream_t st) {
+  return nt == 1 ? launch<D, F16, 1>(a, st) : nt == 2 ? launch<D, F16, 2>(a, st) : launch<D, F16, 4>(a, st);
+}
 
 }  // namespace
 }  // namespace scfa
@@ -113,7 +746,7 @@ extern "C" {
 
 size_t scfa_cache4_attn_workspace_size(int N, int R, int Hq, int Hkv, int D) {
   if (N < 1 || R < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  return sizeof(WsHeader);
+  return c4_ws(D).total;
 }
 
 scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_head, const uint8_t* cache,
@@ -127,23 +760,34 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * page_size >= (1ll << 31))
+      static_cast<long long>(max_pages) * page_size >= (1ll << 31) || static_cast<long long>(N) * Hq >= (1ll << 31))
     return SCFA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SCFA_ERR_INVALID;
   if ((q_token | q_head | o_token | o_head) & 7) return SCFA_ERR_INVALID;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < scfa_cache4_attn_workspace_size(N, R, Hq, Hkv, D))
-    return SCFA_ERR_WORKSPACE;
+  const int G = Hq / Hkv, nt = c4_nt(N, R, G);
+  const C4Ws w = c4_ws(D);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total) return SCFA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const C4AttnArgs a = {q, q_token, q_head, cache, page_size, n_pages, table, max_pages, q_start, vis, N, R, Hq, Hkv,
-                        scale, o, o_token, o_head, lse, static_cast<int*>(ws)};
-  clear_status_kernel<<<1, 1, 0, st>>>(a.status);
-  const bool f = dtype == SCFA_DTYPE_F16;
-  auto kern = D == 64 ? (f ? attn_simple_kernel<64, true> : attn_simple_kernel<64, false>)
-                      : (f ? attn_simple_kernel<128, true> : attn_simple_kernel<128, false>);
-  if (static_cast<long long>(N) * Hq > INT_MAX) return SCFA_ERR_UNSUPPORTED;
-  kern<<<N * Hq, 128, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return SCFA_ERR_CUDA;
+  const bool f16 = dtype == SCFA_DTYPE_F16;
+  char* p = static_cast<char*>(ws);
+  C4AttnArgs a = {};
+  a.q = q, a.qt = q_token, a.qh = q_head;
+  a.cache = cache, a.page_size = page_size, a.n_pages = n_pages;
+  while ((1 << a.log_ps) < page_size) ++a.log_ps;
+  a.table = table, a.max_pages = max_pages, a.q_start = q_start, a.vis = vis;
+  a.N = N, a.R = R, a.Hq = Hq, a.Hkv = Hkv, a.G = G;
+  // K's scales carry 2^-16, its fp16 codes 2^-24
+  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (f16 ? 0x1p40 : 0x1p16));
+  a.o = o, a.ot = o_token, a.oh = o_head, a.lse = lse;
+  a.status = reinterpret_cast<int*>(p);
+  a.desc = reinterpret_cast<C4Desc*>(p + w.desc);
+  a.ml = reinterpret_cast<float*>(p + w.ml);
+  a.part = reinterpret_cast<float*>(p + w.part);
+  a.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0;
+  const cudaError_t e = D == 64 ? (f16 ? launch_nt<64, true>(nt, a, st) : launch_nt<64, false>(nt, a, st))
+                                : (f16 ? launch_nt<128, true>(nt, a, st) : launch_nt<128, false>(nt, a, st));
+  if (e != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;
 }

@@ -397,6 +397,17 @@ def test_attn_wild_row_bounds(scfa):
     torch.cuda.synchronize()
 
 
+def test_attn_stalled_pipeline_reports_a_timeout(scfa):
+    p = attn_problem(scfa, 9, [300, 20], [1, 1], 8, 2, 64, 16, BF)
+    N, Hq, D = p["q"].shape
+    o, lse = torch.empty_like(p["q"]), torch.empty((N, Hq), device="cuda")
+    ws = scfa.workspace(scfa.cache4_attn_workspace_size(N, 2, Hq, 2, D))
+    scfa.scfa_cache4_attn(p["q"], p["cache"], 16, p["table"], p["q_start"], p["vis"], 0.125, o, lse, ws,
+                          scfa.FLAG_DEBUG_STALL)
+    assert scfa.scfa_get_device_status(ws) == 5
+    check_attn(scfa, p)  # the device stays usable
+
+
 # ---------------------------------------------------------------- steps
 @pytest.mark.parametrize("dt,D,Hq,Hkv,ps", [(BF, 64, 12, 12, 64), (HF, 128, 8, 2, 16)])
 @pytest.mark.parametrize("drop", [None, 0.6])
