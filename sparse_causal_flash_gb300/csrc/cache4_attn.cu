@@ -18,12 +18,17 @@
 // shuffle between the copy and the MMA. The matrix instructions are the
 // warp-level ones: a decode step does 8 * rows flops per cached byte, far
 // below what any of them bounds.
-//   K: codes become 128 + (c + 8) in bf16 by one AND-OR (for fp16 queries the
-//      bits of c + 8 are read as a subnormal, (c + 8) 2^-24); the offset is
-//      taken off by starting the accumulator at -136 sum(q) (-8 2^-24 sum(q)),
-//      and the group's scale multiplies the fp32 sum.
-//   V: codes become c s in bf16 by one FMA (exact: seven significant bits);
-//      P is rounded to bf16, as in the training kernels.
+//   Both operands are fp16, whatever the rows' type. Unpacking is bit work at
+//   half the rate of the FMA pipe, so it is what bounds the kernel: per eight
+//   codes one shift and four AND(-OR)s, the rest is left to the FMA pipe.
+//   K: the bits of c + 8 are read as a subnormal, (c + 8) 2^-24 (2^-20 for
+//      the upper half of a byte, whose query channels are divided by 16); the
+//      offset comes off as -8 sum(q), with the group's scale, in fp32. A query
+//      row is brought to a largest magnitude in [2^13, 2^14) by a power of two,
+//      which fp16 and bf16 values survive down to 2^-30 of that magnitude.
+//   V: codes become c s in fp16 (exact: seven significant bits below 2^16).
+//      P is held times 2^7 in fp16, so weights down to 2^-32 of the largest
+//      count.
 #include <climits>
 #include <cmath>
 
@@ -58,7 +63,7 @@ struct C4AttnArgs {
   int max_pages;
   const int32_t *q_start, *vis;
   int N, R, Hq, Hkv, G;
-  float factor;  // score in log2 units = accumulated sum * factor
+  float factor;  // scale * log2(e) * 2^24
   uint16_t* o;
   long long ot, oh;
   float* lse;
@@ -67,6 +72,10 @@ struct C4AttnArgs {
   float* part;  // [cta][2][rows][D]
   float* ml;    // [cta][2][rows][2]
   int stall;
+  // 16, 128 and fp16 1024 twice, as values the compiler does not know: a
+  // multiplication then stays on the FMA pipe (a shift-and-add is ALU work,
+  // which is what is short), and an AND-OR stays one instruction
+  uint32_t k16, k128, magic;
 };
 
 // What a stage holds.
@@ -75,7 +84,7 @@ struct C4Stage {
   int base;                    // position of the chunk's first token
   int tiles;                   // bit t: tile t was copied
   int flags;
-  int pad;
+  int seen;                    // tokens that the item's last row sees
 };
 enum { kFirst = 1, kLast = 2, kOpenStart = 4, kOpenEnd = 8 };
 
@@ -92,24 +101,27 @@ struct C4Cfg {
   static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kPartBytes + kQBytes;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = a b + c, 16 x 8 x 16
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                        float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// (a & b) | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
 // transpose of an 8 x 8 matrix of 16-bit values, one row per four lanes
@@ -311,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         d.head = h;
         d.base = ch * kCh;
         d.tiles = static_cast<int>(mask);
+        d.seen = seen;
         const bool began = ch <= u, goes_on = !last_chunk && u + 1 == n_units;  // the item, in this piece
         d.flags = (first ? kFirst : 0) | (last_chunk || goes_on ? kLast : 0) | (began ? 0 : kOpenStart) |
                   (goes_on ? kOpenEnd : 0);
@@ -368,8 +381,10 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
                      static_cast<size_t>(w) * NT * G * 32;
   float O[NT][G][2][4];
   uint32_t Q[C::kQSmem ? 1 : NT][G][4];
-  float x0[NT][G][2];  // accumulator start per group and column
-  float m[NT][2], l[NT][2];
+  float x0[NT][G][4];     // -8 sum(q) 2^-24 per group and accumulator
+  const uint32_t k16 = a.k16, k128 = a.k128, magic = a.magic;
+  float factor[NT][2];    // score in log2 units = sum * factor
+  float m[NT][2], l[NT][2];  // reference of the weights (a running maximum - 7), and their sum
   int seen[NT][2], full_to = 0, items = 0;
   for (int u = 0; u < n_units; ++u) {
     const int s = u % S;
@@ -383,24 +398,49 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         const bool in = row < d.rows;
         const int tok = row / a.G;
         const uint16_t* qp = a.q + (d.tok0 + tok) * a.qt + (d.head * a.G + row - tok * a.G) * a.qh + 8 * j;
+        uint4 v[G];
+        float mx = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint4 v = in ? *reinterpret_cast<const uint4*>(qp + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
-          const float2 f0 = c4_unpack<F16>(v.x), f1 = c4_unpack<F16>(v.y), f2 = c4_unpack<F16>(v.z),
-                       f3 = c4_unpack<F16>(v.w);
-          float sum = ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+          v[g] = in ? *reinterpret_cast<const uint4*>(qp + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+          const float2 f0 = c4_unpack<F16>(v[g].x), f1 = c4_unpack<F16>(v[g].y), f2 = c4_unpack<F16>(v[g].z),
+                       f3 = c4_unpack<F16>(v[g].w);
+          mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                               fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // exponent of the power of two that brings the row to [2^13, 2^14)
+        const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
+        const float up = __uint_as_float(ex << 23);
+        const float fac = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
+        factor[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * j);
+        factor[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * j + 4);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint32_t in4[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
+          uint32_t h[4];
+          float sum = 0.f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = c4_unpack<F16>(in4[y]);
+            const float k = (y & 1) ? up * 0.0625f : up;
+            h[y] = c4_pack<true>(f.x * k, f.y * k);
+            sum += f.x * up + f.y * up;
+          }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= F16 ? -8.f * 0x1p-24f : -136.f;
-          x0[nt][g][0] = __shfl_sync(0xffffffffu, sum, 8 * j);
-          x0[nt][g][1] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
+          sum *= -8.f * 0x1p-24f;
+          x0[nt][g][0] = x0[nt][g][2] = __shfl_sync(0xffffffffu, sum, 8 * j);
+          x0[nt][g][1] = x0[nt][g][3] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
           if (C::kQSmem) {
-            s_q[(nt * G + g) * 32 + lane] = v;
+            s_q[(nt * G + g) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
           } else {
-            Q[nt][g][0] = v.x, Q[nt][g][1] = v.y, Q[nt][g][2] = v.z, Q[nt][g][3] = v.w;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) Q[C::kQSmem ? 0 : nt][g][y] = h[y];
           }
-          O[nt][g][0][0] = O[nt][g][0][1] = O[nt][g][0][2] = O[nt][g][0][3] = 0.f;
-          O[nt][g][1][0] = O[nt][g][1][1] = O[nt][g][1][2] = O[nt][g][1][3] = 0.f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) O[nt][g][0][y] = O[nt][g][1][y] = 0.f;
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -440,30 +480,25 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint32_t magic = F16 ? 0u : 0x43004300u;
           uint32_t A[2][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            A[k][0] = ((kw[0][g] >> (8 * k)) & 0x000F000Fu) | magic;
-            A[k][1] = ((kw[1][g] >> (8 * k)) & 0x000F000Fu) | magic;
-            A[k][2] = ((kw[0][g] >> (8 * k + 4)) & 0x000F000Fu) | magic;
-            A[k][3] = ((kw[1][g] >> (8 * k + 4)) & 0x000F000Fu) | magic;
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t lo = kw[y][g], hi = lo >> 8;
+            A[0][y] = lo & 0x000F000Fu, A[0][y + 2] = lo & 0x00F000F0u;
+            A[1][y] = hi & 0x000F000Fu, A[1][y + 2] = hi & 0x00F000F0u;
           }
-          const float s0 = c4_scale((ks[0] >> (8 * g)) & 255u, 96u), s1 = c4_scale((ks[1] >> (8 * g)) & 255u, 96u);
+          // scale = (b << 20) + (112 << 23), from the byte at bits 16-23
+          const float s0 = __uint_as_float(__byte_perm(ks[0], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
+          const float s1 = __uint_as_float(__byte_perm(ks[1], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {x0[nt][g][0], x0[nt][g][1], x0[nt][g][0], x0[nt][g][1]};
+            float acc[4];
             uint4 qv;
             if (C::kQSmem) qv = s_q[(nt * G + g) * 32 + lane];
             else qv = make_uint4(Q[C::kQSmem ? 0 : nt][g][0], Q[C::kQSmem ? 0 : nt][g][1],
                                  Q[C::kQSmem ? 0 : nt][g][2], Q[C::kQSmem ? 0 : nt][g][3]);
-            if (F16) {
-              mma_f16(acc, A[0], qv.x, qv.y);
-              mma_f16(acc, A[1], qv.z, qv.w);
-            } else {
-              mma_bf16(acc, A[0], qv.x, qv.y);
-              mma_bf16(acc, A[1], qv.z, qv.w);
-            }
+            mma_f16(acc, A[0], qv.x, qv.y, x0[nt][g][0], x0[nt][g][1], x0[nt][g][2], x0[nt][g][3]);
+            mma_f16(acc, A[1], qv.z, qv.w, acc[0], acc[1], acc[2], acc[3]);
             x[i][nt][0] = fmaf(acc[0], s0, x[i][nt][0]);
             x[i][nt][1] = fmaf(acc[1], s0, x[i][nt][1]);
             x[i][nt][2] = fmaf(acc[2], s1, x[i][nt][2]);
@@ -480,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
               if (!there || key + 8 * (e >> 1) >= seen[nt][e & 1]) x[i][nt][e] = -INFINITY;
         }
       }
-      // ---- softmax: the maximum moves only when a score exceeds it by 2^8
+      // ---- softmax: the reference moves only when a weight would exceed 2^15
       uint32_t P[kTpw][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -488,7 +523,10 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 #pragma unroll
         for (int i = 0; i < kTpw; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) over |= fmaf(x[i][nt][e], a.factor, -m[nt][e & 1]) > 8.f;
+          for (int e = 0; e < 4; ++e) {
+            // in log2 units over the reference (computed again if it moves)
+            over |= fmaf(x[i][nt][e], factor[nt][e & 1], -m[nt][e & 1]) > 15.f;
+          }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -497,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             for (int i = 0; i < kTpw; ++i) mx = fmaxf(mx, fmaxf(x[i][nt][c], x[i][nt][c + 2]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(m[nt][c], mx * a.factor);
+            mx = fmaxf(m[nt][c], fmaf(mx, factor[nt][c], -7.f));
             const float f = ex2_approx(m[nt][c] - mx);
             m[nt][c] = mx;
             l[nt][c] *= f;
@@ -511,11 +549,11 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         for (int i = 0; i < kTpw; ++i) {
           float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(x[i][nt][e], a.factor, -m[nt][e & 1]));
+          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(x[i][nt][e], factor[nt][e & 1], -m[nt][e & 1]));
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
-          P[i][nt][0] = transpose8(pack_bf16x2(p[0], p[1]));
-          P[i][nt][1] = transpose8(pack_bf16x2(p[2], p[3]));
+          P[i][nt][0] = transpose8(c4_pack<true>(p[0], p[1]));
+          P[i][nt][1] = transpose8(c4_pack<true>(p[2], p[3]));
         }
       }
       // ---- values
@@ -540,25 +578,49 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             vs[y][0] = f & 0xFFFFu, vs[y][1] = f >> 16;
           }
         }
+        // scale bytes behind the last visible token are not a row's: they could
+        // be infinite in fp16
+        const int key0 = d.base + (t0 + i) * kC4Tile;
+        if (!((d.tiles >> (t0 + i)) & 1) || key0 + kC4Tile > d.seen) {
+          const int n = (d.tiles >> (t0 + i)) & 1 ? d.seen - key0 : 0;
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              if (8 * y + 2 * j + b >= n) vs[y][b] = 0;
+        }
+        uint32_t sb[2][2][2];  // [y][group parity][key]: two scale bytes, in bits 0-7 and 16-23
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            sb[y][0][b] = vs[y][b] & 0x00FF00FFu;
+            sb[y][1][b] = __byte_perm(vs[y][b], 0u, 0x4341);
+          }
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t A[2][4];  // channels 4 r + 2 t, + 1 of two m16 tiles
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t pair = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
-            // the two keys' scales times 2^-16, and -136 of them
-            const uint32_t sb = __byte_perm(vs[y][0], vs[y][1], g | g << 4 | (4 + g) << 8 | (4 + g) << 12);
-            const uint32_t sc = ((sb << 4) & 0x0FF00FF0u) | 0x30003000u;
-            const uint32_t off = mul_bf16x2(sc, 0xC308C308u);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              A[c >> 1][(c & 1) + 2 * y] = fma_bf16x2(((pair >> (4 * c)) & 0x000F000Fu) | 0x43004300u, sc, off);
+            const uint32_t lo = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
+            const uint32_t hi = lo >> 8;
+            // the two keys' scales times 2: fp16 bits (b << 7) + (1 << 10), normal for every byte of a row
+            const uint32_t sc = __byte_perm(sb[y][g & 1][0], sb[y][g & 1][1], g < 2 ? 0x5410 : 0x7632) * k128 + 0x04000400u;
+            // 1024 + (c + 8) and 1024 + 16 (c + 8) -> c / 2
+            const uint32_t c0 = fma_f16x2(and_or(lo, 0x000F000Fu, magic), 0x38003800u, 0xE008E008u);
+            const uint32_t c1 = fma_f16x2(and_or(lo, 0x00F000F0u, magic), 0x28002800u, 0xD080D080u);
+            const uint32_t c2 = fma_f16x2(and_or(hi, 0x000F000Fu, magic), 0x38003800u, 0xE008E008u);
+            const uint32_t c3 = fma_f16x2(and_or(hi, 0x00F000F0u, magic), 0x28002800u, 0xD080D080u);
+            A[0][2 * y] = mul_f16x2(c0, sc), A[0][2 * y + 1] = mul_f16x2(c1, sc);
+            A[1][2 * y] = mul_f16x2(c2, sc), A[1][2 * y + 1] = mul_f16x2(c3, sc);
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(O[nt][g][0], A[0], P[i][nt][0], P[i][nt][1]);
-            mma_bf16(O[nt][g][1], A[1], P[i][nt][0], P[i][nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              float(&z)[4] = O[nt][g][t];
+              mma_f16(z, A[t], P[i][nt][0], P[i][nt][1], z[0], z[1], z[2], z[3]);
+            }
         }
       }
     }
@@ -613,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
           const bool tail = d.flags & kOpenStart, open = d.flags & kOpenEnd;
           if (!tail && !open) {
             const int tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-            const float inv = lt > 0.f ? 0x1p16f / lt : 0.f;  // V's scales carried 2^-16
+            const float inv = lt > 0.f ? 1.f / lt : 0.f;
             uint32_t z[CPT / 2];
 #pragma unroll
             for (int e = 0; e < CPT; e += 2) z[e / 2] = c4_pack<F16>(o[e] * inv, o[e + 1] * inv);
@@ -640,55 +702,70 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 }
 
 // Joins the partial rows of the items that were cut, in the order of their
-// chunks, and gathers the CTAs' errors. One CTA per piece: the one in which
-// the item begins.
+// chunks, and gathers the CTAs' errors. One CTA per piece, the one in which an
+// item begins, and a warp per row: lanes first weigh the parts, then each
+// takes four channels of every part, so a long request's many parts are loaded
+// side by side.
+constexpr int kJoinThreads = 256;
 template <int D, bool F16, int ROWS>
-__global__ void __launch_bounds__(128) cache4_join_kernel(C4AttnArgs a, int n_desc) {
-  const int tid = threadIdx.x;
+__global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a, int n_desc) {
+  const int tid = threadIdx.x, lane = tid & 31;
   if (blockIdx.x == 0) {
+    __shared__ int s_err[kJoinThreads / 32];
     int err = 0;
-    for (int i = tid; i < n_desc; i += 128) err = max(err, a.desc[i].err);
+    for (int i = tid; i < n_desc; i += kJoinThreads) err = max(err, a.desc[i].err);
     err = __reduce_max_sync(0xffffffffu, err);
-    __shared__ int s_err[4];
-    if ((tid & 31) == 0) s_err[tid >> 5] = err;
+    if (lane == 0) s_err[tid >> 5] = err;
     __syncthreads();
-    if (tid == 0) *a.status = max(max(s_err[0], s_err[1]), max(s_err[2], s_err[3]));
+    if (tid == 0) {
+      for (int i = 1; i < kJoinThreads / 32; ++i) err = max(err, s_err[i]);
+      *a.status = err;
+    }
   }
   const C4Desc d = a.desc[blockIdx.x];
   if (d.parts <= 0) return;
-  constexpr int CPT = D / 16;
-  const int ch0 = (tid & 15) * CPT;
-  for (int row = tid >> 4; row < ROWS; row += 8) {
-    const int grow = d.row0 + row;
-    if (grow >= d.rows) break;
+  constexpr int LPP = D / 4;       // lanes per part
+  constexpr int PPW = 32 / LPP;    // parts side by side in a warp
+  const int n = d.parts + 1, sub = lane / LPP, ch0 = lane % LPP * 4;
+  for (int row = tid >> 5; row < ROWS && d.row0 + row < d.rows; row += kJoinThreads / 32) {
     auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
     float mt = kNoMax;
-    for (int i = 0; i <= d.parts; ++i) mt = fmaxf(mt, a.ml[2 * at(i)]);
-    float lt = 0.f, o[CPT];
+    for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
 #pragma unroll
-    for (int e = 0; e < CPT; ++e) o[e] = 0.f;
-    for (int i = 0; i <= d.parts; ++i) {
-      const long long p = at(i);
-      const float f = ex2_approx(a.ml[2 * p] - mt);
-      lt = fmaf(a.ml[2 * p + 1], f, lt);
-#pragma unroll
-      for (int e = 0; e < CPT; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(a.part + p * D + ch0 + e);
-        o[e] = fmaf(v.x, f, o[e]), o[e + 1] = fmaf(v.y, f, o[e + 1]);
-        o[e + 2] = fmaf(v.z, f, o[e + 2]), o[e + 3] = fmaf(v.w, f, o[e + 3]);
+    for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    float lt = 0.f;
+    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int base = 0; base < n; base += 32) {
+      float f = 0.f;
+      if (base + lane < n) {
+        const float2 v = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
+        f = ex2_approx(v.x - mt);
+        lt = fmaf(v.y, f, lt);
+      }
+      const int cnt = min(32, n - base);
+#pragma unroll 8
+      for (int i = 0; i < cnt; i += PPW) {
+        const float fi = __shfl_sync(0xffffffffu, f, i + sub);
+        if (i + sub < cnt) {
+          const float4 v = *reinterpret_cast<const float4*>(a.part + at(base + i + sub) * D + ch0);
+          o4.x = fmaf(v.x, fi, o4.x), o4.y = fmaf(v.y, fi, o4.y);
+          o4.z = fmaf(v.z, fi, o4.z), o4.w = fmaf(v.w, fi, o4.w);
+        }
       }
     }
-    const int tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-    const float inv = lt > 0.f ? 0x1p16f / lt : 0.f;
-    uint32_t z[CPT / 2];
 #pragma unroll
-    for (int e = 0; e < CPT; e += 2) z[e / 2] = c4_pack<F16>(o[e] * inv, o[e + 1] * inv);
-    uint16_t* op = a.o + tok * a.ot + head * a.oh + ch0;
-    if (CPT == 8) *reinterpret_cast<uint4*>(op) = make_uint4(z[0], z[1], z[CPT / 2 - 2], z[CPT / 2 - 1]);
-    else *reinterpret_cast<uint2*>(op) = make_uint2(z[0], z[1]);
-    if ((tid & 15) == 0)
-      a.lse[static_cast<long long>(tok) * a.Hq + head] =
-          lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    if (PPW == 2) {
+      o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
+      o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
+    }
+    const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    if (sub == 0)
+      *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
+          make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
+    if (lane == 0)
+      a.lse[static_cast<long long>(tok) * a.Hq + head] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
   }
 }
 
@@ -728,7 +805,7 @@ cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, C::kSmem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cache4_join_kernel<D, F16, C::kRows><<<grid, 128, 0, st>>>(a, grid);
+  cache4_join_kernel<D, F16, C::kRows><<<grid, kJoinThreads, 0, st>>>(a, grid);
   return cudaGetLastError();
 }
 
@@ -777,14 +854,15 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   while ((1 << a.log_ps) < page_size) ++a.log_ps;
   a.table = table, a.max_pages = max_pages, a.q_start = q_start, a.vis = vis;
   a.N = N, a.R = R, a.Hq = Hq, a.Hkv = Hkv, a.G = G;
-  // K's scales carry 2^-16, its fp16 codes 2^-24
-  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (f16 ? 0x1p40 : 0x1p16));
+  // K's codes are read as multiples of 2^-24
+  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * 0x1p24);
   a.o = o, a.ot = o_token, a.oh = o_head, a.lse = lse;
   a.status = reinterpret_cast<int*>(p);
   a.desc = reinterpret_cast<C4Desc*>(p + w.desc);
   a.ml = reinterpret_cast<float*>(p + w.ml);
   a.part = reinterpret_cast<float*>(p + w.part);
   a.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0;
+  a.k16 = 16u, a.k128 = 128u, a.magic = 0x64006400u;
   const cudaError_t e = D == 64 ? (f16 ? launch_nt<64, true>(nt, a, st) : launch_nt<64, false>(nt, a, st))
                                 : (f16 ? launch_nt<128, true>(nt, a, st) : launch_nt<128, false>(nt, a, st));
   if (e != cudaSuccess) return SCFA_ERR_CUDA;

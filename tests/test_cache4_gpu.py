@@ -195,15 +195,16 @@ def test_append_and_read_past_32_bit_offsets(scfa):
 def check_rows(q, k, v, vis, scale, o, lse, dt):
     """Rows q [n, Hq, D] over k, v [L, Hkv, D] (the exact values the cache holds).
 
-    Bounds. u8 = 2^-8 is half a bf16 step, uo half a step of the output type.
-    A weight p is rounded to bf16 before it meets V: at most u8 sum(p |v|) in
-    O. A score is a sum of D exact products kept as sums of q (c + 136) <= 144
-    |q| in fp32, each of the D / 8 + 2 accumulations off by at most 2^-23 of
-    144 sum |q| over its group: e = (D / 8 + 2) 2^-23 144 scale sum_g s_g
-    sum |q_g|, plus 2^-20 of a score for the products with the scales and the
-    change of base. Weights are then off by 2 e relative (numerator and
+    Bounds. uo is half a step of the output type. A weight p is rounded to
+    fp16 (half a step: 2^-11) before it meets V: at most 2^-11 sum(p |v|) in O,
+    and weights below 2^-21 of the largest lose up to 2^-32 of it: 2^-32 n
+    max|v|. A score is, per group, a sum of 32 products q (c + 8) <= 15 |q| in
+    fp32, each of its D / 8 + 4 additions off by at most 2^-23 of 15 sum |q|, and
+    q itself by 2^-25 of its row's largest: e = (D / 8 + 4) 2^-23 15 scale
+    sum_g s_g sum |q_g| + 2^-20 |score| for the products with the scales and
+    the change of base. Weights are then off by 2 e relative (numerator and
     denominator), LSE by e; exp2 and the fp32 sums add 2^-18."""
-    uo, u8 = (2.0 ** -8 if dt is BF else 2.0 ** -11), 2.0 ** -8
+    uo, up = (2.0 ** -8 if dt is BF else 2.0 ** -11), 2.0 ** -11
     o, lse = dbl(o), dbl(lse)
     G, D = q.shape[1] // k.shape[1], q.shape[2]
     for t in range(q.shape[0]):
@@ -218,12 +219,12 @@ def check_rows(q, k, v, vis, scale, o, lse, dt):
             sg = np.abs(kk).reshape(n, -1, 32).max(-1) / 6 + 2.0 ** -15
             qg = np.abs(q[t, h]).reshape(-1, 32).sum(-1)
             s = np.abs(kk @ q[t, h] * scale).max()
-            e = (D / 8 + 2) * 2.0 ** -23 * 144 * scale * (sg @ qg).max() + 2.0 ** -20 * s
+            e = (D / 8 + 4) * 2.0 ** -23 * 15 * scale * (sg @ qg).max() + 2.0 ** -20 * s
             p = np.exp(kk @ q[t, h] * scale - rl)
             a = p @ np.abs(vv)
             assert abs(lse[t, h] - rl) <= e + 2.0 ** -18 * max(1.0, abs(rl)), (t, h, lse[t, h], rl)
             err = np.abs(o[t, h] - ro)
-            tol = uo * np.abs(ro) + (u8 + 2 * e + 2.0 ** -18) * a + 2.0 ** -24
+            tol = uo * np.abs(ro) + (up + 2 * e + 2.0 ** -18) * a + 2.0 ** -32 * n * np.abs(vv).max() + 2.0 ** -24
             assert np.all(err <= tol), (t, h, n, float((err / tol).max()))
 
 
