@@ -38,7 +38,15 @@
 namespace scfa {
 namespace {
 
-constexpr int kCh = 128;             // tokens per chunk
+#ifndef X_CTAS
+#define X_CTAS 3
+#define X_ST 3
+#define X_ST64 6
+#endif
+#ifndef X_CH
+#define X_CH 128
+#endif
+constexpr int kCh = X_CH;             // tokens per chunk
 constexpr int kChTiles = kCh / kC4Tile;
 constexpr int kWarps = 4;            // compute warps
 constexpr int kTpw = kChTiles / kWarps;
@@ -85,21 +93,39 @@ struct C4Stage {
   int tiles;                   // bit t: tile t was copied
   int flags;
   int seen;                    // tokens that the item's last row sees
+  int qslot;                   // where its queries are
+  int pad[3];
 };
 enum { kFirst = 1, kLast = 2, kOpenStart = 4, kOpenEnd = 8 };
+
+// The query rows of an item, as the producer leaves them: B operands of the
+// score MMAs, and per row what turns sums into scores.
+template <int D, int NT>
+struct C4Queries {
+  uint4 frag[NT][D / 32][32];
+  uint32_t offset[NT][32];  // B operand of the offset MMA
+  float factor[8 * NT];     // score in log2 units = sum * factor
+  int seen[8 * NT];         // tokens that the row sees
+  int all_see[4];           // [0]: tokens that every row sees
+};
 
 template <int D, int NT>
 struct C4Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = kChTiles * C4<D>::kTileBytes;
-  static constexpr int kCtas = NT == 1 ? 3 : NT == 2 ? 2 : 1;  // per SM
-  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 6);
-  static constexpr int kPad = D + 4;  // floats per row of the warps' partial O (conflict-free float4 stores)
-  static constexpr bool kQSmem = NT > 2;
-  static constexpr size_t kPartBytes = sizeof(float) * kWarps * kRows * kPad;
-  static constexpr size_t kQBytes = kQSmem ? static_cast<size_t>(kWarps) * NT * (D / 32) * 32 * 16 : 0;
-  static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStageBytes + kPartBytes + kQBytes;
+  static constexpr int kCtas = NT == 1 ? X_CTAS : NT == 2 ? 2 : 1;  // per SM
+  static constexpr int kStages = NT == 1 ? (D == 128 ? X_ST : X_ST64) : (D == 128 ? 4 : 6);
+  static constexpr size_t kPartBytes = sizeof(float) * kWarps * kRows * D;
+  static constexpr size_t kSmem =
+      static_cast<size_t>(kStages) * (kStageBytes + sizeof(C4Queries<D, NT>)) + kPartBytes;
 };
+
+// Place of four channels of a row in the warps' partial O: chunks are swapped
+// by row so that a warp's stores (two rows per lane quad) meet no bank twice.
+template <int D>
+__device__ __forceinline__ int c4_part_at(int row, int chunk) {
+  return row * D + (chunk ^ (row & 6)) * 4;
+}
 
 // d = a b + c, 16 x 8 x 16
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -107,6 +133,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+// d = a b, 16 x 8 x 8
+__device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -159,6 +191,83 @@ __device__ __forceinline__ int c4_seen(const C4AttnArgs& a, const C4Req& q, int 
 }
 __device__ __forceinline__ int c4_chunks(int seen) { return max(1, (seen + kCh - 1) / kCh); }
 
+// The query rows from row0 on of key head h, by one warp: lane (r8, j) takes
+// channels 32 g + 8 j + 0..7 of row r8, the B operand's place of them.
+template <int D, bool F16, int NT>
+__device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Req& q, int row0, int h, int lane,
+                                           C4Queries<D, NT>& s) {
+  constexpr int G = D / 32;
+  const int r8 = lane >> 2, j = lane & 3;
+  uint4 v[NT][G];
+  int seen[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = row0 + nt * 8 + r8, tok = row / a.G;
+    const bool in = row < q.rows;
+    const uint16_t* p = a.q + (q.tok0 + tok) * a.qt + (h * a.G + row - tok * a.G) * a.qh + 8 * j;
+#pragma unroll
+    for (int g = 0; g < G; ++g) v[nt][g] = in ? *reinterpret_cast<const uint4*>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+    seen[nt] = in ? a.vis[q.tok0 + tok] : INT_MAX;
+  }
+  int all = INT_MAX;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mx = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t in4[4] = {v[nt][g].x, v[nt][g].y, v[nt][g].z, v[nt][g].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float2 f = c4_unpack<F16>(in4[y]);
+        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // exponent of the power of two that brings the row to [2^13, 2^14)
+    const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
+    const float up = __uint_as_float(ex << 23);
+    float off[G];  // -4 2^-14 sum(q): times 2 s and 2^-10 it is -8 2^-24 sum(q) s
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t in4[4] = {v[nt][g].x, v[nt][g].y, v[nt][g].z, v[nt][g].w};
+      uint32_t hq[4];
+      float sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float2 f = c4_unpack<F16>(in4[y]);
+        const float k = (y & 1) ? up * 0.0625f : up;
+        hq[y] = c4_pack<true>(f.x * k, f.y * k);
+        sum += f.x * up + f.y * up;
+      }
+      s.frag[nt][g][lane] = make_uint4(hq[0], hq[1], hq[2], hq[3]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      off[g] = sum * -0x1p-12f;
+    }
+    // the offset MMA's k: the groups' sums rounded to fp16, then what that left
+    const int lo = G == 4 ? j >> 1 : j & 1, pair = G == 4 ? j & 1 : 0;
+    float o0 = pair ? off[G - 2] : off[0], o1 = pair ? off[G - 1] : off[1];
+    if (lo) {
+      o0 -= __half2float(__float2half_rn(o0));
+      o1 -= __half2float(__float2half_rn(o1));
+    }
+    s.offset[nt][lane] = G == 4 || j < 2 ? c4_pack<true>(o0, o1) : 0u;
+    if (j == 0) {
+      s.factor[nt * 8 + r8] = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
+      s.seen[nt * 8 + r8] = seen[nt];
+    }
+    all = min(all, seen[nt]);
+  }
+  all = __reduce_min_sync(0xffffffffu, all);
+  if (lane == 0) s.all_see[0] = all;
+}
+
+// a / b, in 32 bits where they hold it
+__device__ __forceinline__ long long c4_div(long long a, int b) {
+  return a >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 template <int D, bool F16, int NT>
 __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_kernel(C4AttnArgs a) {
   using L = C4<D>;
@@ -172,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   __shared__ long long s_prefix;
   __shared__ int s_req;
   __shared__ volatile int abort_flag;
-  float* const s_part = reinterpret_cast<float*>(smem + static_cast<size_t>(S) * C::kStageBytes);
+  C4Queries<D, NT>* const s_q = reinterpret_cast<C4Queries<D, NT>*>(smem + static_cast<size_t>(S) * C::kStageBytes);
+  float* const s_part = reinterpret_cast<float*>(s_q + S);
 
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   C4Desc* const desc = a.desc + blockIdx.x;
@@ -239,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
     block_incl(mine, &sum);
     total += sum;
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
+  const long long per = c4_div(total + gridDim.x - 1, gridDim.x);
   const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
   if (u0 >= u1) return;  // (the whole CTA)
   long long before = 0;
@@ -284,13 +394,13 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
     }
     seen = c4_seen<ROWS>(a, q, b);
     int chunks = c4_chunks(seen);
-    h = static_cast<int>(rem / chunks);
-    ch = static_cast<int>(rem % chunks);
+    h = static_cast<int>(c4_div(rem, chunks));
+    ch = static_cast<int>(rem - static_cast<long long>(h) * chunks);
     bool first = true;  // of its item in this CTA
 
     const int psub = min(a.page_size, kCh), npc = kCh / psub;
     int have_r = -1, have_p = 0, page = -1;  // the 32 pieces whose pages the lanes hold
-    int issued = 0;
+    int issued = 0, qslot = -1;
     for (int u = 0; u < n_units; ++u) {
       const int s = u % S;
       if (u >= S && !wait_all(&empty[s], ((u / S) & 1) ^ 1, &abort_flag, &desc->err)) break;
@@ -314,7 +424,20 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
       const uint32_t mask =
           __reduce_or_sync(0xffffffffu, tiles > 0 ? ((1u << tiles) - 1u) << (lane * (psub / kC4Tile)) : 0u);
       const uint32_t bytes = __popc(mask) * L::kTileBytes;
-      const bool last_chunk = ch + 1 == chunks;
+      const bool last_chunk = ch + 1 == chunks, go = !(a.stall && u == 0);
+      if (tiles > 0 && go) {
+        const long long tok = static_cast<long long>(p0 + lane) * psub;
+        const uint8_t* src =
+            a.cache + c4_tile_base(pg, a.Hkv, h, a.page_size, static_cast<int>(tok & (a.page_size - 1)), L::kTileBytes);
+        bulk_load(smem + static_cast<size_t>(s) * C::kStageBytes + lane * (psub / kC4Tile) * L::kTileBytes, src,
+                  tiles * L::kTileBytes, &full[s]);
+      }
+      if (first) {
+        // at most S items have units in the ring, so the slot of the item S before is free
+        if (++qslot == S) qslot = 0;
+        c4_queries<D, F16, NT>(a, q, b * ROWS, h, lane, s_q[qslot]);
+      }
+      __syncwarp();
       if (lane == 0) {
         C4Stage d;
         d.tok0 = q.tok0;
@@ -324,27 +447,21 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         d.base = ch * kCh;
         d.tiles = static_cast<int>(mask);
         d.seen = seen;
+        d.qslot = qslot;
         const bool began = ch <= u, goes_on = !last_chunk && u + 1 == n_units;  // the item, in this piece
         d.flags = (first ? kFirst : 0) | (last_chunk || goes_on ? kLast : 0) | (began ? 0 : kOpenStart) |
                   (goes_on ? kOpenEnd : 0);
         stage[s] = d;
         if (goes_on && began) {
           const long long last = u1 - 1 + (chunks - 1 - ch);  // the item's last unit
-          desc->parts = static_cast<int>(last / per - blockIdx.x);
+          desc->parts = static_cast<int>(c4_div(last, static_cast<int>(per)) - blockIdx.x);
           desc->tok0 = q.tok0;
           desc->rows = q.rows;
           desc->row0 = b * ROWS;
           desc->head = h;
         }
-        if (!(a.stall && u == 0)) mbar_arrive_expect_tx(&full[s], bytes);
-      }
-      __syncwarp();
-      if (tiles > 0 && !(a.stall && u == 0)) {
-        const long long tok = static_cast<long long>(p0 + lane) * psub;
-        const uint8_t* src =
-            a.cache + c4_tile_base(pg, a.Hkv, h, a.page_size, static_cast<int>(tok & (a.page_size - 1)), L::kTileBytes);
-        bulk_load(smem + static_cast<size_t>(s) * C::kStageBytes + lane * (psub / kC4Tile) * L::kTileBytes, src,
-                  tiles * L::kTileBytes, &full[s]);
+        // (the copies may have landed already: the phase ends with this arrival and all bytes)
+        if (go) mbar_arrive_expect_tx(&full[s], bytes);
       }
       issued = u + 1;
       // next chunk
@@ -377,142 +494,103 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 
   // =================================================== compute warps
   const int r8 = lane >> 2, j = lane & 3;
-  uint4* const s_q = reinterpret_cast<uint4*>(smem + static_cast<size_t>(S) * C::kStageBytes + C::kPartBytes) +
-                     static_cast<size_t>(w) * NT * G * 32;
-  float O[NT][G][2][4];
-  uint32_t Q[C::kQSmem ? 1 : NT][G][4];
-  float x0[NT][G][4];     // -8 sum(q) 2^-24 per group and accumulator
   const uint32_t k16 = a.k16, k128 = a.k128, magic = a.magic;
-  float factor[NT][2];    // score in log2 units = sum * factor
+  const uint32_t off_sel = G == 4 && (j & 1) ? 0x4342 : 0x4140;  // the scale bytes of this lane's k of the offset MMA
+  float O[NT][G][2][4];
+  float factor[NT][2];
   float m[NT][2], l[NT][2];  // reference of the weights (a running maximum - 7), and their sum
-  int seen[NT][2], full_to = 0, items = 0;
+  int items = 0;
   for (int u = 0; u < n_units; ++u) {
     const int s = u % S;
     if (!wait_all(&full[s], (u / S) & 1, &abort_flag, &desc->err)) return;
     const C4Stage d = stage[s];
+    const C4Queries<D, NT>& qs = s_q[d.qslot];
     if (d.flags & kFirst) {
-      int lo = INT_MAX;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int row = d.row0 + nt * 8 + r8;
-        const bool in = row < d.rows;
-        const int tok = row / a.G;
-        const uint16_t* qp = a.q + (d.tok0 + tok) * a.qt + (d.head * a.G + row - tok * a.G) * a.qh + 8 * j;
-        uint4 v[G];
-        float mx = 0.f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          v[g] = in ? *reinterpret_cast<const uint4*>(qp + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
-          const float2 f0 = c4_unpack<F16>(v[g].x), f1 = c4_unpack<F16>(v[g].y), f2 = c4_unpack<F16>(v[g].z),
-                       f3 = c4_unpack<F16>(v[g].w);
-          mx = fmaxf(mx, fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
-                               fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // exponent of the power of two that brings the row to [2^13, 2^14)
-        const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
-        const float up = __uint_as_float(ex << 23);
-        const float fac = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
-        factor[nt][0] = __shfl_sync(0xffffffffu, fac, 8 * j);
-        factor[nt][1] = __shfl_sync(0xffffffffu, fac, 8 * j + 4);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t in4[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
-          uint32_t h[4];
-          float sum = 0.f;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = c4_unpack<F16>(in4[y]);
-            const float k = (y & 1) ? up * 0.0625f : up;
-            h[y] = c4_pack<true>(f.x * k, f.y * k);
-            sum += f.x * up + f.y * up;
-          }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          sum *= -8.f * 0x1p-24f;
-          x0[nt][g][0] = x0[nt][g][2] = __shfl_sync(0xffffffffu, sum, 8 * j);
-          x0[nt][g][1] = x0[nt][g][3] = __shfl_sync(0xffffffffu, sum, 8 * j + 4);
-          if (C::kQSmem) {
-            s_q[(nt * G + g) * 32 + lane] = make_uint4(h[0], h[1], h[2], h[3]);
-          } else {
-#pragma unroll
-            for (int y = 0; y < 4; ++y) Q[C::kQSmem ? 0 : nt][g][y] = h[y];
-          }
+        for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int y = 0; y < 4; ++y) O[nt][g][0][y] = O[nt][g][1][y] = 0.f;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = d.row0 + nt * 8 + 2 * j + c;
-          seen[nt][c] = col < d.rows ? a.vis[d.tok0 + col / a.G] : INT_MAX;
-          lo = min(lo, seen[nt][c]);
-          m[nt][c] = kNoMax;
-          l[nt][c] = 0.f;
-        }
+        const float2 f = *reinterpret_cast<const float2*>(&qs.factor[nt * 8 + 2 * j]);
+        factor[nt][0] = f.x, factor[nt][1] = f.y;
+        m[nt][0] = m[nt][1] = kNoMax;
+        l[nt][0] = l[nt][1] = 0.f;
       }
-      full_to = __reduce_min_sync(0xffffffffu, lo);
-      if (C::kQSmem) __syncwarp();
     }
     const int t0 = w * kTpw;
     if ((d.tiles >> t0) & ((1 << kTpw) - 1)) {
       const uint8_t* tile0 = smem + static_cast<size_t>(s) * C::kStageBytes + t0 * L::kTileBytes;
       float x[kTpw][NT][4];
       // ---- scores
+      uint32_t kw[kTpw][2][G], ks[kTpw][2];
 #pragma unroll
       for (int i = 0; i < kTpw; ++i) {
         const uint8_t* tile = tile0 + i * L::kTileBytes;
-        uint32_t kw[2][G], ks[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const uint8_t* p = tile + L::k_row(r8 + 8 * y) + j * 4 * G;
           if (G == 4) {
             const uint4 v = *reinterpret_cast<const uint4*>(p);
-            kw[y][0] = v.x, kw[y][1] = v.y, kw[y][G - 2] = v.z, kw[y][G - 1] = v.w;
-            ks[y] = *reinterpret_cast<const uint32_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
+            kw[i][y][0] = v.x, kw[i][y][1] = v.y, kw[i][y][G - 2] = v.z, kw[i][y][G - 1] = v.w;
+            ks[i][y] = *reinterpret_cast<const uint32_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
-            kw[y][0] = v.x, kw[y][1] = v.y;
-            ks[y] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
+            kw[i][y][0] = v.x, kw[i][y][1] = v.y;
+            ks[i][y] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
           }
         }
+        // the offsets of the codes: twice the scales (fp16) by -4 sum(q)
+        const uint32_t a0 = __byte_perm(ks[i][0], 0u, off_sel) * k128 + 0x04000400u;
+        const uint32_t a1 = __byte_perm(ks[i][1], 0u, off_sel) * k128 + 0x04000400u;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_f16_k8(x[i][nt], a0, a1, qs.offset[nt][lane]);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
+          for (int e = 0; e < 4; ++e) x[i][nt][e] *= 0x1p-10f;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        uint4 qv[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qv[nt] = qs.frag[nt][g][lane];
+#pragma unroll
+        for (int i = 0; i < kTpw; ++i) {
           uint32_t A[2][4];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t lo = kw[y][g], hi = lo >> 8;
+            const uint32_t lo = kw[i][y][g], hi = lo >> 8;
             A[0][y] = lo & 0x000F000Fu, A[0][y + 2] = lo & 0x00F000F0u;
             A[1][y] = hi & 0x000F000Fu, A[1][y + 2] = hi & 0x00F000F0u;
           }
           // scale = (b << 20) + (112 << 23), from the byte at bits 16-23
-          const float s0 = __uint_as_float(__byte_perm(ks[0], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
-          const float s1 = __uint_as_float(__byte_perm(ks[1], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
+          const float s0 = __uint_as_float(__byte_perm(ks[i][0], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
+          const float s1 = __uint_as_float(__byte_perm(ks[i][1], 0u, 0x4044 | g << 8) * k16 + (112u << 23));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float acc[4];
-            uint4 qv;
-            if (C::kQSmem) qv = s_q[(nt * G + g) * 32 + lane];
-            else qv = make_uint4(Q[C::kQSmem ? 0 : nt][g][0], Q[C::kQSmem ? 0 : nt][g][1],
-                                 Q[C::kQSmem ? 0 : nt][g][2], Q[C::kQSmem ? 0 : nt][g][3]);
-            mma_f16(acc, A[0], qv.x, qv.y, x0[nt][g][0], x0[nt][g][1], x0[nt][g][2], x0[nt][g][3]);
-            mma_f16(acc, A[1], qv.z, qv.w, acc[0], acc[1], acc[2], acc[3]);
+            mma_f16(acc, A[0], qv[nt].x, qv[nt].y, 0.f, 0.f, 0.f, 0.f);
+            mma_f16(acc, A[1], qv[nt].z, qv[nt].w, acc[0], acc[1], acc[2], acc[3]);
             x[i][nt][0] = fmaf(acc[0], s0, x[i][nt][0]);
             x[i][nt][1] = fmaf(acc[1], s0, x[i][nt][1]);
             x[i][nt][2] = fmaf(acc[2], s1, x[i][nt][2]);
             x[i][nt][3] = fmaf(acc[3], s1, x[i][nt][3]);
           }
         }
-        const int key = d.base + (t0 + i) * kC4Tile + r8;
-        const bool there = (d.tiles >> (t0 + i)) & 1;
-        if (!there || key - r8 + kC4Tile > full_to) {
+      }
+      const int key0 = d.base + t0 * kC4Tile;
+      const uint32_t there = static_cast<uint32_t>(d.tiles) >> t0 & ((1u << kTpw) - 1u);
+      if (there != (1u << kTpw) - 1u || key0 + kTpw * kC4Tile > qs.all_see[0]) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const int2 seen = *reinterpret_cast<const int2*>(&qs.seen[nt * 8 + 2 * j]);
+#pragma unroll
+          for (int i = 0; i < kTpw; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!there || key + 8 * (e >> 1) >= seen[nt][e & 1]) x[i][nt][e] = -INFINITY;
+              if (!(there >> i & 1) || key0 + i * kC4Tile + r8 + 8 * (e >> 1) >= ((e & 1) ? seen.y : seen.x))
+                x[i][nt][e] = -INFINITY;
         }
       }
       // ---- softmax: the reference moves only when a weight would exceed 2^15
@@ -580,9 +658,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         }
         // scale bytes behind the last visible token are not a row's: they could
         // be infinite in fp16
-        const int key0 = d.base + (t0 + i) * kC4Tile;
-        if (!((d.tiles >> (t0 + i)) & 1) || key0 + kC4Tile > d.seen) {
-          const int n = (d.tiles >> (t0 + i)) & 1 ? d.seen - key0 : 0;
+        if (there != (1u << kTpw) - 1u || key0 + kTpw * kC4Tile > d.seen) {
+          const int n = there >> i & 1 ? d.seen - key0 - i * kC4Tile : 0;
 #pragma unroll
           for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -641,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
           if (r8 == 0) s_ml[w][row][0] = m[nt][c], s_ml[w][row][1] = z;
 #pragma unroll
           for (int g = 0; g < G; ++g)
-            *reinterpret_cast<float4*>(s_part + (w * ROWS + row) * C::kPad + 32 * g + 4 * r8) =
+            *reinterpret_cast<float4*>(s_part + c4_part_at<D>(w * ROWS + row, 8 * g + r8)) =
                 make_float4(O[nt][g][0][c], O[nt][g][0][c + 2], O[nt][g][1][c], O[nt][g][1][c + 2]);
         }
       }
@@ -664,10 +741,9 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
           for (int i = 0; i < kWarps; ++i) {
             const float f = ex2_approx(s_ml[i][row][0] - mt);
             lt = fmaf(s_ml[i][row][1], f, lt);
-            const float* p = s_part + (i * ROWS + row) * C::kPad + ch0;
 #pragma unroll
             for (int e = 0; e < CPT; e += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(p + e);
+              const float4 v = *reinterpret_cast<const float4*>(s_part + c4_part_at<D>(i * ROWS + row, (ch0 + e) / 4));
               o[e] = fmaf(v.x, f, o[e]), o[e + 1] = fmaf(v.y, f, o[e + 1]);
               o[e + 2] = fmaf(v.z, f, o[e + 2]), o[e + 3] = fmaf(v.w, f, o[e + 3]);
             }
@@ -703,69 +779,90 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 
 // Joins the partial rows of the items that were cut, in the order of their
 // chunks, and gathers the CTAs' errors. One CTA per piece, the one in which an
-// item begins, and a warp per row: lanes first weigh the parts, then each
-// takes four channels of every part, so a long request's many parts are loaded
-// side by side.
-constexpr int kJoinThreads = 256;
+// item begins, and two warps per row, each for half the parts: lanes first
+// weigh the parts, then each takes four channels of every part, eight parts
+// at a time.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 template <int D, bool F16, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a, int n_desc) {
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ float4 s_o[kJoinWarps / 2][32];
+  __shared__ float s_l[kJoinWarps / 2];
+  __shared__ int s_err[kJoinWarps];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const C4Desc d = a.desc[blockIdx.x];
   if (blockIdx.x == 0) {
-    __shared__ int s_err[kJoinThreads / 32];
     int err = 0;
     for (int i = tid; i < n_desc; i += kJoinThreads) err = max(err, a.desc[i].err);
     err = __reduce_max_sync(0xffffffffu, err);
-    if (lane == 0) s_err[tid >> 5] = err;
+    if (lane == 0) s_err[w] = err;
     __syncthreads();
     if (tid == 0) {
-      for (int i = 1; i < kJoinThreads / 32; ++i) err = max(err, s_err[i]);
+      for (int i = 1; i < kJoinWarps; ++i) err = max(err, s_err[i]);
       *a.status = err;
     }
   }
-  const C4Desc d = a.desc[blockIdx.x];
   if (d.parts <= 0) return;
-  constexpr int LPP = D / 4;       // lanes per part
-  constexpr int PPW = 32 / LPP;    // parts side by side in a warp
+  constexpr int LPP = D / 4;     // lanes per part
+  constexpr int PPW = 32 / LPP;  // parts side by side in a warp
   const int n = d.parts + 1, sub = lane / LPP, ch0 = lane % LPP * 4;
-  for (int row = tid >> 5; row < ROWS && d.row0 + row < d.rows; row += kJoinThreads / 32) {
+  const int half = w & 1, mid = (n + 1) / 2, i0 = half ? mid : 0, i1 = half ? n : mid;
+  for (int row0 = 0; row0 < ROWS && d.row0 + row0 < d.rows; row0 += kJoinWarps / 2) {
+    const int row = row0 + (w >> 1);
+    const bool in = row < ROWS && d.row0 + row < d.rows;
     auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-    float mt = kNoMax;
-    for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    float lt = 0.f;
+    float mt = kNoMax, lt = 0.f;
     float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int base = 0; base < n; base += 32) {
-      float f = 0.f;
-      if (base + lane < n) {
-        const float2 v = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
-        f = ex2_approx(v.x - mt);
-        lt = fmaf(v.y, f, lt);
-      }
-      const int cnt = min(32, n - base);
-#pragma unroll 8
-      for (int i = 0; i < cnt; i += PPW) {
-        const float fi = __shfl_sync(0xffffffffu, f, i + sub);
-        if (i + sub < cnt) {
-          const float4 v = *reinterpret_cast<const float4*>(a.part + at(base + i + sub) * D + ch0);
-          o4.x = fmaf(v.x, fi, o4.x), o4.y = fmaf(v.y, fi, o4.y);
-          o4.z = fmaf(v.z, fi, o4.z), o4.w = fmaf(v.w, fi, o4.w);
+    if (in) {
+      for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+      for (int base = i0; base < i1; base += 32) {
+        float f = 0.f;  // weight of part base + lane
+        if (base + lane < i1) {
+          const float2 v = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
+          f = ex2_approx(v.x - mt);
+          lt = fmaf(v.y, f, lt);
+        }
+        const int cnt = min(32, i1 - base);
+        for (int i = 0; i < cnt; i += 8) {
+          float4 v[8 / PPW];
+#pragma unroll
+          for (int y = 0; y < 8 / PPW; ++y)
+            v[y] = *reinterpret_cast<const float4*>(a.part + at(min(base + i + y * PPW + sub, i1 - 1)) * D + ch0);
+#pragma unroll
+          for (int y = 0; y < 8 / PPW; ++y) {
+            const float fi = __shfl_sync(0xffffffffu, f, i + y * PPW + sub);  // 0 behind the last part
+            o4.x = fmaf(v[y].x, fi, o4.x), o4.y = fmaf(v[y].y, fi, o4.y);
+            o4.z = fmaf(v[y].z, fi, o4.z), o4.w = fmaf(v[y].w, fi, o4.w);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-    if (PPW == 2) {
-      o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
-      o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
+      for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+      if (PPW == 2) {
+        o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
+        o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
+      }
     }
-    const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
-    if (sub == 0)
-      *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
-          make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
-    if (lane == 0)
-      a.lse[static_cast<long long>(tok) * a.Hq + head] = lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    if (half) {
+      s_o[w >> 1][lane] = o4;
+      if (lane == 0) s_l[w >> 1] = lt;
+    }
+    __syncthreads();
+    if (!half && in) {
+      const float4 v = s_o[w >> 1][lane];
+      o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
+      lt += s_l[w >> 1];
+      const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
+      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      if (sub == 0)
+        *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
+            make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
+      if (lane == 0)
+        a.lse[static_cast<long long>(tok) * a.Hq + head] =
+            lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    }
+    __syncthreads();
   }
 }
 
@@ -775,7 +872,7 @@ int c4_nt(int N, int R, int G) {
   const long long rows = (static_cast<long long>(N) + R - 1) / R * G;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
-int c4_ctas(int nt) { return (nt == 1 ? 3 : nt == 2 ? 2 : 1) * num_sms(); }
+int c4_ctas(int nt) { return (nt == 1 ? X_CTAS : nt == 2 ? 2 : 1) * num_sms(); }
 
 struct C4Ws {
   size_t desc = 0, ml = 0, part = 0, total = 0;
