@@ -29,81 +29,23 @@
 //   V: codes become c s in fp16 (exact: seven significant bits below 2^16).
 //      P is held times 2^7 in fp16, so weights down to 2^-32 of the largest
 //      count.
-#include <climits>
 #include <cmath>
 
-#include "cache4.cuh"
-#include "internal.h"
+#include "cache4_attn.cuh"
 
 namespace scfa {
 namespace {
 
-#ifndef X_CTAS
-#define X_CTAS 3
-#define X_ST 3
-#define X_ST64 6
-#endif
-#ifndef X_CH
-#define X_CH 128
-#endif
-constexpr int kCh = X_CH;             // tokens per chunk
-constexpr int kChTiles = kCh / kC4Tile;
-constexpr int kWarps = 4;            // compute warps
+constexpr int kWarps = 4;  // compute warps
 constexpr int kTpw = kChTiles / kWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr float kNoMax = -1e30f;     // running maximum before any key (finite: differences stay defined)
-
-// Where the partial rows of a CTA go, and what it reports. One per CTA,
-// written by every call.
-struct C4Desc {
-  int err;     // SCFA_OK or the CTA's first error
-  int parts;   // > 0: an item begins here and ends `parts` CTAs later
-  int tok0, rows, row0, head;
-  int pad[2];
-};
-
-struct C4AttnArgs {
-  const uint16_t* q;
-  long long qt, qh;
-  const uint8_t* cache;
-  int page_size, log_ps, n_pages;
-  const int32_t* table;
-  int max_pages;
-  const int32_t *q_start, *vis;
-  int N, R, Hq, Hkv, G;
-  float factor;  // scale * log2(e) * 2^24
-  uint16_t* o;
-  long long ot, oh;
-  float* lse;
-  int* status;
-  C4Desc* desc;
-  float* part;  // [cta][2][rows][D]
-  float* ml;    // [cta][2][rows][2]
-  int stall;
-  // 16, 128 and fp16 1024 twice, as values the compiler does not know: a
-  // multiplication then stays on the FMA pipe (a shift-and-add is ALU work,
-  // which is what is short), and an AND-OR stays one instruction
-  uint32_t k16, k128, magic;
-};
-
-// What a stage holds.
-struct C4Stage {
-  int tok0, rows, row0, head;  // first token of the request, its rows, first row of the item, key head
-  int base;                    // position of the chunk's first token
-  int tiles;                   // bit t: tile t was copied
-  int flags;
-  int seen;                    // tokens that the item's last row sees
-  int qslot;                   // where its queries are
-  int pad[3];
-};
-enum { kFirst = 1, kLast = 2, kOpenStart = 4, kOpenEnd = 8 };
 
 // The query rows of an item, as the producer leaves them: B operands of the
 // score MMAs, and per row what turns sums into scores.
 template <int D, int NT>
 struct C4Queries {
   uint4 frag[NT][D / 32][32];
-  uint32_t offset[NT][32];  // B operand of the offset MMA
+  float offset[NT][D / 32][8];  // -8 2^-24 sum(q) per group
   float factor[8 * NT];     // score in log2 units = sum * factor
   int seen[8 * NT];         // tokens that the row sees
   int all_see[4];           // [0]: tokens that every row sees
@@ -113,8 +55,8 @@ template <int D, int NT>
 struct C4Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = kChTiles * C4<D>::kTileBytes;
-  static constexpr int kCtas = NT == 1 ? X_CTAS : NT == 2 ? 2 : 1;  // per SM
-  static constexpr int kStages = NT == 1 ? (D == 128 ? X_ST : X_ST64) : (D == 128 ? 4 : 6);
+  static constexpr int kCtas = NT == 1 ? (D == 128 ? 3 : 4) : NT == 2 ? 2 : 1;  // per SM
+  static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 6);
   static constexpr size_t kPartBytes = sizeof(float) * kWarps * kRows * D;
   static constexpr size_t kSmem =
       static_cast<size_t>(kStages) * (kStageBytes + sizeof(C4Queries<D, NT>)) + kPartBytes;
@@ -134,62 +76,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-// d = a b, 16 x 8 x 8
-__device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
-  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b), "f"(0.f));
-}
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// (a & b) | c
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
 // transpose of an 8 x 8 matrix of 16-bit values, one row per four lanes
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-// bounded wait of a whole warp: its lanes go on, or give up, together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
-}
-
-// Row blocks of a request and the chunks of one of them.
-struct C4Req {
-  int tok0, rows, blocks;
-};
-template <int ROWS>
-__device__ __forceinline__ C4Req c4_request(const C4AttnArgs& a, int r) {
-  C4Req q;
-  // (indices are clamped: nothing is read out of bounds whatever q_start holds)
-  q.tok0 = min(max(a.q_start[r], 0), a.N);
-  const int end = min(max(a.q_start[r + 1], q.tok0), a.N);
-  q.rows = (end - q.tok0) * a.G;
-  q.blocks = (q.rows + ROWS - 1) / ROWS;
-  return q;
-}
-// tokens that the last row of block b sees (vis does not decrease within a request)
-template <int ROWS>
-__device__ __forceinline__ int c4_seen(const C4AttnArgs& a, const C4Req& q, int b) {
-  const int last = min((b + 1) * ROWS, q.rows) - 1;
-  const long long cap = static_cast<long long>(a.max_pages) << a.log_ps;
-  return static_cast<int>(min(cap, static_cast<long long>(max(0, a.vis[q.tok0 + last / a.G]))));
-}
-__device__ __forceinline__ int c4_chunks(int seen) { return max(1, (seen + kCh - 1) / kCh); }
 
 // The query rows from row0 on of key head h, by one warp: lane (r8, j) takes
 // channels 32 g + 8 j + 0..7 of row r8, the B operand's place of them.
@@ -227,7 +119,6 @@ __device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Req& q, 
     // exponent of the power of two that brings the row to [2^13, 2^14)
     const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
     const float up = __uint_as_float(ex << 23);
-    float off[G];  // -4 2^-14 sum(q): times 2 s and 2^-10 it is -8 2^-24 sum(q) s
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint32_t in4[4] = {v[nt][g].x, v[nt][g].y, v[nt][g].z, v[nt][g].w};
@@ -243,29 +134,16 @@ __device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Req& q, 
       s.frag[nt][g][lane] = make_uint4(hq[0], hq[1], hq[2], hq[3]);
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      off[g] = sum * -0x1p-12f;
+      if (j == 0) s.offset[nt][g][r8] = sum * (-8.f * 0x1p-24f);
     }
-    // the offset MMA's k: the groups' sums rounded to fp16, then what that left
-    const int lo = G == 4 ? j >> 1 : j & 1, pair = G == 4 ? j & 1 : 0;
-    float o0 = pair ? off[G - 2] : off[0], o1 = pair ? off[G - 1] : off[1];
-    if (lo) {
-      o0 -= __half2float(__float2half_rn(o0));
-      o1 -= __half2float(__float2half_rn(o1));
-    }
-    s.offset[nt][lane] = G == 4 || j < 2 ? c4_pack<true>(o0, o1) : 0u;
     if (j == 0) {
-      s.factor[nt * 8 + r8] = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
+      s.factor[nt * 8 + r8] = fmaxf(a.factor * 0x1p24f * __uint_as_float((254u - ex) << 23), 0x1p-126f);
       s.seen[nt * 8 + r8] = seen[nt];
     }
     all = min(all, seen[nt]);
   }
   all = __reduce_min_sync(0xffffffffu, all);
   if (lane == 0) s.all_see[0] = all;
-}
-
-// a / b, in 32 bits where they hold it
-__device__ __forceinline__ long long c4_div(long long a, int b) {
-  return a >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
 }
 
 template <int D, bool F16, int NT>
@@ -277,9 +155,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   __shared__ uint64_t full[S], empty[S], mfull, mempty;
   __shared__ C4Stage stage[S];
   __shared__ float s_ml[kWarps][ROWS][2];
-  __shared__ long long s_sum[kWarps + 2];
-  __shared__ long long s_prefix;
-  __shared__ int s_req;
+  __shared__ C4SpanSmem<kThreads> s_span;
   __shared__ volatile int abort_flag;
   C4Queries<D, NT>* const s_q = reinterpret_cast<C4Queries<D, NT>*>(smem + static_cast<size_t>(S) * C::kStageBytes);
   float* const s_part = reinterpret_cast<float*>(s_q + S);
@@ -295,196 +171,44 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
     mbar_init(&mempty, kWarps);
     fence_mbar_init();
     abort_flag = 0;
-    s_req = -1;
     desc->err = SCFA_OK;
     desc->parts = 0;
   }
 
-  // ---- chunks of all requests, and the request in which this CTA's piece begins
-  auto request_units = [&](int r) {
-    C4Req q = {0, 0, 0};
-    if (r < a.R) q = c4_request<ROWS>(a, r);
-    long long sum = 0;
-    if (q.blocks <= 4) {
-      for (int b = 0; b < q.blocks; ++b) sum += c4_chunks(c4_seen<ROWS>(a, q, b));
-    }
-    // requests of many blocks: the warp together
-    uint32_t big = __ballot_sync(0xffffffffu, q.blocks > 4);
-    while (big) {
-      const int src = __ffs(big) - 1;
-      big &= big - 1;
-      C4Req p;
-      p.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
-      p.rows = __shfl_sync(0xffffffffu, q.rows, src);
-      p.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
-      int x = 0;
-      for (int b = lane; b < p.blocks; b += 32) x += c4_chunks(c4_seen<ROWS>(a, p, b));
-      x = __reduce_add_sync(0xffffffffu, x);
-      if (lane == src) sum = x;
-    }
-    return sum * a.Hkv;
-  };
-  // inclusive sum over the block; *total gets the sum
-  auto block_incl = [&](long long x, long long* total) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_sum[w] = x;
-    __syncthreads();
-    long long all = 0;
-    for (int i = 0; i <= kWarps; ++i) {
-      if (i == w) x += all;
-      all += s_sum[i];
-    }
-    *total = all;
-    return x;
-  };
-  long long total = 0, mine = 0;
-  for (int base = 0; base < a.R; base += kThreads) {
-    long long sum;
-    mine = request_units(base + tid);
-    block_incl(mine, &sum);
-    total += sum;
-  }
-  const long long per = c4_div(total + gridDim.x - 1, gridDim.x);
-  const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
-  if (u0 >= u1) return;  // (the whole CTA)
-  long long before = 0;
-  for (int base = 0; base < a.R; base += kThreads) {
-    long long sum;
-    if (a.R > kThreads) mine = request_units(base + tid);
-    const long long upto = before + block_incl(mine, &sum);
-    if (u0 < upto && u0 >= upto - mine) {
-      s_req = base + tid;
-      s_prefix = upto - mine;
-    }
-    before += sum;
-    if (u0 < before) break;  // (uniform)
-  }
-  __syncthreads();
-  const int n_units = static_cast<int>(u1 - u0);
+  C4Span span;
+  if (!c4_span<ROWS, kThreads>(a, s_span, span)) return;  // (the whole CTA)
+  const int n_units = span.units;
 
   if (w == kWarps) {
     // ================================================= producer
-    int r = s_req, b = 0, h, ch, seen;
-    C4Req q = c4_request<ROWS>(a, r);
-    long long rem = u0 - s_prefix;
-    for (;; b += 32) {  // the block: 32 at a time
-      const int mb = b + lane;
-      const int c = mb < q.blocks ? c4_chunks(c4_seen<ROWS>(a, q, mb)) : 0;
-      long long x = static_cast<long long>(c) * a.Hkv;
-      const long long own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, rem < x);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b += src;
-        rem -= __shfl_sync(0xffffffffu, x - own, src);
-        break;
-      }
-      rem -= __shfl_sync(0xffffffffu, x, 31);
-      if (b + 32 >= q.blocks) break;  // (does not happen: the piece begins in this request)
-    }
-    seen = c4_seen<ROWS>(a, q, b);
-    int chunks = c4_chunks(seen);
-    h = static_cast<int>(c4_div(rem, chunks));
-    ch = static_cast<int>(rem - static_cast<long long>(h) * chunks);
-    bool first = true;  // of its item in this CTA
-
-    const int psub = min(a.page_size, kCh), npc = kCh / psub;
-    int have_r = -1, have_p = 0, page = -1;  // the 32 pieces whose pages the lanes hold
+    C4Walk<ROWS> walk;
+    walk.begin(a, span, lane);
+    C4Pages pages(a);
     int issued = 0, qslot = -1;
     for (int u = 0; u < n_units; ++u) {
       const int s = u % S;
       if (u >= S && !wait_all(&empty[s], ((u / S) & 1) ^ 1, &abort_flag, &desc->err)) break;
-      // pages of this chunk
-      const int p0 = ch * npc;
-      if (have_r != r || p0 < have_p || p0 + npc > have_p + 32) {
-        have_r = r;
-        have_p = p0;
-        const long long tokpos = static_cast<long long>(p0 + lane) * psub;
-        page = -1;
-        if (tokpos < (static_cast<long long>(a.max_pages) << a.log_ps))
-          page = a.table[static_cast<long long>(r) * a.max_pages + (tokpos >> a.log_ps)];
-      }
-      const int pg = __shfl_sync(0xffffffffu, page, (p0 - have_p + lane) & 31);
-      const int n = min(kCh, seen - ch * kCh) - lane * psub;  // tokens of this lane's piece
-      int tiles = lane < npc && n > 0 ? (min(n, psub) + kC4Tile - 1) / kC4Tile : 0;
-      if (tiles > 0 && (pg < 0 || pg >= a.n_pages)) {
-        raise_status(&desc->err, SCFA_ERR_INVALID);
-        tiles = 0;
-      }
-      const uint32_t mask =
-          __reduce_or_sync(0xffffffffu, tiles > 0 ? ((1u << tiles) - 1u) << (lane * (psub / kC4Tile)) : 0u);
-      const uint32_t bytes = __popc(mask) * L::kTileBytes;
-      const bool last_chunk = ch + 1 == chunks, go = !(a.stall && u == 0);
-      if (tiles > 0 && go) {
-        const long long tok = static_cast<long long>(p0 + lane) * psub;
-        const uint8_t* src =
-            a.cache + c4_tile_base(pg, a.Hkv, h, a.page_size, static_cast<int>(tok & (a.page_size - 1)), L::kTileBytes);
-        bulk_load(smem + static_cast<size_t>(s) * C::kStageBytes + lane * (psub / kC4Tile) * L::kTileBytes, src,
-                  tiles * L::kTileBytes, &full[s]);
-      }
-      if (first) {
+      const uint32_t mask = pages.look_up(a, walk, lane, &desc->err);
+      const bool go = !(a.stall && u == 0);
+      if (go) pages.copy<D>(a, walk, lane, smem + static_cast<size_t>(s) * C::kStageBytes, &full[s]);
+      if (walk.ch == 0 || u == 0) {
         // at most S items have units in the ring, so the slot of the item S before is free
         if (++qslot == S) qslot = 0;
-        c4_queries<D, F16, NT>(a, q, b * ROWS, h, lane, s_q[qslot]);
+        c4_queries<D, F16, NT>(a, walk.q, walk.b * ROWS, walk.h, lane, s_q[qslot]);
       }
       __syncwarp();
       if (lane == 0) {
         C4Stage d;
-        d.tok0 = q.tok0;
-        d.rows = q.rows;
-        d.row0 = b * ROWS;
-        d.head = h;
-        d.base = ch * kCh;
+        walk.describe(span, u, desc, d);
         d.tiles = static_cast<int>(mask);
-        d.seen = seen;
         d.qslot = qslot;
-        const bool began = ch <= u, goes_on = !last_chunk && u + 1 == n_units;  // the item, in this piece
-        d.flags = (first ? kFirst : 0) | (last_chunk || goes_on ? kLast : 0) | (began ? 0 : kOpenStart) |
-                  (goes_on ? kOpenEnd : 0);
         stage[s] = d;
-        if (goes_on && began) {
-          const long long last = u1 - 1 + (chunks - 1 - ch);  // the item's last unit
-          desc->parts = static_cast<int>(c4_div(last, static_cast<int>(per)) - blockIdx.x);
-          desc->tok0 = q.tok0;
-          desc->rows = q.rows;
-          desc->row0 = b * ROWS;
-          desc->head = h;
-        }
         // (the copies may have landed already: the phase ends with this arrival and all bytes)
-        if (go) mbar_arrive_expect_tx(&full[s], bytes);
+        if (go) mbar_arrive_expect_tx(&full[s], __popc(mask) * L::kTileBytes);
       }
+      __syncwarp();
       issued = u + 1;
-      // next chunk
-      first = false;
-      if (last_chunk) {
-        first = true;
-        ch = 0;
-        if (++h == a.Hkv) {
-          h = 0;
-          if (u + 1 < n_units) {
-            if (++b == q.blocks) {
-              b = 0;
-              do {
-                q = c4_request<ROWS>(a, ++r);
-              } while (q.blocks == 0 && r + 1 < a.R);
-            }
-            seen = c4_seen<ROWS>(a, q, b);
-            chunks = c4_chunks(seen);
-          }
-        }
-      } else {
-        ++ch;
-      }
+      walk.next(a, u + 1 < n_units);
     }
     // copies in flight land before the shared memory goes
     for (int u = max(0, issued - S); u < issued; ++u)
@@ -495,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   // =================================================== compute warps
   const int r8 = lane >> 2, j = lane & 3;
   const uint32_t k16 = a.k16, k128 = a.k128, magic = a.magic;
-  const uint32_t off_sel = G == 4 && (j & 1) ? 0x4342 : 0x4140;  // the scale bytes of this lane's k of the offset MMA
   float O[NT][G][2][4];
   float factor[NT][2];
   float m[NT][2], l[NT][2];  // reference of the weights (a running maximum - 7), and their sum
@@ -519,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
       }
     }
     const int t0 = w * kTpw;
-    if ((d.tiles >> t0) & ((1 << kTpw) - 1)) {
+    const uint32_t there = static_cast<uint32_t>(d.tiles) >> t0 & ((1u << kTpw) - 1u);
+    if (there != 0) {
       const uint8_t* tile0 = smem + static_cast<size_t>(s) * C::kStageBytes + t0 * L::kTileBytes;
       float x[kTpw][NT][4];
       // ---- scores
@@ -540,21 +264,18 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             ks[i][y] = *reinterpret_cast<const uint16_t*>(tile + L::kKScales + (r8 + 8 * y) * G);
           }
         }
-        // the offsets of the codes: twice the scales (fp16) by -4 sum(q)
-        const uint32_t a0 = __byte_perm(ks[i][0], 0u, off_sel) * k128 + 0x04000400u;
-        const uint32_t a1 = __byte_perm(ks[i][1], 0u, off_sel) * k128 + 0x04000400u;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_k8(x[i][nt], a0, a1, qs.offset[nt][lane]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[i][nt][e] *= 0x1p-10f;
-        }
+        for (int nt = 0; nt < NT; ++nt) x[i][nt][0] = x[i][nt][1] = x[i][nt][2] = x[i][nt][3] = 0.f;
       }
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         uint4 qv[NT];
+        float2 x0[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) qv[nt] = qs.frag[nt][g][lane];
+        for (int nt = 0; nt < NT; ++nt) {
+          qv[nt] = qs.frag[nt][g][lane];
+          x0[nt] = *reinterpret_cast<const float2*>(&qs.offset[nt][g][2 * j]);
+        }
 #pragma unroll
         for (int i = 0; i < kTpw; ++i) {
           uint32_t A[2][4];
@@ -572,15 +293,14 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             float acc[4];
             mma_f16(acc, A[0], qv[nt].x, qv[nt].y, 0.f, 0.f, 0.f, 0.f);
             mma_f16(acc, A[1], qv[nt].z, qv[nt].w, acc[0], acc[1], acc[2], acc[3]);
-            x[i][nt][0] = fmaf(acc[0], s0, x[i][nt][0]);
-            x[i][nt][1] = fmaf(acc[1], s0, x[i][nt][1]);
-            x[i][nt][2] = fmaf(acc[2], s1, x[i][nt][2]);
-            x[i][nt][3] = fmaf(acc[3], s1, x[i][nt][3]);
+            x[i][nt][0] = fmaf(acc[0] + x0[nt].x, s0, x[i][nt][0]);
+            x[i][nt][1] = fmaf(acc[1] + x0[nt].y, s0, x[i][nt][1]);
+            x[i][nt][2] = fmaf(acc[2] + x0[nt].x, s1, x[i][nt][2]);
+            x[i][nt][3] = fmaf(acc[3] + x0[nt].y, s1, x[i][nt][3]);
           }
         }
       }
       const int key0 = d.base + t0 * kC4Tile;
-      const uint32_t there = static_cast<uint32_t>(d.tiles) >> t0 & ((1u << kTpw) - 1u);
       if (there != (1u << kTpw) - 1u || key0 + kTpw * kC4Tile > qs.all_see[0]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -683,11 +403,10 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             const uint32_t hi = lo >> 8;
             // the two keys' scales times 2: fp16 bits (b << 7) + (1 << 10), normal for every byte of a row
             const uint32_t sc = __byte_perm(sb[y][g & 1][0], sb[y][g & 1][1], g < 2 ? 0x5410 : 0x7632) * k128 + 0x04000400u;
-            // 1024 + (c + 8) and 1024 + 16 (c + 8) -> c / 2
-            const uint32_t c0 = fma_f16x2(and_or(lo, 0x000F000Fu, magic), 0x38003800u, 0xE008E008u);
-            const uint32_t c1 = fma_f16x2(and_or(lo, 0x00F000F0u, magic), 0x28002800u, 0xD080D080u);
-            const uint32_t c2 = fma_f16x2(and_or(hi, 0x000F000Fu, magic), 0x38003800u, 0xE008E008u);
-            const uint32_t c3 = fma_f16x2(and_or(hi, 0x00F000F0u, magic), 0x28002800u, 0xD080D080u);
+            const uint32_t c0 = c4_half_lo(lo, magic);
+            const uint32_t c1 = c4_half_hi(lo, magic);
+            const uint32_t c2 = c4_half_lo(hi, magic);
+            const uint32_t c3 = c4_half_hi(hi, magic);
             A[0][2 * y] = mul_f16x2(c0, sc), A[0][2 * y + 1] = mul_f16x2(c1, sc);
             A[1][2 * y] = mul_f16x2(c2, sc), A[1][2 * y + 1] = mul_f16x2(c3, sc);
           }
@@ -777,102 +496,13 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   }
 }
 
-// Joins the partial rows of the items that were cut, in the order of their
-// chunks, and gathers the CTAs' errors. One CTA per piece, the one in which an
-// item begins, and two warps per row, each for half the parts: lanes first
-// weigh the parts, then each takes four channels of every part, eight parts
-// at a time.
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
-template <int D, bool F16, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a, int n_desc) {
-  __shared__ float4 s_o[kJoinWarps / 2][32];
-  __shared__ float s_l[kJoinWarps / 2];
-  __shared__ int s_err[kJoinWarps];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const C4Desc d = a.desc[blockIdx.x];
-  if (blockIdx.x == 0) {
-    int err = 0;
-    for (int i = tid; i < n_desc; i += kJoinThreads) err = max(err, a.desc[i].err);
-    err = __reduce_max_sync(0xffffffffu, err);
-    if (lane == 0) s_err[w] = err;
-    __syncthreads();
-    if (tid == 0) {
-      for (int i = 1; i < kJoinWarps; ++i) err = max(err, s_err[i]);
-      *a.status = err;
-    }
-  }
-  if (d.parts <= 0) return;
-  constexpr int LPP = D / 4;     // lanes per part
-  constexpr int PPW = 32 / LPP;  // parts side by side in a warp
-  const int n = d.parts + 1, sub = lane / LPP, ch0 = lane % LPP * 4;
-  const int half = w & 1, mid = (n + 1) / 2, i0 = half ? mid : 0, i1 = half ? n : mid;
-  for (int row0 = 0; row0 < ROWS && d.row0 + row0 < d.rows; row0 += kJoinWarps / 2) {
-    const int row = row0 + (w >> 1);
-    const bool in = row < ROWS && d.row0 + row < d.rows;
-    auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-    float mt = kNoMax, lt = 0.f;
-    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-      for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-      for (int base = i0; base < i1; base += 32) {
-        float f = 0.f;  // weight of part base + lane
-        if (base + lane < i1) {
-          const float2 v = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
-          f = ex2_approx(v.x - mt);
-          lt = fmaf(v.y, f, lt);
-        }
-        const int cnt = min(32, i1 - base);
-        for (int i = 0; i < cnt; i += 8) {
-          float4 v[8 / PPW];
-#pragma unroll
-          for (int y = 0; y < 8 / PPW; ++y)
-            v[y] = *reinterpret_cast<const float4*>(a.part + at(min(base + i + y * PPW + sub, i1 - 1)) * D + ch0);
-#pragma unroll
-          for (int y = 0; y < 8 / PPW; ++y) {
-            const float fi = __shfl_sync(0xffffffffu, f, i + y * PPW + sub);  // 0 behind the last part
-            o4.x = fmaf(v[y].x, fi, o4.x), o4.y = fmaf(v[y].y, fi, o4.y);
-            o4.z = fmaf(v[y].z, fi, o4.z), o4.w = fmaf(v[y].w, fi, o4.w);
-          }
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-      if (PPW == 2) {
-        o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
-        o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
-      }
-    }
-    if (half) {
-      s_o[w >> 1][lane] = o4;
-      if (lane == 0) s_l[w >> 1] = lt;
-    }
-    __syncthreads();
-    if (!half && in) {
-      const float4 v = s_o[w >> 1][lane];
-      o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
-      lt += s_l[w >> 1];
-      const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      if (sub == 0)
-        *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
-            make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
-      if (lane == 0)
-        a.lse[static_cast<long long>(tok) * a.Hq + head] =
-            lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-    }
-    __syncthreads();
-  }
-}
-
 // Query rows of an item, 8 * NT: the average request's rows in as few passes
 // over its tokens as registers allow.
 int c4_nt(int N, int R, int G) {
   const long long rows = (static_cast<long long>(N) + R - 1) / R * G;
   return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
-int c4_ctas(int nt) { return (nt == 1 ? X_CTAS : nt == 2 ? 2 : 1) * num_sms(); }
+int c4_ctas(int nt, int D) { return (nt == 1 ? (D == 128 ? 3 : 4) : nt == 2 ? 2 : 1) * num_sms(); }
 
 struct C4Ws {
   size_t desc = 0, ml = 0, part = 0, total = 0;
@@ -882,7 +512,7 @@ C4Ws c4_ws(int D) {
   C4Ws w;
   size_t n = 0, rows = 0;
   for (int nt = 1; nt <= 4; nt *= 2) {
-    const size_t c = c4_ctas(nt);
+    const size_t c = c4_ctas(nt, D);
     n = c > n ? c : n;
     rows = c * 2 * 8 * nt > rows ? c * 2 * 8 * nt : rows;
   }
@@ -896,7 +526,7 @@ C4Ws c4_ws(int D) {
 template <int D, bool F16, int NT>
 cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
   using C = C4Cfg<D, NT>;
-  const int grid = c4_ctas(NT);
+  const int grid = c4_ctas(NT, D);
   auto kern = cache4_attn_kernel<D, F16, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
@@ -934,7 +564,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * page_size >= (1ll << 31) || static_cast<long long>(N) * Hq >= (1ll << 31))
+      static_cast<long long>(max_pages) * page_size >= (1ll << 31) || static_cast<long long>(N) * Hq >= (1ll << 31) - 256)
     return SCFA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SCFA_ERR_INVALID;
@@ -951,8 +581,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   while ((1 << a.log_ps) < page_size) ++a.log_ps;
   a.table = table, a.max_pages = max_pages, a.q_start = q_start, a.vis = vis;
   a.N = N, a.R = R, a.Hq = Hq, a.Hkv = Hkv, a.G = G;
-  // K's codes are read as multiples of 2^-24
-  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * 0x1p24);
+  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.o = o, a.ot = o_token, a.oh = o_head, a.lse = lse;
   a.status = reinterpret_cast<int*>(p);
   a.desc = reinterpret_cast<C4Desc*>(p + w.desc);
