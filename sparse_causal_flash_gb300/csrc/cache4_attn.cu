@@ -36,6 +36,10 @@
 namespace scfa {
 namespace {
 
+#ifndef X_NR
+#define X_NR 16
+#endif
+constexpr int kNarrowRows = X_NR;
 constexpr int kWarps = 4;  // compute warps
 constexpr int kTpw = kChTiles / kWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
@@ -55,7 +59,7 @@ template <int D, int NT>
 struct C4Cfg {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = kChTiles * C4<D>::kTileBytes;
-  static constexpr int kCtas = NT == 1 ? (D == 128 ? 3 : 4) : NT == 2 ? 2 : 1;  // per SM
+  static constexpr int kCtas = NT == 1 ? (D == 128 ? 3 : 4) : 2;  // per SM
   static constexpr int kStages = NT == 1 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 6);
   static constexpr size_t kPartBytes = sizeof(float) * kWarps * kRows * D;
   static constexpr size_t kSmem =
@@ -496,13 +500,13 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   }
 }
 
-// Query rows of an item, 8 * NT: the average request's rows in as few passes
-// over its tokens as registers allow.
-int c4_nt(int N, int R, int G) {
+// Query rows of an item, from the average request's. Up to 8 NT of them with
+// the warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05.
+int c4_rows(int N, int R, int G) {
   const long long rows = (static_cast<long long>(N) + R - 1) / R * G;
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  return rows <= 8 ? 8 : rows <= kNarrowRows ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
-int c4_ctas(int nt, int D) { return (nt == 1 ? (D == 128 ? 3 : 4) : nt == 2 ? 2 : 1) * num_sms(); }
+int c4_ctas(int rows, int D) { return (rows == 8 ? (D == 128 ? 3 : 4) : rows == 16 ? 2 : 1) * num_sms(); }
 
 struct C4Ws {
   size_t desc = 0, ml = 0, part = 0, total = 0;
@@ -511,10 +515,10 @@ struct C4Ws {
 C4Ws c4_ws(int D) {
   C4Ws w;
   size_t n = 0, rows = 0;
-  for (int nt = 1; nt <= 4; nt *= 2) {
-    const size_t c = c4_ctas(nt, D);
+  for (int x = 8; x <= 128; x *= 2) {
+    const size_t c = c4_ctas(x, D);
     n = c > n ? c : n;
-    rows = c * 2 * 8 * nt > rows ? c * 2 * 8 * nt : rows;
+    rows = c * 2 * x > rows ? c * 2 * x : rows;
   }
   w.desc = sizeof(WsHeader);
   w.ml = align_up(w.desc + n * sizeof(C4Desc), 256);
@@ -526,7 +530,7 @@ C4Ws c4_ws(int D) {
 template <int D, bool F16, int NT>
 cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
   using C = C4Cfg<D, NT>;
-  const int grid = c4_ctas(NT, D);
+  const int grid = c4_ctas(8 * NT, D);
   auto kern = cache4_attn_kernel<D, F16, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
@@ -537,8 +541,8 @@ cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
 }
 
 template <int D, bool F16>
-cudaError_t launch_nt(int nt, const C4AttnArgs& a, cudaStream_t st) {
-  return nt == 1 ? launch<D, F16, 1>(a, st) : nt == 2 ? launch<D, F16, 2>(a, st) : launch<D, F16, 4>(a, st);
+cudaError_t launch_rows(int rows, const C4AttnArgs& a, cudaStream_t st) {
+  return rows == 8 ? launch<D, F16, 1>(a, st) : launch<D, F16, 2>(a, st);
 }
 
 }  // namespace
@@ -569,7 +573,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SCFA_ERR_INVALID;
   if ((q_token | q_head | o_token | o_head) & 7) return SCFA_ERR_INVALID;
-  const int G = Hq / Hkv, nt = c4_nt(N, R, G);
+  const int G = Hq / Hkv, rows = c4_rows(N, R, G);
   const C4Ws w = c4_ws(D);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total) return SCFA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -589,8 +593,9 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   a.part = reinterpret_cast<float*>(p + w.part);
   a.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0;
   a.k16 = 16u, a.k128 = 128u, a.magic = 0x64006400u;
-  const cudaError_t e = D == 64 ? (f16 ? launch_nt<64, true>(nt, a, st) : launch_nt<64, false>(nt, a, st))
-                                : (f16 ? launch_nt<128, true>(nt, a, st) : launch_nt<128, false>(nt, a, st));
+  const cudaError_t e = rows > 16 ? launch_cache4_wide(D, f16, rows, a, st)
+                        : D == 64 ? (f16 ? launch_rows<64, true>(rows, a, st) : launch_rows<64, false>(rows, a, st))
+                                  : (f16 ? launch_rows<128, true>(rows, a, st) : launch_rows<128, false>(rows, a, st));
   if (e != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;

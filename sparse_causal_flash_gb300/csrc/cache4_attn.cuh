@@ -327,6 +327,9 @@ struct C4Pages {
   }
 };
 
+// cache4_wide.cu: blocks of rp = 32, 64 or 128 query rows, one CTA per SM
+cudaError_t launch_cache4_wide(int D, bool f16, int rp, const C4AttnArgs& a, cudaStream_t st);
+
 namespace {
 // Joins the partial rows of the items that were cut, in the order of their
 // chunks, and gathers the CTAs' errors. One CTA per piece, the one in which an

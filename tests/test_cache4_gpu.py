@@ -295,7 +295,10 @@ def test_attn_page_sizes_and_ragged_tokens(scfa, ps, D):
 @pytest.mark.parametrize("lens,news,Hq,Hkv,D,dt", [
     ([3001], [1], 8, 1, 128, BF), ([2049, 3, 700], [1, 1, 1], 16, 2, 64, HF), ([1500], [130], 4, 2, 128, BF),
     ([70, 333, 64], [70, 65, 64], 6, 2, 64, BF), ([900, 33], [37, 33], 5, 1, 128, HF), ([0, 0], [3, 1], 4, 2, 64, BF),
-    ([130] * 70, [1] * 70, 8, 8, 64, BF), ([20] * 9, [16] * 9, 2, 1, 128, BF), ([4, 4], [9, 2], 2, 2, 64, BF)])
+    ([130] * 70, [1] * 70, 8, 8, 64, BF), ([20] * 9, [16] * 9, 2, 1, 128, BF), ([4, 4], [9, 2], 2, 2, 64, BF),
+    ([700, 2100], [12, 9], 4, 1, 64, BF), ([2100, 5], [12, 5], 5, 1, 128, HF), ([1000] * 20, [7] * 20, 8, 2, 128, BF),
+    ([1000, 40, 3, 600], [9, 1, 2, 7], 12, 2, 64, HF), ([129] * 3, [1] * 3, 48, 1, 128, BF), ([300], [257], 3, 3, 128, HF),
+    ([0, 7, 0], [40, 7, 1], 4, 4, 64, BF), ([64] * 4, [33, 1, 64, 2], 2, 1, 128, BF), ([33] * 50, [17] * 50, 2, 2, 64, BF)])
 def test_attn_shapes(scfa, lens, news, Hq, Hkv, D, dt):
     check_attn(scfa, attn_problem(scfa, sum(lens), lens, news, Hq, Hkv, D, 16, dt))
 
@@ -305,10 +308,11 @@ def test_attn_without_any_token(scfa):
     check_attn(scfa, p)
 
 
+@pytest.mark.parametrize("news", [[1, 3], [9, 7], [90, 25]])
 @pytest.mark.parametrize("dt", [BF, HF])
-def test_attn_far_scores(scfa, dt):
+def test_attn_far_scores(scfa, dt, news):
     """Scores far from zero, of both signs: the running maximum grows and the first keys hold next to nothing."""
-    p = attn_problem(scfa, 8, [400, 90], [1, 3], 4, 2, 64, 32, dt, spread=1.5)
+    p = attn_problem(scfa, 8, [400, 90], news, 4, 2, 64, 32, dt, spread=1.5)
     p["scale"] = 0.9
     p["q"] *= torch.linspace(-6, 6, p["q"].shape[0] * 4, device="cuda").view(-1, 4, 1).to(dt)
     check_attn(scfa, p)
@@ -357,8 +361,9 @@ def test_attn_on_a_side_stream_and_in_a_graph(scfa):
     assert torch.equal(outs[0][0], o3) and torch.equal(outs[0][1], l3)
 
 
-def test_attn_page_ids_out_of_range_are_masked_and_reported(scfa):
-    p = attn_problem(scfa, 5, [200, 90], [1, 2], 4, 2, 64, 16, BF)
+@pytest.mark.parametrize("news", [[1, 2], [20, 30]])
+def test_attn_page_ids_out_of_range_are_masked_and_reported(scfa, news):
+    p = attn_problem(scfa, 5, [200, 90], news, 4, 2, 64, 16, BF)
     P = p["cache"].shape[0]
     p["table"][0, 3], p["table"][1, 0], p["table"][1, 5] = -5, P, 2 ** 30
     o, lse, ws = run_attn(scfa, p)
@@ -376,8 +381,9 @@ def test_attn_page_ids_out_of_range_are_masked_and_reported(scfa):
     assert scfa.scfa_get_device_status(ws2) == 0
 
 
-def test_attn_page_id_out_of_range_for_all_keys(scfa):
-    p = attn_problem(scfa, 6, [10], [1], 2, 1, 64, 16, BF)
+@pytest.mark.parametrize("new", [1, 10])
+def test_attn_page_id_out_of_range_for_all_keys(scfa, new):
+    p = attn_problem(scfa, 6, [10], [new], 2, 1, 64, 16, BF)
     p["table"].fill_(-1)
     o, lse, ws = run_attn(scfa, p)
     assert scfa.scfa_get_device_status(ws) == 1
@@ -398,8 +404,9 @@ def test_attn_wild_row_bounds(scfa):
     torch.cuda.synchronize()
 
 
-def test_attn_stalled_pipeline_reports_a_timeout(scfa):
-    p = attn_problem(scfa, 9, [300, 20], [1, 1], 8, 2, 64, 16, BF)
+@pytest.mark.parametrize("news", [[1, 1], [20, 3]])
+def test_attn_stalled_pipeline_reports_a_timeout(scfa, news):
+    p = attn_problem(scfa, 9, [300, 20], news, 8, 2, 64, 16, BF)
     N, Hq, D = p["q"].shape
     o, lse = torch.empty_like(p["q"]), torch.empty((N, Hq), device="cuda")
     ws = scfa.workspace(scfa.cache4_attn_workspace_size(N, 2, Hq, 2, D))
