@@ -36,10 +36,6 @@
 namespace scfa {
 namespace {
 
-#ifndef X_NR
-#define X_NR 16
-#endif
-constexpr int kNarrowRows = X_NR;
 constexpr int kWarps = 4;  // compute warps
 constexpr int kTpw = kChTiles / kWarps;
 constexpr int kThreads = 32 * (kWarps + 1);
@@ -404,15 +400,11 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t lo = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
-            const uint32_t hi = lo >> 8;
             // the two keys' scales times 2: fp16 bits (b << 7) + (1 << 10), normal for every byte of a row
             const uint32_t sc = __byte_perm(sb[y][g & 1][0], sb[y][g & 1][1], g < 2 ? 0x5410 : 0x7632) * k128 + 0x04000400u;
-            const uint32_t c0 = c4_half_lo(lo, magic);
-            const uint32_t c1 = c4_half_hi(lo, magic);
-            const uint32_t c2 = c4_half_lo(hi, magic);
-            const uint32_t c3 = c4_half_hi(hi, magic);
-            A[0][2 * y] = mul_f16x2(c0, sc), A[0][2 * y + 1] = mul_f16x2(c1, sc);
-            A[1][2 * y] = mul_f16x2(c2, sc), A[1][2 * y + 1] = mul_f16x2(c3, sc);
+            const uint4 v = c4_unpack8(lo, sc, magic);
+            A[0][2 * y] = v.x, A[0][2 * y + 1] = v.y;
+            A[1][2 * y] = v.z, A[1][2 * y + 1] = v.w;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -500,11 +492,14 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   }
 }
 
-// Query rows of an item, from the average request's. Up to 8 NT of them with
-// the warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05.
+// Query rows of an item, from the average request's: up to 16 with the
+// warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05. Requests of
+// several tokens are ragged and may have twice the average, so they leave the
+// warp-level kernel at 8 (drafts of 1 to 7 tokens, groups of 4, 128 channels:
+// 176 us with blocks of 32, 197 us with blocks of 16).
 int c4_rows(int N, int R, int G) {
-  const long long rows = (static_cast<long long>(N) + R - 1) / R * G;
-  return rows <= 8 ? 8 : rows <= kNarrowRows ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const long long tokens = (static_cast<long long>(N) + R - 1) / R, rows = tokens * G;
+  return rows <= 8 ? 8 : rows <= 16 && tokens == 1 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 int c4_ctas(int rows, int D) { return (rows == 8 ? (D == 128 ? 3 : 4) : rows == 16 ? 2 : 1) * num_sms(); }
 
@@ -592,7 +587,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   a.ml = reinterpret_cast<float*>(p + w.ml);
   a.part = reinterpret_cast<float*>(p + w.part);
   a.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0;
-  a.k16 = 16u, a.k128 = 128u, a.magic = 0x64006400u;
+  a.k16 = 16u, a.k128 = 128u, a.magic = 0x60006000u;
   const cudaError_t e = rows > 16 ? launch_cache4_wide(D, f16, rows, a, st)
                         : D == 64 ? (f16 ? launch_rows<64, true>(rows, a, st) : launch_rows<64, false>(rows, a, st))
                                   : (f16 ? launch_rows<128, true>(rows, a, st) : launch_rows<128, false>(rows, a, st));

@@ -49,7 +49,7 @@ struct C4AttnArgs {
   float* part;  // [cta][2][rows][D]: the tail of an item begun before the piece; an item that goes on behind it
   float* ml;    // [cta][2][rows][2]
   int stall;
-  // 16, 128 and fp16 1024 twice, as values the compiler does not know: a
+  // 16, 128 and fp16 512 twice, as values the compiler does not know: a
   // multiplication then stays on the FMA pipe (a shift-and-add is ALU work,
   // which is what is short), and an AND-OR stays one instruction
   uint32_t k16, k128, magic;
@@ -68,9 +68,9 @@ struct C4Stage {
 // of the item, in this piece: first and last unit; it began before, it goes on behind
 enum { kFirst = 1, kLast = 2, kOpenStart = 4, kOpenEnd = 8 };
 
-__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -84,17 +84,44 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-// codes in bits 0-3 (lo) or 4-7 (hi) of both halves of x, as fp16 c / 2
-__device__ __forceinline__ uint32_t c4_half_lo(uint32_t x, uint32_t magic) {
-  return fma_f16x2(and_or(x, 0x000F000Fu, magic), 0x38003800u, 0xE008E008u);  // 1024 + (c + 8)
-}
-__device__ __forceinline__ uint32_t c4_half_hi(uint32_t x, uint32_t magic) {
-  return fma_f16x2(and_or(x, 0x00F000F0u, magic), 0x28002800u, 0xD080D080u);  // 1024 + 16 (c + 8)
+// Eight codes of a word, four in each half, as fp16 c s (exact): pairs of bits
+// 0-3 and 16-19, 4-7 and 20-23, 8-11 and 24-27, 12-15 and 28-31. sc2: twice
+// the scales of the two halves. The bits of c + 8 under the exponent of 512
+// are 512 + (c + 8) / 2 at the bottom and 512 + 8 (c + 8) four bits up.
+__device__ __forceinline__ uint4 c4_unpack8(uint32_t x, uint32_t sc2, uint32_t magic) {
+  const uint32_t y = x >> 8, sc_hi = mul_f16x2(sc2, 0x2C002C00u);  // s / 8
+  const uint32_t lo = 0xE008E008u, hi = 0xE080E080u;               // -516, -576
+  return make_uint4(mul_f16x2(add_f16x2(and_or(x, 0x000F000Fu, magic), lo), sc2),
+                    mul_f16x2(add_f16x2(and_or(x, 0x00F000F0u, magic), hi), sc_hi),
+                    mul_f16x2(add_f16x2(and_or(y, 0x000F000Fu, magic), lo), sc2),
+                    mul_f16x2(add_f16x2(and_or(y, 0x00F000F0u, magic), hi), sc_hi));
 }
 
-// bounded wait of a whole warp: its lanes go on, or give up, together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status));
+// Bounded wait that polls every `ns` nanoseconds (0: at once) and looks at the
+// abort flag and the clock once in 16 polls. Twenty warps that poll without a
+// pause take most of an SM's issue slots from the few that work.
+__device__ __forceinline__ bool c4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                        uint32_t ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      if (ns != 0) __nanosleep(ns);
+      if (mbar_try_wait(bar, parity)) return true;
+    }
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      raise_status(status, SCFA_ERR_TIMEOUT);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+// of a whole warp: its lanes go on, or give up, together
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                         uint32_t ns = 0) {
+  return __all_sync(0xffffffffu, c4_wait(bar, parity, abort_flag, status, ns));
 }
 
 // a / b, in 32 bits where they hold it

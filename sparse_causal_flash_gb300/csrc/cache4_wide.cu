@@ -5,29 +5,34 @@
 // a cycle and SM, which is enough for 16 rows and bounds more. Here a unit of
 // 128 tokens is unpacked once into fp16 tiles in shared memory (c s is exact
 // in fp16) and S = Q K^T and O += P V run on tcgen05 with 128 rows:
-//   warp 0      copies the pages of the next units into a ring of raw stages;
-//   warps 2-9   unpack a stage into a K and a V tile (two of each, 128-byte
-//               swizzle), and at an item's first unit put its queries, brought
-//               to a largest magnitude in [2^13, 2^14), into TMEM;
-//   warp 1      issues the MMAs, the scores of unit u + 1 before the values of
-//               u; both A operands, Q and P, are read from TMEM, because a
-//               128 x 128 MMA with both in shared memory reads it at twice its
-//               rate;
-//   warps 10-13 softmax, thread = row = TMEM lane; P (fp16, weights times 2^7)
-//               overwrites the scores it came from.
+//   warp 0       copies the pages of the next units into a ring of raw stages;
+//   warps 2-9    unpack the keys of a stage into one of two tiles (128-byte
+//                swizzle), and at an item's first unit put its queries, brought
+//                to a largest magnitude in [2^13, 2^14), into TMEM;
+//   warps 10-17  unpack the values;
+//   warps 1, 22  issue the MMAs of the scores and of the values; both A
+//                operands, Q and P, are read from TMEM, so that only B takes
+//                shared-memory bandwidth;
+//   warps 18-21  softmax, thread = row = TMEM lane; P (fp16, weights times 2^7)
+//                overwrites the scores it came from.
 // With few rows the 128 lanes hold the same RP = 32 or 64 rows several times,
 // and each copy weighs its own part of every unit's tokens (its other weights
 // are zero): the softmax of 32 rows then takes a quarter of the time, and the
 // copies, which keep their own maximum and sum, meet once per item.
-// Shared memory bounds it: per unit and SM 64 KB of unpacked tiles written and
-// as much read by the MMAs, 35 KB raw, some 1,300 cycles at 128 channels.
+// A unit takes an SM some 3,000 cycles at 128 channels, whatever the rows and
+// however many warps unpack or weigh. The MMAs alone, with nothing else
+// running, take 1,300 of them (80 cycles each where the tensor core is busy for
+// 34), and the 64 KB that unpacking writes to shared memory share its bandwidth
+// with their operand reads.
+#include <type_traits>
+
 #include "cache4_attn.cuh"
 
 namespace scfa {
 namespace {
 
-constexpr int kDqWarps = 8;
-constexpr int kWideThreads = 32 * (2 + kDqWarps + 4);
+constexpr int kDqWarps = 16;  // the first eight unpack K, the others V
+constexpr int kWideThreads = 32 * (2 + kDqWarps + 4 + 1);
 constexpr int kWideStages = 3;
 constexpr int kDescs = 16;  // more than the units between the copies and the softmax
 constexpr uint32_t kSub = 16384;  // one [128][64] fp16 tile
@@ -47,24 +52,23 @@ struct WideSmem {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], q_ready[4];
   // (P and its MMA have two barriers each: the softmax may be a unit ahead of
   // the MMAs, and a single barrier's parity can not tell phases two apart)
-  uint64_t p_full[2], pv_done[2], o_empty, group, drain;
+  uint64_t p_full[2], pv_done[2], o_empty, group, drain[2];
   C4SpanSmem<kWideThreads> span;
   uint32_t tmem_base;
   int abort_flag;
 };
 
+// true in one lane of the warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // kind::f16 with fp16 operands, fp32 accumulators
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn) {
   return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// 8 codes of a word -> 8 fp16 values in four registers (pairs of bits 0-3 and
-// 16-19, 4-7 and 20-23, ...), sc2: twice the scales of the two halves
-__device__ __forceinline__ uint4 unpack8(uint32_t x, uint32_t sc2, uint32_t magic) {
-  const uint32_t y = x >> 8;
-  return make_uint4(mul_f16x2(c4_half_lo(x, magic), sc2), mul_f16x2(c4_half_hi(x, magic), sc2),
-                    mul_f16x2(c4_half_lo(y, magic), sc2), mul_f16x2(c4_half_hi(y, magic), sc2));
 }
 
 template <int D, bool F16, int RP>
@@ -82,18 +86,19 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
     }
     for (int s = 0; s < kDescs; ++s) mbar_init(&sm.desc_full[s], 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.k_full[i], kDqWarps);
+      mbar_init(&sm.k_full[i], 8);
       mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_full[i], kDqWarps);
+      mbar_init(&sm.v_full[i], 8);
       mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.pv_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sm.q_ready[i], kDqWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.q_ready[i], 8);
     mbar_init(&sm.o_empty, 4);
     mbar_init(&sm.group, 4);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     fence_mbar_init();
     sm.abort_flag = 0;
     desc->err = SCFA_OK;
@@ -107,6 +112,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, 0), idesc_o = idesc_f16_f32(128, D, 1);
+  constexpr uint64_t kBuf16 = (D / 64) * kSub >> 4;
+  const uint64_t kdesc = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+  const uint64_t vdesc = smem_desc_sw128(smem_u32(sm.v[0][0]), kSub, 1024);
+  constexpr std::integral_constant<int, 0> c0{};
+  constexpr std::integral_constant<int, 1> c1{};
   volatile int* const abort_flag = &sm.abort_flag;
   int* const err = &desc->err;
 
@@ -139,172 +150,202 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
     for (int u = max(0, issued - S); u < issued; ++u)
       if (!(a.stall && u == 0)) mbar_wait_drain(&sm.raw_full[u % S], (u / S) & 1, err);
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, 0), idesc_o = idesc_f16_f32(128, D, 1);
-      const uint64_t kdesc = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
-      const uint64_t vdesc = smem_desc_sw128(smem_u32(sm.v[0][0]), kSub, 1024);
-      constexpr uint64_t kBuf16 = (D / 64) * kSub >> 4;
-      int items_s = 0, items_o = 0;
-      auto issue_s = [&](int u) -> bool {
-        const int i = u & 1;
-        if (!mbar_wait(&sm.desc_full[u % kDescs], (u / kDescs) & 1, abort_flag, err)) return false;
-        if (sm.stage[u % kDescs].flags & kFirst) ++items_s;
-        if (!mbar_wait(&sm.k_full[i], (u >> 1) & 1, abort_flag, err)) return false;
-        tc_fence_after();
-        const uint32_t q = tmem + kColQ + ((items_s - 1) & 1) * kColQ2;
-        const uint64_t b = kdesc + i * kBuf16;
+    // ------------------------------------------------------------ score MMAs
+    // Issuing an MMA takes longer than the MMA: two warps share them. Operand
+    // places are constants of the unit's and the item's parity (the whole of
+    // TMEM is this CTA's, so its columns begin at 0), and the warps stay
+    // together but for the elected lane, so that descriptors are uniform.
+    int items = 0;
+    auto scores = [&](auto unit, auto item) {
+      constexpr int I = decltype(unit)::value, Q = decltype(item)::value;
+      if (elect_one()) {
+        const uint64_t b = kdesc + I * kBuf16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16_ts(tmem + kColS + i * 128, q + kk * 8, b + kstep_off16(kk, kSub), idesc_s, kk > 0);
-        tc_commit(&sm.s_full[i]);
-        tc_commit(&sm.k_empty[i]);
-        return true;
-      };
-      bool ok = issue_s(0);
-      for (int u = 0; ok && u < n_units; ++u) {
-        const int i = u & 1;
-        // the scores of u + 1 go where P of u - 1 was
-        if (u > 0 && !mbar_wait(&sm.pv_done[i ^ 1], ((u - 1) >> 1) & 1, abort_flag, err)) break;
-        if (u + 1 < n_units && !issue_s(u + 1)) break;
-        const bool first = sm.stage[u % kDescs].flags & kFirst;
-        if (first && !mbar_wait(&sm.o_empty, (items_o++ & 1) ^ 1, abort_flag, err)) break;
-        if (!mbar_wait(&sm.v_full[i], (u >> 1) & 1, abort_flag, err)) break;
-        if (!mbar_wait(&sm.p_full[i], (u >> 1) & 1, abort_flag, err)) break;
-        tc_fence_after();
-        const uint64_t b = vdesc + i * kBuf16;
+          mma_bf16_ts(kColS + I * 128, kColQ + Q * kColQ2 + kk * 8, b + kstep_off16(kk, kSub), idesc_s, kk > 0);
+        tc_commit(&sm.s_full[I]);
+        tc_commit(&sm.k_empty[I]);
+      }
+      __syncwarp();
+    };
+    for (int u = 0; u < n_units; ++u) {
+      const int i = u & 1;
+      if (!wait_all(&sm.desc_full[u % kDescs], (u / kDescs) & 1, abort_flag, err)) break;
+      if (sm.stage[u % kDescs].flags & kFirst) ++items;
+      // P of u - 2 lies where these scores go
+      if (u > 1 && !wait_all(&sm.pv_done[i], ((u - 2) >> 1) & 1, abort_flag, err)) break;
+      if (!wait_all(&sm.k_full[i], (u >> 1) & 1, abort_flag, err)) break;
+      tc_fence_after();
+      if (items & 1) {
+        if (i) scores(c1, c0);
+        else scores(c0, c0);
+      } else {
+        if (i) scores(c1, c1);
+        else scores(c0, c1);
+      }
+    }
+    if (elect_one()) tc_commit(&sm.drain[0]);
+    __syncwarp();
+    mbar_wait_drain(&sm.drain[0], 0, err);
+  } else if (warp == 22) {
+    // ------------------------------------------------------------ value MMAs
+    int items = 0;
+    auto values = [&](auto unit, uint32_t accumulate) {
+      constexpr int I = decltype(unit)::value;
+      if (elect_one()) {
+        const uint64_t b = vdesc + I * kBuf16;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tmem + kColO, tmem + kColS + i * 128 + kk * 8, b + static_cast<uint64_t>(kk * 128), idesc_o,
-                      kk > 0 || !first);
-        tc_commit(&sm.pv_done[i]);
-        tc_commit(&sm.v_empty[i]);
+          mma_bf16_ts(kColO, kColS + I * 128 + kk * 8, b + static_cast<uint64_t>(kk * 128), idesc_o,
+                      kk > 0 ? 1u : accumulate);
+        tc_commit(&sm.pv_done[I]);
+        tc_commit(&sm.v_empty[I]);
       }
-      tc_commit(&sm.drain);
-      mbar_wait_drain(&sm.drain, 0, err);
+      __syncwarp();
+    };
+    for (int u = 0; u < n_units; ++u) {
+      const int i = u & 1;
+      if (!wait_all(&sm.desc_full[u % kDescs], (u / kDescs) & 1, abort_flag, err)) break;
+      const bool first = sm.stage[u % kDescs].flags & kFirst;
+      if (first && !wait_all(&sm.o_empty, (items++ & 1) ^ 1, abort_flag, err)) break;
+      if (!wait_all(&sm.v_full[i], (u >> 1) & 1, abort_flag, err)) break;
+      if (!wait_all(&sm.p_full[i], (u >> 1) & 1, abort_flag, err)) break;
+      tc_fence_after();
+      if (i) values(c1, first ? 0u : 1u);
+      else values(c0, first ? 0u : 1u);
     }
+    if (elect_one()) tc_commit(&sm.drain[1]);
+    __syncwarp();
+    mbar_wait_drain(&sm.drain[1], 0, err);
   } else if (warp < 2 + kDqWarps) {
     // ------------------------------------------------------------ unpacking, queries
-    const int dw = warp - 2, quad = warp & 3, dt = dw * 32 + lane;
+    const int dw = (warp - 2) & 7, quad = warp & 3, dt = dw * 32 + lane;
+    const bool keys = warp < 10;
     const uint32_t k128 = a.k128, magic = a.magic;
     int items = 0;
     for (int u = 0; u < n_units; ++u) {
       const int s = u % S, i = u & 1;
       if (!wait_all(&sm.raw_full[s], (u / S) & 1, abort_flag, err)) break;
       const C4Stage d = sm.stage[u % kDescs];
-      if (!wait_all(&sm.k_empty[i], ((u >> 1) & 1) ^ 1, abort_flag, err)) break;
-      if (d.flags & kFirst) {
-        // Two warps per TMEM lane quarter, each half of the channels. Q has two
-        // places: the scores of the item before last are done, they came two
-        // units ago. What the softmax reads has four: it is past the unit four
-        // before this one, whose P had to be used up for the scores two before.
-        const int ib = items++ & 3, half = dw >> 2;
-        const int row = d.row0 + (quad * 32) % RP + lane;
-        const bool in = row < d.rows;
-        const int tok = in ? row / a.G : 0;
-        const uint4* qp = reinterpret_cast<const uint4*>(a.q + (d.tok0 + tok) * a.qt +
-                                                         (d.head * a.G + (in ? row - tok * a.G : 0)) * a.qh);
-        float mx = 0.f;
-        if (in) {
+      const uint8_t* raw = sm.raw[s];
+      if (keys) {
+        if (!wait_all(&sm.k_empty[i], ((u >> 1) & 1) ^ 1, abort_flag, err)) break;
+        if (d.flags & kFirst) {
+          // Two warps per TMEM lane quarter, each half of the channels. Q has two
+          // places: the scores of the item before last are done, they came two
+          // units ago. What the softmax reads has four: it is past the unit four
+          // before this one, whose P had to be used up for the scores two before.
+          const int ib = items++ & 3, half = dw >> 2;
+          const int row = d.row0 + (quad * 32) % RP + lane;
+          const bool in = row < d.rows;
+          const int tok = in ? row / a.G : 0;
+          const uint4* qp = reinterpret_cast<const uint4*>(a.q + (d.tok0 + tok) * a.qt +
+                                                           (d.head * a.G + (in ? row - tok * a.G : 0)) * a.qh);
+          float mx = 0.f;
+          if (in) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = qp[c];
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 v = qp[c];
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float2 f = c4_unpack<F16>(x[y]);
+                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+          }
+          const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
+          const float up = __uint_as_float(ex << 23);
+          uint32_t reg[D / 4];
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 v = in ? qp[half * (D / 16) + c] : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const float2 f = c4_unpack<F16>(x[y]);
-              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+              reg[4 * c + y] = c4_pack<true>(f.x * up, f.y * up);
             }
           }
+          const uint32_t col =
+              tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColQ + (ib & 1) * kColQ2 + half * (D / 4);
+          if constexpr (D == 128) tmem_st32(col, reg);
+          else tmem_st16(col, reg);
+          if (half == 0) {
+            sm.factor[ib][quad * 32 + lane] = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
+            sm.seen[ib][quad * 32 + lane] = in ? a.vis[d.tok0 + tok] : INT_MAX;
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.q_ready[ib]);
         }
-        const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
-        const float up = __uint_as_float(ex << 23);
-        uint32_t reg[D / 4];
+        // K: lane = (key, j), the 8 channels 32 g + 8 j of every group
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int key = (dt >> 2) + 64 * x, j = dt & 3, tile = key >> 4, t = key & 15;
+          const uint8_t* p = raw + tile * L::kTileBytes;
+          uint32_t w[G], sb;
+          if (G == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + L::k_row(t) + j * 16);
+            w[0] = v.x, w[1] = v.y, w[G - 2] = v.z, w[G - 1] = v.w;
+            sb = *reinterpret_cast<const uint32_t*>(p + L::kKScales + t * 4);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + L::k_row(t) + j * 8);
+            w[0] = v.x, w[1] = v.y;
+            sb = *reinterpret_cast<const uint16_t*>(p + L::kKScales + t * 2);
+          }
+          // what is not a visible row may hold scales that are infinite in fp16
+          if (!(d.tiles >> tile & 1) || d.base + key >= d.seen) sb = 0;
+          const bool odd = key & 1;  // odd keys take the groups of a pair the other way round: no bank twice
+          uint8_t* const row = &sm.k[i][0][0] + key * 128;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          const uint4 v = in ? qp[half * (D / 16) + c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 f = c4_unpack<F16>(x[y]);
-            reg[4 * c + y] = c4_pack<true>(f.x * up, f.y * up);
+          for (int g = 0; g < G; ++g) {
+            const uint32_t word = odd ? w[g ^ 1] : w[g];
+            const uint32_t sel = odd ? (0x4040u | (g ^ 1) | (g ^ 1) << 8) : (0x4040u | g | g << 8);
+            const uint32_t sc = __byte_perm(sb, 0u, sel) * k128 + 0x04000400u;
+            const int chunk = ((odd ? (g ^ 1) : g) & 1) * 4 + j;
+            *reinterpret_cast<uint4*>(row + (g >> 1) * kSub + ((chunk ^ (key & 7)) << 4)) = c4_unpack8(word, sc, magic);
           }
         }
-        const uint32_t col =
-            tmem + (static_cast<uint32_t>(quad * 32) << 16) + kColQ + (ib & 1) * kColQ2 + half * (D / 4);
-        if constexpr (D == 128) tmem_st32(col, reg);
-        else tmem_st16(col, reg);
-        if (half == 0) {
-          sm.factor[ib][quad * 32 + lane] = fmaxf(a.factor * __uint_as_float((254u - ex) << 23), 0x1p-126f);
-          sm.seen[ib][quad * 32 + lane] = in ? a.vis[d.tok0 + tok] : INT_MAX;
-        }
-        tmem_wait_st();
-        tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_ready[ib]);
-      }
-      // K: lane = (key, j), the 8 channels 32 g + 8 j of every group
-      const uint8_t* raw = sm.raw[s];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int key = (dt >> 2) + 64 * x, j = dt & 3, tile = key >> 4, t = key & 15;
-        const uint8_t* p = raw + tile * L::kTileBytes;
-        uint32_t w[G], sb;
-        if (G == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + L::k_row(t) + j * 16);
-          w[0] = v.x, w[1] = v.y, w[G - 2] = v.z, w[G - 1] = v.w;
-          sb = *reinterpret_cast<const uint32_t*>(p + L::kKScales + t * 4);
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(p + L::k_row(t) + j * 8);
-          w[0] = v.x, w[1] = v.y;
-          sb = *reinterpret_cast<const uint16_t*>(p + L::kKScales + t * 2);
+        if (lane == 0) {
+          mbar_arrive(&sm.k_full[i]);
+          mbar_arrive(&sm.raw_empty[s]);
         }
-        // what is not a visible row may hold scales that are infinite in fp16
-        if (!(d.tiles >> tile & 1) || d.base + key >= d.seen) sb = 0;
-        const bool odd = key & 1;  // odd keys take the groups of a pair the other way round: no bank twice
-        uint8_t* const row = &sm.k[i][0][0] + key * 128;
+      } else {
+        // V: lane = (key, r). A 64-column half holds groups 2 x and 2 x + 1, column 8 r + 2 i + b = channel
+        // 32 (2 x + b) + 4 r + i
+        if (!wait_all(&sm.v_empty[i], ((u >> 1) & 1) ^ 1, abort_flag, err)) break;
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          const int item = dw + 8 * x, key = (item >> 1) * 8 + (lane & 7), r = (item & 1) * 4 + (lane >> 3);
+          const int tile = key >> 4, t = key & 15;
+          const uint8_t* p = raw + tile * L::kTileBytes;
+          uint32_t w[G / 2], sb;
+          if (G == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p + L::v_piece(t, r));
+            w[0] = v.x, w[G / 2 - 1] = v.y;
+            sb = *reinterpret_cast<const uint32_t*>(p + L::kVScales + t * 4);
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(p + L::v_piece(t, r));
+            sb = *reinterpret_cast<const uint16_t*>(p + L::kVScales + t * 2);
+          }
+          if (!(d.tiles >> tile & 1) || d.base + key >= d.seen) sb = 0;
+          uint8_t* const row = &sm.v[i][0][0] + key * 128 + ((r ^ (key & 7)) << 4);
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const uint32_t word = odd ? w[g ^ 1] : w[g];
-          const uint32_t sel = odd ? (0x4040u | (g ^ 1) | (g ^ 1) << 8) : (0x4040u | g | g << 8);
-          const uint32_t sc = __byte_perm(sb, 0u, sel) * k128 + 0x04000400u;
-          const int chunk = ((odd ? (g ^ 1) : g) & 1) * 4 + j;
-          *reinterpret_cast<uint4*>(row + (g >> 1) * kSub + ((chunk ^ (key & 7)) << 4)) = unpack8(word, sc, magic);
+          for (int y = 0; y < G / 2; ++y) {
+            const uint32_t sc = __byte_perm(sb, 0u, y ? 0x4342 : 0x4140) * k128 + 0x04000400u;
+            *reinterpret_cast<uint4*>(row + y * kSub) = c4_unpack8(w[y], sc, magic);
+          }
         }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.k_full[i]);
-      // V: lane = (key, r). A 64-column half holds groups 2 x and 2 x + 1, column 8 r + 2 i + b = channel
-      // 32 (2 x + b) + 4 r + i
-      if (!wait_all(&sm.v_empty[i], ((u >> 1) & 1) ^ 1, abort_flag, err)) break;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int item = dw + 8 * x, key = (item >> 1) * 8 + (lane & 7), r = (item & 1) * 4 + (lane >> 3);
-        const int tile = key >> 4, t = key & 15;
-        const uint8_t* p = raw + tile * L::kTileBytes;
-        uint32_t w[G / 2], sb;
-        if (G == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(p + L::v_piece(t, r));
-          w[0] = v.x, w[G / 2 - 1] = v.y;
-          sb = *reinterpret_cast<const uint32_t*>(p + L::kVScales + t * 4);
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(p + L::v_piece(t, r));
-          sb = *reinterpret_cast<const uint16_t*>(p + L::kVScales + t * 2);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.v_full[i]);
+          mbar_arrive(&sm.raw_empty[s]);
         }
-        if (!(d.tiles >> tile & 1) || d.base + key >= d.seen) sb = 0;
-        uint8_t* const row = &sm.v[i][0][0] + key * 128 + ((r ^ (key & 7)) << 4);
-#pragma unroll
-        for (int y = 0; y < G / 2; ++y) {
-          const uint32_t sc = __byte_perm(sb, 0u, y ? 0x4342 : 0x4140) * k128 + 0x04000400u;
-          *reinterpret_cast<uint4*>(row + y * kSub) = unpack8(w[y], sc, magic);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.v_full[i]);
-        mbar_arrive(&sm.raw_empty[s]);
       }
     }
   } else {
@@ -345,12 +386,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         tmem_ld32(sc + key_lo + 32 * c, x);
         tmem_wait_ld();
         tmem_ld_fence(x);
-        if (edge) {
+#pragma unroll 1
+        for (int once = edge; once; once = 0) {
+          const int n = min(max(row_seen - (key0 + 32 * c), 0), 32);
+          const uint32_t tt = static_cast<uint32_t>(d.tiles) >> ((key_lo + 32 * c) / 16);
+          const uint32_t bits = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ((tt & 1 ? 0xFFFFu : 0u) | (tt & 2 ? 0xFFFF0000u : 0u));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int key = 32 * c + e;
-            if (!(d.tiles >> ((key_lo + key) / 16) & 1) || key0 + key >= row_seen) x[e] = 0xFF800000u;
-          }
+          for (int e = 0; e < 32; ++e)
+            if (!(bits >> e & 1)) x[e] = 0xFF800000u;
         }
       };
       float mx = -INFINITY;
