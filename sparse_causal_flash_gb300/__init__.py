@@ -98,6 +98,7 @@ class _Lib:
                 raise ImportError(f"{LIB_PATH} lacks {name}: rebuild it") from e
             fn.argtypes = args
             fn.restype = res
+            setattr(self, name, fn)  # found without __getattr__ from now on
         self._dll = dll
 
     def __getattr__(self, name):
@@ -308,38 +309,60 @@ def cache4_attn_workspace_size(N, R, Hq, Hkv, D) -> int:
     return int(_lib.scfa_cache4_attn_workspace_size(int(N), int(R), int(Hq), int(Hkv), int(D)))
 
 
-def _ints(name, device, **tensors):
-    for key, (t, n) in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name}: {key} must be a contiguous int32 tensor of {n} on {device}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
+# These calls serve single tokens, where the host's time counts: each checks its
+# tensors in one expression and only a call that fails it looks for the
+# argument to name.
+_i32 = torch.int32
 
 
-def _rows4(name, key, t, shape, dtype, device):
-    """Strides per token and head of a row tensor [N, heads, D]."""
-    if t.dtype != dtype or t.device != device or t.shape != shape or (t.stride(2) != 1):
-        raise ValueError(f"{name}: {key} must be {dtype} {tuple(shape)} on {device} with contiguous channels, got "
-                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+def _is(t, dtype, dev, n) -> bool:
+    return t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous()
+
+
+def _refuse(name, dev, **tensors):
+    """Raise for the first of key=(tensor, dtype, size) that is not a contiguous tensor of that kind on device dev."""
+    if dev < 0:
+        raise ValueError(f"{name}: expected CUDA tensors")
+    for key, (t, dtype, n) in tensors.items():
+        if not _is(t, dtype, dev, n):
+            raise ValueError(f"{name}: {key} must be a contiguous {dtype} tensor of {n} on cuda:{dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _rows4(name, key, t, N, H, D, dtype, dev):
+    """Strides per token and head of a row tensor [N, H, D]."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (N, H, D):
+        raise ValueError(f"{name}: {key} must be {dtype} {(N, H, D)} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: {key} must have contiguous channels, got strides {t.stride()}")
     # the stride of an axis of one is never used, and may be anything
-    return (t.stride(0) if shape[0] > 1 else 0), (t.stride(1) if shape[1] > 1 else 0)
+    return (st if N > 1 else 0), (sh if H > 1 else 0)
 
 
 def _cache4(name, cache, page_size, D):
-    """(pages, key heads) of a cache tensor."""
-    if (cache.dtype != torch.uint8 or not cache.is_cuda or cache.dim() != 3 or not cache.is_contiguous()
-            or cache.shape[2] != page_size * (D + D // 16)):
-        raise ValueError(f"{name}: cache must be a contiguous CUDA uint8 tensor [pages, heads, "
-                         f"{page_size * (D + D // 16)}], got {cache.dtype} {tuple(cache.shape)} on {cache.device}")
-    return cache.shape[0], cache.shape[1]
+    """(device index, pages, key heads) of a cache tensor."""
+    dev = cache.get_device()
+    if cache.dtype is not torch.uint8 or dev < 0 or cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError(f"{name}: cache must be a contiguous CUDA uint8 tensor [pages, heads, bytes], got {cache.dtype} "
+                         f"{tuple(cache.shape)} on {cache.device}")
+    P, H, nbytes = cache.shape
+    if nbytes != page_size * (D + D // 16):
+        raise ValueError(f"{name}: a page of {page_size} tokens, {D} channels has {page_size * (D + D // 16)} bytes a head, "
+                         f"not {nbytes}")
+    return dev, P, H
 
 
-def _launch(fn, device, stream, *args):
-    """Call a C entry point whose last argument is the stream, with `device` current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(fn, device, stream, *args)
-    st = torch.cuda.current_stream(device) if stream is None else stream
-    _check(fn, getattr(_lib, fn)(*args, st.cuda_stream))
+def _launch(fn, dev, stream, *args):
+    """Call a C entry point whose last argument is the stream, with device `dev` current."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _launch(fn, dev, stream, *args)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    code = getattr(_lib, fn)(*args, st)
+    if code != 0:
+        raise ScfaError(fn, code)
 
 
 def scfa_cache4_plan(len_, new_len, keep, free_pages, n_free, table, page_size, n_pages, len_out, n_free_out, q_start,
@@ -348,48 +371,46 @@ def scfa_cache4_plan(len_, new_len, keep, free_pages, n_free, table, page_size, 
     [N] uint8 or None): len_, new_len, len_out [R]; free_pages [n_pages];
     n_free, n_free_out [1]; table [R, max_pages]; q_start [R + 1]; slot, vis
     [N]. len_out / n_free_out may be len_ / n_free."""
-    R, N, dev = len_.numel(), slot.numel(), table.device
-    if not table.is_cuda or table.dim() != 2:
-        raise ValueError(f"scfa_cache4_plan: table must be a CUDA tensor [R, max_pages], got {tuple(table.shape)}")
-    _ints("scfa_cache4_plan", dev, len=(len_, R), new_len=(new_len, R), free_pages=(free_pages, n_pages),
-          n_free=(n_free, 1), table=(table, R * table.shape[1]), len_out=(len_out, R), n_free_out=(n_free_out, 1),
-          q_start=(q_start, R + 1), slot=(slot, N), vis=(vis, N))
-    if keep is not None and (keep.dtype != torch.uint8 or keep.device != dev or keep.numel() != N
-                             or not keep.is_contiguous()):
-        raise ValueError(f"scfa_cache4_plan: keep must be a contiguous uint8 tensor of {N} on {dev}")
+    R, N, dev, mp = len_.numel(), slot.numel(), table.get_device(), table.shape[-1]
+    if not (dev >= 0 and _is(table, _i32, dev, R * mp) and _is(len_, _i32, dev, R) and _is(new_len, _i32, dev, R)
+            and _is(free_pages, _i32, dev, n_pages) and _is(n_free, _i32, dev, 1) and _is(len_out, _i32, dev, R)
+            and _is(n_free_out, _i32, dev, 1) and _is(q_start, _i32, dev, R + 1) and _is(slot, _i32, dev, N)
+            and _is(vis, _i32, dev, N) and (keep is None or _is(keep, torch.uint8, dev, N))):
+        _refuse("scfa_cache4_plan", dev, table=(table, _i32, R * mp), len=(len_, _i32, R), new_len=(new_len, _i32, R),
+                free_pages=(free_pages, _i32, n_pages), n_free=(n_free, _i32, 1), len_out=(len_out, _i32, R),
+                n_free_out=(n_free_out, _i32, 1), q_start=(q_start, _i32, R + 1), slot=(slot, _i32, N),
+                vis=(vis, _i32, N), **({} if keep is None else {"keep": (keep, torch.uint8, N)}))
     _launch("scfa_cache4_plan", dev, stream, len_.data_ptr(), new_len.data_ptr(),
             None if keep is None else keep.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), table.data_ptr(), N, R,
-            table.shape[1], page_size, n_pages, len_out.data_ptr(), n_free_out.data_ptr(), q_start.data_ptr(),
-            slot.data_ptr(), vis.data_ptr(), ws.data_ptr(), ws.numel())
+            mp, page_size, n_pages, len_out.data_ptr(), n_free_out.data_ptr(), q_start.data_ptr(), slot.data_ptr(),
+            vis.data_ptr(), ws.data_ptr(), ws.numel())
 
 
 def scfa_cache4_append(k, v, slot, cache, page_size, stream=None):
     """Quantise the rows k, v [N, Hkv, D] (bf16 or fp16; any token and head
     strides that are multiples of 8) into their slots of the cache."""
-    N, H, D = k.shape
-    P, Hkv = _cache4("scfa_cache4_append", cache, page_size, D)
-    dev = cache.device
-    dt = _DTYPES.get(k.dtype, -1)
-    shape = (N, Hkv, D)
-    kt, kh = _rows4("scfa_cache4_append", "k", k, shape, k.dtype, dev)
-    vt, vh = _rows4("scfa_cache4_append", "v", v, shape, k.dtype, dev)
-    _ints("scfa_cache4_append", dev, slot=(slot, N))
-    _launch("scfa_cache4_append", dev, stream, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slot.data_ptr(), N, Hkv, D,
-            dt, cache.data_ptr(), page_size, P)
+    N, _, D = k.shape
+    dev, P, H = _cache4("scfa_cache4_append", cache, page_size, D)
+    dt = k.dtype
+    kt, kh = _rows4("scfa_cache4_append", "k", k, N, H, D, dt, dev)
+    vt, vh = _rows4("scfa_cache4_append", "v", v, N, H, D, dt, dev)
+    if not _is(slot, _i32, dev, N):
+        _refuse("scfa_cache4_append", dev, slot=(slot, _i32, N))
+    _launch("scfa_cache4_append", dev, stream, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, slot.data_ptr(), N, H, D,
+            _DTYPES.get(dt, -1), cache.data_ptr(), page_size, P)
 
 
 def scfa_cache4_read(cache, page_size, slot, k_out, v_out, stream=None):
     """k_out, v_out [N, Hkv, D] = the values of the slots' rows (zero rows for slots outside the cache)."""
-    N, H, D = k_out.shape
-    P, Hkv = _cache4("scfa_cache4_read", cache, page_size, D)
-    dev = cache.device
-    dt = _DTYPES.get(k_out.dtype, -1)
-    shape = (N, Hkv, D)
-    kt, kh = _rows4("scfa_cache4_read", "k_out", k_out, shape, k_out.dtype, dev)
-    vt, vh = _rows4("scfa_cache4_read", "v_out", v_out, shape, k_out.dtype, dev)
-    _ints("scfa_cache4_read", dev, slot=(slot, N))
-    _launch("scfa_cache4_read", dev, stream, cache.data_ptr(), page_size, P, slot.data_ptr(), N, Hkv, D, dt,
-            k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh)
+    N, _, D = k_out.shape
+    dev, P, H = _cache4("scfa_cache4_read", cache, page_size, D)
+    dt = k_out.dtype
+    kt, kh = _rows4("scfa_cache4_read", "k_out", k_out, N, H, D, dt, dev)
+    vt, vh = _rows4("scfa_cache4_read", "v_out", v_out, N, H, D, dt, dev)
+    if not _is(slot, _i32, dev, N):
+        _refuse("scfa_cache4_read", dev, slot=(slot, _i32, N))
+    _launch("scfa_cache4_read", dev, stream, cache.data_ptr(), page_size, P, slot.data_ptr(), N, H, D,
+            _DTYPES.get(dt, -1), k_out.data_ptr(), kt, kh, v_out.data_ptr(), vt, vh)
 
 
 def scfa_cache4_attn(q, cache, page_size, table, q_start, vis, scale, o, lse, ws, flags=0, stream=None):
@@ -397,19 +418,18 @@ def scfa_cache4_attn(q, cache, page_size, table, q_start, vis, scale, o, lse, ws
     tokens: token t of request r (q_start[r] <= t < q_start[r + 1]) sees the
     first vis[t] of them. o [N, Hq, D], lse [N, Hq] fp32."""
     N, Hq, D = q.shape
-    P, Hkv = _cache4("scfa_cache4_attn", cache, page_size, D)
-    dev = cache.device
-    dt = _DTYPES.get(q.dtype, -1)
-    shape = (N, Hq, D)
-    qt, qh = _rows4("scfa_cache4_attn", "q", q, shape, q.dtype, dev)
-    ot, oh = _rows4("scfa_cache4_attn", "o", o, shape, q.dtype, dev)
+    dev, P, Hkv = _cache4("scfa_cache4_attn", cache, page_size, D)
+    dt = q.dtype
+    qt, qh = _rows4("scfa_cache4_attn", "q", q, N, Hq, D, dt, dev)
+    ot, oh = _rows4("scfa_cache4_attn", "o", o, N, Hq, D, dt, dev)
     R, mp = table.shape
-    _ints("scfa_cache4_attn", dev, table=(table, R * mp), q_start=(q_start, R + 1), vis=(vis, N))
-    if lse.dtype != torch.float32 or lse.device != dev or lse.shape != (N, Hq) or not lse.is_contiguous():
-        raise ValueError(f"scfa_cache4_attn: lse must be a contiguous fp32 tensor ({N}, {Hq}) on {dev}")
+    if not (_is(table, _i32, dev, R * mp) and _is(q_start, _i32, dev, R + 1) and _is(vis, _i32, dev, N)
+            and _is(lse, torch.float32, dev, N * Hq)):
+        _refuse("scfa_cache4_attn", dev, table=(table, _i32, R * mp), q_start=(q_start, _i32, R + 1), vis=(vis, _i32, N),
+                lse=(lse, torch.float32, N * Hq))
     _launch("scfa_cache4_attn", dev, stream, q.data_ptr(), qt, qh, cache.data_ptr(), page_size, P, table.data_ptr(), mp,
-            q_start.data_ptr(), vis.data_ptr(), N, R, Hq, Hkv, D, scale, dt, o.data_ptr(), ot, oh, lse.data_ptr(),
-            ws.data_ptr(), ws.numel(), flags)
+            q_start.data_ptr(), vis.data_ptr(), N, R, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), o.data_ptr(), ot, oh,
+            lse.data_ptr(), ws.data_ptr(), ws.numel(), flags)
 
 
 # ---------------------------------------------------------------- tiles

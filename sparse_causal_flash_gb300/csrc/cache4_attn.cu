@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
     desc->parts = 0;
   }
 
+  grid_release();
   C4Span span;
   if (!c4_span<ROWS, kThreads>(a, s_span, span)) return;  // (the whole CTA)
   const int n_units = span.units;
@@ -501,17 +502,17 @@ int c4_rows(int N, int R, int G) {
   const long long tokens = (static_cast<long long>(N) + R - 1) / R, rows = tokens * G;
   return rows <= 8 ? 8 : rows <= 16 && tokens == 1 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
-int c4_ctas(int rows, int D) { return (rows == 8 ? (D == 128 ? 3 : 4) : rows == 16 ? 2 : 1) * num_sms(); }
+int c4_ctas(int rows, int D, int sms) { return (rows == 8 ? (D == 128 ? 3 : 4) : rows == 16 ? 2 : 1) * sms; }
 
 struct C4Ws {
   size_t desc = 0, ml = 0, part = 0, total = 0;
 };
 // One size for every N and R, so that a workspace serves smaller steps too.
-C4Ws c4_ws(int D) {
+C4Ws c4_ws(int D, int sms) {
   C4Ws w;
   size_t n = 0, rows = 0;
   for (int x = 8; x <= 128; x *= 2) {
-    const size_t c = c4_ctas(x, D);
+    const size_t c = c4_ctas(x, D, sms);
     n = c > n ? c : n;
     rows = c * 2 * x > rows ? c * 2 * x : rows;
   }
@@ -523,21 +524,14 @@ C4Ws c4_ws(int D) {
 }
 
 template <int D, bool F16, int NT>
-cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
+cudaError_t launch(int grid, const C4AttnArgs& a, cudaStream_t st) {
   using C = C4Cfg<D, NT>;
-  const int grid = c4_ctas(8 * NT, D);
-  auto kern = cache4_attn_kernel<D, F16, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-  if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, C::kSmem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cache4_join_kernel<D, F16, C::kRows><<<grid, kJoinThreads, 0, st>>>(a, grid);
-  return cudaGetLastError();
+  return launch_and_join<D, F16, C::kRows>(cache4_attn_kernel<D, F16, NT>, grid, kThreads, C::kSmem, a, st);
 }
 
 template <int D, bool F16>
-cudaError_t launch_rows(int rows, const C4AttnArgs& a, cudaStream_t st) {
-  return rows == 8 ? launch<D, F16, 1>(a, st) : launch<D, F16, 2>(a, st);
+cudaError_t launch_rows(int rows, int grid, const C4AttnArgs& a, cudaStream_t st) {
+  return rows == 8 ? launch<D, F16, 1>(grid, a, st) : launch<D, F16, 2>(grid, a, st);
 }
 
 }  // namespace
@@ -549,7 +543,7 @@ extern "C" {
 
 size_t scfa_cache4_attn_workspace_size(int N, int R, int Hq, int Hkv, int D) {
   if (N < 1 || R < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  return c4_ws(D).total;
+  return c4_ws(D, num_sms()).total;
 }
 
 scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_head, const uint8_t* cache,
@@ -563,13 +557,14 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * page_size >= (1ll << 31) || static_cast<long long>(N) * Hq >= (1ll << 31) - 256)
+      static_cast<long long>(max_pages) * page_size >= (1ll << 31) ||
+      static_cast<long long>(N) * Hq >= (1ll << 31) - 256)
     return SCFA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SCFA_ERR_INVALID;
   if ((q_token | q_head | o_token | o_head) & 7) return SCFA_ERR_INVALID;
-  const int G = Hq / Hkv, rows = c4_rows(N, R, G);
-  const C4Ws w = c4_ws(D);
+  const int G = Hq / Hkv, rows = c4_rows(N, R, G), sms = num_sms(), grid = c4_ctas(rows, D, sms);
+  const C4Ws w = c4_ws(D, sms);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total) return SCFA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = dtype == SCFA_DTYPE_F16;
@@ -588,9 +583,10 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   a.part = reinterpret_cast<float*>(p + w.part);
   a.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0;
   a.k16 = 16u, a.k128 = 128u, a.magic = 0x60006000u;
-  const cudaError_t e = rows > 16 ? launch_cache4_wide(D, f16, rows, a, st)
-                        : D == 64 ? (f16 ? launch_rows<64, true>(rows, a, st) : launch_rows<64, false>(rows, a, st))
-                                  : (f16 ? launch_rows<128, true>(rows, a, st) : launch_rows<128, false>(rows, a, st));
+  const cudaError_t e =
+      rows > 16 ? launch_cache4_wide(D, f16, rows, grid, a, st)
+      : D == 64 ? (f16 ? launch_rows<64, true>(rows, grid, a, st) : launch_rows<64, false>(rows, grid, a, st))
+                : (f16 ? launch_rows<128, true>(rows, grid, a, st) : launch_rows<128, false>(rows, grid, a, st));
   if (e != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;

@@ -124,6 +124,11 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, c4_wait(bar, parity, abort_flag, status, ns));
 }
 
+// Let the kernel launched behind this one start its CTAs as these leave; it
+// waits with grid_wait() before it reads what this one writes.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // a / b, in 32 bits where they hold it
 __device__ __forceinline__ long long c4_div(long long a, int b) {
   return a >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -355,7 +360,7 @@ struct C4Pages {
 };
 
 // cache4_wide.cu: blocks of rp = 32, 64 or 128 query rows, one CTA per SM
-cudaError_t launch_cache4_wide(int D, bool f16, int rp, const C4AttnArgs& a, cudaStream_t st);
+cudaError_t launch_cache4_wide(int D, bool f16, int rp, int grid, const C4AttnArgs& a, cudaStream_t st);
 
 namespace {
 // Joins the partial rows of the items that were cut, in the order of their
@@ -370,6 +375,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a,
   __shared__ float s_l[kJoinWarps / 2];
   __shared__ int s_err[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  grid_wait();
   const C4Desc d = a.desc[blockIdx.x];
   if (blockIdx.x == 0) {
     int err = 0;
@@ -445,6 +451,34 @@ __global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a,
     }
     __syncthreads();
   }
+}
+
+
+// The main kernel (its dynamic shared memory allowed once per device) and
+// behind it the join, whose launch hides under the main kernel's end.
+template <int D, bool F16, int ROWS, typename Kernel>
+cudaError_t launch_and_join(Kernel kern, int grid, int threads, size_t smem, const C4AttnArgs& a, cudaStream_t st) {
+  static bool allowed[64] = {};  // by device; setting it twice does no harm
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  kern<<<grid, threads, smem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache4_join_kernel<D, F16, ROWS>, a, grid);
 }
 
 }  // namespace

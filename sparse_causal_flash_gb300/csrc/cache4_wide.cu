@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
     desc->err = SCFA_OK;
     desc->parts = 0;
   }
+  grid_release();
   C4Span span;
   if (!c4_span<RP, kWideThreads>(a, sm.span, span)) return;  // (the whole CTA)
   const int n_units = span.units;
@@ -559,28 +560,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
 }
 
 template <int D, bool F16, int RP>
-cudaError_t launch(const C4AttnArgs& a, cudaStream_t st) {
-  const int grid = num_sms();
-  const size_t smem = sizeof(WideSmem<D>) + 1024;
-  auto kern = cache4_wide_kernel<D, F16, RP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  kern<<<grid, kWideThreads, smem, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cache4_join_kernel<D, F16, RP><<<grid, kJoinThreads, 0, st>>>(a, grid);
-  return cudaGetLastError();
+cudaError_t launch(int grid, const C4AttnArgs& a, cudaStream_t st) {
+  return launch_and_join<D, F16, RP>(cache4_wide_kernel<D, F16, RP>, grid, kWideThreads, sizeof(WideSmem<D>) + 1024, a,
+                                     st);
 }
 
 template <int D, bool F16>
-cudaError_t launch_rp(int rp, const C4AttnArgs& a, cudaStream_t st) {
-  return rp == 32 ? launch<D, F16, 32>(a, st) : rp == 64 ? launch<D, F16, 64>(a, st) : launch<D, F16, 128>(a, st);
+cudaError_t launch_rp(int rp, int grid, const C4AttnArgs& a, cudaStream_t st) {
+  return rp == 32   ? launch<D, F16, 32>(grid, a, st)
+         : rp == 64 ? launch<D, F16, 64>(grid, a, st)
+                    : launch<D, F16, 128>(grid, a, st);
 }
 
 }  // namespace
 
-cudaError_t launch_cache4_wide(int D, bool f16, int rp, const C4AttnArgs& a, cudaStream_t st) {
-  if (D == 64) return f16 ? launch_rp<64, true>(rp, a, st) : launch_rp<64, false>(rp, a, st);
-  return f16 ? launch_rp<128, true>(rp, a, st) : launch_rp<128, false>(rp, a, st);
+cudaError_t launch_cache4_wide(int D, bool f16, int rp, int grid, const C4AttnArgs& a, cudaStream_t st) {
+  if (D == 64) return f16 ? launch_rp<64, true>(rp, grid, a, st) : launch_rp<64, false>(rp, grid, a, st);
+  return f16 ? launch_rp<128, true>(rp, grid, a, st) : launch_rp<128, false>(rp, grid, a, st);
 }
 
 }  // namespace scfa
