@@ -101,12 +101,35 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
   if (tid == 0) s_bad = 0;
   long long kept_all = 0;
   if (a.keep != nullptr) {
-    for (int base = 0; base < a.N; base += nt) {
-      const int t = base + tid;
-      const int k = t < a.N && a.keep[t] != 0;
+    // 16 tokens a thread and round, by one load where the mask allows it
+    const bool vec = (reinterpret_cast<uintptr_t>(a.keep) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.vis) & 15u) == 0;
+    for (long long base = 0; base < a.N; base += 16ll * nt) {
+      const long long t0 = base + 16ll * tid;
+      uint32_t bits = 0;  // of the kept ones
+      const bool whole = vec && t0 + 16 <= a.N;
+      if (whole) {
+        const uint4 v = *reinterpret_cast<const uint4*>(a.keep + t0);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bits |= ((x[i / 4] >> (8 * (i % 4)) & 255u) != 0u ? 1u : 0u) << i;
+      } else {
+        for (int i = 0; i < 16 && t0 + i < a.N; ++i) bits |= (a.keep[t0 + i] != 0 ? 1u : 0u) << i;
+      }
       long long sum;
-      const long long before = block_excl(k, part, &sum);
-      if (t < a.N) a.vis[t] = static_cast<int32_t>(kept_all + before);
+      const int before = static_cast<int>(kept_all + block_excl(__popc(bits), part, &sum));
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          int4 v;
+          v.x = before + __popc(bits & ((1u << i) - 1u));
+          v.y = before + __popc(bits & ((2u << i) - 1u));
+          v.z = before + __popc(bits & ((4u << i) - 1u));
+          v.w = before + __popc(bits & ((8u << i) - 1u));
+          *reinterpret_cast<int4*>(a.vis + t0 + i) = v;
+        }
+      } else {
+        for (int i = 0; i < 16 && t0 + i < a.N; ++i) a.vis[t0 + i] = before + __popc(bits & ((1u << i) - 1u));
+      }
       kept_all += sum;
     }
   }
@@ -170,27 +193,46 @@ struct RowArgs {
   uint16_t *k_out, *v_out;
   long long kt, kh, vt, vh;  // strides per token and head
   const int32_t* slot;
-  long long rows;  // N * Hkv
-  int Hkv, page_size, log_ps;
+  long long rows;  // Hkv times N, rounded up to four
+  int N, Hkv, page_size, log_ps;
   long long slots;  // slots of the cache
   uint8_t* cache;
 };
 
-// Eight threads per row (one token of one head): HBM bound, the rows read
-// once and the codes written once. Thread i quantises D / 8 consecutive
-// channels of K (D / 64 words) and the channels 32 g + 4 i + 0..3 of V, which
-// is how the tile groups them, so every store is a whole word.
+// Eight threads per row (one token of one head), the four rows of a warp four
+// tokens in a row of one head: tokens appended together mostly follow each
+// other in a tile, and the V codes of four such tokens fill whole 32-byte
+// sectors. Thread i takes D / 8 consecutive channels of K (D / 64 words) and
+// the channels 32 g + 4 i + 0..3 of V, as the tile groups them, so every store
+// is a whole word.
+struct RowAt {
+  long long tok;
+  int head, i;
+  bool in;
+};
+__device__ __forceinline__ RowAt row_at(const RowArgs& a) {
+  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
+  const long long quad = row >> 2, four = quad / a.Hkv;
+  RowAt r;
+  r.tok = four * 4 + (row & 3);
+  r.head = static_cast<int>(quad - four * a.Hkv);
+  r.i = threadIdx.x & 7;
+  r.in = r.tok < a.N;
+  return r;
+}
+
+// HBM bound: the rows are read once and the codes written once. A group's
+// largest magnitude is taken on the bits, two values at a time (a NaN is then
+// larger than infinity and is seen); groups with a value that is not finite or
+// beyond the largest scale take the careful way.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) append_kernel(RowArgs a) {
   using L = C4<D>;
   constexpr int W = D / 64;  // K words per thread
   constexpr int G = L::kG;
-  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
-  const int i = threadIdx.x & 7;
-  const bool in = row < a.rows;
-  const long long tok = in ? row / a.Hkv : 0;
-  const int head = static_cast<int>(in ? row - tok * a.Hkv : 0);
-  const long long slot = in ? a.slot[tok] : -1;
+  const RowAt r = row_at(a);
+  const int i = r.i;
+  const long long slot = r.in ? a.slot[r.tok] : -1;
   const bool live = slot >= 0 && slot < a.slots;
   // every thread stays for the shuffles
   uint32_t kw[4 * W], vw[2 * G];
@@ -199,66 +241,102 @@ __global__ void __launch_bounds__(256) append_kernel(RowArgs a) {
 #pragma unroll
   for (int x = 0; x < 2 * G; ++x) vw[x] = 0;
   if (live) {
-    const uint4* ks = reinterpret_cast<const uint4*>(a.k + tok * a.kt + head * a.kh + i * (8 * W));
+    const uint4* ks = reinterpret_cast<const uint4*>(a.k + r.tok * a.kt + r.head * a.kh + i * (8 * W));
 #pragma unroll
     for (int x = 0; x < W; ++x) {
       const uint4 u = ks[x];
       kw[4 * x] = u.x, kw[4 * x + 1] = u.y, kw[4 * x + 2] = u.z, kw[4 * x + 3] = u.w;
     }
-    const uint16_t* vs = a.v + tok * a.vt + head * a.vh + 4 * i;
+    const uint16_t* vs = a.v + r.tok * a.vt + r.head * a.vh + 4 * i;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint2 u = *reinterpret_cast<const uint2*>(vs + 32 * g);
       vw[2 * g] = u.x, vw[2 * g + 1] = u.y;
     }
   }
-  float amax = 0.f;  // fmaxf leaves a NaN out
+  // bits of the largest magnitude of a group, K and V of up to four groups
+  uint32_t kmax = 0;
 #pragma unroll
-  for (int x = 0; x < 4 * W; ++x) {
-    const float2 f = c4_unpack<F16>(kw[x]);
-    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-  }
-  // a group of 32 channels lies in 32 / (D / 8) threads
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  if (W == 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  float vmax[G];
+  for (int x = 0; x < 4 * W; ++x) kmax = __vmaxu2(kmax, kw[x] & 0x7FFF7FFFu);
+  // (a group of 32 channels of K lies in 32 / (D / 8) threads)
+  kmax = __vmaxu2(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
+  if (W == 1) kmax = __vmaxu2(kmax, __shfl_xor_sync(0xffffffffu, kmax, 2));
+  uint32_t vmax[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const float2 f = c4_unpack<F16>(vw[2 * g]), h = c4_unpack<F16>(vw[2 * g + 1]);
-    vmax[g] = fmaxf(fmaxf(fmaxf(0.f, fabsf(f.x)), fabsf(f.y)), fmaxf(fabsf(h.x), fabsf(h.y)));
+    vmax[g] = __vmaxu2(vw[2 * g] & 0x7FFF7FFFu, vw[2 * g + 1] & 0x7FFF7FFFu);
+    vmax[g] = max(vmax[g] & 0xFFFFu, vmax[g] >> 16);
+  }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) vmax[g] = fmaxf(vmax[g], __shfl_xor_sync(0xffffffffu, vmax[g], o));
+  for (int g = 0; g < G; g += 2) {  // two groups a shuffle
+    uint32_t m = vmax[g] | vmax[g + 1] << 16;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    vmax[g] = m & 0xFFFFu, vmax[g + 1] = m >> 16;
+  }
+  kmax = max(kmax & 0xFFFFu, kmax >> 16);
+  // 64512 in bf16 and fp16: from here on codes would leave -7..7
+  constexpr uint32_t kMost = F16 ? 0x7BE0u : 0x477Cu;
+  bool careful = kmax > kMost;
+#pragma unroll
+  for (int g = 0; g < G; ++g) careful |= vmax[g] > kMost;
+  if (__any_sync(0xffffffffu, careful)) {
+    // cut to what the format holds, NaN to 0, and take the maxima again
+    auto cut = [](uint32_t w) {
+      const float2 f = c4_unpack<F16>(w);
+      return c4_pack<F16>(c4_cut(f.x), c4_cut(f.y));
+    };
+    kmax = 0;
+#pragma unroll
+    for (int x = 0; x < 4 * W; ++x) {
+      kw[x] = cut(kw[x]);
+      kmax = __vmaxu2(kmax, kw[x] & 0x7FFF7FFFu);
+    }
+    kmax = __vmaxu2(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
+    if (W == 1) kmax = __vmaxu2(kmax, __shfl_xor_sync(0xffffffffu, kmax, 2));
+    kmax = max(kmax & 0xFFFFu, kmax >> 16);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      vw[2 * g] = cut(vw[2 * g]), vw[2 * g + 1] = cut(vw[2 * g + 1]);
+      uint32_t m = __vmaxu2(vw[2 * g] & 0x7FFF7FFFu, vw[2 * g + 1] & 0x7FFF7FFFu);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      vmax[g] = max(m & 0xFFFFu, m >> 16);
+    }
   }
   if (!live) return;
   const int at = static_cast<int>(slot & (a.page_size - 1)), t = at & 15;
-  uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, head, a.page_size, at, L::kTileBytes);
-  const uint32_t kb = c4_scale_byte(amax);
-  const float ksc = c4_scale(kb);
+  uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, r.head, a.page_size, at, L::kTileBytes);
+  const uint32_t kb = c4_scale_byte(c4_unpack<F16>(kmax).x);
+  const float kinv = c4_reciprocal(c4_scale(kb));
 #pragma unroll
   for (int x = 0; x < W; ++x) {
     const int word = i * W + x, g = word >> 2, j = word & 3;
+    // channels 2 y and 2 y + 1 of the word in bits 4 y and 4 y + 16; the codes' common high bits add up to a constant
     uint32_t c = 0;
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {  // channels 2 y and 2 y + 1 of the word
+    for (int y = 0; y < 4; ++y) {
       const float2 f = c4_unpack<F16>(kw[4 * x + y]);
-      c |= c4_code(f.x, ksc) << (4 * y) | c4_code(f.y, ksc) << (4 * y + 16);
+      c += (c4_code(f.x, kinv) << (4 * y)) + (c4_code(f.y, kinv) << (4 * y + 16));
     }
-    *reinterpret_cast<uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4) = c;
+    *reinterpret_cast<uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4) = c - 0x4B400000u * 0x1111u;
     if (j == 0) tile[L::kKScales + t * G + g] = static_cast<uint8_t>(kb);
   }
-  uint32_t piece[G / 2];
+  uint32_t piece[G / 2], mine = 0;
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const uint32_t b = c4_scale_byte(vmax[g]);
-    const float s = c4_scale(b);
+    const uint32_t b = c4_scale_byte(c4_unpack<F16>(vmax[g]).x);
+    const float inv = c4_reciprocal(c4_scale(b));
     const float2 f = c4_unpack<F16>(vw[2 * g]), h = c4_unpack<F16>(vw[2 * g + 1]);
-    const uint32_t c = c4_code(f.x, s) | c4_code(f.y, s) << 4 | c4_code(h.x, s) << 8 | c4_code(h.y, s) << 12;
-    if (g & 1) piece[g / 2] |= c << 16;
+    const uint32_t c = c4_code(f.x, inv) + (c4_code(f.y, inv) << 4) + (c4_code(h.x, inv) << 8) +
+                       (c4_code(h.y, inv) << 12);  // right in its low 16 bits
+    if (g & 1) piece[g / 2] = __byte_perm(piece[g / 2], c, 0x5410);
     else piece[g / 2] = c;
-    if (i == g) tile[L::kVScales + t * G + g] = static_cast<uint8_t>(b);
+    if (i == g) mine = b;
   }
-#pragma unroll
-  for (int x = 0; x < G / 2; ++x) *reinterpret_cast<uint32_t*>(tile + L::v_piece(t, i) + 4 * x) = piece[x];
+  if (G == 4) *reinterpret_cast<uint2*>(tile + L::v_piece(t, i)) = make_uint2(piece[0], piece[G / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(tile + L::v_piece(t, i)) = piece[0];
+  if (i < G) tile[L::kVScales + t * G + i] = static_cast<uint8_t>(mine);
 }
 
 // The reverse, with the same threads: a thread writes the channels it read
@@ -268,14 +346,12 @@ __global__ void __launch_bounds__(256) read_kernel(RowArgs a) {
   using L = C4<D>;
   constexpr int W = D / 64;
   constexpr int G = L::kG;
-  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
-  const int i = threadIdx.x & 7;
-  if (row >= a.rows) return;
-  const long long tok = row / a.Hkv;
-  const int head = static_cast<int>(row - tok * a.Hkv);
-  const long long slot = a.slot[tok];
-  uint16_t* ko = a.k_out + tok * a.kt + head * a.kh + i * (8 * W);
-  uint16_t* vo = a.v_out + tok * a.vt + head * a.vh + 4 * i;
+  const RowAt r = row_at(a);
+  if (!r.in) return;
+  const int i = r.i;
+  const long long slot = a.slot[r.tok];
+  uint16_t* ko = a.k_out + r.tok * a.kt + r.head * a.kh + i * (8 * W);
+  uint16_t* vo = a.v_out + r.tok * a.vt + r.head * a.vh + 4 * i;
   if (slot < 0 || slot >= a.slots) {
 #pragma unroll
     for (int x = 0; x < W; ++x) reinterpret_cast<uint4*>(ko)[x] = make_uint4(0u, 0u, 0u, 0u);
@@ -284,27 +360,40 @@ __global__ void __launch_bounds__(256) read_kernel(RowArgs a) {
     return;
   }
   const int at = static_cast<int>(slot & (a.page_size - 1)), t = at & 15;
-  const uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, head, a.page_size, at, L::kTileBytes);
+  const uint8_t* tile = a.cache + c4_tile_base(slot >> a.log_ps, a.Hkv, r.head, a.page_size, at, L::kTileBytes);
+  uint32_t kc[W], ks[W], vc[G / 2];
 #pragma unroll
   for (int x = 0; x < W; ++x) {
     const int word = i * W + x, g = word >> 2, j = word & 3;
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4);
-    const float s = c4_scale(tile[L::kKScales + t * G + g]);
+    kc[x] = *reinterpret_cast<const uint32_t*>(tile + L::k_row(t) + (j * G + g) * 4);
+    ks[x] = tile[L::kKScales + t * G + g];
+  }
+  uint32_t vs;  // the scale bytes of the groups
+  if (G == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(tile + L::v_piece(t, i));
+    vc[0] = u.x, vc[G / 2 - 1] = u.y;
+    vs = *reinterpret_cast<const uint32_t*>(tile + L::kVScales + t * G);
+  } else {
+    vc[0] = *reinterpret_cast<const uint32_t*>(tile + L::v_piece(t, i));
+    vs = *reinterpret_cast<const uint16_t*>(tile + L::kVScales + t * G);
+  }
+  // a code's bits under the exponent of 2^23 are 2^23 + (c + 8)
+  auto value = [](uint32_t c, float s) { return (__uint_as_float(c | 0x4B000000u) - (8388608.f + 8.f)) * s; };
+#pragma unroll
+  for (int x = 0; x < W; ++x) {
+    const float s = c4_scale(ks[x]);
     uint32_t w[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y)
-      w[y] = c4_pack<F16>(static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8) * s,
-                          static_cast<float>(static_cast<int>(c >> (4 * y + 16) & 15u) - 8) * s);
+      w[y] = c4_pack<F16>(value(kc[x] >> (4 * y) & 15u, s), value(kc[x] >> (4 * y + 16) & 15u, s));
     reinterpret_cast<uint4*>(ko)[x] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const uint32_t c = *reinterpret_cast<const uint16_t*>(tile + L::v_piece(t, i) + 2 * g);
-    const float s = c4_scale(tile[L::kVScales + t * G + g]);
-    float f[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) f[y] = static_cast<float>(static_cast<int>(c >> (4 * y) & 15u) - 8) * s;
-    *reinterpret_cast<uint2*>(vo + 32 * g) = make_uint2(c4_pack<F16>(f[0], f[1]), c4_pack<F16>(f[2], f[3]));
+    const uint32_t c = vc[g / 2] >> (16 * (g & 1));
+    const float s = c4_scale(vs >> (8 * g) & 255u);
+    *reinterpret_cast<uint2*>(vo + 32 * g) = make_uint2(c4_pack<F16>(value(c & 15u, s), value(c >> 4 & 15u, s)),
+                                                        c4_pack<F16>(value(c >> 8 & 15u, s), value(c >> 12 & 15u, s)));
   }
 }
 
@@ -340,7 +429,8 @@ RowArgs row_args(long long kt, long long kh, long long vt, long long vh, const i
   RowArgs a = {};
   a.kt = kt, a.kh = kh, a.vt = vt, a.vh = vh;
   a.slot = slot;
-  a.rows = static_cast<long long>(N) * Hkv;
+  a.N = N;
+  a.rows = (static_cast<long long>(N) + 3) / 4 * 4 * Hkv;
   a.Hkv = Hkv;
   a.page_size = page_size;
   while ((1 << a.log_ps) < page_size) ++a.log_ps;
@@ -388,7 +478,7 @@ scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const u
                       reinterpret_cast<int32_t*>(p + w.free_before), reinterpret_cast<PlanReq*>(p + w.req)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int fill = N <= kPlanOneCta;
-  const int most = (fill || keep) && N > R ? N : R;  // items of the longest loop
+  const int items = fill ? N : keep ? (N + 15) / 16 : 1, most = items > R ? items : R;  // of the longest loop
   const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
   plan_kernel<<<1, threads, 0, st>>>(a, fill);
   if (!fill) plan_fill_kernel<<<(N + 255) / 256, 256, 0, st>>>(a);

@@ -41,22 +41,34 @@ __device__ __forceinline__ float c4_scale(uint32_t b, uint32_t shift = 112u) {
 }
 
 // Scale byte of a group with largest magnitude a (a NaN has been left out of
-// a). a / 7 must be the correctly rounded quotient: bf16 and fp16 inputs then
-// round to four bits exactly as the real quotient does (a = 7 t for a tie t
-// divides exactly, any other quotient is at least 2^-15 of itself away).
+// a): a / 7 rounded to four significant bits, ties to even. The product with
+// 1 / 7 is within 2^-23 of the quotient; rounding it to 17 bits first brings
+// a tie (a = 7 t) back to t exactly and can not make one, since any other
+// quotient of a bf16 or fp16 number is 2^-11 of itself or more away from a tie.
 __device__ __forceinline__ uint32_t c4_scale_byte(float a) {
-  const float t = fminf(fmaxf(__fdiv_rn(a, 7.f), 0x1p-15f), 9216.f);
-  uint32_t u = __float_as_uint(t);
+  const float t = fminf(fmaxf(a * (1.f / 7.f), 0x1p-15f), 9216.f);
+  uint32_t u = (__float_as_uint(t) + 0x40u) & ~0x7Fu;
   u += 0x7FFFFu + ((u >> 20) & 1u);
   return (u >> 20) - (112u << 3);
 }
 
-// code + 8 of x under scale s: x / s to nearest even, within -7..7. The
-// quotient is correctly rounded, so a tie (x = (k + 1/2) s, exact) stays one.
-__device__ __forceinline__ uint32_t c4_code(float x, float s) {
-  x = x == x ? x : 0.f;
-  return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, s)), -7.f), 7.f)) + 8);
+// Code + 8 of x under the scale whose reciprocal is inv: x / s to nearest
+// even. fma(x, 1 / s, 384) rounds the quotient to a multiple of 2^-15,
+// which restores a tie (x = (k + 1/2) s) and makes none: any other quotient of
+// a bf16 or fp16 number by a scale is 2^-13 or more away from one, the product
+// within 2^-20 of it. Adding 1.5 2^23 + 8 - 384 then rounds to a whole number,
+// ties to even in the low bits. A magnitude of at most 64512 is below 7.5 s, so no
+// code leaves -7..7.
+__device__ __forceinline__ float c4_reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
 }
+__device__ __forceinline__ uint32_t c4_code(float x, float inv) {  // 0x4B400000 + code + 8
+  return __float_as_uint(fmaf(x, inv, 384.f) + (12582912.f + 8.f - 384.f));
+}
+// for what is not finite or above 64512: NaN is 0, magnitudes are cut
+__device__ __forceinline__ float c4_cut(float x) { return x == x ? fminf(fmaxf(x, -64512.f), 64512.f) : 0.f; }
 
 template <bool F16>
 __device__ __forceinline__ float2 c4_unpack(uint32_t w) {
