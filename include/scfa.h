@@ -347,8 +347,9 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   |value| <= 64512, larger magnitudes saturate, and c s has at most seven
  *   significant bits: every value is exact in bf16 and in fp16.
  *   The scale is one byte b: s = (1 + (b & 7) / 8) 2^((b >> 3) - 15); a code
- *   is stored as c + 8 in four bits. Every byte pattern is a finite value, so
- *   what earlier requests left in a page can not spoil a sum it is masked from.
+ *   is stored as c + 8 in four bits. What a page held before (any bytes) can
+ *   not spoil a sum it is masked from; read as fp16 rows, bytes that no append
+ *   wrote may be infinite.
  * A page of one head is a run of tiles of 16 tokens; with G = D / 32 a tile is
  *   K codes  [16 tokens][4 j][G g] 32-bit words: channels 32 g + 8 j + i, the
  *            channel i = 0 2 4 6 1 3 5 7 in bits 0-3, 4-7, ..., 28-31;
@@ -367,12 +368,12 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   q_start [R + 1], the sums of new_len; for the tokens below q_start[R]
  *   slot = page * page_size + place in it (-1: dropped) and vis, for those
  *   up to N -1 and 0; len_out [R] and n_free_out [1], which may be len and
- *   n_free themselves. A request is released by pushing its pages on the stack and setting its
- *   len to 0. The status word reads SCFA_ERR_INVALID for a negative length,
+ *   n_free themselves. A request is released by pushing its pages on the
+ *   stack and setting its len to 0. The status word reads SCFA_ERR_INVALID for a negative length,
  *   sum(new_len) > N, more than max_pages pages in a request, or n_free
  *   outside [0, n_pages], SCFA_ERR_WORKSPACE when there are too few free
- *   pages: then nothing is taken, table, len and n_free stay, and q_start and vis are
- *   all 0 and slot all -1. A page id outside [0, n_pages) gives slots of
+ *   pages: then nothing is taken, table, len and n_free stay, and q_start and
+ *   vis are all 0 and slot all -1. A page id outside [0, n_pages) gives slots of
  *   -1 and SCFA_ERR_INVALID.
  * scfa_cache4_append: quantises the rows k, v [N][Hkv][D] into their slots.
  *   A slot outside [0, n_pages * page_size) is skipped. Slots must be
@@ -386,7 +387,10 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   within a request. q, o [N][Hq][D], lse [N][Hq] fp32; Hq a multiple of
  *   Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
  *   outside [0, n_pages) within a request's visible pages is skipped, its
- *   keys masked, and raises SCFA_ERR_INVALID in the status word.
+ *   keys masked, and raises SCFA_ERR_INVALID in the status word. A query row
+ *   that is not finite gives NaN in its own o and lse only; scale times a row's
+ *   largest |q| is below 2^96. The workspace (some 20 MB, one size for every N
+ *   and R) serves one call at a time, and holds nothing from call to call.
  *   flags: SCFA_FLAG_DEBUG_SYNC, SCFA_FLAG_DEBUG_STALL.
  * ------------------------------------------------------------------------- */
 enum { SCFA_DTYPE_BF16 = 0, SCFA_DTYPE_F16 = 1 };

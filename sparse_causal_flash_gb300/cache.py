@@ -21,14 +21,17 @@ class KVCache4:
     def __init__(self, R: int, n_pages: int, Hq: int, Hkv: int, D: int, max_len: int, max_tokens: int,
                  page_size: int = 64, dtype=torch.bfloat16, device="cuda"):
         """R request rows share n_pages pages of page_size tokens; a request
-        caches at most max_len tokens, a step brings at most max_tokens new
-        ones over all requests."""
+        caches at most max_len tokens (rounded up to whole pages), a step
+        brings at most max_tokens new ones over all requests."""
         nbytes = cache4_page_bytes(page_size, D)
         if nbytes == 0:
             raise ValueError(f"KVCache4: head dimension {D} or page size {page_size} is not supported")
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"KVCache4: rows are bf16 or fp16, not {dtype}")
-        if Hkv < 1 or Hq % Hkv != 0:
+        if min(R, n_pages, max_len, max_tokens) < 1:
+            raise ValueError(f"KVCache4: {R} requests, {n_pages} pages, {max_len} tokens a request and {max_tokens} a "
+                             "step must be positive")
+        if Hkv < 1 or Hq < Hkv or Hq % Hkv != 0:
             raise ValueError(f"KVCache4: {Hq} query heads are no multiple of {Hkv} key heads")
         dev = torch.device(device)
         self.device, self.dtype = dev, dtype
@@ -54,9 +57,11 @@ class KVCache4:
         """One serving step: new_len [R] int32 new tokens of each request, packed
         request by request in q [N, Hq, D], k, v [N, Hkv, D] (N at most
         max_tokens; the sum of new_len may be smaller), keep [N] uint8 or
-        None. Returns views of o [N, Hq, D] and lse [N, Hq], whose rows from
-        the sum of new_len on are left as they were. A step that does not fit
-        (status()) caches nothing and computes nothing."""
+        None. Returns views of o [N, Hq, D] and lse [N, Hq], which the next
+        step overwrites and whose rows from the sum of new_len on are left as
+        they were. A step that does not fit (status()) caches nothing and
+        computes nothing. Steps follow one another on one stream, or the
+        caller orders them."""
         N = q.shape[0]
         if N > self.max_tokens:
             raise ValueError(f"KVCache4.step: {N} token rows, room for {self.max_tokens}")
@@ -70,15 +75,17 @@ class KVCache4:
 
     def capture(self, q, k, v, new_len, scale, keep=None):
         """The step on these input tensors as a CUDA graph; each replay() is
-        one more step. They must stay alive and in place. Nothing is run: the
-        cache is as before."""
+        one more step. They and this object must stay alive and in place.
+        Nothing is run: the cache is as before."""
         g = torch.cuda.CUDAGraph()
         with torch.cuda.device(self.device), torch.cuda.graph(g):
             self.step(q, k, v, new_len, scale, keep)
         return g
 
     def rows(self, request: int):
-        """(k, v) [tokens, Hkv, D]: the values the cache holds of a request (reads its length back)."""
+        """(k, v) [tokens, Hkv, D]: the values the cache holds of a request.
+        Reads its length back; like release() and status() on the current
+        stream, which must be behind the steps."""
         n = int(self.len[request])
         shape = (max(n, 1), self.Hkv, self.D)
         k = torch.empty(shape, dtype=self.dtype, device=self.device)

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
   long long kept_all = 0;
   if (a.keep != nullptr) {
     // 16 tokens a thread and round, by one load where the mask allows it
-    const bool vec = (reinterpret_cast<uintptr_t>(a.keep) & 15u) == 0 && (reinterpret_cast<uintptr_t>(a.vis) & 15u) == 0;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.keep) | reinterpret_cast<uintptr_t>(a.vis)) & 15u) == 0;
     for (long long base = 0; base < a.N; base += 16ll * nt) {
       const long long t0 = base + 16ll * tid;
       uint32_t bits = 0;  // of the kept ones

@@ -46,9 +46,9 @@ template <int D, int NT>
 struct C4Queries {
   uint4 frag[NT][D / 32][32];
   float offset[NT][D / 32][8];  // -8 2^-24 sum(q) per group
-  float factor[8 * NT];     // score in log2 units = sum * factor
-  int seen[8 * NT];         // tokens that the row sees
-  int all_see[4];           // [0]: tokens that every row sees
+  float factor[8 * NT];         // score in log2 units = sum * factor
+  int seen[8 * NT];             // tokens that the row sees
+  int all_see[4];               // [0]: tokens that every row sees
 };
 
 template <int D, int NT>
@@ -98,7 +98,8 @@ __device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Req& q, 
     const bool in = row < q.rows;
     const uint16_t* p = a.q + (q.tok0 + tok) * a.qt + (h * a.G + row - tok * a.G) * a.qh + 8 * j;
 #pragma unroll
-    for (int g = 0; g < G; ++g) v[nt][g] = in ? *reinterpret_cast<const uint4*>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+    for (int g = 0; g < G; ++g)
+      v[nt][g] = in ? *reinterpret_cast<const uint4*>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
     seen[nt] = in ? a.vis[q.tok0 + tok] : INT_MAX;
   }
   int all = INT_MAX;
@@ -402,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
           for (int y = 0; y < 2; ++y) {
             const uint32_t lo = __byte_perm(vw[y][0][g / 2], vw[y][1][g / 2], (g & 1) ? 0x7632 : 0x5410);
             // the two keys' scales times 2: fp16 bits (b << 7) + (1 << 10), normal for every byte of a row
-            const uint32_t sc = __byte_perm(sb[y][g & 1][0], sb[y][g & 1][1], g < 2 ? 0x5410 : 0x7632) * k128 + 0x04000400u;
+            const uint32_t sc =
+                __byte_perm(sb[y][g & 1][0], sb[y][g & 1][1], g < 2 ? 0x5410 : 0x7632) * k128 + 0x04000400u;
             const uint4 v = c4_unpack8(lo, sc, magic);
             A[0][2 * y] = v.x, A[0][2 * y + 1] = v.y;
             A[1][2 * y] = v.z, A[1][2 * y + 1] = v.w;
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
           const bool tail = d.flags & kOpenStart, open = d.flags & kOpenEnd;
           if (!tail && !open) {
             const int tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-            const float inv = lt > 0.f ? 1.f / lt : 0.f;
+            const float inv = lt != 0.f ? 1.f / lt : 0.f;
             uint32_t z[CPT / 2];
 #pragma unroll
             for (int e = 0; e < CPT; e += 2) z[e / 2] = c4_pack<F16>(o[e] * inv, o[e + 1] * inv);
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             else *reinterpret_cast<uint2*>(op) = make_uint2(z[0], z[1]);
             if ((tid & 15) == 0)
               a.lse[static_cast<long long>(tok) * a.Hq + head] =
-                  lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                  lt != 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           } else {
             const long long at = (static_cast<long long>(blockIdx.x) * 2 + (tail ? 0 : 1)) * ROWS + row;
 #pragma unroll

@@ -441,13 +441,13 @@ __global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a,
       o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
       lt += s_l[w >> 1];
       const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      const float inv = lt != 0.f ? 1.f / lt : 0.f;
       if (sub == 0)
         *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
             make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
       if (lane == 0)
         a.lse[static_cast<long long>(tok) * a.Hq + head] =
-            lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+            lt != 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
     }
     __syncthreads();
   }

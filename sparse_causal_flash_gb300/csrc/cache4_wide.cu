@@ -1,10 +1,10 @@
 // Attention over the paged 4-bit cache for many query rows of a request (a
 // prompt chunk, a handful of drafted tokens): tcgen05 tiles.
 //
-// The warp-level matrix instructions of cache4_attn.cu give 256 multiply-adds
-// a cycle and SM, which is enough for 16 rows and bounds more. Here a unit of
-// 128 tokens is unpacked once into fp16 tiles in shared memory (c s is exact
-// in fp16) and S = Q K^T and O += P V run on tcgen05 with 128 rows:
+// The kernel of cache4_attn.cu holds O in registers: 16 rows are what fits, and
+// every further 16 would unpack the cached codes again. Here a unit of 128
+// tokens is unpacked once for up to 128 rows, into fp16 tiles in shared memory
+// (c s is exact in fp16), and S = Q K^T and O += P V run on tcgen05:
 //   warp 0       copies the pages of the next units into a ring of raw stages;
 //   warps 2-9    unpack the keys of a stage into one of two tiles (128-byte
 //                swizzle), and at an item's first unit put its queries, brought
@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         for (int once = edge; once; once = 0) {
           const int n = min(max(row_seen - (key0 + 32 * c), 0), 32);
           const uint32_t tt = static_cast<uint32_t>(d.tiles) >> ((key_lo + 32 * c) / 16);
-          const uint32_t bits = (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ((tt & 1 ? 0xFFFFu : 0u) | (tt & 2 ? 0xFFFF0000u : 0u));
+          const uint32_t bits =
+              (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ((tt & 1 ? 0xFFFFu : 0u) | (tt & 2 ? 0xFFFF0000u : 0u));
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (!(bits >> e & 1)) x[e] = 0xFF800000u;
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
           for (int y = 0; y < REP; ++y) lt = fmaf(sm.ml[y * RP + row][1], ex2_approx(sm.ml[y * RP + row][0] - mt), lt);
           weight = ex2_approx(m - mt);
         }
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = lt != 0.f ? 1.f / lt : 0.f;
         const int tok = d.tok0 + (in ? grow / a.G : 0), head = d.head * a.G + (in ? grow % a.G : 0);
         const long long at = (static_cast<long long>(blockIdx.x) * 2 + (tail ? 0 : 1)) * RP + row;
         uint16_t* const op = a.o + tok * a.ot + head * a.oh;
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         if (in && rep == 0) {
           if (!tail && !open) {
             a.lse[static_cast<long long>(tok) * a.Hq + head] =
-                lt > 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+                lt != 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           } else {
             a.ml[2 * at] = mt;
             a.ml[2 * at + 1] = lt;

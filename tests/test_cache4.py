@@ -137,8 +137,8 @@ def attn_args(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(q=None), 1), (dict(vis=None), 1), (dict(lse=None), 1), (dict(ws=None), 1), (dict(N=0), 1), (dict(R=0), 1),
     (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(Hq=2), 1), (dict(D=80), 2), (dict(scale=0.0), 1),
-    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=-1.0), 1), (dict(dt=3), 2), (dict(ps=8), 2), (dict(mp=0), 1), (dict(pages=0), 1),
-    (dict(mp=1 << 26), 2), (dict(qt=12), 1), (dict(oh=68), 1), (dict(o=ctypes.c_void_p(4098)), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=-1.0), 1), (dict(dt=3), 2), (dict(ps=8), 2),
+    (dict(mp=0), 1), (dict(pages=0), 1), (dict(mp=1 << 26), 2), (dict(qt=12), 1), (dict(oh=68), 1), (dict(o=ctypes.c_void_p(4098)), 1),
     (dict(ws=ctypes.c_void_p(4100)), 3), (dict(nb=128), 3)])
 def test_attn_refusals(scfa, kw, code):
     assert scfa._lib.scfa_cache4_attn(*attn_args(**kw)) == code
@@ -165,6 +165,7 @@ def test_binding_refuses_tensors_it_cannot_take(scfa):
         scfa.scfa_cache4_plan(slot, slot, None, slot, slot[:1], slot.view(4, 1), 64, 4, slot, slot[:1], slot, slot, slot,
                               cache.view(-1))
     from sparse_causal_flash_gb300.cache import KVCache4
-    for kw in (dict(D=96), dict(page_size=48), dict(dtype=torch.float32), dict(Hq=5)):
+    for kw in (dict(D=96), dict(page_size=48), dict(dtype=torch.float32), dict(Hq=5), dict(Hq=0), dict(R=0), dict(n_pages=0),
+               dict(max_len=0), dict(max_tokens=0)):
         with pytest.raises(ValueError):
             KVCache4(**{**dict(R=2, n_pages=4, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=2, device="cpu"), **kw})

@@ -487,3 +487,106 @@ def test_step_without_room_computes_nothing(scfa):
     assert not c.o.any() and not c.cache.any()
     c.step(q[:40], kv[:40, :2], kv[:40, 2:], i32([32, 8]), 0.125)
     assert c.status() == 0 and c.len.tolist() == [32, 8] and int(c.n_free) == 0
+
+
+@pytest.mark.parametrize("Hq", [8, 9, 16, 17, 32, 33, 64, 65, 128, 129, 200])
+def test_attn_query_heads_per_key_head(scfa, Hq):
+    """Single tokens on both sides of every change of the row block."""
+    check_attn(scfa, attn_problem(scfa, Hq, [1, 130, 700], [1] * 3, Hq, 1, 64, 32, BF))
+
+
+@pytest.mark.parametrize("R,per", [(161, 1), (400, 1), (737, 9), (900, 12)])
+def test_attn_more_requests_than_threads(scfa, R, per):
+    """The requests of a CTA's piece are found in several rounds; some bring nothing."""
+    news = [0 if r % 7 == 3 else per + (r % 3 if per > 1 else 0) for r in range(R)]
+    lens = [n + (r * 37) % 150 for r, n in enumerate(news)]
+    check_attn(scfa, attn_problem(scfa, R, lens, news, 2, 1, 64, 32, BF, extra=2))
+
+
+@pytest.mark.parametrize("news", [[1, 1], [1, 3], [9, 7], [90, 25]])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_attn_a_query_that_is_not_finite_spoils_its_row_only(scfa, news, bad):
+    p = attn_problem(scfa, 12, [1400, 90], news, 4, 2, 128, 32, BF)
+    p["q"][1, 2, 5] = bad
+    o, lse, _ = run_attn(scfa, p)
+    assert torch.isnan(lse[1, 2]) and torch.isnan(o[1, 2]).all()
+    qs, vis = p["q_start"].tolist(), p["vis"].tolist()
+    for r, (k, v) in enumerate(p["rows"]):
+        for t in range(qs[r], qs[r + 1]):
+            for h in (h for h in range(4) if (t, h) != (1, 2)):
+                check_rows(dbl(p["q"][t:t + 1, h:h + 1]), k[:, h // 2:h // 2 + 1], v[:, h // 2:h // 2 + 1], [vis[t]],
+                           p["scale"], o[t:t + 1, h:h + 1], lse[t:t + 1, h:h + 1], BF)
+
+
+@pytest.mark.parametrize("news", [[1, 3], [9, 7], [90, 25]])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("k_by,v_by,q_by", [(2.0 ** -14, 2.0 ** -13, 2.0 ** 10), (2.0 ** 12, 2.0 ** 13, 2.0 ** -13)])
+def test_attn_small_and_large_rows(scfa, news, dt, k_by, v_by, q_by):
+    """Scales at both ends of the format, queries that undo those of the keys."""
+    p = attn_problem(scfa, 14, [200, 90], news, 4, 2, 64, 32, dt)
+    ps, rows = p["ps"], []
+    for r, n in enumerate([200, 90]):
+        k, v = rand(50 + r, (n, 2, 64), dt).cuda() * k_by, rand(60 + r, (n, 2, 64), dt).cuda() * v_by
+        pos = torch.arange(n, device="cuda")
+        scfa.scfa_cache4_append(k, v, (p["table"][r, pos // ps] * ps + pos % ps).int(), p["cache"], ps)
+        rows.append((oc.values(dbl(k)), oc.values(dbl(v))))
+    check_attn(scfa, {**p, "rows": rows, "q": p["q"] * q_by})
+
+
+def test_two_streams_with_workspaces_of_their_own(scfa):
+    ps = [attn_problem(scfa, 20 + i, [900, 5000, 33], news, 8, 2, 64, 64, BF)
+          for i, news in enumerate([[1] * 3, [40, 9, 20]])]
+    ref = [run_attn(scfa, p)[:2] for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    for _ in range(20):
+        got = [run_attn(scfa, p, stream=s)[:2] + (s,) for p, s in zip(ps, streams)]
+        torch.cuda.synchronize()
+        for (o, lse), (a, b, _) in zip(ref, got):
+            assert torch.equal(o, a) and torch.equal(lse, b)
+
+
+@pytest.mark.parametrize("N,R", [(5, 2), (40, 3), (4097, 2), (20011, 3), (70000, 1200)])
+@pytest.mark.parametrize("ko,vo", [(0, 0), (3, 0), (0, 1)])
+def test_plan_masks_at_any_address(scfa, N, R, ko, vo):
+    """The keep mask is read 16 tokens at a time where it and vis are aligned, one by one elsewhere."""
+    g = np.random.default_rng(N + ko)
+    cut = np.sort(g.integers(0, N + 1, R - 1))
+    new = np.diff(np.concatenate([[0], cut, [N - N // 5]]).clip(max=N - N // 5))
+    length = g.integers(0, 50, R)
+    mp = int(-(-(length + new).max() // 16))
+    table, at = np.full((R, mp), -1), 0
+    for r in range(R):
+        n = -(-int(length[r]) // 16)
+        table[r, :n] = np.arange(at, at + n)
+        at += n
+    P = at + int((-(-(length + new) // 16)).sum())
+    keep = (g.random(N) < 0.5).astype(np.uint8)
+    ref = oc.plan(length, new, keep, list(range(at, P)), P - at, table, N, 16, P)
+    kp, vis = torch.zeros(N + 16, dtype=torch.uint8, device="cuda")[ko:ko + N], i32([-9] * (N + 4))[vo:vo + N]
+    kp.copy_(torch.as_tensor(keep))
+    ln, nf, tb, fr = i32(length), i32([P - at]), i32(table), i32(list(range(at, P)) + [-1] * at)
+    qs, slot = i32([-9] * (R + 1)), i32([-9] * N)
+    ws = scfa.workspace(scfa.cache4_plan_workspace_size(N, R))
+    scfa.scfa_cache4_plan(ln, i32(new), kp, fr, nf, tb, 16, P, ln, nf, qs, slot, vis, ws)
+    assert scfa.scfa_get_device_status(ws) == 0
+    for key, got in dict(table=tb, len=ln, n_free=nf, q_start=qs, slot=slot, vis=vis).items():
+        assert np.array_equal(got.cpu().numpy().reshape(np.shape(ref[key])), ref[key]), key
+
+
+def test_steps_on_another_stream(scfa):
+    from sparse_causal_flash_gb300.cache import KVCache4
+    R, Hq, Hkv, D = 2, 4, 2, 128
+    a, b, c = (KVCache4(R, 20, Hq, Hkv, D, max_len=96, max_tokens=100, page_size=32) for _ in "abc")
+    side = torch.cuda.Stream()
+    for i, new in enumerate([[50, 0], [1, 30], [1, 1]]):
+        q, kv, n = rand(i, (sum(new), Hq, D)).cuda(), rand(9 + i, (sum(new), 2 * Hkv, D)).cuda(), i32(new)
+        torch.cuda.synchronize()
+        o, lse = a.step(q, kv[:, :Hkv], kv[:, Hkv:], n, 0.1)
+        ob, lb = b.step(q, kv[:, :Hkv], kv[:, Hkv:], n, 0.1, stream=side)
+        with torch.cuda.stream(side):
+            oc_, lc = c.step(q, kv[:, :Hkv], kv[:, Hkv:], n, 0.1)
+        torch.cuda.synchronize()
+        for x, y in ((ob, lb), (oc_, lc)):
+            assert torch.equal(o, x) and torch.equal(lse, y)
+    assert a.status() == b.status() == c.status() == 0
