@@ -84,24 +84,34 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // The query rows from row0 on of key head h, by one warp: lane (r8, j) takes
-// channels 32 g + 8 j + 0..7 of row r8, the B operand's place of them.
-template <int D, bool F16, int NT>
-__device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Req& q, int row0, int h, int lane,
-                                           C4Queries<D, NT>& s) {
-  constexpr int G = D / 32;
-  const int r8 = lane >> 2, j = lane & 3;
-  uint4 v[NT][G];
+// channels 32 g + 8 j + 0..7 of row r8, the B operand's place of them. Their
+// loads come first, the pages' copies next, the work on them last.
+template <int D, int NT>
+struct C4Raw {
+  uint4 v[NT][D / 32];
   int seen[NT];
+};
+template <int D, int NT>
+__device__ __forceinline__ void c4_load_queries(const C4AttnArgs& a, const C4Req& q, int row0, int h, int lane,
+                                                C4Raw<D, NT>& x) {
+  const int r8 = lane >> 2, j = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int row = row0 + nt * 8 + r8, tok = row / a.G;
     const bool in = row < q.rows;
     const uint16_t* p = a.q + (q.tok0 + tok) * a.qt + (h * a.G + row - tok * a.G) * a.qh + 8 * j;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-      v[nt][g] = in ? *reinterpret_cast<const uint4*>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
-    seen[nt] = in ? a.vis[q.tok0 + tok] : INT_MAX;
+    for (int g = 0; g < D / 32; ++g)
+      x.v[nt][g] = in ? *reinterpret_cast<const uint4*>(p + 32 * g) : make_uint4(0u, 0u, 0u, 0u);
+    x.seen[nt] = in ? a.vis[q.tok0 + tok] : INT_MAX;
   }
+}
+template <int D, bool F16, int NT>
+__device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Raw<D, NT>& x, int lane, C4Queries<D, NT>& s) {
+  constexpr int G = D / 32;
+  const int r8 = lane >> 2, j = lane & 3;
+  auto& v = x.v;
+  auto& seen = x.seen;
   int all = INT_MAX;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -179,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
   grid_release();
   C4Span span;
   if (!c4_span<ROWS, kThreads>(a, s_span, span)) return;  // (the whole CTA)
+  __syncthreads();
   const int n_units = span.units;
 
   if (w == kWarps) {
@@ -190,13 +201,16 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
     for (int u = 0; u < n_units; ++u) {
       const int s = u % S;
       if (u >= S && !wait_all(&empty[s], ((u / S) & 1) ^ 1, &abort_flag, &desc->err)) break;
+      const bool first = walk.ch == 0 || u == 0;
+      C4Raw<D, NT> raw;
+      if (first) c4_load_queries<D, NT>(a, walk.q, walk.b * ROWS, walk.h, lane, raw);
       const uint32_t mask = pages.look_up(a, walk, lane, &desc->err);
       const bool go = !(a.stall && u == 0);
       if (go) pages.copy<D>(a, walk, lane, smem + static_cast<size_t>(s) * C::kStageBytes, &full[s]);
-      if (walk.ch == 0 || u == 0) {
+      if (first) {
         // at most S items have units in the ring, so the slot of the item S before is free
         if (++qslot == S) qslot = 0;
-        c4_queries<D, F16, NT>(a, walk.q, walk.b * ROWS, walk.h, lane, s_q[qslot]);
+        c4_queries<D, F16, NT>(a, raw, lane, s_q[qslot]);
       }
       __syncwarp();
       if (lane == 0) {

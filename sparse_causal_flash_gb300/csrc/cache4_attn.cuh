@@ -162,15 +162,73 @@ struct C4Span {
   long long per, u0;  // units per piece; first unit
   long long prefix;   // units before the request
   int units, req;
+  C4Req q;   // that request,
+  int seen;  // and, if it is of one block, the tokens it sees
 };
 template <int THREADS>
 struct C4SpanSmem {
   long long sum[THREADS / 32], prefix;
   int req;
 };
-// By the whole CTA; false: an empty piece.
+// Up to 32 requests: by each warp for itself, a lane per request. Nothing else
+// can start before this has, so it waits for memory once: the count that a
+// lane's request sees is fetched with the request's bounds, at the place where
+// it is if every request brings one token.
+template <int ROWS>
+__device__ __forceinline__ bool c4_span_warp(const C4AttnArgs& a, C4Span& span) {
+  const int lane = threadIdx.x & 31;
+  const bool in = lane < a.R;
+  const int guess = a.vis[min(lane, a.N - 1)];
+  C4Req q = {0, 0, 0};
+  if (in) q = c4_request<ROWS>(a, lane);
+  long long mine = 0;
+  int seen = 0;
+  if (q.blocks == 1) {
+    const int tok = q.tok0 + (q.rows <= a.G ? 0 : (q.rows - 1) / a.G);
+    const long long cap = static_cast<long long>(a.max_pages) << a.log_ps;
+    seen = static_cast<int>(min(cap, static_cast<long long>(max(0, tok == lane ? guess : a.vis[tok]))));
+    mine = c4_chunks(seen);
+  }
+  uint32_t big = __ballot_sync(0xffffffffu, q.blocks > 1);
+  while (big) {  // requests of several blocks: the warp together
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    C4Req p;
+    p.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
+    p.rows = __shfl_sync(0xffffffffu, q.rows, src);
+    p.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
+    long long x = 0;
+    for (int b = lane; b < p.blocks; b += 32) x += c4_chunks(c4_seen<ROWS>(a, p, b));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == src) mine = x;
+  }
+  mine *= a.Hkv;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const long long total = __shfl_sync(0xffffffffu, upto, 31);
+  span.per = c4_div(total + gridDim.x - 1, gridDim.x);
+  span.u0 = span.per * blockIdx.x;
+  const long long u1 = min(total, span.u0 + span.per);
+  if (span.u0 >= u1) return false;
+  span.units = static_cast<int>(u1 - span.u0);
+  const int src = __ffs(__ballot_sync(0xffffffffu, span.u0 < upto)) - 1;
+  span.req = src;
+  span.prefix = __shfl_sync(0xffffffffu, upto - mine, src);
+  span.q.tok0 = __shfl_sync(0xffffffffu, q.tok0, src);
+  span.q.rows = __shfl_sync(0xffffffffu, q.rows, src);
+  span.q.blocks = __shfl_sync(0xffffffffu, q.blocks, src);
+  span.seen = __shfl_sync(0xffffffffu, seen, src);
+  return true;
+}
+// By the whole CTA (the caller's barrier comes behind); false: an empty piece.
 template <int ROWS, int THREADS>
 __device__ __forceinline__ bool c4_span(const C4AttnArgs& a, C4SpanSmem<THREADS>& sm, C4Span& span) {
+  if (a.R <= 32) return c4_span_warp<ROWS>(a, span);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   auto request_units = [&](int r) {
     C4Req q = {0, 0, 0};
@@ -243,6 +301,8 @@ __device__ __forceinline__ bool c4_span(const C4AttnArgs& a, C4SpanSmem<THREADS>
   __syncthreads();
   span.req = sm.req;
   span.prefix = sm.prefix;
+  span.q = c4_request<ROWS>(a, span.req);
+  span.seen = span.q.blocks == 1 ? c4_seen<ROWS>(a, span.q, 0) : 0;
   return true;
 }
 
@@ -254,9 +314,9 @@ struct C4Walk {
   __device__ __forceinline__ void begin(const C4AttnArgs& a, const C4Span& span, int lane) {
     r = span.req;
     b = 0;
-    q = c4_request<ROWS>(a, r);
+    q = span.q;
     long long rem = span.u0 - span.prefix;
-    for (;; b += 32) {  // the block: 32 at a time
+    for (; q.blocks > 1; b += 32) {  // the block: 32 at a time
       const int mb = b + lane;
       const int c = mb < q.blocks ? c4_chunks(c4_seen<ROWS>(a, q, mb)) : 0;
       const long long own = static_cast<long long>(c) * a.Hkv;
@@ -276,7 +336,7 @@ struct C4Walk {
       rem -= __shfl_sync(0xffffffffu, x, 31);
       if (b + 32 >= q.blocks) break;  // (does not happen: the piece begins in this request)
     }
-    seen = c4_seen<ROWS>(a, q, b);
+    seen = q.blocks > 1 ? c4_seen<ROWS>(a, q, b) : span.seen;
     chunks = c4_chunks(seen);
     h = static_cast<int>(c4_div(rem, chunks));
     ch = static_cast<int>(rem - static_cast<long long>(h) * chunks);
