@@ -424,20 +424,28 @@ cudaError_t launch_cache4_wide(int D, bool f16, int rp, int grid, const C4AttnAr
 
 namespace {
 // Joins the partial rows of the items that were cut, in the order of their
-// chunks, and gathers the CTAs' errors. One CTA per piece, the one in which an
-// item begins, and two warps per row, each for half the parts: lanes first
-// weigh the parts, then each takes four channels of every part, eight parts
-// at a time.
+// chunks, and gathers the CTAs' errors. A CTA per eight or 16 rows of a piece,
+// the one in which an item begins. Lanes first weigh the parts, then each takes
+// four channels of every part, kFly parts at a time. Few rows (long items, up to
+// hundreds of parts): two warps per row, each for half the parts. Blocks of 32
+// rows and more have few parts each and there are many of them: one warp per
+// row and fewer registers, so that more CTAs are resident.
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
+template <int ROWS>
+struct C4Join {
+  static constexpr int kWarpsPerRow = ROWS <= 16 ? 2 : 1, kFly = ROWS <= 16 ? 8 : 4, kCtas = ROWS <= 16 ? 2 : 3;
+  static constexpr int kRows = kJoinWarps / kWarpsPerRow;  // per CTA
+};
 template <int D, bool F16, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a, int n_desc) {
-  __shared__ float4 s_o[kJoinWarps / 2][32];
-  __shared__ float s_l[kJoinWarps / 2];
+__global__ void __launch_bounds__(kJoinThreads, C4Join<ROWS>::kCtas) cache4_join_kernel(C4AttnArgs a, int n_desc) {
+  using J = C4Join<ROWS>;
+  __shared__ float4 s_o[J::kRows][32];
+  __shared__ float s_l[J::kRows];
   __shared__ int s_err[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   grid_wait();
   const C4Desc d = a.desc[blockIdx.x];
-  if (blockIdx.x == 0) {
+  if (blockIdx.x + blockIdx.y == 0) {
     int err = 0;
     for (int i = tid; i < n_desc; i += kJoinThreads) err = max(err, a.desc[i].err);
     err = __reduce_max_sync(0xffffffffu, err);
@@ -448,71 +456,76 @@ __global__ void __launch_bounds__(kJoinThreads) cache4_join_kernel(C4AttnArgs a,
       *a.status = err;
     }
   }
-  if (d.parts <= 0) return;
+  if (d.parts <= 0 || d.row0 + static_cast<int>(blockIdx.y) * J::kRows >= d.rows) return;
   constexpr int LPP = D / 4;     // lanes per part
   constexpr int PPW = 32 / LPP;  // parts side by side in a warp
   const int n = d.parts + 1, sub = lane / LPP, ch0 = lane % LPP * 4;
-  const int half = w & 1, mid = (n + 1) / 2, i0 = half ? mid : 0, i1 = half ? n : mid;
-  for (int row0 = 0; row0 < ROWS && d.row0 + row0 < d.rows; row0 += kJoinWarps / 2) {
-    const int row = row0 + (w >> 1);
-    const bool in = row < ROWS && d.row0 + row < d.rows;
-    auto at = [&](int i) { return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-    float mt = kNoMax, lt = 0.f;
-    float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-      for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
+  const int half = J::kWarpsPerRow == 2 ? w & 1 : 0, mid = J::kWarpsPerRow == 2 ? (n + 1) / 2 : n;
+  const int i0 = half ? mid : 0, i1 = half ? n : mid, slot = w / J::kWarpsPerRow;
+  const int row = blockIdx.y * J::kRows + slot;
+  const bool in = d.row0 + row < d.rows;
+  // index of part i of the row: [cta][2][ROWS], below 2^31
+  auto at = [&](int i) { return ((blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+  float mt = kNoMax, lt = 0.f;
+  float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f), v[J::kFly / PPW];
+  const float* const part = a.part + ch0;
+  auto load = [&](int i) {  // parts i to i + kFly - 1
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-      for (int base = i0; base < i1; base += 32) {
-        float f = 0.f;  // weight of part base + lane
-        if (base + lane < i1) {
-          const float2 v = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
-          f = ex2_approx(v.x - mt);
-          lt = fmaf(v.y, f, lt);
-        }
-        const int cnt = min(32, i1 - base);
-        for (int i = 0; i < cnt; i += 8) {
-          float4 v[8 / PPW];
+    for (int y = 0; y < J::kFly / PPW; ++y)
+      v[y] = *reinterpret_cast<const float4*>(part + at(min(i + y * PPW + sub, i1 - 1)) * D);
+  };
+  if (in) {
+    load(i0);  // (under the wait for the maxima)
+    for (int i = lane; i < n; i += 32) mt = fmaxf(mt, a.ml[2 * at(i)]);
 #pragma unroll
-          for (int y = 0; y < 8 / PPW; ++y)
-            v[y] = *reinterpret_cast<const float4*>(a.part + at(min(base + i + y * PPW + sub, i1 - 1)) * D + ch0);
-#pragma unroll
-          for (int y = 0; y < 8 / PPW; ++y) {
-            const float fi = __shfl_sync(0xffffffffu, f, i + y * PPW + sub);  // 0 behind the last part
-            o4.x = fmaf(v[y].x, fi, o4.x), o4.y = fmaf(v[y].y, fi, o4.y);
-            o4.z = fmaf(v[y].z, fi, o4.z), o4.w = fmaf(v[y].w, fi, o4.w);
-          }
-        }
+    for (int o = 16; o; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    for (int base = i0; base < i1; base += 32) {
+      float f = 0.f;  // weight of part base + lane
+      if (base + lane < i1) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.ml + 2 * at(base + lane));
+        f = ex2_approx(ml.x - mt);
+        lt = fmaf(ml.y, f, lt);
       }
+      const int cnt = min(32, i1 - base);
+      for (int i = 0; i < cnt; i += J::kFly) {
+        if (base + i != i0) load(base + i);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-      if (PPW == 2) {
-        o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
-        o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
+        for (int y = 0; y < J::kFly / PPW; ++y) {
+          const float fi = __shfl_sync(0xffffffffu, f, i + y * PPW + sub);  // 0 behind the last part
+          o4.x = fmaf(v[y].x, fi, o4.x), o4.y = fmaf(v[y].y, fi, o4.y);
+          o4.z = fmaf(v[y].z, fi, o4.z), o4.w = fmaf(v[y].w, fi, o4.w);
+        }
       }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    if (PPW == 2) {
+      o4.x += __shfl_xor_sync(0xffffffffu, o4.x, 16), o4.y += __shfl_xor_sync(0xffffffffu, o4.y, 16);
+      o4.z += __shfl_xor_sync(0xffffffffu, o4.z, 16), o4.w += __shfl_xor_sync(0xffffffffu, o4.w, 16);
+    }
+  }
+  if (J::kWarpsPerRow == 2) {
     if (half) {
-      s_o[w >> 1][lane] = o4;
-      if (lane == 0) s_l[w >> 1] = lt;
+      s_o[slot][lane] = o4;
+      if (lane == 0) s_l[slot] = lt;
     }
     __syncthreads();
-    if (!half && in) {
-      const float4 v = s_o[w >> 1][lane];
-      o4.x += v.x, o4.y += v.y, o4.z += v.z, o4.w += v.w;
-      lt += s_l[w >> 1];
-      const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
-      const float inv = lt != 0.f ? 1.f / lt : 0.f;
-      if (sub == 0)
-        *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
-            make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
-      if (lane == 0)
-        a.lse[static_cast<long long>(tok) * a.Hq + head] =
-            lt != 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-    }
-    __syncthreads();
+    if (half) return;
+    const float4 z = s_o[slot][lane];
+    o4.x += z.x, o4.y += z.y, o4.z += z.z, o4.w += z.w;
+    lt += s_l[slot];
+  }
+  if (in) {
+    const int grow = d.row0 + row, tok = d.tok0 + grow / a.G, head = d.head * a.G + grow % a.G;
+    const float inv = lt != 0.f ? 1.f / lt : 0.f;
+    if (sub == 0)
+      *reinterpret_cast<uint2*>(a.o + tok * a.ot + head * a.oh + ch0) =
+          make_uint2(c4_pack<F16>(o4.x * inv, o4.y * inv), c4_pack<F16>(o4.z * inv, o4.w * inv));
+    if (lane == 0)
+      a.lse[static_cast<long long>(tok) * a.Hq + head] =
+          lt != 0.f ? (mt + log2f(lt)) * 0.69314718055994531f : -INFINITY;
   }
 }
-
 
 // The main kernel (its dynamic shared memory allowed once per device) and
 // behind it the join, whose launch hides under the main kernel's end.
@@ -530,7 +543,7 @@ cudaError_t launch_and_join(Kernel kern, int grid, int threads, size_t smem, con
   kern<<<grid, threads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(grid, (ROWS + C4Join<ROWS>::kRows - 1) / C4Join<ROWS>::kRows);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
