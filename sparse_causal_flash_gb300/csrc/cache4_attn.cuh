@@ -97,31 +97,29 @@ __device__ __forceinline__ uint4 c4_unpack8(uint32_t x, uint32_t sc2, uint32_t m
                     mul_f16x2(add_f16x2(and_or(y, 0x00F000F0u, magic), hi), sc_hi));
 }
 
-// Bounded wait that polls every `ns` nanoseconds (0: at once) and looks at the
-// abort flag and the clock once in 16 polls. Twenty warps that poll without a
-// pause take most of an SM's issue slots from the few that work.
-__device__ __forceinline__ bool c4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                        uint32_t ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
+// The rare part of a wait, out of line: the roles of a CTA share the schedulers'
+// instruction caches.
+static __device__ __noinline__ bool c4_gave_up(uint32_t t0, volatile int* abort_flag, int* status) {
+  if (*abort_flag) return true;
+  if (static_cast<uint32_t>(global_timer_ns()) - t0 <= static_cast<uint32_t>(kWaitLimitNs)) return false;
+  raise_status(status, SCFA_ERR_TIMEOUT);
+  *abort_flag = 1;
+  return true;
+}
+// Bounded wait: looks at the abort flag and the clock once in 16 polls.
+__device__ __forceinline__ bool c4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (!mbar_try_wait(bar, parity)) {
+    const uint32_t t0 = static_cast<uint32_t>(global_timer_ns());
+    uint32_t polls = 0;
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i) {
-      if (ns != 0) __nanosleep(ns);
-      if (mbar_try_wait(bar, parity)) return true;
-    }
-    if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      raise_status(status, SCFA_ERR_TIMEOUT);
-      *abort_flag = 1;
-      return false;
-    }
+    while (!mbar_try_wait(bar, parity))
+      if ((++polls & 15u) == 0 && c4_gave_up(t0, abort_flag, status)) return false;
   }
+  return true;
 }
 // of a whole warp: its lanes go on, or give up, together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
-                                         uint32_t ns = 0) {
-  return __all_sync(0xffffffffu, c4_wait(bar, parity, abort_flag, status, ns));
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xffffffffu, c4_wait(bar, parity, abort_flag, status));
 }
 
 // Let the kernel launched behind this one start its CTAs as these leave; it

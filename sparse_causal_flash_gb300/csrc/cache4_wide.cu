@@ -58,6 +58,7 @@ struct WideSmem {
   int abort_flag;
 };
 
+
 // true in one lane of the warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -156,12 +157,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
     // places are constants of the unit's and the item's parity (the whole of
     // TMEM is this CTA's, so its columns begin at 0), and the warps stay
     // together but for the elected lane, so that descriptors are uniform.
+    // The loops are not unrolled: the roles of a scheduler share its
+    // instruction cache, and fetching code is what most of their waits were.
     int items = 0;
     auto scores = [&](auto unit, auto item) {
       constexpr int I = decltype(unit)::value, Q = decltype(item)::value;
       if (elect_one()) {
         const uint64_t b = kdesc + I * kBuf16;
-#pragma unroll
+#pragma unroll 1
         for (int kk = 0; kk < D / 16; ++kk)
           mma_bf16_ts(kColS + I * 128, kColQ + Q * kColQ2 + kk * 8, b + kstep_off16(kk, kSub), idesc_s, kk > 0);
         tc_commit(&sm.s_full[I]);
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
       constexpr int I = decltype(unit)::value;
       if (elect_one()) {
         const uint64_t b = vdesc + I * kBuf16;
-#pragma unroll
+#pragma unroll 1
         for (int kk = 0; kk < 8; ++kk)
           mma_bf16_ts(kColO, kColS + I * 128 + kk * 8, b + static_cast<uint64_t>(kk * 128), idesc_o,
                       kk > 0 ? 1u : accumulate);
@@ -383,21 +386,25 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
       const bool edge = (static_cast<uint32_t>(d.tiles) & key_tiles) != key_tiles ||
                         __any_sync(0xffffffffu, key0 + KEYS > row_seen);
       uint32_t x[32];
-      auto load = [&](int c) {  // 32 scores, those out of sight at -inf
+      auto load = [&](int c) {
         tmem_ld32(sc + key_lo + 32 * c, x);
         tmem_wait_ld();
         tmem_ld_fence(x);
-#pragma unroll 1
-        for (int once = edge; once; once = 0) {
-          const int n = min(max(row_seen - (key0 + 32 * c), 0), 32);
-          const uint32_t tt = static_cast<uint32_t>(d.tiles) >> ((key_lo + 32 * c) / 16);
-          const uint32_t bits =
-              (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ((tt & 1 ? 0xFFFFu : 0u) | (tt & 2 ? 0xFFFF0000u : 0u));
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(bits >> e & 1)) x[e] = 0xFF800000u;
-        }
       };
+      // scores out of sight to -inf, in TMEM: the loops below stay short
+#pragma unroll 1
+      for (int c = edge ? 0 : KEYS / 32; c < KEYS / 32; ++c) {
+        load(c);
+        const int n = min(max(row_seen - (key0 + 32 * c), 0), 32);
+        const uint32_t tt = static_cast<uint32_t>(d.tiles) >> ((key_lo + 32 * c) / 16);
+        const uint32_t bits =
+            (n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u) & ((tt & 1 ? 0xFFFFu : 0u) | (tt & 2 ? 0xFFFF0000u : 0u));
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!(bits >> e & 1)) x[e] = 0xFF800000u;
+        tmem_st32(sc + key_lo + 32 * c, x);
+        tmem_wait_st();
+      }
       float mx = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < KEYS / 32; ++c) {
