@@ -106,20 +106,17 @@ static __device__ __noinline__ bool c4_gave_up(uint32_t t0, volatile int* abort_
   *abort_flag = 1;
   return true;
 }
-// Bounded wait: looks at the abort flag and the clock once in 16 polls.
-__device__ __forceinline__ bool c4_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (!mbar_try_wait(bar, parity)) {
+// Bounded wait of a whole warp, whose lanes go on, or give up, together: looks at
+// the abort flag and the clock once in 16 polls.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
     const uint32_t t0 = static_cast<uint32_t>(global_timer_ns());
     uint32_t polls = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-      if ((++polls & 15u) == 0 && c4_gave_up(t0, abort_flag, status)) return false;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+      if ((++polls & 15u) == 0 && __any_sync(0xffffffffu, c4_gave_up(t0, abort_flag, status))) return false;
   }
   return true;
-}
-// of a whole warp: its lanes go on, or give up, together
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xffffffffu, c4_wait(bar, parity, abort_flag, status));
 }
 
 // Let the kernel launched behind this one start its CTAs as these leave; it

@@ -405,13 +405,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         tmem_st32(sc + key_lo + 32 * c, x);
         tmem_wait_st();
       }
-      float mx = -INFINITY;
+      float mx = -INFINITY, mx2 = -INFINITY, l2 = 0.f;
 #pragma unroll 1
       for (int c = 0; c < KEYS / 32; ++c) {
         load(c);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) mx = max3f(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        for (int e = 0; e < 32; e += 4) {
+          mx = max3f(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          mx2 = max3f(mx2, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        }
       }
+      mx = fmaxf(mx, mx2);
       // the reference moves only when a weight would exceed 2^15
       if (__any_sync(0xffffffffu, fmaf(mx, f, -m) > 15.f)) {
         const float mn = fmaxf(m, fmaf(mx, f, -7.f)), fix = ex2_approx(m - mn);
@@ -442,12 +446,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         for (int e = 0; e < 32; e += 2) {
           const float p0 = ex2_approx(fmaf(__uint_as_float(x[e]), f, -m));
           const float p1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), f, -m));
-          l += p0 + p1;
+          l += p0;
+          l2 += p1;
           p[e / 2] = c4_pack<true>(p0, p1);
         }
         // P of keys 32 c.. lies over scores that have been read
         tmem_st16(sc + (key_lo + 32 * c) / 2, p);
       }
+      l += l2;
       if (REP > 1) {  // the other copies' tokens weigh nothing here
         uint32_t z[16];
 #pragma unroll
