@@ -16,11 +16,15 @@
 // O^T = V^T P^T with 16 keys or channels by 8 query rows by 16, so up to 8
 // rows cost what one does, and the page layout is the operand layout: no
 // shuffle between the copy and the MMA. The matrix instructions are the
-// warp-level ones: a decode step does 8 * rows flops per cached byte, far
-// below what any of them bounds.
-//   Both operands are fp16, whatever the rows' type. Unpacking is bit work at
-//   half the rate of the FMA pipe, so it is what bounds the kernel: per eight
-//   codes one shift and four AND(-OR)s, the rest is left to the FMA pipe.
+// warp-level ones: they are 20% busy here.
+//   Both operands are fp16, whatever the rows' type. Unpacking bounds the
+//   kernel: per eight codes one shift and four AND(-OR)s on the ALU, the rest,
+//   for V an addition and a multiplication a pair, on the FMA pipe, both at half
+//   rate. In the steady state the ALU is 62-65% busy, issue slots 60-70%.
+//   One request of 131,072 tokens, 8 key heads of 128 channels, 4 query heads
+//   each (143 MB): 37 us, 3.9 TB/s, 57% of the copy rate, some 5 us of it before
+//   the first unit's data; the join 7 us more. 61 ragged requests, 12 heads of 64
+//   channels (408 MB): 123 us, 3.3 TB/s. 8 requests of up to 512: 6 + 4 us.
 //   K: the bits of c + 8 are read as a subnormal, (c + 8) 2^-24 (2^-20 for
 //      the upper half of a byte, whose query channels are divided by 16); the
 //      offset comes off as -8 sum(q), with the group's scale, in fp32. A query
@@ -512,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 // Query rows of an item, from the average request's: up to 16 with the
 // warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05. Requests of
 // several tokens are ragged and may have twice the average, so they leave the
-// warp-level kernel at 8 (drafts of 1 to 7 tokens, groups of 4, 128 channels:
-// 176 us with blocks of 32, 197 us with blocks of 16).
+// warp-level kernel at 8 (32 requests with drafts of 1 to 7 tokens, groups of 4,
+// 128 channels: 154 us with blocks of 32, 204 us with blocks of 16).
 int c4_rows(int N, int R, int G) {
   const long long tokens = (static_cast<long long>(N) + R - 1) / R, rows = tokens * G;
   return rows <= 8 ? 8 : rows <= 16 && tokens == 1 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;

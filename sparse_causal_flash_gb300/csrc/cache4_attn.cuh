@@ -424,7 +424,9 @@ namespace {
 // four channels of every part, kFly parts at a time. Few rows (long items, up to
 // hundreds of parts): two warps per row, each for half the parts. Blocks of 32
 // rows and more have few parts each and there are many of them: one warp per
-// row and fewer registers, so that more CTAs are resident.
+// row and fewer registers, so that more CTAs are resident. Latency bound: the
+// descriptor, then maxima and parts. 57 parts of 8 rows for each of 8 heads
+// 7 us, two or three parts of 128 rows for each of 152 pieces 9 us.
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 template <int ROWS>
 struct C4Join {
