@@ -484,10 +484,10 @@ scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const u
                       reinterpret_cast<int32_t*>(p + w.free_before), reinterpret_cast<PlanReq*>(p + w.req)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int fill = N <= kPlanOneCta;
-  const int items = fill ? N : keep ? (N + 15) / 16 : 1, most = items > R ? items : R;  // of the longest loop
+  const int items = fill ? N : keep ? N / 16 + 1 : 1, most = items > R ? items : R;  // of the longest loop
   const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
   plan_kernel<<<1, threads, 0, st>>>(a, fill);
-  if (!fill) plan_fill_kernel<<<(N + 255) / 256, 256, 0, st>>>(a);
+  if (!fill) plan_fill_kernel<<<N / 256 + 1, 256, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
 }
 

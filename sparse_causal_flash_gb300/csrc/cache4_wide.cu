@@ -21,8 +21,8 @@
 // copies, which keep their own maximum and sum, meet once per item.
 // At 128 channels a unit takes an SM some 2,300 cycles with 32 rows and 3,100
 // with 128; the tensor cores are 45% and 30% busy, the issue slots 68% and 59%.
-// The MMAs alone, with nothing else running, take 1,300 cycles (80 each where
-// the tensor core is busy for 34). With 32 rows the unpacking warps work for
+// The MMAs alone, with nothing else running, take 1,300 cycles (80 each, 64 at
+// the peak rate). With 32 rows the unpacking warps work for
 // 1,800 of a unit's cycles, with 128 the softmax warps for 2,500; eight of those
 // instead of four take as long each (141 us instead of 142 in all), and so do
 // loads of 16 scores under the work on the 16 before (144). Code size counts: see
