@@ -1,4 +1,8 @@
 """Parity of the paged 4-bit cache on the GPU against the float64 oracle."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +12,7 @@ from oracle import cache4 as oc
 pytestmark = pytest.mark.gpu
 
 BF, HF = torch.bfloat16, torch.float16
+ROOT = pathlib.Path(__file__).resolve().parents[1]
 
 
 @pytest.fixture(scope="module")
@@ -590,3 +595,41 @@ def test_steps_on_another_stream(scfa):
         for x, y in ((ob, lb), (oc_, lc)):
             assert torch.equal(o, x) and torch.equal(lse, y)
     assert a.status() == b.status() == c.status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attn_past_32_bit_offsets(scfa, new):
+    """The same rows in the first and in the last pages of a cache of more than 2^32 bytes: the same bits."""
+    H, D, ps, L = 8, 128, 256, 700
+    P = 2 ** 32 // (H * ps * (D + D // 16)) + 8
+    cache = torch.empty((P, H, ps * (D + D // 16)), dtype=torch.uint8, device="cuda")
+    k, v, q = rand(1, (L, H, D)).cuda(), rand(2, (L, H, D)).cuda(), rand(3, (new, 16, D)).cuda()
+    t, got = torch.arange(L, device="cuda"), []
+    for pages in ([0, 1, 2], [P - 1, P - 3, P - 2]):
+        table = i32([pages])
+        scfa.scfa_cache4_append(k, v, (table[0, t // ps] * ps + t % ps).int(), cache, ps)
+        p = dict(q=q, cache=cache, ps=ps, table=table, q_start=i32([0, new]), vis=i32(range(L - new + 1, L + 1)),
+                 scale=D ** -0.5, dt=BF)
+        got.append(run_attn(scfa, p)[:2])
+        cache[pages].fill_(0)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert torch.isfinite(got[0][1]).all()
+
+
+def test_a_first_call_may_be_captured(scfa):
+    """In a process that has run no kernel of the library yet."""
+    code = """if 1:
+        import torch
+        from sparse_causal_flash_gb300.cache import KVCache4
+        for new in (1, 40):
+            q, kv = torch.randn(2 * new, 4, 64).cuda().bfloat16(), torch.randn(2 * new, 4, 64).cuda().bfloat16()
+            n = torch.full((2,), new, dtype=torch.int32, device="cuda")
+            a, b = (KVCache4(2, 20, 4, 2, 64, max_len=128, max_tokens=80, page_size=16) for _ in "ab")
+            g = a.capture(q, kv[:, :2], kv[:, 2:], n, 0.125)
+            g.replay()
+            o, lse = b.step(q, kv[:, :2], kv[:, 2:], n, 0.125)
+            torch.cuda.synchronize()
+            assert a.status() == 0 and torch.equal(a.o[:2 * new], o) and torch.equal(a.lse[:2 * new], lse) and o.any()
+    """
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
