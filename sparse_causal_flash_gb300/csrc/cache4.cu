@@ -25,6 +25,7 @@ struct PlanArgs {
   int* status;
   int32_t* free_before;  // n_free as it was (n_free_out may be n_free)
   PlanReq* req;
+  uint2* kept;  // per 32 tokens: the kept ones before them, and which of them are kept
 };
 
 // exclusive sum over the block; *total gets the sum. `part`: 33 entries.
@@ -54,8 +55,14 @@ __device__ __forceinline__ long long block_excl(long long x, long long* part, lo
   return before + s - x;
 }
 
-// Slot, vis and a fresh table entry of token t. vis[t] holds the number of
-// kept tokens before t when there is a keep mask.
+// kept tokens before token t; *keep: it is kept
+__device__ __forceinline__ int kept_before(const PlanArgs& a, long long t, bool* keep) {
+  const uint2 c = a.kept[t >> 5];
+  *keep = c.y >> (t & 31) & 1u;
+  return static_cast<int>(c.x) + __popc(c.y & ((1u << (t & 31)) - 1u));
+}
+
+// Slot, vis and a fresh table entry of token t.
 __device__ __forceinline__ void plan_token(const PlanArgs& a, int t) {
   const int total = a.q_start[a.R];
   if (t >= total) {
@@ -70,8 +77,8 @@ __device__ __forceinline__ void plan_token(const PlanArgs& a, int t) {
     else hi = mid;
   }
   const PlanReq q = a.req[lo];
-  const bool keep = a.keep == nullptr || a.keep[t] != 0;
-  const int upto = a.keep == nullptr ? t : a.vis[t];
+  bool keep = true;
+  const int upto = a.keep == nullptr ? t : kept_before(a, t, &keep);
   const int pos = q.len + upto - q.first;
   int slot = -1;
   if (keep) {
@@ -94,55 +101,45 @@ __device__ __forceinline__ void plan_token(const PlanArgs& a, int t) {
 // One CTA: kept-token prefix, sums over the requests, the checks, the new
 // state; with fill also the tokens (few of them). Latency bound: the requests
 // and tokens of a decode step fit one CTA's threads once. 48 requests of one
-// token: 3.9 us; 97 prompts, 24,000 tokens and a mask: 9.4 us, and 4.4 us for
-// plan_fill_kernel (a CTA's prefix over the mask is most of it; a second
-// launch costs more than splitting it would save).
+// token: 3.9 us; 97 prompts, 24,000 tokens and a mask: 5.5 us, and 4.2 us for
+// plan_fill_kernel, whose launch hides under it. The prefix leaves 8 bytes per 32
+// tokens: an SM that writes every token's count takes 3 us more.
 __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
   __shared__ long long part[33];
   __shared__ int s_bad;
   const int tid = threadIdx.x, nt = blockDim.x;
   if (tid == 0) s_bad = 0;
+  grid_release();
+  // (on their way while the mask is counted)
+  const int n_free = *a.n_free, len0 = tid < a.R ? a.len[tid] : 0, new0 = tid < a.R ? a.new_len[tid] : 0;
   long long kept_all = 0;
   if (a.keep != nullptr) {
-    // 16 tokens a thread and round, by one load where the mask allows it
-    const bool vec = ((reinterpret_cast<uintptr_t>(a.keep) | reinterpret_cast<uintptr_t>(a.vis)) & 15u) == 0;
-    for (long long base = 0; base < a.N; base += 16ll * nt) {
-      const long long t0 = base + 16ll * tid;
+    // 32 tokens a thread and round, by two loads where the mask allows it
+    const bool vec = (reinterpret_cast<uintptr_t>(a.keep) & 15u) == 0;
+    for (long long base = 0; base < a.N; base += 32ll * nt) {
+      const long long t0 = base + 32ll * tid;
       uint32_t bits = 0;  // of the kept ones
-      const bool whole = vec && t0 + 16 <= a.N;
-      if (whole) {
-        const uint4 v = *reinterpret_cast<const uint4*>(a.keep + t0);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      if (vec && t0 + 32 <= a.N) {
+        const uint4* const src = reinterpret_cast<const uint4*>(a.keep + t0);
+        const uint4 v = src[0], z = src[1];
+        const uint32_t x[8] = {v.x, v.y, v.z, v.w, z.x, z.y, z.z, z.w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) bits |= ((x[i / 4] >> (8 * (i % 4)) & 255u) != 0u ? 1u : 0u) << i;
+        for (int i = 0; i < 32; ++i) bits |= ((x[i / 4] >> (8 * (i % 4)) & 255u) != 0u ? 1u : 0u) << i;
       } else {
-        for (int i = 0; i < 16 && t0 + i < a.N; ++i) bits |= (a.keep[t0 + i] != 0 ? 1u : 0u) << i;
+        for (int i = 0; i < 32 && t0 + i < a.N; ++i) bits |= (a.keep[t0 + i] != 0 ? 1u : 0u) << i;
       }
       long long sum;
-      const int before = static_cast<int>(kept_all + block_excl(__popc(bits), part, &sum));
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          int4 v;
-          v.x = before + __popc(bits & ((1u << i) - 1u));
-          v.y = before + __popc(bits & ((2u << i) - 1u));
-          v.z = before + __popc(bits & ((4u << i) - 1u));
-          v.w = before + __popc(bits & ((8u << i) - 1u));
-          *reinterpret_cast<int4*>(a.vis + t0 + i) = v;
-        }
-      } else {
-        for (int i = 0; i < 16 && t0 + i < a.N; ++i) a.vis[t0 + i] = before + __popc(bits & ((1u << i) - 1u));
-      }
+      const long long before = kept_all + block_excl(__popc(bits), part, &sum);
+      if (t0 < a.N) a.kept[t0 >> 5] = make_uint2(static_cast<uint32_t>(before), bits);
       kept_all += sum;
     }
   }
   __syncthreads();
-  const int n_free = *a.n_free;
   long long tokens = 0, taken = 0;
   for (int base = 0; base < a.R; base += nt) {
     const int r = base + tid;
     const bool in = r < a.R;
-    const int len = in ? a.len[r] : 0, n = in ? a.new_len[r] : 0;
+    const int len = base == 0 ? len0 : in ? a.len[r] : 0, n = base == 0 ? new0 : in ? a.new_len[r] : 0;
     bool bad = len < 0 || n < 0;
     long long sum;
     const long long start = tokens + block_excl(bad ? 0 : n, part, &sum);
@@ -150,8 +147,9 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
     const long long end = start + (bad ? 0 : n);
     long long first = start, last = end;
     if (a.keep != nullptr) {
-      first = start < a.N ? a.vis[start] : kept_all;
-      last = end < a.N ? a.vis[end] : kept_all;
+      bool unused;
+      first = start < a.N ? kept_before(a, start, &unused) : kept_all;
+      last = end < a.N ? kept_before(a, end, &unused) : kept_all;
     }
     const long long kept = last - first;
     const long long have = (static_cast<long long>(len) + a.page_size - 1) / a.page_size;
@@ -186,6 +184,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int fill) {
 }
 
 __global__ void __launch_bounds__(256) plan_fill_kernel(PlanArgs a) {
+  grid_wait();
   const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (t < a.N) plan_token(a, static_cast<int>(t));
 }
@@ -406,11 +405,12 @@ __global__ void __launch_bounds__(256) read_kernel(RowArgs a) {
 constexpr int kPlanOneCta = 4096;  // tokens one CTA fills itself
 
 struct PlanWs {
-  size_t free_before = sizeof(WsHeader), req = sizeof(WsHeader) + 256, total = 0;
+  size_t free_before = sizeof(WsHeader), req = sizeof(WsHeader) + 256, kept = 0, total = 0;
 };
 bool plan_ws_layout(int N, int R, PlanWs* w) {
   if (N < 1 || R < 1) return false;
-  w->total = align_up(w->req + sizeof(PlanReq) * static_cast<size_t>(R), 256);
+  w->kept = align_up(w->req + sizeof(PlanReq) * static_cast<size_t>(R), 256);
+  w->total = align_up(w->kept + sizeof(uint2) * (static_cast<size_t>(N) / 32 + 1), 256);
   return true;
 }
 
@@ -481,14 +481,16 @@ scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const u
   char* p = static_cast<char*>(ws);
   const PlanArgs a = {len, new_len, keep, free_pages, n_free, table, N, R, max_pages, page_size, n_pages,
                       len_out, n_free_out, q_start, slot, vis, reinterpret_cast<int*>(p),
-                      reinterpret_cast<int32_t*>(p + w.free_before), reinterpret_cast<PlanReq*>(p + w.req)};
+                      reinterpret_cast<int32_t*>(p + w.free_before), reinterpret_cast<PlanReq*>(p + w.req),
+                      reinterpret_cast<uint2*>(p + w.kept)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int fill = N <= kPlanOneCta;
-  const int items = fill ? N : keep ? N / 16 + 1 : 1, most = items > R ? items : R;  // of the longest loop
+  const int items = fill ? N : keep ? N / 32 + 1 : 1, most = items > R ? items : R;  // of the longest loop
   const int threads = most >= 1024 ? 1024 : (most + 31) / 32 * 32;
   plan_kernel<<<1, threads, 0, st>>>(a, fill);
-  if (!fill) plan_fill_kernel<<<N / 256 + 1, 256, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && !fill) e = launch_behind(plan_fill_kernel, dim3(N / 256 + 1), 256, st, a);
+  return e == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
 }
 
 scfa_status scfa_cache4_append(const uint16_t* k, long long k_token, long long k_head, const uint16_t* v,

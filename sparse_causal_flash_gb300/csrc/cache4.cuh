@@ -86,4 +86,24 @@ __device__ __forceinline__ uint32_t c4_pack(float lo, float hi) {
 
 inline bool c4_page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
+// Let the kernel launched behind this one start its CTAs as these leave; it
+// waits with grid_wait() before it reads what this one writes.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch behind a kernel that calls grid_release(); the launched one calls grid_wait().
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kern)(Params...), dim3 grid, int threads, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace scfa

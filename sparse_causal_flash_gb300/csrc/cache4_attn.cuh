@@ -119,11 +119,6 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
   return true;
 }
 
-// Let the kernel launched behind this one start its CTAs as these leave; it
-// waits with grid_wait() before it reads what this one writes.
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // a / b, in 32 bits where they hold it
 __device__ __forceinline__ long long c4_div(long long a, int b) {
   return a >> 32 ? a / b : static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -539,16 +534,8 @@ cudaError_t launch_and_join(Kernel kern, int grid, int threads, size_t smem, con
   }
   kern<<<grid, threads, smem, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (ROWS + C4Join<ROWS>::kRows - 1) / C4Join<ROWS>::kRows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache4_join_kernel<D, F16, ROWS>, a, grid);
+  return launch_behind(cache4_join_kernel<D, F16, ROWS>,
+                       dim3(grid, (ROWS + C4Join<ROWS>::kRows - 1) / C4Join<ROWS>::kRows), kJoinThreads, st, a, grid);
 }
 
 }  // namespace
