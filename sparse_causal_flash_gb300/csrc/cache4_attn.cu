@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 // warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05. Requests of
 // several tokens are ragged and may have twice the average, so they leave the
 // warp-level kernel at 8 (32 requests with drafts of 1 to 7 tokens, groups of 4,
-// 128 channels: 154 us with blocks of 32, 204 us with blocks of 16).
+// 128 channels: 148 us with blocks of 32, 204 us with blocks of 16).
 int c4_rows(int N, int R, int G) {
   const long long tokens = (static_cast<long long>(N) + R - 1) / R, rows = tokens * G;
   return rows <= 8 ? 8 : rows <= 16 && tokens == 1 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
