@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (cache4_attn_workspace_size, cache4_page_bytes, cache4_plan_workspace_size, scfa_cache4_append,
+from . import (_rows4, cache4_attn_workspace_size, cache4_page_bytes, cache4_plan_workspace_size, scfa_cache4_append,
                scfa_cache4_attn, scfa_cache4_plan, scfa_cache4_read, scfa_get_device_status, workspace)
 
 
@@ -65,6 +65,14 @@ class KVCache4:
         N = q.shape[0]
         if N > self.max_tokens:
             raise ValueError(f"KVCache4.step: {N} token rows, room for {self.max_tokens}")
+        # all of it before the plan runs: a step that raises must leave the cache as it was
+        for key, t, H in (("q", q, self.Hq), ("k", k, self.Hkv), ("v", v, self.Hkv)):
+            st, sh = _rows4("KVCache4.step", key, t, N, H, self.D, self.dtype, self.len.get_device())
+            if (st | sh) & 7 or t.data_ptr() & 15:
+                raise ValueError(f"KVCache4.step: {key} needs strides that are multiples of 8 and a 16-byte aligned "
+                                 f"start, got {t.stride()} at {t.data_ptr():#x}")
+        if not 0.0 < scale < float("inf"):
+            raise ValueError(f"KVCache4.step: scale {scale} is not positive and finite")
         slot, vis, o, lse = self.slot[:N], self.vis[:N], self.o[:N], self.lse[:N]
         scfa_cache4_plan(self.len, new_len, keep, self.free, self.n_free, self.table, self.page_size, self.n_pages,
                          self.len, self.n_free, self.q_start, slot, vis, self.ws_plan, stream)

@@ -633,3 +633,19 @@ def test_a_first_call_may_be_captured(scfa):
     """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_a_refused_step_leaves_the_cache_as_it_was(scfa):
+    from sparse_causal_flash_gb300.cache import KVCache4
+    c = KVCache4(2, 8, 4, 2, 64, max_len=64, max_tokens=16, page_size=16)
+    q, kv, new = rand(1, (9, 4, 64)).cuda(), rand(2, (9, 4, 64)).cuda(), i32([5, 4])
+    k, v = kv[:, :2], kv[:, 2:]
+    odd = torch.zeros(9 * 4 * 64 + 8, dtype=BF, device="cuda")
+    for bad in (dict(k=k.float()), dict(v=v[:8]), dict(v=kv), dict(q=q.cpu()), dict(q=q[:, :, :32]), dict(scale=0.0),
+                dict(scale=float("nan")), dict(q=odd[4:4 + q.numel()].view(q.shape)), dict(new_len=new.long()),
+                dict(k=odd[:9 * 132].as_strided((9, 2, 64), (132, 64, 1))), dict(keep=torch.ones(9, device="cuda") > 0)):
+        with pytest.raises(ValueError):
+            c.step(**{**dict(q=q, k=k, v=v, new_len=new, scale=0.125), **bad})
+    assert c.len.tolist() == [0, 0] and int(c.n_free) == 8 and not c.cache.any()
+    c.step(q, k, v, new, 0.125)
+    assert c.status() == 0 and c.len.tolist() == [5, 4]
