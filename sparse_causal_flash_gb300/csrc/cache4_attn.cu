@@ -152,7 +152,11 @@ __device__ __forceinline__ void c4_queries(const C4AttnArgs& a, const C4Raw<D, N
       if (j == 0) s.offset[nt][g][r8] = sum * (-8.f * 0x1p-24f);
     }
     if (j == 0) {
-      s.factor[nt * 8 + r8] = fmaxf(a.factor * 0x1p24f * __uint_as_float((254u - ex) << 23), 0x1p-126f);
+      // times 2^(24 + 127 - ex), in two steps so that no product between leaves fp32
+      const int e = 24 + 127 - static_cast<int>(ex), e1 = e >> 1;
+      const float half = __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+      const float rest = __uint_as_float(static_cast<uint32_t>(127 + e - e1) << 23);
+      s.factor[nt * 8 + r8] = fmaxf(a.factor * half * rest, 0x1p-126f);
       s.seen[nt * 8 + r8] = seen[nt];
     }
     all = min(all, seen[nt]);

@@ -538,6 +538,16 @@ def test_attn_small_and_large_rows(scfa, news, dt, k_by, v_by, q_by):
     check_attn(scfa, {**p, "rows": rows, "q": p["q"] * q_by})
 
 
+@pytest.mark.parametrize("news", [[1, 1], [9, 7], [90, 25]])
+@pytest.mark.parametrize("by", [2.0 ** -108, 2.0 ** 100])
+def test_attn_scale_undoes_the_queries(scfa, news, by):
+    """A power of two moved from the queries to the scale changes no bit."""
+    p = attn_problem(scfa, 16, [700, 90], news, 4, 2, 128, 32, BF)
+    o, lse, _ = run_attn(scfa, p)
+    o2, lse2, _ = run_attn(scfa, {**p, "q": p["q"] * by, "scale": p["scale"] / by})
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_two_streams_with_workspaces_of_their_own(scfa):
     ps = [attn_problem(scfa, 20 + i, [900, 5000, 33], news, 8, 2, 64, 64, BF)
           for i, news in enumerate([[1] * 3, [40, 9, 20]])]
@@ -642,7 +652,8 @@ def test_a_refused_step_leaves_the_cache_as_it_was(scfa):
     k, v = kv[:, :2], kv[:, 2:]
     odd = torch.zeros(9 * 4 * 64 + 8, dtype=BF, device="cuda")
     for bad in (dict(k=k.float()), dict(v=v[:8]), dict(v=kv), dict(q=q.cpu()), dict(q=q[:, :, :32]), dict(scale=0.0),
-                dict(scale=float("nan")), dict(q=odd[4:4 + q.numel()].view(q.shape)), dict(new_len=new.long()),
+                dict(scale=float("nan")), dict(scale=1e-50), dict(scale=1e39),
+                dict(q=odd[4:4 + q.numel()].view(q.shape)), dict(new_len=new.long()),
                 dict(k=odd[:9 * 132].as_strided((9, 2, 64), (132, 64, 1))), dict(keep=torch.ones(9, device="cuda") > 0)):
         with pytest.raises(ValueError):
             c.step(**{**dict(q=q, k=k, v=v, new_len=new, scale=0.125), **bad})
