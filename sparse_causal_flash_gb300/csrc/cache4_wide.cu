@@ -245,6 +245,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
           // places: the scores of the item before last are done, they came two
           // units ago. What the softmax reads has four: it is past the unit four
           // before this one, whose P had to be used up for the scores two before.
+          // (those MMAs read the place that is written here: the wait for their commit orders it with this fence)
+          tc_fence_after();
           const int ib = items++ & 3, half = dw >> 2;
           const int row = d.row0 + (quad * 32) % RP + lane;
           const bool in = row < d.rows;

@@ -660,3 +660,21 @@ def test_a_refused_step_leaves_the_cache_as_it_was(scfa):
     assert c.len.tolist() == [0, 0] and int(c.n_free) == 8 and not c.cache.any()
     c.step(q, k, v, new, 0.125)
     assert c.status() == 0 and c.len.tolist() == [5, 4]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [3, 12, 25])
+def test_attn_many_short_items_keep_their_queries(scfa, D, new):
+    """Blocks of 32, 64 and 128 rows, a dozen items of one unit in every CTA: each takes the place of the queries of the
+    item before last, whose scores have to be done."""
+    R = 1000
+    p = attn_problem(scfa, 31, [new + r % 60 for r in range(R)], [new] * R, 8, 2, D, 32, BF)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    for _ in range(10):
+        o2, lse2, _ = run_attn(scfa, p)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    vis = p["vis"].cpu().numpy()
+    for r in range(0, R, 37):
+        a, b = r * new, r * new + new
+        check_rows(dbl(p["q"][a:b]), *p["rows"][r], vis[a:b], p["scale"], o[a:b], lse[a:b], BF)
