@@ -388,8 +388,8 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
  *   outside [0, n_pages) within a request's visible pages is skipped, its
  *   keys masked, and raises SCFA_ERR_INVALID in the status word. A query row
- *   that is not finite gives NaN in its own o and lse only; scale times a row's
- *   largest |q| is below 2^96. The workspace (some 20 MB, one size for every N
+ *   that is not finite and sees a key gives NaN in its own o and lse only;
+ *   scale times a row's largest |q| is below 2^96. The workspace (some 20 MB, one size for every N
  *   and R) serves one call at a time, and holds nothing from call to call.
  *   flags: SCFA_FLAG_DEBUG_SYNC, SCFA_FLAG_DEBUG_STALL.
  * ------------------------------------------------------------------------- */

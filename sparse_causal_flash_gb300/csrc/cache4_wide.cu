@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
             }
           }
           const uint32_t ex = min(253u, 267u - (__float_as_uint(mx) >> 23));
-          const float up = __uint_as_float(ex << 23);
+          // an infinity spoils its row whatever the signs of the codes it meets: all of the row becomes NaN (a NaN does so
+          // by itself)
+          const float up = __uint_as_float(mx < INFINITY ? ex << 23 : 0x7FC00000u);
           uint32_t reg[D / 4];
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {

@@ -678,3 +678,29 @@ def test_attn_many_short_items_keep_their_queries(scfa, D, new):
     for r in range(0, R, 37):
         a, b = r * new, r * new + new
         check_rows(dbl(p["q"][a:b]), *p["rows"][r], vis[a:b], p["scale"], o[a:b], lse[a:b], BF)
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 64), (BF, 128), (HF, 64), (HF, 128)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("new,Hq", [(1, 2), (1, 12), (4, 2), (10, 2), (20, 2), (70, 2)])
+def test_attn_an_infinite_query_over_keys_of_one_sign(scfa, dt, D, bad, new, Hq):
+    """Blocks of 8 to 128 rows, each row with a query channel that is not finite and up to three keys whose codes in it have
+    one sign: NaN in o and lse, and finite rows beside it."""
+    for sign in (1.0, -1.0):
+        p = attn_problem(scfa, 17, [0] * 4, [new] * 4, Hq, 1, D, 16, dt)
+        p["vis"].copy_(i32([min(3, t + r) for r in range(4) for t in range(new)]))
+        P = p["cache"].shape[0]
+        p["table"][:, 0] = i32(np.arange(4) % P)
+        k, v = rand(3, (P * 16, 1, D), dt).cuda(), rand(4, (P * 16, 1, D), dt).cuda()
+        k[..., 7] = sign * (1 + k[..., 7].abs())
+        scfa.scfa_cache4_append(k, v, torch.arange(P * 16, dtype=torch.int32, device="cuda"), p["cache"], 16)
+        p["q"][::2, 0, 7] = bad
+        o, lse, ws = run_attn(scfa, p)
+        assert scfa.scfa_get_device_status(ws) == 0
+        spoilt = torch.zeros_like(lse, dtype=torch.bool)
+        spoilt[::2, 0] = True
+        none = (p["vis"] == 0)[:, None].expand_as(lse)  # a row that sees no key has nothing to spoil
+        assert torch.equal(torch.isnan(lse), spoilt & ~none)
+        assert torch.equal(torch.isnan(o), (spoilt & ~none)[..., None].expand_as(o))
+        assert torch.all(lse[none] == -torch.inf) and not o[none].any()
+        assert torch.isfinite(lse[~none & ~spoilt]).all() and torch.isfinite(o).all(-1)[~none & ~spoilt].all()
