@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         for (int i = 0; i < kTpw; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // in log2 units over the reference (computed again if it moves)
-            over |= fmaf(x[i][nt][e], factor[nt][e & 1], -m[nt][e & 1]) > 15.f;
+            x[i][nt][e] = __fmul_rn(x[i][nt][e], factor[nt][e & 1]);  // in log2 units
+            over |= __fsub_rn(x[i][nt][e], m[nt][e & 1]) > 15.f;
           }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
             for (int i = 0; i < kTpw; ++i) mx = fmaxf(mx, fmaxf(x[i][nt][c], x[i][nt][c + 2]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            mx = fmaxf(m[nt][c], fmaf(mx, factor[nt][c], -7.f));
+            mx = fmaxf(m[nt][c], mx - 7.f);
             const float f = ex2_approx(m[nt][c] - mx);
             m[nt][c] = mx;
             l[nt][c] *= f;
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
         for (int i = 0; i < kTpw; ++i) {
           float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(fmaf(x[i][nt][e], factor[nt][e & 1], -m[nt][e & 1]));
+          for (int e = 0; e < 4; ++e) p[e] = ex2_approx(__fsub_rn(x[i][nt][e], m[nt][e & 1]));
           l[nt][0] += p[0] + p[2];
           l[nt][1] += p[1] + p[3];
           P[i][nt][0] = transpose8(c4_pack<true>(p[0], p[1]));

@@ -20,7 +20,10 @@ namespace scfa {
 
 constexpr int kCh = 128;  // tokens per unit
 constexpr int kChTiles = kCh / kC4Tile;
-constexpr float kNoMax = -1e30f;  // running maximum before any key (finite: differences stay defined)
+// Running maximum before any key: below every score there can be (2^120 in log2 units), and finite, so that differences
+// stay defined. Scores are rounded to fp32 before the maximum comes off (a multiplication and an addition, no fma):
+// past 2^24, where a step of fp32 is more than a softmax is wide, the largest then still has a weight near one.
+constexpr float kNoMax = -3e38f;
 
 // What a CTA reports, and the item that begins in its piece and goes on behind
 // it. One per CTA, written by every call.

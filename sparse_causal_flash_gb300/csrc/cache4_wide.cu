@@ -427,8 +427,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
       }
       mx = fmaxf(mx, mx2);
       // the reference moves only when a weight would exceed 2^15
-      if (__any_sync(0xffffffffu, fmaf(mx, f, -m) > 15.f)) {
-        const float mn = fmaxf(m, fmaf(mx, f, -7.f)), fix = ex2_approx(m - mn);
+      mx = __fmul_rn(mx, f);
+      if (__any_sync(0xffffffffu, __fsub_rn(mx, m) > 15.f)) {
+        const float mn = fmaxf(m, mx - 7.f), fix = ex2_approx(m - mn);
         m = mn;
         l *= fix;
         if (!first) {
@@ -454,8 +455,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(x[e]), f, -m));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(x[e + 1]), f, -m));
+          // (a packed multiplication and addition gave infinities for far scores, as one rounding for both would)
+          const float p0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), f), m));
+          const float p1 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(x[e + 1]), f), m));
           l += p0;
           l2 += p1;
           p[e / 2] = c4_pack<true>(p0, p1);

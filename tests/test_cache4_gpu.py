@@ -704,3 +704,55 @@ def test_attn_an_infinite_query_over_keys_of_one_sign(scfa, dt, D, bad, new, Hq)
         assert torch.equal(torch.isnan(o), (spoilt & ~none)[..., None].expand_as(o))
         assert torch.all(lse[none] == -torch.inf) and not o[none].any()
         assert torch.isfinite(lse[~none & ~spoilt]).all() and torch.isfinite(o).all(-1)[~none & ~spoilt].all()
+
+
+def _far_problem(scfa, news, dt, D, by, far_keys):
+    """Scores of about +-by: one key of each request is nearest to the queries, the others a quarter of its score or more away."""
+    p = attn_problem(scfa, 19, [0] * len(news), news, 4, 2, D, 16, dt)
+    n = 40
+    p["table"] = i32(np.arange(3 * len(news)).reshape(len(news), 3))
+    cache = noise_cache(5, 3 * len(news), 2, D, 16)
+    g = np.random.default_rng(int(sum(news)))
+    u = rand(6, (1, 2, D), torch.float32).cuda()
+    w = torch.tensor(g.uniform(0.3, 0.74, (len(news), 48)), device="cuda", dtype=torch.float32)
+    best = g.integers(0, n, len(news))
+    for r, b in enumerate(best):
+        w[r, b] = 1.0
+    if far_keys:  # all scores are far below zero, the nearest key's the least so
+        w = -1.3 + w
+    rows = []
+    for r in range(len(news)):
+        k = (w[r, :, None, None] * u).to(dt)
+        v = rand(40 + r, (48, 2, D), dt).cuda()
+        scfa.scfa_cache4_append(k, v, i32(np.arange(48) + 48 * r), cache, 16)
+        rows.append((oc.values(dbl(k))[:n], oc.values(dbl(v))[:n]))
+    p["q"] = (u.repeat_interleave(2, 1) * 0.37).to(dt).expand(sum(news), -1, -1).contiguous()
+    p["vis"].fill_(n)
+    top = float(np.abs(rows[0][0][best[0], 0] @ dbl(p["q"])[0, 0]))
+    return {**p, "cache": cache, "rows": rows, "scale": by / top}, best
+
+
+@pytest.mark.parametrize("news", [[1, 1], [3, 2], [9, 7], [20, 16], [90, 25]])
+@pytest.mark.parametrize("dt,D", [(BF, 64), (HF, 128)])
+@pytest.mark.parametrize("by", [2.0 ** 22, 2.0 ** 30, 2.0 ** 60, 2.0 ** 95])
+@pytest.mark.parametrize("far_keys", [False, True])
+def test_attn_scores_that_fp32_can_hardly_tell_apart(scfa, news, dt, D, by, far_keys):
+    """Scores past 2^24 in either direction: steps of fp32 there are whole softmax widths, but the nearest key, whose score
+    is a fifth apart, has all the weight: lse is its score, within the error of a score that check_rows derives, and o its
+    value, but for the rounding of one weight to fp16 (2^-11), exp2 and the sums (2^-18) and that of o."""
+    p, best = _far_problem(scfa, news, dt, D, by, far_keys)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    at, uo = 0, 2.0 ** -8 if dt is BF else 2.0 ** -11
+    for r, new in enumerate(news):
+        k, v = (np.repeat(x, 2, 1) for x in p["rows"][r])
+        q = dbl(p["q"][at:at + new])
+        s = np.einsum("thd,lhd->thl", q, k) * p["scale"]
+        order = np.sort(s, -1)
+        assert np.all(s.argmax(-1) == best[r]) and np.all(order[..., -1] - order[..., -2] > 0.15 * np.abs(order[..., -1]))
+        sg, qg = np.abs(k).reshape(len(k), 4, -1, 32).max(-1) / 6, np.abs(q).reshape(new, 4, -1, 32).sum(-1)
+        e = (D / 8 + 4) * 2.0 ** -23 * 15 * p["scale"] * np.einsum("thg,lhg->thl", qg, sg).max(-1) + 2.0 ** -20 * np.abs(s).max(-1)
+        assert np.all(np.abs(dbl(lse[at:at + new]) - s.max(-1)) <= e + 2.0 ** -18 * np.abs(s.max(-1)))
+        want = v[best[r]]
+        assert np.all(np.abs(dbl(o[at:at + new]) - want) <= (uo + 2.0 ** -11 + 2.0 ** -18) * np.abs(want))
+        at += new
