@@ -389,7 +389,8 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   outside [0, n_pages) within a request's visible pages is skipped, its
  *   keys masked, and raises SCFA_ERR_INVALID in the status word. A query row
  *   that is not finite and sees a key gives NaN in its own o and lse only;
- *   scale times a row's largest |q| is below 2^96. The workspace (some 20 MB, one size for every N
+ *   scale times a row's largest |q| is below 2^96, and scale * log2(e) an fp32
+ *   number (SCFA_ERR_INVALID). The workspace (some 20 MB, one size for every N
  *   and R) serves one call at a time, and holds nothing from call to call.
  *   flags: SCFA_FLAG_DEBUG_SYNC, SCFA_FLAG_DEBUG_STALL.
  * ------------------------------------------------------------------------- */

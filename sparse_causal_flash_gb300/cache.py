@@ -14,7 +14,8 @@ import torch
 from . import (_rows4, cache4_attn_workspace_size, cache4_page_bytes, cache4_plan_workspace_size, scfa_cache4_append,
                scfa_cache4_attn, scfa_cache4_plan, scfa_cache4_read, scfa_get_device_status, workspace)
 
-_F32 = torch.finfo(torch.float32)
+# a scale is a normal fp32 number whose product with log2(e) is one too
+_SCALES = torch.finfo(torch.float32).tiny, float.fromhex("0x1.62e42ep+127")
 
 
 class KVCache4:
@@ -73,8 +74,8 @@ class KVCache4:
             if (st | sh) & 7 or t.data_ptr() & 15:
                 raise ValueError(f"KVCache4.step: {key} needs strides that are multiples of 8 and a 16-byte aligned "
                                  f"start, got {t.stride()} at {t.data_ptr():#x}")
-        if not _F32.tiny <= scale <= _F32.max:
-            raise ValueError(f"KVCache4.step: scale {scale} is not a positive fp32 number")
+        if not _SCALES[0] <= scale <= _SCALES[1]:
+            raise ValueError(f"KVCache4.step: scale {scale} is not a positive fp32 number of at most {_SCALES[1]:.7g}")
         slot, vis, o, lse = self.slot[:N], self.vis[:N], self.o[:N], self.lse[:N]
         scfa_cache4_plan(self.len, new_len, keep, self.free, self.n_free, self.table, self.page_size, self.n_pages,
                          self.len, self.n_free, self.q_start, slot, vis, self.ws_plan, stream)

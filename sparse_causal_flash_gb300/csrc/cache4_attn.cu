@@ -577,7 +577,8 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
                              void* ws, size_t ws_bytes, unsigned flags, void* stream) {
   if (!q || !cache || !table || !q_start || !vis || !o || !lse || !ws) return SCFA_ERR_INVALID;
   if (N < 1 || R < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || n_pages < 1 || max_pages < 1) return SCFA_ERR_INVALID;
-  if (!(scale > 0.f && scale < INFINITY)) return SCFA_ERR_INVALID;
+  const float factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // to log2 units
+  if (!(scale > 0.f && factor < INFINITY)) return SCFA_ERR_INVALID;
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
@@ -599,7 +600,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   while ((1 << a.log_ps) < page_size) ++a.log_ps;
   a.table = table, a.max_pages = max_pages, a.q_start = q_start, a.vis = vis;
   a.N = N, a.R = R, a.Hq = Hq, a.Hkv = Hkv, a.G = G;
-  a.factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.factor = factor;
   a.o = o, a.ot = o_token, a.oh = o_head, a.lse = lse;
   a.status = reinterpret_cast<int*>(p);
   a.desc = reinterpret_cast<C4Desc*>(p + w.desc);

@@ -169,3 +169,22 @@ def test_binding_refuses_tensors_it_cannot_take(scfa):
                dict(max_len=0), dict(max_tokens=0)):
         with pytest.raises(ValueError):
             KVCache4(**{**dict(R=2, n_pages=4, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=2, device="cpu"), **kw})
+
+
+@pytest.mark.parametrize("scale", [2.36e38, 3e38])
+def test_a_scale_past_fp32_in_log2_units_is_refused(scfa, scale):
+    assert scfa._lib.scfa_cache4_attn(*attn_args(scale=scale)) == 1
+    from sparse_causal_flash_gb300.cache import KVCache4
+    c = KVCache4(R=2, n_pages=4, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=2, device="cpu")
+    q, kv = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros((2, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="scale"):
+        c.step(q, kv, kv, torch.ones(2, dtype=torch.int32), scale)
+
+
+def test_the_largest_scale_of_a_step_is_one_that_attn_takes():
+    from sparse_causal_flash_gb300.cache import _SCALES
+    log2e = 1.4426950408889634
+    most, above = np.float32(_SCALES[1]), np.nextafter(np.float32(_SCALES[1]), np.float32(np.inf))
+    assert float(most) == _SCALES[1] and np.isfinite(np.float32(float(most) * log2e))
+    with np.errstate(over="ignore"):
+        assert np.isinf(np.float32(float(above) * log2e))
