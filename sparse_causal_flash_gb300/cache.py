@@ -55,6 +55,8 @@ class KVCache4:
         self.lse = torch.zeros((max_tokens, Hq), dtype=torch.float32, device=dev)
         self.ws_plan = workspace(cache4_plan_workspace_size(max_tokens, R), dev)
         self.ws_attn = workspace(cache4_attn_workspace_size(max_tokens, R, Hq, Hkv, D), dev)
+        for ws in (self.ws_plan, self.ws_attn):
+            ws[:4].zero_()  # the status word: no step has run yet
 
     def step(self, q, k, v, new_len, scale, keep=None, stream=None):
         """One serving step: new_len [R] int32 new tokens of each request, packed
@@ -115,6 +117,7 @@ class KVCache4:
         self.len[request] = 0
 
     def status(self) -> int:
-        """Status of the last step: 0, or the first error of its plan, then of its attention (synchronises)."""
+        """Status of the last step that was launched (0 before the first): 0, or the first error of its plan, then of
+        its attention (synchronises). Each step, a replayed one too, replaces the status of the one before."""
         with torch.cuda.device(self.device):
             return scfa_get_device_status(self.ws_plan) or scfa_get_device_status(self.ws_attn)

@@ -188,3 +188,12 @@ def test_the_largest_scale_of_a_step_is_one_that_attn_takes():
     assert float(most) == _SCALES[1] and np.isfinite(np.float32(float(most) * log2e))
     with np.errstate(over="ignore"):
         assert np.isinf(np.float32(float(above) * log2e))
+
+
+def test_status_words_of_a_new_cache_are_zero(scfa, monkeypatch):
+    """Whatever the memory held before."""
+    from sparse_causal_flash_gb300 import cache
+    monkeypatch.setattr(cache, "workspace", lambda n, dev: torch.full((max(n, 256),), 7, dtype=torch.uint8, device=dev))
+    c = cache.KVCache4(R=2, n_pages=4, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=2, device="cpu")
+    for ws in (c.ws_plan, c.ws_attn):
+        assert int(ws[:4].view(torch.int32)[0]) == 0

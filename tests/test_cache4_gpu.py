@@ -756,3 +756,24 @@ def test_attn_scores_that_fp32_can_hardly_tell_apart(scfa, news, dt, D, by, far_
         want = v[best[r]]
         assert np.all(np.abs(dbl(o[at:at + new]) - want) <= (uo + 2.0 ** -11 + 2.0 ** -18) * np.abs(want))
         at += new
+
+
+def test_status_before_the_first_step(scfa):
+    """Of a new cache, of one whose step is only captured, and of one whose first step was refused: 0, in memory that held something else."""
+    from sparse_causal_flash_gb300.cache import KVCache4
+    size = dict(R=2, n_pages=8, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=16, page_size=16)
+    q, kv, new = rand(1, (9, 4, 64)).cuda(), rand(2, (9, 4, 64)).cuda(), i32([5, 4])
+    c = KVCache4(**size)
+    for ws in (c.ws_plan, c.ws_attn):
+        ws.fill_(7)
+    torch.cuda.synchronize()
+    del c, ws  # the allocator gives the next one the same memory
+    c = KVCache4(**size)
+    assert c.status() == 0
+    g = c.capture(q, kv[:, :2], kv[:, 2:], new, 0.125)
+    assert c.status() == 0
+    with pytest.raises(ValueError):
+        c.step(q.float(), kv[:, :2], kv[:, 2:], new, 0.125)
+    assert c.status() == 0
+    g.replay()
+    assert c.status() == 0 and c.len.tolist() == [5, 4]
