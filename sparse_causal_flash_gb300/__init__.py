@@ -354,6 +354,14 @@ def _cache4(name, cache, page_size, D):
     return dev, P, H
 
 
+def _ws_bytes(name, ws, dev) -> int:
+    """Size of a workspace, which the kernels write: on the device of the call."""
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{name}: ws must be a contiguous torch.uint8 tensor on cuda:{dev}, got {ws.dtype} (strides "
+                         f"{ws.stride()}) on {ws.device}")
+    return ws.numel()
+
+
 def _launch(fn, dev, stream, *args):
     """Call a C entry point whose last argument is the stream, with device `dev` current."""
     if dev != torch._C._cuda_getDevice():
@@ -383,7 +391,7 @@ def scfa_cache4_plan(len_, new_len, keep, free_pages, n_free, table, page_size, 
     _launch("scfa_cache4_plan", dev, stream, len_.data_ptr(), new_len.data_ptr(),
             None if keep is None else keep.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(), table.data_ptr(), N, R,
             mp, page_size, n_pages, len_out.data_ptr(), n_free_out.data_ptr(), q_start.data_ptr(), slot.data_ptr(),
-            vis.data_ptr(), ws.data_ptr(), ws.numel())
+            vis.data_ptr(), ws.data_ptr(), _ws_bytes("scfa_cache4_plan", ws, dev))
 
 
 def scfa_cache4_append(k, v, slot, cache, page_size, stream=None):
@@ -429,7 +437,7 @@ def scfa_cache4_attn(q, cache, page_size, table, q_start, vis, scale, o, lse, ws
                 lse=(lse, torch.float32, N * Hq))
     _launch("scfa_cache4_attn", dev, stream, q.data_ptr(), qt, qh, cache.data_ptr(), page_size, P, table.data_ptr(), mp,
             q_start.data_ptr(), vis.data_ptr(), N, R, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), o.data_ptr(), ot, oh,
-            lse.data_ptr(), ws.data_ptr(), ws.numel(), flags)
+            lse.data_ptr(), ws.data_ptr(), _ws_bytes("scfa_cache4_attn", ws, dev), flags)
 
 
 # ---------------------------------------------------------------- tiles

@@ -197,3 +197,51 @@ def test_status_words_of_a_new_cache_are_zero(scfa, monkeypatch):
     c = cache.KVCache4(R=2, n_pages=4, Hq=4, Hkv=2, D=64, max_len=64, max_tokens=2, device="cpu")
     for ws in (c.ws_plan, c.ws_attn):
         assert int(ws[:4].view(torch.int32)[0]) == 0
+
+
+class OnGpu:
+    """What the binding asks of a tensor, for one said to lie on a GPU."""
+
+    def __init__(self, *shape, dtype=torch.int32, dev=0, strides=None):
+        t = torch.empty(1, dtype=dtype).expand(shape)
+        self.shape, self.dtype, self.dev, self.strides = t.shape, dtype, dev, strides
+        self.device = torch.device("cuda", dev) if dev >= 0 else torch.device("cpu")
+
+    def get_device(self):
+        return self.dev
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return self.strides or torch.empty(self.shape, device="meta").stride()
+
+    def is_contiguous(self):
+        return self.strides is None or self.strides == torch.empty(self.shape, device="meta").stride()
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.mark.parametrize("ws,fine", [
+    (dict(), True), (dict(dev=-1), False), (dict(dev=1), False), (dict(dtype=torch.int32), False), (dict(strides=(2,)), False)])
+def test_binding_refuses_workspaces_it_cannot_take(scfa, monkeypatch, ws, fine):
+    """The kernels write the workspace: one in host memory, on another device or of other strides would be a wild address."""
+    calls = []
+    monkeypatch.setattr(scfa, "_launch", lambda fn, *a: calls.append(fn))
+    ws, u8, bf = OnGpu(1 << 20, **{"dtype": torch.uint8, **ws}), torch.uint8, torch.bfloat16
+    v = {n: OnGpu(n) for n in (1, 4, 5, 9)}
+    plan = lambda: scfa.scfa_cache4_plan(v[4], v[4], None, v[9], v[1], OnGpu(4, 3), 64, 9, v[4], v[1], v[5], v[4], v[4], ws)
+    rows = OnGpu(4, 2, 64, dtype=bf)
+    attn = lambda: scfa.scfa_cache4_attn(rows, OnGpu(9, 2, 64 * 68, dtype=u8), 64, OnGpu(4, 3), v[5], v[4], 0.125, rows,
+                                         OnGpu(4, 2, dtype=torch.float32), ws)
+    for call in (plan, attn):
+        if fine:
+            call()
+        else:
+            with pytest.raises(ValueError, match="ws"):
+                call()
+    assert len(calls) == (2 if fine else 0)
