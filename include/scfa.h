@@ -336,7 +336,8 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  * 64, 128 or 256. Row tensors of N tokens take a stride in elements per token
  * and per head (channels contiguous, strides multiples of 8, pointers 16-byte
  * aligned), so views of a fused projection need no copy. n_pages * page_size
- * and N are below 2^31; byte offsets are 64-bit.
+ * and N are below 2^31, max_pages * page_size (the longest request) is at most
+ * 2^31 - 256; byte offsets are 64-bit.
  *
  * The cache is a uint8 array [n_pages][Hkv][scfa_cache4_page_bytes], 16-byte
  * aligned. A group is 32 consecutive channels of one row of K or V and holds

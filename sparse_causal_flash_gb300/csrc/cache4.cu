@@ -473,7 +473,7 @@ scfa_status scfa_cache4_plan(const int32_t* len, const int32_t* new_len, const u
   if (N < 1 || R < 1 || max_pages < 1 || n_pages < 1) return SCFA_ERR_INVALID;
   if (!c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * page_size >= (1ll << 31))
+      static_cast<long long>(max_pages) * page_size > kC4MostTokens)
     return SCFA_ERR_UNSUPPORTED;
   PlanWs w;
   plan_ws_layout(N, R, &w);

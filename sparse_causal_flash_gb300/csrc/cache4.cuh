@@ -84,6 +84,9 @@ __device__ __forceinline__ uint32_t c4_pack(float lo, float hi) {
   return pack_bf16x2(lo, hi);
 }
 
+// Tokens that a request's row of the block table may stand for: positions, rounded up to whole units of 128, stay ints.
+constexpr long long kC4MostTokens = (1ll << 31) - 256;
+
 inline bool c4_page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
 // Let the kernel launched behind this one start its CTAs as these leave; it

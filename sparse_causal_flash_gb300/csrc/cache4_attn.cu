@@ -582,7 +582,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || !c4_page_size_ok(page_size)) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(n_pages) * page_size >= (1ll << 31) ||
-      static_cast<long long>(max_pages) * page_size >= (1ll << 31) ||
+      static_cast<long long>(max_pages) * page_size > kC4MostTokens ||
       static_cast<long long>(N) * Hq >= (1ll << 31) - 256)
     return SCFA_ERR_UNSUPPORTED;
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})

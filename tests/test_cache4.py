@@ -245,3 +245,11 @@ def test_binding_refuses_workspaces_it_cannot_take(scfa, monkeypatch, ws, fine):
             with pytest.raises(ValueError, match="ws"):
                 call()
     assert len(calls) == (2 if fine else 0)
+
+
+@pytest.mark.parametrize("ps,mp", [(16, 2 ** 27 - 1), (16, 2 ** 27 - 15), (64, 2 ** 25 - 1), (128, 2 ** 24 - 1)])
+def test_a_block_table_of_positions_past_ints_is_refused(scfa, ps, mp):
+    """Behind 2^31 - 256 the end of a unit of 128 tokens is no 32-bit int."""
+    assert 2 ** 31 - 256 < ps * mp < 2 ** 31
+    assert scfa._lib.scfa_cache4_plan(*plan_args(ps=ps, mp=mp)) == 2
+    assert scfa._lib.scfa_cache4_attn(*attn_args(ps=ps, mp=mp)) == 2

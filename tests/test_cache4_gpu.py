@@ -777,3 +777,28 @@ def test_status_before_the_first_step(scfa):
     assert c.status() == 0
     g.replay()
     assert c.status() == 0 and c.len.tolist() == [5, 4]
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_attn_the_longest_request(scfa, new):
+    """2^31 - 256 positions, all but the last pages one page of zero keys: the last visible key outweighs them (e^60 to
+    2^31), those behind it would outweigh it."""
+    D, ps, L = 64, 16, 2 ** 31 - 256
+    k = torch.zeros((64, 1, D), dtype=BF)
+    v = rand(2, (64, 1, D))
+    q = rand(3, (1, 2, D)).repeat(new, 1, 1)
+    q[:, 1] = q[:, 0]
+    scale = 0.125
+    one = (60 / scale / (q[0, 0].double() @ q[0, 0].double()) * q[0, 0].double()).to(BF)  # a score of about 60
+    k[48 + 10, 0], k[48 + 11:, 0] = one, 2 * one
+    cache = noise_cache(1, 4, 1, D, ps)
+    scfa.scfa_cache4_append(k.cuda(), v.cuda(), torch.arange(64, dtype=torch.int32, device="cuda"), cache, ps)
+    table = torch.zeros((1, L // ps), dtype=torch.int32, device="cuda")
+    table[0, -1] = 3
+    p = dict(q=q.cuda().contiguous(), cache=cache, ps=ps, table=table, q_start=i32([0, new]), vis=i32([L - 5] * new),
+             scale=scale, dt=BF)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    kk, vv = oc.values(dbl(k))[48:59], oc.values(dbl(v))[48:59]
+    assert np.all(np.abs(kk[10, 0] @ dbl(q[0, 0]) * scale - 60) < 10)
+    check_rows(dbl(p["q"]), kk, vv, [11] * new, scale, o, lse, BF)
