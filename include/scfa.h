@@ -335,7 +335,9 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  * Types: bf16 or fp16 rows (SCFA_DTYPE_*), D = 64 or 128, page_size 16, 32,
  * 64, 128 or 256. Row tensors of N tokens take a stride in elements per token
  * and per head (channels contiguous, strides multiples of 8, pointers 16-byte
- * aligned), so views of a fused projection need no copy. n_pages * page_size
+ * aligned), so views of a fused projection need no copy. Rows that are written
+ * must not share elements (strides shorter than a row, or two equal ones, are
+ * SCFA_ERR_INVALID). n_pages * page_size
  * and N are below 2^31, max_pages * page_size (the longest request) is at most
  * 2^31 - 256; byte offsets are 64-bit.
  *

@@ -516,6 +516,8 @@ scfa_status scfa_cache4_read(const uint8_t* cache, int page_size, int n_pages, c
   const scfa_status s =
       check_rows(k, k_token, k_head, v, v_token, v_head, slot, N, Hkv, D, dtype, cache, page_size, n_pages);
   if (s != SCFA_OK) return s;
+  if (c4_rows_overlap(k_token, k_head, N, Hkv, D) || c4_rows_overlap(v_token, v_head, N, Hkv, D))
+    return SCFA_ERR_INVALID;
   RowArgs a = row_args(k_token, k_head, v_token, v_head, slot, N, Hkv, page_size, n_pages, cache);
   a.k_out = k, a.v_out = v;
   const long long grid = (a.rows + 31) / 32;

@@ -89,6 +89,11 @@ constexpr long long kC4MostTokens = (1ll << 31) - 256;
 
 inline bool c4_page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
+// Rows [N][H] of D channels to write that certainly share elements: a stride shorter than a row, or two equal ones.
+inline bool c4_rows_overlap(long long token, long long head, int N, int H, int D) {
+  return (N > 1 && token < D && token > -D) || (H > 1 && head < D && head > -D) || (N > 1 && H > 1 && token == head);
+}
+
 // Let the kernel launched behind this one start its CTAs as these leave; it
 // waits with grid_wait() before it reads what this one writes.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

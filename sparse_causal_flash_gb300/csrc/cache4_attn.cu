@@ -588,6 +588,7 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
   for (const void* p : {static_cast<const void*>(q), static_cast<const void*>(cache), static_cast<const void*>(o)})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return SCFA_ERR_INVALID;
   if ((q_token | q_head | o_token | o_head) & 7) return SCFA_ERR_INVALID;
+  if (c4_rows_overlap(o_token, o_head, N, Hq, D)) return SCFA_ERR_INVALID;
   const int G = Hq / Hkv, rows = c4_rows(N, R, G), sms = num_sms(), grid = c4_ctas(rows, D, sms);
   const C4Ws w = c4_ws(D, sms);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.total) return SCFA_ERR_WORKSPACE;

@@ -253,3 +253,18 @@ def test_a_block_table_of_positions_past_ints_is_refused(scfa, ps, mp):
     assert 2 ** 31 - 256 < ps * mp < 2 ** 31
     assert scfa._lib.scfa_cache4_plan(*plan_args(ps=ps, mp=mp)) == 2
     assert scfa._lib.scfa_cache4_attn(*attn_args(ps=ps, mp=mp)) == 2
+
+
+@pytest.mark.parametrize("kw", [dict(kt=0), dict(vt=0), dict(kh=0), dict(vh=32), dict(kt=64), dict(kt=-56), dict(vt=256, vh=256)])
+def test_rows_to_write_that_share_elements_are_refused(scfa, kw):
+    """An expanded output would hold whichever row came last."""
+    assert scfa._lib.scfa_cache4_read(*rows_args(True, **kw)) == 1
+    if "kt" in kw or "kh" in kw:
+        o = {{"kt": "ot", "kh": "oh"}[x]: v for x, v in kw.items()}
+        assert scfa._lib.scfa_cache4_attn(*attn_args(**o)) == 1
+
+
+def test_strides_of_a_single_row_are_not_looked_at(scfa):
+    """No launch: the call is refused for its dtype behind, or its workspace before, the strides."""
+    assert scfa._lib.scfa_cache4_attn(*attn_args(N=1, ot=0, nb=128)) == 3
+    assert scfa._lib.scfa_cache4_attn(*attn_args(Hq=1, Hkv=1, oh=0, nb=128)) == 3

@@ -802,3 +802,24 @@ def test_attn_the_longest_request(scfa, new):
     kk, vv = oc.values(dbl(k))[48:59], oc.values(dbl(v))[48:59]
     assert np.all(np.abs(kk[10, 0] @ dbl(q[0, 0]) * scale - 60) < 10)
     check_rows(dbl(p["q"]), kk, vv, [11] * new, scale, o, lse, BF)
+
+
+def test_expanded_rows_are_read_but_not_written(scfa):
+    """Inputs may repeat a row by a stride of 0; outputs may not."""
+    N, H, D, ps = 20, 2, 64, 16
+    row, cache = rand(1, (1, H, D)).cuda(), noise_cache(2, 2, H, D, ps)
+    k, v, slot = row.expand(N, -1, -1), row[:, :1].expand(N, H, -1), torch.arange(N, dtype=torch.int32, device="cuda")
+    scfa.scfa_cache4_append(k, v, slot, cache, ps)
+    ko, vo = (torch.full((N, H, D), 3.0, dtype=BF, device="cuda") for _ in "kv")
+    scfa.scfa_cache4_read(cache, ps, slot, ko, vo)
+    assert np.array_equal(dbl(ko), oc.values(dbl(k))) and np.array_equal(dbl(vo), oc.values(dbl(v)))
+    for bad in (dict(k_out=ko[:1].expand(N, -1, -1)), dict(v_out=vo[:, :1].expand(-1, H, -1))):
+        with pytest.raises(scfa.ScfaError):
+            scfa.scfa_cache4_read(cache, ps, slot, **{**dict(k_out=ko, v_out=vo), **bad})
+    q = rand(3, (1, 2 * H, D)).cuda().expand(N, -1, -1)
+    p = dict(q=q, cache=cache, ps=ps, table=i32([[0, 1]]), q_start=i32([0, N]), vis=i32(range(1, N + 1)), scale=0.125, dt=BF)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    check_rows(dbl(q), dbl(ko), dbl(vo), list(range(1, N + 1)), 0.125, o, lse, BF)
+    with pytest.raises(scfa.ScfaError):
+        run_attn(scfa, p, o=o[:1].expand(N, -1, -1))
