@@ -36,8 +36,9 @@ class KVCache4:
                              "step must be positive")
         if Hkv < 1 or Hq < Hkv or Hq % Hkv != 0:
             raise ValueError(f"KVCache4: {Hq} query heads are no multiple of {Hkv} key heads")
-        dev = torch.device(device)
-        self.device, self.dtype = dev, dtype
+        # with its index: "cuda" is the device that is current now, not the one that is at a later call
+        self.device = dev = torch.empty(0, device=device).device
+        self.dtype = dtype
         self.R, self.n_pages, self.Hq, self.Hkv, self.D, self.page_size = R, n_pages, Hq, Hkv, D, page_size
         self.max_len, self.max_tokens = max_len, max_tokens
         max_pages = -(-max_len // page_size)

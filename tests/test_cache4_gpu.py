@@ -823,3 +823,11 @@ def test_expanded_rows_are_read_but_not_written(scfa):
     check_rows(dbl(q), dbl(ko), dbl(vo), list(range(1, N + 1)), 0.125, o, lse, BF)
     with pytest.raises(scfa.ScfaError):
         run_attn(scfa, p, o=o[:1].expand(N, -1, -1))
+
+
+def test_a_cache_keeps_the_index_of_its_device(scfa):
+    """"cuda" names the current device at every call; the cache stays where it was made."""
+    from sparse_causal_flash_gb300.cache import KVCache4
+    for device in ("cuda", torch.device("cuda"), torch.device("cuda", 0)):
+        c = KVCache4(2, 4, 4, 2, 64, max_len=32, max_tokens=4, device=device)
+        assert c.device == c.cache.device == torch.device("cuda", 0)
