@@ -449,15 +449,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache4_wide_kernel(C4AttnArgs
           if (KEYS == 32) load(0);
         }
       }
+      const uint64_t mm = f2(-m, -m);
 #pragma unroll 1
       for (int c = 0; c < KEYS / 32; ++c) {
         if (KEYS > 32) load(c);
         uint32_t p[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          // (a packed multiplication and addition gave infinities for far scores, as one rounding for both would)
-          const float p0 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), f), m));
-          const float p1 = ex2_approx(__fsub_rn(__fmul_rn(__uint_as_float(x[e + 1]), f), m));
+          // (two multiplications that are rounded, one packed subtraction; packed both gave infinities for far scores, as
+          // one rounding for both would)
+          float y0, y1;
+          f2_split(add2(f2(__fmul_rn(__uint_as_float(x[e]), f), __fmul_rn(__uint_as_float(x[e + 1]), f)), mm), y0, y1);
+          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
           l += p0;
           l2 += p1;
           p[e / 2] = c4_pack<true>(p0, p1);
