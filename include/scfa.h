@@ -327,10 +327,12 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  * it: the serving form of the causal attention above. Rows are tokens packed
  * request by request ([N][heads][D]); a request's cached tokens live in pages
  * of page_size tokens named by its row of a block table, in the order they
- * were appended. A dropped key (QK-sparse attention, scfa_qk_select) is
- * simply not cached: every cached token of a request precedes its later
- * tokens, so the causal mask of a query token is one number, vis: the count of
- * the request's cached tokens it sees, itself included when it was kept.
+ * were appended. A dropped key is simply not cached: every cached token of a
+ * request precedes its later tokens, so the causal mask of a query token is one
+ * number, vis: the count of the request's cached tokens it sees, itself
+ * included when it was kept. A token is dropped for all heads or none: this is
+ * the serving form of dense attention and of a QK-sparse mask that its heads
+ * share, not of one mask per head (scfa_qk_select takes such) nor of hash mode.
  *
  * Types: bf16 or fp16 rows (SCFA_DTYPE_*), D = 64 or 128, page_size 16, 32,
  * 64, 128 or 256. Row tensors of N tokens take a stride in elements per token
@@ -372,7 +374,8 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   slot = page * page_size + place in it (-1: dropped) and vis, for those
  *   up to N -1 and 0; len_out [R] and n_free_out [1], which may be len and
  *   n_free themselves. A request is released by pushing its pages on the
- *   stack and setting its len to 0. The status word reads SCFA_ERR_INVALID for a negative length,
+ *   stack and setting its len to 0 (a len that is lowered otherwise needs the
+ *   pages behind it pushed too: the next plan takes fresh ones there). The status word reads SCFA_ERR_INVALID for a negative length,
  *   sum(new_len) > N, more than max_pages pages in a request, or n_free
  *   outside [0, n_pages], SCFA_ERR_WORKSPACE when there are too few free
  *   pages: then nothing is taken, table, len and n_free stay, and q_start and
@@ -387,8 +390,8 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   q_start[r + 1], and query head h, over the first vis[t] cached tokens of r
  *   (head h / (Hq / Hkv)): o = softmax(scale q K^T) V, lse = its natural-log
  *   denominator; vis[t] = 0 gives o = 0, lse = -inf. vis must not decrease
- *   within a request. q, o [N][Hq][D], lse [N][Hq] fp32; Hq a multiple of
- *   Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
+ *   within a request. q, o [N][Hq][D] (o may be q itself, and must not overlap
+ *   it otherwise), lse [N][Hq] fp32; Hq a multiple of Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
  *   outside [0, n_pages) within a request's visible pages is skipped, its
  *   keys masked, and raises SCFA_ERR_INVALID in the status word. A query row
  *   that is not finite and sees a key gives NaN in its own o and lse only;

@@ -4,8 +4,10 @@ KVCache4 owns the pages, block tables and workspaces of a fixed number of
 request rows; step() plans the new tokens' slots on the GPU, quantises their
 keys and values into the pages and attends over what each token sees. Nothing
 is read back on the host, so a step can be captured as one CUDA graph and
-replayed for as long as its inputs keep their shapes. Keys dropped by a keep
-mask (QK-sparse attention) take no room: the cache holds the kept ones.
+replayed for as long as its inputs keep their shapes. Tokens whose keys a keep
+mask drops take no room: the cache holds the kept ones. The mask is one for all
+heads; QK-sparse masks that differ from head to head and hash-sparse attention
+have no serving form here.
 """
 from __future__ import annotations
 
@@ -61,7 +63,7 @@ class KVCache4:
 
     def step(self, q, k, v, new_len, scale, keep=None, stream=None):
         """One serving step: new_len [R] int32 new tokens of each request, packed
-        request by request in q [N, Hq, D], k, v [N, Hkv, D] (N at most
+        request by request in q [N, Hq, D], k, v [N, Hkv, D] (N from 1 to
         max_tokens; the sum of new_len may be smaller), keep [N] uint8 or
         None. Returns views of o [N, Hq, D] and lse [N, Hq], which the next
         step overwrites and whose rows from the sum of new_len on are left as

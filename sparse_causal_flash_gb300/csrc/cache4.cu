@@ -224,11 +224,13 @@ __device__ __forceinline__ RowAt row_at(const RowArgs& a) {
 }
 
 // The rows are read once and the codes written once; HBM and the issue slots
-// (69% busy, conversions, rounding and packing) bound it alike. 16,384 rows of 8
-// heads and 128 channels (67 MB in, 18 MB out): 20 us, 4.2 TB/s, 63% of the copy
-// rate. A group's largest magnitude is taken on the bits, two values at a time (a NaN is then
-// larger than infinity and is seen); groups with a value that is not finite or
-// beyond the largest scale take the careful way.
+// (74% busy: 13.5 lane operations a value, of conversions, rounding and packing,
+// but also of the row's place and of scales that its threads repeat) bound it
+// alike. 16,384 rows of 8 heads and 128 channels (67 MB in, 18 MB out): 20 us,
+// 4.2 TB/s, 63% of the copy rate. A group's largest magnitude is taken on the
+// bits, two values at a time (a NaN is then larger than infinity and is seen);
+// groups with a value that is not finite or beyond the largest scale take the
+// careful way.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) append_kernel(RowArgs a) {
   using L = C4<D>;
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(256) append_kernel(RowArgs a) {
 
 // The reverse, with the same threads: a thread writes the channels it read
 // there. 32,768 rows of 8 heads and 128 channels (36 MB in, 134 MB out): 32 us,
-// 5.3 TB/s, 79% of the copy rate, issue slots 63% busy.
+// 5.3 TB/s, 79% of the copy rate, issue slots 65% busy, 10.5 lane operations a value.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) read_kernel(RowArgs a) {
   using L = C4<D>;

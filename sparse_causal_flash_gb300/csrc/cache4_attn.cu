@@ -20,7 +20,9 @@
 //   Both operands are fp16, whatever the rows' type. Unpacking bounds the
 //   kernel: per eight codes one shift and four AND(-OR)s on the ALU, the rest,
 //   for V an addition and a multiplication a pair, on the FMA pipe, both at half
-//   rate. In the steady state the ALU is 62-65% busy, issue slots 60-70%.
+//   rate. Of the 2.9 (128 channels) or 3.8 (64) lane operations a value takes in
+//   all, some 1.7 unpack it; over the whole of the two cases below the issue
+//   slots are 51% and 67% busy, the ALU 39% and 51%.
 //   One request of 131,072 tokens, 8 key heads of 128 channels, 4 query heads
 //   each (143 MB): 37 us, 3.9 TB/s, 57% of the copy rate, some 5 us of it before
 //   the first unit's data; the join 7 us more. 61 ragged requests, 12 heads of 64
@@ -28,11 +30,14 @@
 //   K: the bits of c + 8 are read as a subnormal, (c + 8) 2^-24 (2^-20 for
 //      the upper half of a byte, whose query channels are divided by 16); the
 //      offset comes off as -8 sum(q), with the group's scale, in fp32. A query
-//      row is brought to a largest magnitude in [2^13, 2^14) by a power of two,
-//      which fp16 and bf16 values survive down to 2^-30 of that magnitude.
+//      row is brought to a largest magnitude in [2^13, 2^14) by a power of two.
+//      It is then exact in fp16 down to 2^-23 of that magnitude if it was fp16
+//      (2^-26 if bf16), what is smaller within 2^-34 of it; the channels that
+//      are not divided by 16 have four bits more.
 //   V: codes become c s in fp16 (exact: seven significant bits below 2^16).
 //      P is held times 2^7 in fp16, so weights down to 2^-32 of the largest
-//      count.
+//      count; each is rounded once (2^-11 of itself), as 16-bit operands ask,
+//      while their sum takes them in 32 bits.
 #include <cmath>
 
 #include "cache4_attn.cuh"
@@ -521,7 +526,11 @@ __global__ void __launch_bounds__(kThreads, C4Cfg<D, NT>::kCtas) cache4_attn_ker
 // warp-level kernel, more in blocks of 32, 64 or 128 on tcgen05. Requests of
 // several tokens are ragged and may have twice the average, so they leave the
 // warp-level kernel at 8 (32 requests with drafts of 1 to 7 tokens, groups of 4,
-// 128 channels: 148 us with blocks of 32, 204 us with blocks of 16).
+// 128 channels: 149 us with blocks of 32, 204 us with blocks of 16).
+// One size serves the whole call, and N and R, which the host knows, count
+// padding and requests without a new token too. So a call that mixes a long
+// prompt with many idle or single-token requests gets blocks that fit neither:
+// right, but slower than the two kinds in calls of their own.
 int c4_rows(int N, int R, int G) {
   const long long tokens = (static_cast<long long>(N) + R - 1) / R, rows = tokens * G;
   return rows <= 8 ? 8 : rows <= 16 && tokens == 1 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;

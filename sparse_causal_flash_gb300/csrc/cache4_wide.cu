@@ -20,16 +20,16 @@
 // are zero): the softmax of 32 rows then takes a quarter of the time, and the
 // copies, which keep their own maximum and sum, meet once per item.
 // At 128 channels a unit takes an SM some 2,300 cycles with 32 rows and 3,100
-// with 128; the tensor cores are 45% and 30% busy, the issue slots 68% and 59%.
+// with 128; the tensor cores are 45% and 30% busy, the issue slots 64% and 59%.
 // The MMAs alone, with nothing else running, take 1,300 cycles (80 each, 64 at
 // the peak rate). With 32 rows the unpacking warps work for
 // 1,800 of a unit's cycles, with 128 the softmax warps for 2,500; eight of those
 // instead of four take as long each (141 us instead of 142 in all), and so do
 // loads of 16 scores under the work on the 16 before (144). Code size counts: see
 // the loops that are not unrolled.
-// Two chunks of 500 tokens over 4,000 to 8,000 (96 GFLOP): 134 us and 9 us for
+// Two chunks of 500 tokens over 4,000 to 8,000 (96 GFLOP): 136 us and 8 us for
 // the join, 650 TFLOP/s, 33% of the measured matrix product; 32 requests with
-// drafts of 1 to 7 tokens (276 MB): 142 and 4 us.
+// drafts of 1 to 7 tokens (276 MB): 145 and 4 us (pages elsewhere: up to 158).
 #include <type_traits>
 
 #include "cache4_attn.cuh"

@@ -831,3 +831,14 @@ def test_a_cache_keeps_the_index_of_its_device(scfa):
     for device in ("cuda", torch.device("cuda"), torch.device("cuda", 0)):
         c = KVCache4(2, 4, 4, 2, 64, max_len=32, max_tokens=4, device=device)
         assert c.device == c.cache.device == torch.device("cuda", 0)
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [3, 1, 2], [40, 9, 20]])
+def test_attn_in_place_of_its_queries(scfa, news):
+    """o may be q itself: a row's queries have been read by all that need them when its o is written."""
+    p = attn_problem(scfa, 23, [900, 5000, 40], news, 8, 2, 64, 64, BF)
+    o, lse, _ = run_attn(scfa, p)
+    for _ in range(5):
+        q = p["q"].clone()
+        o2, lse2, _ = run_attn(scfa, {**p, "q": q}, o=q)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
