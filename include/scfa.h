@@ -339,9 +339,9 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  * and per head (channels contiguous, strides multiples of 8, pointers 16-byte
  * aligned), so views of a fused projection need no copy. Rows that are written
  * must not share elements (strides shorter than a row, or two equal ones, are
- * SCFA_ERR_INVALID). n_pages * page_size
- * and N are below 2^31, max_pages * page_size (the longest request) is at most
- * 2^31 - 256; byte offsets are 64-bit.
+ * SCFA_ERR_INVALID). n_pages * page_size and N are below 2^31, max_pages *
+ * page_size (the longest request) is at most 2^31 - 256; byte offsets are
+ * 64-bit.
  *
  * The cache is a uint8 array [n_pages][Hkv][scfa_cache4_page_bytes], 16-byte
  * aligned. A group is 32 consecutive channels of one row of K or V and holds
@@ -375,10 +375,11 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   up to N -1 and 0; len_out [R] and n_free_out [1], which may be len and
  *   n_free themselves. A request is released by pushing its pages on the
  *   stack and setting its len to 0 (a len that is lowered otherwise needs the
- *   pages behind it pushed too: the next plan takes fresh ones there). The status word reads SCFA_ERR_INVALID for a negative length,
- *   sum(new_len) > N, more than max_pages pages in a request, or n_free
- *   outside [0, n_pages], SCFA_ERR_WORKSPACE when there are too few free
- *   pages: then nothing is taken, table, len and n_free stay, and q_start and
+ *   pages behind it pushed too: the next plan takes fresh ones there). The
+ *   status word reads SCFA_ERR_INVALID for a negative length, sum(new_len) > N,
+ *   more than max_pages pages in a request, or n_free outside [0, n_pages],
+ *   SCFA_ERR_WORKSPACE when there are too few free pages: then nothing is
+ *   taken, table, len and n_free stay, and q_start and
  *   vis are all 0 and slot all -1. A page id outside [0, n_pages) gives slots of
  *   -1 and SCFA_ERR_INVALID.
  * scfa_cache4_append: quantises the rows k, v [N][Hkv][D] into their slots.
@@ -391,10 +392,11 @@ scfa_status lsh_unsort(const uint16_t* y_sorted, const int32_t* perm, int B, int
  *   (head h / (Hq / Hkv)): o = softmax(scale q K^T) V, lse = its natural-log
  *   denominator; vis[t] = 0 gives o = 0, lse = -inf. vis must not decrease
  *   within a request. q, o [N][Hq][D] (o may be q itself, and must not overlap
- *   it otherwise), lse [N][Hq] fp32; Hq a multiple of Hkv. Rows of o and lse from q_start[R] on are left as they are. A page id
- *   outside [0, n_pages) within a request's visible pages is skipped, its
- *   keys masked, and raises SCFA_ERR_INVALID in the status word. A query row
- *   that is not finite and sees a key gives NaN in its own o and lse only;
+ *   it otherwise), lse [N][Hq] fp32; Hq a multiple of Hkv. Rows of o and lse
+ *   from q_start[R] on are left as they are. A page id outside [0, n_pages)
+ *   within a request's visible pages is skipped, its keys masked, and raises
+ *   SCFA_ERR_INVALID in the status word. A query row that is not finite and
+ *   sees a key gives NaN in its own o and lse only;
  *   scale times a row's largest |q| is below 2^96, and scale * log2(e) an fp32
  *   number (SCFA_ERR_INVALID). The workspace (some 20 MB, one size for every N
  *   and R) serves one call at a time, and holds nothing from call to call.

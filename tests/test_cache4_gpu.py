@@ -842,3 +842,49 @@ def test_attn_in_place_of_its_queries(scfa, news):
         q = p["q"].clone()
         o2, lse2, _ = run_attn(scfa, {**p, "q": q}, o=q)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("new", [1, 4, 20, 70])
+@pytest.mark.parametrize("by", [2.0 ** 30, -2.0 ** 95])
+def test_attn_far_scores_of_requests_that_are_cut(scfa, new, by):
+    """The same over so many keys that every request's parts are joined: pages of one row each, one page nearest."""
+    D, L, ps, Hq = 64, 40000, 16, 2
+    u = rand(6, (1, 1, D), torch.float32)
+    near = 777 if by > 0 else 1234  # its page
+    w = torch.full((2, ps, 1, 1), 0.5 if by > 0 else 1.0)
+    w[1] = 1.0 if by > 0 else 0.5
+    k, v = (w * u).to(BF).flatten(0, 1), rand(7, (2, 1, 1, D)).expand(2, ps, 1, D).flatten(0, 1)
+    cache = noise_cache(1, 2, 1, D, ps)
+    scfa.scfa_cache4_append(k.cuda(), v.cuda(), torch.arange(2 * ps, dtype=torch.int32, device="cuda"), cache, ps)
+    table = torch.zeros((3, L // ps), dtype=torch.int32, device="cuda")
+    table[:, near] = 1
+    q = (u * 0.37 * np.sign(by)).to(BF).expand(3 * new, Hq, D).contiguous().cuda()
+    kk, vv = oc.values(dbl(k))[::ps], oc.values(dbl(v))[::ps]
+    scale = abs(by) / abs(float(kk[1, 0] @ dbl(q)[0, 0]))
+    p = dict(q=q, cache=cache, ps=ps, table=table, q_start=i32(np.arange(4) * new), vis=i32([L] * 3 * new), scale=scale, dt=BF)
+    o, lse, ws = run_attn(scfa, p)
+    assert scfa.scfa_get_device_status(ws) == 0
+    s = kk[:, 0] @ dbl(q)[0, 0] * scale
+    assert s[1] - s[0] > 0.3 * abs(s[1])
+    sg, qg = np.abs(kk[:, 0]).reshape(2, -1, 32).max(-1) / 6, np.abs(dbl(q)[0, 0]).reshape(-1, 32).sum(-1)
+    e = (D / 8 + 4) * 2.0 ** -23 * 15 * scale * (sg @ qg).max() + 2.0 ** -20 * np.abs(s).max()  # as check_rows derives it
+    assert np.all(np.abs(dbl(lse) - s[1]) <= e + 2.0 ** -18 * abs(s[1]) + np.log(ps))
+    # sixteen equal weights, each rounded to fp16 once
+    assert np.all(np.abs(dbl(o) - vv[1]) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18) * np.abs(vv[1]))
+
+
+def test_a_request_that_is_released_twice_gives_its_pages_back_once(scfa):
+    from sparse_causal_flash_gb300.cache import KVCache4
+    c = KVCache4(2, 6, 4, 2, 64, max_len=64, max_tokens=60, page_size=16)
+    q, kv = rand(1, (50, 4, 64)).cuda(), rand(2, (50, 4, 64)).cuda()
+    c.step(q, kv[:, :2], kv[:, 2:], i32([33, 17]), 0.125)
+    assert c.status() == 0 and int(c.n_free) == 1
+    for _ in range(2):
+        c.release(0)
+        assert int(c.n_free) == 4 and c.len.tolist() == [0, 17]
+    held = c.table[1, :2].tolist()
+    assert sorted(c.free[:4].tolist() + held) == list(range(6))
+    with pytest.raises(IndexError):
+        c.release(2)
+    k, v = c.rows(0)
+    assert k.shape == v.shape == (0, 2, 64)
