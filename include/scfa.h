@@ -429,6 +429,99 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
                              void* ws, size_t ws_bytes, unsigned flags, void* stream);
 
 /* ----------------------------------------------------------------------------
+ * Rotary positions of query and key rows, with the root-mean-square norm that
+ * may stand before them, and their gradients (not in the pages: what a model's
+ * projections pass through before the attention calls).
+ *
+ * Rows q [N][Hq][D], k [N][Hkv][D] of `dtype`, D = 64 or 128, 16-byte aligned,
+ * with token and head strides that are multiples of 8 elements (views of a
+ * fused projection); Hkv = 0: no keys. A row is turned by its token's position
+ * pos[t], any int32. For rows that each have a position of their own (the kept
+ * rows of QK-sparse heads), pass B*H*T tokens of one head; for [B][H][T][D]
+ * rows at positions 0..T-1, T tokens of B*H heads with token stride D and head
+ * stride T*D.
+ *   - Of the first rot channels (even, 0..D), pair i is (i, i + rot / 2), or
+ *     (2 i, 2 i + 1) with interleaved = 1. It turns by pos * f[i] radians and is
+ *     multiplied by `factor`; channels from rot on pass as they are.
+ *   - table [rot / 2]: f[i] / (2 pi) as 2^-64ths of a turn, modulo 2^64, so that
+ *     pos * table[i] modulo 2^64 is the angle at any position.
+ *   - With weights wq, wk [D] fp32 (both, or wq alone without keys) a row is
+ *     first divided by sqrt(mean(x^2) + eps) and multiplied by its weight.
+ *     |x| must stay below 2^60. Without weights there is no norm.
+ * scfa_rope_fwd: the turned rows; q_out may be q itself (k_out k), and must not
+ *   overlap it otherwise. Sums are fp32, each output is rounded once.
+ * scfa_rope_bwd: dq, dk are the gradients of scfa_rope_fwd's outputs, dq_out,
+ *   dk_out those of its inputs (may be dq, dk themselves). With a norm it takes
+ *   the forward's inputs q, k and weights too and writes dwq, dwk [D] fp32,
+ *   summed in an order that the sizes alone decide; ws: as
+ *   scfa_rope_workspace_size gives. Without a norm q, k, weights, their
+ *   gradients and ws are NULL.
+ * N = 0 is no error; dwq, dwk are then zero.
+ * ------------------------------------------------------------------------- */
+size_t scfa_rope_workspace_size(int N, int Hq, int Hkv, int D);
+scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head,
+                          const uint16_t* k, long long k_token, long long k_head,
+                          const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D,
+                          int rot, int interleaved, float factor, const float* wq, const float* wk,
+                          float eps, int dtype, uint16_t* q_out, long long qo_token,
+                          long long qo_head, uint16_t* k_out, long long ko_token,
+                          long long ko_head, void* stream);
+scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_head,
+                          const uint16_t* dk, long long dk_token, long long dk_head,
+                          const uint16_t* q, long long q_token, long long q_head,
+                          const uint16_t* k, long long k_token, long long k_head,
+                          const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D,
+                          int rot, int interleaved, float factor, const float* wq, const float* wk,
+                          float eps, int dtype, uint16_t* dq_out, long long dqo_token,
+                          long long dqo_head, uint16_t* dk_out, long long dko_token,
+                          long long dko_head, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* ----------------------------------------------------------------------------
+ * Causal attention over packed sequences whose query heads share key heads
+ * (not in the pages: the dense comparator's operation for batches of unlike
+ * lengths and for models with fewer key heads than query heads).
+ *
+ * Sequence r (0 <= r < R) has the query rows q_start[r] .. q_start[r + 1] of
+ * q [N][Hq][D] and the key rows k_start[r] .. k_start[r + 1] of k, v
+ * [M][Hkv][D]; Hq is a multiple of Hkv, at most 128 times it, and query head h
+ * reads key head h / (Hq / Hkv). With n queries and m keys, query t sees keys
+ * j <= t + m - n (the last query is aligned with the last key), and with
+ * window > 0 only j > t + m - n - window. A query that sees nothing gets o = 0,
+ * lse = -inf and passes no gradient.
+ *
+ * scfa_packed_plan: the work lists of a batch into `plan` (256-byte aligned, as
+ *   scfa_packed_plan_size gives; it depends on the number of SMs of the current
+ *   device, which must be that of the calls). One plan serves every later call
+ *   on tensors of N and M rows, of any layer, direction, D and type, also
+ *   several at once; it holds the starts itself. Starts that fall, or lie
+ *   outside [0, N] or [0, M], raise SCFA_ERR_INVALID in the plan's status word,
+ *   and in that of every call with the plan, which then computes nothing.
+ * scfa_packed_fwd: o [N][Hq][D], lse [N][Hq] fp32, natural log.
+ * Rows are bf16 or fp16 (dtype), D = 64 or 128, 16-byte aligned, with token and
+ * head strides that are positive multiples of 8 elements. Rows that belong to no
+ * sequence are neither read into results nor written. Inputs and outputs must
+ * not overlap. scale is positive, scale * log2(e) an fp32 number. The workspace
+ * (scfa_packed_workspace_size) holds nothing from call to call; a plan for other
+ * sizes raises SCFA_ERR_INVALID in its status word. Results are the same bits on
+ * every run. A row of q, k or v that is not finite may reach any row of its own
+ * sequence and key head, and no other. flags: SCFA_FLAG_DEBUG_SYNC,
+ * SCFA_FLAG_DEBUG_STALL.
+ * ------------------------------------------------------------------------- */
+size_t scfa_packed_plan_size(int N, int M, int R, int Hq, int Hkv);
+size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int Hkv, int D);
+scfa_status scfa_packed_plan(const int32_t* q_start, const int32_t* k_start, int N, int M, int R,
+                             int Hq, int Hkv, int window, void* plan, size_t plan_bytes,
+                             void* stream);
+scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, long long q_head,
+                            const uint16_t* k, long long k_token, long long k_head,
+                            const uint16_t* v, long long v_token, long long v_head,
+                            const void* plan, size_t plan_bytes, int N, int M, int Hq, int Hkv,
+                            int D, float scale, int dtype, uint16_t* o, long long o_token,
+                            long long o_head, float* lse, void* ws, size_t ws_bytes,
+                            unsigned flags, void* stream);
+
+/* ----------------------------------------------------------------------------
  * Tile metadata and the live-tile work list (page section "SCFA 解决方案":
  * tile pruning of part 1, bucket and causal pruning of part 2). Normally run
  * inside the attention calls; exposed for inspection and tests. Writes into

@@ -12,6 +12,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -77,6 +78,14 @@ _SIGS = {
     "scfa_cache4_read": ([_P, _I, _I, _P, _I, _I, _I, _I, _P, _L, _L, _P, _L, _L, _P], _I),
     "scfa_cache4_attn": ([_P, _L, _L, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _L, _L, _P, _P, _S,
                           _U, _P], _I),
+    "scfa_rope_workspace_size": ([_I, _I, _I, _I], _S),
+    "scfa_rope_fwd": ([_P, _L, _L] * 2 + [_P, _P] + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P], _I),
+    "scfa_rope_bwd": ([_P, _L, _L] * 4 + [_P, _P] + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P, _P, _P, _S, _P],
+                      _I),
+    "scfa_packed_plan_size": ([_I] * 5, _S),
+    "scfa_packed_workspace_size": ([_I] * 7, _S),
+    "scfa_packed_plan": ([_P, _P] + [_I] * 6 + [_P, _S, _P], _I),
+    "scfa_packed_fwd": ([_P, _L, _L] * 3 + [_P, _S] + [_I] * 5 + [_F, _I, _P, _L, _L, _P, _P, _S, _U, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
 
@@ -438,6 +447,132 @@ def scfa_cache4_attn(q, cache, page_size, table, q_start, vis, scale, o, lse, ws
     _launch("scfa_cache4_attn", dev, stream, q.data_ptr(), qt, qh, cache.data_ptr(), page_size, P, table.data_ptr(), mp,
             q_start.data_ptr(), vis.data_ptr(), N, R, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), o.data_ptr(), ot, oh,
             lse.data_ptr(), ws.data_ptr(), _ws_bytes("scfa_cache4_attn", ws, dev), flags)
+
+
+# ---------------------------------------------------------------- rotary positions
+def rope_table(inv_freq, device="cuda") -> torch.Tensor:
+    """The frequencies of rotary positions as scfa_rope_fwd takes them: inv_freq [rot / 2], radians per position (rounded
+    to float64), as int64 2^-64ths of a turn. A position's angle is then exact modulo one turn, however far it is."""
+    turns = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu") / (2 * math.pi)
+    if turns.dim() != 1 or not bool(torch.isfinite(turns).all()):
+        raise ValueError(f"rope_table: inv_freq must be finite numbers [rot / 2], got {tuple(turns.shape)}")
+    turns = turns - torch.round(turns)  # -1/2 .. 1/2: whole turns do nothing
+    # 2^64 turns in two exact steps: the high 32 bits, then what is left of them
+    high = torch.floor(turns * 2.0 ** 32)
+    low = torch.round((turns * 2.0 ** 32 - high) * 2.0 ** 32)
+    table = high.to(torch.int64) * 2 ** 32 + low.to(torch.int64)  # wraps at half a turn, as angles do
+    return table.to(torch.device(inv_freq.device if isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda else device))
+
+
+def rope_workspace_size(N, Hq, Hkv, D) -> int:
+    """Bytes of the workspace of scfa_rope_bwd with a norm."""
+    return int(_lib.scfa_rope_workspace_size(int(N), int(Hq), int(Hkv), int(D)))
+
+
+def _rope_args(name, dev, pos, table, N, D, wq, wk, k):
+    """Checks what both directions share; the pairs that are turned."""
+    rot = 2 * table.numel()
+    if not (_is(pos, _i32, dev, N) and _is(table, torch.int64, dev, rot // 2)):
+        _refuse(name, dev, pos=(pos, _i32, N), table=(table, torch.int64, rot // 2))
+    if rot > D:
+        raise ValueError(f"{name}: table has {rot // 2} frequencies, a row {D} channels")
+    for key, w in (("wq", wq), ("wk", wk)):
+        if w is not None and not _is(w, torch.float32, dev, D):
+            _refuse(name, dev, **{key: (w, torch.float32, D)})
+    if (wk is not None) != (wq is not None and k is not None):
+        raise ValueError(f"{name}: the norm takes a weight for queries and one for keys, or none")
+    return rot
+
+
+def scfa_rope_fwd(q, k, pos, table, q_out, k_out, interleaved=False, factor=1.0, wq=None, wk=None, eps=1e-6, stream=None):
+    """Turn the rows q [N, Hq, D] and k [N, Hkv, D] (or None) by their positions pos [N] int32 into q_out, k_out (which
+    may be q, k themselves); table from rope_table. With the weights wq, wk [D] fp32, rows pass a root-mean-square norm
+    first."""
+    N, Hq, D = q.shape
+    dev, dt = q.get_device(), q.dtype
+    Hkv = 0 if k is None else k.shape[1]
+    rot = _rope_args("scfa_rope_fwd", dev, pos, table, N, D, wq, wk, k)
+    qt, qh = _rows4("scfa_rope_fwd", "q", q, N, Hq, D, dt, dev)
+    ot, oh = _rows4("scfa_rope_fwd", "q_out", q_out, N, Hq, D, dt, dev)
+    kp = kt = kh = lp = lt = lh = 0
+    if k is not None:
+        kt, kh = _rows4("scfa_rope_fwd", "k", k, N, Hkv, D, dt, dev)
+        lt, lh = _rows4("scfa_rope_fwd", "k_out", k_out, N, Hkv, D, dt, dev)
+        kp, lp = k.data_ptr(), k_out.data_ptr()
+    _launch("scfa_rope_fwd", dev, stream, q.data_ptr(), qt, qh, kp, kt, kh, pos.data_ptr(), table.data_ptr(), N, Hq, Hkv, D,
+            rot, int(interleaved), factor, None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
+            _DTYPES.get(dt, -1), q_out.data_ptr(), ot, oh, lp, lt, lh)
+
+
+def scfa_rope_bwd(dq, dk, pos, table, dq_out, dk_out, interleaved=False, factor=1.0, q=None, k=None, wq=None, wk=None,
+                  eps=1e-6, dwq=None, dwk=None, ws=None, stream=None):
+    """Gradients of scfa_rope_fwd: dq, dk are those of its outputs, dq_out, dk_out (which may be dq, dk themselves) those
+    of its inputs. With a norm also its inputs q, k and weights, and dwq, dwk [D] fp32 for the weights' gradients, with a
+    workspace (rope_workspace_size)."""
+    N, Hq, D = dq.shape
+    dev, dt = dq.get_device(), dq.dtype
+    Hkv = 0 if dk is None else dk.shape[1]
+    rot = _rope_args("scfa_rope_bwd", dev, pos, table, N, D, wq, wk, dk)
+    rows = [dq, dk, None, None, dq_out, dk_out]
+    ptrs = [0] * 4
+    nbytes = 0
+    if wq is not None:
+        if q is None or dwq is None or ws is None or (dk is not None and (k is None or dwk is None)):
+            raise ValueError("scfa_rope_bwd: a norm's gradient needs the rows, weights, weight gradients and a workspace")
+        for key, w in (("dwq", dwq), ("dwk", dwk)):
+            if w is not None and not _is(w, torch.float32, dev, D):
+                _refuse("scfa_rope_bwd", dev, **{key: (w, torch.float32, D)})
+        rows[2:4] = [q, k if dk is not None else None]
+        nbytes = _ws_bytes("scfa_rope_bwd", ws, dev)
+        ptrs = [wq.data_ptr(), wk.data_ptr() if dk is not None else None, dwq.data_ptr(),
+                dwk.data_ptr() if dk is not None else None]
+    args = []
+    for i, (key, t) in enumerate(zip(("dq", "dk", "q", "k", "dq_out", "dk_out"), rows)):
+        if t is None:
+            if i == 5 and dk is not None:
+                raise ValueError("scfa_rope_bwd: dk needs dk_out")
+            args.append((0, 0, 0))
+        else:
+            args.append((t.data_ptr(), *_rows4("scfa_rope_bwd", key, t, N, (Hq, Hkv)[i & 1], D, dt, dev)))
+    _launch("scfa_rope_bwd", dev, stream, *args[0], *args[1], *args[2], *args[3], pos.data_ptr(), table.data_ptr(), N, Hq,
+            Hkv, D, rot, int(interleaved), factor, ptrs[0], ptrs[1], eps, _DTYPES.get(dt, -1), *args[4], *args[5], ptrs[2],
+            ptrs[3], None if ws is None else ws.data_ptr(), nbytes)
+
+
+# ---------------------------------------------------------------- packed sequences, shared key heads
+def packed_plan_size(N, M, R, Hq, Hkv) -> int:
+    """Bytes of a plan (a workspace() tensor) for N query rows and M key rows in R sequences."""
+    return int(_lib.scfa_packed_plan_size(int(N), int(M), int(R), int(Hq), int(Hkv)))
+
+
+def packed_workspace_size(backward, N, M, R, Hq, Hkv, D) -> int:
+    return int(_lib.scfa_packed_workspace_size(int(backward), int(N), int(M), int(R), int(Hq), int(Hkv), int(D)))
+
+
+def scfa_packed_plan(q_start, k_start, N, M, Hq, Hkv, window, plan, stream=None):
+    """The work lists of a batch of R sequences into `plan`: q_start, k_start [R + 1] int32 (one tensor may be both),
+    window 0 or the number of keys that a query sees at most. One plan serves every forward and backward call on tensors
+    of N query and M key rows, until its starts change."""
+    R, dev = q_start.numel() - 1, q_start.get_device()
+    if not (dev >= 0 and _is(q_start, _i32, dev, R + 1) and _is(k_start, _i32, dev, R + 1)):
+        _refuse("scfa_packed_plan", dev, q_start=(q_start, _i32, R + 1), k_start=(k_start, _i32, R + 1))
+    _launch("scfa_packed_plan", dev, stream, q_start.data_ptr(), k_start.data_ptr(), N, M, R, Hq, Hkv, window,
+            plan.data_ptr(), _ws_bytes("scfa_packed_plan", plan, dev))
+
+
+def scfa_packed_fwd(q, k, v, plan, scale, o, lse, ws, flags=0, stream=None):
+    """Attention of q [N, Hq, D] over k, v [M, Hkv, D] by the sequences of `plan`: o [N, Hq, D], lse [N, Hq] fp32. Rows of
+    no sequence are left as they were."""
+    N, Hq, D = q.shape
+    M, Hkv = k.shape[:2]
+    dev, dt = q.get_device(), q.dtype
+    rows = [(t.data_ptr(), *_rows4("scfa_packed_fwd", key, t, n, h, D, dt, dev))
+            for key, t, n, h in (("q", q, N, Hq), ("k", k, M, Hkv), ("v", v, M, Hkv), ("o", o, N, Hq))]
+    if not _is(lse, torch.float32, dev, N * Hq):
+        _refuse("scfa_packed_fwd", dev, lse=(lse, torch.float32, N * Hq))
+    _launch("scfa_packed_fwd", dev, stream, *rows[0], *rows[1], *rows[2], plan.data_ptr(),
+            _ws_bytes("scfa_packed_fwd", plan, dev), N, M, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), *rows[3], lse.data_ptr(),
+            ws.data_ptr(), _ws_bytes("scfa_packed_fwd", ws, dev), flags)
 
 
 # ---------------------------------------------------------------- tiles

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "packed.cuh"
 
 namespace scfa {
 
@@ -61,6 +62,22 @@ bool make_tmap_bf16_rows(CUtensorMap* map, const void* base, int D, long long ro
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows(CUtensorMap* map, const void* base, bool f16, int D, int heads, long long tokens, long long head_stride,
+                    long long token_stride, int box_heads, int box_tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  // the stride of an axis of one is never used, and may be anything
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(heads > 1 ? head_stride : D) * 2,
+                           static_cast<cuuint64_t>(tokens > 1 ? token_stride : D) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                  dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -1,0 +1,161 @@
+// Attention over packed sequences with shared key heads: what the plan, the forward and the backward have in common.
+//
+// A tile of query rows is TPT = 128 / G tokens times the G query heads of one key head, row (token, head of the group)
+// at token * G + head: the heads that share keys share every key tile that is loaded, and a causal border inside a
+// tile is TPT tokens wide instead of 128. (G = 3: 42 tokens, 126 rows; the rows behind stay zero in shared memory.)
+// A tile of keys is 128 keys of one sequence. The plan cuts the work of one key head into entries; a kernel's work item
+// w is entry w / Hkv for key head w % Hkv.
+#pragma once
+
+#include "cache4.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace scfa {
+
+constexpr uint32_t kPackMagic = 0x50414b31u;
+constexpr int kPackSub = kTile * 128;  // bytes of a [128 rows][64 channels] swizzled sub-tile
+constexpr float kPackLog2e = 1.4426950408889634f;
+constexpr float kPackLn2 = 0.6931471805599453f;
+// Chunks that cut entries may leave behind for their join, over all key heads.
+constexpr int kPackSlotsPerSm = 4;
+
+enum { kListFwd = 0, kListDq = 1, kListDkv = 2, kLists = 3 };
+
+// One piece of work of one key head. Query lists: the tokens q0 .. q0 + n_tok (rows of q) see the keys k0 .. of one
+// sequence; token i sees the sequence's keys up to diag + i, and in this entry tiles [a, b) of them. Key list: the keys
+// k0 .. k0 + n_tok (rows of k; at `diag` in their sequence) with the query tiles [a, b) of the sequence, whose tokens
+// start at row q0; token t sees the keys up to t + shift.
+struct PackEntry {
+  int q0, k0, n_tok, diag;
+  int a, b;
+  int m;       // query lists: keys of the sequence. Key list: its tokens
+  int shift;   // key list: keys minus queries of the sequence
+  int tile0;   // number of the (first) query tile over all sequences
+  int slot;    // first partial slot of the cut entry (per key head); -1: not cut
+  int chunk, chunks;
+  int cut;     // number of the cut entry
+  int pad[3];
+};
+static_assert(sizeof(PackEntry) == 64, "entries are copied as 16 words");
+
+struct PackHeader {
+  int status;  // SCFA_OK or what is wrong with the sequences
+  uint32_t magic;
+  int N, M, R, Hq, Hkv, window;
+  int n_entries[kLists];
+  int n_qtiles;            // query tiles of all sequences
+  int list_status[kLists];  // (each list is built by a CTA of its own)
+  int pad0;
+  long long entries[kLists];  // byte offsets from the plan's start
+  long long qtiles;           // int2 (first token, tokens) of each query tile
+  long long bytes;
+  int pad[38];
+};
+static_assert(sizeof(PackHeader) == 256, "the plan's header");
+
+struct PackPlanLayout {
+  // first tile of each sequence [kLists + 1][R + 1] (the last one: query tiles again, for the key list's CTA); (units,
+  // sequence) of each tile, list by list; the rest is what the header names
+  size_t pre = 0, units[kLists] = {}, qtiles = 0, entries[kLists] = {}, total = 0;
+  long long most[kLists] = {};  // entries of each list at most
+};
+
+inline int pack_slots(int sms) { return kPackSlotsPerSm * sms; }
+
+// false if the sizes are out of range
+inline bool pack_plan_layout(int N, int M, int R, int Hq, int Hkv, int sms, PackPlanLayout* L) {
+  if (N < 0 || M < 0 || R < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > kTile) return false;
+  const int tpt = kTile / (Hq / Hkv);
+  PackPlanLayout w;
+  const long long extra = static_cast<long long>(R) + pack_slots(sms);
+  w.most[kListFwd] = N / (2 * tpt) + extra;
+  w.most[kListDq] = N / tpt + extra;
+  w.most[kListDkv] = M / kTile + extra;
+  for (long long n : w.most)
+    if (n * Hkv >= (1ll << 31) - 1024) return false;
+  size_t off = sizeof(PackHeader);
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  w.pre = take(static_cast<size_t>(kLists + 1) * (R + 1) * sizeof(int));
+  for (int i = 0; i < kLists; ++i) w.units[i] = take(static_cast<size_t>(w.most[i]) * sizeof(int2));
+  w.qtiles = take((static_cast<size_t>(N / tpt) + R) * sizeof(int2));
+  for (int i = 0; i < kLists; ++i) w.entries[i] = take(static_cast<size_t>(w.most[i]) * sizeof(PackEntry));
+  w.total = off;
+  *L = w;
+  return true;
+}
+
+// Workspace: status and counters, then the partial results of cut entries, then (backward) the rows' statistics.
+struct PackWs {
+  size_t counters = 0;  // ints: work counters [2], then arrivals of cut entries [2][slots][2]
+  size_t part = 0;      // fp32
+  size_t stats = 0;     // backward: [3][query tiles][Hkv][128]
+  size_t clear = 0;     // bytes from the start that a call clears
+};
+inline PackWs pack_ws(bool backward, int D, int sms) {
+  PackWs w;
+  const size_t slots = static_cast<size_t>(pack_slots(sms));
+  w.counters = sizeof(WsHeader);
+  w.clear = align_up(w.counters + (2 + 4 * slots) * sizeof(int), 256);
+  w.part = w.clear;
+  // forward: two tiles of D + 2 columns; backward: dK and dV, or dQ
+  w.stats = align_up(w.part + slots * 2 * kTile * (D + (backward ? 0 : 2)) * sizeof(float), 256);
+  return w;
+}
+inline long long pack_stats_tile_bytes(int Hkv) { return 3ll * Hkv * kTile * sizeof(float); }
+
+// What every kernel checks first: the plan is one for this call and lies in its buffer.
+__device__ __forceinline__ int pack_plan_status(const PackHeader* h, long long bytes, int N, int M, int Hq, int Hkv) {
+  if (h->magic != kPackMagic || h->N != N || h->M != M || h->Hq != Hq || h->Hkv != Hkv || h->bytes > bytes) return SCFA_ERR_INVALID;
+  for (int i = 0; i < kLists; ++i)
+    if (h->list_status[i] != SCFA_OK) return h->list_status[i];
+  return SCFA_OK;
+}
+
+// instruction descriptor of kind::f16 with fp32 accumulators, both operands bf16 or both fp16
+template <bool F16>
+__host__ __device__ constexpr uint32_t pack_idesc(int M, int N, int a_mn, int b_mn) {
+  return F16 ? (idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10))) : idesc_bf16_f32(M, N, a_mn, b_mn);
+}
+
+// one arrival for a warp, behind all its lanes' work
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// a wait by a whole warp (false for every lane if one gave up)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  const bool ok = mbar_wait(bar, parity, abort_flag, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Registers of a warpgroup's threads, which all of its warps change together: fewer, or more of what others gave up.
+template <int N>
+__device__ __forceinline__ void regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// Rows [from, to) of a tile in shared memory become zero (whole rows: the swizzle moves 16-byte pieces inside a row).
+__device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int subs, int from, int to, int lane, int lanes) {
+  for (int i = lane; i < (to - from) * 8 * subs; i += lanes) {
+    const int sub = i / ((to - from) * 8), at = i % ((to - from) * 8);
+    *reinterpret_cast<uint4*>(tile + sub * kPackSub + from * 128 + at * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// 3-D map {channels, heads, tokens} over rows with their own strides (in elements); box = 64 channels x `box_heads`
+// heads x `box_tokens` tokens, 128-byte swizzle, zeros behind the ends.
+bool make_tmap_rows(CUtensorMap* map, const void* base, bool f16, int D, int heads, long long tokens, long long head_stride,
+                    long long token_stride, int box_heads, int box_tokens);
+
+// A read operand of the packed calls: aligned, with positive strides where an axis is longer than one.
+inline bool pack_rows_ok(const void* p, long long token, long long head, long long N, int H) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) & 15u) || ((token | head) & 7)) return false;
+  return (N <= 1 || (token > 0 && token < (1ll << 38))) && (H <= 1 || (head > 0 && head < (1ll << 38)));
+}
+
+}  // namespace scfa

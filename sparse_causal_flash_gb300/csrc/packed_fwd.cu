@@ -1,0 +1,575 @@
+// Attention over packed sequences with shared key heads, forward: o = softmax(scale q K^T) V and the log-sum-exp of each
+// query row, over the keys that its token sees (causal, the last query at the last key; optionally the last `window`).
+//
+// One pass over the keys with a running reference m and sum l per row: P = 2^(s scale log2(e) - m), O += P V, and when a
+// row's maximum outgrows m by more than 8 (log2 units) O and l are brought to the new one. O / l and m + log2(l) at the
+// end. S, O, m and l are fp32; P is rounded once to the rows' type for its product with V (the tensor cores take 16-bit
+// operands), at most 2^8 by the rule above.
+//
+// One CTA per SM, work from a counter, longest first. A work item is two tiles of query rows of one key head that share
+// each K and V tile. Roles:
+//   warp 0        producer: TMA of the item's two Q tiles and of K_j, V_j into rings
+//   warps 1, 2    MMA issuers of tile 0 and 1: S = Q K^T, then O += P V with P read from TMEM, in two halves of the keys
+//   warps 4-7, 8-11  softmax of tile 0 and 1: thread = row = TMEM lane; a row's 128 scores stay in its registers (216 of
+//                 them; the first four warps give up what they do not need)
+// TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 behind it. At D = 128 that is all of it and P_g takes the first
+// half of S_g; at D = 64 P_g has columns of its own and S of the next key tile runs under the softmax of this one.
+//
+// Keys behind the last one of a sequence belong to another: their scores are masked, and the V rows among the 16 of the
+// last MMA step are zeroed in shared memory (0 x NaN is NaN), the steps behind it left out.
+//
+// Entries that the plan cut leave (O, m, l) in the workspace; the last of an entry's chunks to arrive joins them in the
+// order of the chunks, so results do not depend on which it was.
+#include <climits>
+
+#include "packed.cuh"
+
+namespace scfa {
+namespace {
+
+constexpr int kThreads = 384;
+// registers of a thread of warps 0-3 and of the softmax warps: 128 x 72 + 256 x 216 = 384 x 168, what the CTA starts with
+constexpr int kRegsFew = 72, kRegsMany = 216;
+constexpr int kSlots = 2;  // items known ahead
+constexpr float kGrow = 8.f;
+constexpr float kFarScore = 65536.f;
+
+template <int D>
+struct PFwdCfg {
+  static constexpr int kSubs = D / 64;
+  static constexpr int kQ = D == 64 ? 4 : 3;       // Q tiles in the ring
+  static constexpr int kStages = D == 64 ? 4 : 2;  // K and V tiles
+  static constexpr bool kOwnP = D == 64;
+};
+
+struct PItem {
+  PackEntry e;
+  int head;  // -1: no more work
+  int pad[15];
+};
+
+template <int D>
+struct __align__(1024) PFwdSmem {
+  using C = PFwdCfg<D>;
+  uint8_t q[C::kQ][C::kSubs][kPackSub];
+  uint8_t k[C::kStages][C::kSubs][kPackSub];
+  uint8_t v[C::kStages][C::kSubs][kPackSub];
+  PItem item[kSlots];
+  uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kStages], v_full[C::kStages], kv_empty[C::kStages];
+  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2], sync[2];
+  uint64_t tail, item_full[kSlots], item_empty[kSlots];
+  uint32_t tmem_base;
+  int abort_flag, last[2];
+};
+
+struct PFwdParams {
+  const char* plan;
+  long long plan_bytes;
+  int N, M, Hq, Hkv, G, tpt;
+  float scale_log2;
+  uint16_t* o;
+  long long ot, oh;
+  float* lse;
+  int* counter;   // next item
+  int* arrivals;  // [cut][Hkv][2]
+  float* part;    // [slot][Hkv][2][(D + 2) x 128]
+  int stall;
+  int* status;
+};
+
+// Key tiles [a, b) of query tile g of an entry (empty: nothing to compute for it here).
+__device__ __forceinline__ void fwd_range(const PackEntry& e, int g, int tpt, int window, int& a, int& b) {
+  const int first = e.diag + g * tpt, n = min(tpt, e.n_tok - g * tpt), last = first + n - 1;
+  a = b = 0;
+  if (n <= 0 || last < 0) return;
+  b = min(e.b, last / kTile + 1);
+  a = e.a;
+  if (window && first - window + 1 > 0) a = max(a, (first - window + 1) / kTile);
+  if (a >= b) a = b = 0;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PFwdParams p) {
+  using C = PFwdCfg<D>;
+  constexpr int kSubs = C::kSubs, kStages = C::kStages, kQ = C::kQ;
+  constexpr bool kOwnP = C::kOwnP;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  PFwdSmem<D>& sm = *reinterpret_cast<PFwdSmem<D>*>(smem_raw + pad);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
+  const int plan_status = pack_plan_status(h, p.plan_bytes, p.N, p.M, p.Hq, p.Hkv);
+  if (plan_status != SCFA_OK) {  // the same for every thread
+    if (threadIdx.x == 0) raise_status(p.status, plan_status);
+    return;
+  }
+  const int window = h->window, n_work = h->n_entries[kListFwd] * p.Hkv;
+  const int used = p.G * p.tpt;  // rows of a tile that hold a query
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kQ; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.v_full[s], 1), mbar_init(&sm.kv_empty[s], 2);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sm.s_full[g], 1), mbar_init(&sm.s_free[g], 4);
+      mbar_init(&sm.p_full[g][0], 4), mbar_init(&sm.p_full[g][1], 4);
+      mbar_init(&sm.pv_done[g], 1), mbar_init(&sm.o_full[g], 1), mbar_init(&sm.o_empty[g], 4);
+      mbar_init(&sm.drain[g], 1), mbar_init(&sm.sync[g], 4);
+    }
+    mbar_init(&sm.tail, 1);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 2 + 8);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
+  }
+  if (used < kTile) {  // rows that no copy writes: zero for good
+    for (int s = 0; s < kQ; ++s) zero_tile_rows(sm.q[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* const abort_flag = &sm.abort_flag;
+
+  if (warp < 4) {
+  regs_release<kRegsFew>();
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListFwd]);
+    int q_it = 0, kv_it = 0, tails = 0, unmarked = -1;  // unmarked: V tile whose zeros an abort kept from being written
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int slot = it % kSlots;
+      ok = warp_wait(&sm.item_empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, p.status);
+      if (!ok) break;
+      int w = 0;
+      if (lane == 0) w = atomicAdd(p.counter, 1);
+      w = __shfl_sync(0xffffffffu, w, 0);
+      const int head = w < n_work ? w % p.Hkv : -1;
+      PItem& item = sm.item[slot];
+      if (head >= 0 && lane < 16)
+        reinterpret_cast<int*>(&item.e)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / p.Hkv) + lane);
+      if (lane == 0) item.head = head;
+      warp_arrive(&sm.item_full[slot]);
+      if (head < 0) break;
+      const PackEntry e = item.e;
+      int a[2], b[2];
+      fwd_range(e, 0, p.tpt, window, a[0], b[0]);
+      fwd_range(e, 1, p.tpt, window, a[1], b[1]);
+      for (int g = 0; g < 2 && ok; ++g) {
+        if (a[g] == b[g]) continue;
+        const int s = q_it % kQ;
+        ok = warp_wait(&sm.q_empty[s], ((q_it / kQ) & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full[s], D * used * 2);
+          for (int sub = 0; sub < kSubs; ++sub)
+            tma_load_3d(sm.q[s][sub], &tm_q, &sm.q_full[s], sub * 64, head * p.G, e.q0 + g * p.tpt);
+        }
+        ++q_it;
+      }
+      if (p.stall && kv_it == 0 && a[0] + b[0] + a[1] + b[1] > 0) break;  // debug stall: no K / V load ever arrives
+      const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
+      for (int j = j0; j < j1 && ok; ++j) {
+        const int s = kv_it % kStages;
+        ok = warp_wait(&sm.kv_empty[s], ((kv_it / kStages) & 1) ^ 1, abort_flag, p.status);
+        if (!ok) break;
+        const int valid = e.m - j * kTile;  // keys of the sequence in the tile, if below 128
+        const bool cut = valid < kTile && (valid & 15) != 0;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.k_full[s], D * kTile * 2);
+          for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.k[s][sub], &tm_k, &sm.k_full[s], sub * 64, head, e.k0 + j * kTile);
+          uint64_t* const vb = cut ? &sm.tail : &sm.v_full[s];
+          mbar_arrive_expect_tx(vb, D * kTile * 2);
+          for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.v[s][sub], &tm_v, vb, sub * 64, head, e.k0 + j * kTile);
+        }
+        ++kv_it;
+        if (cut) {
+          ok = warp_wait(&sm.tail, tails & 1, abort_flag, p.status);
+          ++tails;
+          if (!ok) {
+            unmarked = kv_it - 1;
+            break;
+          }
+          zero_tile_rows(sm.v[s][0], kSubs, valid, (valid + 15) & ~15, lane, 32);
+          fence_proxy_async_smem();
+          warp_arrive(&sm.v_full[s]);
+        }
+      }
+    }
+    if (lane == 0) {
+      // every copy issued has landed before the CTA exits, also after an abort
+      if (tails > 0) mbar_wait_drain(&sm.tail, (tails - 1) & 1, p.status);
+      for (int d = 1; d <= kStages && d <= kv_it; ++d) {
+        const int i = kv_it - d;
+        mbar_wait_drain(&sm.k_full[i % kStages], (i / kStages) & 1, p.status);
+        if (i != unmarked) mbar_wait_drain(&sm.v_full[i % kStages], (i / kStages) & 1, p.status);
+      }
+      for (int d = 1; d <= kQ && d <= q_it; ++d)
+        mbar_wait_drain(&sm.q_full[(q_it - d) % kQ], ((q_it - d) / kQ) & 1, p.status);
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers
+    const int g = warp - 1;
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = pack_idesc<F16>(kTile, kTile, 0, 0);
+      constexpr uint32_t idesc_o = pack_idesc<F16>(kTile, D, 0, 1);
+      constexpr uint32_t kTile16 = (kSubs * kPackSub) >> 4;
+      const uint64_t qdesc0 = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+      const uint64_t kdesc = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+      const uint64_t vdesc = smem_desc_sw128(smem_u32(sm.v[0][0]), kPackSub, 1024);
+      const uint32_t dS = tmem + 128u * g, dO = tmem + 256u + D * g;
+      const uint32_t aP = kOwnP ? tmem + 384u + 64u * g : dS;
+      int q_it = 0, kv_it = 0, n_s = 0, n_p = 0, n_o = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kSlots;
+        if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+        const int head = sm.item[slot].head;
+        const PackEntry e = sm.item[slot].e;
+        mbar_arrive(&sm.item_empty[slot]);
+        if (head < 0) break;
+        int a[2], b[2];
+        fwd_range(e, 0, p.tpt, window, a[0], b[0]);
+        fwd_range(e, 1, p.tpt, window, a[1], b[1]);
+        const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
+        const bool mine = a[g] < b[g];
+        // Q tiles pass through one ring; the other issuer's tiles are released by that one
+        const int qi = q_it + (g == 1 && a[0] < b[0] ? 1 : 0), qs = qi % kQ;
+        q_it += (a[0] < b[0]) + (a[1] < b[1]);
+        const uint64_t qdesc = qdesc0 + static_cast<uint64_t>(qs * kTile16);
+        auto issue_s = [&](int kvi) -> bool {
+          const int s = kvi % kStages;
+          if (kOwnP && n_s > 0 && !mbar_wait(&sm.s_free[g], (n_s - 1) & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&sm.k_full[s], (kvi / kStages) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint64_t bk = kdesc + static_cast<uint64_t>(s * kTile16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_bf16_ss(dS, qdesc + kstep_off16(kk, kPackSub), bk + kstep_off16(kk, kPackSub), idesc_s, kk > 0);
+          tc_commit(&sm.s_full[g]);
+          ++n_s;
+          return true;
+        };
+        if (mine && !mbar_wait(&sm.q_full[qs], (qi / kQ) & 1, abort_flag, p.status)) break;
+        if (mine && a[g] == j0 && !issue_s(kv_it)) break;
+        bool first = true;
+        for (int j = j0; j < j1; ++j, ++kv_it) {
+          const int s = kv_it % kStages;
+          const bool now = j >= a[g] && j < b[g], next = j + 1 >= a[g] && j + 1 < b[g];
+          if (now) {
+            if (kOwnP && next && !issue_s(kv_it + 1)) { ok = false; break; }
+            if (!next) tc_commit(&sm.q_empty[qs]);  // the last S of this tile is issued
+            const int steps = min(kTile / 16, (e.m - j * kTile + 15) >> 4);
+            const uint64_t bv = vdesc + static_cast<uint64_t>(s * kTile16);
+            if (!mbar_wait(&sm.v_full[s], (kv_it / kStages) & 1, abort_flag, p.status)) { ok = false; break; }
+            if (first && !mbar_wait(&sm.o_empty[g], (n_o & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+            if (!mbar_wait(&sm.p_full[g][0], n_p & 1, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                mma_bf16_ts(dO, aP + kk * 8, bv + static_cast<uint64_t>(kk * 128), idesc_o, first && kk == 0 ? 0u : 1u);
+            if (!mbar_wait(&sm.p_full[g][1], n_p & 1, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              if (kk < steps) mma_bf16_ts(dO, aP + kk * 8, bv + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+            if (kOwnP) tc_commit(&sm.pv_done[g]);
+            first = false;
+            ++n_p;
+          } else {
+            // released only once it has landed: a run through tiles that are not
+            // this issuer's must not give both arrivals of a stage by itself
+            if (!mbar_wait(&sm.k_full[s], (kv_it / kStages) & 1, abort_flag, p.status)) { ok = false; break; }
+          }
+          tc_commit(&sm.kv_empty[s]);
+          if (next && (!kOwnP || !now) && !issue_s(kv_it + 1)) { ok = false; break; }
+        }
+        if (!ok) break;
+        if (mine) {
+          tc_commit(&sm.o_full[g]);
+          ++n_o;
+        }
+      }
+      tc_commit(&sm.drain[g]);
+      mbar_wait_drain(&sm.drain[g], 0, p.status);
+    }
+  }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_take<kRegsMany>();
+    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t colS = 128u * g, colO = 256u + D * g, colP = kOwnP ? 384u + 64u * g : colS;
+    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+    int n_s = 0, n_o = 0, n_sync = 0;
+    for (int it = 0;; ++it) {
+      const int slot = it % kSlots;
+      if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+      const int head = sm.item[slot].head;
+      const PackEntry e = sm.item[slot].e;
+      warp_arrive(&sm.item_empty[slot]);
+      if (head < 0) break;
+      int a, b;
+      fwd_range(e, g, p.tpt, window, a, b);
+      const int first = e.diag + g * p.tpt, n_tok = min(p.tpt, e.n_tok - g * p.tpt);
+      if (n_tok <= 0) continue;
+      const bool valid = r_tok < n_tok;
+      const int hi = valid ? first + r_tok : -1;           // the last key that the row sees
+      const int lo = window ? hi - window + 1 : INT_MIN;   // the first
+      float m = -INFINITY, l = 0.f;
+      float top = -INFINITY;  // largest score so far, log2 units
+      bool ok = true;
+      for (int j = a; j < b; ++j) {
+        if (!warp_wait(&sm.s_full[g], n_s & 1, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t sr[kTile];
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) tmem_ld32(lanes + colS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+        tmem_wait_ld();
+        tmem_ld_fence(sr);
+        if (kOwnP) {
+          tc_fence_before();
+          warp_arrive(&sm.s_free[g]);
+        }
+        const int k0 = j * kTile;
+        if (k0 + kTile - 1 > first) {  // keys that some row does not see
+          const int lim = hi - k0;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c > lim) sr[c] = 0xff800000u;
+        }
+        if (window && k0 < first + n_tok - window) {
+          const int lim = lo - k0;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c < lim) sr[c] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(sr[u]);
+#pragma unroll
+        for (int c = 4; c < kTile; c += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx[u] = max3f(mx[u], __uint_as_float(sr[c + 2 * u < kTile ? c + 2 * u : u]), __uint_as_float(sr[c + 2 * u + 1 < kTile ? c + 2 * u + 1 : u]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        top = fmaxf(top, mt);
+        const bool grown = mt > m + kGrow;
+        float alpha = 1.f;
+        if (grown) {
+          alpha = ex2_approx(m - mt);
+          m = mt;
+        }
+        float sub = m == -INFINITY ? 0.f : -m;
+        float sl = p.scale_log2;
+        if (__any_sync(0xffffffffu, fabsf(sub) > kFarScore)) {
+          // far from zero an fma would give the largest score its product's rounding as a weight: both rounded alike
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), sl), sub));
+          sl = 1.f, sub = 0.f;
+        }
+        if (kOwnP && n_s > 0) {
+          if (!warp_wait(&sm.pv_done[g], (n_s - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+        }
+        // O to the new reference (rare). The product before is complete: with
+        // P's own columns by the wait above, else because S came behind it
+        if (j > a && __any_sync(0xffffffffu, grown)) {
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t oo[32];
+            tmem_ld32(lanes + colO + cc * 32, oo);
+            tmem_wait_ld();
+            tmem_ld_fence(oo);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) oo[c] = __float_as_uint(__uint_as_float(oo[c]) * alpha);
+            tmem_st32(lanes + colO + cc * 32, oo);
+          }
+        }
+        const uint64_t sl2 = f2(sl, sl), sub2 = f2(sub, sub);
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            f2_split(fma2(f2(__uint_as_float(sr[q * 32 + c]), __uint_as_float(sr[q * 32 + c + 1])), sl2, sub2), x0, x1);
+            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+            sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], f2(x0, x1));
+            pk[c >> 1] = c4_pack<F16>(x0, x1);
+          }
+          tmem_st16(lanes + colP + q * 16, pk);
+          if (q & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&sm.p_full[g][q >> 1]);
+          }
+        }
+        float s0, s1;
+        f2_split(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+        l = fmaf(l, alpha, s0 + s1);
+        ++n_s;
+      }
+      if (!ok) break;
+      uint32_t acc[D / 32][32];
+      float round = 0.f;  // what the rounding of the largest weight adds to the sum
+      if (a < b) {
+        if (!warp_wait(&sm.o_full[g], n_o & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) tmem_ld32(lanes + colO + cc * 32, acc[cc]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) tmem_ld_fence(acc[cc]);
+        tc_fence_before();
+        warp_arrive(&sm.o_empty[g]);
+        ++n_o;
+        // the largest score's weight as the product saw it: a row with one key gives that row of V exactly
+        const float w = ex2_approx(top - m);
+        float w_r;
+        if (F16) w_r = __half2float(__float2half_rn(w));
+        else w_r = __bfloat162float(__float2bfloat16_rn(w));
+        if (l > 0.f) round = w_r - w;
+      } else {
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
+      }
+      if (e.slot >= 0) {
+        // leave this chunk's share; the last to arrive takes them all
+        const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * (D + 2);
+        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
+        float* const mine = base + e.chunk * stride;
+#pragma unroll
+        for (int c = 0; c < D / 4; ++c)
+          reinterpret_cast<float4*>(mine)[c * kTile + r] =
+              make_float4(__uint_as_float(acc[c / 8][c % 8 * 4]), __uint_as_float(acc[c / 8][c % 8 * 4 + 1]),
+                          __uint_as_float(acc[c / 8][c % 8 * 4 + 2]), __uint_as_float(acc[c / 8][c % 8 * 4 + 3]));
+        reinterpret_cast<float2*>(mine + kTile * D)[r] = make_float2(m, l);
+        __threadfence();
+        warp_arrive(&sm.sync[g]);
+        if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (r == 0) sm.last[g] = atomicAdd(p.arrivals + (static_cast<long long>(e.cut) * p.Hkv + head) * 2 + g, 1) == e.chunks - 1;
+        warp_arrive(&sm.sync[g]);
+        if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (!*reinterpret_cast<volatile int*>(&sm.last[g])) continue;
+        __threadfence();
+        m = -INFINITY, round = 0.f;
+        for (int c = 0; c < e.chunks; ++c) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r).x);
+        l = 0.f;
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
+        for (int c = 0; c < e.chunks; ++c) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r);
+          const float f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2_approx(ml.x - m);
+          l = fmaf(ml.y, f, l);
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(base + c * stride) + i * kTile + r);
+            uint32_t* y = &acc[i / 8][i % 8 * 4];
+            y[0] = __float_as_uint(fmaf(x.x, f, __uint_as_float(y[0]))), y[1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(y[1])));
+            y[2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(y[2]))), y[3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(y[3])));
+          }
+        }
+      }
+      if (valid) {
+        const float inv = l > 0.f ? 1.f / (l + round) : l == 0.f ? 0.f : l;
+        const long long tok = e.q0 + g * p.tpt + r_tok;
+        const int qh = head * p.G + r_head;
+        uint4* dst = reinterpret_cast<uint4*>(p.o + tok * p.ot + qh * p.oh);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t* y = &acc[c / 4][c % 4 * 8];
+          uint32_t u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            u[i] = c4_pack<F16>(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
+          dst[c] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        p.lse[tok * p.Hq + qh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const PFwdParams& p, int grid, cudaStream_t st) {
+  static bool allowed[64] = {};  // by device; setting it twice does no harm
+  constexpr size_t smem = sizeof(PFwdSmem<D>) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory per CTA");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {
+    e = cudaFuncSetAttribute(packed_fwd_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  packed_fwd_kernel<D, F16><<<grid, kThreads, smem, st>>>(q, k, v, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace scfa
+
+using namespace scfa;
+
+extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, long long q_head, const uint16_t* k, long long k_token,
+                                       long long k_head, const uint16_t* v, long long v_token, long long v_head,
+                                       const void* plan, size_t plan_bytes, int N, int M, int Hq, int Hkv, int D, float scale,
+                                       int dtype, uint16_t* o, long long o_token, long long o_head, float* lse, void* ws,
+                                       size_t ws_bytes, unsigned flags, void* stream) {
+  if (!plan || !ws || N < 0 || M < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return SCFA_ERR_INVALID;
+  const float factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // to log2 units
+  if (!(scale > 0.f && factor < INFINITY)) return SCFA_ERR_INVALID;
+  if ((D != 64 && D != 128) || (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) || Hq / Hkv > kTile) return SCFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * Hq >= (1ll << 31) - 256 || static_cast<long long>(M) * Hkv >= (1ll << 31) - 256) return SCFA_ERR_UNSUPPORTED;
+  const int sms = num_sms();
+  const PackWs w = pack_ws(false, D, sms);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.stats) return SCFA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < sizeof(PackHeader)) return SCFA_ERR_INVALID;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N > 0 && (!lse || !pack_rows_ok(q, q_token, q_head, N, Hq) || !o || (reinterpret_cast<uintptr_t>(o) & 15u) ||
+                ((o_token | o_head) & 7) || c4_rows_overlap(o_token, o_head, N, Hq, D)))
+    return SCFA_ERR_INVALID;
+  if (M > 0 && (!pack_rows_ok(k, k_token, k_head, M, Hkv) || !pack_rows_ok(v, v_token, v_head, M, Hkv))) return SCFA_ERR_INVALID;
+  char* c = static_cast<char*>(ws);
+  if (cudaMemsetAsync(c, 0, w.clear, st) != cudaSuccess) return SCFA_ERR_CUDA;
+  if (N == 0) return SCFA_OK;
+  PFwdParams p = {};
+  p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
+  p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.scale_log2 = factor;
+  p.o = o, p.ot = o_token, p.oh = o_head, p.lse = lse;
+  p.counter = reinterpret_cast<int*>(c + w.counters), p.arrivals = p.counter + 2;
+  p.part = reinterpret_cast<float*>(c + w.part);
+  p.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0, p.status = reinterpret_cast<int*>(c);
+  const bool f16 = dtype == SCFA_DTYPE_F16;
+  CUtensorMap tq, tk, tv;
+  // without keys every row is empty and no K or V is ever copied: any valid map will do
+  if (!make_tmap_rows(&tq, q, f16, D, Hq, N, q_head, q_token, p.G, p.tpt)) return SCFA_ERR_INVALID;
+  if (M > 0 ? !make_tmap_rows(&tk, k, f16, D, Hkv, M, k_head, k_token, 1, kTile) || !make_tmap_rows(&tv, v, f16, D, Hkv, M, v_head, v_token, 1, kTile)
+            : (tk = tv = tq, false))
+    return SCFA_ERR_INVALID;
+  const cudaError_t e = D == 64 ? (f16 ? launch<64, true>(tq, tk, tv, p, sms, st) : launch<64, false>(tq, tk, tv, p, sms, st))
+                                : (f16 ? launch<128, true>(tq, tk, tv, p, sms, st) : launch<128, false>(tq, tk, tv, p, sms, st));
+  if (e != cudaSuccess) return SCFA_ERR_CUDA;
+  if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
+  return SCFA_OK;
+}

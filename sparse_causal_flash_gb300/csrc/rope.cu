@@ -1,0 +1,426 @@
+// Rotary positions of query and key rows, with the root-mean-square norm that may stand before them, and the gradients.
+//
+// A row x of D channels at position p: with a norm, n = x / sqrt(mean(x^2) + eps) and x becomes n w. Of the first `rot`
+// channels pair i turns by p f[i] radians: (a, b) -> factor (a cos - b sin, b cos + a sin). A rotation's transpose turns
+// back, so with g = the gradient turned back (times factor), dw = sum over rows of g n and
+// dx = (g w - n mean(g w n)) / sqrt(mean(x^2) + eps).
+//
+// Angles. f[i] comes as a whole number F of 2^-64 turns, so p F mod 2^64 is the angle modulo one turn with no error at
+// all; its high 32 bits (2^-32 of a turn) become an fp32 angle in [-pi, pi) for the hardware's sine and cosine (error
+// below 2^-20), below the rounding of the 16-bit rows. With fp32 angles position 10^6 would be off by 0.06 radians.
+//
+// One row is held by D / 16 threads, each with two 16-byte pieces such that both halves of its eight pairs are its own:
+// a norm is a few shuffles, and a row may be turned in place. What bounds it is HBM: each row is read once and written
+// once (gradients with a norm: two read, one written). A thread turns up to four heads of a token with one set of sines
+// (they cost 100 lane operations, a row's other work some 80), all loads before the first use.
+#include "cache4.cuh"
+#include "internal.h"
+
+namespace scfa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+enum { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };  // kHalfOdd: halves that do not fall on 16-byte pieces
+
+struct RopeSide {
+  const uint16_t *x, *dy;  // forward: x only; backward without a norm: the gradient as x
+  uint16_t* y;
+  long long xt, xh, dyt, dyh, yt, yh;
+  const float* w;
+  float* dw;
+  int H, slices, blocks;  // heads; units per token; CTAs of this side
+};
+struct RopeArgs {
+  RopeSide side[2];
+  const int32_t* pos;
+  const uint64_t* table;
+  float* part;  // [CTA][D] partial dw
+  int N, rot;
+  float factor, eps, turn;  // turn: +-2 pi / 2^32
+};
+
+// The eight pairs of thread t of a row: slot(i) numbers them, 0 .. rot / 2 are turned; a(i), b(i) are their channels.
+template <int D, int KIND>
+struct RopeMap {
+  int t, rot;
+  __device__ __forceinline__ int piece(int j) const {  // 16-byte piece j of the thread's two
+    constexpr int T = D / 16;
+    if (KIND == kInterleaved) return t + j * T;
+    const int n = rot >> 4;  // pieces of a half
+    return t < n ? t + j * n : 2 * t + j;
+  }
+  __device__ __forceinline__ int slot(int i) const {
+    constexpr int T = D / 16;
+    if (KIND == kInterleaved) return piece(i >> 2) * 4 + (i & 3);
+    if (KIND == kHalfOdd) return t + i * T;
+    return t * 8 + i;
+  }
+  __device__ __forceinline__ int a(int i) const {
+    const int s = slot(i), h = rot >> 1;
+    if (KIND == kInterleaved) return 2 * s;
+    if (KIND == kHalfOdd) return s < h ? s : 2 * s;
+    return piece(0) * 8 + i;
+  }
+  __device__ __forceinline__ int b(int i) const {
+    const int s = slot(i), h = rot >> 1;
+    if (KIND == kInterleaved) return 2 * s + 1;
+    if (KIND == kHalfOdd) return s < h ? s + h : 2 * s + 1;
+    return piece(1) * 8 + i;
+  }
+};
+
+struct RopeRaw {
+  uint32_t w[8];
+};
+
+template <int D, bool F16, int KIND>
+__device__ __forceinline__ RopeRaw rope_load(const uint16_t* row, const RopeMap<D, KIND>& m) {
+  RopeRaw r;
+  if (KIND == kHalfOdd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = row[m.a(i)] | static_cast<uint32_t>(row[m.b(i)]) << 16;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + m.piece(0) * 8);
+    const uint4 v = *reinterpret_cast<const uint4*>(row + m.piece(1) * 8);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w, r.w[4] = v.x, r.w[5] = v.y, r.w[6] = v.z, r.w[7] = v.w;
+  }
+  return r;
+}
+// words of (channel, next channel) or, for halves on pieces, of (pair, next pair) -> pairs
+template <int D, bool F16, int KIND>
+__device__ __forceinline__ void rope_unpack(const RopeRaw& r, float (&a)[8], float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = c4_unpack<F16>(r.w[i]);
+    if (KIND == kHalf) {
+      float* z = i < 4 ? a : b;
+      z[(i & 3) * 2] = f.x, z[(i & 3) * 2 + 1] = f.y;
+    } else {
+      a[i] = f.x, b[i] = f.y;
+    }
+  }
+}
+template <int D, bool F16, int KIND>
+__device__ __forceinline__ void rope_store(uint16_t* row, const RopeMap<D, KIND>& m, const float (&a)[8], const float (&b)[8]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float* z = i < 4 ? a : b;
+    w[i] = KIND == kHalf ? c4_pack<F16>(z[(i & 3) * 2], z[(i & 3) * 2 + 1]) : c4_pack<F16>(a[i], b[i]);
+  }
+  if (KIND == kHalfOdd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) row[m.a(i)] = static_cast<uint16_t>(w[i]), row[m.b(i)] = static_cast<uint16_t>(w[i] >> 16);
+  } else {
+    *reinterpret_cast<uint4*>(row + m.piece(0) * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(row + m.piece(1) * 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float rope_row_sum(float x) {
+#pragma unroll
+  for (int o = D / 32; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// cosine and sine of each pair, times factor; 1 and 0 where a pair is not turned
+template <int D, int KIND>
+__device__ __forceinline__ void rope_angles(const RopeArgs& g, const RopeMap<D, KIND>& m, int pos, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = m.slot(i);
+    c[i] = 1.f, s[i] = 0.f;
+    if (k < g.rot >> 1) {
+      const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(g.table) + k);
+      const uint32_t lo = static_cast<uint32_t>(f), hi = static_cast<uint32_t>(f >> 32), p = static_cast<uint32_t>(pos);
+      // bits 32..63 of the signed position times f
+      const uint32_t z = p * hi + __umulhi(p, lo) - (pos < 0 ? lo : 0u);
+      const float t = static_cast<float>(static_cast<int32_t>(z)) * g.turn;
+      c[i] = __cosf(t) * g.factor;
+      s[i] = __sinf(t) * g.factor;
+    }
+  }
+}
+
+// Forward, and the gradient without a norm (turn < 0). One unit is HP heads of one token.
+template <int D, bool F16, int KIND, bool NORM, int HP>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs g) {
+  constexpr int T = D / 16;
+  const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
+  const RopeSide& sd = g.side[si];
+  const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
+  const long long unit = static_cast<long long>(block) * (kRopeThreads / T) + threadIdx.x / T;
+  const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
+  const bool live = tok_ < g.N;
+  const int tok = live ? tok_ : g.N - 1;
+  RopeMap<D, KIND> m;
+  m.t = threadIdx.x % T, m.rot = g.rot;
+  RopeRaw raw[HP];
+#pragma unroll
+  for (int u = 0; u < HP; ++u)
+    raw[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + min(h0 + u, sd.H - 1) * sd.xh, m);
+  float c[8], s[8];
+  rope_angles(g, m, __ldg(g.pos + tok), c, s);
+#pragma unroll
+  for (int u = 0; u < HP; ++u) {
+    float a[8], b[8];
+    rope_unpack<D, F16, KIND>(raw[u], a, b);
+    if (NORM) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+      const float r = rsqrtf(fmaf(rope_row_sum<D>(ss), 1.f / D, g.eps));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] *= r * __ldg(sd.w + m.a(i)), b[i] *= r * __ldg(sd.w + m.b(i));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = a[i];
+      a[i] = fmaf(x, c[i], -b[i] * s[i]);
+      b[i] = fmaf(b[i], c[i], x * s[i]);
+    }
+    if (live && h0 + u < sd.H) rope_store<D, F16, KIND>(sd.y + tok * sd.yt + (h0 + u) * sd.yh, m, a, b);
+  }
+}
+
+// Gradients with a norm. A CTA takes every side.blocks-th unit and keeps its sum of dw in registers, which it leaves in
+// `part`: rows are summed in an order that the sizes alone decide.
+template <int D, bool F16, int KIND, int HP>
+__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs g) {
+  constexpr int T = D / 16;
+  __shared__ float s_dw[kRopeThreads / 32][D];
+  const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
+  const RopeSide& sd = g.side[si];
+  const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
+  RopeMap<D, KIND> m;
+  m.t = threadIdx.x % T, m.rot = g.rot;
+  float wa[8], wb[8], da[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wa[i] = __ldg(sd.w + m.a(i)), wb[i] = __ldg(sd.w + m.b(i)), da[i] = db[i] = 0.f;
+  const long long units = static_cast<long long>(g.N) * sd.slices;
+  for (long long first = static_cast<long long>(block) * (kRopeThreads / T); first < units;
+       first += static_cast<long long>(sd.blocks) * (kRopeThreads / T)) {
+    const long long unit = first + threadIdx.x / T;
+    const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
+    const bool live = tok_ < g.N;
+    const int tok = live ? tok_ : g.N - 1;
+    RopeRaw rx[HP], rd[HP];
+#pragma unroll
+    for (int u = 0; u < HP; ++u) {
+      const int h = min(h0 + u, sd.H - 1);
+      rx[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + h * sd.xh, m);
+      rd[u] = rope_load<D, F16, KIND>(sd.dy + tok * sd.dyt + h * sd.dyh, m);
+    }
+    float c[8], s[8];
+    rope_angles(g, m, __ldg(g.pos + tok), c, s);
+#pragma unroll
+    for (int u = 0; u < HP; ++u) {
+      float xa[8], xb[8], ga[8], gb[8];
+      rope_unpack<D, F16, KIND>(rx[u], xa, xb);
+      rope_unpack<D, F16, KIND>(rd[u], ga, gb);
+      float ss = 0.f, dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = ga[i];
+        ga[i] = fmaf(y, c[i], -gb[i] * s[i]);
+        gb[i] = fmaf(gb[i], c[i], y * s[i]);
+        ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
+        dot = fmaf(ga[i] * wa[i], xa[i], fmaf(gb[i] * wb[i], xb[i], dot));
+      }
+      const float r = rsqrtf(fmaf(rope_row_sum<D>(ss), 1.f / D, g.eps));
+      const float k = rope_row_sum<D>(dot) * r * r * (1.f / D);
+      if (live && h0 + u < sd.H) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          da[i] = fmaf(ga[i], xa[i] * r, da[i]), db[i] = fmaf(gb[i], xb[i] * r, db[i]);
+          ga[i] = r * fmaf(ga[i], wa[i], -xa[i] * k);
+          gb[i] = r * fmaf(gb[i], wb[i], -xb[i] * k);
+        }
+        rope_store<D, F16, KIND>(sd.y + tok * sd.yt + (h0 + u) * sd.yh, m, ga, gb);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = T; o < 32; o <<= 1) {
+      da[i] += __shfl_xor_sync(0xffffffffu, da[i], o);
+      db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
+    }
+    if ((threadIdx.x & 31) < T) s_dw[threadIdx.x >> 5][m.a(i)] = da[i], s_dw[threadIdx.x >> 5][m.b(i)] = db[i];
+  }
+  __syncthreads();
+  for (int ch = threadIdx.x; ch < D; ch += kRopeThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRopeThreads / 32; ++i) v += s_dw[i][ch];
+    g.part[static_cast<long long>(blockIdx.x) * D + ch] = v;
+  }
+  __syncthreads();
+  grid_release();
+}
+
+// dw[ch] = sum of the CTAs' partial sums: CTA (x, side) takes 8 channels, 32 threads share a channel's column.
+template <int D>
+__global__ void __launch_bounds__(256) rope_dw_kernel(const __grid_constant__ RopeArgs g) {
+  const RopeSide& sd = g.side[blockIdx.y];
+  __shared__ float s_v[32][9];
+  const int ch = blockIdx.x * 8 + threadIdx.x % 8, lane = threadIdx.x / 8;
+  grid_wait();
+  const float* part = g.part + static_cast<long long>(blockIdx.y ? g.side[0].blocks : 0) * D + ch;
+  float v = 0.f;
+  for (int i = lane; i < sd.blocks; i += 32) v += part[static_cast<long long>(i) * D];
+  s_v[lane][threadIdx.x % 8] = v;
+  __syncthreads();
+  if (threadIdx.x < 8 && sd.H > 0) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += s_v[i][threadIdx.x];
+    sd.dw[ch] = v;
+  }
+}
+
+// CTAs of the gradient with a norm, by what fills the GPU: 4 per SM, no more than there is work for.
+constexpr int kBwdHeads = 2;
+int rope_bwd_ctas(int N, int H, int D, int most) {
+  if (H == 0) return 0;
+  const long long n = (static_cast<long long>(N) * ((H + kBwdHeads - 1) / kBwdHeads) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
+  return static_cast<int>(n < most ? n : most);
+}
+int rope_most_ctas() { return 4 * num_sms(); }
+
+template <int D, bool F16, int KIND>
+cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
+  constexpr int T = D / 16;
+  if (bwd && norm) {
+    const int most = rope_most_ctas(), H = g.side[0].H + g.side[1].H;
+    for (RopeSide& s : g.side) {
+      s.slices = (s.H + kBwdHeads - 1) / kBwdHeads;
+      s.blocks = rope_bwd_ctas(g.N, s.H, D, s.H ? (most * s.H + H - 1) / H : 0);
+    }
+    rope_bwd_kernel<D, F16, KIND, kBwdHeads><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, 0, st>>>(g);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_behind(rope_dw_kernel<D>, dim3(D / 8, g.side[1].H ? 2 : 1), 256, st, g);
+  }
+  // Four heads a thread once one head each fills the GPU twice over.
+  const bool many = static_cast<long long>(g.N) * (g.side[0].H + g.side[1].H) * T > 2ll * 2048 * num_sms();
+  for (RopeSide& s : g.side) {
+    s.slices = many ? (s.H + 3) / 4 : s.H;
+    s.blocks = static_cast<int>((static_cast<long long>(g.N) * s.slices * T + kRopeThreads - 1) / kRopeThreads);
+  }
+  const int grid = g.side[0].blocks + g.side[1].blocks;
+  if (norm)
+    many ? rope_kernel<D, F16, KIND, true, 4><<<grid, kRopeThreads, 0, st>>>(g)
+         : rope_kernel<D, F16, KIND, true, 1><<<grid, kRopeThreads, 0, st>>>(g);
+  else
+    many ? rope_kernel<D, F16, KIND, false, 4><<<grid, kRopeThreads, 0, st>>>(g)
+         : rope_kernel<D, F16, KIND, false, 1><<<grid, kRopeThreads, 0, st>>>(g);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t rope_launch_d(RopeArgs& g, bool bwd, bool norm, bool f16, int interleaved, cudaStream_t st) {
+  if (interleaved) return f16 ? rope_launch<D, true, kInterleaved>(g, bwd, norm, st) : rope_launch<D, false, kInterleaved>(g, bwd, norm, st);
+  if (g.rot % 16) return f16 ? rope_launch<D, true, kHalfOdd>(g, bwd, norm, st) : rope_launch<D, false, kHalfOdd>(g, bwd, norm, st);
+  return f16 ? rope_launch<D, true, kHalf>(g, bwd, norm, st) : rope_launch<D, false, kHalf>(g, bwd, norm, st);
+}
+
+scfa_status rope_rows(const void* p, long long token, long long head) {
+  return !p || (reinterpret_cast<uintptr_t>(p) & 15u) || ((token | head) & 7) ? SCFA_ERR_INVALID : SCFA_OK;
+}
+
+// what both directions check
+scfa_status rope_check(const void* pos, const void* table, int N, int Hq, int Hkv, int D, int rot, int interleaved, float factor,
+                       float eps, int dtype) {
+  if (!pos || N < 0 || Hq < 1 || Hkv < 0 || rot < 0 || rot > D || (rot & 1) || (rot > 0 && !table)) return SCFA_ERR_INVALID;
+  if (interleaved != 0 && interleaved != 1) return SCFA_ERR_INVALID;
+  if (!(factor > -INFINITY && factor < INFINITY) || !(eps >= 0.f && eps < INFINITY)) return SCFA_ERR_INVALID;
+  if (D != 64 && D != 128) return SCFA_ERR_UNSUPPORTED;
+  if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * (static_cast<long long>(Hq) + Hkv) >= (1ll << 31) - 256) return SCFA_ERR_UNSUPPORTED;
+  return SCFA_OK;
+}
+
+RopeArgs rope_args(const int32_t* pos, const uint64_t* table, int N, int rot, float factor, float eps, bool back) {
+  RopeArgs g = {};
+  g.pos = pos, g.table = table, g.N = N, g.rot = rot, g.factor = factor, g.eps = eps;
+  g.turn = (back ? -1.f : 1.f) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  return g;
+}
+
+}  // namespace
+}  // namespace scfa
+
+using namespace scfa;
+
+extern "C" {
+
+scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head, const uint16_t* k, long long k_token,
+                          long long k_head, const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D, int rot,
+                          int interleaved, float factor, const float* wq, const float* wk, float eps, int dtype,
+                          uint16_t* q_out, long long qo_token, long long qo_head, uint16_t* k_out, long long ko_token,
+                          long long ko_head, void* stream) {
+  if (scfa_status e = rope_check(pos, table, N, Hq, Hkv, D, rot, interleaved, factor, eps, dtype)) return e;
+  const bool norm = wq != nullptr;
+  if (norm ? Hkv > 0 && !wk : wk != nullptr) return SCFA_ERR_INVALID;
+  if (N == 0) return SCFA_OK;
+  if (rope_rows(q, q_token, q_head) || rope_rows(q_out, qo_token, qo_head) || c4_rows_overlap(qo_token, qo_head, N, Hq, D))
+    return SCFA_ERR_INVALID;
+  if (Hkv > 0 && (rope_rows(k, k_token, k_head) || rope_rows(k_out, ko_token, ko_head) || c4_rows_overlap(ko_token, ko_head, N, Hkv, D)))
+    return SCFA_ERR_INVALID;
+  RopeArgs g = rope_args(pos, table, N, rot, factor, eps, false);
+  g.side[0] = {q, nullptr, q_out, q_token, q_head, 0, 0, qo_token, qo_head, wq, nullptr, Hq, 0, 0};
+  g.side[1] = {k, nullptr, k_out, k_token, k_head, 0, 0, ko_token, ko_head, wk, nullptr, Hkv, 0, 0};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == SCFA_DTYPE_F16;
+  const cudaError_t e = D == 64 ? rope_launch_d<64>(g, false, norm, f16, interleaved, st)
+                                : rope_launch_d<128>(g, false, norm, f16, interleaved, st);
+  return e == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
+size_t scfa_rope_workspace_size(int N, int Hq, int Hkv, int D) {
+  if (N < 0 || Hq < 1 || Hkv < 0 || (D != 64 && D != 128)) return 0;
+  return align_up(static_cast<size_t>(rope_most_ctas() + 2) * D * sizeof(float), 256);
+}
+
+scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_head, const uint16_t* dk, long long dk_token,
+                          long long dk_head, const uint16_t* q, long long q_token, long long q_head, const uint16_t* k,
+                          long long k_token, long long k_head, const int32_t* pos, const uint64_t* table, int N, int Hq,
+                          int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk, float eps,
+                          int dtype, uint16_t* dq_out, long long dqo_token, long long dqo_head, uint16_t* dk_out,
+                          long long dko_token, long long dko_head, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+                          void* stream) {
+  if (scfa_status e = rope_check(pos, table, N, Hq, Hkv, D, rot, interleaved, factor, eps, dtype)) return e;
+  const bool norm = wq != nullptr;
+  if (norm ? !dwq || (Hkv > 0 && (!wk || !dwk)) : wk || dwq || dwk) return SCFA_ERR_INVALID;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) {
+    if (!norm) return SCFA_OK;
+    cudaError_t e = cudaMemsetAsync(dwq, 0, D * sizeof(float), st);
+    if (e == cudaSuccess && Hkv > 0) e = cudaMemsetAsync(dwk, 0, D * sizeof(float), st);
+    return e == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+  }
+  if (rope_rows(dq, dq_token, dq_head) || rope_rows(dq_out, dqo_token, dqo_head) || c4_rows_overlap(dqo_token, dqo_head, N, Hq, D))
+    return SCFA_ERR_INVALID;
+  if (Hkv > 0 && (rope_rows(dk, dk_token, dk_head) || rope_rows(dk_out, dko_token, dko_head) || c4_rows_overlap(dko_token, dko_head, N, Hkv, D)))
+    return SCFA_ERR_INVALID;
+  RopeArgs g = rope_args(pos, table, N, rot, factor, eps, true);
+  if (norm) {
+    if (rope_rows(q, q_token, q_head) || (Hkv > 0 && rope_rows(k, k_token, k_head))) return SCFA_ERR_INVALID;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < scfa_rope_workspace_size(N, Hq, Hkv, D)) return SCFA_ERR_WORKSPACE;
+    g.side[0] = {q, dq, dq_out, q_token, q_head, dq_token, dq_head, dqo_token, dqo_head, wq, dwq, Hq, 0, 0};
+    g.side[1] = {k, dk, dk_out, k_token, k_head, dk_token, dk_head, dko_token, dko_head, wk, dwk, Hkv, 0, 0};
+    g.part = static_cast<float*>(ws);
+  } else {
+    g.side[0] = {dq, nullptr, dq_out, dq_token, dq_head, 0, 0, dqo_token, dqo_head, nullptr, nullptr, Hq, 0, 0};
+    g.side[1] = {dk, nullptr, dk_out, dk_token, dk_head, 0, 0, dko_token, dko_head, nullptr, nullptr, Hkv, 0, 0};
+  }
+  const bool f16 = dtype == SCFA_DTYPE_F16;
+  const cudaError_t e = D == 64 ? rope_launch_d<64>(g, true, norm, f16, interleaved, st)
+                                : rope_launch_d<128>(g, true, norm, f16, interleaved, st);
+  return e == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
+}  // extern "C"
