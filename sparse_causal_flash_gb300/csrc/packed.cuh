@@ -122,6 +122,58 @@ __host__ __device__ constexpr uint32_t pack_idesc(int M, int N, int a_mn, int b_
   return F16 ? (idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10))) : idesc_bf16_f32(M, N, a_mn, b_mn);
 }
 
+// One lane of a whole warp, by the instruction that the compiler knows as such: code under it may keep its operands in
+// uniform registers, as MMAs want them (under `lane == 0` a 128 x 128 x 16 MMA took XXX cycles to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// MMAs whose operands lie at a fixed distance (OFF, in 16-byte units) from a descriptor of which only the low word
+// changes: the distance is added inside, so that one word per operand is all that has to reach the uniform registers.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 bytes, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((lbo_bytes >> 4) & 0x3FFFu) << 16);
+}
+template <int A_OFF, int B_OFF>
+__device__ __forceinline__ void mma_ss_at(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\tmov.b64 a, {x, %7};\n\tmov.b64 b, {y, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(A_OFF), "n"(B_OFF), "n"(kDescHigh) : "memory");
+}
+// A in tensor memory, A_COL columns from a_tmem
+template <int A_COL, int B_OFF>
+__device__ __forceinline__ void mma_ts_at(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\tmov.b64 b, {y, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(A_COL), "n"(B_OFF), "n"(kDescHigh) : "memory");
+}
+// Steps KK .. END of a product over K-major operands in shared memory (64-channel sub-tiles), 16 channels a step.
+template <int KK, int END>
+__device__ __forceinline__ void mma_ss_steps(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool add_to) {
+  if constexpr (KK < END) {
+    constexpr int off = static_cast<int>(kstep_off16(KK, kPackSub));
+    mma_ss_at<off, off>(d_tmem, a_low, b_low, idesc, KK > 0 || add_to ? 1u : 0u);
+    mma_ss_steps<KK + 1, END>(d_tmem, a_low, b_low, idesc, add_to);
+  }
+}
+// Steps KK .. END of a product whose A (16 bits, K pairs along the columns) is in tensor memory and whose B has its rows
+// along K in shared memory, 16 rows a step; `steps` of all of them hold something.
+template <int KK, int END>
+__device__ __forceinline__ void mma_ts_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add_to, int steps) {
+  if constexpr (KK < END) {
+    if (KK < steps) mma_ts_at<KK * 8, KK * 128>(d_tmem, a_tmem, b_low, idesc, KK > 0 || add_to ? 1u : 0u);
+    mma_ts_steps<KK + 1, END>(d_tmem, a_tmem, b_low, idesc, add_to, steps);
+  }
+}
+
 // one arrival for a warp, behind all its lanes' work
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -131,6 +183,64 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
   const bool ok = mbar_wait(bar, parity, abort_flag, status);
   return __all_sync(0xffffffffu, ok);
+}
+
+// 16 lanes x 64 columns: r[4 i + 2 u + v] is lane (lane / 4 + 8 u), column 8 i + 2 (lane % 4) + v
+__device__ __forceinline__ void tmem_ld_quad(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_quad(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      :: "r"(taddr),
+         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// the same of 32 columns
+__device__ __forceinline__ void tmem_ld_quad16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_quad16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr),
+         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 16 lanes x 32 columns: r[2 i + u] is lane (lane / 4 + 8 u), column 4 i + lane % 4
+__device__ __forceinline__ void tmem_st_quad_half(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr),
+         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float pack_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Registers of a warpgroup's threads, which all of its warps change together: fewer, or more of what others gave up.

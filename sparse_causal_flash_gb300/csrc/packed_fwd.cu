@@ -9,7 +9,7 @@
 // One CTA per SM, work from a counter, longest first. A work item is two tiles of query rows of one key head that share
 // each K and V tile. Roles:
 //   warp 0        producer: TMA of the item's two Q tiles and of K_j, V_j into rings
-//   warps 1, 2    MMA issuers of tile 0 and 1: S = Q K^T, then O += P V with P read from TMEM, in two halves of the keys
+//   warp 1        MMA issuer: S = Q K^T, then O += P V with P read from TMEM, in two halves of the keys
 //   warps 4-7, 8-11  softmax of tile 0 and 1: thread = row = TMEM lane; a row's 128 scores stay in its registers (216 of
 //                 them; the first four warps give up what they do not need)
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 behind it. At D = 128 that is all of it and P_g takes the first
@@ -21,6 +21,7 @@
 // Entries that the plan cut leave (O, m, l) in the workspace; the last of an entry's chunks to arrive joins them in the
 // order of the chunks, so results do not depend on which it was.
 #include <climits>
+#include <type_traits>
 
 #include "packed.cuh"
 
@@ -30,7 +31,7 @@ namespace {
 constexpr int kThreads = 384;
 // registers of a thread of warps 0-3 and of the softmax warps: 128 x 72 + 256 x 216 = 384 x 168, what the CTA starts with
 constexpr int kRegsFew = 72, kRegsMany = 216;
-constexpr int kSlots = 2;  // items known ahead
+constexpr int kSlots = 3;  // items known ahead
 constexpr float kGrow = 8.f;
 constexpr float kFarScore = 65536.f;
 
@@ -55,8 +56,8 @@ struct __align__(1024) PFwdSmem {
   uint8_t k[C::kStages][C::kSubs][kPackSub];
   uint8_t v[C::kStages][C::kSubs][kPackSub];
   PItem item[kSlots];
-  uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kStages], v_full[C::kStages], kv_empty[C::kStages];
-  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2], sync[2];
+  uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kStages], v_full[C::kStages], k_empty[C::kStages], v_empty[C::kStages];
+  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain, sync[2];
   uint64_t tail, item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
   int abort_flag, last[2];
@@ -110,15 +111,15 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQ; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.v_full[s], 1), mbar_init(&sm.kv_empty[s], 2);
+    for (int s = 0; s < kStages; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.v_full[s], 1), mbar_init(&sm.k_empty[s], 1), mbar_init(&sm.v_empty[s], 1);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1), mbar_init(&sm.s_free[g], 4);
       mbar_init(&sm.p_full[g][0], 4), mbar_init(&sm.p_full[g][1], 4);
       mbar_init(&sm.pv_done[g], 1), mbar_init(&sm.o_full[g], 1), mbar_init(&sm.o_empty[g], 4);
-      mbar_init(&sm.drain[g], 1), mbar_init(&sm.sync[g], 4);
+      mbar_init(&sm.sync[g], 4);
     }
-    mbar_init(&sm.tail, 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 2 + 8);
+    mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
@@ -139,7 +140,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListFwd]);
-    int q_it = 0, kv_it = 0, tails = 0, unmarked = -1;  // unmarked: V tile whose zeros an abort kept from being written
+    int q_it = 0, k_it = 0, kv_it = 0, tails = 0, unmarked = -1;  // unmarked: V tile whose zeros an abort kept from being written
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int slot = it % kSlots;
@@ -171,17 +172,23 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         ++q_it;
       }
-      if (p.stall && kv_it == 0 && a[0] + b[0] + a[1] + b[1] > 0) break;  // debug stall: no K / V load ever arrives
+      if (p.stall && k_it == 0 && a[0] + b[0] + a[1] + b[1] > 0) break;  // debug stall: no K / V load ever arrives
       const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
       for (int j = j0; j < j1 && ok; ++j) {
         const int s = kv_it % kStages;
-        ok = warp_wait(&sm.kv_empty[s], ((kv_it / kStages) & 1) ^ 1, abort_flag, p.status);
-        if (!ok) break;
+        const uint32_t free = ((kv_it / kStages) & 1) ^ 1;
         const int valid = e.m - j * kTile;  // keys of the sequence in the tile, if below 128
         const bool cut = valid < kTile && (valid & 15) != 0;
+        ok = warp_wait(&sm.k_empty[s], free, abort_flag, p.status);
+        if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.k_full[s], D * kTile * 2);
           for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.k[s][sub], &tm_k, &sm.k_full[s], sub * 64, head, e.k0 + j * kTile);
+        }
+        ++k_it;
+        ok = warp_wait(&sm.v_empty[s], free, abort_flag, p.status);
+        if (!ok) break;
+        if (lane == 0) {
           uint64_t* const vb = cut ? &sm.tail : &sm.v_full[s];
           mbar_arrive_expect_tx(vb, D * kTile * 2);
           for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.v[s][sub], &tm_v, vb, sub * 64, head, e.k0 + j * kTile);
@@ -203,100 +210,104 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (lane == 0) {
       // every copy issued has landed before the CTA exits, also after an abort
       if (tails > 0) mbar_wait_drain(&sm.tail, (tails - 1) & 1, p.status);
+      for (int d = 1; d <= kStages && d <= k_it; ++d)
+        mbar_wait_drain(&sm.k_full[(k_it - d) % kStages], ((k_it - d) / kStages) & 1, p.status);
       for (int d = 1; d <= kStages && d <= kv_it; ++d) {
         const int i = kv_it - d;
-        mbar_wait_drain(&sm.k_full[i % kStages], (i / kStages) & 1, p.status);
         if (i != unmarked) mbar_wait_drain(&sm.v_full[i % kStages], (i / kStages) & 1, p.status);
       }
       for (int d = 1; d <= kQ && d <= q_it; ++d)
         mbar_wait_drain(&sm.q_full[(q_it - d) % kQ], ((q_it - d) / kQ) & 1, p.status);
     }
-  } else if (warp == 1 || warp == 2) {
-    // ------------------------------------------------------------ MMA issuers
-    const int g = warp - 1;
-    if (lane == 0) {
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    // One thread issues for both tiles, in turns: tile 0's products come whole
+    // before tile 1's, which keeps one tile's softmax under the other's
+    // products. (With a thread for each, the two fell into step: both in the
+    // softmax, then both waiting for the tensor cores; 533 us instead of XXX.)
+    if (elect_one()) {
       constexpr uint32_t idesc_s = pack_idesc<F16>(kTile, kTile, 0, 0);
       constexpr uint32_t idesc_o = pack_idesc<F16>(kTile, D, 0, 1);
       constexpr uint32_t kTile16 = (kSubs * kPackSub) >> 4;
-      const uint64_t qdesc0 = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
-      const uint64_t kdesc = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
-      const uint64_t vdesc = smem_desc_sw128(smem_u32(sm.v[0][0]), kPackSub, 1024);
-      const uint32_t dS = tmem + 128u * g, dO = tmem + 256u + D * g;
-      const uint32_t aP = kOwnP ? tmem + 384u + 64u * g : dS;
-      int q_it = 0, kv_it = 0, n_s = 0, n_p = 0, n_o = 0;
+      const uint32_t qdesc = desc_low(smem_u32(sm.q[0][0]), 16), kdesc = desc_low(smem_u32(sm.k[0][0]), 16);
+      const uint32_t vdesc = desc_low(smem_u32(sm.v[0][0]), kPackSub);
+      int q_it = 0, kv_it = 0, n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const int slot = it % kSlots;
         if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
-        const int head = sm.item[slot].head;
-        const PackEntry e = sm.item[slot].e;
-        mbar_arrive(&sm.item_empty[slot]);
-        if (head < 0) break;
-        int a[2], b[2];
+        const PackEntry& e = sm.item[slot].e;
+        if (sm.item[slot].head < 0) break;
+        int a[2], b[2], qi[2];
         fwd_range(e, 0, p.tpt, window, a[0], b[0]);
         fwd_range(e, 1, p.tpt, window, a[1], b[1]);
+        const int m_keys = e.m;
         const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
-        const bool mine = a[g] < b[g];
-        // Q tiles pass through one ring; the other issuer's tiles are released by that one
-        const int qi = q_it + (g == 1 && a[0] < b[0] ? 1 : 0), qs = qi % kQ;
-        q_it += (a[0] < b[0]) + (a[1] < b[1]);
-        const uint64_t qdesc = qdesc0 + static_cast<uint64_t>(qs * kTile16);
-        auto issue_s = [&](int kvi) -> bool {
-          const int s = kvi % kStages;
-          if (kOwnP && n_s > 0 && !mbar_wait(&sm.s_free[g], (n_s - 1) & 1, abort_flag, p.status)) return false;
+        qi[0] = q_it, qi[1] = q_it + (a[0] < b[0]);
+        q_it = qi[1] + (a[1] < b[1]);
+        bool first[2] = {true, true};
+        // S_g of key tile j (number kvi); behind the last one Q_g is free
+        auto issue_s = [&](int g, int j, int kvi) -> bool {
+          const int s = kvi % kStages, qs = qi[g] % kQ;
+          if (j == a[g] && !mbar_wait(&sm.q_full[qs], (qi[g] / kQ) & 1, abort_flag, p.status)) return false;
+          if (kOwnP && n_s[g] > 0 && !mbar_wait(&sm.s_free[g], (n_s[g] - 1) & 1, abort_flag, p.status)) return false;
           if (!mbar_wait(&sm.k_full[s], (kvi / kStages) & 1, abort_flag, p.status)) return false;
           tc_fence_after();
-          const uint64_t bk = kdesc + static_cast<uint64_t>(s * kTile16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16_ss(dS, qdesc + kstep_off16(kk, kPackSub), bk + kstep_off16(kk, kPackSub), idesc_s, kk > 0);
+          mma_ss_steps<0, D / 16>(tmem + 128u * g, qdesc + qs * kTile16, kdesc + s * kTile16, idesc_s, false);
           tc_commit(&sm.s_full[g]);
-          ++n_s;
+          if (j == b[g] - 1) tc_commit(&sm.q_empty[qs]);
+          ++n_s[g];
           return true;
         };
-        if (mine && !mbar_wait(&sm.q_full[qs], (qi / kQ) & 1, abort_flag, p.status)) break;
-        if (mine && a[g] == j0 && !issue_s(kv_it)) break;
-        bool first = true;
-        for (int j = j0; j < j1; ++j, ++kv_it) {
-          const int s = kv_it % kStages;
-          const bool now = j >= a[g] && j < b[g], next = j + 1 >= a[g] && j + 1 < b[g];
-          if (now) {
-            if (kOwnP && next && !issue_s(kv_it + 1)) { ok = false; break; }
-            if (!next) tc_commit(&sm.q_empty[qs]);  // the last S of this tile is issued
-            const int steps = min(kTile / 16, (e.m - j * kTile + 15) >> 4);
-            const uint64_t bv = vdesc + static_cast<uint64_t>(s * kTile16);
-            if (!mbar_wait(&sm.v_full[s], (kv_it / kStages) & 1, abort_flag, p.status)) { ok = false; break; }
-            if (first && !mbar_wait(&sm.o_empty[g], (n_o & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
-            if (!mbar_wait(&sm.p_full[g][0], n_p & 1, abort_flag, p.status)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < steps)
-                mma_bf16_ts(dO, aP + kk * 8, bv + static_cast<uint64_t>(kk * 128), idesc_o, first && kk == 0 ? 0u : 1u);
-            if (!mbar_wait(&sm.p_full[g][1], n_p & 1, abort_flag, p.status)) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              if (kk < steps) mma_bf16_ts(dO, aP + kk * 8, bv + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-            if (kOwnP) tc_commit(&sm.pv_done[g]);
-            first = false;
-            ++n_p;
+        auto issue_pv = [&](int g, int j, int kvi) -> bool {
+          const int s = kvi % kStages, steps = min(kTile / 16, (m_keys - j * kTile + 15) >> 4);
+          const uint32_t bv = vdesc + s * kTile16;
+          const uint32_t dO = tmem + 256u + D * g, aP = kOwnP ? tmem + 384u + 64u * g : tmem + 128u * g;
+          if (!mbar_wait(&sm.v_full[s], (kvi / kStages) & 1, abort_flag, p.status)) return false;
+          if (first[g] && !mbar_wait(&sm.o_empty[g], (n_o[g] & 1) ^ 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&sm.p_full[g][0], n_p[g] & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          if (steps == 8) mma_ts_steps<0, 4>(dO, aP, bv, idesc_o, !first[g], 8);
+          else mma_ts_steps<0, 4>(dO, aP, bv, idesc_o, !first[g], steps);
+          if (!mbar_wait(&sm.p_full[g][1], n_p[g] & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+          if (steps == 8) mma_ts_steps<4, 8>(dO, aP, bv, idesc_o, true, 8);
+          else mma_ts_steps<4, 8>(dO, aP, bv, idesc_o, true, steps);
+          if (kOwnP) tc_commit(&sm.pv_done[g]);
+          first[g] = false;
+          ++n_p[g];
+          return true;
+        };
+        auto in = [&](int g, int j) { return j >= a[g] && j < b[g]; };
+        // K_j goes back once both tiles' S of it are issued, long before V_j
+        for (int g = 0; g < 2 && ok; ++g)
+          if (in(g, j0)) ok = issue_s(g, j0, kv_it);
+        if (j0 < j1) tc_commit(&sm.k_empty[kv_it % kStages]);
+        for (int j = j0; j < j1 && ok; ++j, ++kv_it) {
+          if (kOwnP) {
+            for (int g = 0; g < 2 && ok; ++g)
+              if (in(g, j + 1)) ok = issue_s(g, j + 1, kv_it + 1);
+            for (int g = 0; g < 2 && ok; ++g)
+              if (in(g, j)) ok = issue_pv(g, j, kv_it);
           } else {
-            // released only once it has landed: a run through tiles that are not
-            // this issuer's must not give both arrivals of a stage by itself
-            if (!mbar_wait(&sm.k_full[s], (kv_it / kStages) & 1, abort_flag, p.status)) { ok = false; break; }
+            for (int g = 0; g < 2 && ok; ++g) {
+              if (in(g, j)) ok = issue_pv(g, j, kv_it);
+              if (ok && in(g, j + 1)) ok = issue_s(g, j + 1, kv_it + 1);
+            }
           }
-          tc_commit(&sm.kv_empty[s]);
-          if (next && (!kOwnP || !now) && !issue_s(kv_it + 1)) { ok = false; break; }
+          tc_commit(&sm.v_empty[kv_it % kStages]);
+          if (j + 1 < j1) tc_commit(&sm.k_empty[(kv_it + 1) % kStages]);
         }
         if (!ok) break;
-        if (mine) {
-          tc_commit(&sm.o_full[g]);
-          ++n_o;
-        }
+        for (int g = 0; g < 2; ++g)
+          if (a[g] < b[g]) {
+            tc_commit(&sm.o_full[g]);
+            ++n_o[g];
+          }
+        mbar_arrive(&sm.item_empty[slot]);
       }
-      tc_commit(&sm.drain[g]);
-      mbar_wait_drain(&sm.drain[g], 0, p.status);
+      tc_commit(&sm.drain);
+      mbar_wait_drain(&sm.drain, 0, p.status);
     }
   }
   } else {
@@ -305,60 +316,57 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int g = (warp - 4) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t colS = 128u * g, colO = 256u + D * g, colP = kOwnP ? 384u + 64u * g : colS;
+    const uint32_t tS = lanes + 128u * g, tO = lanes + 256u + D * g, tP = kOwnP ? lanes + 384u + 64u * g : tS;
     const int r_tok = r / p.G, r_head = r - r_tok * p.G;
     int n_s = 0, n_o = 0, n_sync = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+      const PackEntry& e = sm.item[slot].e;
       const int head = sm.item[slot].head;
-      const PackEntry e = sm.item[slot].e;
-      warp_arrive(&sm.item_empty[slot]);
       if (head < 0) break;
       int a, b;
       fwd_range(e, g, p.tpt, window, a, b);
       const int first = e.diag + g * p.tpt, n_tok = min(p.tpt, e.n_tok - g * p.tpt);
-      if (n_tok <= 0) continue;
+      if (n_tok <= 0) {
+        warp_arrive(&sm.item_empty[slot]);
+        continue;
+      }
       const bool valid = r_tok < n_tok;
-      const int hi = valid ? first + r_tok : -1;           // the last key that the row sees
-      const int lo = window ? hi - window + 1 : INT_MIN;   // the first
+      const int hi = valid ? first + r_tok : -1;  // the last key that the row sees
       float m = -INFINITY, l = 0.f;
       float top = -INFINITY;  // largest score so far, log2 units
-      bool ok = true;
-      for (int j = a; j < b; ++j) {
-        if (!warp_wait(&sm.s_full[g], n_s & 1, abort_flag, p.status)) { ok = false; break; }
+      // one key tile. The loop's usual path is one straight run of code: masked
+      // tiles have a copy of their own, and what is rare stands apart
+      auto tile = [&](auto masked, int j) -> bool {
+        if (!warp_wait(&sm.s_full[g], n_s & 1, abort_flag, p.status)) return false;
         tc_fence_after();
         uint32_t sr[kTile];
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) tmem_ld32(lanes + colS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+        for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
         tmem_wait_ld();
         tmem_ld_fence(sr);
         if (kOwnP) {
           tc_fence_before();
           warp_arrive(&sm.s_free[g]);
         }
-        const int k0 = j * kTile;
-        if (k0 + kTile - 1 > first) {  // keys that some row does not see
-          const int lim = hi - k0;
+        if (decltype(masked)::value) {
+          // lo <= column <= lim as one unsigned comparison
+          const int lim = hi - j * kTile, lo = window ? max(lim - window + 1, -kTile) : -kTile;
+          const uint32_t span = lim < lo ? 0u : static_cast<uint32_t>(lim - lo) + 1u;
 #pragma unroll
           for (int c = 0; c < kTile; ++c)
-            if (c > lim) sr[c] = 0xff800000u;
-        }
-        if (window && k0 < first + n_tok - window) {
-          const int lim = lo - k0;
-#pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c < lim) sr[c] = 0xff800000u;
+            if (static_cast<uint32_t>(c - lo) >= span) sr[c] = 0xff800000u;
         }
         float mx[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = __uint_as_float(sr[u]);
+        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(__uint_as_float(sr[2 * u]), __uint_as_float(sr[2 * u + 1]));
 #pragma unroll
-        for (int c = 4; c < kTile; c += 8)
+        for (int c = 8; c < kTile; c += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx[u] = max3f(mx[u], __uint_as_float(sr[c + 2 * u < kTile ? c + 2 * u : u]), __uint_as_float(sr[c + 2 * u + 1 < kTile ? c + 2 * u + 1 : u]));
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          for (int u = 0; u < 4; ++u) mx[u] = pack_max3(mx[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
+        float sl = p.scale_log2;
+        const float mt = pack_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
         top = fmaxf(top, mt);
         const bool grown = mt > m + kGrow;
         float alpha = 1.f;
@@ -367,34 +375,35 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           m = mt;
         }
         float sub = m == -INFINITY ? 0.f : -m;
-        float sl = p.scale_log2;
-        if (__any_sync(0xffffffffu, fabsf(sub) > kFarScore)) {
-          // far from zero an fma would give the largest score its product's rounding as a weight: both rounded alike
-#pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), sl), sub));
-          sl = 1.f, sub = 0.f;
-        }
+        const bool far = fabsf(sub) > kFarScore;
         if (kOwnP && n_s > 0) {
-          if (!warp_wait(&sm.pv_done[g], (n_s - 1) & 1, abort_flag, p.status)) { ok = false; break; }
+          if (!warp_wait(&sm.pv_done[g], (n_s - 1) & 1, abort_flag, p.status)) return false;
           tc_fence_after();
         }
-        // O to the new reference (rare). The product before is complete: with
-        // P's own columns by the wait above, else because S came behind it
-        if (j > a && __any_sync(0xffffffffu, grown)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, grown || far), 0)) {
+          if (far) {
+            // far from zero an fma would give the largest score its product's rounding as a weight: both rounded alike
 #pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t oo[32];
-            tmem_ld32(lanes + colO + cc * 32, oo);
-            tmem_wait_ld();
-            tmem_ld_fence(oo);
+            for (int c = 0; c < kTile; ++c) sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), sl), sub));
+            sl = 1.f, sub = 0.f;
+          }
+          // O to the new reference. The product before is complete: with P's
+          // own columns by the wait above, else because S came behind it
+          if (j > a) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) oo[c] = __float_as_uint(__uint_as_float(oo[c]) * alpha);
-            tmem_st32(lanes + colO + cc * 32, oo);
+            for (int cc = 0; cc < D / 16; ++cc) {
+              uint32_t oo[16];
+              tmem_ld16(tO + cc * 16, oo);
+              tmem_wait_ld();
+              tmem_ld_fence(oo);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) oo[c] = __float_as_uint(__uint_as_float(oo[c]) * alpha);
+              tmem_st16(tO + cc * 16, oo);
+            }
           }
         }
         const uint64_t sl2 = f2(sl, sl), sub2 = f2(sub, sub);
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+        uint64_t sum[2] = {f2(l * alpha, 0.f), 0ull};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t pk[16];
@@ -403,10 +412,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             float x0, x1;
             f2_split(fma2(f2(__uint_as_float(sr[q * 32 + c]), __uint_as_float(sr[q * 32 + c + 1])), sl2, sub2), x0, x1);
             x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-            sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], f2(x0, x1));
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(x0, x1));
             pk[c >> 1] = c4_pack<F16>(x0, x1);
           }
-          tmem_st16(lanes + colP + q * 16, pk);
+          tmem_st16(tP + q * 16, pk);
           if (q & 1) {
             tmem_wait_st();
             tc_fence_before();
@@ -414,9 +423,16 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
         }
         float s0, s1;
-        f2_split(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
-        l = fmaf(l, alpha, s0 + s1);
+        f2_split(add2(sum[0], sum[1]), s0, s1);
+        l = s0 + s1;
         ++n_s;
+        return true;
+      };
+      bool ok = true;
+      for (int j = a; j < b && ok; ++j) {
+        // keys that some row does not see: behind the first token's last, before the last token's first
+        if (j * kTile + kTile - 1 > first || (window && j * kTile < first + n_tok - window)) ok = tile(std::true_type{}, j);
+        else ok = tile(std::false_type{}, j);
       }
       if (!ok) break;
       uint32_t acc[D / 32][32];
@@ -425,7 +441,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (!warp_wait(&sm.o_full[g], n_o & 1, abort_flag, p.status)) break;
         tc_fence_after();
 #pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) tmem_ld32(lanes + colO + cc * 32, acc[cc]);
+        for (int cc = 0; cc < D / 32; ++cc) tmem_ld32(tO + cc * 32, acc[cc]);
         tmem_wait_ld();
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) tmem_ld_fence(acc[cc]);
@@ -445,7 +461,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
       }
       if (e.slot >= 0) {
-        // leave this chunk's share; the last to arrive takes them all
+        // leave this chunk's share (column by column: neighbouring threads, neighbouring places); the last to arrive takes them all
         const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * (D + 2);
         float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
         float* const mine = base + e.chunk * stride;
@@ -463,11 +479,13 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         warp_arrive(&sm.sync[g]);
         if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
         ++n_sync;
-        if (!*reinterpret_cast<volatile int*>(&sm.last[g])) continue;
+        if (!*reinterpret_cast<volatile int*>(&sm.last[g])) {
+          warp_arrive(&sm.item_empty[slot]);
+          continue;
+        }
         __threadfence();
-        m = -INFINITY, round = 0.f;
+        m = -INFINITY, round = 0.f, l = 0.f;
         for (int c = 0; c < e.chunks; ++c) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r).x);
-        l = 0.f;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc)
 #pragma unroll
@@ -495,12 +513,12 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const uint32_t* y = &acc[c / 4][c % 4 * 8];
           uint32_t u[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            u[i] = c4_pack<F16>(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
+          for (int i = 0; i < 4; ++i) u[i] = c4_pack<F16>(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
           dst[c] = make_uint4(u[0], u[1], u[2], u[3]);
         }
         p.lse[tok * p.Hq + qh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
       }
+      warp_arrive(&sm.item_empty[slot]);
     }
   }
   tc_fence_before();
