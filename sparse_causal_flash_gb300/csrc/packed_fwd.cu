@@ -9,7 +9,7 @@
 // One CTA per SM, work from a counter, longest first. A work item is two tiles of query rows of one key head that share
 // each K and V tile. Roles:
 //   warp 0        producer: TMA of the item's two Q tiles and of K_j, V_j into rings
-//   warp 1        MMA issuer: S = Q K^T, then O += P V with P read from TMEM, in two halves of the keys
+//   warp 1 (2)    MMA issuers: S = Q K^T, then O += P V with P read from TMEM, in two halves of the keys
 //   warps 4-7, 8-11  softmax of tile 0 and 1: thread = row = TMEM lane; a row's 128 scores stay in its registers (216 of
 //                 them; the first four warps give up what they do not need)
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+D), O_1 behind it. At D = 128 that is all of it and P_g takes the first
@@ -38,9 +38,11 @@ constexpr float kFarScore = 65536.f;
 template <int D>
 struct PFwdCfg {
   static constexpr int kSubs = D / 64;
-  static constexpr int kQ = D == 64 ? 4 : 3;       // Q tiles in the ring
-  static constexpr int kStages = D == 64 ? 4 : 2;  // K and V tiles
+  static constexpr int kQ = D == 64 ? 4 : 3;  // Q tiles in the ring
+  static constexpr int kKs = D == 64 ? 4 : 2;  // K tiles
+  static constexpr int kVs = D == 64 ? 4 : 2;  // V tiles
   static constexpr bool kOwnP = D == 64;
+  static constexpr int kIssuers = D == 64 ? 2 : 1;
 };
 
 struct PItem {
@@ -53,11 +55,11 @@ template <int D>
 struct __align__(1024) PFwdSmem {
   using C = PFwdCfg<D>;
   uint8_t q[C::kQ][C::kSubs][kPackSub];
-  uint8_t k[C::kStages][C::kSubs][kPackSub];
-  uint8_t v[C::kStages][C::kSubs][kPackSub];
+  uint8_t k[C::kKs][C::kSubs][kPackSub];
+  uint8_t v[C::kVs][C::kSubs][kPackSub];
   PItem item[kSlots];
-  uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kStages], v_full[C::kStages], k_empty[C::kStages], v_empty[C::kStages];
-  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain, sync[2];
+  uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kKs], v_full[C::kVs], k_empty[C::kKs], v_empty[C::kVs];
+  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2], sync[2];
   uint64_t tail, item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
   int abort_flag, last[2];
@@ -89,12 +91,17 @@ __device__ __forceinline__ void fwd_range(const PackEntry& e, int g, int tpt, in
   if (a >= b) a = b = 0;
 }
 
+// weight of a chunk's sums beside the largest reference
+__device__ __forceinline__ float share(float2 ml, float m) {
+  return ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2_approx(ml.x - m);
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PFwdParams p) {
   using C = PFwdCfg<D>;
-  constexpr int kSubs = C::kSubs, kStages = C::kStages, kQ = C::kQ;
+  constexpr int kSubs = C::kSubs, kKs = C::kKs, kVs = C::kVs, kQ = C::kQ;
   constexpr bool kOwnP = C::kOwnP;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -111,15 +118,16 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQ; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
-    for (int s = 0; s < kStages; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.v_full[s], 1), mbar_init(&sm.k_empty[s], 1), mbar_init(&sm.v_empty[s], 1);
+    for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], C::kIssuers);
+    for (int s = 0; s < kVs; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], C::kIssuers);
     for (int g = 0; g < 2; ++g) {
       mbar_init(&sm.s_full[g], 1), mbar_init(&sm.s_free[g], 4);
       mbar_init(&sm.p_full[g][0], 4), mbar_init(&sm.p_full[g][1], 4);
       mbar_init(&sm.pv_done[g], 1), mbar_init(&sm.o_full[g], 1), mbar_init(&sm.o_empty[g], 4);
       mbar_init(&sm.sync[g], 4);
     }
-    mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
+    mbar_init(&sm.tail, 1), mbar_init(&sm.drain[0], 1), mbar_init(&sm.drain[1], 1);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], C::kIssuers + 8);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v);
@@ -175,18 +183,17 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (p.stall && k_it == 0 && a[0] + b[0] + a[1] + b[1] > 0) break;  // debug stall: no K / V load ever arrives
       const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
       for (int j = j0; j < j1 && ok; ++j) {
-        const int s = kv_it % kStages;
-        const uint32_t free = ((kv_it / kStages) & 1) ^ 1;
         const int valid = e.m - j * kTile;  // keys of the sequence in the tile, if below 128
         const bool cut = valid < kTile && (valid & 15) != 0;
-        ok = warp_wait(&sm.k_empty[s], free, abort_flag, p.status);
+        const int ks = k_it % kKs, s = kv_it % kVs;
+        ok = warp_wait(&sm.k_empty[ks], ((k_it / kKs) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&sm.k_full[s], D * kTile * 2);
-          for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.k[s][sub], &tm_k, &sm.k_full[s], sub * 64, head, e.k0 + j * kTile);
+          mbar_arrive_expect_tx(&sm.k_full[ks], D * kTile * 2);
+          for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.k[ks][sub], &tm_k, &sm.k_full[ks], sub * 64, head, e.k0 + j * kTile);
         }
         ++k_it;
-        ok = warp_wait(&sm.v_empty[s], free, abort_flag, p.status);
+        ok = warp_wait(&sm.v_empty[s], ((kv_it / kVs) & 1) ^ 1, abort_flag, p.status);
         if (!ok) break;
         if (lane == 0) {
           uint64_t* const vb = cut ? &sm.tail : &sm.v_full[s];
@@ -210,27 +217,29 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (lane == 0) {
       // every copy issued has landed before the CTA exits, also after an abort
       if (tails > 0) mbar_wait_drain(&sm.tail, (tails - 1) & 1, p.status);
-      for (int d = 1; d <= kStages && d <= k_it; ++d)
-        mbar_wait_drain(&sm.k_full[(k_it - d) % kStages], ((k_it - d) / kStages) & 1, p.status);
-      for (int d = 1; d <= kStages && d <= kv_it; ++d) {
+      for (int d = 1; d <= kKs && d <= k_it; ++d)
+        mbar_wait_drain(&sm.k_full[(k_it - d) % kKs], ((k_it - d) / kKs) & 1, p.status);
+      for (int d = 1; d <= kVs && d <= kv_it; ++d) {
         const int i = kv_it - d;
-        if (i != unmarked) mbar_wait_drain(&sm.v_full[i % kStages], (i / kStages) & 1, p.status);
+        if (i != unmarked) mbar_wait_drain(&sm.v_full[i % kVs], (i / kVs) & 1, p.status);
       }
       for (int d = 1; d <= kQ && d <= q_it; ++d)
         mbar_wait_drain(&sm.q_full[(q_it - d) % kQ], ((q_it - d) / kQ) & 1, p.status);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // One thread issues for both tiles, in turns: tile 0's products come whole
-    // before tile 1's, which keeps one tile's softmax under the other's
-    // products. (With a thread for each, the two fell into step: both in the
-    // softmax, then both waiting for the tensor cores; 533 us instead of XXX.)
+  } else if (warp <= C::kIssuers) {
+    // ------------------------------------------------------------ MMA issuers
+    // D = 128: one thread issues for both tiles, in turns: tile 0's products
+    // come whole before tile 1's, which keeps one tile's softmax under the
+    // other's products. (With a thread for each the two fell into step, both in
+    // the softmax, then both waiting for the tensor cores.) D = 64: a thread
+    // for each; its MMAs are so short that issuing them counts.
     if (elect_one()) {
       constexpr uint32_t idesc_s = pack_idesc<F16>(kTile, kTile, 0, 0);
       constexpr uint32_t idesc_o = pack_idesc<F16>(kTile, D, 0, 1);
       constexpr uint32_t kTile16 = (kSubs * kPackSub) >> 4;
       const uint32_t qdesc = desc_low(smem_u32(sm.q[0][0]), 16), kdesc = desc_low(smem_u32(sm.k[0][0]), 16);
       const uint32_t vdesc = desc_low(smem_u32(sm.v[0][0]), kPackSub);
+      const int g0 = C::kIssuers == 2 ? warp - 1 : 0, g1 = C::kIssuers == 2 ? warp : 2;  // this thread's tiles
       int q_it = 0, kv_it = 0, n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
       bool ok = true;
       for (int it = 0; ok; ++it) {
@@ -248,10 +257,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         bool first[2] = {true, true};
         // S_g of key tile j (number kvi); behind the last one Q_g is free
         auto issue_s = [&](int g, int j, int kvi) -> bool {
-          const int s = kvi % kStages, qs = qi[g] % kQ;
+          const int s = kvi % kKs, qs = qi[g] % kQ;
           if (j == a[g] && !mbar_wait(&sm.q_full[qs], (qi[g] / kQ) & 1, abort_flag, p.status)) return false;
           if (kOwnP && n_s[g] > 0 && !mbar_wait(&sm.s_free[g], (n_s[g] - 1) & 1, abort_flag, p.status)) return false;
-          if (!mbar_wait(&sm.k_full[s], (kvi / kStages) & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&sm.k_full[s], (kvi / kKs) & 1, abort_flag, p.status)) return false;
           tc_fence_after();
           mma_ss_steps<0, D / 16>(tmem + 128u * g, qdesc + qs * kTile16, kdesc + s * kTile16, idesc_s, false);
           tc_commit(&sm.s_full[g]);
@@ -260,10 +269,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           return true;
         };
         auto issue_pv = [&](int g, int j, int kvi) -> bool {
-          const int s = kvi % kStages, steps = min(kTile / 16, (m_keys - j * kTile + 15) >> 4);
+          const int s = kvi % kVs, steps = min(kTile / 16, (m_keys - j * kTile + 15) >> 4);
           const uint32_t bv = vdesc + s * kTile16;
           const uint32_t dO = tmem + 256u + D * g, aP = kOwnP ? tmem + 384u + 64u * g : tmem + 128u * g;
-          if (!mbar_wait(&sm.v_full[s], (kvi / kStages) & 1, abort_flag, p.status)) return false;
+          if (!mbar_wait(&sm.v_full[s], (kvi / kVs) & 1, abort_flag, p.status)) return false;
           if (first[g] && !mbar_wait(&sm.o_empty[g], (n_o[g] & 1) ^ 1, abort_flag, p.status)) return false;
           if (!mbar_wait(&sm.p_full[g][0], n_p[g] & 1, abort_flag, p.status)) return false;
           tc_fence_after();
@@ -279,35 +288,52 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           return true;
         };
         auto in = [&](int g, int j) { return j >= a[g] && j < b[g]; };
-        // K_j goes back once both tiles' S of it are issued, long before V_j
-        for (int g = 0; g < 2 && ok; ++g)
-          if (in(g, j0)) ok = issue_s(g, j0, kv_it);
-        if (j0 < j1) tc_commit(&sm.k_empty[kv_it % kStages]);
-        for (int j = j0; j < j1 && ok; ++j, ++kv_it) {
-          if (kOwnP) {
-            for (int g = 0; g < 2 && ok; ++g)
+        // K_j goes back once both tiles' S of it are issued, long before V_j.
+        // A tile that this thread skips goes back once it has landed: a run
+        // through such tiles must not give another thread's arrivals too
+        auto release_k = [&](bool used, int kvi) -> bool {
+          if (C::kIssuers == 2 && !used && !mbar_wait(&sm.k_full[kvi % kKs], (kvi / kKs) & 1, abort_flag, p.status)) return false;
+          tc_commit(&sm.k_empty[kvi % kKs]);
+          return true;
+        };
+        if (C::kIssuers == 2) {
+          const int g = g0;
+          if (j0 < j1) {
+            if (in(g, j0)) ok = issue_s(g, j0, kv_it);
+            ok = ok && release_k(in(g, j0), kv_it);
+          }
+          for (int j = j0; j < j1 && ok; ++j, ++kv_it) {
+            if (j + 1 < j1) {
               if (in(g, j + 1)) ok = issue_s(g, j + 1, kv_it + 1);
-            for (int g = 0; g < 2 && ok; ++g)
-              if (in(g, j)) ok = issue_pv(g, j, kv_it);
-          } else {
+              ok = ok && release_k(in(g, j + 1), kv_it + 1);
+            }
+            if (ok && in(g, j)) ok = issue_pv(g, j, kv_it);
+            else if (ok) ok = mbar_wait(&sm.v_full[kv_it % kVs], (kv_it / kVs) & 1, abort_flag, p.status);
+            if (ok) tc_commit(&sm.v_empty[kv_it % kVs]);
+          }
+        } else {
+          for (int g = 0; g < 2 && ok; ++g)
+            if (in(g, j0)) ok = issue_s(g, j0, kv_it);
+          if (j0 < j1) tc_commit(&sm.k_empty[kv_it % kKs]);
+          for (int j = j0; j < j1 && ok; ++j, ++kv_it) {
             for (int g = 0; g < 2 && ok; ++g) {
               if (in(g, j)) ok = issue_pv(g, j, kv_it);
               if (ok && in(g, j + 1)) ok = issue_s(g, j + 1, kv_it + 1);
             }
+            tc_commit(&sm.v_empty[kv_it % kVs]);
+            if (j + 1 < j1) tc_commit(&sm.k_empty[(kv_it + 1) % kKs]);
           }
-          tc_commit(&sm.v_empty[kv_it % kStages]);
-          if (j + 1 < j1) tc_commit(&sm.k_empty[(kv_it + 1) % kStages]);
         }
         if (!ok) break;
-        for (int g = 0; g < 2; ++g)
+        for (int g = g0; g < g1; ++g)
           if (a[g] < b[g]) {
             tc_commit(&sm.o_full[g]);
             ++n_o[g];
           }
         mbar_arrive(&sm.item_empty[slot]);
       }
-      tc_commit(&sm.drain);
-      mbar_wait_drain(&sm.drain, 0, p.status);
+      tc_commit(&sm.drain[g0]);
+      mbar_wait_drain(&sm.drain[g0], 0, p.status);
     }
   }
   } else {
@@ -428,49 +454,47 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         ++n_s;
         return true;
       };
+      // Tiles [plain, masked) are seen whole by every row: those before hold keys before the last token's first, those
+      // behind keys after the first token's last. The plain loop stands by itself, with nothing to jump over.
+      const int plain = window ? min(b, max(a, (first + n_tok - window + kTile - 1) / kTile)) : a;
+      const int masked = max(plain, min(b, max(0, first + 1) / kTile));
       bool ok = true;
-      for (int j = a; j < b && ok; ++j) {
-        // keys that some row does not see: behind the first token's last, before the last token's first
-        if (j * kTile + kTile - 1 > first || (window && j * kTile < first + n_tok - window)) ok = tile(std::true_type{}, j);
-        else ok = tile(std::false_type{}, j);
+      int j = a;
+      for (int part = 0; part < 2 && ok; ++part) {
+        const int stop = part ? b : plain;
+        for (; j < stop && ok; ++j) ok = tile(std::true_type{}, j);
+        if (part == 0)
+          for (; j < masked && ok; ++j) ok = tile(std::false_type{}, j);
       }
       if (!ok) break;
-      uint32_t acc[D / 32][32];
-      float round = 0.f;  // what the rounding of the largest weight adds to the sum
       if (a < b) {
         if (!warp_wait(&sm.o_full[g], n_o & 1, abort_flag, p.status)) break;
         tc_fence_after();
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) tmem_ld32(tO + cc * 32, acc[cc]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) tmem_ld_fence(acc[cc]);
-        tc_fence_before();
-        warp_arrive(&sm.o_empty[g]);
         ++n_o;
-        // the largest score's weight as the product saw it: a row with one key gives that row of V exactly
-        const float w = ex2_approx(top - m);
-        float w_r;
-        if (F16) w_r = __half2float(__float2half_rn(w));
-        else w_r = __bfloat162float(__float2bfloat16_rn(w));
-        if (l > 0.f) round = w_r - w;
-      } else {
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc)
-#pragma unroll
-          for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
       }
-      if (e.slot >= 0) {
-        // leave this chunk's share (column by column: neighbouring threads, neighbouring places); the last to arrive takes them all
-        const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * (D + 2);
-        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
+      float inv;
+      const bool joined = e.slot >= 0;
+      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * (D + 2);  // from chunk to chunk
+      float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
+      if (joined) {
+        // leave this chunk's share; the last to arrive takes them all, in their order
         float* const mine = base + e.chunk * stride;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t acc[D / 64][32];
+          quad_rows<D>(acc, tO, hf, a < b);
 #pragma unroll
-        for (int c = 0; c < D / 4; ++c)
-          reinterpret_cast<float4*>(mine)[c * kTile + r] =
-              make_float4(__uint_as_float(acc[c / 8][c % 8 * 4]), __uint_as_float(acc[c / 8][c % 8 * 4 + 1]),
-                          __uint_as_float(acc[c / 8][c % 8 * 4 + 2]), __uint_as_float(acc[c / 8][c % 8 * 4 + 3]));
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              *reinterpret_cast<float2*>(mine + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)) =
+                  make_float2(__uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u]), __uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u + 1]));
+        }
         reinterpret_cast<float2*>(mine + kTile * D)[r] = make_float2(m, l);
+        if (a < b) {
+          tc_fence_before();
+          warp_arrive(&sm.o_empty[g]);
+        }
         __threadfence();
         warp_arrive(&sm.sync[g]);
         if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
@@ -484,40 +508,53 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           continue;
         }
         __threadfence();
-        m = -INFINITY, round = 0.f, l = 0.f;
+        m = -INFINITY, l = 0.f;
         for (int c = 0; c < e.chunks; ++c) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r).x);
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc)
-#pragma unroll
-          for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
         for (int c = 0; c < e.chunks; ++c) {
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r);
-          const float f = ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2_approx(ml.x - m);
-          l = fmaf(ml.y, f, l);
+          l = fmaf(ml.y, share(ml, m), l);
+        }
+        inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+      } else {
+        // O is divided by the sum with the largest score's weight as the product saw it, rounded: a row with one key gives
+        // that row of V exactly
+        const float w = ex2_approx(top - m);
+        float w_r;
+        if (F16) w_r = __half2float(__float2half_rn(w));
+        else w_r = __bfloat162float(__float2bfloat16_rn(w));
+        inv = l > 0.f ? 1.f / (l + (w_r - w)) : l == 0.f ? 0.f : l;
+      }
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t acc[D / 64][32];
+        quad_rows<D>(acc, tO, hf, !joined && a < b);
+        if (joined) {
+          for (int c = 0; c < e.chunks; ++c) {
+            const float f = share(__ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r), m);
+            const float fu[2] = {__shfl_sync(0xffffffffu, f, hf * 16 + (lane >> 2)), __shfl_sync(0xffffffffu, f, hf * 16 + (lane >> 2) + 8)};
 #pragma unroll
-          for (int i = 0; i < D / 4; ++i) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(base + c * stride) + i * kTile + r);
-            uint32_t* y = &acc[i / 8][i % 8 * 4];
-            y[0] = __float_as_uint(fmaf(x.x, f, __uint_as_float(y[0]))), y[1] = __float_as_uint(fmaf(x.y, f, __uint_as_float(y[1])));
-            y[2] = __float_as_uint(fmaf(x.z, f, __uint_as_float(y[2]))), y[3] = __float_as_uint(fmaf(x.w, f, __uint_as_float(y[3])));
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)));
+                uint32_t* y = &acc[i >> 3][(i & 7) * 4 + 2 * u];
+                y[0] = __float_as_uint(fmaf(x.x, fu[u], __uint_as_float(y[0]))), y[1] = __float_as_uint(fmaf(x.y, fu[u], __uint_as_float(y[1])));
+              }
           }
         }
-      }
-      if (valid) {
-        const float inv = l > 0.f ? 1.f / (l + round) : l == 0.f ? 0.f : l;
-        const long long tok = e.q0 + g * p.tpt + r_tok;
-        const int qh = head * p.G + r_head;
-        uint4* dst = reinterpret_cast<uint4*>(p.o + tok * p.ot + qh * p.oh);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t* y = &acc[c / 4][c % 4 * 8];
-          uint32_t u[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[i] = c4_pack<F16>(__uint_as_float(y[2 * i]) * inv, __uint_as_float(y[2 * i + 1]) * inv);
-          dst[c] = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int u = 0; u < 2; ++u) {
+          const int from = hf * 16 + (lane >> 2) + 8 * u;
+          const float f = __shfl_sync(0xffffffffu, inv, from);
+          const int t = __shfl_sync(0xffffffffu, r_tok, from), qh = head * p.G + quarter * 32 + from - t * p.G;
+          quad_store<D, F16>(p.o + (e.q0 + g * p.tpt + t) * p.ot + qh * p.oh, t < n_tok, acc, u, f);
         }
-        p.lse[tok * p.Hq + qh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
       }
+      if (!joined && a < b) {
+        tc_fence_before();
+        warp_arrive(&sm.o_empty[g]);
+      }
+      if (valid) p.lse[(static_cast<long long>(e.q0) + g * p.tpt + r_tok) * p.Hq + head * p.G + r_head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
       warp_arrive(&sm.item_empty[slot]);
     }
   }
