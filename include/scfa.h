@@ -498,6 +498,9 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  *   outside [0, N] or [0, M], raise SCFA_ERR_INVALID in the plan's status word,
  *   and in that of every call with the plan, which then computes nothing.
  * scfa_packed_fwd: o [N][Hq][D], lse [N][Hq] fp32, natural log.
+ * scfa_packed_bwd: from the forward's q, k, v, o, lse and do [N][Hq][D], the
+ *   gradients dq [N][Hq][D], dk, dv [M][Hkv][D]; those of a key head are the sums
+ *   over its query heads.
  * Rows are bf16 or fp16 (dtype), D = 64 or 128, 16-byte aligned, with token and
  * head strides that are positive multiples of 8 elements. Rows that belong to no
  * sequence are neither read into results nor written. Inputs and outputs must
@@ -519,6 +522,17 @@ scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, long long q_he
                             const void* plan, size_t plan_bytes, int N, int M, int Hq, int Hkv,
                             int D, float scale, int dtype, uint16_t* o, long long o_token,
                             long long o_head, float* lse, void* ws, size_t ws_bytes,
+                            unsigned flags, void* stream);
+scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, long long q_head,
+                            const uint16_t* k, long long k_token, long long k_head,
+                            const uint16_t* v, long long v_token, long long v_head,
+                            const uint16_t* o, long long o_token, long long o_head,
+                            const float* lse, const uint16_t* dO, long long do_token,
+                            long long do_head, const void* plan, size_t plan_bytes, int N, int M,
+                            int Hq, int Hkv, int D, float scale, int dtype, uint16_t* dq,
+                            long long dq_token, long long dq_head, uint16_t* dk,
+                            long long dk_token, long long dk_head, uint16_t* dv,
+                            long long dv_token, long long dv_head, void* ws, size_t ws_bytes,
                             unsigned flags, void* stream);
 
 /* ----------------------------------------------------------------------------

@@ -85,6 +85,8 @@ _SIGS = {
     "scfa_packed_plan_size": ([_I] * 5, _S),
     "scfa_packed_workspace_size": ([_I] * 7, _S),
     "scfa_packed_plan": ([_P, _P] + [_I] * 6 + [_P, _S, _P], _I),
+    "scfa_packed_bwd": ([_P, _L, _L] * 4 + [_P] + [_P, _L, _L] + [_P, _S] + [_I] * 5 + [_F, _I] + [_P, _L, _L] * 3
+                        + [_P, _S, _U, _P], _I),
     "scfa_packed_fwd": ([_P, _L, _L] * 3 + [_P, _S] + [_I] * 5 + [_F, _I, _P, _L, _L, _P, _P, _S, _U, _P], _I),
 }
 EXPORTED = tuple(_SIGS)
@@ -573,6 +575,22 @@ def scfa_packed_fwd(q, k, v, plan, scale, o, lse, ws, flags=0, stream=None):
     _launch("scfa_packed_fwd", dev, stream, *rows[0], *rows[1], *rows[2], plan.data_ptr(),
             _ws_bytes("scfa_packed_fwd", plan, dev), N, M, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), *rows[3], lse.data_ptr(),
             ws.data_ptr(), _ws_bytes("scfa_packed_fwd", ws, dev), flags)
+
+
+def scfa_packed_bwd(q, k, v, o, lse, do, plan, scale, dq, dk, dv, ws, flags=0, stream=None):
+    """Gradients of scfa_packed_fwd for dO = do [N, Hq, D]: dq [N, Hq, D], dk, dv [M, Hkv, D], those of shared key heads
+    summed over their query heads. o, lse are the forward's. Rows of no sequence are left as they were."""
+    N, Hq, D = q.shape
+    M, Hkv = k.shape[:2]
+    dev, dt = q.get_device(), q.dtype
+    rows = [(t.data_ptr(), *_rows4("scfa_packed_bwd", key, t, n, h, D, dt, dev))
+            for key, t, n, h in (("q", q, N, Hq), ("k", k, M, Hkv), ("v", v, M, Hkv), ("o", o, N, Hq), ("do", do, N, Hq),
+                                 ("dq", dq, N, Hq), ("dk", dk, M, Hkv), ("dv", dv, M, Hkv))]
+    if not _is(lse, torch.float32, dev, N * Hq):
+        _refuse("scfa_packed_bwd", dev, lse=(lse, torch.float32, N * Hq))
+    _launch("scfa_packed_bwd", dev, stream, *rows[0], *rows[1], *rows[2], *rows[3], lse.data_ptr(), *rows[4],
+            plan.data_ptr(), _ws_bytes("scfa_packed_bwd", plan, dev), N, M, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), *rows[5],
+            *rows[6], *rows[7], ws.data_ptr(), _ws_bytes("scfa_packed_bwd", ws, dev), flags)
 
 
 # ---------------------------------------------------------------- tiles

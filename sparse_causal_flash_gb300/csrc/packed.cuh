@@ -48,7 +48,7 @@ struct PackHeader {
   int list_status[kLists];  // (each list is built by a CTA of its own)
   int pad0;
   long long entries[kLists];  // byte offsets from the plan's start
-  long long qtiles;           // int2 (first token, tokens) of each query tile
+  long long qtiles;           // int4 (first token, tokens, last key of the first token, 0) of each query tile
   long long bytes;
   int pad[38];
 };
@@ -82,7 +82,7 @@ inline bool pack_plan_layout(int N, int M, int R, int Hq, int Hkv, int sms, Pack
   };
   w.pre = take(static_cast<size_t>(kLists + 1) * (R + 1) * sizeof(int));
   for (int i = 0; i < kLists; ++i) w.units[i] = take(static_cast<size_t>(w.most[i]) * sizeof(int2));
-  w.qtiles = take((static_cast<size_t>(N / tpt) + R) * sizeof(int2));
+  w.qtiles = take((static_cast<size_t>(N / tpt) + R) * sizeof(int4));
   for (int i = 0; i < kLists; ++i) w.entries[i] = take(static_cast<size_t>(w.most[i]) * sizeof(PackEntry));
   w.total = off;
   *L = w;

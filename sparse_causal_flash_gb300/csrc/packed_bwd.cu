@@ -1,0 +1,953 @@
+// Attention over packed sequences with shared key heads, backward: dQ, dK and dV from dO.
+//
+// With P = 2^(s scale log2(e) - lse log2(e)) recomputed from q, k and the forward's lse, delta = rowsum(dO * O),
+// dP = dO V^T and dS = P (dP - delta):  dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
+//
+// Three kernels. `packed_stats_kernel` writes -lse log2(e), -delta and the last visible key of every query row, in rows
+// of query tiles. `packed_dq_kernel` holds a query tile and walks its key tiles (S, dP, dQ: three products a tile);
+// `packed_dkv_kernel` holds a key tile and walks the query tiles of all its heads (S^T, dP^T, dV, dK: four). Seven
+// products a tile pair where one kernel for all would do five, and no sums in memory: such a kernel has to add its dQ
+// tiles into fp32 rows across CTAs (64 KB per tile pair through L2, in an order that changes from run to run, with a
+// pass to clear and one to convert), which held the one-kernel backward of the tile-list attention to 820-870 TFLOP/s at
+// 128 channels. Here the gradients of heads that share a key head are summed in TMEM and every result is the same bits on
+// every run.
+//
+// P, dS are fp32 up to one rounding to the rows' type for the products that take them; every sum is fp32; scale comes in
+// at the end. Rows that lie behind a sequence's last in a tile are masked (bits, so NaN stays out), those among the 16
+// rows of the last MMA step zeroed in shared memory where they are summed over.
+//
+// Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
+// MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane). Chunks of cut pieces are
+// joined by the last to arrive, in the order of the chunks.
+#include <climits>
+#include <type_traits>
+
+#include "packed.cuh"
+
+namespace scfa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsFew = 72, kRegsMany = 216;  // 128 x 72 + 256 x 216 = 384 x 168, what a CTA starts with
+constexpr int kSlots = 3;                      // items known ahead
+constexpr int kStatStages = 3;
+
+struct PItem {
+  PackEntry e;
+  int head;  // -1: no more work
+  int pad[15];
+};
+
+struct PBwdParams {
+  const char* plan;
+  long long plan_bytes;
+  int N, M, Hq, Hkv, G, tpt, D;
+  float scale, scale_log2;
+  const uint16_t *o, *dO;
+  long long ot, oh, dot, doh;
+  const float* lse;
+  uint16_t *dq, *dk, *dv;
+  long long dqt, dqh, dkt, dkh, dvt, dvh;
+  float* stats;             // [3][tiles][Hkv][128]
+  long long stats_bytes;    // room for them
+  int* counter;
+  int* arrivals;            // [cut][Hkv]
+  float* part;
+  int stall;
+  int* status;
+};
+
+__device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
+  const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
+  const int s = pack_plan_status(h, p.plan_bytes, p.N, p.M, p.Hq, p.Hkv);
+  if (s != SCFA_OK) return s;
+  return 3ll * h->n_qtiles * p.Hkv * kTile * static_cast<long long>(sizeof(float)) > p.stats_bytes ? SCFA_ERR_WORKSPACE : SCFA_OK;
+}
+
+// ------------------------------------------------------------------ row statistics
+// A warp takes 32 / (D / 8) rows at a time, a 16-byte piece of O and dO per lane. Bounded by HBM: both are read once.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant__ PBwdParams p) {
+  constexpr int L = D / 8, RW = 32 / L;
+  const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
+  const int status = bwd_plan_status(p);
+  if (status != SCFA_OK) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, status);
+    return;
+  }
+  const int4* const tiles = reinterpret_cast<const int4*>(p.plan + h->qtiles);
+  const int lane = threadIdx.x & 31, ch = lane % L;
+  const long long n = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;  // rows
+  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 32) * RW;
+  for (long long r0 = (static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * RW; r0 < n; r0 += step) {
+    const long long at = r0 + lane / L;  // (n is a multiple of 128)
+    const int row = static_cast<int>(at % kTile), head = static_cast<int>(at / kTile % p.Hkv);
+    const int4 t = __ldg(tiles + at / kTile / p.Hkv);
+    const int tok = row / p.G, qh = head * p.G + row - tok * p.G;
+    const bool live = tok < t.y;
+    float s = 0.f;
+    if (live) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p.o + static_cast<long long>(t.x + tok) * p.ot + qh * p.oh + ch * 8);
+      const uint4 b = *reinterpret_cast<const uint4*>(p.dO + static_cast<long long>(t.x + tok) * p.dot + qh * p.doh + ch * 8);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = c4_unpack<F16>(aw[i]), y = c4_unpack<F16>(bw[i]);
+        s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+      }
+    }
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (ch == 0) {
+      const float lse = live ? p.lse[static_cast<long long>(t.x + tok) * p.Hq + qh] : -INFINITY;
+      // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
+      p.stats[at] = lse == -INFINITY ? -INFINITY : -(lse * kPackLog2e);
+      p.stats[n + at] = live && lse != -INFINITY ? -s : 0.f;
+      reinterpret_cast<int*>(p.stats)[2 * n + at] = live ? t.z + tok : -1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ what both kernels share
+// The next piece of work into its slot, by the whole producer warp; false at the end.
+__device__ __forceinline__ bool next_item(PItem* items, uint64_t* full, uint64_t* empty, int it, const PackEntry* entries,
+                                          int n_work, int Hkv, int* counter, int lane, volatile int* abort_flag, int* status,
+                                          bool& ok) {
+  const int slot = it % kSlots;
+  ok = warp_wait(&empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, status);
+  if (!ok) return false;
+  int w = 0;
+  if (lane == 0) w = atomicAdd(counter, 1);
+  w = __shfl_sync(0xffffffffu, w, 0);
+  const int head = w < n_work ? w % Hkv : -1;
+  if (head >= 0 && lane < 16)
+    reinterpret_cast<int*>(&items[slot].e)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / Hkv) + lane);
+  if (lane == 0) items[slot].head = head;
+  warp_arrive(&full[slot]);
+  return head >= 0;
+}
+
+// Leave the rows of an accumulator as a chunk's share: 16 rows of a warp's 32, as quad_rows gives them.
+template <int D>
+__device__ __forceinline__ void leave_quads(float* mine, const uint32_t (&acc)[D / 64][32], int row) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + 2 * (lane & 3)) =
+          make_float2(__uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u]), __uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u + 1]));
+}
+template <int D>
+__device__ __forceinline__ void join_quads(uint32_t (&acc)[D / 64][32], const float* base, long long stride, int chunks, int row) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int cc = 0; cc < D / 64; ++cc)
+#pragma unroll
+    for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
+  for (int c = 0; c < chunks; ++c)
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (row + 8 * u) * D + 8 * i + 2 * (lane & 3)));
+        uint32_t* y = &acc[i >> 3][(i & 7) * 4 + 2 * u];
+        y[0] = __float_as_uint(__uint_as_float(y[0]) + x.x), y[1] = __float_as_uint(__uint_as_float(y[1]) + x.y);
+      }
+}
+
+// ------------------------------------------------------------------ dQ
+// TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. Products in the order
+// S(j+1) dP(j+1) dQ(j): the softmax warps take S and dP of a tile into registers while dQ of the tile before runs, and
+// have both other products to make dS from them, so the tensor cores wait for neither. K stays for two products.
+template <int D>
+struct __align__(1024) DqSmem {
+  static constexpr int kSubs = D / 64, kQs = D == 64 ? 2 : 1, kKs = D == 64 ? 4 : 3, kVs = D == 64 ? 4 : 2;
+  uint8_t q[kQs][kSubs][kPackSub];
+  uint8_t dO[kQs][kSubs][kPackSub];
+  uint8_t k[kKs][kSubs][kPackSub];
+  uint8_t v[kVs][kSubs][kPackSub];
+  PItem item[kSlots];
+  uint64_t q_full[kQs], q_empty[kQs], k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
+  uint64_t s_full, s_free, ds_full, ds_free[2], dq_full, dq_empty, tail, drain, sync, item_full[kSlots], item_empty[kSlots];
+  uint32_t tmem_base;
+  int abort_flag, last;
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                 const __grid_constant__ PBwdParams p) {
+  using Sm = DqSmem<D>;
+  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kKs = Sm::kKs, kVs = Sm::kVs;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + pad);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
+  const int window = h->window, n_work = h->n_entries[kListDq] * p.Hkv, used = p.G * p.tpt;
+  const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
+    for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < kVs; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], 1);
+    mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, 8), mbar_init(&sm.ds_full, 8);
+    mbar_init(&sm.ds_free[0], 1), mbar_init(&sm.ds_free[1], 1);
+    mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, 8), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, 8);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
+  }
+  if (used < kTile) {  // rows that no copy writes: zero for good
+    for (int s = 0; s < kQs; ++s) {
+      zero_tile_rows(sm.q[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+      zero_tile_rows(sm.dO[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* const abort_flag = &sm.abort_flag;
+
+  if (warp < 4) {
+    regs_release<kRegsFew>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDq]);
+      int q_it = 0, k_it = 0, v_it = 0, tails = 0, unmarked = -1;  // unmarked: K tile whose zeros an abort kept from being written
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
+        const PackEntry& e = sm.item[it % kSlots].e;
+        const int head = sm.item[it % kSlots].head, a = e.a, b = e.b;
+        if (a == b) continue;
+        if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
+        {
+          const int s = q_it % kQs;
+          ok = warp_wait(&sm.q_empty[s], ((q_it / kQs) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.q_full[s], 2 * D * used * 2);
+            for (int sub = 0; sub < kSubs; ++sub) {
+              tma_load_3d(sm.q[s][sub], &tm_q, &sm.q_full[s], sub * 64, head * p.G, e.q0);
+              tma_load_3d(sm.dO[s][sub], &tm_do, &sm.q_full[s], sub * 64, head * p.G, e.q0);
+            }
+          }
+          ++q_it;
+        }
+        for (int j = a; j < b && ok; ++j) {
+          const int valid = e.m - j * kTile;
+          const bool cut = valid < kTile && (valid & 15) != 0;
+          const int s = k_it % kKs, vs = v_it % kVs;
+          ok = warp_wait(&sm.k_empty[s], ((k_it / kKs) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            uint64_t* const kb = cut ? &sm.tail : &sm.k_full[s];
+            mbar_arrive_expect_tx(kb, D * kTile * 2);
+            for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.k[s][sub], &tm_k, kb, sub * 64, head, e.k0 + j * kTile);
+          }
+          ++k_it;
+          if (cut) {
+            ok = warp_wait(&sm.tail, tails & 1, abort_flag, p.status);
+            ++tails;
+            if (!ok) {
+              unmarked = k_it - 1;
+              break;
+            }
+            zero_tile_rows(sm.k[s][0], kSubs, valid, (valid + 15) & ~15, lane, 32);
+            fence_proxy_async_smem();
+            warp_arrive(&sm.k_full[s]);
+          }
+          ok = warp_wait(&sm.v_empty[vs], ((v_it / kVs) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.v_full[vs], D * kTile * 2);
+            for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.v[vs][sub], &tm_v, &sm.v_full[vs], sub * 64, head, e.k0 + j * kTile);
+          }
+          ++v_it;
+        }
+      }
+      if (lane == 0) {
+        // every copy issued has landed before the CTA exits, also after an abort
+        if (tails > 0) mbar_wait_drain(&sm.tail, (tails - 1) & 1, p.status);
+        for (int d = 1; d <= kKs && d <= k_it; ++d)
+          if (k_it - d != unmarked) mbar_wait_drain(&sm.k_full[(k_it - d) % kKs], ((k_it - d) / kKs) & 1, p.status);
+        for (int d = 1; d <= kVs && d <= v_it; ++d) mbar_wait_drain(&sm.v_full[(v_it - d) % kVs], ((v_it - d) / kVs) & 1, p.status);
+        for (int d = 1; d <= kQs && d <= q_it; ++d) mbar_wait_drain(&sm.q_full[(q_it - d) % kQs], ((q_it - d) / kQs) & 1, p.status);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = pack_idesc<F16>(kTile, kTile, 0, 0), idesc_q = pack_idesc<F16>(kTile, D, 0, 1);
+        constexpr uint32_t kTile16 = (kSubs * kPackSub) >> 4;
+        const uint32_t qd = desc_low(smem_u32(sm.q[0][0]), 16), dod = desc_low(smem_u32(sm.dO[0][0]), 16);
+        const uint32_t kd = desc_low(smem_u32(sm.k[0][0]), 16), vd = desc_low(smem_u32(sm.v[0][0]), 16);
+        const uint32_t kn = desc_low(smem_u32(sm.k[0][0]), kPackSub);
+        int q_it = 0, kv = 0, n_q = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          const int slot = it % kSlots;
+          if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+          if (sm.item[slot].head < 0) break;
+          const int a = sm.item[slot].e.a, b = sm.item[slot].e.b, m_keys = sm.item[slot].e.m;
+          if (a < b) {
+            const int qs = q_it % kQs;
+            auto scores = [&](int i) -> bool {  // S and dP of key tile number i
+              const int s = i % kKs, vs = i % kVs;
+              if (i > 0 && !mbar_wait(&sm.s_free, (i - 1) & 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.k_full[s], (i / kKs) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_ss_steps<0, D / 16>(tmem, qd + qs * kTile16, kd + s * kTile16, idesc_s, false);
+              if (!mbar_wait(&sm.v_full[vs], (i / kVs) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_ss_steps<0, D / 16>(tmem + 128, dod + qs * kTile16, vd + vs * kTile16, idesc_s, false);
+              tc_commit(&sm.s_full);
+              tc_commit(&sm.v_empty[vs]);
+              return true;
+            };
+            ok = mbar_wait(&sm.q_full[qs], (q_it / kQs) & 1, abort_flag, p.status) && scores(kv);
+            for (int j = a; j < b && ok; ++j, ++kv) {
+              if (j + 1 < b) ok = scores(kv + 1);
+              else tc_commit(&sm.q_empty[qs]);
+              if (!ok) break;
+              if (j == a && !mbar_wait(&sm.dq_empty, (n_q & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+              if (!mbar_wait(&sm.ds_full, kv & 1, abort_flag, p.status)) { ok = false; break; }
+              tc_fence_after();
+              const uint32_t ds = tmem + 384u + 64u * (kv & 1), bk = kn + (kv % kKs) * kTile16;
+              const int steps = min(kTile / 16, (m_keys - j * kTile + 15) >> 4);
+              if (steps == 8) mma_ts_steps<0, 8>(tmem + 256, ds, bk, idesc_q, j > a, 8);
+              else mma_ts_steps<0, 8>(tmem + 256, ds, bk, idesc_q, j > a, steps);
+              tc_commit(&sm.k_empty[kv % kKs]);
+              tc_commit(&sm.ds_free[kv & 1]);
+            }
+            if (!ok) break;
+            tc_commit(&sm.dq_full);
+            ++n_q, ++q_it;
+          }
+          mbar_arrive(&sm.item_empty[slot]);
+        }
+        tc_commit(&sm.drain);
+        mbar_wait_drain(&sm.drain, 0, p.status);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_take<kRegsMany>();
+    const int hc = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int r_tok = r / p.G;
+    int n = 0, n_q = 0, n_sync = 0;
+    for (int it = 0;; ++it) {
+      const int slot = it % kSlots;
+      if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+      const PackEntry& e = sm.item[slot].e;
+      const int head = sm.item[slot].head;
+      if (head < 0) break;
+      const int a = e.a, b = e.b, first = e.diag, n_tok = e.n_tok;
+      const bool valid = r_tok < n_tok;
+      const int hi = valid ? first + r_tok : -1;
+      const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
+      const float nl = p.stats[at], nd = p.stats[n_stats + at];
+      auto tile = [&](auto masked, int j) -> bool {
+        if (!warp_wait(&sm.s_full, n & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        uint32_t sr[64], dr[64];
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          tmem_ld32(lanes + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+          tmem_ld32(lanes + 128 + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
+        }
+        tmem_wait_ld();
+        tmem_ld_fence(sr);
+        tmem_ld_fence(dr);
+        tc_fence_before();
+        warp_arrive(&sm.s_free);
+        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), nd2 = f2(nd, nd);
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          float x0, x1;
+          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, nl2), x0, x1);
+          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+          f2_split(mul2(f2(x0, x1), add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2)), x0, x1);
+          pk[c >> 1] = c4_pack<F16>(x0, x1);
+        }
+        if (decltype(masked)::value) {
+          // lo <= column <= lim as one unsigned comparison
+          const int lim = hi - j * kTile - hc * 64, lo = window ? max(lim - window + 1, -kTile) : -kTile;
+          const uint32_t span = lim < lo ? 0u : static_cast<uint32_t>(lim - lo) + 1u;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2)
+            pk[c >> 1] &= (static_cast<uint32_t>(c - lo) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(c + 1 - lo) < span ? 0xffff0000u : 0u);
+        }
+        if (n > 1) {  // dQ two tiles back has read this buffer
+          if (!warp_wait(&sm.ds_free[n & 1], ((n >> 1) - 1) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+        }
+        const uint32_t ds = lanes + 384u + 64u * (n & 1) + hc * 32;
+        tmem_st16(ds, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+        tmem_st16(ds + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.ds_full);
+        ++n;
+        return true;
+      };
+      // tiles [plain, masked) are seen whole by every row, as in the forward
+      const int plain = window ? min(b, max(a, (first + n_tok - window + kTile - 1) / kTile)) : a;
+      const int masked = max(plain, min(b, max(0, first + 1) / kTile));
+      bool ok = true;
+      int j = a;
+      for (int part = 0; part < 2 && ok; ++part) {
+        const int stop = part ? b : plain;
+        for (; j < stop && ok; ++j) ok = tile(std::true_type{}, j);
+        if (part == 0)
+          for (; j < masked && ok; ++j) ok = tile(std::false_type{}, j);
+      }
+      if (!ok) break;
+      // this warp's 16 rows of dQ
+      uint32_t acc[D / 64][32];
+      if (a < b) {
+        if (!warp_wait(&sm.dq_full, n_q & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        ++n_q;
+      }
+      quad_rows<D>(acc, lanes + 256, hc, a < b);
+      if (a < b) {
+        tc_fence_before();
+        warp_arrive(&sm.dq_empty);
+      }
+      const int row = quarter * 32 + hc * 16 + (lane >> 2);
+      if (e.slot >= 0) {
+        const long long stride = static_cast<long long>(p.Hkv) * kTile * D;
+        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * kTile * D;
+        leave_quads<D>(base + e.chunk * stride, acc, row);
+        __threadfence();
+        warp_arrive(&sm.sync);
+        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (warp == 4 && lane == 0) sm.last = atomicAdd(p.arrivals + static_cast<long long>(e.cut) * p.Hkv + head, 1) == e.chunks - 1;
+        warp_arrive(&sm.sync);
+        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (!*reinterpret_cast<volatile int*>(&sm.last)) {
+          warp_arrive(&sm.item_empty[slot]);
+          continue;
+        }
+        __threadfence();
+        join_quads<D>(acc, base, stride, e.chunks, row);
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - t * p.G;
+        quad_store<D, F16>(p.dq + static_cast<long long>(e.q0 + t) * p.dqt + qh * p.dqh, t < n_tok, acc, u, p.scale);
+      }
+      warp_arrive(&sm.item_empty[slot]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dK and dV
+// Tiles are transposed: lanes are keys, columns queries. D = 128: S^T [0,128), dP^T [128,256), dV, dK behind. A warpgroup
+// writes P^T and dS^T of its 64 queries over its own half of S^T, so the two never wait for each other, and products come
+// in the order dP(t+1) dV(t) dK(t) S(t+1): dP^T is in registers long before its turn, and the tensor cores run dP(t+1)
+// while P(t) is made. D = 64: P^T and dS^T have columns of their own and S(t+1), dP(t+1) run under the softmax of t.
+template <int D>
+struct __align__(1024) DkvSmem {
+  static constexpr int kSubs = D / 64, kQs = D == 64 ? 4 : 2, kKs = D == 64 ? 2 : 1;
+  uint8_t k[kKs][kSubs][kPackSub];
+  uint8_t v[kKs][kSubs][kPackSub];
+  uint8_t q[kQs][kSubs][kPackSub];
+  uint8_t dO[kQs][kSubs][kPackSub];
+  alignas(16) float nl[kStatStages][kTile];
+  alignas(16) float nd[kStatStages][kTile];
+  alignas(16) int hi[kStatStages][kTile];
+  PItem item[kSlots];
+  uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kQs], do_empty[kQs];
+  uint64_t st_full[kStatStages], st_empty[kStatStages];
+  uint64_t s_full, dp_full, s_free, p_full, ds_full, pd_free, acc_full, acc_empty, tail[2], drain, sync;
+  uint64_t item_full[kSlots], item_empty[kSlots];
+  uint32_t tmem_base;
+  int abort_flag, last;
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                  const __grid_constant__ PBwdParams p) {
+  using Sm = DkvSmem<D>;
+  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kKs = Sm::kKs;
+  constexpr bool kOwn = D == 64;
+  constexpr uint32_t colDP = 128, colP = kOwn ? 256 : 0, colDS = kOwn ? 320 : 32, colDV = kOwn ? 384 : 256, colDK = kOwn ? 448 : 384;
+  constexpr uint32_t kHalfCols = kOwn ? 32 : 64;  // from the first 64 queries' P^T to the others'
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + pad);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
+  const int window = h->window, n_work = h->n_entries[kListDkv] * p.Hkv, used = p.G * p.tpt;
+  const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
+    for (int s = 0; s < kQs; ++s)
+      mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1), mbar_init(&sm.do_full[s], 1), mbar_init(&sm.do_empty[s], 1);
+    for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_empty[s], 8);
+    mbar_init(&sm.s_full, 1), mbar_init(&sm.dp_full, 1), mbar_init(&sm.s_free, 8), mbar_init(&sm.p_full, 8), mbar_init(&sm.ds_full, 8);
+    mbar_init(&sm.pd_free, 1), mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, 8), mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1);
+    mbar_init(&sm.drain, 1), mbar_init(&sm.sync, 8);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
+    sm.abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
+  }
+  if (used < kTile) {  // rows that no copy writes: zero for good
+    for (int s = 0; s < kQs; ++s) {
+      zero_tile_rows(sm.q[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+      zero_tile_rows(sm.dO[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+    }
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* const abort_flag = &sm.abort_flag;
+
+  if (warp < 4) {
+    regs_release<kRegsFew>();
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDkv]);
+      int k_it = 0, q_it = 0, do_it = 0, st_it = 0, tails[2] = {0, 0}, unmarked[2] = {-1, -1};
+      bool ok = true;
+      // Q or dO tile of query tile i into its ring; rows behind the sequence's
+      // last, up to the last MMA step's end, become zero
+      auto load = [&](int which, const CUtensorMap* map, uint8_t (*ring)[kSubs][kPackSub], uint64_t* full, uint64_t* empty, int& n, int head,
+                      const PackEntry& e, int i) -> bool {
+        const int s = n % kQs, rows = min(p.tpt, e.m - i * p.tpt) * p.G;
+        const bool cut = rows < used && (rows & 15) != 0;
+        if (!warp_wait(&empty[s], ((n / kQs) & 1) ^ 1, abort_flag, p.status)) return false;
+        if (lane == 0) {
+          uint64_t* const bar = cut ? &sm.tail[which] : &full[s];
+          mbar_arrive_expect_tx(bar, D * used * 2);
+          for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(ring[s][sub], map, bar, sub * 64, head * p.G, e.q0 + i * p.tpt);
+        }
+        ++n;
+        if (cut) {
+          const bool got = warp_wait(&sm.tail[which], tails[which] & 1, abort_flag, p.status);
+          ++tails[which];
+          if (!got) {
+            unmarked[which] = n - 1;
+            return false;
+          }
+          zero_tile_rows(ring[s][0], kSubs, rows, (rows + 15) & ~15, lane, 32);
+          fence_proxy_async_smem();
+          warp_arrive(&full[s]);
+        }
+        return true;
+      };
+      for (int it = 0; ok; ++it) {
+        if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
+        const PackEntry& e = sm.item[it % kSlots].e;
+        const int head = sm.item[it % kSlots].head, a = e.a, b = e.b;
+        if (a == b) continue;
+        if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
+        {
+          const int s = k_it % kKs;
+          ok = warp_wait(&sm.k_empty[s], ((k_it / kKs) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.k_full[s], 2 * D * kTile * 2);
+            for (int sub = 0; sub < kSubs; ++sub) {
+              tma_load_3d(sm.v[s][sub], &tm_v, &sm.k_full[s], sub * 64, head, e.k0);
+              tma_load_3d(sm.k[s][sub], &tm_k, &sm.k_full[s], sub * 64, head, e.k0);
+            }
+          }
+          ++k_it;
+        }
+        for (int i = a; i < b && ok; ++i) {
+          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, head, e, i);
+          if (!ok) break;
+          const int s = st_it % kStatStages;
+          ok = warp_wait(&sm.st_empty[s], ((st_it / kStatStages) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            const float* const st = p.stats + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile;
+            mbar_arrive_expect_tx(&sm.st_full[s], 3 * kTile * 4);
+            bulk_load(sm.nl[s], st, kTile * 4, &sm.st_full[s]);
+            bulk_load(sm.nd[s], st + n_stats, kTile * 4, &sm.st_full[s]);
+            bulk_load(sm.hi[s], st + 2 * n_stats, kTile * 4, &sm.st_full[s]);
+          }
+          ++st_it;
+          ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, head, e, i);
+        }
+      }
+      if (lane == 0) {
+        // every copy issued has landed before the CTA exits, also after an abort
+        for (int x = 0; x < 2; ++x)
+          if (tails[x] > 0) mbar_wait_drain(&sm.tail[x], (tails[x] - 1) & 1, p.status);
+        for (int d = 1; d <= kQs && d <= q_it; ++d)
+          if (q_it - d != unmarked[0]) mbar_wait_drain(&sm.q_full[(q_it - d) % kQs], ((q_it - d) / kQs) & 1, p.status);
+        for (int d = 1; d <= kQs && d <= do_it; ++d)
+          if (do_it - d != unmarked[1]) mbar_wait_drain(&sm.do_full[(do_it - d) % kQs], ((do_it - d) / kQs) & 1, p.status);
+        for (int d = 1; d <= kStatStages && d <= st_it; ++d)
+          mbar_wait_drain(&sm.st_full[(st_it - d) % kStatStages], ((st_it - d) / kStatStages) & 1, p.status);
+        for (int d = 1; d <= kKs && d <= k_it; ++d) mbar_wait_drain(&sm.k_full[(k_it - d) % kKs], ((k_it - d) / kKs) & 1, p.status);
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = pack_idesc<F16>(kTile, kTile, 0, 0), idesc_a = pack_idesc<F16>(kTile, D, 0, 1);
+        constexpr uint32_t kTile16 = (kSubs * kPackSub) >> 4;
+        const uint32_t kd = desc_low(smem_u32(sm.k[0][0]), 16), vd = desc_low(smem_u32(sm.v[0][0]), 16);
+        const uint32_t qd = desc_low(smem_u32(sm.q[0][0]), 16), dod = desc_low(smem_u32(sm.dO[0][0]), 16);
+        const uint32_t qn = desc_low(smem_u32(sm.q[0][0]), kPackSub), don = desc_low(smem_u32(sm.dO[0][0]), kPackSub);
+        int k_it = 0, t = 0, n_acc = 0;
+        bool ok = true;
+        for (int it = 0; ok; ++it) {
+          const int slot = it % kSlots;
+          if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+          if (sm.item[slot].head < 0) break;
+          const int a = sm.item[slot].e.a, b = sm.item[slot].e.b, m_tok = sm.item[slot].e.m;
+          if (a < b) {
+            const int ks = k_it % kKs;
+            // t: query tile number over the CTA's whole work
+            auto do_dp = [&](int n) -> bool {
+              if (n > 0 && !kOwn && !mbar_wait(&sm.s_free, (n - 1) & 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.do_full[n % kQs], (n / kQs) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_ss_steps<0, D / 16>(tmem + colDP, vd + ks * kTile16, dod + (n % kQs) * kTile16, idesc_s, false);
+              if (!kOwn) tc_commit(&sm.dp_full);
+              return true;
+            };
+            auto do_s = [&](int n) -> bool {
+              if (!mbar_wait(&sm.q_full[n % kQs], (n / kQs) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_ss_steps<0, D / 16>(tmem, kd + ks * kTile16, qd + (n % kQs) * kTile16, idesc_s, false);
+              tc_commit(&sm.s_full);
+              return true;
+            };
+            auto scores = [&](int n) -> bool {  // D = 64: both, once the softmax has the last ones in registers
+              if (n > 0 && !mbar_wait(&sm.s_free, (n - 1) & 1, abort_flag, p.status)) return false;
+              return do_dp(n) && do_s(n);
+            };
+            ok = mbar_wait(&sm.k_full[ks], (k_it / kKs) & 1, abort_flag, p.status);
+            if (ok) ok = kOwn ? scores(t) : do_dp(t) && do_s(t);
+            for (int i = a; i < b && ok; ++i, ++t) {
+              const int s = t % kQs, steps = min(kTile / 16, (min(p.tpt, m_tok - i * p.tpt) * p.G + 15) >> 4);
+              if (i + 1 < b) ok = kOwn ? scores(t + 1) : do_dp(t + 1);
+              if (!ok) break;
+              if (i == a && !mbar_wait(&sm.acc_empty, (n_acc & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+              if (!mbar_wait(&sm.p_full, t & 1, abort_flag, p.status)) { ok = false; break; }
+              tc_fence_after();
+              // dV += P^T dO, dK += dS^T Q, the first 64 queries' columns and the others'
+              const uint32_t bo = don + s * kTile16, bq = qn + s * kTile16;
+              if (steps == 8) {
+                mma_ts_steps<0, 4>(tmem + colDV, tmem + colP, bo, idesc_a, i > a, 8);
+                mma_ts_steps<4, 8>(tmem + colDV, tmem + colP + kHalfCols - 32, bo, idesc_a, true, 8);
+              } else {
+                mma_ts_steps<0, 4>(tmem + colDV, tmem + colP, bo, idesc_a, i > a, steps);
+                mma_ts_steps<4, 8>(tmem + colDV, tmem + colP + kHalfCols - 32, bo, idesc_a, true, steps);
+              }
+              tc_commit(&sm.do_empty[s]);
+              if (!kOwn && !mbar_wait(&sm.ds_full, t & 1, abort_flag, p.status)) { ok = false; break; }
+              tc_fence_after();
+              if (steps == 8) {
+                mma_ts_steps<0, 4>(tmem + colDK, tmem + colDS, bq, idesc_a, i > a, 8);
+                mma_ts_steps<4, 8>(tmem + colDK, tmem + colDS + kHalfCols - 32, bq, idesc_a, true, 8);
+              } else {
+                mma_ts_steps<0, 4>(tmem + colDK, tmem + colDS, bq, idesc_a, i > a, steps);
+                mma_ts_steps<4, 8>(tmem + colDK, tmem + colDS + kHalfCols - 32, bq, idesc_a, true, steps);
+              }
+              tc_commit(&sm.q_empty[s]);
+              if (kOwn) tc_commit(&sm.pd_free);
+              if (!kOwn && i + 1 < b) ok = do_s(t + 1);
+            }
+            if (!ok) break;
+            tc_commit(&sm.acc_full);
+            tc_commit(&sm.k_empty[ks]);
+            ++n_acc, ++k_it;
+          }
+          mbar_arrive(&sm.item_empty[slot]);
+        }
+        tc_commit(&sm.drain);
+        mbar_wait_drain(&sm.drain, 0, p.status);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_take<kRegsMany>();
+    const int hc = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
+    int t = 0, n_acc = 0, n_sync = 0;
+    for (int it = 0;; ++it) {
+      const int slot = it % kSlots;
+      if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+      const PackEntry& e = sm.item[slot].e;
+      const int head = sm.item[slot].head;
+      if (head < 0) break;
+      const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
+      auto tile = [&](auto masked) -> bool {
+        const int ss = t % kStatStages;
+        uint32_t sr[64], dr[64], pk[32];
+        // dP^T first: it was there before S^T, and the next one may follow
+        if (!kOwn) {
+          if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(lanes + colDP + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
+          tmem_wait_ld();
+          tmem_ld_fence(dr);
+          tc_fence_before();
+          warp_arrive(&sm.s_free);
+        }
+        if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
+        if (!warp_wait(&sm.s_full, t & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          tmem_ld32(lanes + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+          if (kOwn) tmem_ld32(lanes + colDP + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
+        }
+        tmem_wait_ld();
+        tmem_ld_fence(sr);
+        if (kOwn) {
+          tmem_ld_fence(dr);
+          tc_fence_before();
+          warp_arrive(&sm.s_free);
+        }
+        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][hc * 64 + c]);
+          float x[4];
+          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, f2(l4.x, l4.y)), x[0], x[1]);
+          f2_split(fma2(f2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2, f2(l4.z, l4.w)), x[2], x[3]);
+          uint32_t keep[2] = {~0u, ~0u};
+          if (decltype(masked)::value) {
+            const int4 h4 = *reinterpret_cast<const int4*>(&sm.hi[ss][hc * 64 + c]);
+            keep[0] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
+            keep[1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = ex2_approx(x[i]);
+            sr[c + i] = __float_as_uint(x[i]);
+          }
+          pk[c >> 1] = c4_pack<F16>(x[0], x[1]) & keep[0];
+          pk[(c >> 1) + 1] = c4_pack<F16>(x[2], x[3]) & keep[1];
+        }
+        if (kOwn && t > 0) {  // dV, dK of the tile before have read P^T, dS^T
+          if (!warp_wait(&sm.pd_free, (t - 1) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+        }
+        tmem_st16(lanes + colP + hc * kHalfCols, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+        tmem_st16(lanes + colP + hc * kHalfCols + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+        if (!kOwn) {
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.p_full);
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][hc * 64 + c]);
+          float x[4];
+          f2_split(mul2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                        add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), f2(d4.x, d4.y))), x[0], x[1]);
+          f2_split(mul2(f2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])),
+                        add2(f2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), f2(d4.z, d4.w))), x[2], x[3]);
+          uint32_t keep[2] = {~0u, ~0u};
+          if (decltype(masked)::value) {
+            const int4 h4 = *reinterpret_cast<const int4*>(&sm.hi[ss][hc * 64 + c]);
+            keep[0] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
+            keep[1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
+          }
+          pk[c >> 1] = c4_pack<F16>(x[0], x[1]) & keep[0];
+          pk[(c >> 1) + 1] = c4_pack<F16>(x[2], x[3]) & keep[1];
+        }
+        warp_arrive(&sm.st_empty[ss]);
+        tmem_st16(lanes + colDS + hc * kHalfCols, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+        tmem_st16(lanes + colDS + hc * kHalfCols + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(kOwn ? &sm.p_full : &sm.ds_full);
+        ++t;
+        return true;
+      };
+      bool ok = true;
+      const int last_key = e.diag + kTile - 1;  // (of a whole tile)
+      for (int i = a; i < b && ok; ++i) {
+        const int first = i * p.tpt + e.shift;  // the last key of the tile's first token
+        const bool whole = first >= last_key && (i + 1) * p.tpt <= e.m && (!window || first + p.tpt - 1 - window < e.diag);
+        ok = whole ? tile(std::false_type{}) : tile(std::true_type{});
+      }
+      if (!ok) break;
+      if (a < b) {
+        if (!warp_wait(&sm.acc_full, n_acc & 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        ++n_acc;
+      }
+      // the first warpgroup writes dV, the second dK
+      const bool joined = e.slot >= 0;
+      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
+      float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + hc) * kTile * D;
+      const int row = quarter * 32 + (lane >> 2);
+      const uint32_t from = lanes + (hc ? colDK : colDV);
+      if (joined) {
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t acc[D / 64][32];
+          quad_rows<D>(acc, from, hf, a < b);
+          leave_quads<D>(base + e.chunk * stride, acc, row + 16 * hf);
+        }
+        if (a < b) {
+          tc_fence_before();
+          warp_arrive(&sm.acc_empty);
+        }
+        __threadfence();
+        warp_arrive(&sm.sync);
+        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (warp == 4 && lane == 0) sm.last = atomicAdd(p.arrivals + static_cast<long long>(e.cut) * p.Hkv + head, 1) == e.chunks - 1;
+        warp_arrive(&sm.sync);
+        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
+        ++n_sync;
+        if (!*reinterpret_cast<volatile int*>(&sm.last)) {
+          warp_arrive(&sm.item_empty[slot]);
+          continue;
+        }
+        __threadfence();
+      }
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t acc[D / 64][32];
+        if (joined) join_quads<D>(acc, base, stride, e.chunks, row + 16 * hf);
+        else quad_rows<D>(acc, from, hf, a < b);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = row + 16 * hf + 8 * u;
+          uint16_t* const dst = hc ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
+                                   : p.dv + static_cast<long long>(e.k0 + c) * p.dvt + head * p.dvh;
+          quad_store<D, F16>(dst, c < n_tok, acc, u, hc ? p.scale : 1.f);
+        }
+      }
+      if (!joined && a < b) {
+        tc_fence_before();
+        warp_arrive(&sm.acc_empty);
+      }
+      warp_arrive(&sm.item_empty[slot]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <typename Kernel>
+cudaError_t launch_one(Kernel kern, size_t smem, bool (&allowed)[64], const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                       const CUtensorMap& dO, const PBwdParams& p, int grid, cudaStream_t st) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !allowed[dev]) {  // (setting it twice does no harm)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) allowed[dev] = true;
+  }
+  kern<<<grid, kThreads, smem, st>>>(q, k, v, dO, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t launch_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, PBwdParams p, int sms,
+                       int slots, cudaStream_t st) {
+  static bool dq_allowed[64] = {}, dkv_allowed[64] = {};
+  constexpr size_t dq_smem = sizeof(DqSmem<D>) + 1024, dkv_smem = sizeof(DkvSmem<D>) + 1024;
+  static_assert(dq_smem <= 227 * 1024 && dkv_smem <= 227 * 1024, "shared memory per CTA");
+  packed_stats_kernel<D, F16><<<8 * sms, 256, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && p.M > 0) e = launch_one(packed_dkv_kernel<D, F16>, dkv_smem, dkv_allowed, q, k, v, dO, p, sms, st);
+  ++p.counter, p.arrivals += slots;
+  if (e == cudaSuccess && p.N > 0) e = launch_one(packed_dq_kernel<D, F16>, dq_smem, dq_allowed, q, k, v, dO, p, sms, st);
+  return e;
+}
+
+bool write_rows_ok(const void* p, long long token, long long head, int n, int H, int D) {
+  return p && !(reinterpret_cast<uintptr_t>(p) & 15u) && !((token | head) & 7) && !c4_rows_overlap(token, head, n, H, D);
+}
+
+}  // namespace
+}  // namespace scfa
+
+using namespace scfa;
+
+extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, long long q_head, const uint16_t* k, long long k_token,
+                                       long long k_head, const uint16_t* v, long long v_token, long long v_head, const uint16_t* o,
+                                       long long o_token, long long o_head, const float* lse, const uint16_t* dO, long long do_token,
+                                       long long do_head, const void* plan, size_t plan_bytes, int N, int M, int Hq, int Hkv, int D,
+                                       float scale, int dtype, uint16_t* dq, long long dq_token, long long dq_head, uint16_t* dk,
+                                       long long dk_token, long long dk_head, uint16_t* dv, long long dv_token, long long dv_head,
+                                       void* ws, size_t ws_bytes, unsigned flags, void* stream) {
+  if (!plan || !ws || N < 0 || M < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0) return SCFA_ERR_INVALID;
+  const float factor = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // to log2 units
+  if (!(scale > 0.f && factor < INFINITY)) return SCFA_ERR_INVALID;
+  if ((D != 64 && D != 128) || (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) || Hq / Hkv > kTile) return SCFA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * Hq >= (1ll << 31) - 256 || static_cast<long long>(M) * Hkv >= (1ll << 31) - 256) return SCFA_ERR_UNSUPPORTED;
+  const int sms = num_sms();
+  const PackWs w = pack_ws(true, D, sms);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.stats) return SCFA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < sizeof(PackHeader)) return SCFA_ERR_INVALID;
+  if (N > 0 && (!lse || !pack_rows_ok(q, q_token, q_head, N, Hq) || !pack_rows_ok(o, o_token, o_head, N, Hq) ||
+                !pack_rows_ok(dO, do_token, do_head, N, Hq) || !write_rows_ok(dq, dq_token, dq_head, N, Hq, D)))
+    return SCFA_ERR_INVALID;
+  if (M > 0 && (!pack_rows_ok(k, k_token, k_head, M, Hkv) || !pack_rows_ok(v, v_token, v_head, M, Hkv) ||
+                !write_rows_ok(dk, dk_token, dk_head, M, Hkv, D) || !write_rows_ok(dv, dv_token, dv_head, M, Hkv, D)))
+    return SCFA_ERR_INVALID;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* c = static_cast<char*>(ws);
+  if (cudaMemsetAsync(c, 0, w.clear, st) != cudaSuccess) return SCFA_ERR_CUDA;
+  if (N == 0 && M == 0) return SCFA_OK;
+  PBwdParams p = {};
+  p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
+  p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.D = D, p.scale = scale, p.scale_log2 = factor;
+  p.o = o, p.ot = o_token, p.oh = o_head, p.dO = dO, p.dot = do_token, p.doh = do_head, p.lse = lse;
+  p.dq = dq, p.dqt = dq_token, p.dqh = dq_head, p.dk = dk, p.dkt = dk_token, p.dkh = dk_head, p.dv = dv, p.dvt = dv_token, p.dvh = dv_head;
+  p.counter = reinterpret_cast<int*>(c + w.counters), p.arrivals = p.counter + 2;
+  p.part = reinterpret_cast<float*>(c + w.part), p.stats = reinterpret_cast<float*>(c + w.stats);
+  p.stats_bytes = static_cast<long long>(ws_bytes - w.stats);
+  p.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0, p.status = reinterpret_cast<int*>(c);
+  const bool f16 = dtype == SCFA_DTYPE_F16;
+  CUtensorMap tq = {}, tk = {}, tv = {}, tdo = {};
+  if (N > 0 && (!make_tmap_rows(&tq, q, f16, D, Hq, N, q_head, q_token, p.G, p.tpt) ||
+                !make_tmap_rows(&tdo, dO, f16, D, Hq, N, do_head, do_token, p.G, p.tpt)))
+    return SCFA_ERR_INVALID;
+  if (M > 0 && (!make_tmap_rows(&tk, k, f16, D, Hkv, M, k_head, k_token, 1, kTile) ||
+                !make_tmap_rows(&tv, v, f16, D, Hkv, M, v_head, v_token, 1, kTile)))
+    return SCFA_ERR_INVALID;
+  // without queries (or keys) no tile of them is ever copied: any valid map will do
+  if (N == 0) tq = tdo = tk;
+  if (M == 0) tk = tv = tq;
+  const int slots = pack_slots(sms);
+  const cudaError_t e = D == 64 ? (f16 ? launch_bwd<64, true>(tq, tk, tv, tdo, p, sms, slots, st) : launch_bwd<64, false>(tq, tk, tv, tdo, p, sms, slots, st))
+                                : (f16 ? launch_bwd<128, true>(tq, tk, tv, tdo, p, sms, slots, st) : launch_bwd<128, false>(tq, tk, tv, tdo, p, sms, slots, st));
+  if (e != cudaSuccess) return SCFA_ERR_CUDA;
+  if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
+  return SCFA_OK;
+}

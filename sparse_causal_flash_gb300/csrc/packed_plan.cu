@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     units[g] = make_int2(b - a, lo);
     sum += b - a, most = max(most, b - a);
     if (list == kListDq)
-      reinterpret_cast<int2*>(p.plan + p.L.qtiles)[g] = make_int2(q0 + i * p.tpt, min(p.tpt, n - i * p.tpt));
+      reinterpret_cast<int4*>(p.plan + p.L.qtiles)[g] = make_int4(q0 + i * p.tpt, min(p.tpt, n - i * p.tpt), i * p.tpt + m - n, 0);
   }
   most = __reduce_max_sync(0xffffffffu, most);
 #pragma unroll
