@@ -35,7 +35,8 @@ struct PackEntry {
   int slot;    // first partial slot of the cut entry (per key head); -1: not cut
   int chunk, chunks;
   int cut;     // number of the cut entry
-  int pad[3];
+  int head;    // (in shared memory) key head, -1: no more work
+  int pad[2];
 };
 static_assert(sizeof(PackEntry) == 64, "entries are copied as 16 words");
 
@@ -237,37 +238,35 @@ __device__ __forceinline__ void tmem_st_quad_half(uint32_t taddr, const uint32_t
          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Rows 16 hf .. 16 hf + 15 of the warp's 32 (its lanes start at taddr), all D columns, as tmem_ld_quad gives them; zeros
+// Rows 16 hf .. 16 hf + 15 of the warp's 32 (its lanes start at taddr), W columns, as tmem_ld_quad16 gives them; zeros
 // without `some`.
-template <int D>
-__device__ __forceinline__ void quad_rows(uint32_t (&acc)[D / 64][32], uint32_t taddr, int hf, bool some) {
+template <int W>
+__device__ __forceinline__ void quad_part(uint32_t (&acc)[W / 32][16], uint32_t taddr, int hf, bool some) {
   if (some) {
 #pragma unroll
-    for (int cc = 0; cc < D / 64; ++cc) tmem_ld_quad(taddr + (static_cast<uint32_t>(hf * 16) << 16) + cc * 64, acc[cc]);
+    for (int cc = 0; cc < W / 32; ++cc) tmem_ld_quad16(taddr + (static_cast<uint32_t>(hf * 16) << 16) + cc * 32, acc[cc]);
     tmem_wait_ld();
 #pragma unroll
-    for (int cc = 0; cc < D / 64; ++cc) tmem_ld_fence(acc[cc]);
+    for (int cc = 0; cc < W / 32; ++cc) tmem_ld_fence(acc[cc]);
   } else {
 #pragma unroll
-    for (int cc = 0; cc < D / 64; ++cc)
+    for (int cc = 0; cc < W / 32; ++cc)
 #pragma unroll
-      for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
+      for (int c = 0; c < 16; ++c) acc[cc][c] = 0u;
   }
 }
 // One of the two rows that a quad of lanes holds (u), times f, in the rows' type to `row`. Four words change places
 // inside the quad so that each lane has 16 bytes and the quad 64 in a row: a quarter of the stores' lines that whole rows
 // per thread would touch (those took 6,500 cycles for a tile of 128 x 128).
-template <int D, bool F16>
-__device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint32_t (&acc)[D / 64][32], int u, float f) {
+template <int W, bool F16>
+__device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint32_t (&acc)[W / 32][16], int u, float f) {
   const int t = threadIdx.x & 3;
 #pragma unroll
-  for (int b = 0; b < D / 32; ++b) {
+  for (int b = 0; b < W / 32; ++b) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int g = 4 * b + i;
-      w[i] = c4_pack<F16>(__uint_as_float(acc[g >> 3][(g & 7) * 4 + 2 * u]) * f, __uint_as_float(acc[g >> 3][(g & 7) * 4 + 2 * u + 1]) * f);
-    }
+    for (int i = 0; i < 4; ++i)
+      w[i] = c4_pack<F16>(__uint_as_float(acc[b][i * 4 + 2 * u]) * f, __uint_as_float(acc[b][i * 4 + 2 * u + 1]) * f);
     const uint32_t x0 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[0] : w[1], 1), x1 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[2] : w[3], 1);
     const uint32_t p0 = t & 1 ? x0 : w[0], p1 = t & 1 ? w[1] : x0, p2 = t & 1 ? x1 : w[2], p3 = t & 1 ? w[3] : x1;
     const uint32_t y0 = __shfl_xor_sync(0xffffffffu, t & 2 ? p0 : p2, 2), y1 = __shfl_xor_sync(0xffffffffu, t & 2 ? p1 : p3, 2);

@@ -17,7 +17,8 @@
 // rows of the last MMA step zeroed in shared memory where they are summed over.
 //
 // Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
-// MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane). Chunks of cut pieces are
+// MMAs, warps 4-19 the scores, four warps to a quarter of the rows and 32 of a tile's columns each
+// (thread = TMEM lane): what lies between a product and the next that needs its result is short then. Chunks of cut pieces are
 // joined by the last to arrive, in the order of the chunks.
 #include <climits>
 #include <type_traits>
@@ -27,16 +28,11 @@
 namespace scfa {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsFew = 72, kRegsMany = 216;  // 128 x 72 + 256 x 216 = 384 x 168, what a CTA starts with
+constexpr int kThreads = 640;
+constexpr int kRegsFew = 64, kRegsMany = 104;  // 128 x 64 + 512 x 104 = 640 x 96, what a CTA starts with
+constexpr int kSoftWarps = 16;                 // four warpgroups, 32 columns of a tile each
 constexpr int kSlots = 3;                      // items known ahead
-constexpr int kStatStages = 3;
-
-struct PItem {
-  PackEntry e;
-  int head;  // -1: no more work
-  int pad[15];
-};
+constexpr int kStatStages = 2;
 
 struct PBwdParams {
   const char* plan;
@@ -110,7 +106,7 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ what both kernels share
 // The next piece of work into its slot, by the whole producer warp; false at the end.
-__device__ __forceinline__ bool next_item(PItem* items, uint64_t* full, uint64_t* empty, int it, const PackEntry* entries,
+__device__ __forceinline__ bool next_item(PackEntry* items, uint64_t* full, uint64_t* empty, int it, const PackEntry* entries,
                                           int n_work, int Hkv, int* counter, int lane, volatile int* abort_flag, int* status,
                                           bool& ok) {
   const int slot = it % kSlots;
@@ -121,45 +117,47 @@ __device__ __forceinline__ bool next_item(PItem* items, uint64_t* full, uint64_t
   w = __shfl_sync(0xffffffffu, w, 0);
   const int head = w < n_work ? w % Hkv : -1;
   if (head >= 0 && lane < 16)
-    reinterpret_cast<int*>(&items[slot].e)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / Hkv) + lane);
+    reinterpret_cast<int*>(&items[slot])[lane] = __ldg(reinterpret_cast<const int*>(entries + w / Hkv) + lane);
+  __syncwarp();
   if (lane == 0) items[slot].head = head;
   warp_arrive(&full[slot]);
   return head >= 0;
 }
 
-// Leave the rows of an accumulator as a chunk's share: 16 rows of a warp's 32, as quad_rows gives them.
-template <int D>
-__device__ __forceinline__ void leave_quads(float* mine, const uint32_t (&acc)[D / 64][32], int row) {
-  const int lane = threadIdx.x & 31;
+// Leave W columns of an accumulator (rows of D) as a chunk's share: 16 rows of a warp's 32, as quad_part gives them.
+template <int W, int D>
+__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[W / 32][16], int row) {
+  const int c0 = 2 * (threadIdx.x & 3);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+  for (int i = 0; i < W / 8; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + 2 * (lane & 3)) =
-          make_float2(__uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u]), __uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u + 1]));
+      *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
+          make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
 }
-template <int D>
-__device__ __forceinline__ void join_quads(uint32_t (&acc)[D / 64][32], const float* base, long long stride, int chunks, int row) {
-  const int lane = threadIdx.x & 31;
+template <int W, int D>
+__device__ __forceinline__ void join_part(uint32_t (&acc)[W / 32][16], const float* base, long long stride, int chunks, int row) {
+  const int c0 = 2 * (threadIdx.x & 3);
 #pragma unroll
-  for (int cc = 0; cc < D / 64; ++cc)
+  for (int cc = 0; cc < W / 32; ++cc)
 #pragma unroll
-    for (int c = 0; c < 32; ++c) acc[cc][c] = 0u;
+    for (int c = 0; c < 16; ++c) acc[cc][c] = 0u;
   for (int c = 0; c < chunks; ++c)
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < W / 8; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (row + 8 * u) * D + 8 * i + 2 * (lane & 3)));
-        uint32_t* y = &acc[i >> 3][(i & 7) * 4 + 2 * u];
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (row + 8 * u) * D + 8 * i + c0));
+        uint32_t* y = &acc[i >> 2][(i & 3) * 4 + 2 * u];
         y[0] = __float_as_uint(__uint_as_float(y[0]) + x.x), y[1] = __float_as_uint(__uint_as_float(y[1]) + x.y);
       }
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. Products in the order
-// S(j+1) dP(j+1) dQ(j): the softmax warps take S and dP of a tile into registers while dQ of the tile before runs, and
-// have both other products to make dS from them, so the tensor cores wait for neither. K stays for two products.
+// TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. P(j) is made while dP(j) runs, so that
+// dS follows shortly behind it; meanwhile the tensor cores do S(j+1) (D = 128) or S(j+1) and dP(j+1) (D = 64, where a
+// product takes half the time), then dQ(j). K stays for two products; at D = 128, where shared memory holds three K
+// tiles, dQ(j) comes before dP(j+1) so that K_j goes back early enough to be loaded again in time.
 template <int D>
 struct __align__(1024) DqSmem {
   static constexpr int kSubs = D / 64, kQs = D == 64 ? 2 : 1, kKs = D == 64 ? 4 : 3, kVs = D == 64 ? 4 : 2;
@@ -167,9 +165,10 @@ struct __align__(1024) DqSmem {
   uint8_t dO[kQs][kSubs][kPackSub];
   uint8_t k[kKs][kSubs][kPackSub];
   uint8_t v[kVs][kSubs][kPackSub];
-  PItem item[kSlots];
+  PackEntry item[kSlots];
   uint64_t q_full[kQs], q_empty[kQs], k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
-  uint64_t s_full, s_free, ds_full, ds_free[2], dq_full, dq_empty, tail, drain, sync, item_full[kSlots], item_empty[kSlots];
+  uint64_t s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_empty, tail, drain, sync;
+  uint64_t item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
   int abort_flag, last;
 };
@@ -181,11 +180,14 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ PBwdParams p) {
   using Sm = DqSmem<D>;
   constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kKs = Sm::kKs, kVs = Sm::kVs;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + pad);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
+    if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
+    return;
+  }
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
   const int window = h->window, n_work = h->n_entries[kListDq] * p.Hkv, used = p.G * p.tpt;
   const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
@@ -194,10 +196,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
     for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
     for (int s = 0; s < kVs; ++s) mbar_init(&sm.v_full[s], 1), mbar_init(&sm.v_empty[s], 1);
-    mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, 8), mbar_init(&sm.ds_full, 8);
+    mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, kSoftWarps), mbar_init(&sm.ds_full[0], kSoftWarps);
+    mbar_init(&sm.ds_full[1], kSoftWarps), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
     mbar_init(&sm.ds_free[0], 1), mbar_init(&sm.ds_free[1], 1);
-    mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, 8), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, 8);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
+    mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, kSoftWarps), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, kSoftWarps);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
@@ -225,8 +228,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       bool ok = true;
       for (int it = 0; ok; ++it) {
         if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
-        const PackEntry& e = sm.item[it % kSlots].e;
-        const int head = sm.item[it % kSlots].head, a = e.a, b = e.b;
+        const PackEntry& e = sm.item[it % kSlots];
+        const int head = e.head, a = e.a, b = e.b;
         if (a == b) continue;
         if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
         {
@@ -296,36 +299,48 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const int slot = it % kSlots;
           if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
           if (sm.item[slot].head < 0) break;
-          const int a = sm.item[slot].e.a, b = sm.item[slot].e.b, m_keys = sm.item[slot].e.m;
+          const int a = sm.item[slot].a, b = sm.item[slot].b, m_keys = sm.item[slot].m;
           if (a < b) {
             const int qs = q_it % kQs;
-            auto scores = [&](int i) -> bool {  // S and dP of key tile number i
-              const int s = i % kKs, vs = i % kVs;
+            auto do_s = [&](int i) -> bool {  // S of key tile number i
+              const int s = i % kKs;
               if (i > 0 && !mbar_wait(&sm.s_free, (i - 1) & 1, abort_flag, p.status)) return false;
               if (!mbar_wait(&sm.k_full[s], (i / kKs) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
               mma_ss_steps<0, D / 16>(tmem, qd + qs * kTile16, kd + s * kTile16, idesc_s, false);
-              if (!mbar_wait(&sm.v_full[vs], (i / kVs) & 1, abort_flag, p.status)) return false;
-              tc_fence_after();
-              mma_ss_steps<0, D / 16>(tmem + 128, dod + qs * kTile16, vd + vs * kTile16, idesc_s, false);
               tc_commit(&sm.s_full);
-              tc_commit(&sm.v_empty[vs]);
               return true;
             };
-            ok = mbar_wait(&sm.q_full[qs], (q_it / kQs) & 1, abort_flag, p.status) && scores(kv);
-            for (int j = a; j < b && ok; ++j, ++kv) {
-              if (j + 1 < b) ok = scores(kv + 1);
-              else tc_commit(&sm.q_empty[qs]);
-              if (!ok) break;
-              if (j == a && !mbar_wait(&sm.dq_empty, (n_q & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
-              if (!mbar_wait(&sm.ds_full, kv & 1, abort_flag, p.status)) { ok = false; break; }
+            auto do_dp = [&](int i) -> bool {
+              const int s = i % kVs;
+              if (i > 0 && !mbar_wait(&sm.dp_free, (i - 1) & 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.v_full[s], (i / kVs) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              const uint32_t ds = tmem + 384u + 64u * (kv & 1), bk = kn + (kv % kKs) * kTile16;
+              mma_ss_steps<0, D / 16>(tmem + 128, dod + qs * kTile16, vd + s * kTile16, idesc_s, false);
+              tc_commit(&sm.dp_full);
+              tc_commit(&sm.v_empty[s]);
+              return true;
+            };
+            auto do_dq = [&](int i, int j) -> bool {
+              if (j == a && !mbar_wait(&sm.dq_empty, (n_q & 1) ^ 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.ds_full[i & 1], (i >> 1) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              const uint32_t ds = tmem + 384u + 64u * (i & 1), bk = kn + (i % kKs) * kTile16;
               const int steps = min(kTile / 16, (m_keys - j * kTile + 15) >> 4);
               if (steps == 8) mma_ts_steps<0, 8>(tmem + 256, ds, bk, idesc_q, j > a, 8);
               else mma_ts_steps<0, 8>(tmem + 256, ds, bk, idesc_q, j > a, steps);
-              tc_commit(&sm.k_empty[kv % kKs]);
-              tc_commit(&sm.ds_free[kv & 1]);
+              tc_commit(&sm.k_empty[i % kKs]);
+              tc_commit(&sm.ds_free[i & 1]);
+              return true;
+            };
+            ok = mbar_wait(&sm.q_full[qs], (q_it / kQs) & 1, abort_flag, p.status) && do_s(kv) && do_dp(kv);
+            for (int j = a; j < b && ok; ++j, ++kv) {
+              const bool next = j + 1 < b;
+              if (next) ok = do_s(kv + 1);
+              if (D == 64 && ok && next) ok = do_dp(kv + 1);
+              if (!next) tc_commit(&sm.q_empty[qs]);
+              if (ok) ok = do_dq(kv, j);
+              if (D == 128 && ok && next) ok = do_dp(kv + 1);
             }
             if (!ok) break;
             tc_commit(&sm.dq_full);
@@ -340,15 +355,15 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   } else {
     // ------------------------------------------------------------ softmax
     regs_take<kRegsMany>();
-    const int hc = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 32;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int r_tok = r / p.G;
     int n = 0, n_q = 0, n_sync = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
-      const PackEntry& e = sm.item[slot].e;
-      const int head = sm.item[slot].head;
+      const PackEntry& e = sm.item[slot];
+      const int head = e.head;
       if (head < 0) break;
       const int a = e.a, b = e.b, first = e.diag, n_tok = e.n_tok;
       const bool valid = r_tok < n_tok;
@@ -356,47 +371,52 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
       const float nl = p.stats[at], nd = p.stats[n_stats + at];
       auto tile = [&](auto masked, int j) -> bool {
+        uint32_t x[32];
         if (!warp_wait(&sm.s_full, n & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-        uint32_t sr[64], dr[64];
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          tmem_ld32(lanes + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-          tmem_ld32(lanes + 128 + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
-        }
+        tmem_ld32(lanes + col0, x);
         tmem_wait_ld();
-        tmem_ld_fence(sr);
-        tmem_ld_fence(dr);
+        tmem_ld_fence(x);
         tc_fence_before();
         warp_arrive(&sm.s_free);
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), nd2 = f2(nd, nd);
-        uint32_t pk[32];
+        uint64_t pr[16];  // P, in pairs
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < 16; ++c) {
           float x0, x1;
-          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, nl2), x0, x1);
-          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-          f2_split(mul2(f2(x0, x1), add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2)), x0, x1);
-          pk[c >> 1] = c4_pack<F16>(x0, x1);
+          f2_split(fma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nl2), x0, x1);
+          pr[c] = f2(ex2_approx(x0), ex2_approx(x1));
+        }
+        if (!warp_wait(&sm.dp_full, n & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        tmem_ld32(lanes + 128 + col0, x);
+        tmem_wait_ld();
+        tmem_ld_fence(x);
+        tc_fence_before();
+        warp_arrive(&sm.dp_free);
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x0, x1;
+          f2_split(mul2(pr[c], add2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), nd2)), x0, x1);
+          pk[c] = c4_pack<F16>(x0, x1);
         }
         if (decltype(masked)::value) {
           // lo <= column <= lim as one unsigned comparison
-          const int lim = hi - j * kTile - hc * 64, lo = window ? max(lim - window + 1, -kTile) : -kTile;
+          const int lim = hi - j * kTile - col0, lo = window ? max(lim - window + 1, -kTile) : -kTile;
           const uint32_t span = lim < lo ? 0u : static_cast<uint32_t>(lim - lo) + 1u;
 #pragma unroll
-          for (int c = 0; c < 64; c += 2)
+          for (int c = 0; c < 32; c += 2)
             pk[c >> 1] &= (static_cast<uint32_t>(c - lo) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(c + 1 - lo) < span ? 0xffff0000u : 0u);
         }
         if (n > 1) {  // dQ two tiles back has read this buffer
           if (!warp_wait(&sm.ds_free[n & 1], ((n >> 1) - 1) & 1, abort_flag, p.status)) return false;
           tc_fence_after();
         }
-        const uint32_t ds = lanes + 384u + 64u * (n & 1) + hc * 32;
-        tmem_st16(ds, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-        tmem_st16(ds + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+        tmem_st16(lanes + 384u + 64u * (n & 1) + wg * 16, pk);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(&sm.ds_full);
+        warp_arrive(&sm.ds_full[n & 1]);  // (two: at D = 64 a warp may be a whole tile ahead of another)
         ++n;
         return true;
       };
@@ -412,23 +432,24 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (; j < masked && ok; ++j) ok = tile(std::false_type{}, j);
       }
       if (!ok) break;
-      // this warp's 16 rows of dQ
-      uint32_t acc[D / 64][32];
+      // this warp's part of dQ: 16 rows, half of the columns
+      constexpr int W = D / 2;
+      const int hf = wg & 1, half = wg >> 1, row = quarter * 32 + hf * 16 + (lane >> 2);
+      uint32_t acc[W / 32][16];
       if (a < b) {
         if (!warp_wait(&sm.dq_full, n_q & 1, abort_flag, p.status)) break;
         tc_fence_after();
         ++n_q;
       }
-      quad_rows<D>(acc, lanes + 256, hc, a < b);
+      quad_part<W>(acc, lanes + 256 + half * W, hf, a < b);
       if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.dq_empty);
       }
-      const int row = quarter * 32 + hc * 16 + (lane >> 2);
       if (e.slot >= 0) {
         const long long stride = static_cast<long long>(p.Hkv) * kTile * D;
-        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * kTile * D;
-        leave_quads<D>(base + e.chunk * stride, acc, row);
+        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * kTile * D + half * W;
+        leave_part<W, D>(base + e.chunk * stride, acc, row);
         __threadfence();
         warp_arrive(&sm.sync);
         if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
@@ -442,12 +463,12 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           continue;
         }
         __threadfence();
-        join_quads<D>(acc, base, stride, e.chunks, row);
+        join_part<W, D>(acc, base, stride, e.chunks, row);
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int t = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - t * p.G;
-        quad_store<D, F16>(p.dq + static_cast<long long>(e.q0 + t) * p.dqt + qh * p.dqh, t < n_tok, acc, u, p.scale);
+        const int tk = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - tk * p.G;
+        quad_store<W, F16>(p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh + half * W, tk < n_tok, acc, u, p.scale);
       }
       warp_arrive(&sm.item_empty[slot]);
     }
@@ -459,24 +480,35 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // ------------------------------------------------------------------ dK and dV
-// Tiles are transposed: lanes are keys, columns queries. D = 128: S^T [0,128), dP^T [128,256), dV, dK behind. A warpgroup
-// writes P^T and dS^T of its 64 queries over its own half of S^T, so the two never wait for each other, and products come
-// in the order dP(t+1) dV(t) dK(t) S(t+1): dP^T is in registers long before its turn, and the tensor cores run dP(t+1)
-// while P(t) is made. D = 64: P^T and dS^T have columns of their own and S(t+1), dP(t+1) run under the softmax of t.
+// Eight MMA steps of 16 queries whose A lies two steps (16 columns) to every 32 columns; `steps` of them hold something.
+template <int KK>
+__device__ __forceinline__ void mma_quarter_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add_to, int steps) {
+  if constexpr (KK < 8) {
+    if (KK < steps) mma_ts_at<(KK >> 1) * 32 + (KK & 1) * 8, KK * 128>(d_tmem, a_tmem, b_low, idesc, KK > 0 || add_to ? 1u : 0u);
+    mma_quarter_steps<KK + 1>(d_tmem, a_tmem, b_low, idesc, add_to, steps);
+  }
+}
+
+// Tiles are transposed: lanes are keys, columns queries. Scores take turns in regions of 128 TMEM columns: S^T(t) in one,
+// and a warpgroup writes P^T and dS^T of its 32 queries over its own 32 columns of it; dP^T(t) in another, free again once
+// it is in registers. D = 128 has two regions (dV and dK take the rest); its products come in the order
+//   dP(t) dV(t) S(t+1) dK(t),
+// which gives the softmax two products' time (1,024 cycles) for P behind S and for dS behind dP, and the tensor cores
+// work without a pause. D = 64, with products half as long, has three regions and the order S(t+1) dV(t) dK(t) dP(t+1):
+// four products for P, two for dS.
 template <int D>
 struct __align__(1024) DkvSmem {
-  static constexpr int kSubs = D / 64, kQs = D == 64 ? 4 : 2, kKs = D == 64 ? 2 : 1;
+  static constexpr int kSubs = D / 64, kQs = D == 64 ? 4 : 3, kOs = D == 64 ? 4 : 2, kKs = D == 64 ? 2 : 1;
   uint8_t k[kKs][kSubs][kPackSub];
   uint8_t v[kKs][kSubs][kPackSub];
   uint8_t q[kQs][kSubs][kPackSub];
-  uint8_t dO[kQs][kSubs][kPackSub];
+  uint8_t dO[kOs][kSubs][kPackSub];
   alignas(16) float nl[kStatStages][kTile];
   alignas(16) float nd[kStatStages][kTile];
-  alignas(16) int hi[kStatStages][kTile];
-  PItem item[kSlots];
-  uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kQs], do_empty[kQs];
+  PackEntry item[kSlots];
+  uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kOs], do_empty[kOs];
   uint64_t st_full[kStatStages], st_empty[kStatStages];
-  uint64_t s_full, dp_full, s_free, p_full, ds_full, pd_free, acc_full, acc_empty, tail[2], drain, sync;
+  uint64_t s_full[2], dp_full, dp_free, p_full[2], ds_full, acc_full, acc_empty, tail[2], drain, sync;
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
   int abort_flag, last;
@@ -488,37 +520,38 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ PBwdParams p) {
   using Sm = DkvSmem<D>;
-  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kKs = Sm::kKs;
-  constexpr bool kOwn = D == 64;
-  constexpr uint32_t colDP = 128, colP = kOwn ? 256 : 0, colDS = kOwn ? 320 : 32, colDV = kOwn ? 384 : 256, colDK = kOwn ? 448 : 384;
-  constexpr uint32_t kHalfCols = kOwn ? 32 : 64;  // from the first 64 queries' P^T to the others'
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
-  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + pad);
+  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kOs = Sm::kOs, kKs = Sm::kKs;
+  constexpr int kRegions = D == 64 ? 3 : 2;
+  constexpr uint32_t colDV = 512 - 2 * D, colDK = 512 - D;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
+    if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
+    return;
+  }
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
   const int window = h->window, n_work = h->n_entries[kListDkv] * p.Hkv, used = p.G * p.tpt;
   const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
-    for (int s = 0; s < kQs; ++s)
-      mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1), mbar_init(&sm.do_full[s], 1), mbar_init(&sm.do_empty[s], 1);
-    for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_empty[s], 8);
-    mbar_init(&sm.s_full, 1), mbar_init(&sm.dp_full, 1), mbar_init(&sm.s_free, 8), mbar_init(&sm.p_full, 8), mbar_init(&sm.ds_full, 8);
-    mbar_init(&sm.pd_free, 1), mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, 8), mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1);
-    mbar_init(&sm.drain, 1), mbar_init(&sm.sync, 8);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + 8);
+    for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
+    for (int s = 0; s < kOs; ++s) mbar_init(&sm.do_full[s], 1), mbar_init(&sm.do_empty[s], 1);
+    for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_empty[s], kSoftWarps);
+    mbar_init(&sm.s_full[0], 1), mbar_init(&sm.s_full[1], 1), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
+    mbar_init(&sm.p_full[0], kSoftWarps), mbar_init(&sm.p_full[1], kSoftWarps);
+    mbar_init(&sm.ds_full, kSoftWarps), mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, kSoftWarps);
+    mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, kSoftWarps);
+    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
   }
   if (used < kTile) {  // rows that no copy writes: zero for good
-    for (int s = 0; s < kQs; ++s) {
-      zero_tile_rows(sm.q[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
-      zero_tile_rows(sm.dO[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
-    }
+    for (int s = 0; s < kQs; ++s) zero_tile_rows(sm.q[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
+    for (int s = 0; s < kOs; ++s) zero_tile_rows(sm.dO[s][0], kSubs, used, kTile, threadIdx.x, kThreads);
     fence_proxy_async_smem();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
@@ -537,11 +570,11 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       bool ok = true;
       // Q or dO tile of query tile i into its ring; rows behind the sequence's
       // last, up to the last MMA step's end, become zero
-      auto load = [&](int which, const CUtensorMap* map, uint8_t (*ring)[kSubs][kPackSub], uint64_t* full, uint64_t* empty, int& n, int head,
-                      const PackEntry& e, int i) -> bool {
-        const int s = n % kQs, rows = min(p.tpt, e.m - i * p.tpt) * p.G;
+      auto load = [&](int which, const CUtensorMap* map, uint8_t (*ring)[kSubs][kPackSub], uint64_t* full, uint64_t* empty, int& n, int stages,
+                      int head, const PackEntry& e, int i) -> bool {
+        const int s = n % stages, rows = min(p.tpt, e.m - i * p.tpt) * p.G;
         const bool cut = rows < used && (rows & 15) != 0;
-        if (!warp_wait(&empty[s], ((n / kQs) & 1) ^ 1, abort_flag, p.status)) return false;
+        if (!warp_wait(&empty[s], ((n / stages) & 1) ^ 1, abort_flag, p.status)) return false;
         if (lane == 0) {
           uint64_t* const bar = cut ? &sm.tail[which] : &full[s];
           mbar_arrive_expect_tx(bar, D * used * 2);
@@ -563,8 +596,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       };
       for (int it = 0; ok; ++it) {
         if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
-        const PackEntry& e = sm.item[it % kSlots].e;
-        const int head = sm.item[it % kSlots].head, a = e.a, b = e.b;
+        const PackEntry& e = sm.item[it % kSlots];
+        const int head = e.head, a = e.a, b = e.b;
         if (a == b) continue;
         if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
         {
@@ -581,20 +614,19 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           ++k_it;
         }
         for (int i = a; i < b && ok; ++i) {
-          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, head, e, i);
+          ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, kQs, head, e, i);
           if (!ok) break;
           const int s = st_it % kStatStages;
           ok = warp_wait(&sm.st_empty[s], ((st_it / kStatStages) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           if (lane == 0) {
             const float* const st = p.stats + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile;
-            mbar_arrive_expect_tx(&sm.st_full[s], 3 * kTile * 4);
+            mbar_arrive_expect_tx(&sm.st_full[s], 2 * kTile * 4);
             bulk_load(sm.nl[s], st, kTile * 4, &sm.st_full[s]);
             bulk_load(sm.nd[s], st + n_stats, kTile * 4, &sm.st_full[s]);
-            bulk_load(sm.hi[s], st + 2 * n_stats, kTile * 4, &sm.st_full[s]);
           }
           ++st_it;
-          ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, head, e, i);
+          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i);
         }
       }
       if (lane == 0) {
@@ -603,8 +635,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           if (tails[x] > 0) mbar_wait_drain(&sm.tail[x], (tails[x] - 1) & 1, p.status);
         for (int d = 1; d <= kQs && d <= q_it; ++d)
           if (q_it - d != unmarked[0]) mbar_wait_drain(&sm.q_full[(q_it - d) % kQs], ((q_it - d) / kQs) & 1, p.status);
-        for (int d = 1; d <= kQs && d <= do_it; ++d)
-          if (do_it - d != unmarked[1]) mbar_wait_drain(&sm.do_full[(do_it - d) % kQs], ((do_it - d) / kQs) & 1, p.status);
+        for (int d = 1; d <= kOs && d <= do_it; ++d)
+          if (do_it - d != unmarked[1]) mbar_wait_drain(&sm.do_full[(do_it - d) % kOs], ((do_it - d) / kOs) & 1, p.status);
         for (int d = 1; d <= kStatStages && d <= st_it; ++d)
           mbar_wait_drain(&sm.st_full[(st_it - d) % kStatStages], ((st_it - d) / kStatStages) & 1, p.status);
         for (int d = 1; d <= kKs && d <= k_it; ++d) mbar_wait_drain(&sm.k_full[(k_it - d) % kKs], ((k_it - d) / kKs) & 1, p.status);
@@ -623,60 +655,59 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const int slot = it % kSlots;
           if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
           if (sm.item[slot].head < 0) break;
-          const int a = sm.item[slot].e.a, b = sm.item[slot].e.b, m_tok = sm.item[slot].e.m;
+          const int a = sm.item[slot].a, b = sm.item[slot].b, m_tok = sm.item[slot].m;
           if (a < b) {
             const int ks = k_it % kKs;
-            // t: query tile number over the CTA's whole work
-            auto do_dp = [&](int n) -> bool {
-              if (n > 0 && !kOwn && !mbar_wait(&sm.s_free, (n - 1) & 1, abort_flag, p.status)) return false;
-              if (!mbar_wait(&sm.do_full[n % kQs], (n / kQs) & 1, abort_flag, p.status)) return false;
-              tc_fence_after();
-              mma_ss_steps<0, D / 16>(tmem + colDP, vd + ks * kTile16, dod + (n % kQs) * kTile16, idesc_s, false);
-              if (!kOwn) tc_commit(&sm.dp_full);
-              return true;
-            };
+            // t: query tile number over the CTA's whole work. Regions: S in 0 2 1 0 2 1 .. and dP in 1 0 2 1 0 2 ..
+            // of three, or each in turn in the one and the other of two
+            auto s_at = [&](int n) { return tmem + 128u * (kRegions == 2 ? n & 1 : 2 * n % 3); };
+            auto dp_at = [&](int n) { return tmem + 128u * (kRegions == 2 ? (n & 1) ^ 1 : (2 * n + 1) % 3); };
             auto do_s = [&](int n) -> bool {
+              // two regions: where dP of the tile before was. Three: of the one before that, which dS has followed
+              if (kRegions == 2 && n > 0 && !mbar_wait(&sm.dp_free, (n - 1) & 1, abort_flag, p.status)) return false;
               if (!mbar_wait(&sm.q_full[n % kQs], (n / kQs) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              mma_ss_steps<0, D / 16>(tmem, kd + ks * kTile16, qd + (n % kQs) * kTile16, idesc_s, false);
-              tc_commit(&sm.s_full);
+              mma_ss_steps<0, D / 16>(s_at(n), kd + ks * kTile16, qd + (n % kQs) * kTile16, idesc_s, false);
+              tc_commit(&sm.s_full[n & 1]);  // (two: with three regions S(t+1) may be complete before S(t) is waited for)
               return true;
             };
-            auto scores = [&](int n) -> bool {  // D = 64: both, once the softmax has the last ones in registers
-              if (n > 0 && !mbar_wait(&sm.s_free, (n - 1) & 1, abort_flag, p.status)) return false;
-              return do_dp(n) && do_s(n);
+            auto do_dp = [&](int n) -> bool {  // (its region's P and dS are behind dV and dK that are issued already)
+              if (!mbar_wait(&sm.do_full[n % kOs], (n / kOs) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_ss_steps<0, D / 16>(dp_at(n), vd + ks * kTile16, dod + (n % kOs) * kTile16, idesc_s, false);
+              tc_commit(&sm.dp_full);
+              return true;
             };
-            ok = mbar_wait(&sm.k_full[ks], (k_it / kKs) & 1, abort_flag, p.status);
-            if (ok) ok = kOwn ? scores(t) : do_dp(t) && do_s(t);
+            // dV += P^T dO, dK += dS^T Q: A is 8 columns a step, two steps to a warpgroup's 32 columns
+            auto do_dv = [&](int n, int i, int steps) -> bool {
+              if (i == a && !mbar_wait(&sm.acc_empty, (n_acc & 1) ^ 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.p_full[n & 1], (n >> 1) & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_quarter_steps<0>(tmem + colDV, s_at(n), don + (n % kOs) * kTile16, idesc_a, i > a, steps);
+              tc_commit(&sm.do_empty[n % kOs]);
+              return true;
+            };
+            auto do_dk = [&](int n, int i, int steps) -> bool {
+              if (!mbar_wait(&sm.ds_full, n & 1, abort_flag, p.status)) return false;
+              tc_fence_after();
+              mma_quarter_steps<0>(tmem + colDK, s_at(n) + 16, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
+              tc_commit(&sm.q_empty[n % kQs]);
+              return true;
+            };
+            ok = mbar_wait(&sm.k_full[ks], (k_it / kKs) & 1, abort_flag, p.status) && do_s(t);
+            if (kRegions == 3) ok = ok && do_dp(t);
             for (int i = a; i < b && ok; ++i, ++t) {
-              const int s = t % kQs, steps = min(kTile / 16, (min(p.tpt, m_tok - i * p.tpt) * p.G + 15) >> 4);
-              if (i + 1 < b) ok = kOwn ? scores(t + 1) : do_dp(t + 1);
-              if (!ok) break;
-              if (i == a && !mbar_wait(&sm.acc_empty, (n_acc & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
-              if (!mbar_wait(&sm.p_full, t & 1, abort_flag, p.status)) { ok = false; break; }
-              tc_fence_after();
-              // dV += P^T dO, dK += dS^T Q, the first 64 queries' columns and the others'
-              const uint32_t bo = don + s * kTile16, bq = qn + s * kTile16;
-              if (steps == 8) {
-                mma_ts_steps<0, 4>(tmem + colDV, tmem + colP, bo, idesc_a, i > a, 8);
-                mma_ts_steps<4, 8>(tmem + colDV, tmem + colP + kHalfCols - 32, bo, idesc_a, true, 8);
+              const bool next = i + 1 < b;
+              const int steps = min(kTile / 16, (min(p.tpt, m_tok - i * p.tpt) * p.G + 15) >> 4);
+              if (kRegions == 3) {
+                if (next) ok = do_s(t + 1);
+                ok = ok && do_dv(t, i, steps) && do_dk(t, i, steps);
+                if (next) ok = ok && do_dp(t + 1);
               } else {
-                mma_ts_steps<0, 4>(tmem + colDV, tmem + colP, bo, idesc_a, i > a, steps);
-                mma_ts_steps<4, 8>(tmem + colDV, tmem + colP + kHalfCols - 32, bo, idesc_a, true, steps);
+                ok = do_dp(t) && do_dv(t, i, steps);
+                if (next) ok = ok && do_s(t + 1);
+                ok = ok && do_dk(t, i, steps);
               }
-              tc_commit(&sm.do_empty[s]);
-              if (!kOwn && !mbar_wait(&sm.ds_full, t & 1, abort_flag, p.status)) { ok = false; break; }
-              tc_fence_after();
-              if (steps == 8) {
-                mma_ts_steps<0, 4>(tmem + colDK, tmem + colDS, bq, idesc_a, i > a, 8);
-                mma_ts_steps<4, 8>(tmem + colDK, tmem + colDS + kHalfCols - 32, bq, idesc_a, true, 8);
-              } else {
-                mma_ts_steps<0, 4>(tmem + colDK, tmem + colDS, bq, idesc_a, i > a, steps);
-                mma_ts_steps<4, 8>(tmem + colDK, tmem + colDS + kHalfCols - 32, bq, idesc_a, true, steps);
-              }
-              tc_commit(&sm.q_empty[s]);
-              if (kOwn) tc_commit(&sm.pd_free);
-              if (!kOwn && i + 1 < b) ok = do_s(t + 1);
             }
             if (!ok) break;
             tc_commit(&sm.acc_full);
@@ -692,101 +723,81 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else {
     // ------------------------------------------------------------ softmax
     regs_take<kRegsMany>();
-    const int hc = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 32;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
+    const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
     int t = 0, n_acc = 0, n_sync = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
-      const PackEntry& e = sm.item[slot].e;
-      const int head = sm.item[slot].head;
+      const PackEntry& e = sm.item[slot];
+      const int head = e.head;
       if (head < 0) break;
       const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
-      auto tile = [&](auto masked) -> bool {
+      auto tile = [&](auto masked, int i) -> bool {
         const int ss = t % kStatStages;
-        uint32_t sr[64], dr[64], pk[32];
-        // dP^T first: it was there before S^T, and the next one may follow
-        if (!kOwn) {
-          if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
+        const uint32_t s_at = lanes + 128u * (kRegions == 2 ? t & 1 : 2 * t % 3) + col0;
+        const uint32_t dp_at = lanes + 128u * (kRegions == 2 ? (t & 1) ^ 1 : (2 * t + 1) % 3) + col0;
+        uint32_t x[32], pk[16], keep[16];
+        if (decltype(masked)::value) {
+          const int* const hi = all_hi + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile + col0;
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) tmem_ld32(lanes + colDP + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
-          tmem_wait_ld();
-          tmem_ld_fence(dr);
-          tc_fence_before();
-          warp_arrive(&sm.s_free);
+          for (int c = 0; c < 32; c += 4) {
+            const int4 h4 = __ldg(reinterpret_cast<const int4*>(hi + c));
+            keep[c >> 1] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
+            keep[(c >> 1) + 1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
+          }
         }
         if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
-        if (!warp_wait(&sm.s_full, t & 1, abort_flag, p.status)) return false;
+        if (!warp_wait(&sm.s_full[t & 1], (t >> 1) & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          tmem_ld32(lanes + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-          if (kOwn) tmem_ld32(lanes + colDP + hc * 64 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
-        }
+        tmem_ld32(s_at, x);
         tmem_wait_ld();
-        tmem_ld_fence(sr);
-        if (kOwn) {
-          tmem_ld_fence(dr);
-          tc_fence_before();
-          warp_arrive(&sm.s_free);
-        }
+        tmem_ld_fence(x);
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+        uint64_t pr[16];  // P, in pairs
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][hc * 64 + c]);
-          float x[4];
-          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, f2(l4.x, l4.y)), x[0], x[1]);
-          f2_split(fma2(f2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])), sl2, f2(l4.z, l4.w)), x[2], x[3]);
-          uint32_t keep[2] = {~0u, ~0u};
-          if (decltype(masked)::value) {
-            const int4 h4 = *reinterpret_cast<const int4*>(&sm.hi[ss][hc * 64 + c]);
-            keep[0] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
-            keep[1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
-          }
+        for (int c = 0; c < 32; c += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][col0 + c]);
+          float y[4];
+          f2_split(fma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, f2(l4.x, l4.y)), y[0], y[1]);
+          f2_split(fma2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, f2(l4.z, l4.w)), y[2], y[3]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = ex2_approx(x[i]);
-            sr[c + i] = __float_as_uint(x[i]);
-          }
-          pk[c >> 1] = c4_pack<F16>(x[0], x[1]) & keep[0];
-          pk[(c >> 1) + 1] = c4_pack<F16>(x[2], x[3]) & keep[1];
+          for (int k = 0; k < 4; ++k) y[k] = ex2_approx(y[k]);
+          pr[c >> 1] = f2(y[0], y[1]), pr[(c >> 1) + 1] = f2(y[2], y[3]);
+          pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
         }
-        if (kOwn && t > 0) {  // dV, dK of the tile before have read P^T, dS^T
-          if (!warp_wait(&sm.pd_free, (t - 1) & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
-        }
-        tmem_st16(lanes + colP + hc * kHalfCols, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-        tmem_st16(lanes + colP + hc * kHalfCols + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
-        if (!kOwn) {
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(&sm.p_full);
-        }
+        if (decltype(masked)::value)
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][hc * 64 + c]);
-          float x[4];
-          f2_split(mul2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
-                        add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), f2(d4.x, d4.y))), x[0], x[1]);
-          f2_split(mul2(f2(__uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3])),
-                        add2(f2(__uint_as_float(dr[c + 2]), __uint_as_float(dr[c + 3])), f2(d4.z, d4.w))), x[2], x[3]);
-          uint32_t keep[2] = {~0u, ~0u};
-          if (decltype(masked)::value) {
-            const int4 h4 = *reinterpret_cast<const int4*>(&sm.hi[ss][hc * 64 + c]);
-            keep[0] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
-            keep[1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
-          }
-          pk[c >> 1] = c4_pack<F16>(x[0], x[1]) & keep[0];
-          pk[(c >> 1) + 1] = c4_pack<F16>(x[2], x[3]) & keep[1];
-        }
-        warp_arrive(&sm.st_empty[ss]);
-        tmem_st16(lanes + colDS + hc * kHalfCols, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-        tmem_st16(lanes + colDS + hc * kHalfCols + 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+          for (int c = 0; c < 16; ++c) pk[c] &= keep[c];
+        tmem_st16(s_at, pk);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(kOwn ? &sm.p_full : &sm.ds_full);
+        warp_arrive(&sm.p_full[t & 1]);  // (two: with three regions a warp may be a whole tile ahead of another)
+        if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+        tmem_ld32(dp_at, x);
+        tmem_wait_ld();
+        tmem_ld_fence(x);
+        tc_fence_before();
+        if (kRegions == 2) warp_arrive(&sm.dp_free);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
+          float y[4];
+          f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
+          f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
+          pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
+        }
+        if (decltype(masked)::value)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) pk[c] &= keep[c];
+        warp_arrive(&sm.st_empty[ss]);
+        tmem_st16(s_at + 16, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&sm.ds_full);
         ++t;
         return true;
       };
@@ -795,7 +806,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int i = a; i < b && ok; ++i) {
         const int first = i * p.tpt + e.shift;  // the last key of the tile's first token
         const bool whole = first >= last_key && (i + 1) * p.tpt <= e.m && (!window || first + p.tpt - 1 - window < e.diag);
-        ok = whole ? tile(std::false_type{}) : tile(std::true_type{});
+        ok = whole ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
       }
       if (!ok) break;
       if (a < b) {
@@ -803,23 +814,19 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
         ++n_acc;
       }
-      // the first warpgroup writes dV, the second dK
+      // warpgroups 0 and 1 write dV, 2 and 3 dK, 16 rows a warp
+      const int hf = wg & 1, is_k = wg >> 1, row = quarter * 32 + hf * 16 + (lane >> 2);
       const bool joined = e.slot >= 0;
-      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
-      float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + hc) * kTile * D;
-      const int row = quarter * 32 + (lane >> 2);
-      const uint32_t from = lanes + (hc ? colDK : colDV);
+      uint32_t acc[D / 32][16];
+      quad_part<D>(acc, lanes + (is_k ? colDK : colDV), hf, a < b);
+      if (a < b) {
+        tc_fence_before();
+        warp_arrive(&sm.acc_empty);
+      }
       if (joined) {
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t acc[D / 64][32];
-          quad_rows<D>(acc, from, hf, a < b);
-          leave_quads<D>(base + e.chunk * stride, acc, row + 16 * hf);
-        }
-        if (a < b) {
-          tc_fence_before();
-          warp_arrive(&sm.acc_empty);
-        }
+        const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
+        float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + is_k) * kTile * D;
+        leave_part<D, D>(base + e.chunk * stride, acc, row);
         __threadfence();
         warp_arrive(&sm.sync);
         if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
@@ -833,23 +840,14 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           continue;
         }
         __threadfence();
+        join_part<D, D>(acc, base, stride, e.chunks, row);
       }
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t acc[D / 64][32];
-        if (joined) join_quads<D>(acc, base, stride, e.chunks, row + 16 * hf);
-        else quad_rows<D>(acc, from, hf, a < b);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int c = row + 16 * hf + 8 * u;
-          uint16_t* const dst = hc ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
+      for (int u = 0; u < 2; ++u) {
+        const int c = row + 8 * u;
+        uint16_t* const dst = is_k ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
                                    : p.dv + static_cast<long long>(e.k0 + c) * p.dvt + head * p.dvh;
-          quad_store<D, F16>(dst, c < n_tok, acc, u, hc ? p.scale : 1.f);
-        }
-      }
-      if (!joined && a < b) {
-        tc_fence_before();
-        warp_arrive(&sm.acc_empty);
+        quad_store<D, F16>(dst, c < n_tok, acc, u, is_k ? p.scale : 1.f);
       }
       warp_arrive(&sm.item_empty[slot]);
     }
@@ -879,7 +877,7 @@ template <int D, bool F16>
 cudaError_t launch_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, PBwdParams p, int sms,
                        int slots, cudaStream_t st) {
   static bool dq_allowed[64] = {}, dkv_allowed[64] = {};
-  constexpr size_t dq_smem = sizeof(DqSmem<D>) + 1024, dkv_smem = sizeof(DkvSmem<D>) + 1024;
+  constexpr size_t dq_smem = sizeof(DqSmem<D>), dkv_smem = sizeof(DkvSmem<D>);
   static_assert(dq_smem <= 227 * 1024 && dkv_smem <= 227 * 1024, "shared memory per CTA");
   packed_stats_kernel<D, F16><<<8 * sms, 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();

@@ -45,19 +45,13 @@ struct PFwdCfg {
   static constexpr int kIssuers = D == 64 ? 2 : 1;
 };
 
-struct PItem {
-  PackEntry e;
-  int head;  // -1: no more work
-  int pad[15];
-};
-
 template <int D>
 struct __align__(1024) PFwdSmem {
   using C = PFwdCfg<D>;
   uint8_t q[C::kQ][C::kSubs][kPackSub];
   uint8_t k[C::kKs][C::kSubs][kPackSub];
   uint8_t v[C::kVs][C::kSubs][kPackSub];
-  PItem item[kSlots];
+  PackEntry item[kSlots];
   uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kKs], v_full[C::kVs], k_empty[C::kKs], v_empty[C::kVs];
   uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2], sync[2];
   uint64_t tail, item_full[kSlots], item_empty[kSlots];
@@ -158,13 +152,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if (lane == 0) w = atomicAdd(p.counter, 1);
       w = __shfl_sync(0xffffffffu, w, 0);
       const int head = w < n_work ? w % p.Hkv : -1;
-      PItem& item = sm.item[slot];
+      PackEntry& item = sm.item[slot];
       if (head >= 0 && lane < 16)
-        reinterpret_cast<int*>(&item.e)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / p.Hkv) + lane);
+        reinterpret_cast<int*>(&item)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / p.Hkv) + lane);
+      __syncwarp();
       if (lane == 0) item.head = head;
       warp_arrive(&sm.item_full[slot]);
       if (head < 0) break;
-      const PackEntry e = item.e;
+      const PackEntry& e = item;
       int a[2], b[2];
       fwd_range(e, 0, p.tpt, window, a[0], b[0]);
       fwd_range(e, 1, p.tpt, window, a[1], b[1]);
@@ -245,7 +240,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int it = 0; ok; ++it) {
         const int slot = it % kSlots;
         if (!mbar_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
-        const PackEntry& e = sm.item[slot].e;
+        const PackEntry& e = sm.item[slot];
         if (sm.item[slot].head < 0) break;
         int a[2], b[2], qi[2];
         fwd_range(e, 0, p.tpt, window, a[0], b[0]);
@@ -348,8 +343,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
-      const PackEntry& e = sm.item[slot].e;
-      const int head = sm.item[slot].head;
+      const PackEntry& e = sm.item[slot];
+      const int head = e.head;
       if (head < 0) break;
       int a, b;
       fwd_range(e, g, p.tpt, window, a, b);
@@ -481,14 +476,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         float* const mine = base + e.chunk * stride;
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
-          uint32_t acc[D / 64][32];
-          quad_rows<D>(acc, tO, hf, a < b);
+          uint32_t acc[D / 32][16];
+          quad_part<D>(acc, tO, hf, a < b);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               *reinterpret_cast<float2*>(mine + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)) =
-                  make_float2(__uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u]), __uint_as_float(acc[i >> 3][(i & 7) * 4 + 2 * u + 1]));
+                  make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
         }
         reinterpret_cast<float2*>(mine + kTile * D)[r] = make_float2(m, l);
         if (a < b) {
@@ -526,8 +521,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
-        uint32_t acc[D / 64][32];
-        quad_rows<D>(acc, tO, hf, !joined && a < b);
+        uint32_t acc[D / 32][16];
+        quad_part<D>(acc, tO, hf, !joined && a < b);
         if (joined) {
           for (int c = 0; c < e.chunks; ++c) {
             const float f = share(__ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r), m);
@@ -537,7 +532,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
                 const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)));
-                uint32_t* y = &acc[i >> 3][(i & 7) * 4 + 2 * u];
+                uint32_t* y = &acc[i >> 2][(i & 3) * 4 + 2 * u];
                 y[0] = __float_as_uint(fmaf(x.x, fu[u], __uint_as_float(y[0]))), y[1] = __float_as_uint(fmaf(x.y, fu[u], __uint_as_float(y[1])));
               }
           }
