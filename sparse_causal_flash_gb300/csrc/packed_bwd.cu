@@ -17,8 +17,8 @@
 // rows of the last MMA step zeroed in shared memory where they are summed over.
 //
 // Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
-// MMAs, warps 4-19 the scores, four warps to a quarter of the rows and 32 of a tile's columns each
-// (thread = TMEM lane): what lies between a product and the next that needs its result is short then. Chunks of cut pieces are
+// MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
+// thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of XXX). Chunks of cut pieces are
 // joined by the last to arrive, in the order of the chunks.
 #include <climits>
 #include <type_traits>
@@ -28,9 +28,9 @@
 namespace scfa {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kRegsFew = 64, kRegsMany = 104;  // 128 x 64 + 512 x 104 = 640 x 96, what a CTA starts with
-constexpr int kSoftWarps = 16;                 // four warpgroups, 32 columns of a tile each
+constexpr int kThreads = 384;
+constexpr int kRegsFew = 72, kRegsMany = 216;  // 128 x 72 + 256 x 216 = 384 x 168, what a CTA starts with
+constexpr int kSoftWarps = 8;                  // two warpgroups, 64 columns of a tile each
 constexpr int kSlots = 3;                      // items known ahead
 constexpr int kStatStages = 2;
 
@@ -154,10 +154,10 @@ __device__ __forceinline__ void join_part(uint32_t (&acc)[W / 32][16], const flo
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. P(j) is made while dP(j) runs, so that
-// dS follows shortly behind it; meanwhile the tensor cores do S(j+1) (D = 128) or S(j+1) and dP(j+1) (D = 64, where a
-// product takes half the time), then dQ(j). K stays for two products; at D = 128, where shared memory holds three K
-// tiles, dQ(j) comes before dP(j+1) so that K_j goes back early enough to be loaded again in time.
+// TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. Products in the order
+// dP(j+1) S(j+1) dQ(j): dP of a tile is in registers while its S runs, and there are two products' time to make dS from
+// them. V comes first so that K_j, which stays until dQ(j), is needed again late: at D = 128 shared memory holds three K
+// tiles, and a fourth product's time for loading the next is what L2 needs.
 template <int D>
 struct __align__(1024) DqSmem {
   static constexpr int kSubs = D / 64, kQs = D == 64 ? 2 : 1, kKs = D == 64 ? 4 : 3, kVs = D == 64 ? 4 : 2;
@@ -249,6 +249,13 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const int valid = e.m - j * kTile;
           const bool cut = valid < kTile && (valid & 15) != 0;
           const int s = k_it % kKs, vs = v_it % kVs;
+          ok = warp_wait(&sm.v_empty[vs], ((v_it / kVs) & 1) ^ 1, abort_flag, p.status);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.v_full[vs], D * kTile * 2);
+            for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.v[vs][sub], &tm_v, &sm.v_full[vs], sub * 64, head, e.k0 + j * kTile);
+          }
+          ++v_it;
           ok = warp_wait(&sm.k_empty[s], ((k_it / kKs) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
           if (lane == 0) {
@@ -268,13 +275,6 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_proxy_async_smem();
             warp_arrive(&sm.k_full[s]);
           }
-          ok = warp_wait(&sm.v_empty[vs], ((v_it / kVs) & 1) ^ 1, abort_flag, p.status);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.v_full[vs], D * kTile * 2);
-            for (int sub = 0; sub < kSubs; ++sub) tma_load_3d(sm.v[vs][sub], &tm_v, &sm.v_full[vs], sub * 64, head, e.k0 + j * kTile);
-          }
-          ++v_it;
         }
       }
       if (lane == 0) {
@@ -333,14 +333,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               tc_commit(&sm.ds_free[i & 1]);
               return true;
             };
-            ok = mbar_wait(&sm.q_full[qs], (q_it / kQs) & 1, abort_flag, p.status) && do_s(kv) && do_dp(kv);
+            ok = mbar_wait(&sm.q_full[qs], (q_it / kQs) & 1, abort_flag, p.status) && do_dp(kv) && do_s(kv);
             for (int j = a; j < b && ok; ++j, ++kv) {
-              const bool next = j + 1 < b;
-              if (next) ok = do_s(kv + 1);
-              if (D == 64 && ok && next) ok = do_dp(kv + 1);
-              if (!next) tc_commit(&sm.q_empty[qs]);
+              if (j + 1 < b) ok = do_dp(kv + 1) && do_s(kv + 1);
+              else tc_commit(&sm.q_empty[qs]);
               if (ok) ok = do_dq(kv, j);
-              if (D == 128 && ok && next) ok = do_dp(kv + 1);
             }
             if (!ok) break;
             tc_commit(&sm.dq_full);
@@ -355,7 +352,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   } else {
     // ------------------------------------------------------------ softmax
     regs_take<kRegsMany>();
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 32;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 64;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int r_tok = r / p.G;
     int n = 0, n_q = 0, n_sync = 0;
@@ -371,49 +368,46 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
       const float nl = p.stats[at], nd = p.stats[n_stats + at];
       auto tile = [&](auto masked, int j) -> bool {
-        uint32_t x[32];
+        uint32_t sr[64], dr[64];
+        if (!warp_wait(&sm.dp_full, n & 1, abort_flag, p.status)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(lanes + 128 + col0 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&dr[cc * 32]));
+        tmem_wait_ld();
+        tmem_ld_fence(dr);
+        tc_fence_before();
+        warp_arrive(&sm.dp_free);
         if (!warp_wait(&sm.s_full, n & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-        tmem_ld32(lanes + col0, x);
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(lanes + col0 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
         tmem_wait_ld();
-        tmem_ld_fence(x);
+        tmem_ld_fence(sr);
         tc_fence_before();
         warp_arrive(&sm.s_free);
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), nd2 = f2(nd, nd);
-        uint64_t pr[16];  // P, in pairs
+        uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+        for (int c = 0; c < 64; c += 2) {
           float x0, x1;
-          f2_split(fma2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), sl2, nl2), x0, x1);
-          pr[c] = f2(ex2_approx(x0), ex2_approx(x1));
-        }
-        if (!warp_wait(&sm.dp_full, n & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-        tmem_ld32(lanes + 128 + col0, x);
-        tmem_wait_ld();
-        tmem_ld_fence(x);
-        tc_fence_before();
-        warp_arrive(&sm.dp_free);
-        uint32_t pk[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float x0, x1;
-          f2_split(mul2(pr[c], add2(f2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), nd2)), x0, x1);
-          pk[c] = c4_pack<F16>(x0, x1);
+          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, nl2), x0, x1);
+          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+          f2_split(mul2(f2(x0, x1), add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2)), x0, x1);
+          pk[c >> 1] = c4_pack<F16>(x0, x1);
         }
         if (decltype(masked)::value) {
           // lo <= column <= lim as one unsigned comparison
           const int lim = hi - j * kTile - col0, lo = window ? max(lim - window + 1, -kTile) : -kTile;
           const uint32_t span = lim < lo ? 0u : static_cast<uint32_t>(lim - lo) + 1u;
 #pragma unroll
-          for (int c = 0; c < 32; c += 2)
+          for (int c = 0; c < 64; c += 2)
             pk[c >> 1] &= (static_cast<uint32_t>(c - lo) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(c + 1 - lo) < span ? 0xffff0000u : 0u);
         }
         if (n > 1) {  // dQ two tiles back has read this buffer
           if (!warp_wait(&sm.ds_free[n & 1], ((n >> 1) - 1) & 1, abort_flag, p.status)) return false;
           tc_fence_after();
         }
-        tmem_st16(lanes + 384u + 64u * (n & 1) + wg * 16, pk);
+        tmem_st32(lanes + 384u + 64u * (n & 1) + wg * 32, pk);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.ds_full[n & 1]);  // (two: at D = 64 a warp may be a whole tile ahead of another)
@@ -432,9 +426,9 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (; j < masked && ok; ++j) ok = tile(std::false_type{}, j);
       }
       if (!ok) break;
-      // this warp's part of dQ: 16 rows, half of the columns
-      constexpr int W = D / 2;
-      const int hf = wg & 1, half = wg >> 1, row = quarter * 32 + hf * 16 + (lane >> 2);
+      // this warp's 16 rows of dQ
+      constexpr int W = D;
+      const int hf = wg, half = 0, row = quarter * 32 + hf * 16 + (lane >> 2);
       uint32_t acc[W / 32][16];
       if (a < b) {
         if (!warp_wait(&sm.dq_full, n_q & 1, abort_flag, p.status)) break;
@@ -480,17 +474,17 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // ------------------------------------------------------------------ dK and dV
-// Eight MMA steps of 16 queries whose A lies two steps (16 columns) to every 32 columns; `steps` of them hold something.
+// Eight MMA steps of 16 queries whose A lies four steps (32 columns) to every 64 columns; `steps` of them hold something.
 template <int KK>
-__device__ __forceinline__ void mma_quarter_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add_to, int steps) {
+__device__ __forceinline__ void mma_half_steps(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool add_to, int steps) {
   if constexpr (KK < 8) {
-    if (KK < steps) mma_ts_at<(KK >> 1) * 32 + (KK & 1) * 8, KK * 128>(d_tmem, a_tmem, b_low, idesc, KK > 0 || add_to ? 1u : 0u);
-    mma_quarter_steps<KK + 1>(d_tmem, a_tmem, b_low, idesc, add_to, steps);
+    if (KK < steps) mma_ts_at<(KK >> 2) * 64 + (KK & 3) * 8, KK * 128>(d_tmem, a_tmem, b_low, idesc, KK > 0 || add_to ? 1u : 0u);
+    mma_half_steps<KK + 1>(d_tmem, a_tmem, b_low, idesc, add_to, steps);
   }
 }
 
 // Tiles are transposed: lanes are keys, columns queries. Scores take turns in regions of 128 TMEM columns: S^T(t) in one,
-// and a warpgroup writes P^T and dS^T of its 32 queries over its own 32 columns of it; dP^T(t) in another, free again once
+// and a warpgroup writes P^T and dS^T of its 64 queries over its own 64 columns of it; dP^T(t) in another, free again once
 // it is in registers. D = 128 has two regions (dV and dK take the rest); its products come in the order
 //   dP(t) dV(t) S(t+1) dK(t),
 // which gives the softmax two products' time (1,024 cycles) for P behind S and for dS behind dP, and the tensor cores
@@ -678,19 +672,19 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
               tc_commit(&sm.dp_full);
               return true;
             };
-            // dV += P^T dO, dK += dS^T Q: A is 8 columns a step, two steps to a warpgroup's 32 columns
+            // dV += P^T dO, dK += dS^T Q
             auto do_dv = [&](int n, int i, int steps) -> bool {
               if (i == a && !mbar_wait(&sm.acc_empty, (n_acc & 1) ^ 1, abort_flag, p.status)) return false;
               if (!mbar_wait(&sm.p_full[n & 1], (n >> 1) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              mma_quarter_steps<0>(tmem + colDV, s_at(n), don + (n % kOs) * kTile16, idesc_a, i > a, steps);
+              mma_half_steps<0>(tmem + colDV, s_at(n), don + (n % kOs) * kTile16, idesc_a, i > a, steps);
               tc_commit(&sm.do_empty[n % kOs]);
               return true;
             };
             auto do_dk = [&](int n, int i, int steps) -> bool {
               if (!mbar_wait(&sm.ds_full, n & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              mma_quarter_steps<0>(tmem + colDK, s_at(n) + 16, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
+              mma_half_steps<0>(tmem + colDK, s_at(n) + 32, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
               tc_commit(&sm.q_empty[n % kQs]);
               return true;
             };
@@ -723,7 +717,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   } else {
     // ------------------------------------------------------------ softmax
     regs_take<kRegsMany>();
-    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 32;
+    const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 64;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
     const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
@@ -739,26 +733,24 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         const int ss = t % kStatStages;
         const uint32_t s_at = lanes + 128u * (kRegions == 2 ? t & 1 : 2 * t % 3) + col0;
         const uint32_t dp_at = lanes + 128u * (kRegions == 2 ? (t & 1) ^ 1 : (2 * t + 1) % 3) + col0;
-        uint32_t x[32], pk[16], keep[16];
-        if (decltype(masked)::value) {
-          const int* const hi = all_hi + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile + col0;
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const int4 h4 = __ldg(reinterpret_cast<const int4*>(hi + c));
-            keep[c >> 1] = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
-            keep[(c >> 1) + 1] = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
-          }
-        }
+        uint32_t x[64], pk[32];
+        // which of the queries c .. c + 3 see this thread's key, as masks of two 16-bit pairs
+        auto keep = [&](int c, uint32_t& k0, uint32_t& k1) {
+          const int4 h4 = __ldg(reinterpret_cast<const int4*>(all_hi + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile + col0 + c));
+          k0 = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
+          k1 = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
+        };
         if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
         if (!warp_wait(&sm.s_full[t & 1], (t >> 1) & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-        tmem_ld32(s_at, x);
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
         tmem_wait_ld();
         tmem_ld_fence(x);
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
-        uint64_t pr[16];  // P, in pairs
+        uint64_t pr[32];  // P, in pairs
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
+        for (int c = 0; c < 64; c += 4) {
           const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][col0 + c]);
           float y[4];
           f2_split(fma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, f2(l4.x, l4.y)), y[0], y[1]);
@@ -767,34 +759,39 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int k = 0; k < 4; ++k) y[k] = ex2_approx(y[k]);
           pr[c >> 1] = f2(y[0], y[1]), pr[(c >> 1) + 1] = f2(y[2], y[3]);
           pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
+          if (decltype(masked)::value) {
+            uint32_t k0, k1;
+            keep(c, k0, k1);
+            pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+          }
         }
-        if (decltype(masked)::value)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] &= keep[c];
-        tmem_st16(s_at, pk);
+        tmem_st32(s_at, pk);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.p_full[t & 1]);  // (two: with three regions a warp may be a whole tile ahead of another)
         if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-        tmem_ld32(dp_at, x);
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) tmem_ld32(dp_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
         tmem_wait_ld();
         tmem_ld_fence(x);
         tc_fence_before();
         if (kRegions == 2) warp_arrive(&sm.dp_free);
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
+        for (int c = 0; c < 64; c += 4) {
           const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
           float y[4];
           f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
           f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
           pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
+          if (decltype(masked)::value) {
+            uint32_t k0, k1;
+            keep(c, k0, k1);
+            pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+          }
         }
-        if (decltype(masked)::value)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] &= keep[c];
         warp_arrive(&sm.st_empty[ss]);
-        tmem_st16(s_at + 16, pk);
+        tmem_st32(s_at + 32, pk);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(&sm.ds_full);
@@ -814,19 +811,23 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
         ++n_acc;
       }
-      // warpgroups 0 and 1 write dV, 2 and 3 dK, 16 rows a warp
-      const int hf = wg & 1, is_k = wg >> 1, row = quarter * 32 + hf * 16 + (lane >> 2);
+      // the first warpgroup writes dV, the second dK, 16 rows of a warp's 32 at a time
       const bool joined = e.slot >= 0;
-      uint32_t acc[D / 32][16];
-      quad_part<D>(acc, lanes + (is_k ? colDK : colDV), hf, a < b);
-      if (a < b) {
-        tc_fence_before();
-        warp_arrive(&sm.acc_empty);
-      }
+      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
+      float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + wg) * kTile * D;
+      const int row = quarter * 32 + (lane >> 2);
+      const uint32_t from = lanes + (wg ? colDK : colDV);
       if (joined) {
-        const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
-        float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + is_k) * kTile * D;
-        leave_part<D, D>(base + e.chunk * stride, acc, row);
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t acc[D / 32][16];
+          quad_part<D>(acc, from, hf, a < b);
+          leave_part<D, D>(base + e.chunk * stride, acc, row + 16 * hf);
+        }
+        if (a < b) {
+          tc_fence_before();
+          warp_arrive(&sm.acc_empty);
+        }
         __threadfence();
         warp_arrive(&sm.sync);
         if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
@@ -840,14 +841,23 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           continue;
         }
         __threadfence();
-        join_part<D, D>(acc, base, stride, e.chunks, row);
       }
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t acc[D / 32][16];
+        if (joined) join_part<D, D>(acc, base, stride, e.chunks, row + 16 * hf);
+        else quad_part<D>(acc, from, hf, a < b);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = row + 8 * u;
-        uint16_t* const dst = is_k ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
+        for (int u = 0; u < 2; ++u) {
+          const int c = row + 16 * hf + 8 * u;
+          uint16_t* const dst = wg ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
                                    : p.dv + static_cast<long long>(e.k0 + c) * p.dvt + head * p.dvh;
-        quad_store<D, F16>(dst, c < n_tok, acc, u, is_k ? p.scale : 1.f);
+          quad_store<D, F16>(dst, c < n_tok, acc, u, wg ? p.scale : 1.f);
+        }
+      }
+      if (!joined && a < b) {
+        tc_fence_before();
+        warp_arrive(&sm.acc_empty);
       }
       warp_arrive(&sm.item_empty[slot]);
     }
