@@ -456,13 +456,15 @@ scfa_status scfa_cache4_attn(const uint16_t* q, long long q_token, long long q_h
  *   summed in an order that the sizes alone decide; ws: as
  *   scfa_rope_workspace_size gives. Without a norm q, k, weights, their
  *   gradients and ws are NULL.
+ * count: NULL, or a device int: only the first *count of the N tokens (clamped to
+ *   0..N) are read into results or written, as when a batch fills its rows in part.
  * N = 0 is no error; dwq, dwk are then zero.
  * ------------------------------------------------------------------------- */
 size_t scfa_rope_workspace_size(int N, int Hq, int Hkv, int D);
 scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head,
                           const uint16_t* k, long long k_token, long long k_head,
-                          const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D,
-                          int rot, int interleaved, float factor, const float* wq, const float* wk,
+                          const int32_t* pos, const int32_t* count, const uint64_t* table, int N,
+                          int Hq, int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk,
                           float eps, int dtype, uint16_t* q_out, long long qo_token,
                           long long qo_head, uint16_t* k_out, long long ko_token,
                           long long ko_head, void* stream);
@@ -470,8 +472,8 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
                           const uint16_t* dk, long long dk_token, long long dk_head,
                           const uint16_t* q, long long q_token, long long q_head,
                           const uint16_t* k, long long k_token, long long k_head,
-                          const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D,
-                          int rot, int interleaved, float factor, const float* wq, const float* wk,
+                          const int32_t* pos, const int32_t* count, const uint64_t* table, int N,
+                          int Hq, int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk,
                           float eps, int dtype, uint16_t* dq_out, long long dqo_token,
                           long long dqo_head, uint16_t* dk_out, long long dko_token,
                           long long dko_head, float* dwq, float* dwk, void* ws, size_t ws_bytes,
@@ -505,7 +507,8 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  * head strides that are positive multiples of 8 elements. Rows that belong to no
  * sequence are neither read into results nor written. Inputs and outputs must
  * not overlap. scale is positive, scale * log2(e) an fp32 number. The workspace
- * (scfa_packed_workspace_size) holds nothing from call to call; a plan for other
+ * (scfa_packed_workspace_size; one for a backward serves a forward too) holds
+ * nothing from call to call; a plan for other
  * sizes raises SCFA_ERR_INVALID in its status word. Results are the same bits on
  * every run. A row of q, k or v that is not finite may reach any row of its own
  * sequence and key head, and no other. flags: SCFA_FLAG_DEBUG_SYNC,

@@ -79,8 +79,8 @@ _SIGS = {
     "scfa_cache4_attn": ([_P, _L, _L, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _L, _L, _P, _P, _S,
                           _U, _P], _I),
     "scfa_rope_workspace_size": ([_I, _I, _I, _I], _S),
-    "scfa_rope_fwd": ([_P, _L, _L] * 2 + [_P, _P] + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P], _I),
-    "scfa_rope_bwd": ([_P, _L, _L] * 4 + [_P, _P] + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P, _P, _P, _S, _P],
+    "scfa_rope_fwd": ([_P, _L, _L] * 2 + [_P] * 3 + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P], _I),
+    "scfa_rope_bwd": ([_P, _L, _L] * 4 + [_P] * 3 + [_I] * 6 + [_F, _P, _P, _F, _I] + [_P, _L, _L] * 2 + [_P, _P, _P, _S, _P],
                       _I),
     "scfa_packed_plan_size": ([_I] * 5, _S),
     "scfa_packed_workspace_size": ([_I] * 7, _S),
@@ -471,10 +471,12 @@ def rope_workspace_size(N, Hq, Hkv, D) -> int:
     return int(_lib.scfa_rope_workspace_size(int(N), int(Hq), int(Hkv), int(D)))
 
 
-def _rope_args(name, dev, pos, table, N, D, wq, wk, k):
+def _rope_args(name, dev, pos, table, N, D, wq, wk, k, count):
     """Checks what both directions share; the pairs that are turned."""
     rot = 2 * table.numel()
-    if not (_is(pos, _i32, dev, N) and _is(table, torch.int64, dev, rot // 2)):
+    if count is not None and not _is(count, _i32, dev, 1):
+        _refuse(name, dev, count=(count, _i32, 1))
+    if not (dev >= 0 and _is(pos, _i32, dev, N) and _is(table, torch.int64, dev, rot // 2)):
         _refuse(name, dev, pos=(pos, _i32, N), table=(table, torch.int64, rot // 2))
     if rot > D:
         raise ValueError(f"{name}: table has {rot // 2} frequencies, a row {D} channels")
@@ -486,14 +488,15 @@ def _rope_args(name, dev, pos, table, N, D, wq, wk, k):
     return rot
 
 
-def scfa_rope_fwd(q, k, pos, table, q_out, k_out, interleaved=False, factor=1.0, wq=None, wk=None, eps=1e-6, stream=None):
+def scfa_rope_fwd(q, k, pos, table, q_out, k_out, interleaved=False, factor=1.0, wq=None, wk=None, eps=1e-6, count=None,
+                  stream=None):
     """Turn the rows q [N, Hq, D] and k [N, Hkv, D] (or None) by their positions pos [N] int32 into q_out, k_out (which
     may be q, k themselves); table from rope_table. With the weights wq, wk [D] fp32, rows pass a root-mean-square norm
-    first."""
+    first. count [1] int32: only so many tokens are there, the rows behind them are left as they were."""
     N, Hq, D = q.shape
     dev, dt = q.get_device(), q.dtype
     Hkv = 0 if k is None else k.shape[1]
-    rot = _rope_args("scfa_rope_fwd", dev, pos, table, N, D, wq, wk, k)
+    rot = _rope_args("scfa_rope_fwd", dev, pos, table, N, D, wq, wk, k, count)
     qt, qh = _rows4("scfa_rope_fwd", "q", q, N, Hq, D, dt, dev)
     ot, oh = _rows4("scfa_rope_fwd", "q_out", q_out, N, Hq, D, dt, dev)
     kp = kt = kh = lp = lt = lh = 0
@@ -501,20 +504,21 @@ def scfa_rope_fwd(q, k, pos, table, q_out, k_out, interleaved=False, factor=1.0,
         kt, kh = _rows4("scfa_rope_fwd", "k", k, N, Hkv, D, dt, dev)
         lt, lh = _rows4("scfa_rope_fwd", "k_out", k_out, N, Hkv, D, dt, dev)
         kp, lp = k.data_ptr(), k_out.data_ptr()
-    _launch("scfa_rope_fwd", dev, stream, q.data_ptr(), qt, qh, kp, kt, kh, pos.data_ptr(), table.data_ptr(), N, Hq, Hkv, D,
+    _launch("scfa_rope_fwd", dev, stream, q.data_ptr(), qt, qh, kp, kt, kh, pos.data_ptr(),
+            None if count is None else count.data_ptr(), table.data_ptr(), N, Hq, Hkv, D,
             rot, int(interleaved), factor, None if wq is None else wq.data_ptr(), None if wk is None else wk.data_ptr(), eps,
             _DTYPES.get(dt, -1), q_out.data_ptr(), ot, oh, lp, lt, lh)
 
 
 def scfa_rope_bwd(dq, dk, pos, table, dq_out, dk_out, interleaved=False, factor=1.0, q=None, k=None, wq=None, wk=None,
-                  eps=1e-6, dwq=None, dwk=None, ws=None, stream=None):
+                  eps=1e-6, dwq=None, dwk=None, ws=None, count=None, stream=None):
     """Gradients of scfa_rope_fwd: dq, dk are those of its outputs, dq_out, dk_out (which may be dq, dk themselves) those
     of its inputs. With a norm also its inputs q, k and weights, and dwq, dwk [D] fp32 for the weights' gradients, with a
     workspace (rope_workspace_size)."""
     N, Hq, D = dq.shape
     dev, dt = dq.get_device(), dq.dtype
     Hkv = 0 if dk is None else dk.shape[1]
-    rot = _rope_args("scfa_rope_bwd", dev, pos, table, N, D, wq, wk, dk)
+    rot = _rope_args("scfa_rope_bwd", dev, pos, table, N, D, wq, wk, dk, count)
     rows = [dq, dk, None, None, dq_out, dk_out]
     ptrs = [0] * 4
     nbytes = 0
@@ -536,7 +540,8 @@ def scfa_rope_bwd(dq, dk, pos, table, dq_out, dk_out, interleaved=False, factor=
             args.append((0, 0, 0))
         else:
             args.append((t.data_ptr(), *_rows4("scfa_rope_bwd", key, t, N, (Hq, Hkv)[i & 1], D, dt, dev)))
-    _launch("scfa_rope_bwd", dev, stream, *args[0], *args[1], *args[2], *args[3], pos.data_ptr(), table.data_ptr(), N, Hq,
+    _launch("scfa_rope_bwd", dev, stream, *args[0], *args[1], *args[2], *args[3], pos.data_ptr(),
+            None if count is None else count.data_ptr(), table.data_ptr(), N, Hq,
             Hkv, D, rot, int(interleaved), factor, ptrs[0], ptrs[1], eps, _DTYPES.get(dt, -1), *args[4], *args[5], ptrs[2],
             ptrs[3], None if ws is None else ws.data_ptr(), nbytes)
 
@@ -570,7 +575,7 @@ def scfa_packed_fwd(q, k, v, plan, scale, o, lse, ws, flags=0, stream=None):
     dev, dt = q.get_device(), q.dtype
     rows = [(t.data_ptr(), *_rows4("scfa_packed_fwd", key, t, n, h, D, dt, dev))
             for key, t, n, h in (("q", q, N, Hq), ("k", k, M, Hkv), ("v", v, M, Hkv), ("o", o, N, Hq))]
-    if not _is(lse, torch.float32, dev, N * Hq):
+    if not (dev >= 0 and _is(lse, torch.float32, dev, N * Hq)):
         _refuse("scfa_packed_fwd", dev, lse=(lse, torch.float32, N * Hq))
     _launch("scfa_packed_fwd", dev, stream, *rows[0], *rows[1], *rows[2], plan.data_ptr(),
             _ws_bytes("scfa_packed_fwd", plan, dev), N, M, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), *rows[3], lse.data_ptr(),
@@ -586,7 +591,7 @@ def scfa_packed_bwd(q, k, v, o, lse, do, plan, scale, dq, dk, dv, ws, flags=0, s
     rows = [(t.data_ptr(), *_rows4("scfa_packed_bwd", key, t, n, h, D, dt, dev))
             for key, t, n, h in (("q", q, N, Hq), ("k", k, M, Hkv), ("v", v, M, Hkv), ("o", o, N, Hq), ("do", do, N, Hq),
                                  ("dq", dq, N, Hq), ("dk", dk, M, Hkv), ("dv", dv, M, Hkv))]
-    if not _is(lse, torch.float32, dev, N * Hq):
+    if not (dev >= 0 and _is(lse, torch.float32, dev, N * Hq)):
         _refuse("scfa_packed_bwd", dev, lse=(lse, torch.float32, N * Hq))
     _launch("scfa_packed_bwd", dev, stream, *rows[0], *rows[1], *rows[2], *rows[3], lse.data_ptr(), *rows[4],
             plan.data_ptr(), _ws_bytes("scfa_packed_bwd", plan, dev), N, M, Hq, Hkv, D, scale, _DTYPES.get(dt, -1), *rows[5],

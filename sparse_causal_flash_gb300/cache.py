@@ -24,10 +24,13 @@ class KVCache4:
     """Pages, tables and the launch sequence of serving steps for R request rows."""
 
     def __init__(self, R: int, n_pages: int, Hq: int, Hkv: int, D: int, max_len: int, max_tokens: int,
-                 page_size: int = 64, dtype=torch.bfloat16, device="cuda"):
+                 page_size: int = 64, dtype=torch.bfloat16, device="cuda", rope=None, wq=None, wk=None, eps: float = 1e-6):
         """R request rows share n_pages pages of page_size tokens; a request
         caches at most max_len tokens (rounded up to whole pages), a step
-        brings at most max_tokens new ones over all requests."""
+        brings at most max_tokens new ones over all requests. rope: a rope.Rope;
+        steps then take their tokens' positions and turn queries and keys by
+        them before all else, with wq and wk [D] fp32 behind a root-mean-square
+        norm of each head."""
         nbytes = cache4_page_bytes(page_size, D)
         if nbytes == 0:
             raise ValueError(f"KVCache4: head dimension {D} or page size {page_size} is not supported")
@@ -56,12 +59,21 @@ class KVCache4:
         self.vis = torch.empty(max_tokens, **i32)
         self.o = torch.zeros((max_tokens, Hq, D), dtype=dtype, device=dev)
         self.lse = torch.zeros((max_tokens, Hq), dtype=torch.float32, device=dev)
+        self.rope, self.wq, self.wk, self.eps = rope, wq, wk, float(eps)
+        self.q_r = self.k_r = None
+        if rope is None and (wq is not None or wk is not None):
+            raise ValueError("KVCache4: the norm comes with the rotary positions; Rope(0) turns nothing")
+        if rope is not None:
+            if rope.rot > D or (wq is None) != (wk is None):
+                raise ValueError(f"KVCache4: {rope.rot} of {D} channels to turn, or a weight without the other")
+            self.q_r = torch.empty((max_tokens, Hq, D), dtype=dtype, device=dev)
+            self.k_r = torch.empty((max_tokens, Hkv, D), dtype=dtype, device=dev)
         self.ws_plan = workspace(cache4_plan_workspace_size(max_tokens, R), dev)
         self.ws_attn = workspace(cache4_attn_workspace_size(max_tokens, R, Hq, Hkv, D), dev)
         for ws in (self.ws_plan, self.ws_attn):
             ws[:4].zero_()  # the status word: no step has run yet
 
-    def step(self, q, k, v, new_len, scale, keep=None, stream=None):
+    def step(self, q, k, v, new_len, scale, keep=None, stream=None, pos=None):
         """One serving step: new_len [R] int32 new tokens of each request, packed
         request by request in q [N, Hq, D], k, v [N, Hkv, D] (N from 1 to
         max_tokens; the sum of new_len may be smaller), keep [N] uint8 or
@@ -69,7 +81,8 @@ class KVCache4:
         step overwrites and whose rows from the sum of new_len on are left as
         they were. A step that does not fit (status()) caches nothing and
         computes nothing. Steps follow one another on one stream, or the
-        caller orders them."""
+        caller orders them. pos [N] int32, with a rope and only with one: the
+        tokens' positions in their texts (dropped tokens count)."""
         N = q.shape[0]
         if N > self.max_tokens:
             raise ValueError(f"KVCache4.step: {N} token rows, room for {self.max_tokens}")
@@ -81,6 +94,12 @@ class KVCache4:
                                  f"start, got {t.stride()} at {t.data_ptr():#x}")
         if not _SCALES[0] <= scale <= _SCALES[1]:
             raise ValueError(f"KVCache4.step: scale {scale} is not a positive fp32 number of at most {_SCALES[1]:.7g}")
+        if (pos is None) != (self.rope is None):
+            raise ValueError("KVCache4.step: positions come with a rope, and only with one")
+        if self.rope is not None:
+            qr, kr = self.q_r[:N], self.k_r[:N]
+            self.rope.fwd(q, k, pos, qr, kr, self.wq, self.wk, self.eps, stream=stream)
+            q, k = qr, kr
         slot, vis, o, lse = self.slot[:N], self.vis[:N], self.o[:N], self.lse[:N]
         scfa_cache4_plan(self.len, new_len, keep, self.free, self.n_free, self.table, self.page_size, self.n_pages,
                          self.len, self.n_free, self.q_start, slot, vis, self.ws_plan, stream)
@@ -89,13 +108,14 @@ class KVCache4:
                          stream)
         return o, lse
 
-    def capture(self, q, k, v, new_len, scale, keep=None):
+    def capture(self, q, k, v, new_len, scale, keep=None, pos=None):
         """The step on these input tensors as a CUDA graph; each replay() is
-        one more step. They and this object must stay alive and in place.
+        one more step. They and this object must stay alive and in place; with
+        a rope the caller moves pos on between replays.
         Nothing is run: the cache is as before."""
         g = torch.cuda.CUDAGraph()
         with torch.cuda.device(self.device), torch.cuda.graph(g):
-            self.step(q, k, v, new_len, scale, keep)
+            self.step(q, k, v, new_len, scale, keep, pos=pos)
         return g
 
     def rows(self, request: int):

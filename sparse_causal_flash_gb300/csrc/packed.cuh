@@ -97,14 +97,14 @@ struct PackWs {
   size_t stats = 0;     // backward: [3][query tiles][Hkv][128]
   size_t clear = 0;     // bytes from the start that a call clears
 };
-inline PackWs pack_ws(bool backward, int D, int sms) {
+inline PackWs pack_ws(int D, int sms) {
   PackWs w;
   const size_t slots = static_cast<size_t>(pack_slots(sms));
   w.counters = sizeof(WsHeader);
   w.clear = align_up(w.counters + (2 + 4 * slots) * sizeof(int), 256);
   w.part = w.clear;
-  // forward: two tiles of D + 2 columns; backward: dK and dV, or dQ
-  w.stats = align_up(w.part + slots * 2 * kTile * (D + (backward ? 0 : 2)) * sizeof(float), 256);
+  // forward: two tiles of D + 2 columns; backward: dK and dV, or dQ. A backward's workspace serves a forward too
+  w.stats = align_up(w.part + slots * 2 * kTile * (D + 2) * sizeof(float), 256);
   return w;
 }
 inline long long pack_stats_tile_bytes(int Hkv) { return 3ll * Hkv * kTile * sizeof(float); }

@@ -592,7 +592,7 @@ extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, lon
   if ((D != 64 && D != 128) || (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) || Hq / Hkv > kTile) return SCFA_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * Hq >= (1ll << 31) - 256 || static_cast<long long>(M) * Hkv >= (1ll << 31) - 256) return SCFA_ERR_UNSUPPORTED;
   const int sms = num_sms();
-  const PackWs w = pack_ws(false, D, sms);
+  const PackWs w = pack_ws(D, sms);
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.stats) return SCFA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < sizeof(PackHeader)) return SCFA_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

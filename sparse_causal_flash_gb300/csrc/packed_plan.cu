@@ -261,7 +261,7 @@ size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int
   PackPlanLayout L;
   const int sms = num_sms();
   if ((D != 64 && D != 128) || !pack_plan_layout(N, M, R, Hq, Hkv, sms, &L)) return 0;
-  const PackWs w = pack_ws(backward != 0, D, sms);
+  const PackWs w = pack_ws(D, sms);
   if (!backward) return w.stats;
   const int tpt = kTile / (Hq / Hkv);
   return align_up(w.stats + static_cast<size_t>((N / tpt + static_cast<long long>(R)) * pack_stats_tile_bytes(Hkv)), 256);

@@ -33,11 +33,14 @@ struct RopeSide {
 struct RopeArgs {
   RopeSide side[2];
   const int32_t* pos;
+  const int32_t* count;  // null, or how many of the N tokens there are
   const uint64_t* table;
   float* part;  // [CTA][D] partial dw
   int N, rot;
   float factor, eps, turn;  // turn: +-2 pi / 2^32
 };
+
+__device__ __forceinline__ int rope_tokens(const RopeArgs& g) { return g.count ? max(0, min(g.N, __ldg(g.count))) : g.N; }
 
 // The eight pairs of thread t of a row: slot(i) numbers them, 0 .. rot / 2 are turned; a(i), b(i) are their channels.
 template <int D, int KIND>
@@ -152,8 +155,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
   const long long unit = static_cast<long long>(block) * (kRopeThreads / T) + threadIdx.x / T;
   const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
-  const bool live = tok_ < g.N;
-  const int tok = live ? tok_ : g.N - 1;
+  const bool live = tok_ < rope_tokens(g);
+  const int tok = min(tok_, g.N - 1);
   RopeMap<D, KIND> m;
   m.t = threadIdx.x % T, m.rot = g.rot;
   RopeRaw raw[HP];
@@ -198,13 +201,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_con
   float wa[8], wb[8], da[8], db[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) wa[i] = __ldg(sd.w + m.a(i)), wb[i] = __ldg(sd.w + m.b(i)), da[i] = db[i] = 0.f;
-  const long long units = static_cast<long long>(g.N) * sd.slices;
+  const int tokens = rope_tokens(g);
+  const long long units = static_cast<long long>(tokens) * sd.slices;
   for (long long first = static_cast<long long>(block) * (kRopeThreads / T); first < units;
        first += static_cast<long long>(sd.blocks) * (kRopeThreads / T)) {
     const long long unit = first + threadIdx.x / T;
     const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
-    const bool live = tok_ < g.N;
-    const int tok = live ? tok_ : g.N - 1;
+    const bool live = tok_ < tokens;
+    const int tok = min(tok_, g.N - 1);
     RopeRaw rx[HP], rd[HP];
 #pragma unroll
     for (int u = 0; u < HP; ++u) {
@@ -334,7 +338,7 @@ scfa_status rope_rows(const void* p, long long token, long long head) {
 // what both directions check
 scfa_status rope_check(const void* pos, const void* table, int N, int Hq, int Hkv, int D, int rot, int interleaved, float factor,
                        float eps, int dtype) {
-  if (!pos || N < 0 || Hq < 1 || Hkv < 0 || rot < 0 || rot > D || (rot & 1) || (rot > 0 && !table)) return SCFA_ERR_INVALID;
+  if ((!pos && N > 0) || N < 0 || Hq < 1 || Hkv < 0 || rot < 0 || rot > D || (rot & 1) || (rot > 0 && !table)) return SCFA_ERR_INVALID;
   if (interleaved != 0 && interleaved != 1) return SCFA_ERR_INVALID;
   if (!(factor > -INFINITY && factor < INFINITY) || !(eps >= 0.f && eps < INFINITY)) return SCFA_ERR_INVALID;
   if (D != 64 && D != 128) return SCFA_ERR_UNSUPPORTED;
@@ -343,9 +347,9 @@ scfa_status rope_check(const void* pos, const void* table, int N, int Hq, int Hk
   return SCFA_OK;
 }
 
-RopeArgs rope_args(const int32_t* pos, const uint64_t* table, int N, int rot, float factor, float eps, bool back) {
+RopeArgs rope_args(const int32_t* pos, const int32_t* count, const uint64_t* table, int N, int rot, float factor, float eps, bool back) {
   RopeArgs g = {};
-  g.pos = pos, g.table = table, g.N = N, g.rot = rot, g.factor = factor, g.eps = eps;
+  g.pos = pos, g.count = count, g.table = table, g.N = N, g.rot = rot, g.factor = factor, g.eps = eps;
   g.turn = (back ? -1.f : 1.f) * 1.4629180792671596e-9f;  // 2 pi / 2^32
   return g;
 }
@@ -358,8 +362,8 @@ using namespace scfa;
 extern "C" {
 
 scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head, const uint16_t* k, long long k_token,
-                          long long k_head, const int32_t* pos, const uint64_t* table, int N, int Hq, int Hkv, int D, int rot,
-                          int interleaved, float factor, const float* wq, const float* wk, float eps, int dtype,
+                          long long k_head, const int32_t* pos, const int32_t* count, const uint64_t* table, int N, int Hq,
+                          int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk, float eps, int dtype,
                           uint16_t* q_out, long long qo_token, long long qo_head, uint16_t* k_out, long long ko_token,
                           long long ko_head, void* stream) {
   if (scfa_status e = rope_check(pos, table, N, Hq, Hkv, D, rot, interleaved, factor, eps, dtype)) return e;
@@ -370,7 +374,7 @@ scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head
     return SCFA_ERR_INVALID;
   if (Hkv > 0 && (rope_rows(k, k_token, k_head) || rope_rows(k_out, ko_token, ko_head) || c4_rows_overlap(ko_token, ko_head, N, Hkv, D)))
     return SCFA_ERR_INVALID;
-  RopeArgs g = rope_args(pos, table, N, rot, factor, eps, false);
+  RopeArgs g = rope_args(pos, count, table, N, rot, factor, eps, false);
   g.side[0] = {q, nullptr, q_out, q_token, q_head, 0, 0, qo_token, qo_head, wq, nullptr, Hq, 0, 0};
   g.side[1] = {k, nullptr, k_out, k_token, k_head, 0, 0, ko_token, ko_head, wk, nullptr, Hkv, 0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -387,8 +391,8 @@ size_t scfa_rope_workspace_size(int N, int Hq, int Hkv, int D) {
 
 scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_head, const uint16_t* dk, long long dk_token,
                           long long dk_head, const uint16_t* q, long long q_token, long long q_head, const uint16_t* k,
-                          long long k_token, long long k_head, const int32_t* pos, const uint64_t* table, int N, int Hq,
-                          int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk, float eps,
+                          long long k_token, long long k_head, const int32_t* pos, const int32_t* count,
+                          const uint64_t* table, int N, int Hq, int Hkv, int D, int rot, int interleaved, float factor, const float* wq, const float* wk, float eps,
                           int dtype, uint16_t* dq_out, long long dqo_token, long long dqo_head, uint16_t* dk_out,
                           long long dko_token, long long dko_head, float* dwq, float* dwk, void* ws, size_t ws_bytes,
                           void* stream) {
@@ -406,7 +410,7 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
     return SCFA_ERR_INVALID;
   if (Hkv > 0 && (rope_rows(dk, dk_token, dk_head) || rope_rows(dk_out, dko_token, dko_head) || c4_rows_overlap(dko_token, dko_head, N, Hkv, D)))
     return SCFA_ERR_INVALID;
-  RopeArgs g = rope_args(pos, table, N, rot, factor, eps, true);
+  RopeArgs g = rope_args(pos, count, table, N, rot, factor, eps, true);
   if (norm) {
     if (rope_rows(q, q_token, q_head) || (Hkv > 0 && rope_rows(k, k_token, k_head))) return SCFA_ERR_INVALID;
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < scfa_rope_workspace_size(N, Hq, Hkv, D)) return SCFA_ERR_WORKSPACE;

@@ -40,7 +40,7 @@ class Step:
 
     def __init__(self, mode: int, B: int, H: int, Tq: int, Tk: int, D: int, n_buckets: int = 0,
                  device="cuda", flags: int = 0, tiled=None, shared_qk: bool = False, gather=None,
-                 per_head_r: bool = False, keep_o32: bool = False):
+                 per_head_r: bool = False, keep_o32: bool = False, rope=None):
         """tiled (hash mode; the default): sort into the tile-aligned layout,
         every bucket starting on a tile boundary (lsh_bucket_sort_tiled); the
         sorted tensors then have Ts = scfa_tiled_rows(T, n_buckets) rows per
@@ -61,7 +61,10 @@ class Step:
         keep_o32: the forward also keeps O in fp32 for the backward's
         rowsum(dO * O) (SCFA_FLAG_KEEP_O32). The default uses the bf16 O, as
         FlashAttention's backward does: 2-4% faster per step on GB300, and
-        the gradients stay within the parity tolerance with room to spare."""
+        the gradients stay within the parity tolerance with room to spare.
+        rope: a rope.Rope; queries and keys are turned by their original
+        positions first (0 .. T - 1, in QK mode q_idx and k_idx), everything
+        behind that sees the turned rows, and dq and dk are turned back."""
         self.mode, self.B, self.H, self.Tq, self.Tk, self.D = mode, B, H, Tq, Tk, D
         self.nb = n_buckets
         self.flags = flags
@@ -92,6 +95,13 @@ class Step:
         self.device = dev
         Ta, Tb = (self.Ts, self.Ts) if mode == MODE_HASH else (Tq, Tk)  # rows the attention calls see
         self.Ta = Ta
+        self.rope = rope
+        if rope is not None:
+            if rope.rot > D:
+                raise ValueError(f"Step: {rope.rot} channels to turn, a head has {D}")
+            self.q_r, self.k_r = torch.empty((B, H, Tq, D), **bf), torch.empty((B, H, Tk, D), **bf)
+            if mode != MODE_QK:
+                self.pos = torch.arange(max(Tq, Tk), **i32)
         worst = attn_workspace_size(mode, 1, B, H, Ta, Tb, D)
         fixed = attn_workspace_size_live(mode, 1, B, H, Ta, Tb, D, 0)
         self.live_sized = mode == MODE_HASH and worst - fixed > LIVE_SIZED_ABOVE
@@ -138,6 +148,9 @@ class Step:
         # keep_o32, its fp32 O in the shared workspace)
         f = self.flags | (FLAG_KEEP_O32 if self.keep_o32 else 0)
         fr = f | FLAG_REUSE_TILES
+        if self.rope is not None:
+            self._turn(q, k, self.q_r, self.k_r, q_idx, k_idx, self.rope.fwd, stream)
+            q, k = self.q_r, self.k_r
         tick = mark if mark is not None else (lambda name: None)
         if self.mode == MODE_DENSE:
             scfa_dense_fwd(q, k, v, scale, self.o, self.lse, self.ws_f, f, stream)
@@ -178,7 +191,22 @@ class Step:
             scfa_hash_bwd(xq, xk, xv, self.o, self.lse, xdo, self.pq, self.pk, self.qh, self.kh, scale, self.dq,
                           self.dk, self.dv, self.ws_b, fr | g, main)
             tick("bwd")
+        if self.rope is not None:
+            self._turn(self.dq, self.dk, self.dq, self.dk, q_idx, k_idx, self.rope.bwd, stream)
         return self
+
+    def _turn(self, q, k, q_out, k_out, q_idx, k_idx, call, stream):
+        """Query and key rows (or their gradients) by their positions: in QK mode each row has its own, else a position is
+        a token of all heads."""
+        def rows(x):
+            B, H, T, D = x.shape
+            return x.view(-1, 1, D) if self.mode == MODE_QK else x.view(B * H, T, D).transpose(0, 1)
+
+        if self.mode == MODE_QK:
+            call(rows(q), None, q_idx.view(-1), rows(q_out), None, stream=stream)
+            call(rows(k), None, k_idx.view(-1), rows(k_out), None, stream=stream)
+        else:
+            call(rows(q), rows(k), self.pos, rows(q_out), rows(k_out), stream=stream)
 
     def capture(self, q, k, v, do, scale, q_idx=None, k_idx=None, R=None):
         """One whole step (every kernel of run(), both streams joined by
@@ -307,10 +335,11 @@ class HostPipeline:
 
     def __init__(self, mode: int, B: int, H: int, Tq: int, Tk: int, D: int, n_buckets: int = 0,
                  device="cuda", flags: int = 0, tiled=None, shared_qk: bool = False, gather=None,
-                 per_head_r: bool = False, graphs: bool = True):
+                 per_head_r: bool = False, graphs: bool = True, rope=None):
         self.device = torch.device(device)
         self.steps = [Step(mode, B, H, Tq, Tk, D, n_buckets=n_buckets, device=self.device, flags=flags,
-                           tiled=tiled, shared_qk=shared_qk, gather=gather, per_head_r=per_head_r)
+                           tiled=tiled, shared_qk=shared_qk, gather=gather, per_head_r=per_head_r,
+                           **({} if rope is None else {"rope": rope}))
                       for _ in range(2)]
         # graphs: from its second use on, a slot's step runs as one CUDA graph
         # captured on the slot's device input buffers (not for live-sized
