@@ -120,6 +120,47 @@ __device__ __forceinline__ void rope_store(uint16_t* row, const RopeMap<D, KIND>
   }
 }
 
+// The weights of a thread's channels, from global or shared memory.
+template <int D, int KIND>
+__device__ __forceinline__ void rope_weights(const float* w, const RopeMap<D, KIND>& m, float (&a)[8], float (&b)[8]) {
+  if constexpr (KIND == kHalfOdd) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = w[m.a(i)], b[i] = w[m.b(i)];
+  } else {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<float4*>(&v[4 * j]) = *reinterpret_cast<const float4*>(w + m.piece(j >> 1) * 8 + (j & 1) * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (KIND == kHalf) a[i] = v[i], b[i] = v[8 + i];
+      else a[i] = v[2 * i], b[i] = v[2 * i + 1];
+    }
+  }
+}
+
+// (a, b) -> (a c - b s, b c + a s) for eight pairs, two at a time
+__device__ __forceinline__ void rope_turn(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t x = f2(a[i], a[i + 1]), y = f2(b[i], b[i + 1]), co = f2(c[i], c[i + 1]);
+    f2_split(fma2(x, co, mul2(y, f2(-s[i], -s[i + 1]))), a[i], a[i + 1]);
+    f2_split(fma2(y, co, mul2(x, f2(s[i], s[i + 1]))), b[i], b[i + 1]);
+  }
+}
+// sum over the thread's channels of x y
+__device__ __forceinline__ float rope_dot(const float (&xa)[8], const float (&xb)[8], const float (&ya)[8], const float (&yb)[8]) {
+  uint64_t t[2] = {0ull, 0ull};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    t[0] = fma2(f2(xa[i], xa[i + 1]), f2(ya[i], ya[i + 1]), t[0]);
+    t[1] = fma2(f2(xb[i], xb[i + 1]), f2(yb[i], yb[i + 1]), t[1]);
+  }
+  float lo, hi;
+  f2_split(add2(t[0], t[1]), lo, hi);
+  return lo + hi;
+}
+
 template <int D>
 __device__ __forceinline__ float rope_row_sum(float x) {
 #pragma unroll
@@ -130,31 +171,43 @@ __device__ __forceinline__ float rope_row_sum(float x) {
 // cosine and sine of each pair, times factor; 1 and 0 where a pair is not turned
 template <int D, int KIND>
 __device__ __forceinline__ void rope_angles(const RopeArgs& g, const RopeMap<D, KIND>& m, int pos, float (&c)[8], float (&s)[8]) {
+  const int h = g.rot >> 1;
+  const uint32_t p = static_cast<uint32_t>(pos);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; i += 2) {
     const int k = m.slot(i);
-    c[i] = 1.f, s[i] = 0.f;
-    if (k < g.rot >> 1) {
-      const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(g.table) + k);
-      const uint32_t lo = static_cast<uint32_t>(f), hi = static_cast<uint32_t>(f >> 32), p = static_cast<uint32_t>(pos);
+    uint64_t f[2];
+    if (KIND == kHalf || (KIND == kInterleaved && k + 1 < h)) {  // two neighbours, both turned or neither
+      const ulonglong2 u = k < h ? __ldg(reinterpret_cast<const ulonglong2*>(g.table + k)) : make_ulonglong2(0, 0);
+      f[0] = u.x, f[1] = u.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        f[j] = m.slot(i + j) < h ? __ldg(reinterpret_cast<const unsigned long long*>(g.table) + m.slot(i + j)) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t lo = static_cast<uint32_t>(f[j]), hi = static_cast<uint32_t>(f[j] >> 32);
       // bits 32..63 of the signed position times f
       const uint32_t z = p * hi + __umulhi(p, lo) - (pos < 0 ? lo : 0u);
       const float t = static_cast<float>(static_cast<int32_t>(z)) * g.turn;
-      c[i] = __cosf(t) * g.factor;
-      s[i] = __sinf(t) * g.factor;
+      const bool turned = m.slot(i + j) < h;
+      c[i + j] = turned ? __cosf(t) * g.factor : 1.f;
+      s[i + j] = turned ? __sinf(t) * g.factor : 0.f;
     }
   }
 }
 
 // Forward, and the gradient without a norm (turn < 0). One unit is HP heads of one token.
 template <int D, bool F16, int KIND, bool NORM, int HP>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs g) {
+__global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 3) rope_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int T = D / 16;
   const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
   const RopeSide& sd = g.side[si];
   const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
-  const long long unit = static_cast<long long>(block) * (kRopeThreads / T) + threadIdx.x / T;
-  const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
+  // (units are fewer than 2^31: N Hq is)
+  const uint32_t unit = static_cast<uint32_t>(block) * (kRopeThreads / T) + threadIdx.x / T;
+  const int tok_ = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok_) * sd.slices) * HP;
   const bool live = tok_ < rope_tokens(g);
   const int tok = min(tok_, g.N - 1);
   RopeMap<D, KIND> m;
@@ -163,26 +216,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 #pragma unroll
   for (int u = 0; u < HP; ++u)
     raw[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + min(h0 + u, sd.H - 1) * sd.xh, m);
-  float c[8], s[8];
+  float c[8], s[8], wa[8], wb[8];
   rope_angles(g, m, __ldg(g.pos + tok), c, s);
+  if (NORM) rope_weights<D, KIND>(sd.w, m, wa, wb);
 #pragma unroll
   for (int u = 0; u < HP; ++u) {
     float a[8], b[8];
     rope_unpack<D, F16, KIND>(raw[u], a, b);
     if (NORM) {
-      float ss = 0.f;
+      const float r = rsqrtf(fmaf(rope_row_sum<D>(rope_dot(a, b, a, b)), 1.f / D, g.eps));
+      const uint64_t r2 = f2(r, r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-      const float r = rsqrtf(fmaf(rope_row_sum<D>(ss), 1.f / D, g.eps));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] *= r * __ldg(sd.w + m.a(i)), b[i] *= r * __ldg(sd.w + m.b(i));
+      for (int i = 0; i < 8; i += 2) {
+        f2_split(mul2(f2(a[i], a[i + 1]), mul2(f2(wa[i], wa[i + 1]), r2)), a[i], a[i + 1]);
+        f2_split(mul2(f2(b[i], b[i + 1]), mul2(f2(wb[i], wb[i + 1]), r2)), b[i], b[i + 1]);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = a[i];
-      a[i] = fmaf(x, c[i], -b[i] * s[i]);
-      b[i] = fmaf(b[i], c[i], x * s[i]);
-    }
+    rope_turn(a, b, c, s);
     if (live && h0 + u < sd.H) rope_store<D, F16, KIND>(sd.y + tok * sd.yt + (h0 + u) * sd.yh, m, a, b);
   }
 }
@@ -190,7 +240,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 // Gradients with a norm. A CTA takes every side.blocks-th unit and keeps its sum of dw in registers, which it leaves in
 // `part`: rows are summed in an order that the sizes alone decide.
 template <int D, bool F16, int KIND, int HP>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeArgs g) {
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int T = D / 16;
   __shared__ float s_dw[kRopeThreads / 32][D];
   const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
@@ -198,15 +248,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_con
   const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
   RopeMap<D, KIND> m;
   m.t = threadIdx.x % T, m.rot = g.rot;
-  float wa[8], wb[8], da[8], db[8];
+  __shared__ __align__(16) float s_w[D];  // (sixteen registers less)
+  if (threadIdx.x < D) s_w[threadIdx.x] = __ldg(sd.w + threadIdx.x);
+  __syncthreads();
+  float da[8], db[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) wa[i] = __ldg(sd.w + m.a(i)), wb[i] = __ldg(sd.w + m.b(i)), da[i] = db[i] = 0.f;
+  for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.f;
   const int tokens = rope_tokens(g);
-  const long long units = static_cast<long long>(tokens) * sd.slices;
-  for (long long first = static_cast<long long>(block) * (kRopeThreads / T); first < units;
-       first += static_cast<long long>(sd.blocks) * (kRopeThreads / T)) {
-    const long long unit = first + threadIdx.x / T;
-    const int tok_ = static_cast<int>(unit / sd.slices), h0 = static_cast<int>(unit - static_cast<long long>(tok_) * sd.slices) * HP;
+  const uint32_t units = static_cast<uint32_t>(tokens) * sd.slices;  // (fewer than 2^31: N Hq is)
+  for (uint32_t first = static_cast<uint32_t>(block) * (kRopeThreads / T); first < units; first += static_cast<uint32_t>(sd.blocks) * (kRopeThreads / T)) {
+    const uint32_t unit = first + threadIdx.x / T;
+    const int tok_ = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok_) * sd.slices) * HP;
     const bool live = tok_ < tokens;
     const int tok = min(tok_, g.N - 1);
     RopeRaw rx[HP], rd[HP];
@@ -220,26 +272,35 @@ __global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_con
     rope_angles(g, m, __ldg(g.pos + tok), c, s);
 #pragma unroll
     for (int u = 0; u < HP; ++u) {
-      float xa[8], xb[8], ga[8], gb[8];
+      float xa[8], xb[8], ga[8], gb[8], wa[8], wb[8];
+      rope_weights<D, KIND>(s_w, m, wa, wb);
       rope_unpack<D, F16, KIND>(rx[u], xa, xb);
       rope_unpack<D, F16, KIND>(rd[u], ga, gb);
-      float ss = 0.f, dot = 0.f;
+      rope_turn(ga, gb, c, s);
+      const float r = rsqrtf(fmaf(rope_row_sum<D>(rope_dot(xa, xb, xa, xb)), 1.f / D, g.eps));
+      const uint64_t r2 = f2(r, r);
+      const bool in = live && h0 + u < sd.H;
+      // n = x r in place of x; dw += g n; then g w in place of g
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = ga[i];
-        ga[i] = fmaf(y, c[i], -gb[i] * s[i]);
-        gb[i] = fmaf(gb[i], c[i], y * s[i]);
-        ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-        dot = fmaf(ga[i] * wa[i], xa[i], fmaf(gb[i] * wb[i], xb[i], dot));
+      for (int i = 0; i < 8; i += 2) {
+        const uint64_t na = mul2(f2(xa[i], xa[i + 1]), r2), nb = mul2(f2(xb[i], xb[i + 1]), r2);
+        const uint64_t a2 = f2(ga[i], ga[i + 1]), b2 = f2(gb[i], gb[i + 1]);
+        if (in) {
+          f2_split(fma2(a2, na, f2(da[i], da[i + 1])), da[i], da[i + 1]);
+          f2_split(fma2(b2, nb, f2(db[i], db[i + 1])), db[i], db[i + 1]);
+        }
+        f2_split(mul2(a2, f2(wa[i], wa[i + 1])), ga[i], ga[i + 1]);
+        f2_split(mul2(b2, f2(wb[i], wb[i + 1])), gb[i], gb[i + 1]);
+        f2_split(na, xa[i], xa[i + 1]);
+        f2_split(nb, xb[i], xb[i + 1]);
       }
-      const float r = rsqrtf(fmaf(rope_row_sum<D>(ss), 1.f / D, g.eps));
-      const float k = rope_row_sum<D>(dot) * r * r * (1.f / D);
-      if (live && h0 + u < sd.H) {
+      const float k = rope_row_sum<D>(rope_dot(ga, gb, xa, xb)) * (-1.f / D);
+      const uint64_t k2 = f2(k, k);
+      if (in) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          da[i] = fmaf(ga[i], xa[i] * r, da[i]), db[i] = fmaf(gb[i], xb[i] * r, db[i]);
-          ga[i] = r * fmaf(ga[i], wa[i], -xa[i] * k);
-          gb[i] = r * fmaf(gb[i], wb[i], -xb[i] * k);
+        for (int i = 0; i < 8; i += 2) {
+          f2_split(mul2(r2, fma2(f2(xa[i], xa[i + 1]), k2, f2(ga[i], ga[i + 1]))), ga[i], ga[i + 1]);
+          f2_split(mul2(r2, fma2(f2(xb[i], xb[i + 1]), k2, f2(gb[i], gb[i + 1]))), gb[i], gb[i + 1]);
         }
         rope_store<D, F16, KIND>(sd.y + tok * sd.yt + (h0 + u) * sd.yh, m, ga, gb);
       }
@@ -292,7 +353,7 @@ int rope_bwd_ctas(int N, int H, int D, int most) {
   const long long n = (static_cast<long long>(N) * ((H + kBwdHeads - 1) / kBwdHeads) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   return static_cast<int>(n < most ? n : most);
 }
-int rope_most_ctas() { return 4 * num_sms(); }
+int rope_most_ctas() { return 8 * num_sms(); }
 
 template <int D, bool F16, int KIND>
 cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
@@ -308,8 +369,8 @@ cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     return launch_behind(rope_dw_kernel<D>, dim3(D / 8, g.side[1].H ? 2 : 1), 256, st, g);
   }
-  // Four heads a thread once one head each fills the GPU twice over.
-  const bool many = static_cast<long long>(g.N) * (g.side[0].H + g.side[1].H) * T > 2ll * 2048 * num_sms();
+  // Four heads a thread once one head each fills the GPU twice over, and where there are as many.
+  const bool many = g.side[0].H > 2 && static_cast<long long>(g.N) * (g.side[0].H + g.side[1].H) * T > 2ll * 2048 * num_sms();
   for (RopeSide& s : g.side) {
     s.slices = many ? (s.H + 3) / 4 : s.H;
     s.blocks = static_cast<int>((static_cast<long long>(g.N) * s.slices * T + kRopeThreads - 1) / kRopeThreads);
@@ -340,6 +401,7 @@ scfa_status rope_check(const void* pos, const void* table, int N, int Hq, int Hk
                        float eps, int dtype) {
   if ((!pos && N > 0) || N < 0 || Hq < 1 || Hkv < 0 || rot < 0 || rot > D || (rot & 1) || (rot > 0 && !table)) return SCFA_ERR_INVALID;
   if (interleaved != 0 && interleaved != 1) return SCFA_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(table) & 15u) return SCFA_ERR_INVALID;
   if (!(factor > -INFINITY && factor < INFINITY) || !(eps >= 0.f && eps < INFINITY)) return SCFA_ERR_INVALID;
   if (D != 64 && D != 128) return SCFA_ERR_UNSUPPORTED;
   if (dtype != SCFA_DTYPE_BF16 && dtype != SCFA_DTYPE_F16) return SCFA_ERR_UNSUPPORTED;
@@ -369,6 +431,7 @@ scfa_status scfa_rope_fwd(const uint16_t* q, long long q_token, long long q_head
   if (scfa_status e = rope_check(pos, table, N, Hq, Hkv, D, rot, interleaved, factor, eps, dtype)) return e;
   const bool norm = wq != nullptr;
   if (norm ? Hkv > 0 && !wk : wk != nullptr) return SCFA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(wq) | reinterpret_cast<uintptr_t>(wk)) & 15u) return SCFA_ERR_INVALID;
   if (N == 0) return SCFA_OK;
   if (rope_rows(q, q_token, q_head) || rope_rows(q_out, qo_token, qo_head) || c4_rows_overlap(qo_token, qo_head, N, Hq, D))
     return SCFA_ERR_INVALID;
@@ -399,6 +462,7 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
   if (scfa_status e = rope_check(pos, table, N, Hq, Hkv, D, rot, interleaved, factor, eps, dtype)) return e;
   const bool norm = wq != nullptr;
   if (norm ? !dwq || (Hkv > 0 && (!wk || !dwk)) : wk || dwq || dwk) return SCFA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(wq) | reinterpret_cast<uintptr_t>(wk)) & 15u) return SCFA_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N == 0) {
     if (!norm) return SCFA_OK;
