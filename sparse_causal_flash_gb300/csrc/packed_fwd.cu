@@ -379,15 +379,67 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int c = 0; c < kTile; ++c)
             if (static_cast<uint32_t>(c - lo) >= span) sr[c] = 0xff800000u;
         }
-        float mx[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) mx[u] = fmaxf(__uint_as_float(sr[2 * u]), __uint_as_float(sr[2 * u + 1]));
-#pragma unroll
-        for (int c = 8; c < kTile; c += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) mx[u] = pack_max3(mx[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
         float sl = p.scale_log2;
-        const float mt = pack_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl;
+        // 32 columns of P under the reference `from` (its negative), into TMEM
+        uint64_t sum[2];
+        auto weigh = [&](int q, uint64_t sl2, uint64_t from) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float x0, x1;
+            f2_split(fma2(f2(__uint_as_float(sr[q * 32 + c]), __uint_as_float(sr[q * 32 + c + 1])), sl2, from), x0, x1);
+            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(x0, x1));
+            pk[c >> 1] = c4_pack<F16>(x0, x1);
+          }
+          tmem_st16(tP + q * 16, pk);
+        };
+        auto signal = [&](int half) {
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.p_full[g][half]);
+        };
+        auto taken = [&]() {
+          float s0, s1;
+          f2_split(add2(sum[0], sum[1]), s0, s1);
+          l = s0 + s1;
+        };
+        auto largest = [&]() {
+          float mx[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(__uint_as_float(sr[2 * u]), __uint_as_float(sr[2 * u + 1]));
+#pragma unroll
+          for (int c = 8; c < kTile; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mx[u] = pack_max3(mx[u], __uint_as_float(sr[c + 2 * u]), __uint_as_float(sr[c + 2 * u + 1]));
+          return pack_max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        };
+        if (kOwnP && n_s > 0) {
+          if (!warp_wait(&sm.pv_done[g], (n_s - 1) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+        }
+        float mt;
+        if (!decltype(masked)::value && j > a) {
+          // The reference seldom moves behind an item's first tile. So the weights of the first half are made under the old
+          // one while the maximum is still being found (on other units); if it moved after all they are made again below
+          sum[0] = f2(l, 0.f), sum[1] = 0ull;
+          const uint64_t sl2 = f2(sl, sl), from = f2(-m, -m);
+          weigh(0, sl2, from);
+          weigh(1, sl2, from);
+          mt = largest() * sl;
+          if (__builtin_expect(!__any_sync(0xffffffffu, mt > m + kGrow || !(fabsf(m) <= kFarScore)), 1)) {
+            signal(0);
+            top = fmaxf(top, mt);
+            weigh(2, sl2, from);
+            weigh(3, sl2, from);
+            signal(1);
+            taken();
+            ++n_s;
+            return true;
+          }
+        } else {
+          mt = largest() * sl;
+        }
         top = fmaxf(top, mt);
         const bool grown = mt > m + kGrow;
         float alpha = 1.f;
@@ -397,55 +449,34 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         float sub = m == -INFINITY ? 0.f : -m;
         const bool far = fabsf(sub) > kFarScore;
-        if (kOwnP && n_s > 0) {
-          if (!warp_wait(&sm.pv_done[g], (n_s - 1) & 1, abort_flag, p.status)) return false;
-          tc_fence_after();
+        if (far) {
+          // far from zero an fma would give the largest score its product's rounding as a weight: both rounded alike
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), sl), sub));
+          sl = 1.f, sub = 0.f;
         }
-        if (__builtin_expect(__any_sync(0xffffffffu, grown || far), 0)) {
-          if (far) {
-            // far from zero an fma would give the largest score its product's rounding as a weight: both rounded alike
+        // O to the new reference. The product before is complete: with P's
+        // own columns by the wait above, else because S came behind it
+        if (j > a && __any_sync(0xffffffffu, grown)) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c) sr[c] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(sr[c]), sl), sub));
-            sl = 1.f, sub = 0.f;
-          }
-          // O to the new reference. The product before is complete: with P's
-          // own columns by the wait above, else because S came behind it
-          if (j > a) {
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t oo[16];
+            tmem_ld16(tO + cc * 16, oo);
+            tmem_wait_ld();
+            tmem_ld_fence(oo);
 #pragma unroll
-            for (int cc = 0; cc < D / 16; ++cc) {
-              uint32_t oo[16];
-              tmem_ld16(tO + cc * 16, oo);
-              tmem_wait_ld();
-              tmem_ld_fence(oo);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) oo[c] = __float_as_uint(__uint_as_float(oo[c]) * alpha);
-              tmem_st16(tO + cc * 16, oo);
-            }
+            for (int c = 0; c < 16; ++c) oo[c] = __float_as_uint(__uint_as_float(oo[c]) * alpha);
+            tmem_st16(tO + cc * 16, oo);
           }
         }
-        const uint64_t sl2 = f2(sl, sl), sub2 = f2(sub, sub);
-        uint64_t sum[2] = {f2(l * alpha, 0.f), 0ull};
+        const uint64_t sl2 = f2(sl, sl), from = f2(sub, sub);
+        sum[0] = f2(l * alpha, 0.f), sum[1] = 0ull;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float x0, x1;
-            f2_split(fma2(f2(__uint_as_float(sr[q * 32 + c]), __uint_as_float(sr[q * 32 + c + 1])), sl2, sub2), x0, x1);
-            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(x0, x1));
-            pk[c >> 1] = c4_pack<F16>(x0, x1);
-          }
-          tmem_st16(tP + q * 16, pk);
-          if (q & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&sm.p_full[g][q >> 1]);
-          }
+          weigh(q, sl2, from);
+          if (q & 1) signal(q >> 1);
         }
-        float s0, s1;
-        f2_split(add2(sum[0], sum[1]), s0, s1);
-        l = s0 + s1;
+        taken();
         ++n_s;
         return true;
       };
