@@ -19,7 +19,7 @@ BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libscfa.so")
 SOURCES = ["api.cu", "tiles.cu", "lsh.cu", "attn_fwd.cu", "attn_bwd.cu", "coverage.cu", "noalloc.cu", "select.cu",
            "cache4.cu", "cache4_attn.cu", "cache4_wide.cu", "rope.cu", "packed_plan.cu", "packed_fwd.cu",
-           "packed_bwd.cu"]
+           "packed_bwd.cu", "packed_join.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

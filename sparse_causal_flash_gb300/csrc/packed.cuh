@@ -34,9 +34,8 @@ struct PackEntry {
   int tile0;   // number of the (first) query tile over all sequences
   int slot;    // first partial slot of the cut entry (per key head); -1: not cut
   int chunk, chunks;
-  int cut;     // number of the cut entry
   int head;    // (in shared memory) key head, -1: no more work
-  int pad[2];
+  int pad[3];
 };
 static_assert(sizeof(PackEntry) == 64, "entries are copied as 16 words");
 
@@ -47,18 +46,20 @@ struct PackHeader {
   int n_entries[kLists];
   int n_qtiles;            // query tiles of all sequences
   int list_status[kLists];  // (each list is built by a CTA of its own)
-  int pad0;
+  int n_cuts[kLists];       // entries that are cut, per key head
+  int pad0[2];
   long long entries[kLists];  // byte offsets from the plan's start
+  long long cuts[kLists];     // int: the first chunk's entry of each cut one
   long long qtiles;           // int4 (first token, tokens, last key of the first token, 0) of each query tile
   long long bytes;
-  int pad[38];
+  int pad[28];
 };
 static_assert(sizeof(PackHeader) == 256, "the plan's header");
 
 struct PackPlanLayout {
   // first tile of each sequence [kLists + 1][R + 1] (the last one: query tiles again, for the key list's CTA); (units,
   // sequence) of each tile, list by list; the rest is what the header names
-  size_t pre = 0, units[kLists] = {}, qtiles = 0, entries[kLists] = {}, total = 0;
+  size_t pre = 0, units[kLists] = {}, qtiles = 0, entries[kLists] = {}, cuts[kLists] = {}, total = 0;
   long long most[kLists] = {};  // entries of each list at most
 };
 
@@ -85,29 +86,46 @@ inline bool pack_plan_layout(int N, int M, int R, int Hq, int Hkv, int sms, Pack
   for (int i = 0; i < kLists; ++i) w.units[i] = take(static_cast<size_t>(w.most[i]) * sizeof(int2));
   w.qtiles = take((static_cast<size_t>(N / tpt) + R) * sizeof(int4));
   for (int i = 0; i < kLists; ++i) w.entries[i] = take(static_cast<size_t>(w.most[i]) * sizeof(PackEntry));
+  for (int i = 0; i < kLists; ++i) w.cuts[i] = take(static_cast<size_t>(pack_slots(sms)) * sizeof(int));
   w.total = off;
   *L = w;
   return true;
 }
 
-// Workspace: status and counters, then the partial results of cut entries, then (backward) the rows' statistics.
+// Workspace: status and work counters, then the chunks' partial results, then (backward) the rows' statistics.
 struct PackWs {
-  size_t counters = 0;  // ints: work counters [2], then arrivals of cut entries [2][slots][2]
-  size_t part = 0;      // fp32
-  size_t stats = 0;     // backward: [3][query tiles][Hkv][128]
-  size_t clear = 0;     // bytes from the start that a call clears
+  size_t counters = 0;          // ints: next item of each kernel
+  size_t part = 0, part_q = 0;  // fp32, [slot][Hkv]: two tiles of D + 2 columns, or dV and dK; (backward) dQ
+  size_t forward = 0;           // what a forward needs
+  size_t stats = 0;             // backward: [3][query tiles][Hkv][128]
+  size_t clear = 0;             // bytes from the start that a call clears
 };
+// A backward's workspace serves a forward too.
 inline PackWs pack_ws(int D, int sms) {
   PackWs w;
-  const size_t slots = static_cast<size_t>(pack_slots(sms));
+  const size_t slots = static_cast<size_t>(pack_slots(sms)), row = static_cast<size_t>(kTile) * sizeof(float);
   w.counters = sizeof(WsHeader);
-  w.clear = align_up(w.counters + (2 + 4 * slots) * sizeof(int), 256);
-  w.part = w.clear;
-  // forward: two tiles of D + 2 columns; backward: dK and dV, or dQ. A backward's workspace serves a forward too
-  w.stats = align_up(w.part + slots * 2 * kTile * (D + 2) * sizeof(float), 256);
+  w.clear = w.part = align_up(w.counters + 2 * sizeof(int), 256);
+  w.forward = align_up(w.part + slots * 2 * row * (D + 2), 256);
+  w.part_q = align_up(w.part + slots * 2 * row * D, 256);
+  w.stats = align_up(w.part_q + slots * row * D, 256);
   return w;
 }
 inline long long pack_stats_tile_bytes(int Hkv) { return 3ll * Hkv * kTile * sizeof(float); }
+
+// The join of what the chunks left, behind the kernel that left it: o and lse (forward), or dV, dK and dQ.
+struct PackJoin {
+  const char* plan;
+  long long plan_bytes;
+  int N, M, Hq, Hkv, G, tpt;
+  const float *part, *part_q;
+  float scale;
+  uint16_t *o, *dq, *dk, *dv;
+  long long ot, oh, dqt, dqh, dkt, dkh, dvt, dvh;
+  float* lse;
+  const int* status;
+};
+cudaError_t launch_pack_join(const PackJoin& j, int D, bool f16, bool backward, int sms, cudaStream_t st);
 
 // What every kernel checks first: the plan is one for this call and lies in its buffer.
 __device__ __forceinline__ int pack_plan_status(const PackHeader* h, long long bytes, int N, int M, int Hq, int Hkv) {
@@ -273,6 +291,17 @@ __device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint3
     const uint4 v = t & 2 ? make_uint4(y0, y1, p2, p3) : make_uint4(p0, p1, y0, y1);
     if (live) *reinterpret_cast<uint4*>(row + 32 * b + 8 * t) = v;
   }
+}
+// Leave W columns of an accumulator (rows of D) as a chunk's share: 16 rows of a warp's 32, as quad_part gives them.
+template <int W, int D>
+__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[W / 32][16], int row) {
+  const int c0 = 2 * (threadIdx.x & 3);
+#pragma unroll
+  for (int i = 0; i < W / 8; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
+          make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
 }
 __device__ __forceinline__ float pack_max3(float a, float b, float c) {
   float d;

@@ -18,8 +18,8 @@
 //
 // Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
 // MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
-// thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of XXX). Chunks of cut pieces are
-// joined by the last to arrive, in the order of the chunks.
+// thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of 460). What chunks of cut pieces
+// leave is joined by a kernel behind both, in the order of the chunks.
 #include <climits>
 #include <type_traits>
 
@@ -47,8 +47,7 @@ struct PBwdParams {
   float* stats;             // [3][tiles][Hkv][128]
   long long stats_bytes;    // room for them
   int* counter;
-  int* arrivals;            // [cut][Hkv]
-  float* part;
+  float *part, *part_q;     // chunks' shares of dV and dK, and of dQ
   int stall;
   int* status;
 };
@@ -67,10 +66,8 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
   constexpr int L = D / 8, RW = 32 / L;
   const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
   const int status = bwd_plan_status(p);
-  if (status != SCFA_OK) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(p.status, status);
-    return;
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = status, p.counter[0] = p.counter[1] = 0;  // for the kernels behind
+  if (status != SCFA_OK) return;
   const int4* const tiles = reinterpret_cast<const int4*>(p.plan + h->qtiles);
   const int lane = threadIdx.x & 31, ch = lane % L;
   const long long n = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;  // rows
@@ -124,35 +121,6 @@ __device__ __forceinline__ bool next_item(PackEntry* items, uint64_t* full, uint
   return head >= 0;
 }
 
-// Leave W columns of an accumulator (rows of D) as a chunk's share: 16 rows of a warp's 32, as quad_part gives them.
-template <int W, int D>
-__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[W / 32][16], int row) {
-  const int c0 = 2 * (threadIdx.x & 3);
-#pragma unroll
-  for (int i = 0; i < W / 8; ++i)
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
-          make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
-}
-template <int W, int D>
-__device__ __forceinline__ void join_part(uint32_t (&acc)[W / 32][16], const float* base, long long stride, int chunks, int row) {
-  const int c0 = 2 * (threadIdx.x & 3);
-#pragma unroll
-  for (int cc = 0; cc < W / 32; ++cc)
-#pragma unroll
-    for (int c = 0; c < 16; ++c) acc[cc][c] = 0u;
-  for (int c = 0; c < chunks; ++c)
-#pragma unroll
-    for (int i = 0; i < W / 8; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (row + 8 * u) * D + 8 * i + c0));
-        uint32_t* y = &acc[i >> 2][(i & 3) * 4 + 2 * u];
-        y[0] = __float_as_uint(__uint_as_float(y[0]) + x.x), y[1] = __float_as_uint(__uint_as_float(y[1]) + x.y);
-      }
-}
-
 // ------------------------------------------------------------------ dQ
 // TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. Products in the order
 // dP(j+1) S(j+1) dQ(j): dP of a tile is in registers while its S runs, and there are two products' time to make dS from
@@ -167,10 +135,10 @@ struct __align__(1024) DqSmem {
   uint8_t v[kVs][kSubs][kPackSub];
   PackEntry item[kSlots];
   uint64_t q_full[kQs], q_empty[kQs], k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
-  uint64_t s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_empty, tail, drain, sync;
+  uint64_t s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_empty, tail, drain;
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
-  int abort_flag, last;
+  int abort_flag;
 };
 
 template <int D, bool F16>
@@ -183,7 +151,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  if (bwd_plan_status(p) != SCFA_OK) return;  // (the kernel before has said so)
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
     if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
     return;
@@ -199,7 +167,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, kSoftWarps), mbar_init(&sm.ds_full[0], kSoftWarps);
     mbar_init(&sm.ds_full[1], kSoftWarps), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
     mbar_init(&sm.ds_free[0], 1), mbar_init(&sm.ds_free[1], 1);
-    mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, kSoftWarps), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, kSoftWarps);
+    mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, kSoftWarps), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -355,7 +323,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 64;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const int r_tok = r / p.G;
-    int n = 0, n_q = 0, n_sync = 0;
+    int n = 0, n_q = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -427,42 +395,27 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (!ok) break;
       // this warp's 16 rows of dQ
-      constexpr int W = D;
-      const int hf = wg, half = 0, row = quarter * 32 + hf * 16 + (lane >> 2);
-      uint32_t acc[W / 32][16];
+      const int hf = wg, row = quarter * 32 + hf * 16 + (lane >> 2);
+      uint32_t acc[D / 32][16];
       if (a < b) {
         if (!warp_wait(&sm.dq_full, n_q & 1, abort_flag, p.status)) break;
         tc_fence_after();
         ++n_q;
       }
-      quad_part<W>(acc, lanes + 256 + half * W, hf, a < b);
+      quad_part<D>(acc, lanes + 256, hf, a < b);
       if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.dq_empty);
       }
-      if (e.slot >= 0) {
-        const long long stride = static_cast<long long>(p.Hkv) * kTile * D;
-        float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * kTile * D + half * W;
-        leave_part<W, D>(base + e.chunk * stride, acc, row);
-        __threadfence();
-        warp_arrive(&sm.sync);
-        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (warp == 4 && lane == 0) sm.last = atomicAdd(p.arrivals + static_cast<long long>(e.cut) * p.Hkv + head, 1) == e.chunks - 1;
-        warp_arrive(&sm.sync);
-        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (!*reinterpret_cast<volatile int*>(&sm.last)) {
-          warp_arrive(&sm.item_empty[slot]);
-          continue;
-        }
-        __threadfence();
-        join_part<W, D>(acc, base, stride, e.chunks, row);
+      if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
+        leave_part<D, D>(p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D, acc, row);
+        warp_arrive(&sm.item_empty[slot]);
+        continue;
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tk = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - tk * p.G;
-        quad_store<W, F16>(p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh + half * W, tk < n_tok, acc, u, p.scale);
+        quad_store<D, F16>(p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh, tk < n_tok, acc, u, p.scale);
       }
       warp_arrive(&sm.item_empty[slot]);
     }
@@ -502,10 +455,10 @@ struct __align__(1024) DkvSmem {
   PackEntry item[kSlots];
   uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kOs], do_empty[kOs];
   uint64_t st_full[kStatStages], st_empty[kStatStages];
-  uint64_t s_full[2], dp_full, dp_free, p_full[2], ds_full, acc_full, acc_empty, tail[2], drain, sync;
+  uint64_t s_full[2], dp_full, dp_free, p_full[2], ds_full, acc_full, acc_empty, tail[2], drain;
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
-  int abort_flag, last;
+  int abort_flag;
 };
 
 template <int D, bool F16>
@@ -520,7 +473,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (bwd_plan_status(p) != SCFA_OK) return;  // (raised by the kernel before)
+  if (bwd_plan_status(p) != SCFA_OK) return;  // (the kernel before has said so)
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
     if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
     return;
@@ -537,7 +490,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(&sm.s_full[0], 1), mbar_init(&sm.s_full[1], 1), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
     mbar_init(&sm.p_full[0], kSoftWarps), mbar_init(&sm.p_full[1], kSoftWarps);
     mbar_init(&sm.ds_full, kSoftWarps), mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, kSoftWarps);
-    mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1), mbar_init(&sm.drain, 1), mbar_init(&sm.sync, kSoftWarps);
+    mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1), mbar_init(&sm.drain, 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -721,7 +674,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
     const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
-    int t = 0, n_acc = 0, n_sync = 0;
+    int t = 0, n_acc = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -812,41 +765,16 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         ++n_acc;
       }
       // the first warpgroup writes dV, the second dK, 16 rows of a warp's 32 at a time
-      const bool joined = e.slot >= 0;
-      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * D;
-      float* const base = p.part + ((static_cast<long long>(e.slot) * p.Hkv + head) * 2 + wg) * kTile * D;
       const int row = quarter * 32 + (lane >> 2);
       const uint32_t from = lanes + (wg ? colDK : colDV);
-      if (joined) {
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t acc[D / 32][16];
-          quad_part<D>(acc, from, hf, a < b);
-          leave_part<D, D>(base + e.chunk * stride, acc, row + 16 * hf);
-        }
-        if (a < b) {
-          tc_fence_before();
-          warp_arrive(&sm.acc_empty);
-        }
-        __threadfence();
-        warp_arrive(&sm.sync);
-        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (warp == 4 && lane == 0) sm.last = atomicAdd(p.arrivals + static_cast<long long>(e.cut) * p.Hkv + head, 1) == e.chunks - 1;
-        warp_arrive(&sm.sync);
-        if (!warp_wait(&sm.sync, n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (!*reinterpret_cast<volatile int*>(&sm.last)) {
-          warp_arrive(&sm.item_empty[slot]);
-          continue;
-        }
-        __threadfence();
-      }
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t acc[D / 32][16];
-        if (joined) join_part<D, D>(acc, base, stride, e.chunks, row + 16 * hf);
-        else quad_part<D>(acc, from, hf, a < b);
+        quad_part<D>(acc, from, hf, a < b);
+        if (e.slot >= 0) {  // this chunk's share, for the join behind these kernels
+          leave_part<D, D>(p.part + ((static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * 2 + wg) * kTile * D, acc, row + 16 * hf);
+          continue;
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int c = row + 16 * hf + 8 * u;
@@ -855,7 +783,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           quad_store<D, F16>(dst, c < n_tok, acc, u, wg ? p.scale : 1.f);
         }
       }
-      if (!joined && a < b) {
+      if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.acc_empty);
       }
@@ -885,14 +813,14 @@ cudaError_t launch_one(Kernel kern, size_t smem, bool (&allowed)[64], const CUte
 
 template <int D, bool F16>
 cudaError_t launch_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& dO, PBwdParams p, int sms,
-                       int slots, cudaStream_t st) {
+                       cudaStream_t st) {
   static bool dq_allowed[64] = {}, dkv_allowed[64] = {};
   constexpr size_t dq_smem = sizeof(DqSmem<D>), dkv_smem = sizeof(DkvSmem<D>);
   static_assert(dq_smem <= 227 * 1024 && dkv_smem <= 227 * 1024, "shared memory per CTA");
   packed_stats_kernel<D, F16><<<8 * sms, 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && p.M > 0) e = launch_one(packed_dkv_kernel<D, F16>, dkv_smem, dkv_allowed, q, k, v, dO, p, sms, st);
-  ++p.counter, p.arrivals += slots;
+  ++p.counter;
   if (e == cudaSuccess && p.N > 0) e = launch_one(packed_dq_kernel<D, F16>, dq_smem, dq_allowed, q, k, v, dO, p, sms, st);
   return e;
 }
@@ -930,15 +858,14 @@ extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, lon
     return SCFA_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* c = static_cast<char*>(ws);
-  if (cudaMemsetAsync(c, 0, w.clear, st) != cudaSuccess) return SCFA_ERR_CUDA;
-  if (N == 0 && M == 0) return SCFA_OK;
+  if (N == 0 && M == 0) return cudaMemsetAsync(c, 0, w.clear, st) == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
   PBwdParams p = {};
   p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
   p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.D = D, p.scale = scale, p.scale_log2 = factor;
   p.o = o, p.ot = o_token, p.oh = o_head, p.dO = dO, p.dot = do_token, p.doh = do_head, p.lse = lse;
   p.dq = dq, p.dqt = dq_token, p.dqh = dq_head, p.dk = dk, p.dkt = dk_token, p.dkh = dk_head, p.dv = dv, p.dvt = dv_token, p.dvh = dv_head;
-  p.counter = reinterpret_cast<int*>(c + w.counters), p.arrivals = p.counter + 2;
-  p.part = reinterpret_cast<float*>(c + w.part), p.stats = reinterpret_cast<float*>(c + w.stats);
+  p.counter = reinterpret_cast<int*>(c + w.counters);
+  p.part = reinterpret_cast<float*>(c + w.part), p.part_q = reinterpret_cast<float*>(c + w.part_q), p.stats = reinterpret_cast<float*>(c + w.stats);
   p.stats_bytes = static_cast<long long>(ws_bytes - w.stats);
   p.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0, p.status = reinterpret_cast<int*>(c);
   const bool f16 = dtype == SCFA_DTYPE_F16;
@@ -952,10 +879,14 @@ extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, lon
   // without queries (or keys) no tile of them is ever copied: any valid map will do
   if (N == 0) tq = tdo = tk;
   if (M == 0) tk = tv = tq;
-  const int slots = pack_slots(sms);
-  const cudaError_t e = D == 64 ? (f16 ? launch_bwd<64, true>(tq, tk, tv, tdo, p, sms, slots, st) : launch_bwd<64, false>(tq, tk, tv, tdo, p, sms, slots, st))
-                                : (f16 ? launch_bwd<128, true>(tq, tk, tv, tdo, p, sms, slots, st) : launch_bwd<128, false>(tq, tk, tv, tdo, p, sms, slots, st));
+  const cudaError_t e = D == 64 ? (f16 ? launch_bwd<64, true>(tq, tk, tv, tdo, p, sms, st) : launch_bwd<64, false>(tq, tk, tv, tdo, p, sms, st))
+                                : (f16 ? launch_bwd<128, true>(tq, tk, tv, tdo, p, sms, st) : launch_bwd<128, false>(tq, tk, tv, tdo, p, sms, st));
   if (e != cudaSuccess) return SCFA_ERR_CUDA;
+  PackJoin j = {};
+  j.plan = p.plan, j.plan_bytes = p.plan_bytes, j.N = N, j.M = M, j.Hq = Hq, j.Hkv = Hkv, j.G = p.G, j.tpt = p.tpt;
+  j.part = p.part, j.part_q = p.part_q, j.scale = scale, j.status = p.status;
+  j.dq = dq, j.dqt = dq_token, j.dqh = dq_head, j.dk = dk, j.dkt = dk_token, j.dkh = dk_head, j.dv = dv, j.dvt = dv_token, j.dvh = dv_head;
+  if (launch_pack_join(j, D, f16, true, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;
 }

@@ -18,8 +18,8 @@
 // Keys behind the last one of a sequence belong to another: their scores are masked, and the V rows among the 16 of the
 // last MMA step are zeroed in shared memory (0 x NaN is NaN), the steps behind it left out.
 //
-// Entries that the plan cut leave (O, m, l) in the workspace; the last of an entry's chunks to arrive joins them in the
-// order of the chunks, so results do not depend on which it was.
+// Entries that the plan cut leave (O, m, l) in the workspace; a kernel behind this one joins them, chunk by chunk in their
+// order.
 #include <climits>
 #include <type_traits>
 
@@ -53,10 +53,10 @@ struct __align__(1024) PFwdSmem {
   uint8_t v[C::kVs][C::kSubs][kPackSub];
   PackEntry item[kSlots];
   uint64_t q_full[C::kQ], q_empty[C::kQ], k_full[C::kKs], v_full[C::kVs], k_empty[C::kKs], v_empty[C::kVs];
-  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2], sync[2];
+  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
   uint64_t tail, item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
-  int abort_flag, last[2];
+  int abort_flag;
 };
 
 struct PFwdParams {
@@ -68,7 +68,6 @@ struct PFwdParams {
   long long ot, oh;
   float* lse;
   int* counter;   // next item
-  int* arrivals;  // [cut][Hkv][2]
   float* part;    // [slot][Hkv][2][(D + 2) x 128]
   int stall;
   int* status;
@@ -83,11 +82,6 @@ __device__ __forceinline__ void fwd_range(const PackEntry& e, int g, int tpt, in
   a = e.a;
   if (window && first - window + 1 > 0) a = max(a, (first - window + 1) / kTile);
   if (a >= b) a = b = 0;
-}
-
-// weight of a chunk's sums beside the largest reference
-__device__ __forceinline__ float share(float2 ml, float m) {
-  return ml.x == -INFINITY ? (ml.y == ml.y ? 0.f : ml.y) : ex2_approx(ml.x - m);
 }
 
 template <int D, bool F16>
@@ -118,7 +112,6 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(&sm.s_full[g], 1), mbar_init(&sm.s_free[g], 4);
       mbar_init(&sm.p_full[g][0], 4), mbar_init(&sm.p_full[g][1], 4);
       mbar_init(&sm.pv_done[g], 1), mbar_init(&sm.o_full[g], 1), mbar_init(&sm.o_empty[g], 4);
-      mbar_init(&sm.sync[g], 4);
     }
     mbar_init(&sm.tail, 1), mbar_init(&sm.drain[0], 1), mbar_init(&sm.drain[1], 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], C::kIssuers + 8);
@@ -339,7 +332,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = lanes + 128u * g, tO = lanes + 256u + D * g, tP = kOwnP ? lanes + 384u + 64u * g : tS;
     const int r_tok = r / p.G, r_head = r - r_tok * p.G;
-    int n_s = 0, n_o = 0, n_sync = 0;
+    int n_s = 0, n_o = 0;
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -498,49 +491,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_after();
         ++n_o;
       }
-      float inv;
-      const bool joined = e.slot >= 0;
-      const long long stride = static_cast<long long>(p.Hkv) * 2 * kTile * (D + 2);  // from chunk to chunk
-      float* const base = p.part + (static_cast<long long>(e.slot) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
-      if (joined) {
-        // leave this chunk's share; the last to arrive takes them all, in their order
-        float* const mine = base + e.chunk * stride;
-#pragma unroll 1
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t acc[D / 32][16];
-          quad_part<D>(acc, tO, hf, a < b);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<float2*>(mine + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)) =
-                  make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
-        }
+      float inv = 1.f;
+      const bool cut = e.slot >= 0;
+      float* const mine = p.part + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * 2 * kTile * (D + 2) + g * kTile * (D + 2);
+      if (cut) {
         reinterpret_cast<float2*>(mine + kTile * D)[r] = make_float2(m, l);
-        if (a < b) {
-          tc_fence_before();
-          warp_arrive(&sm.o_empty[g]);
-        }
-        __threadfence();
-        warp_arrive(&sm.sync[g]);
-        if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (r == 0) sm.last[g] = atomicAdd(p.arrivals + (static_cast<long long>(e.cut) * p.Hkv + head) * 2 + g, 1) == e.chunks - 1;
-        warp_arrive(&sm.sync[g]);
-        if (!warp_wait(&sm.sync[g], n_sync & 1, abort_flag, p.status)) break;
-        ++n_sync;
-        if (!*reinterpret_cast<volatile int*>(&sm.last[g])) {
-          warp_arrive(&sm.item_empty[slot]);
-          continue;
-        }
-        __threadfence();
-        m = -INFINITY, l = 0.f;
-        for (int c = 0; c < e.chunks; ++c) m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r).x);
-        for (int c = 0; c < e.chunks; ++c) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r);
-          l = fmaf(ml.y, share(ml, m), l);
-        }
-        inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
       } else {
         // O is divided by the sum with the largest score's weight as the product saw it, rounded: a row with one key gives
         // that row of V exactly
@@ -553,20 +508,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t acc[D / 32][16];
-        quad_part<D>(acc, tO, hf, !joined && a < b);
-        if (joined) {
-          for (int c = 0; c < e.chunks; ++c) {
-            const float f = share(__ldcg(reinterpret_cast<const float2*>(base + c * stride + kTile * D) + r), m);
-            const float fu[2] = {__shfl_sync(0xffffffffu, f, hf * 16 + (lane >> 2)), __shfl_sync(0xffffffffu, f, hf * 16 + (lane >> 2) + 8)};
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(base + c * stride + (quarter * 32 + hf * 16 + (lane >> 2) + 8 * u) * D + 8 * i + 2 * (lane & 3)));
-                uint32_t* y = &acc[i >> 2][(i & 3) * 4 + 2 * u];
-                y[0] = __float_as_uint(fmaf(x.x, fu[u], __uint_as_float(y[0]))), y[1] = __float_as_uint(fmaf(x.y, fu[u], __uint_as_float(y[1])));
-              }
-          }
+        quad_part<D>(acc, tO, hf, a < b);
+        if (cut) {  // this chunk's share, for the join behind this kernel
+          leave_part<D, D>(mine, acc, quarter * 32 + hf * 16 + (lane >> 2));
+          continue;
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -576,11 +521,11 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           quad_store<D, F16>(p.o + (e.q0 + g * p.tpt + t) * p.ot + qh * p.oh, t < n_tok, acc, u, f);
         }
       }
-      if (!joined && a < b) {
+      if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.o_empty[g]);
       }
-      if (valid) p.lse[(static_cast<long long>(e.q0) + g * p.tpt + r_tok) * p.Hq + head * p.G + r_head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
+      if (valid && !cut) p.lse[(static_cast<long long>(e.q0) + g * p.tpt + r_tok) * p.Hq + head * p.G + r_head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPackLn2;
       warp_arrive(&sm.item_empty[slot]);
     }
   }
@@ -624,7 +569,7 @@ extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, lon
   if (static_cast<long long>(N) * Hq >= (1ll << 31) - 256 || static_cast<long long>(M) * Hkv >= (1ll << 31) - 256) return SCFA_ERR_UNSUPPORTED;
   const int sms = num_sms();
   const PackWs w = pack_ws(D, sms);
-  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.stats) return SCFA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < w.forward) return SCFA_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < sizeof(PackHeader)) return SCFA_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N > 0 && (!lse || !pack_rows_ok(q, q_token, q_head, N, Hq) || !o || (reinterpret_cast<uintptr_t>(o) & 15u) ||
@@ -638,7 +583,7 @@ extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, lon
   p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
   p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.scale_log2 = factor;
   p.o = o, p.ot = o_token, p.oh = o_head, p.lse = lse;
-  p.counter = reinterpret_cast<int*>(c + w.counters), p.arrivals = p.counter + 2;
+  p.counter = reinterpret_cast<int*>(c + w.counters);
   p.part = reinterpret_cast<float*>(c + w.part);
   p.stall = (flags & SCFA_FLAG_DEBUG_STALL) ? 1 : 0, p.status = reinterpret_cast<int*>(c);
   const bool f16 = dtype == SCFA_DTYPE_F16;
@@ -651,6 +596,10 @@ extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, lon
   const cudaError_t e = D == 64 ? (f16 ? launch<64, true>(tq, tk, tv, p, sms, st) : launch<64, false>(tq, tk, tv, p, sms, st))
                                 : (f16 ? launch<128, true>(tq, tk, tv, p, sms, st) : launch<128, false>(tq, tk, tv, p, sms, st));
   if (e != cudaSuccess) return SCFA_ERR_CUDA;
+  PackJoin j = {};
+  j.plan = p.plan, j.plan_bytes = p.plan_bytes, j.N = N, j.M = M, j.Hq = Hq, j.Hkv = Hkv, j.G = p.G, j.tpt = p.tpt;
+  j.part = p.part, j.o = o, j.ot = o_token, j.oh = o_head, j.lse = lse, j.status = p.status;
+  if (launch_pack_join(j, D, f16, false, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;
 }

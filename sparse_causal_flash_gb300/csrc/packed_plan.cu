@@ -7,9 +7,11 @@
 //
 // Cutting. A kernel's CTAs take pieces from a counter, longest first. Where few tiles have long ranges (a long prefix
 // under few new tokens, few heads) that leaves SMs idle, so ranges longer than L units are cut into equal chunks whose
-// results are joined later, in order. L is the candidate with the least estimate of
-//   time = max(units per SM, L x rounds of chunks near that length) + what leaving and joining a chunk costs,
-// among eighths of the units per SM and "no cut".
+// results are joined later, in order. L is the candidate with the least estimate among eighths of the units per SM and
+// "no cut". The estimate is a round's length times the rounds that the long pieces take, less what the short ones fill of
+// the last round, and three units for leaving and joining a chunk.
+// Where all tiles are alike (a window, equal texts) the last round may be nearly empty: 784 items of 17 units on 152 SMs
+// take six rounds for 5.2. Then the items of that round alone are cut.
 #include "packed.cuh"
 
 namespace scfa {
@@ -86,8 +88,8 @@ __device__ __forceinline__ void tile_range(int list, int i, int n, int m, int tp
 __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs p) {
   __shared__ int s_warp[32];
   __shared__ int s_bin[kBins], s_big[kCandidates], s_cut[kCandidates];
-  __shared__ unsigned long long s_units;
-  __shared__ int s_most, s_bad, s_limit, s_slots, s_cuts;
+  __shared__ unsigned long long s_units, s_work[kCandidates];  // units of long pieces
+  __shared__ int s_most, s_bad, s_limit, s_tail, s_tail_limit, s_slots, s_cuts;
   const int list = blockIdx.x, tid = threadIdx.x;
   PackHeader* h = reinterpret_cast<PackHeader*>(p.plan);
   int* const pre = reinterpret_cast<int*>(p.plan + p.L.pre) + static_cast<long long>(list) * (p.R + 1);
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   int2* const units = reinterpret_cast<int2*>(p.plan + p.L.units[list]);
   PackEntry* const out = reinterpret_cast<PackEntry*>(p.plan + p.L.entries[list]);
   if (tid == 0) s_units = 0, s_most = 0, s_bad = 0, s_slots = 0, s_cuts = 0;
-  if (tid < kCandidates) s_big[tid] = s_cut[tid] = 0;
+  if (tid < kCandidates) s_big[tid] = s_cut[tid] = 0, s_work[tid] = 0;
   s_bin[tid] = 0;
   __syncthreads();
   bool bad = false;
@@ -112,7 +114,8 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
       h->qtiles = static_cast<long long>(p.L.qtiles), h->bytes = static_cast<long long>(p.L.total);
       h->status = refused ? SCFA_ERR_INVALID : SCFA_OK;
     }
-    h->entries[list] = static_cast<long long>(p.L.entries[list]);
+    h->entries[list] = static_cast<long long>(p.L.entries[list]), h->cuts[list] = static_cast<long long>(p.L.cuts[list]);
+    h->n_cuts[list] = 0;
     h->list_status[list] = refused ? SCFA_ERR_INVALID : SCFA_OK;
     if (refused) h->n_entries[list] = 0;
     if (refused && list == kListDq) h->n_qtiles = 0;
@@ -155,43 +158,64 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     return static_cast<int>(min(static_cast<long long>(longest), max(2ll, (per_sm * (c + 2) + 7) / 8)));
   };
   int big[kCandidates], cut[kCandidates];
+  unsigned long long work[kCandidates];
 #pragma unroll
-  for (int c = 0; c < kCandidates; ++c) big[c] = cut[c] = 0;
+  for (int c = 0; c < kCandidates; ++c) big[c] = cut[c] = 0, work[c] = 0;
   for (int g = tid; g < tiles; g += kPlanThreads) {
     const int u = units[g].x;
 #pragma unroll
     for (int c = 0; c < kCandidates; ++c) {
       const int L = candidate(c), n = u > L ? (u + L - 1) / L : 1;
       if (n > 1) cut[c] += n;
-      if (u > L / 2) big[c] += n;
+      if (u > L / 2) big[c] += n, work[c] += u;
     }
   }
 #pragma unroll
   for (int c = 0; c < kCandidates; ++c) {
     const int x = __reduce_add_sync(0xffffffffu, big[c]), y = __reduce_add_sync(0xffffffffu, cut[c]);
+    unsigned long long z = work[c];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if ((tid & 31) == 0 && z) atomicAdd(&s_work[c], z);
     if ((tid & 31) == 0 && x) atomicAdd(&s_big[c], x);
     if ((tid & 31) == 0 && y) atomicAdd(&s_cut[c], y);
   }
   __syncthreads();
   if (tid == 0) {
+    // in quarters of a unit, over all SMs
     long long best = 1ll << 62;
+    s_tail = tiles;
+    const long long room = static_cast<long long>(kPackSlotsPerSm) * p.sms, all = static_cast<long long>(s_units) * p.Hkv;
     for (int c = kCandidates - 1; c >= 0; --c) {
       const long long L = candidate(c), n = static_cast<long long>(s_big[c]) * p.Hkv, k = static_cast<long long>(s_cut[c]) * p.Hkv;
-      if (k > static_cast<long long>(kPackSlotsPerSm) * p.sms) continue;
-      // in quarters of a unit: leaving and joining a chunk costs about two units
-      long long t = n > 3ll * p.sms ? 4 * per_sm + 4 * L / 3 : max(4 * per_sm, 4 * L * ((n + p.sms - 1) / p.sms));
-      t += 8 * k / p.sms + (k ? 4 : 0);
+      if (k > room) continue;
+      const long long rounds = (n + p.sms - 1) / p.sms, fill = all - static_cast<long long>(s_work[c]) * p.Hkv;
+      const long long idle = max(0ll, (rounds * p.sms - n) * L * 3 / 4 - fill);
+      const long long t = 4 * (all + idle) + 12 * k + (k ? 4ll * p.sms : 0);
       if (t < best) best = t, s_limit = static_cast<int>(L);
+    }
+    const long long n = static_cast<long long>(s_big[kCandidates - 1]) * p.Hkv, over = n % p.sms;
+    if (s_limit >= longest && n > p.sms && over > 0 && 8 * (all - static_cast<long long>(s_work[kCandidates - 1]) * p.Hkv) < all) {
+      // the items beyond whole rounds, cut to a share of an SM each
+      const long long cut_tiles = (over + p.Hkv - 1) / p.Hkv, share = max(2ll, (cut_tiles * p.Hkv * longest + p.sms - 1) / p.sms);
+      const long long chunks = cut_tiles * p.Hkv * ((longest + share - 1) / share);
+      const long long t = 4 * p.sms * (n / p.sms * longest + share + 1) + 12 * chunks;
+      if (chunks <= room && cut_tiles <= tiles && share < longest && t < 4 * p.sms * ((n + p.sms - 1) / p.sms) * longest)
+        s_tail = tiles - static_cast<int>(cut_tiles), s_tail_limit = static_cast<int>(share);
     }
   }
   __syncthreads();
-  const int L = s_limit;
+  const int L = s_limit, tail = s_tail, tail_limit = s_tail_limit;
+  auto pieces = [&](int g, int u) {  // of tile g
+    const int most_units = g >= tail ? tail_limit : L;
+    return u > most_units ? (u + most_units - 1) / most_units : 1;
+  };
   const int top = max(1, min(longest, L));
   auto bin = [&](int u) { return kBins - 1 - static_cast<int>(static_cast<long long>(min(u, top)) * (kBins - 1) / top); };
 
   // pieces by length, longest first
   for (int g = tid; g < tiles; g += kPlanThreads) {
-    const int u = units[g].x, n = u > L ? (u + L - 1) / L : 1;
+    const int u = units[g].x, n = pieces(g, u);
     atomicAdd(&s_bin[bin(u / n)], n);
   }
   __syncthreads();
@@ -202,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   __syncthreads();
   for (int g = tid; g < tiles; g += kPlanThreads) {
     const int2 ur = units[g];
-    const int u = ur.x, r = ur.y, n = u > L ? (u + L - 1) / L : 1, i = g - pre[r];
+    const int u = ur.x, r = ur.y, n = pieces(g, u), i = g - pre[r];
     const int q0 = p.q_start[r], nq = p.q_start[r + 1] - q0, k0 = p.k_start[r], m = p.k_start[r + 1] - k0;
     int a, b;
     tile_range(list, i, nq, m, p.tpt, p.window, a, b);
@@ -215,9 +239,12 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
       e.q0 = q0 + i * tile, e.k0 = k0, e.n_tok = min(tile, nq - i * tile), e.diag = i * tile + m - nq, e.m = m;
       e.tile0 = g;
     }
-    e.slot = n > 1 ? atomicAdd(&s_slots, n) : -1;
-    e.cut = n > 1 ? atomicAdd(&s_cuts, 1) : 0;
     const int at = atomicAdd(&s_bin[bin(u / n)], n);
+    e.slot = -1;
+    if (n > 1) {
+      e.slot = atomicAdd(&s_slots, n);
+      reinterpret_cast<int*>(p.plan + p.L.cuts[list])[atomicAdd(&s_cuts, 1)] = at;
+    }
     for (int c = 0; c < n; ++c) {
       e.chunk = c;
       e.a = a + static_cast<int>(static_cast<long long>(u) * c / n);
@@ -225,7 +252,9 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
       out[at + c] = e;
     }
   }
+  __syncthreads();
   if (tid == 0) {
+    h->n_cuts[list] = s_cuts;
     h->n_entries[list] = total;
     if (list == kListDq) h->n_qtiles = tiles;
   }
@@ -262,7 +291,7 @@ size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int
   const int sms = num_sms();
   if ((D != 64 && D != 128) || !pack_plan_layout(N, M, R, Hq, Hkv, sms, &L)) return 0;
   const PackWs w = pack_ws(D, sms);
-  if (!backward) return w.stats;
+  if (!backward) return w.forward;
   const int tpt = kTile / (Hq / Hkv);
   return align_up(w.stats + static_cast<size_t>((N / tpt + static_cast<long long>(R)) * pack_stats_tile_bytes(Hkv)), 256);
 }
