@@ -309,6 +309,22 @@ __device__ __forceinline__ float pack_max3(float a, float b, float c) {
   return d;
 }
 
+// launch_behind() with shared memory; `behind` false: an ordinary launch.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind_with(void (*kern)(Params...), dim3 grid, int threads, size_t smem, bool behind, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Registers of a warpgroup's threads, which all of its warps change together: fewer, or more of what others gave up.
 template <int N>
 __device__ __forceinline__ void regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }

@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
       reinterpret_cast<int*>(p.stats)[2 * n + at] = live ? t.z + tok : -1;
     }
   }
+  grid_release();
 }
 
 // ------------------------------------------------------------------ what both kernels share
@@ -151,9 +152,16 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (bwd_plan_status(p) != SCFA_OK) return;  // (the kernel before has said so)
+  // Nothing here needs the dK / dV kernel: these CTAs come as its CTAs leave, and fill its last round. They end behind it,
+  // so that what follows this kernel follows both.
+  grid_release();
+  if (bwd_plan_status(p) != SCFA_OK) {  // (the first kernel has said so)
+    grid_wait();
+    return;
+  }
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
     if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
+    grid_wait();
     return;
   }
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
@@ -424,6 +432,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
+  grid_wait();
 }
 
 // ------------------------------------------------------------------ dK and dV
@@ -473,7 +482,9 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (bwd_plan_status(p) != SCFA_OK) return;  // (the kernel before has said so)
+  grid_wait();     // the rows' statistics are there,
+  grid_release();  // also for the dQ kernel, whose CTAs may come from now on
+  if (bwd_plan_status(p) != SCFA_OK) return;  // (the first kernel has said so)
   if (smem_u32(smem_raw) & 1023u) {  // the swizzled tiles need this; all shared memory there is leaves no room to move
     if (threadIdx.x == 0) raise_status(p.status, SCFA_ERR_UNSUPPORTED);
     return;
@@ -798,7 +809,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
 template <typename Kernel>
 cudaError_t launch_one(Kernel kern, size_t smem, bool (&allowed)[64], const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                       const CUtensorMap& dO, const PBwdParams& p, int grid, cudaStream_t st) {
+                       const CUtensorMap& dO, const PBwdParams& p, int grid, bool behind, cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -807,8 +818,7 @@ cudaError_t launch_one(Kernel kern, size_t smem, bool (&allowed)[64], const CUte
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) allowed[dev] = true;
   }
-  kern<<<grid, kThreads, smem, st>>>(q, k, v, dO, p);
-  return cudaGetLastError();
+  return launch_behind_with(kern, dim3(grid), kThreads, smem, behind, st, q, k, v, dO, p);
 }
 
 template <int D, bool F16>
@@ -819,9 +829,9 @@ cudaError_t launch_bwd(const CUtensorMap& q, const CUtensorMap& k, const CUtenso
   static_assert(dq_smem <= 227 * 1024 && dkv_smem <= 227 * 1024, "shared memory per CTA");
   packed_stats_kernel<D, F16><<<8 * sms, 256, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && p.M > 0) e = launch_one(packed_dkv_kernel<D, F16>, dkv_smem, dkv_allowed, q, k, v, dO, p, sms, st);
+  if (e == cudaSuccess && p.M > 0) e = launch_one(packed_dkv_kernel<D, F16>, dkv_smem, dkv_allowed, q, k, v, dO, p, sms, true, st);
   ++p.counter;
-  if (e == cudaSuccess && p.N > 0) e = launch_one(packed_dq_kernel<D, F16>, dq_smem, dq_allowed, q, k, v, dO, p, sms, st);
+  if (e == cudaSuccess && p.N > 0) e = launch_one(packed_dq_kernel<D, F16>, dq_smem, dq_allowed, q, k, v, dO, p, sms, p.M > 0, st);
   return e;
 }
 

@@ -129,6 +129,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* const abort_flag = &sm.abort_flag;
+  grid_release();  // the join's CTAs come as these leave
 
   if (warp < 4) {
   regs_release<kRegsFew>();
