@@ -49,7 +49,7 @@ struct PackHeader {
   int n_cuts[kLists];       // entries that are cut, per key head
   int pad0[2];
   long long entries[kLists];  // byte offsets from the plan's start
-  long long cuts[kLists];     // int: the first chunk's entry of each cut one
+  long long cuts[kLists];     // PackEntry: the first chunk of each cut one
   long long qtiles;           // int4 (first token, tokens, last key of the first token, 0) of each query tile
   long long bytes;
   int pad[28];
@@ -86,7 +86,7 @@ inline bool pack_plan_layout(int N, int M, int R, int Hq, int Hkv, int sms, Pack
   for (int i = 0; i < kLists; ++i) w.units[i] = take(static_cast<size_t>(w.most[i]) * sizeof(int2));
   w.qtiles = take((static_cast<size_t>(N / tpt) + R) * sizeof(int4));
   for (int i = 0; i < kLists; ++i) w.entries[i] = take(static_cast<size_t>(w.most[i]) * sizeof(PackEntry));
-  for (int i = 0; i < kLists; ++i) w.cuts[i] = take(static_cast<size_t>(pack_slots(sms)) * sizeof(int));
+  for (int i = 0; i < kLists; ++i) w.cuts[i] = take(static_cast<size_t>(pack_slots(sms)) / 2 * sizeof(PackEntry));
   w.total = off;
   *L = w;
   return true;
@@ -330,6 +330,35 @@ template <int N>
 __device__ __forceinline__ void regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// The producer warp's way to its pieces of work: the CTA's first one by its number, fetched while the CTA is set up, the
+// others from the counter, one ahead.
+struct PackWork {
+  const PackEntry* entries;
+  int n_work, Hkv, w, word;
+  __device__ __forceinline__ void fetch(int lane) {
+    word = w < n_work && lane < 16 ? __ldg(reinterpret_cast<const int*>(entries + w / Hkv) + lane) : 0;
+  }
+  __device__ __forceinline__ void first(const PackEntry* e, int n, int heads, int lane) {
+    entries = e, n_work = n, Hkv = heads, w = static_cast<int>(blockIdx.x);
+    fetch(lane);
+  }
+  __device__ __forceinline__ void next(int* counter, int lane) {
+    int v = 0;
+    if (lane == 0) v = atomicAdd(counter, 1);
+    w = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
+    fetch(lane);
+  }
+  // the piece into its slot; false at the end
+  __device__ __forceinline__ bool publish(PackEntry* slot, uint64_t* full, int lane) {
+    const bool some = w < n_work;
+    if (some && lane < 16) reinterpret_cast<int*>(slot)[lane] = word;
+    __syncwarp();
+    if (lane == 0) slot->head = some ? w % Hkv : -1;
+    warp_arrive(full);
+    return some;
+  }
+};
 
 // Rows [from, to) of a tile in shared memory become zero (whole rows: the swizzle moves 16-byte pieces inside a row).
 __device__ __forceinline__ void zero_tile_rows(uint8_t* tile, int subs, int from, int to, int lane, int lanes) {

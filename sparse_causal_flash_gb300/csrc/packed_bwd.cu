@@ -102,26 +102,6 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
   grid_release();
 }
 
-// ------------------------------------------------------------------ what both kernels share
-// The next piece of work into its slot, by the whole producer warp; false at the end.
-__device__ __forceinline__ bool next_item(PackEntry* items, uint64_t* full, uint64_t* empty, int it, const PackEntry* entries,
-                                          int n_work, int Hkv, int* counter, int lane, volatile int* abort_flag, int* status,
-                                          bool& ok) {
-  const int slot = it % kSlots;
-  ok = warp_wait(&empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, status);
-  if (!ok) return false;
-  int w = 0;
-  if (lane == 0) w = atomicAdd(counter, 1);
-  w = __shfl_sync(0xffffffffu, w, 0);
-  const int head = w < n_work ? w % Hkv : -1;
-  if (head >= 0 && lane < 16)
-    reinterpret_cast<int*>(&items[slot])[lane] = __ldg(reinterpret_cast<const int*>(entries + w / Hkv) + lane);
-  __syncwarp();
-  if (lane == 0) items[slot].head = head;
-  warp_arrive(&full[slot]);
-  return head >= 0;
-}
-
 // ------------------------------------------------------------------ dQ
 // TMEM: S [0,128), dP [128,256), dQ [256,256+D), two buffers of dS at 384 and 448. Products in the order
 // dP(j+1) S(j+1) dQ(j): dP of a tile is in registers while its S runs, and there are two products' time to make dS from
@@ -167,6 +147,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
   const int window = h->window, n_work = h->n_entries[kListDq] * p.Hkv, used = p.G * p.tpt;
   const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
+  PackWork work;
+  if (warp == 0) work.first(reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDq]), n_work, p.Hkv, lane);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
@@ -199,14 +181,18 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     regs_release<kRegsFew>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDq]);
       int q_it = 0, k_it = 0, v_it = 0, tails = 0, unmarked = -1;  // unmarked: K tile whose zeros an abort kept from being written
       bool ok = true;
       for (int it = 0; ok; ++it) {
-        if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
-        const PackEntry& e = sm.item[it % kSlots];
+        const int slot = it % kSlots;
+        ok = warp_wait(&sm.item_empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, p.status);
+        if (!ok || !work.publish(&sm.item[slot], &sm.item_full[slot], lane)) break;
+        const PackEntry& e = sm.item[slot];
         const int head = e.head, a = e.a, b = e.b;
-        if (a == b) continue;
+        if (a == b) {
+          work.next(p.counter, lane);
+          continue;
+        }
         if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
         {
           const int s = q_it % kQs;
@@ -251,6 +237,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             fence_proxy_async_smem();
             warp_arrive(&sm.k_full[s]);
           }
+          if (j == a) work.next(p.counter, lane);  // (under the loads)
         }
       }
       if (lane == 0) {
@@ -492,6 +479,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(p.plan);
   const int window = h->window, n_work = h->n_entries[kListDkv] * p.Hkv, used = p.G * p.tpt;
   const long long n_stats = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;
+  PackWork work;
+  if (warp == 0) work.first(reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDkv]), n_work, p.Hkv, lane);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
@@ -523,7 +512,6 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     regs_release<kRegsFew>();
     if (warp == 0) {
       // ---------------------------------------------------------- producer
-      const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDkv]);
       int k_it = 0, q_it = 0, do_it = 0, st_it = 0, tails[2] = {0, 0}, unmarked[2] = {-1, -1};
       bool ok = true;
       // Q or dO tile of query tile i into its ring; rows behind the sequence's
@@ -553,10 +541,15 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         return true;
       };
       for (int it = 0; ok; ++it) {
-        if (!next_item(sm.item, sm.item_full, sm.item_empty, it, entries, n_work, p.Hkv, p.counter, lane, abort_flag, p.status, ok)) break;
-        const PackEntry& e = sm.item[it % kSlots];
+        const int slot = it % kSlots;
+        ok = warp_wait(&sm.item_empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, p.status);
+        if (!ok || !work.publish(&sm.item[slot], &sm.item_full[slot], lane)) break;
+        const PackEntry& e = sm.item[slot];
         const int head = e.head, a = e.a, b = e.b;
-        if (a == b) continue;
+        if (a == b) {
+          work.next(p.counter, lane);
+          continue;
+        }
         if (p.stall && k_it == 0) break;  // debug stall: no load ever arrives
         {
           const int s = k_it % kKs;
@@ -585,6 +578,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           ++st_it;
           ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i);
+          if (i == a) work.next(p.counter, lane);  // (under the loads)
         }
       }
       if (lane == 0) {

@@ -103,6 +103,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   }
   const int window = h->window, n_work = h->n_entries[kListFwd] * p.Hkv;
   const int used = p.G * p.tpt;  // rows of a tile that hold a query
+  PackWork work;
+  if (warp == 0) work.first(reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListFwd]), n_work, p.Hkv, lane);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kQ; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
@@ -135,25 +137,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   regs_release<kRegsFew>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const PackEntry* const entries = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListFwd]);
     int q_it = 0, k_it = 0, kv_it = 0, tails = 0, unmarked = -1;  // unmarked: V tile whose zeros an abort kept from being written
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int slot = it % kSlots;
       ok = warp_wait(&sm.item_empty[slot], ((it / kSlots) & 1) ^ 1, abort_flag, p.status);
-      if (!ok) break;
-      int w = 0;
-      if (lane == 0) w = atomicAdd(p.counter, 1);
-      w = __shfl_sync(0xffffffffu, w, 0);
-      const int head = w < n_work ? w % p.Hkv : -1;
-      PackEntry& item = sm.item[slot];
-      if (head >= 0 && lane < 16)
-        reinterpret_cast<int*>(&item)[lane] = __ldg(reinterpret_cast<const int*>(entries + w / p.Hkv) + lane);
-      __syncwarp();
-      if (lane == 0) item.head = head;
-      warp_arrive(&sm.item_full[slot]);
-      if (head < 0) break;
-      const PackEntry& e = item;
+      if (!ok || !work.publish(&sm.item[slot], &sm.item_full[slot], lane)) break;
+      const PackEntry& e = sm.item[slot];
+      const int head = e.head;
       int a[2], b[2];
       fwd_range(e, 0, p.tpt, window, a[0], b[0]);
       fwd_range(e, 1, p.tpt, window, a[1], b[1]);
@@ -171,6 +162,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       if (p.stall && k_it == 0 && a[0] + b[0] + a[1] + b[1] > 0) break;  // debug stall: no K / V load ever arrives
       const int j0 = a[0] == b[0] ? a[1] : a[1] == b[1] ? a[0] : min(a[0], a[1]), j1 = max(b[0], b[1]);
+      if (j0 == j1) work.next(p.counter, lane);
       for (int j = j0; j < j1 && ok; ++j) {
         const int valid = e.m - j * kTile;  // keys of the sequence in the tile, if below 128
         const bool cut = valid < kTile && (valid & 15) != 0;
@@ -201,6 +193,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           fence_proxy_async_smem();
           warp_arrive(&sm.v_full[s]);
         }
+        if (j == j0) work.next(p.counter, lane);  // (under the loads)
       }
     }
     if (lane == 0) {

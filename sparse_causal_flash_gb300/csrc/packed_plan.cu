@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     e.slot = -1;
     if (n > 1) {
       e.slot = atomicAdd(&s_slots, n);
-      reinterpret_cast<int*>(p.plan + p.L.cuts[list])[atomicAdd(&s_cuts, 1)] = at;
+      reinterpret_cast<PackEntry*>(p.plan + p.L.cuts[list])[atomicAdd(&s_cuts, 1)] = e;
     }
     for (int c = 0; c < n; ++c) {
       e.chunk = c;
