@@ -680,6 +680,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
     const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
     int t = 0, n_acc = 0;
+    uint32_t s_col = col0;  // of the tile's region, this warpgroup's columns
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -689,8 +690,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
       auto tile = [&](auto masked, int i) -> bool {
         const int ss = t % kStatStages;
-        const uint32_t s_at = lanes + 128u * (kRegions == 2 ? t & 1 : 2 * t % 3) + col0;
-        const uint32_t dp_at = lanes + 128u * (kRegions == 2 ? (t & 1) ^ 1 : (2 * t + 1) % 3) + col0;
+        const uint32_t s_at = lanes + s_col, dp_at = lanes + (kRegions == 2 ? s_col ^ 128u : s_col >= 256u + col0 ? s_col - 256u : s_col + 128u);
         uint32_t x[64], pk[32];
         // which of the queries c .. c + 3 see this thread's key, as masks of two 16-bit pairs
         auto keep = [&](int c, uint32_t& k0, uint32_t& k1) {
@@ -698,8 +698,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           k0 = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
           k1 = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
         };
-        if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
         if (!warp_wait(&sm.s_full[t & 1], (t >> 1) & 1, abort_flag, p.status)) return false;
+        if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
         tc_fence_after();
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
@@ -754,14 +754,29 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_fence_before();
         warp_arrive(&sm.ds_full);
         ++t;
+        s_col = kRegions == 2 ? s_col ^ 128u : s_col >= 128u + col0 ? s_col - 128u : s_col + 256u;  // 0 2 1 0 2 1 ..
         return true;
       };
+      // Tiles [plain, last) need no mask: whole ones whose first token sees the last key of a whole key tile and whose last
+      // token still sees the first
+      int plain = b, last = b;
+      if (a < b) {
+        const long long see = static_cast<long long>(e.diag) + kTile - 1 - e.shift;  // token that sees the last key
+        plain = static_cast<int>(min(static_cast<long long>(b), max(static_cast<long long>(a), see <= 0 ? 0 : (see + p.tpt - 1) / p.tpt)));
+        last = min(b, e.m / p.tpt);
+        if (window) {
+          const long long until = static_cast<long long>(e.diag) + window - e.shift;  // the first token that no longer sees the first key
+          last = until < p.tpt ? plain : static_cast<int>(min(static_cast<long long>(last), until / p.tpt));
+        }
+        last = max(last, plain);
+      }
       bool ok = true;
-      const int last_key = e.diag + kTile - 1;  // (of a whole tile)
-      for (int i = a; i < b && ok; ++i) {
-        const int first = i * p.tpt + e.shift;  // the last key of the tile's first token
-        const bool whole = first >= last_key && (i + 1) * p.tpt <= e.m && (!window || first + p.tpt - 1 - window < e.diag);
-        ok = whole ? tile(std::false_type{}, i) : tile(std::true_type{}, i);
+      int i = a;
+      for (int part = 0; part < 2 && ok; ++part) {
+        const int stop = part ? b : plain;
+        for (; i < stop && ok; ++i) ok = tile(std::true_type{}, i);
+        if (part == 0)
+          for (; i < last && ok; ++i) ok = tile(std::false_type{}, i);
       }
       if (!ok) break;
       if (a < b) {
