@@ -342,21 +342,38 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         warp_arrive(&sm.dp_free);
         if (!warp_wait(&sm.s_full, n & 1, abort_flag, p.status)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) tmem_ld32(lanes + col0 + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-        tmem_wait_ld();
-        tmem_ld_fence(sr);
-        tc_fence_before();
-        warp_arrive(&sm.s_free);
-        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), nd2 = f2(nd, nd);
         uint32_t pk[32];
+        auto weigh = [&](int from, int to) {
+          const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), nl2 = f2(nl, nl), nd2 = f2(nd, nd);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float x0, x1;
-          f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, nl2), x0, x1);
-          x0 = ex2_approx(x0), x1 = ex2_approx(x1);
-          f2_split(mul2(f2(x0, x1), add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2)), x0, x1);
-          pk[c >> 1] = c4_pack<F16>(x0, x1);
+          for (int c = from; c < to; c += 2) {
+            float x0, x1;
+            f2_split(fma2(f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), sl2, nl2), x0, x1);
+            x0 = ex2_approx(x0), x1 = ex2_approx(x1);
+            f2_split(mul2(f2(x0, x1), add2(f2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), nd2)), x0, x1);
+            pk[c >> 1] = c4_pack<F16>(x0, x1);
+          }
+        };
+        uint32_t(&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+        uint32_t(&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+        tmem_ld32(lanes + col0, s0);
+        if (D == 64) {  // the other half of S comes under the first half's exponentials (651 -> 605 us at 16384 tokens, 16 heads
+          tmem_wait_ld();  // over 4; at D = 128, where the MMAs wait for these columns, 447 -> 467 us at 8192, 32 over 8)
+          tmem_ld_fence(s0);
+          tmem_ld32(lanes + col0 + 32, s1);
+          weigh(0, 32);
+          tmem_wait_ld();
+          tmem_ld_fence(s1);
+          tc_fence_before();
+          warp_arrive(&sm.s_free);
+          weigh(32, 64);
+        } else {
+          tmem_ld32(lanes + col0 + 32, s1);
+          tmem_wait_ld();
+          tmem_ld_fence(sr);
+          tc_fence_before();
+          warp_arrive(&sm.s_free);
+          weigh(0, 64);
         }
         if (decltype(masked)::value) {
           // lo <= column <= lim as one unsigned comparison
@@ -432,13 +449,14 @@ __device__ __forceinline__ void mma_half_steps(uint32_t d_tmem, uint32_t a_tmem,
   }
 }
 
-// Tiles are transposed: lanes are keys, columns queries. Scores take turns in regions of 128 TMEM columns: S^T(t) in one,
-// and a warpgroup writes P^T and dS^T of its 64 queries over its own 64 columns of it; dP^T(t) in another, free again once
-// it is in registers. D = 128 has two regions (dV and dK take the rest); its products come in the order
-//   dP(t) dV(t) S(t+1) dK(t),
-// which gives the softmax two products' time (1,024 cycles) for P behind S and for dS behind dP, and the tensor cores
-// work without a pause. D = 64, with products half as long, has three regions and the order S(t+1) dV(t) dK(t) dP(t+1):
-// four products for P, two for dS.
+// Tiles are transposed: lanes are keys, columns queries.
+// D = 128: scores take turns in two regions of 128 TMEM columns (dV and dK take the rest): S^T(t) in one, and a warpgroup
+// writes P^T and dS^T of its 64 queries over its own 64 columns of it; dP^T(t) in the other, free again once it is in
+// registers. Products come in the order dP(t) dV(t) S(t+1) dK(t), which gives the softmax two products' time (1,024 cycles)
+// for P behind S and for dS behind dP, and the tensor cores work without a pause.
+// D = 64: products take half the time, the softmax the same. S^T, dP^T, P^T and dS^T have columns of their own: S(t+1) and
+// dP(t+1) run while P(t) and dS(t) are made, in one go, so that exponentials and products share their cycles (made one
+// after another the kernel took 904 us instead of 832 at 16384 tokens, 16 heads over 4).
 template <int D>
 struct __align__(1024) DkvSmem {
   static constexpr int kSubs = D / 64, kQs = D == 64 ? 4 : 3, kOs = D == 64 ? 4 : 2, kKs = D == 64 ? 2 : 1;
@@ -451,7 +469,7 @@ struct __align__(1024) DkvSmem {
   PackEntry item[kSlots];
   uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kOs], do_empty[kOs];
   uint64_t st_full[kStatStages], st_empty[kStatStages];
-  uint64_t s_full[2], dp_full, dp_free, p_full[2], ds_full, acc_full, acc_empty, tail[2], drain;
+  uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, pd_free, acc_full, acc_empty, tail[2], drain;
   uint64_t item_full[kSlots], item_empty[kSlots];
   uint32_t tmem_base;
   int abort_flag;
@@ -464,7 +482,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const __grid_constant__ PBwdParams p) {
   using Sm = DkvSmem<D>;
   constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kOs = Sm::kOs, kKs = Sm::kKs;
-  constexpr int kRegions = D == 64 ? 3 : 2;
+  constexpr bool kOwn = D == 64;
   constexpr uint32_t colDV = 512 - 2 * D, colDK = 512 - D;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
@@ -487,9 +505,9 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
     for (int s = 0; s < kOs; ++s) mbar_init(&sm.do_full[s], 1), mbar_init(&sm.do_empty[s], 1);
     for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_empty[s], kSoftWarps);
-    mbar_init(&sm.s_full[0], 1), mbar_init(&sm.s_full[1], 1), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
-    mbar_init(&sm.p_full[0], kSoftWarps), mbar_init(&sm.p_full[1], kSoftWarps);
-    mbar_init(&sm.ds_full, kSoftWarps), mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, kSoftWarps);
+    mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, kSoftWarps), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
+    mbar_init(&sm.p_full, kSoftWarps), mbar_init(&sm.ds_full, kSoftWarps), mbar_init(&sm.pd_free, 1);
+    mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, kSoftWarps);
     mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1), mbar_init(&sm.drain, 1);
     for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
     sm.abort_flag = 0;
@@ -610,51 +628,52 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const int a = sm.item[slot].a, b = sm.item[slot].b, m_tok = sm.item[slot].m;
           if (a < b) {
             const int ks = k_it % kKs;
-            // t: query tile number over the CTA's whole work. Regions: S in 0 2 1 0 2 1 .. and dP in 1 0 2 1 0 2 ..
-            // of three, or each in turn in the one and the other of two
-            auto s_at = [&](int n) { return tmem + 128u * (kRegions == 2 ? n & 1 : 2 * n % 3); };
-            auto dp_at = [&](int n) { return tmem + 128u * (kRegions == 2 ? (n & 1) ^ 1 : (2 * n + 1) % 3); };
+            // t: query tile number over the CTA's whole work
+            auto s_at = [&](int n) { return tmem + (kOwn ? 0u : 128u * (n & 1)); };
+            auto dp_at = [&](int n) { return tmem + (kOwn ? 128u : 128u * ((n & 1) ^ 1)); };
             auto do_s = [&](int n) -> bool {
-              // two regions: where dP of the tile before was. Three: of the one before that, which dS has followed
-              if (kRegions == 2 && n > 0 && !mbar_wait(&sm.dp_free, (n - 1) & 1, abort_flag, p.status)) return false;
+              // (own columns: once S and dP of the tile before are in registers. Two regions: where dP of it was)
+              if (n > 0 && !mbar_wait(kOwn ? &sm.s_free : &sm.dp_free, (n - 1) & 1, abort_flag, p.status)) return false;
               if (!mbar_wait(&sm.q_full[n % kQs], (n / kQs) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
               mma_ss_steps<0, D / 16>(s_at(n), kd + ks * kTile16, qd + (n % kQs) * kTile16, idesc_s, false);
-              tc_commit(&sm.s_full[n & 1]);  // (two: with three regions S(t+1) may be complete before S(t) is waited for)
+              if (!kOwn) tc_commit(&sm.s_full);
               return true;
             };
-            auto do_dp = [&](int n) -> bool {  // (its region's P and dS are behind dV and dK that are issued already)
+            auto do_dp = [&](int n) -> bool {  // (two regions: P and dS that were there are behind dV and dK issued already)
               if (!mbar_wait(&sm.do_full[n % kOs], (n / kOs) & 1, abort_flag, p.status)) return false;
               tc_fence_after();
               mma_ss_steps<0, D / 16>(dp_at(n), vd + ks * kTile16, dod + (n % kOs) * kTile16, idesc_s, false);
-              tc_commit(&sm.dp_full);
+              tc_commit(kOwn ? &sm.s_full : &sm.dp_full);
               return true;
             };
             // dV += P^T dO, dK += dS^T Q
             auto do_dv = [&](int n, int i, int steps) -> bool {
               if (i == a && !mbar_wait(&sm.acc_empty, (n_acc & 1) ^ 1, abort_flag, p.status)) return false;
-              if (!mbar_wait(&sm.p_full[n & 1], (n >> 1) & 1, abort_flag, p.status)) return false;
+              if (!mbar_wait(&sm.p_full, n & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              mma_half_steps<0>(tmem + colDV, s_at(n), don + (n % kOs) * kTile16, idesc_a, i > a, steps);
+              if (kOwn) mma_ts_steps<0, 8>(tmem + colDV, tmem + 256, don + (n % kOs) * kTile16, idesc_a, i > a, steps);
+              else mma_half_steps<0>(tmem + colDV, s_at(n), don + (n % kOs) * kTile16, idesc_a, i > a, steps);
               tc_commit(&sm.do_empty[n % kOs]);
               return true;
             };
             auto do_dk = [&](int n, int i, int steps) -> bool {
-              if (!mbar_wait(&sm.ds_full, n & 1, abort_flag, p.status)) return false;
+              if (!kOwn && !mbar_wait(&sm.ds_full, n & 1, abort_flag, p.status)) return false;
               tc_fence_after();
-              mma_half_steps<0>(tmem + colDK, s_at(n) + 32, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
+              if (kOwn) mma_ts_steps<0, 8>(tmem + colDK, tmem + 320, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
+              else mma_half_steps<0>(tmem + colDK, s_at(n) + 32, qn + (n % kQs) * kTile16, idesc_a, i > a, steps);
               tc_commit(&sm.q_empty[n % kQs]);
+              if (kOwn) tc_commit(&sm.pd_free);
               return true;
             };
             ok = mbar_wait(&sm.k_full[ks], (k_it / kKs) & 1, abort_flag, p.status) && do_s(t);
-            if (kRegions == 3) ok = ok && do_dp(t);
+            if (kOwn) ok = ok && do_dp(t);
             for (int i = a; i < b && ok; ++i, ++t) {
               const bool next = i + 1 < b;
               const int steps = min(kTile / 16, (min(p.tpt, m_tok - i * p.tpt) * p.G + 15) >> 4);
-              if (kRegions == 3) {
-                if (next) ok = do_s(t + 1);
+              if (kOwn) {
+                if (next) ok = do_s(t + 1) && do_dp(t + 1);
                 ok = ok && do_dv(t, i, steps) && do_dk(t, i, steps);
-                if (next) ok = ok && do_dp(t + 1);
               } else {
                 ok = do_dp(t) && do_dv(t, i, steps);
                 if (next) ok = ok && do_s(t + 1);
@@ -680,7 +699,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
     const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
     int t = 0, n_acc = 0;
-    uint32_t s_col = col0;  // of the tile's region, this warpgroup's columns
+    uint32_t s_col = col0;  // this warpgroup's columns of S (two regions in turn at D = 128)
     for (int it = 0;; ++it) {
       const int slot = it % kSlots;
       if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -690,71 +709,116 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
       auto tile = [&](auto masked, int i) -> bool {
         const int ss = t % kStatStages;
-        const uint32_t s_at = lanes + s_col, dp_at = lanes + (kRegions == 2 ? s_col ^ 128u : s_col >= 256u + col0 ? s_col - 256u : s_col + 128u);
-        uint32_t x[64], pk[32];
+        const uint32_t s_at = lanes + s_col, dp_at = lanes + (s_col ^ 128u);
         // which of the queries c .. c + 3 see this thread's key, as masks of two 16-bit pairs
         auto keep = [&](int c, uint32_t& k0, uint32_t& k1) {
           const int4 h4 = __ldg(reinterpret_cast<const int4*>(all_hi + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile + col0 + c));
           k0 = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
           k1 = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
         };
-        if (!warp_wait(&sm.s_full[t & 1], (t >> 1) & 1, abort_flag, p.status)) return false;
-        if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
-        tmem_wait_ld();
-        tmem_ld_fence(x);
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
-        uint64_t pr[32];  // P, in pairs
+        if constexpr (kOwn) {
+          uint32_t x[64], y[64], ps[32], ds[32];
+          if (!warp_wait(&sm.s_full, t & 1, abort_flag, p.status)) return false;
+          if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][col0 + c]);
-          float y[4];
-          f2_split(fma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, f2(l4.x, l4.y)), y[0], y[1]);
-          f2_split(fma2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, f2(l4.z, l4.w)), y[2], y[3]);
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+          tmem_wait_ld();
+          tmem_ld_fence(x);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = ex2_approx(y[k]);
-          pr[c >> 1] = f2(y[0], y[1]), pr[(c >> 1) + 1] = f2(y[2], y[3]);
-          pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
-          if (decltype(masked)::value) {
-            uint32_t k0, k1;
-            keep(c, k0, k1);
-            pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(dp_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&y[cc * 32]));
+          tmem_wait_ld();
+          tmem_ld_fence(y);
+          tc_fence_before();
+          warp_arrive(&sm.s_free);
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][col0 + c]), d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
+            float z[4];
+            f2_split(fma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, f2(l4.x, l4.y)), z[0], z[1]);
+            f2_split(fma2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, f2(l4.z, l4.w)), z[2], z[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] = ex2_approx(z[k]);
+            ps[c >> 1] = c4_pack<F16>(z[0], z[1]), ps[(c >> 1) + 1] = c4_pack<F16>(z[2], z[3]);
+            f2_split(mul2(f2(z[0], z[1]), add2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), f2(d4.x, d4.y))), z[0], z[1]);
+            f2_split(mul2(f2(z[2], z[3]), add2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), f2(d4.z, d4.w))), z[2], z[3]);
+            ds[c >> 1] = c4_pack<F16>(z[0], z[1]), ds[(c >> 1) + 1] = c4_pack<F16>(z[2], z[3]);
+            if (decltype(masked)::value) {
+              uint32_t k0, k1;
+              keep(c, k0, k1);
+              ps[c >> 1] &= k0, ps[(c >> 1) + 1] &= k1, ds[c >> 1] &= k0, ds[(c >> 1) + 1] &= k1;
+            }
           }
-        }
-        tmem_st32(s_at, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&sm.p_full[t & 1]);  // (two: with three regions a warp may be a whole tile ahead of another)
-        if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int cc = 0; cc < 2; ++cc) tmem_ld32(dp_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
-        tmem_wait_ld();
-        tmem_ld_fence(x);
-        tc_fence_before();
-        if (kRegions == 2) warp_arrive(&sm.dp_free);
-#pragma unroll
-        for (int c = 0; c < 64; c += 4) {
-          const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
-          float y[4];
-          f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
-          f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
-          pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
-          if (decltype(masked)::value) {
-            uint32_t k0, k1;
-            keep(c, k0, k1);
-            pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+          warp_arrive(&sm.st_empty[ss]);
+          if (t > 0) {  // dV, dK of the tile before have read P and dS
+            if (!warp_wait(&sm.pd_free, (t - 1) & 1, abort_flag, p.status)) return false;
+            tc_fence_after();
           }
+          tmem_st32(lanes + 256 + wg * 32, ps);
+          tmem_st32(lanes + 320 + wg * 32, ds);
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.p_full);
+        } else {
+          uint32_t x[64], pk[32];
+          if (!warp_wait(&sm.s_full, t & 1, abort_flag, p.status)) return false;
+          if (!warp_wait(&sm.st_full[ss], (t / kStatStages) & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(s_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+          tmem_wait_ld();
+          tmem_ld_fence(x);
+          uint64_t pr[32];  // P, in pairs
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(&sm.nl[ss][col0 + c]);
+            float y[4];
+            f2_split(fma2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sl2, f2(l4.x, l4.y)), y[0], y[1]);
+            f2_split(fma2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), sl2, f2(l4.z, l4.w)), y[2], y[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = ex2_approx(y[k]);
+            pr[c >> 1] = f2(y[0], y[1]), pr[(c >> 1) + 1] = f2(y[2], y[3]);
+            pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
+            if (decltype(masked)::value) {
+              uint32_t k0, k1;
+              keep(c, k0, k1);
+              pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+            }
+          }
+          tmem_st32(s_at, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.p_full);
+          if (!warp_wait(&sm.dp_full, t & 1, abort_flag, p.status)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) tmem_ld32(dp_at + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[cc * 32]));
+          tmem_wait_ld();
+          tmem_ld_fence(x);
+          tc_fence_before();
+          warp_arrive(&sm.dp_free);
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
+            float y[4];
+            f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
+            f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
+            pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
+            if (decltype(masked)::value) {
+              uint32_t k0, k1;
+              keep(c, k0, k1);
+              pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
+            }
+          }
+          warp_arrive(&sm.st_empty[ss]);
+          tmem_st32(s_at + 32, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&sm.ds_full);
+          s_col ^= 128u;
         }
-        warp_arrive(&sm.st_empty[ss]);
-        tmem_st32(s_at + 32, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        warp_arrive(&sm.ds_full);
         ++t;
-        s_col = kRegions == 2 ? s_col ^ 128u : s_col >= 128u + col0 ? s_col - 128u : s_col + 256u;  // 0 2 1 0 2 1 ..
         return true;
       };
       // Tiles [plain, last) need no mask: whole ones whose first token sees the last key of a whole key tile and whose last
