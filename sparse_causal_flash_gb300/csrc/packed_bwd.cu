@@ -60,43 +60,57 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
 }
 
 // ------------------------------------------------------------------ row statistics
-// A warp takes 32 / (D / 8) rows at a time, a 16-byte piece of O and dO per lane. Bounded by HBM: both are read once.
+// A warp takes eight rows of a tile at a time, a 16-byte piece of O and dO per lane and row, all on their way at once.
+// Bounded by HBM: both are read once.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant__ PBwdParams p) {
-  constexpr int L = D / 8, RW = 32 / L;
+  constexpr int L = D / 8, RW = 32 / L, kRows = 8, kSteps = kRows / RW;
   const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
   const int status = bwd_plan_status(p);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = status, p.counter[0] = p.counter[1] = 0;  // for the kernels behind
   if (status != SCFA_OK) return;
   const int4* const tiles = reinterpret_cast<const int4*>(p.plan + h->qtiles);
   const int lane = threadIdx.x & 31, ch = lane % L;
-  const long long n = static_cast<long long>(h->n_qtiles) * p.Hkv * kTile;  // rows
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 32) * RW;
-  for (long long r0 = (static_cast<long long>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5)) * RW; r0 < n; r0 += step) {
-    const long long at = r0 + lane / L;  // (n is a multiple of 128)
-    const int row = static_cast<int>(at % kTile), head = static_cast<int>(at / kTile % p.Hkv);
-    const int4 t = __ldg(tiles + at / kTile / p.Hkv);
-    const int tok = row / p.G, qh = head * p.G + row - tok * p.G;
-    const bool live = tok < t.y;
-    float s = 0.f;
-    if (live) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p.o + static_cast<long long>(t.x + tok) * p.ot + qh * p.oh + ch * 8);
-      const uint4 b = *reinterpret_cast<const uint4*>(p.dO + static_cast<long long>(t.x + tok) * p.dot + qh * p.doh + ch * 8);
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+  // (32 bits hold it: each is 96 bytes of the workspace)
+  const uint32_t units = static_cast<uint32_t>(h->n_qtiles) * p.Hkv * (kTile / kRows), step = gridDim.x * (blockDim.x / 32);
+  const long long n = static_cast<long long>(units) * kRows;
+  for (uint32_t unit = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
+    const uint32_t pair = unit / (kTile / kRows), tile = pair / p.Hkv;
+    const int head = static_cast<int>(pair - tile * p.Hkv);
+    const int4 t = __ldg(tiles + tile);
+    uint4 a[kSteps], b[kSteps];
+    float lse[kSteps];
+    int hi[kSteps];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = c4_unpack<F16>(aw[i]), y = c4_unpack<F16>(bw[i]);
-        s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+    for (int i = 0; i < kSteps; ++i) {
+      const int row = static_cast<int>(unit % (kTile / kRows)) * kRows + i * RW + lane / L;
+      const int tok = row / p.G, qh = head * p.G + row - tok * p.G;
+      const bool live = tok < t.y;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0), lse[i] = -INFINITY, hi[i] = live ? t.z + tok : -1;
+      if (live) {
+        a[i] = *reinterpret_cast<const uint4*>(p.o + static_cast<long long>(t.x + tok) * p.ot + qh * p.oh + ch * 8);
+        b[i] = *reinterpret_cast<const uint4*>(p.dO + static_cast<long long>(t.x + tok) * p.dot + qh * p.doh + ch * 8);
+        lse[i] = p.lse[static_cast<long long>(t.x + tok) * p.Hq + qh];
       }
     }
 #pragma unroll
-    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (ch == 0) {
-      const float lse = live ? p.lse[static_cast<long long>(t.x + tok) * p.Hq + qh] : -INFINITY;
-      // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
-      p.stats[at] = lse == -INFINITY ? -INFINITY : -(lse * kPackLog2e);
-      p.stats[n + at] = live && lse != -INFINITY ? -s : 0.f;
-      reinterpret_cast<int*>(p.stats)[2 * n + at] = live ? t.z + tok : -1;
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = c4_unpack<F16>(aw[k]), y = c4_unpack<F16>(bw[k]);
+        s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+      }
+#pragma unroll
+      for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (ch == 0) {
+        const long long at = static_cast<long long>(unit) * kRows + i * RW + lane / L;
+        // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
+        p.stats[at] = lse[i] == -INFINITY ? -INFINITY : -(lse[i] * kPackLog2e);
+        p.stats[n + at] = lse[i] == -INFINITY ? 0.f : -s;
+        reinterpret_cast<int*>(p.stats)[2 * n + at] = hi[i];
+      }
     }
   }
   grid_release();
