@@ -12,14 +12,15 @@
 // One row is held by D / 16 threads, each with two 16-byte pieces such that both halves of its eight pairs are its own:
 // a norm is a few shuffles, and a row may be turned in place. What bounds it is HBM: each row is read once and written
 // once (gradients with a norm: two read, one written). A thread turns up to four heads of a token with one set of sines
-// (they cost 100 lane operations, a row's other work some 80), all loads before the first use.
+// (they cost 100 lane operations, a row's other work some 80), all loads before the first use: 31.5 us for 8192 tokens of
+// 32 and 8 heads of 128 channels with norms, 5.3 TB/s; 12.4 us for 275,280 rows of 64 without, 5.7 TB/s.
 #include "cache4.cuh"
 #include "internal.h"
 
 namespace scfa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeStages = 2;
 enum { kHalf = 0, kInterleaved = 1, kHalfOdd = 2 };  // kHalfOdd: halves that do not fall on 16-byte pieces
 
 struct RopeSide {
@@ -237,11 +238,25 @@ __global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 3) rope_kernel(con
   }
 }
 
+// 16 bytes to shared memory, asynchronously; wait until at most `left` of this thread's groups are on their way
+__device__ __forceinline__ void rope_fetch(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void rope_fetched() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 // Gradients with a norm. A CTA takes every side.blocks-th unit and keeps its sum of dw in registers, which it leaves in
-// `part`: rows are summed in an order that the sizes alone decide.
+// `part`: rows are summed in an order that the sizes alone decide. A thread's pieces of its next unit are on their way to
+// shared memory while it works on one; it reads back what it fetched itself, so it waits for its own copies alone.
+// Bounded by HBM and, near it, by latency: 43.8 us for 8192 tokens of 32 and 8 heads of 128 channels, 5.7 TB/s (61 with
+// loads into registers, all that fit; 45.8 with two units ahead, 54.4 with one head a thread and three CTAs per SM).
 template <int D, bool F16, int KIND, int HP>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int T = D / 16;
+  constexpr bool kStaged = KIND != kHalfOdd;
+  extern __shared__ uint4 s_raw[];  // [stage][head][x, dy][piece][thread]
   __shared__ float s_dw[kRopeThreads / 32][D];
   const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
   const RopeSide& sd = g.side[si];
@@ -256,20 +271,62 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
   for (int i = 0; i < 8; ++i) da[i] = db[i] = 0.f;
   const int tokens = rope_tokens(g);
   const uint32_t units = static_cast<uint32_t>(tokens) * sd.slices;  // (fewer than 2^31: N Hq is)
-  for (uint32_t first = static_cast<uint32_t>(block) * (kRopeThreads / T); first < units; first += static_cast<uint32_t>(sd.blocks) * (kRopeThreads / T)) {
+  const uint32_t step = static_cast<uint32_t>(sd.blocks) * (kRopeThreads / T);
+  auto where = [&](uint32_t first, int& tok, int& h0) {
     const uint32_t unit = first + threadIdx.x / T;
-    const int tok_ = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok_) * sd.slices) * HP;
+    tok = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok) * sd.slices) * HP;
+  };
+  auto slot = [&](int stage, int u, int which, int piece) { return s_raw + (((stage * HP + u) * 2 + which) * 2 + piece) * kRopeThreads + threadIdx.x; };
+  auto fetch = [&](uint32_t first, int stage) {
+    if (first < units) {
+      int tok, h0;
+      where(first, tok, h0);
+      tok = min(tok, g.N - 1);
+#pragma unroll
+      for (int u = 0; u < HP; ++u) {
+        const int h = min(h0 + u, sd.H - 1);
+        const uint16_t* const x = sd.x + tok * sd.xt + h * sd.xh;
+        const uint16_t* const dy = sd.dy + tok * sd.dyt + h * sd.dyh;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          rope_fetch(slot(stage, u, 0, j), x + m.piece(j) * 8), rope_fetch(slot(stage, u, 1, j), dy + m.piece(j) * 8);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetched = [&](int stage, int u, int which) {
+    const uint4 x = *slot(stage, u, which, 0), y = *slot(stage, u, which, 1);
+    return RopeRaw{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
+  };
+  uint32_t first = static_cast<uint32_t>(block) * (kRopeThreads / T);
+  if (kStaged) {
+#pragma unroll
+    for (int i = 0; i < kRopeStages - 1; ++i) fetch(first + i * step, i);
+  }
+  int stage = 0;
+  for (; first < units; first += step) {
+    int tok_, h0;
+    where(first, tok_, h0);
     const bool live = tok_ < tokens;
     const int tok = min(tok_, g.N - 1);
+    const int pos = __ldg(g.pos + tok);
     RopeRaw rx[HP], rd[HP];
+    if (kStaged) {
+      rope_fetched<kRopeStages - 2>();
 #pragma unroll
-    for (int u = 0; u < HP; ++u) {
-      const int h = min(h0 + u, sd.H - 1);
-      rx[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + h * sd.xh, m);
-      rd[u] = rope_load<D, F16, KIND>(sd.dy + tok * sd.dyt + h * sd.dyh, m);
+      for (int u = 0; u < HP; ++u) rx[u] = fetched(stage, u, 0), rd[u] = fetched(stage, u, 1);
+      fetch(first + (kRopeStages - 1) * step, stage == 0 ? kRopeStages - 1 : stage - 1);
+      stage = stage == kRopeStages - 1 ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int u = 0; u < HP; ++u) {
+        const int h = min(h0 + u, sd.H - 1);
+        rx[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + h * sd.xh, m);
+        rd[u] = rope_load<D, F16, KIND>(sd.dy + tok * sd.dyt + h * sd.dyh, m);
+      }
     }
     float c[8], s[8];
-    rope_angles(g, m, __ldg(g.pos + tok), c, s);
+    rope_angles(g, m, pos, c, s);
 #pragma unroll
     for (int u = 0; u < HP; ++u) {
       float xa[8], xb[8], ga[8], gb[8], wa[8], wb[8];
@@ -346,14 +403,15 @@ __global__ void __launch_bounds__(256) rope_dw_kernel(const __grid_constant__ Ro
   }
 }
 
-// CTAs of the gradient with a norm, by what fills the GPU: 4 per SM, no more than there is work for.
+// CTAs of the gradient with a norm: as many as run at once, two per SM, no more than there is work for (four: 49.8 us
+// instead of 43.8 for the call above).
 constexpr int kBwdHeads = 2;
 int rope_bwd_ctas(int N, int H, int D, int most) {
   if (H == 0) return 0;
   const long long n = (static_cast<long long>(N) * ((H + kBwdHeads - 1) / kBwdHeads) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   return static_cast<int>(n < most ? n : most);
 }
-int rope_most_ctas() { return 8 * num_sms(); }
+int rope_most_ctas() { return 2 * num_sms(); }
 
 template <int D, bool F16, int KIND>
 cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
@@ -362,10 +420,19 @@ cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
     const int most = rope_most_ctas(), H = g.side[0].H + g.side[1].H;
     for (RopeSide& s : g.side) {
       s.slices = (s.H + kBwdHeads - 1) / kBwdHeads;
-      s.blocks = rope_bwd_ctas(g.N, s.H, D, s.H ? (most * s.H + H - 1) / H : 0);
+      s.blocks = rope_bwd_ctas(g.N, s.H, D, max(1, most * s.H / H));  // (rounded down: no CTA may wait for another's end)
     }
-    rope_bwd_kernel<D, F16, KIND, kBwdHeads><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, 0, st>>>(g);
-    cudaError_t e = cudaGetLastError();
+    constexpr int smem = KIND == kHalfOdd ? 0 : kRopeStages * kBwdHeads * 4 * kRopeThreads * 16;
+    static bool allowed[64] = {};
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !allowed[dev])) {
+      e = cudaFuncSetAttribute(rope_bwd_kernel<D, F16, KIND, kBwdHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+    }
+    if (e != cudaSuccess) return e;
+    rope_bwd_kernel<D, F16, KIND, kBwdHeads><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, smem, st>>>(g);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_behind(rope_dw_kernel<D>, dim3(D / 8, g.side[1].H ? 2 : 1), 256, st, g);
   }
