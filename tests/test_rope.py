@@ -139,6 +139,13 @@ def test_bwd_refusals(scfa, kw, code):
     assert scfa._lib.scfa_rope_bwd(*bwd_args(**kw)) == code
 
 
+@pytest.mark.parametrize("kw", [dict(table=ctypes.c_void_p(4104)), dict(wq=ctypes.c_void_p(4100), wk=FAKE),
+                                dict(wq=FAKE, wk=ctypes.c_void_p(4108))])
+def test_tables_and_weights_start_on_16_bytes(scfa, kw):
+    assert scfa._lib.scfa_rope_fwd(*fwd_args(**kw)) == 1
+    assert scfa._lib.scfa_rope_bwd(*bwd_args(**kw)) == 1
+
+
 def test_no_tokens_is_no_error(scfa):
     assert scfa._lib.scfa_rope_fwd(*fwd_args(N=0, q=None, k=None, qo=None, ko=None)) == 0
     assert scfa._lib.scfa_rope_bwd(*bwd_args(N=0, dq=None, dk=None, qo=None, ko=None, wq=None, wk=None, dwq=None, dwk=None,

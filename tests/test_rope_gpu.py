@@ -136,6 +136,24 @@ def test_rows_and_gradients(scfa, N, Hq, Hkv, D, rot, il, norm, factor, dt):
         assert all(a is None or torch.equal(a, b) for a, b in zip(first[1], dw))
 
 
+@pytest.mark.parametrize("rot,il", [(128, False), (128, True), (40, False)])
+def test_gradients_of_more_rows_than_run_at_once(scfa, rot, il):
+    """A CTA takes several units of two heads; the last head stands alone; the tokens end inside a unit's row."""
+    N, n, Hq, Hkv, D = 20011, 19990, 5, 1, 128
+    x, dy = rand(1, (N, Hq, D), BF, 0.7), rand(2, (N, Hq, D), BF)
+    k, dk = rand(3, (N, Hkv, D), BF, 0.7), rand(4, (N, Hkv, D), BF)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 3 - 5000
+    w = [1 + 0.3 * rand(5 + i, (D,), torch.float32) for i in range(2)]
+    f, p = freqs(rot), pos[:n].cpu().numpy().astype(np.float64)
+    gq, gk, dw = torch.full_like(dy, 9.0), torch.full_like(dk, 9.0), torch.empty(2, D, device="cuda")
+    scfa.scfa_rope_bwd(dy, dk, pos, scfa.rope_table(f), gq, gk, il, q=x, k=k, wq=w[0], wk=w[1], eps=EPS, dwq=dw[0], dwk=dw[1],
+                       ws=scfa.workspace(scfa.rope_workspace_size(N, Hq, Hkv, D)),
+                       count=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    check_bwd(gq[:n], dw[0], dbl(dy[:n]), dbl(x[:n]), p, f, il, 1.0, dbl(w[0]), BF)
+    check_bwd(gk[:n], dw[1], dbl(dk[:n]), dbl(k[:n]), p, f, il, 1.0, dbl(w[1]), BF)
+    assert bool((gq[n:] == 9).all()) and bool((gk[n:] == 9).all())
+
+
 @pytest.mark.parametrize("norm", [False, True])
 @pytest.mark.parametrize("rot", [64, 38])
 def test_in_place_and_other_strides(scfa, rot, norm):
