@@ -500,6 +500,8 @@ def scfa_rope_fwd(q, k, pos, table, q_out, k_out, interleaved=False, factor=1.0,
     qt, qh = _rows4("scfa_rope_fwd", "q", q, N, Hq, D, dt, dev)
     ot, oh = _rows4("scfa_rope_fwd", "q_out", q_out, N, Hq, D, dt, dev)
     kp = kt = kh = lp = lt = lh = 0
+    if (k is None) != (k_out is None):
+        raise ValueError("scfa_rope_fwd: k and k_out come together")
     if k is not None:
         kt, kh = _rows4("scfa_rope_fwd", "k", k, N, Hkv, D, dt, dev)
         lt, lh = _rows4("scfa_rope_fwd", "k_out", k_out, N, Hkv, D, dt, dev)
@@ -519,31 +521,31 @@ def scfa_rope_bwd(dq, dk, pos, table, dq_out, dk_out, interleaved=False, factor=
     dev, dt = dq.get_device(), dq.dtype
     Hkv = 0 if dk is None else dk.shape[1]
     rot = _rope_args("scfa_rope_bwd", dev, pos, table, N, D, wq, wk, dk, count)
-    rows = [dq, dk, None, None, dq_out, dk_out]
-    ptrs = [0] * 4
-    nbytes = 0
+    at, ah = _rows4("scfa_rope_bwd", "dq", dq, N, Hq, D, dt, dev)
+    ot, oh = _rows4("scfa_rope_bwd", "dq_out", dq_out, N, Hq, D, dt, dev)
+    bp = bt = bh = lp = lt = lh = 0
+    if (dk is None) != (dk_out is None):
+        raise ValueError("scfa_rope_bwd: dk and dk_out come together")
+    if dk is not None:
+        bt, bh = _rows4("scfa_rope_bwd", "dk", dk, N, Hkv, D, dt, dev)
+        lt, lh = _rows4("scfa_rope_bwd", "dk_out", dk_out, N, Hkv, D, dt, dev)
+        bp, lp = dk.data_ptr(), dk_out.data_ptr()
+    qp = qt = qh = kp = kt = kh = wp = xp = ep = fp = sp = nbytes = 0
     if wq is not None:
         if q is None or dwq is None or ws is None or (dk is not None and (k is None or dwk is None)):
             raise ValueError("scfa_rope_bwd: a norm's gradient needs the rows, weights, weight gradients and a workspace")
-        for key, w in (("dwq", dwq), ("dwk", dwk)):
-            if w is not None and not _is(w, torch.float32, dev, D):
-                _refuse("scfa_rope_bwd", dev, **{key: (w, torch.float32, D)})
-        rows[2:4] = [q, k if dk is not None else None]
-        nbytes = _ws_bytes("scfa_rope_bwd", ws, dev)
-        ptrs = [wq.data_ptr(), wk.data_ptr() if dk is not None else None, dwq.data_ptr(),
-                dwk.data_ptr() if dk is not None else None]
-    args = []
-    for i, (key, t) in enumerate(zip(("dq", "dk", "q", "k", "dq_out", "dk_out"), rows)):
-        if t is None:
-            if i == 5 and dk is not None:
-                raise ValueError("scfa_rope_bwd: dk needs dk_out")
-            args.append((0, 0, 0))
-        else:
-            args.append((t.data_ptr(), *_rows4("scfa_rope_bwd", key, t, N, (Hq, Hkv)[i & 1], D, dt, dev)))
-    _launch("scfa_rope_bwd", dev, stream, *args[0], *args[1], *args[2], *args[3], pos.data_ptr(),
-            None if count is None else count.data_ptr(), table.data_ptr(), N, Hq,
-            Hkv, D, rot, int(interleaved), factor, ptrs[0], ptrs[1], eps, _DTYPES.get(dt, -1), *args[4], *args[5], ptrs[2],
-            ptrs[3], None if ws is None else ws.data_ptr(), nbytes)
+        if not _is(dwq, torch.float32, dev, D):
+            _refuse("scfa_rope_bwd", dev, dwq=(dwq, torch.float32, D))
+        qt, qh = _rows4("scfa_rope_bwd", "q", q, N, Hq, D, dt, dev)
+        qp, wp, ep, sp, nbytes = q.data_ptr(), wq.data_ptr(), dwq.data_ptr(), ws.data_ptr(), _ws_bytes("scfa_rope_bwd", ws, dev)
+        if dk is not None:
+            if not _is(dwk, torch.float32, dev, D):
+                _refuse("scfa_rope_bwd", dev, dwk=(dwk, torch.float32, D))
+            kt, kh = _rows4("scfa_rope_bwd", "k", k, N, Hkv, D, dt, dev)
+            kp, xp, fp = k.data_ptr(), wk.data_ptr(), dwk.data_ptr()
+    _launch("scfa_rope_bwd", dev, stream, dq.data_ptr(), at, ah, bp, bt, bh, qp, qt, qh, kp, kt, kh, pos.data_ptr(),
+            None if count is None else count.data_ptr(), table.data_ptr(), N, Hq, Hkv, D, rot, int(interleaved), factor, wp, xp,
+            eps, _DTYPES.get(dt, -1), dq_out.data_ptr(), ot, oh, lp, lt, lh, ep, fp, sp, nbytes)
 
 
 # ---------------------------------------------------------------- packed sequences, shared key heads

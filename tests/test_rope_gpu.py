@@ -231,6 +231,15 @@ def test_values_that_are_not_finite_stay_in_their_rows(scfa):
     assert not y.any()
 
 
+def test_keys_and_their_output_come_together(scfa):
+    x, pos, table = rand(1, (3, 2, 64), BF), torch.zeros(3, dtype=torch.int32, device="cuda"), scfa.rope_table(freqs(64))
+    for f in (scfa.scfa_rope_fwd, scfa.scfa_rope_bwd):
+        with pytest.raises(ValueError, match="together"):
+            f(x, x, pos, table, torch.empty_like(x), None)
+        with pytest.raises(ValueError, match="together"):
+            f(x, None, pos, table, torch.empty_like(x), torch.empty_like(x))
+
+
 def test_no_tokens(scfa):
     e = torch.empty((0, 4, 64), dtype=BF, device="cuda")
     p = torch.empty(0, dtype=torch.int32, device="cuda")
