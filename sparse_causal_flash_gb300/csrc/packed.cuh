@@ -97,7 +97,7 @@ struct PackWs {
   size_t counters = 0;          // ints: next item of each kernel
   size_t part = 0, part_q = 0;  // fp32, [slot][Hkv]: two tiles of D + 2 columns, or dV and dK; (backward) dQ
   size_t forward = 0;           // what a forward needs
-  size_t stats = 0;             // backward: [3][query tiles][Hkv][128]
+  size_t stats = 0;             // backward: [2][query tiles][Hkv][128]
   size_t clear = 0;             // bytes from the start that a call clears
 };
 // A backward's workspace serves a forward too.
@@ -111,7 +111,7 @@ inline PackWs pack_ws(int D, int sms) {
   w.stats = align_up(w.part_q + slots * row * D, 256);
   return w;
 }
-inline long long pack_stats_tile_bytes(int Hkv) { return 3ll * Hkv * kTile * sizeof(float); }
+inline long long pack_stats_tile_bytes(int Hkv) { return 2ll * Hkv * kTile * sizeof(float); }
 
 // The join of what the chunks left, behind the kernel that left it: o and lse (forward), or dV, dK and dQ.
 struct PackJoin {
@@ -302,6 +302,15 @@ __device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[W 
     for (int u = 0; u < 2; ++u)
       *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
           make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
+}
+// Bits from .. to - 1 of 32, either end anywhere.
+__device__ __forceinline__ uint32_t bit_range(int from, int to) {
+  from = max(from, 0), to = min(to, 32);
+  return from < to ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+}
+// Bits c and c + 1 as a mask of two 16-bit values.
+__device__ __forceinline__ uint32_t bit_pair(uint32_t bits, int c) {
+  return (bits >> c & 1u ? 0x0000ffffu : 0u) | (bits >> (c + 1) & 1u ? 0xffff0000u : 0u);
 }
 __device__ __forceinline__ float pack_max3(float a, float b, float c) {
   float d;

@@ -3,8 +3,7 @@
 // With P = 2^(s scale log2(e) - lse log2(e)) recomputed from q, k and the forward's lse, delta = rowsum(dO * O),
 // dP = dO V^T and dS = P (dP - delta):  dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 //
-// Three kernels. `packed_stats_kernel` writes -lse log2(e), -delta and the last visible key of every query row, in rows
-// of query tiles. `packed_dq_kernel` holds a query tile and walks its key tiles (S, dP, dQ: three products a tile);
+// Three kernels. `packed_stats_kernel` writes -lse log2(e) and -delta of every query row, in rows of query tiles. `packed_dq_kernel` holds a query tile and walks its key tiles (S, dP, dQ: three products a tile);
 // `packed_dkv_kernel` holds a key tile and walks the query tiles of all its heads (S^T, dP^T, dV, dK: four). Seven
 // products a tile pair where one kernel for all would do five, and no sums in memory: such a kernel has to add its dQ
 // tiles into fp32 rows across CTAs (64 KB per tile pair through L2, in an order that changes from run to run, with a
@@ -44,7 +43,7 @@ struct PBwdParams {
   const float* lse;
   uint16_t *dq, *dk, *dv;
   long long dqt, dqh, dkt, dkh, dvt, dvh;
-  float* stats;             // [3][tiles][Hkv][128]
+  float* stats;             // [2][tiles][Hkv][128]
   long long stats_bytes;    // room for them
   int* counter;
   float *part, *part_q;     // chunks' shares of dV and dK, and of dQ
@@ -56,7 +55,7 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
   const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
   const int s = pack_plan_status(h, p.plan_bytes, p.N, p.M, p.Hq, p.Hkv);
   if (s != SCFA_OK) return s;
-  return 3ll * h->n_qtiles * p.Hkv * kTile * static_cast<long long>(sizeof(float)) > p.stats_bytes ? SCFA_ERR_WORKSPACE : SCFA_OK;
+  return 2ll * h->n_qtiles * p.Hkv * kTile * static_cast<long long>(sizeof(float)) > p.stats_bytes ? SCFA_ERR_WORKSPACE : SCFA_OK;
 }
 
 // ------------------------------------------------------------------ row statistics
@@ -71,7 +70,7 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
   if (status != SCFA_OK) return;
   const int4* const tiles = reinterpret_cast<const int4*>(p.plan + h->qtiles);
   const int lane = threadIdx.x & 31, ch = lane % L;
-  // (32 bits hold it: each is 96 bytes of the workspace)
+  // (32 bits hold it: each is 64 bytes of the workspace)
   const uint32_t units = static_cast<uint32_t>(h->n_qtiles) * p.Hkv * (kTile / kRows), step = gridDim.x * (blockDim.x / 32);
   const long long n = static_cast<long long>(units) * kRows;
   for (uint32_t unit = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); unit < units; unit += step) {
@@ -80,13 +79,12 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
     const int4 t = __ldg(tiles + tile);
     uint4 a[kSteps], b[kSteps];
     float lse[kSteps];
-    int hi[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int row = static_cast<int>(unit % (kTile / kRows)) * kRows + i * RW + lane / L;
       const int tok = row / p.G, qh = head * p.G + row - tok * p.G;
       const bool live = tok < t.y;
-      a[i] = b[i] = make_uint4(0, 0, 0, 0), lse[i] = -INFINITY, hi[i] = live ? t.z + tok : -1;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0), lse[i] = -INFINITY;
       if (live) {
         a[i] = *reinterpret_cast<const uint4*>(p.o + static_cast<long long>(t.x + tok) * p.ot + qh * p.oh + ch * 8);
         b[i] = *reinterpret_cast<const uint4*>(p.dO + static_cast<long long>(t.x + tok) * p.dot + qh * p.doh + ch * 8);
@@ -109,7 +107,6 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
         // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
         p.stats[at] = lse[i] == -INFINITY ? -INFINITY : -(lse[i] * kPackLog2e);
         p.stats[n + at] = lse[i] == -INFINITY ? 0.f : -s;
-        reinterpret_cast<int*>(p.stats)[2 * n + at] = hi[i];
       }
     }
   }
@@ -344,7 +341,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int hi = valid ? first + r_tok : -1;
       const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
       const float nl = p.stats[at], nd = p.stats[n_stats + at];
-      auto tile = [&](auto masked, int j) -> bool {
+      auto tile = [&](auto may_mask, bool masked, int j) -> bool {
         uint32_t sr[64], dr[64];
         if (!warp_wait(&sm.dp_full, n & 1, abort_flag, p.status)) return false;
         tc_fence_after();
@@ -389,13 +386,11 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           warp_arrive(&sm.s_free);
           weigh(0, 64);
         }
-        if (decltype(masked)::value) {
-          // lo <= column <= lim as one unsigned comparison
-          const int lim = hi - j * kTile - col0, lo = window ? max(lim - window + 1, -kTile) : -kTile;
-          const uint32_t span = lim < lo ? 0u : static_cast<uint32_t>(lim - lo) + 1u;
+        if (decltype(may_mask)::value && masked) {  // columns lo .. lim are seen
+          const int lim = hi - j * kTile - col0, lo = window ? lim - window + 1 : 0;
+          const uint32_t bits[2] = {bit_range(lo, lim + 1), bit_range(lo - 32, lim + 1 - 32)};
 #pragma unroll
-          for (int c = 0; c < 64; c += 2)
-            pk[c >> 1] &= (static_cast<uint32_t>(c - lo) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(c + 1 - lo) < span ? 0xffff0000u : 0u);
+          for (int c = 0; c < 64; c += 2) pk[c >> 1] &= bit_pair(bits[c >> 5], c & 31);
         }
         if (n > 1) {  // dQ two tiles back has read this buffer
           if (!warp_wait(&sm.ds_free[n & 1], ((n >> 1) - 1) & 1, abort_flag, p.status)) return false;
@@ -412,12 +407,16 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int plain = window ? min(b, max(a, (first + n_tok - window + kTile - 1) / kTile)) : a;
       const int masked = max(plain, min(b, max(0, first + 1) / kTile));
       bool ok = true;
-      int j = a;
-      for (int part = 0; part < 2 && ok; ++part) {
-        const int stop = part ? b : plain;
-        for (; j < stop && ok; ++j) ok = tile(std::true_type{}, j);
-        if (part == 0)
-          for (; j < masked && ok; ++j) ok = tile(std::false_type{}, j);
+      if (D == 64) {  // (one copy of the code or two: as in the forward)
+        for (int j = a; j < b && ok; ++j) ok = tile(std::true_type{}, j < plain || j >= masked, j);
+      } else {
+        int j = a;
+        for (int part = 0; part < 2 && ok; ++part) {
+          const int stop = part ? b : plain;
+          for (; j < stop && ok; ++j) ok = tile(std::true_type{}, true, j);
+          if (part == 0)
+            for (; j < masked && ok; ++j) ok = tile(std::false_type{}, false, j);
+        }
       }
       if (!ok) break;
       // this warp's 16 rows of dQ
@@ -710,8 +709,6 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     regs_take<kRegsMany>();
     const int wg = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane, col0 = wg * 64;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t span = window ? static_cast<uint32_t>(window) : 0x80000000u;
-    const int* const all_hi = reinterpret_cast<const int*>(p.stats) + 2 * n_stats;
     int t = 0, n_acc = 0;
     uint32_t s_col = col0;  // this warpgroup's columns of S (two regions in turn at D = 128)
     for (int it = 0;; ++it) {
@@ -721,14 +718,18 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const int head = e.head;
       if (head < 0) break;
       const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
-      auto tile = [&](auto masked, int i) -> bool {
+      auto tile = [&](auto may_mask, bool masked, int i) -> bool {
         const int ss = t % kStatStages;
         const uint32_t s_at = lanes + s_col, dp_at = lanes + (s_col ^ 128u);
-        // which of the queries c .. c + 3 see this thread's key, as masks of two 16-bit pairs
-        auto keep = [&](int c, uint32_t& k0, uint32_t& k1) {
-          const int4 h4 = __ldg(reinterpret_cast<const int4*>(all_hi + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile + col0 + c));
-          k0 = (static_cast<uint32_t>(h4.x - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.y - key) < span ? 0xffff0000u : 0u);
-          k1 = (static_cast<uint32_t>(h4.z - key) < span ? 0x0000ffffu : 0u) | (static_cast<uint32_t>(h4.w - key) < span ? 0xffff0000u : 0u);
+        // P and dS of the queries that see this thread's key: those of tokens from .. to - 1 of the tile
+        auto keep = [&](uint32_t (&w)[32]) {
+          const long long ahead = static_cast<long long>(key) - e.shift - static_cast<long long>(i) * p.tpt;
+          const long long n_left = min(p.tpt, e.m - i * p.tpt);
+          const int from = static_cast<int>(max(0ll, min(n_left, ahead))) * p.G - col0;
+          const int to = static_cast<int>(window ? max(0ll, min(n_left, ahead + window)) : n_left) * p.G - col0;
+          const uint32_t bits[2] = {bit_range(from, to), bit_range(from - 32, to - 32)};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) w[c >> 1] &= bit_pair(bits[c >> 5], c & 31);
         };
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
         if constexpr (kOwn) {
@@ -758,13 +759,9 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             f2_split(mul2(f2(z[0], z[1]), add2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), f2(d4.x, d4.y))), z[0], z[1]);
             f2_split(mul2(f2(z[2], z[3]), add2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), f2(d4.z, d4.w))), z[2], z[3]);
             ds[c >> 1] = c4_pack<F16>(z[0], z[1]), ds[(c >> 1) + 1] = c4_pack<F16>(z[2], z[3]);
-            if (decltype(masked)::value) {
-              uint32_t k0, k1;
-              keep(c, k0, k1);
-              ps[c >> 1] &= k0, ps[(c >> 1) + 1] &= k1, ds[c >> 1] &= k0, ds[(c >> 1) + 1] &= k1;
-            }
           }
           warp_arrive(&sm.st_empty[ss]);
+          if (decltype(may_mask)::value && masked) keep(ps), keep(ds);
           if (t > 0) {  // dV, dK of the tile before have read P and dS
             if (!warp_wait(&sm.pd_free, (t - 1) & 1, abort_flag, p.status)) return false;
             tc_fence_after();
@@ -794,12 +791,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             for (int k = 0; k < 4; ++k) y[k] = ex2_approx(y[k]);
             pr[c >> 1] = f2(y[0], y[1]), pr[(c >> 1) + 1] = f2(y[2], y[3]);
             pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
-            if (decltype(masked)::value) {
-              uint32_t k0, k1;
-              keep(c, k0, k1);
-              pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
-            }
           }
+          if (decltype(may_mask)::value && masked) keep(pk);
           tmem_st32(s_at, pk);
           tmem_wait_st();
           tc_fence_before();
@@ -819,13 +812,9 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
             f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
             pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
-            if (decltype(masked)::value) {
-              uint32_t k0, k1;
-              keep(c, k0, k1);
-              pk[c >> 1] &= k0, pk[(c >> 1) + 1] &= k1;
-            }
           }
           warp_arrive(&sm.st_empty[ss]);
+          if (decltype(may_mask)::value && masked) keep(pk);
           tmem_st32(s_at + 32, pk);
           tmem_wait_st();
           tc_fence_before();
@@ -849,12 +838,16 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         last = max(last, plain);
       }
       bool ok = true;
-      int i = a;
-      for (int part = 0; part < 2 && ok; ++part) {
-        const int stop = part ? b : plain;
-        for (; i < stop && ok; ++i) ok = tile(std::true_type{}, i);
-        if (part == 0)
-          for (; i < last && ok; ++i) ok = tile(std::false_type{}, i);
+      if (D == 64) {
+        for (int i = a; i < b && ok; ++i) ok = tile(std::true_type{}, i < plain || i >= last, i);
+      } else {
+        int i = a;
+        for (int part = 0; part < 2 && ok; ++part) {
+          const int stop = part ? b : plain;
+          for (; i < stop && ok; ++i) ok = tile(std::true_type{}, true, i);
+          if (part == 0)
+            for (; i < last && ok; ++i) ok = tile(std::false_type{}, false, i);
+        }
       }
       if (!ok) break;
       if (a < b) {

@@ -363,8 +363,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const int lim = hi - j * kTile, lo = window ? lim - window + 1 : 0;
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
-            const uint32_t upto = lim < cc * 32 ? 0u : 0xffffffffu >> (31 - min(lim - cc * 32, 31));
-            const uint32_t bits = lo <= cc * 32 ? upto : lo - cc * 32 > 31 ? 0u : upto & (0xffffffffu << (lo - cc * 32));
+            const uint32_t bits = bit_range(lo - cc * 32, lim + 1 - cc * 32);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!(bits >> c & 1u)) sr[cc * 32 + c] = 0xff800000u;
