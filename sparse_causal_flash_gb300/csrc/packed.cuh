@@ -204,32 +204,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// 16 lanes x 64 columns: r[4 i + 2 u + v] is lane (lane / 4 + 8 u), column 8 i + 2 (lane % 4) + v
-__device__ __forceinline__ void tmem_ld_quad(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st_quad(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      :: "r"(taddr),
-         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-         "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-// the same of 32 columns
-__device__ __forceinline__ void tmem_ld_quad16(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 lanes x 32 columns: r[4 i + 2 u + v] is lane (lane / 4 + 8 u), column 8 i + 2 (lane % 4) + v
+__device__ __forceinline__ void tmem_ld_quad(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -237,71 +213,59 @@ __device__ __forceinline__ void tmem_ld_quad16(uint32_t taddr, uint32_t (&r)[16]
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st_quad16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      :: "r"(taddr),
-         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// 16 lanes x 32 columns: r[2 i + u] is lane (lane / 4 + 8 u), column 4 i + lane % 4
-__device__ __forceinline__ void tmem_st_quad_half(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      :: "r"(taddr),
-         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// Rows 16 hf .. 16 hf + 15 of the warp's 32 (its lanes start at taddr), W columns, as tmem_ld_quad16 gives them; zeros
-// without `some`.
-template <int W>
-__device__ __forceinline__ void quad_part(uint32_t (&acc)[W / 32][16], uint32_t taddr, int hf, bool some) {
-  if (some) {
+// use(c, words) for 16 lanes of an accumulator of W columns, 32 columns (from c) at a time, the next ones on their way;
+// zeros without `some`. A loop, and a short one: code that runs once an item is fetched anew each time (unrolled, the
+// forward of 8192 tokens, 32 heads over 8 of 128 channels took 346 us instead of 338).
+template <int W, typename Use>
+__device__ __forceinline__ void quad_blocks(uint32_t taddr, bool some, Use use) {
+  uint32_t next[16];
 #pragma unroll
-    for (int cc = 0; cc < W / 32; ++cc) tmem_ld_quad16(taddr + (static_cast<uint32_t>(hf * 16) << 16) + cc * 32, acc[cc]);
-    tmem_wait_ld();
+  for (int i = 0; i < 16; ++i) next[i] = 0u;
+  if (some) tmem_ld_quad(taddr, next);
+#pragma unroll 1
+  for (int c = 0; c < W; c += 32) {
+    uint32_t acc[16];
+    if (some) {
+      tmem_wait_ld();
+      tmem_ld_fence(next);
+    }
 #pragma unroll
-    for (int cc = 0; cc < W / 32; ++cc) tmem_ld_fence(acc[cc]);
-  } else {
-#pragma unroll
-    for (int cc = 0; cc < W / 32; ++cc)
-#pragma unroll
-      for (int c = 0; c < 16; ++c) acc[cc][c] = 0u;
+    for (int i = 0; i < 16; ++i) acc[i] = next[i];
+    if (some && c + 32 < W) tmem_ld_quad(taddr + c + 32, next);
+    use(c, acc);
   }
 }
-// One of the two rows that a quad of lanes holds (u), times f, in the rows' type to `row`. Four words change places
-// inside the quad so that each lane has 16 bytes and the quad 64 in a row: a quarter of the stores' lines that whole rows
-// per thread would touch (those took 6,500 cycles for a tile of 128 x 128).
-template <int W, bool F16>
-__device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint32_t (&acc)[W / 32][16], int u, float f) {
+// One of the two rows that a quad of lanes holds (u), times f, in the rows' type to `row`: 32 channels. Four words change
+// places inside the quad so that each lane has 16 bytes and the quad 64 in a row: a quarter of the stores' lines that whole
+// rows per thread would touch (those took 6,500 cycles for a tile of 128 x 128).
+template <bool F16>
+__device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint32_t (&acc)[16], int u, float f) {
   const int t = threadIdx.x & 3;
+  uint32_t w[4];
 #pragma unroll
-  for (int b = 0; b < W / 32; ++b) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = c4_pack<F16>(__uint_as_float(acc[b][i * 4 + 2 * u]) * f, __uint_as_float(acc[b][i * 4 + 2 * u + 1]) * f);
-    const uint32_t x0 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[0] : w[1], 1), x1 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[2] : w[3], 1);
-    const uint32_t p0 = t & 1 ? x0 : w[0], p1 = t & 1 ? w[1] : x0, p2 = t & 1 ? x1 : w[2], p3 = t & 1 ? w[3] : x1;
-    const uint32_t y0 = __shfl_xor_sync(0xffffffffu, t & 2 ? p0 : p2, 2), y1 = __shfl_xor_sync(0xffffffffu, t & 2 ? p1 : p3, 2);
-    const uint4 v = t & 2 ? make_uint4(y0, y1, p2, p3) : make_uint4(p0, p1, y0, y1);
-    if (live) *reinterpret_cast<uint4*>(row + 32 * b + 8 * t) = v;
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = c4_pack<F16>(__uint_as_float(acc[i * 4 + 2 * u]) * f, __uint_as_float(acc[i * 4 + 2 * u + 1]) * f);
+  const uint32_t x0 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[0] : w[1], 1), x1 = __shfl_xor_sync(0xffffffffu, t & 1 ? w[2] : w[3], 1);
+  const uint32_t p0 = t & 1 ? x0 : w[0], p1 = t & 1 ? w[1] : x0, p2 = t & 1 ? x1 : w[2], p3 = t & 1 ? w[3] : x1;
+  const uint32_t y0 = __shfl_xor_sync(0xffffffffu, t & 2 ? p0 : p2, 2), y1 = __shfl_xor_sync(0xffffffffu, t & 2 ? p1 : p3, 2);
+  const uint4 v = t & 2 ? make_uint4(y0, y1, p2, p3) : make_uint4(p0, p1, y0, y1);
+  if (live) *reinterpret_cast<uint4*>(row + 8 * t) = v;
 }
-// Leave W columns of an accumulator (rows of D) as a chunk's share: 16 rows of a warp's 32, as quad_part gives them.
-template <int W, int D>
-__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[W / 32][16], int row) {
+// Leave 32 columns of an accumulator (rows of D) as a chunk's share.
+template <int D>
+__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[16], int row) {
   const int c0 = 2 * (threadIdx.x & 3);
 #pragma unroll
-  for (int i = 0; i < W / 8; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
-          make_float2(__uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u]), __uint_as_float(acc[i >> 2][(i & 3) * 4 + 2 * u + 1]));
+          make_float2(__uint_as_float(acc[i * 4 + 2 * u]), __uint_as_float(acc[i * 4 + 2 * u + 1]));
+}
+__device__ __forceinline__ float pack_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // Bits from .. to - 1 of 32, either end anywhere.
 __device__ __forceinline__ uint32_t bit_range(int from, int to) {
@@ -311,11 +275,6 @@ __device__ __forceinline__ uint32_t bit_range(int from, int to) {
 // Bits c and c + 1 as a mask of two 16-bit values.
 __device__ __forceinline__ uint32_t bit_pair(uint32_t bits, int c) {
   return (bits >> c & 1u ? 0x0000ffffu : 0u) | (bits >> (c + 1) & 1u ? 0xffff0000u : 0u);
-}
-__device__ __forceinline__ float pack_max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // launch_behind() with shared memory; `behind` false: an ordinary launch.

@@ -420,27 +420,33 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (!ok) break;
       // this warp's 16 rows of dQ
-      const int hf = wg, row = quarter * 32 + hf * 16 + (lane >> 2);
-      uint32_t acc[D / 32][16];
+      const int row = quarter * 32 + wg * 16 + (lane >> 2);
+      const uint32_t from = lanes + 256 + (static_cast<uint32_t>(wg * 16) << 16);
       if (a < b) {
         if (!warp_wait(&sm.dq_full, n_q & 1, abort_flag, p.status)) break;
         tc_fence_after();
         ++n_q;
       }
-      quad_part<D>(acc, lanes + 256, hf, a < b);
+      if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
+        float* const mine = p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D;
+        quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D>(mine + c, acc, row); });
+      } else {
+        uint16_t* to[2];
+        bool live[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tk = (row + 8 * u) / p.G;
+          live[u] = tk < n_tok;
+          to[u] = p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + (head * p.G + row + 8 * u - tk * p.G) * p.dqh;
+        }
+        quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) quad_store<F16>(to[u] + c, live[u], acc, u, p.scale);
+        });
+      }
       if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.dq_empty);
-      }
-      if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
-        leave_part<D, D>(p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D, acc, row);
-        warp_arrive(&sm.item_empty[slot]);
-        continue;
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int tk = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - tk * p.G;
-        quad_store<D, F16>(p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh, tk < n_tok, acc, u, p.scale);
       }
       warp_arrive(&sm.item_empty[slot]);
     }
@@ -860,19 +866,25 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const uint32_t from = lanes + (wg ? colDK : colDV);
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
-        uint32_t acc[D / 32][16];
-        quad_part<D>(acc, from, hf, a < b);
+        const uint32_t at = from + (static_cast<uint32_t>(hf * 16) << 16);
         if (e.slot >= 0) {  // this chunk's share, for the join behind these kernels
-          leave_part<D, D>(p.part + ((static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * 2 + wg) * kTile * D, acc, row + 16 * hf);
+          float* const mine = p.part + ((static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * 2 + wg) * kTile * D;
+          quad_blocks<D>(at, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D>(mine + c, acc, row + 16 * hf); });
           continue;
         }
+        uint16_t* to[2];
+        bool live[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int c = row + 16 * hf + 8 * u;
-          uint16_t* const dst = wg ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
-                                   : p.dv + static_cast<long long>(e.k0 + c) * p.dvt + head * p.dvh;
-          quad_store<D, F16>(dst, c < n_tok, acc, u, wg ? p.scale : 1.f);
+          live[u] = c < n_tok;
+          to[u] = wg ? p.dk + static_cast<long long>(e.k0 + c) * p.dkt + head * p.dkh
+                     : p.dv + static_cast<long long>(e.k0 + c) * p.dvt + head * p.dvh;
         }
+        quad_blocks<D>(at, a < b, [&](int c, const uint32_t(&acc)[16]) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) quad_store<F16>(to[u] + c, live[u], acc, u, wg ? p.scale : 1.f);
+        });
       }
       if (a < b) {
         tc_fence_before();

@@ -508,19 +508,24 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
-        uint32_t acc[D / 32][16];
-        quad_part<D>(acc, tO, hf, a < b);
+        const uint32_t from = tO + (static_cast<uint32_t>(hf * 16) << 16);
         if (cut) {  // this chunk's share, for the join behind this kernel
-          leave_part<D, D>(mine, acc, quarter * 32 + hf * 16 + (lane >> 2));
+          quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D>(mine + c, acc, quarter * 32 + hf * 16 + (lane >> 2)); });
           continue;
         }
+        uint16_t* row[2];
+        float f[2];
+        bool live[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int from = hf * 16 + (lane >> 2) + 8 * u;
-          const float f = __shfl_sync(0xffffffffu, inv, from);
-          const int t = __shfl_sync(0xffffffffu, r_tok, from), qh = head * p.G + quarter * 32 + from - t * p.G;
-          quad_store<D, F16>(p.o + (e.q0 + g * p.tpt + t) * p.ot + qh * p.oh, t < n_tok, acc, u, f);
+          const int at = hf * 16 + (lane >> 2) + 8 * u, t = __shfl_sync(0xffffffffu, r_tok, at);
+          f[u] = __shfl_sync(0xffffffffu, inv, at), live[u] = t < n_tok;
+          row[u] = p.o + (e.q0 + g * p.tpt + t) * p.ot + (head * p.G + quarter * 32 + at - t * p.G) * p.oh;
         }
+        quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) quad_store<F16>(row[u] + c, live[u], acc, u, f[u]);
+        });
       }
       if (a < b) {
         tc_fence_before();
