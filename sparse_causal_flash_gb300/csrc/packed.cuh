@@ -142,7 +142,8 @@ __host__ __device__ constexpr uint32_t pack_idesc(int M, int N, int a_mn, int b_
 }
 
 // One lane of a whole warp, by the instruction that the compiler knows as such: code under it may keep its operands in
-// uniform registers, as MMAs want them (under `lane == 0` a 128 x 128 x 16 MMA took XXX cycles to issue).
+// uniform registers, as MMAs want them (under `lane == 0` issuing was what bounded
+// the forward: 517 us instead of 440 at 8192 tokens, 32 heads over 8 of 128 channels, at that stage).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
