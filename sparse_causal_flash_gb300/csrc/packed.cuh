@@ -236,6 +236,21 @@ __device__ __forceinline__ void quad_blocks(uint32_t taddr, bool some, Use use) 
     use(c, acc);
   }
 }
+// All W columns of 16 lanes at once.
+template <int W>
+__device__ __forceinline__ void quad_part(uint32_t taddr, bool some, uint32_t (&acc)[W / 32][16]) {
+#pragma unroll
+  for (int b = 0; b < W / 32; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[b][i] = 0u;
+  if (some) {
+#pragma unroll
+    for (int b = 0; b < W / 32; ++b) tmem_ld_quad(taddr + 32 * b, acc[b]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int b = 0; b < W / 32; ++b) tmem_ld_fence(acc[b]);
+  }
+}
 // One of the two rows that a quad of lanes holds (u), times f, in the rows' type to `row`: 32 channels. Four words change
 // places inside the quad so that each lane has 16 bytes and the quad 64 in a row: a quarter of the stores' lines that whole
 // rows per thread would touch (those took 6,500 cycles for a tile of 128 x 128).

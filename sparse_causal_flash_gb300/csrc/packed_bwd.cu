@@ -427,26 +427,26 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_fence_after();
         ++n_q;
       }
-      if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
-        float* const mine = p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D;
-        quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D>(mine + c, acc, row); });
-      } else {
-        uint16_t* to[2];
-        bool live[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int tk = (row + 8 * u) / p.G;
-          live[u] = tk < n_tok;
-          to[u] = p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + (head * p.G + row + 8 * u - tk * p.G) * p.dqh;
-        }
-        quad_blocks<D>(from, a < b, [&](int c, const uint32_t(&acc)[16]) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) quad_store<F16>(to[u] + c, live[u], acc, u, p.scale);
-        });
-      }
+      // (16 rows a warp: all columns at once; in quad_blocks' loop the kernel took 464 us instead of 453, 8192 tokens, 32
+      // heads over 8 of 128 channels)
+      uint32_t acc[D / 32][16];
+      quad_part<D>(from, a < b, acc);
       if (a < b) {
         tc_fence_before();
         warp_arrive(&sm.dq_empty);
+      }
+      if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
+        float* const mine = p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) leave_part<D>(mine + c, acc[c / 32], row);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tk = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - tk * p.G;
+          uint16_t* const to = p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh;
+#pragma unroll
+          for (int c = 0; c < D; c += 32) quad_store<F16>(to + c, tk < n_tok, acc[c / 32], u, p.scale);
+        }
       }
       warp_arrive(&sm.item_empty[slot]);
     }
