@@ -12,8 +12,7 @@
 // One row is held by D / 16 threads, each with two 16-byte pieces such that both halves of its eight pairs are its own:
 // a norm is a few shuffles, and a row may be turned in place. What bounds it is HBM: each row is read once and written
 // once (gradients with a norm: two read, one written). A thread turns up to four heads of a token with one set of sines
-// (they cost 100 lane operations, a row's other work some 80), all loads before the first use: 31.5 us for 8192 tokens of
-// 32 and 8 heads of 128 channels with norms, 5.3 TB/s; 12.4 us for 275,280 rows of 64 without, 5.7 TB/s.
+// (they cost 100 lane operations, a row's other work some 80), all loads before the first use.
 #include "cache4.cuh"
 #include "internal.h"
 
@@ -199,9 +198,37 @@ __device__ __forceinline__ void rope_angles(const RopeArgs& g, const RopeMap<D, 
   }
 }
 
+// 16 bytes to shared memory, asynchronously; wait until at most `left` of this thread's groups are on their way
+__device__ __forceinline__ void rope_fetch(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void rope_fetched() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// One row: norm, turn, store.
+template <int D, bool F16, int KIND, bool NORM>
+__device__ __forceinline__ void rope_row(const RopeArgs& g, const RopeMap<D, KIND>& m, const RopeRaw& raw, const float (&wa)[8],
+                                         const float (&wb)[8], const float (&c)[8], const float (&s)[8], uint16_t* to, bool live) {
+  float a[8], b[8];
+  rope_unpack<D, F16, KIND>(raw, a, b);
+  if (NORM) {
+    const float r = rsqrtf(fmaf(rope_row_sum<D>(rope_dot(a, b, a, b)), 1.f / D, g.eps));
+    const uint64_t r2 = f2(r, r);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      f2_split(mul2(f2(a[i], a[i + 1]), mul2(f2(wa[i], wa[i + 1]), r2)), a[i], a[i + 1]);
+      f2_split(mul2(f2(b[i], b[i + 1]), mul2(f2(wb[i], wb[i + 1]), r2)), b[i], b[i + 1]);
+    }
+  }
+  rope_turn(a, b, c, s);
+  if (live) rope_store<D, F16, KIND>(to, m, a, b);
+}
+
 // Forward, and the gradient without a norm (turn < 0). One unit is HP heads of one token.
 template <int D, bool F16, int KIND, bool NORM, int HP>
-__global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 3) rope_kernel(const __grid_constant__ RopeArgs g) {
+__global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 2) rope_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int T = D / 16;
   const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
   const RopeSide& sd = g.side[si];
@@ -221,30 +248,63 @@ __global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 3) rope_kernel(con
   rope_angles(g, m, __ldg(g.pos + tok), c, s);
   if (NORM) rope_weights<D, KIND>(sd.w, m, wa, wb);
 #pragma unroll
-  for (int u = 0; u < HP; ++u) {
-    float a[8], b[8];
-    rope_unpack<D, F16, KIND>(raw[u], a, b);
-    if (NORM) {
-      const float r = rsqrtf(fmaf(rope_row_sum<D>(rope_dot(a, b, a, b)), 1.f / D, g.eps));
-      const uint64_t r2 = f2(r, r);
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        f2_split(mul2(f2(a[i], a[i + 1]), mul2(f2(wa[i], wa[i + 1]), r2)), a[i], a[i + 1]);
-        f2_split(mul2(f2(b[i], b[i + 1]), mul2(f2(wb[i], wb[i + 1]), r2)), b[i], b[i + 1]);
-      }
-    }
-    rope_turn(a, b, c, s);
-    if (live && h0 + u < sd.H) rope_store<D, F16, KIND>(sd.y + tok * sd.yt + (h0 + u) * sd.yh, m, a, b);
-  }
+  for (int u = 0; u < HP; ++u)
+    rope_row<D, F16, KIND, NORM>(g, m, raw[u], wa, wb, c, s, sd.y + tok * sd.yt + (h0 + u) * sd.yh, live && h0 + u < sd.H);
 }
 
-// 16 bytes to shared memory, asynchronously; wait until at most `left` of this thread's groups are on their way
-__device__ __forceinline__ void rope_fetch(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-template <int LEFT>
-__device__ __forceinline__ void rope_fetched() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+// The same for many units of four heads: a CTA takes every side.blocks-th, and while a thread works on one its pieces of the
+// next are on their way to shared memory. It reads back what it fetched itself, so it waits for its own copies alone.
+// 29.5 us for 8192 tokens of 32 and 8 heads of 128 channels with norms, 5.7 TB/s (34.9 with loads into registers, in units
+// that come and go; 32.3 with three CTAs per SM; 30.4 with two units ahead). Single heads are better off without: 18.4 us for
+// 275,280 rows of 64 channels, staged 19.8 and more.
+constexpr int kFwdHeads = 4, kFwdStages = 2;
+template <int D, bool F16, int KIND, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_staged_kernel(const __grid_constant__ RopeArgs g) {
+  constexpr int T = D / 16, HP = kFwdHeads, STAGES = kFwdStages;
+  extern __shared__ uint4 s_raw[];  // [stage][head][piece][thread]
+  const int si = static_cast<int>(blockIdx.x) >= g.side[0].blocks;
+  const RopeSide& sd = g.side[si];
+  const int block = blockIdx.x - (si ? g.side[0].blocks : 0);
+  RopeMap<D, KIND> m;
+  m.t = threadIdx.x % T, m.rot = g.rot;
+  const int tokens = rope_tokens(g);
+  const uint32_t units = static_cast<uint32_t>(tokens) * sd.slices, step = static_cast<uint32_t>(sd.blocks) * (kRopeThreads / T);
+  auto slot = [&](int stage, int u, int piece) { return s_raw + ((stage * HP + u) * 2 + piece) * kRopeThreads + threadIdx.x; };
+  auto fetch = [&](uint32_t unit, int stage) {
+    if (unit < units) {
+      const int tok = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok) * sd.slices) * HP;
+#pragma unroll
+      for (int u = 0; u < HP; ++u) {
+        const uint16_t* const x = sd.x + tok * sd.xt + min(h0 + u, sd.H - 1) * sd.xh;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rope_fetch(slot(stage, u, j), x + m.piece(j) * 8);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float wa[8], wb[8];
+  if (NORM) rope_weights<D, KIND>(sd.w, m, wa, wb);
+  uint32_t unit = static_cast<uint32_t>(block) * (kRopeThreads / T) + threadIdx.x / T;
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(unit + i * step, i);
+  int stage = 0;
+  // (whole warps stay together: rows are summed across their lanes)
+  for (uint32_t first = unit - threadIdx.x % 32 / T; first < units; first += step, unit += step) {
+    const int tok_ = static_cast<int>(unit / static_cast<uint32_t>(sd.slices)), h0 = static_cast<int>(unit - static_cast<uint32_t>(tok_) * sd.slices) * HP;
+    const bool live = tok_ < tokens;
+    const int tok = min(tok_, g.N - 1);
+    fetch(unit + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    float c[8], s[8];
+    rope_angles(g, m, __ldg(g.pos + tok), c, s);
+    rope_fetched<STAGES - 1>();
+#pragma unroll
+    for (int u = 0; u < HP; ++u) {
+      const uint4 x = *slot(stage, u, 0), y = *slot(stage, u, 1);
+      rope_row<D, F16, KIND, NORM>(g, m, RopeRaw{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}}, wa, wb, c, s,
+                                   sd.y + tok * sd.yt + (h0 + u) * sd.yh, live && h0 + u < sd.H);
+    }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+  }
 }
 
 // Gradients with a norm. A CTA takes every side.blocks-th unit and keeps its sum of dw in registers, which it leaves in
@@ -403,53 +463,71 @@ __global__ void __launch_bounds__(256) rope_dw_kernel(const __grid_constant__ Ro
   }
 }
 
-// CTAs of the gradient with a norm: as many as run at once, two per SM, no more than there is work for (four: 49.8 us
-// instead of 43.8 for the call above).
-constexpr int kBwdHeads = 2;
-int rope_bwd_ctas(int N, int H, int D, int most) {
+// CTAs of a side of H heads, HP a thread: its part of `most`, which is what runs at once (no CTA may wait for another's
+// end), and no more than there is work for.
+int rope_ctas(const RopeArgs& g, int H, int HP, int D, int most) {
   if (H == 0) return 0;
-  const long long n = (static_cast<long long>(N) * ((H + kBwdHeads - 1) / kBwdHeads) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
-  return static_cast<int>(n < most ? n : most);
+  const long long n = (static_cast<long long>(g.N) * ((H + HP - 1) / HP) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
+  return static_cast<int>(min(n, max(1ll, static_cast<long long>(most) * H / (g.side[0].H + g.side[1].H))));
 }
+// Gradients with a norm: two CTAs per SM (launching four, two of which wait: 49.8 us instead of 43.8 for the call above).
+constexpr int kBwdHeads = 2;
 int rope_most_ctas() { return 2 * num_sms(); }
 
+template <typename Kernel>
+cudaError_t rope_allow(Kernel kern, int smem, bool (&allowed)[64]) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !allowed[dev])) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+  }
+  return e;
+}
+
+template <int D, bool F16, int KIND, bool NORM, int HP>
+cudaError_t rope_launch_direct(RopeArgs& g, cudaStream_t st) {
+  for (RopeSide& s : g.side) {
+    s.slices = (s.H + HP - 1) / HP;
+    s.blocks = static_cast<int>((static_cast<long long>(g.N) * s.slices * (D / 16) + kRopeThreads - 1) / kRopeThreads);
+  }
+  rope_kernel<D, F16, KIND, NORM, HP><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, 0, st>>>(g);
+  return cudaGetLastError();
+}
+
+template <int D, bool F16, int KIND, bool NORM>
+cudaError_t rope_launch_staged(RopeArgs& g, cudaStream_t st) {
+  constexpr int HP = kFwdHeads, smem = kFwdStages * HP * 2 * kRopeThreads * 16;
+  static bool allowed[64] = {};
+  const cudaError_t e = rope_allow(rope_staged_kernel<D, F16, KIND, NORM>, smem, allowed);
+  if (e != cudaSuccess) return e;
+  for (RopeSide& s : g.side) s.slices = (s.H + HP - 1) / HP, s.blocks = rope_ctas(g, s.H, HP, D, 2 * num_sms());
+  rope_staged_kernel<D, F16, KIND, NORM><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, smem, st>>>(g);
+  return cudaGetLastError();
+}
 template <int D, bool F16, int KIND>
 cudaError_t rope_launch(RopeArgs& g, bool bwd, bool norm, cudaStream_t st) {
   constexpr int T = D / 16;
   if (bwd && norm) {
-    const int most = rope_most_ctas(), H = g.side[0].H + g.side[1].H;
-    for (RopeSide& s : g.side) {
-      s.slices = (s.H + kBwdHeads - 1) / kBwdHeads;
-      s.blocks = rope_bwd_ctas(g.N, s.H, D, max(1, most * s.H / H));  // (rounded down: no CTA may wait for another's end)
-    }
+    for (RopeSide& s : g.side) s.slices = (s.H + kBwdHeads - 1) / kBwdHeads, s.blocks = rope_ctas(g, s.H, kBwdHeads, D, rope_most_ctas());
     constexpr int smem = KIND == kHalfOdd ? 0 : kRopeStages * kBwdHeads * 4 * kRopeThreads * 16;
     static bool allowed[64] = {};
-    int dev = -1;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && (dev >= 64 || !allowed[dev])) {
-      e = cudaFuncSetAttribute(rope_bwd_kernel<D, F16, KIND, kBwdHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e == cudaSuccess && dev < 64) allowed[dev] = true;
-    }
+    cudaError_t e = rope_allow(rope_bwd_kernel<D, F16, KIND, kBwdHeads>, smem, allowed);
     if (e != cudaSuccess) return e;
     rope_bwd_kernel<D, F16, KIND, kBwdHeads><<<g.side[0].blocks + g.side[1].blocks, kRopeThreads, smem, st>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_behind(rope_dw_kernel<D>, dim3(D / 8, g.side[1].H ? 2 : 1), 256, st, g);
   }
-  // Four heads a thread once one head each fills the GPU twice over, and where there are as many.
+  // Four heads a thread once one head each fills the GPU twice over, and where there are as many; from shared memory where
+  // rows are 16-byte pieces.
   const bool many = g.side[0].H > 2 && static_cast<long long>(g.N) * (g.side[0].H + g.side[1].H) * T > 2ll * 2048 * num_sms();
-  for (RopeSide& s : g.side) {
-    s.slices = many ? (s.H + 3) / 4 : s.H;
-    s.blocks = static_cast<int>((static_cast<long long>(g.N) * s.slices * T + kRopeThreads - 1) / kRopeThreads);
+  if constexpr (KIND == kHalfOdd) {
+    if (many) return norm ? rope_launch_direct<D, F16, KIND, true, kFwdHeads>(g, st) : rope_launch_direct<D, F16, KIND, false, kFwdHeads>(g, st);
+  } else {
+    if (many) return norm ? rope_launch_staged<D, F16, KIND, true>(g, st) : rope_launch_staged<D, F16, KIND, false>(g, st);
   }
-  const int grid = g.side[0].blocks + g.side[1].blocks;
-  if (norm)
-    many ? rope_kernel<D, F16, KIND, true, 4><<<grid, kRopeThreads, 0, st>>>(g)
-         : rope_kernel<D, F16, KIND, true, 1><<<grid, kRopeThreads, 0, st>>>(g);
-  else
-    many ? rope_kernel<D, F16, KIND, false, 4><<<grid, kRopeThreads, 0, st>>>(g)
-         : rope_kernel<D, F16, KIND, false, 1><<<grid, kRopeThreads, 0, st>>>(g);
-  return cudaGetLastError();
+  return norm ? rope_launch_direct<D, F16, KIND, true, 1>(g, st) : rope_launch_direct<D, F16, KIND, false, 1>(g, st);
 }
 
 template <int D>

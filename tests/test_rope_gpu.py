@@ -136,6 +136,27 @@ def test_rows_and_gradients(scfa, N, Hq, Hkv, D, rot, il, norm, factor, dt):
         assert all(a is None or torch.equal(a, b) for a, b in zip(first[1], dw))
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("rot,il", [(128, False), (96, True), (40, False)])
+def test_more_rows_than_run_at_once(scfa, rot, il, norm):
+    """Units of four heads, the last with one; in place; the tokens end inside; a gradient without a norm as well."""
+    N, n, Hq, Hkv, D = 15013, 14990, 5, 1, 128
+    x, k = rand(1, (N, Hq, D), BF, 0.7), rand(2, (N, Hkv, D), BF, 0.7)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 7 - 5000
+    w = [1 + 0.3 * rand(5 + i, (D,), torch.float32) if norm else None for i in range(2)]
+    f, p, table = freqs(rot), pos[:n].cpu().numpy().astype(np.float64), scfa.rope_table(freqs(rot))
+    count = torch.tensor([n], dtype=torch.int32, device="cuda")
+    y, z = x.clone(), k.clone()
+    scfa.scfa_rope_fwd(y, z, pos, table, y, z, il, 1.2, *w, EPS, count)
+    for got, was, wi in ((y, x, w[0]), (z, k, w[1])):
+        check_fwd(got[:n], dbl(was[:n]), p, f, il, 1.2, None if wi is None else dbl(wi), BF)
+        assert torch.equal(got[n:], was[n:])
+    if not norm:
+        scfa.scfa_rope_bwd(y.copy_(x), None, pos, table, y, None, il, 1.2, count=count)
+        check_bwd(y[:n], None, dbl(x[:n]), None, p, f, il, 1.2, None, BF)
+        assert torch.equal(y[n:], x[n:])
+
+
 @pytest.mark.parametrize("rot,il", [(128, False), (128, True), (40, False)])
 def test_gradients_of_more_rows_than_run_at_once(scfa, rot, il):
     """A CTA takes several units of two heads; the last head stands alone; the tokens end inside a unit's row."""
