@@ -276,6 +276,19 @@ def test_work_that_is_cut_over_ctas(scfa, lens, Hq, Hkv, D, dt):
         assert all(torch.equal(a, b) for a, b in zip(first, (p.o, p.lse, p.dq, p.dk, p.dv)))
 
 
+@pytest.mark.parametrize("window", [310, 2 ** 31 - 1])
+def test_a_window_wider_than_the_keys_hides_none(scfa, window):
+    """Also where the first queries stand before the first key."""
+    lens = [(10, 5), (300, 290), (7, 7)]
+    p, r = (Problem(scfa, lens, 4, 2, 64, window=w, seed=12) for w in (window, 0))
+    for x in (p, r):
+        x.forward()
+        x.backward()
+        assert x.status() == 0
+    r.check_forward()
+    assert all(torch.equal(getattr(p, key), getattr(r, key)) for key in ("o", "lse", "dq", "dk", "dv"))
+
+
 def test_many_sequences(scfa):
     """More sequences than the plan has threads, most of them short or empty."""
     g = np.random.default_rng(0)
