@@ -3,16 +3,16 @@
 //
 // One CTA builds each list, in four passes over the tiles of one key head: count the tiles of each sequence, find each
 // tile's range of tiles on the other side (its units: 128 x 128 score tiles), choose how long a piece of work may be,
-// and write the pieces, longest first. Latency is all that counts, a chain of loads and barriers: 19 us for one sequence of
-// 8,192 tokens, 60 for one of 131,072, 85 for 5,000 of one token; once a batch, for all its layers.
+// and write the pieces, longest first. Latency is all that counts, a chain of loads and barriers: 16 us for one sequence of
+// 8,192 tokens, 56 for one of 131,072, 83 for 5,000 of one token; once a batch, for all its layers.
 //
 // Cutting. A kernel's CTAs take pieces from a counter, longest first. Where few tiles have long ranges (a long prefix
 // under few new tokens, few heads) that leaves SMs idle, so ranges longer than L units are cut into equal chunks whose
 // results are joined later, in order. L is the candidate with the least estimate among eighths of the units per SM and
 // "no cut". The estimate is a round's length times the rounds that the long pieces take, less what the short ones fill of
 // the last round, and three units for leaving and joining a chunk.
-// Where all tiles are alike (a window, equal texts) the last round may be nearly empty: 784 items of 17 units on 152 SMs
-// take six rounds for 5.2. Then the items of that round alone are cut.
+// Where all tiles are alike (a window, equal texts) the last round may be nearly empty: 784 equal items on 152 SMs take
+// six rounds for 5.2. Then the items of that round alone are cut.
 #include "packed.cuh"
 
 namespace scfa {
@@ -182,19 +182,30 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     if ((tid & 31) == 0 && y) atomicAdd(&s_cut[c], y);
   }
   __syncthreads();
-  if (tid == 0) {
-    // in quarters of a unit, over all SMs
-    long long best = 1ll << 62;
-    s_tail = tiles;
+  if (tid < 32) {
+    // in quarters of a unit, over all SMs; a candidate by a lane, the last of the cheapest is taken
     const long long room = static_cast<long long>(kPackSlotsPerSm) * p.sms, all = static_cast<long long>(s_units) * p.Hkv;
-    for (int c = kCandidates - 1; c >= 0; --c) {
-      const long long L = candidate(c), n = static_cast<long long>(s_big[c]) * p.Hkv, k = static_cast<long long>(s_cut[c]) * p.Hkv;
-      if (k > room) continue;
+    const int c = min(tid, kCandidates - 1);
+    const long long L = candidate(c), k = static_cast<long long>(s_cut[c]) * p.Hkv;
+    long long best;
+    {
+      const long long n = static_cast<long long>(s_big[c]) * p.Hkv;
       const long long rounds = (n + p.sms - 1) / p.sms, fill = all - static_cast<long long>(s_work[c]) * p.Hkv;
       const long long idle = max(0ll, (rounds * p.sms - n) * L * 3 / 4 - fill);
-      const long long t = 4 * (all + idle) + 12 * k + (k ? 4ll * p.sms : 0);
-      if (t < best) best = t, s_limit = static_cast<int>(L);
+      best = k > room ? 1ll << 62 : 4 * (all + idle) + 12 * k + (k ? 4ll * p.sms : 0);
     }
+    int which = c;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const long long t = __shfl_xor_sync(0xffffffffu, best, o);
+      const int w = __shfl_xor_sync(0xffffffffu, which, o);
+      if (t < best || (t == best && w > which)) best = t, which = w;
+    }
+    if (tid == which) s_limit = static_cast<int>(L), s_tail = tiles;
+    __syncwarp();
+  }
+  if (tid == 0) {
+    const long long room = static_cast<long long>(kPackSlotsPerSm) * p.sms, all = static_cast<long long>(s_units) * p.Hkv;
     const long long n = static_cast<long long>(s_big[kCandidates - 1]) * p.Hkv, over = n % p.sms;
     if (s_limit >= longest && n > p.sms && over > 0 && 8 * (all - static_cast<long long>(s_work[kCandidates - 1]) * p.Hkv) < all) {
       // the items beyond whole rounds, cut to a share of an SM each
