@@ -168,33 +168,32 @@ __device__ __forceinline__ float rope_row_sum(float x) {
   return x;
 }
 
-// cosine and sine of each pair, times factor; 1 and 0 where a pair is not turned
+// 2^-64ths of a turn per position of pairs i and i + 1, zero where they are not turned
 template <int D, int KIND>
-__device__ __forceinline__ void rope_angles(const RopeArgs& g, const RopeMap<D, KIND>& m, int pos, float (&c)[8], float (&s)[8]) {
-  const int h = g.rot >> 1;
-  const uint32_t p = static_cast<uint32_t>(pos);
+__device__ __forceinline__ void rope_turns(const RopeArgs& g, const RopeMap<D, KIND>& m, int i, uint64_t* f) {
+  const int h = g.rot >> 1, k = m.slot(i);
+  if (KIND == kHalf || (KIND == kInterleaved && k + 1 < h)) {  // two neighbours, both turned or neither
+    const ulonglong2 u = k < h ? __ldg(reinterpret_cast<const ulonglong2*>(g.table + k)) : make_ulonglong2(0, 0);
+    f[0] = u.x, f[1] = u.y;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const int k = m.slot(i);
-    uint64_t f[2];
-    if (KIND == kHalf || (KIND == kInterleaved && k + 1 < h)) {  // two neighbours, both turned or neither
-      const ulonglong2 u = k < h ? __ldg(reinterpret_cast<const ulonglong2*>(g.table + k)) : make_ulonglong2(0, 0);
-      f[0] = u.x, f[1] = u.y;
-    } else {
+    for (int j = 0; j < 2; ++j)
+      f[j] = m.slot(i + j) < h ? __ldg(reinterpret_cast<const unsigned long long*>(g.table) + m.slot(i + j)) : 0;
+  }
+}
+// cosine and sine of pairs i and i + 1, times factor; 1 and 0 where a pair is not turned
+template <int D, int KIND>
+__device__ __forceinline__ void rope_angles(const RopeArgs& g, const RopeMap<D, KIND>& m, int i, const uint64_t* f, int pos,
+                                            float (&c)[8], float (&s)[8]) {
+  const uint32_t p = static_cast<uint32_t>(pos), below = pos < 0 ? 0xffffffffu : 0u;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        f[j] = m.slot(i + j) < h ? __ldg(reinterpret_cast<const unsigned long long*>(g.table) + m.slot(i + j)) : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t lo = static_cast<uint32_t>(f[j]), hi = static_cast<uint32_t>(f[j] >> 32);
-      // bits 32..63 of the signed position times f
-      const uint32_t z = p * hi + __umulhi(p, lo) - (pos < 0 ? lo : 0u);
-      const float t = static_cast<float>(static_cast<int32_t>(z)) * g.turn;
-      const bool turned = m.slot(i + j) < h;
-      c[i + j] = turned ? __cosf(t) * g.factor : 1.f;
-      s[i + j] = turned ? __sinf(t) * g.factor : 0.f;
-    }
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t lo = static_cast<uint32_t>(f[j]), hi = static_cast<uint32_t>(f[j] >> 32);
+    // bits 32..63 of the signed position times f
+    const uint32_t z = p * hi + (below * lo + __umulhi(p, lo));
+    const float t = static_cast<float>(static_cast<int32_t>(z)) * g.turn;
+    c[i + j] = m.slot(i + j) < g.rot >> 1 ? __cosf(t) * g.factor : 1.f;
+    s[i + j] = __sinf(t) * g.factor;  // (zero at zero)
   }
 }
 
@@ -245,7 +244,13 @@ __global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 2) rope_kernel(con
   for (int u = 0; u < HP; ++u)
     raw[u] = rope_load<D, F16, KIND>(sd.x + tok * sd.xt + min(h0 + u, sd.H - 1) * sd.xh, m);
   float c[8], s[8], wa[8], wb[8];
-  rope_angles(g, m, __ldg(g.pos + tok), c, s);
+  const int pos = __ldg(g.pos + tok);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    uint64_t f[2];
+    rope_turns(g, m, i, f);
+    rope_angles(g, m, i, f, pos, c, s);
+  }
   if (NORM) rope_weights<D, KIND>(sd.w, m, wa, wb);
 #pragma unroll
   for (int u = 0; u < HP; ++u)
@@ -255,7 +260,7 @@ __global__ void __launch_bounds__(kRopeThreads, HP == 1 ? 1 : 2) rope_kernel(con
 // The same for many units of four heads: a CTA takes every side.blocks-th, and while a thread works on one its pieces of the
 // next are on their way to shared memory. It reads back what it fetched itself, so it waits for its own copies alone.
 // 29.5 us for 8192 tokens of 32 and 8 heads of 128 channels with norms, 5.7 TB/s (34.9 with loads into registers, in units
-// that come and go; 32.3 with three CTAs per SM; 30.4 with two units ahead). Single heads are better off without: 18.4 us for
+// that come and go; 32.3 with three CTAs per SM; 30.4 with two units ahead). Single heads are better off without: 16.9 us for
 // 275,280 rows of 64 channels, staged 19.8 and more.
 constexpr int kFwdHeads = 4, kFwdStages = 2;
 template <int D, bool F16, int KIND, bool NORM>
@@ -284,6 +289,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_staged_kernel(const __gr
   };
   float wa[8], wb[8];
   if (NORM) rope_weights<D, KIND>(sd.w, m, wa, wb);
+  uint64_t f[8];  // (loaded once: 46.4 -> 43.8 us for the gradient below, 31.3 -> 29.5 for the forward)
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) rope_turns(g, m, i, f + i);
   uint32_t unit = static_cast<uint32_t>(block) * (kRopeThreads / T) + threadIdx.x / T;
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(unit + i * step, i);
@@ -295,7 +303,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_staged_kernel(const __gr
     const int tok = min(tok_, g.N - 1);
     fetch(unit + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
     float c[8], s[8];
-    rope_angles(g, m, __ldg(g.pos + tok), c, s);
+    const int pos = __ldg(g.pos + tok);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) rope_angles(g, m, i, f + i, pos, c, s);
     rope_fetched<STAGES - 1>();
 #pragma unroll
     for (int u = 0; u < HP; ++u) {
@@ -310,8 +320,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_staged_kernel(const __gr
 // Gradients with a norm. A CTA takes every side.blocks-th unit and keeps its sum of dw in registers, which it leaves in
 // `part`: rows are summed in an order that the sizes alone decide. A thread's pieces of its next unit are on their way to
 // shared memory while it works on one; it reads back what it fetched itself, so it waits for its own copies alone.
-// Bounded by HBM and, near it, by latency: 43.8 us for 8192 tokens of 32 and 8 heads of 128 channels, 5.7 TB/s (61 with
-// loads into registers, all that fit; 45.8 with two units ahead, 54.4 with one head a thread and three CTAs per SM).
+// Bounded by HBM and, near it, by latency: 43.9 us for 8192 tokens of 32 and 8 heads of 128 channels, 5.7 TB/s (with loads
+// into registers, all that fit, 61; at 46.4, two units ahead cost 2 more, one head a thread and three CTAs per SM 10).
 template <int D, bool F16, int KIND, int HP>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeArgs g) {
   constexpr int T = D / 16;
@@ -358,6 +368,9 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
     const uint4 x = *slot(stage, u, which, 0), y = *slot(stage, u, which, 1);
     return RopeRaw{{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}};
   };
+  uint64_t f[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) rope_turns(g, m, i, f + i);
   uint32_t first = static_cast<uint32_t>(block) * (kRopeThreads / T);
   if (kStaged) {
 #pragma unroll
@@ -386,7 +399,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
       }
     }
     float c[8], s[8];
-    rope_angles(g, m, pos, c, s);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) rope_angles(g, m, i, f + i, pos, c, s);
 #pragma unroll
     for (int u = 0; u < HP; ++u) {
       float xa[8], xb[8], ga[8], gb[8], wa[8], wb[8];
@@ -470,7 +484,7 @@ int rope_ctas(const RopeArgs& g, int H, int HP, int D, int most) {
   const long long n = (static_cast<long long>(g.N) * ((H + HP - 1) / HP) * (D / 16) + kRopeThreads - 1) / kRopeThreads;
   return static_cast<int>(min(n, max(1ll, static_cast<long long>(most) * H / (g.side[0].H + g.side[1].H))));
 }
-// Gradients with a norm: two CTAs per SM (launching four, two of which wait: 49.8 us instead of 43.8 for the call above).
+// Gradients with a norm: two CTAs per SM (launching four, two of which wait: 6 us more for the call above).
 constexpr int kBwdHeads = 2;
 int rope_most_ctas() { return 2 * num_sms(); }
 
