@@ -31,7 +31,6 @@ constexpr int kThreads = 384;
 constexpr int kRegsFew = 72, kRegsMany = 216;  // 128 x 72 + 256 x 216 = 384 x 168, what a CTA starts with
 constexpr int kSoftWarps = 8;                  // two warpgroups, 64 columns of a tile each
 constexpr int kSlots = 3;                      // items known ahead
-constexpr int kStatStages = 2;
 
 struct PBwdParams {
   const char* plan;
@@ -483,6 +482,7 @@ struct __align__(1024) DkvSmem {
   uint8_t v[kKs][kSubs][kPackSub];
   uint8_t q[kQs][kSubs][kPackSub];
   uint8_t dO[kOs][kSubs][kPackSub];
+  static constexpr int kStatStages = D == 64 ? 4 : 2;  // (all that fits at D = 128)
   alignas(16) float nl[kStatStages][kTile];
   alignas(16) float nd[kStatStages][kTile];
   PackEntry item[kSlots];
@@ -500,7 +500,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                   const __grid_constant__ PBwdParams p) {
   using Sm = DkvSmem<D>;
-  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kOs = Sm::kOs, kKs = Sm::kKs;
+  constexpr int kSubs = Sm::kSubs, kQs = Sm::kQs, kOs = Sm::kOs, kKs = Sm::kKs, kStatStages = Sm::kStatStages;
   constexpr bool kOwn = D == 64;
   constexpr uint32_t colDV = 512 - 2 * D, colDK = 512 - D;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -604,6 +604,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int i = a; i < b && ok; ++i) {
           ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, kQs, head, e, i);
           if (!ok) break;
+          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i);
+          if (!ok) break;
           const int s = st_it % kStatStages;
           ok = warp_wait(&sm.st_empty[s], ((st_it / kStatStages) & 1) ^ 1, abort_flag, p.status);
           if (!ok) break;
@@ -614,7 +616,6 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             bulk_load(sm.nd[s], st + n_stats, kTile * 4, &sm.st_full[s]);
           }
           ++st_it;
-          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i);
           if (i == a) work.next(p.counter, lane);  // (under the loads)
         }
       }
