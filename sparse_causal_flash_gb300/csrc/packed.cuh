@@ -20,6 +20,13 @@ constexpr float kPackLn2 = 0.6931471805599453f;
 // Chunks that cut entries may leave behind for their join, over all key heads.
 constexpr int kPackSlotsPerSm = 4;
 
+// Work of so many tiles is never cut, so that calls on few rows need no join (7 short texts, in a graph:
+// 9.4 us instead of 10.8 forward, 16.8 instead of 19.0 backward).
+constexpr int kPackNeverCut = 3;
+inline bool pack_may_cut(int N, int M, int tpt, bool backward) {
+  return M > kPackNeverCut * kTile || (backward && N > kPackNeverCut * tpt);
+}
+
 enum { kListFwd = 0, kListDq = 1, kListDkv = 2, kLists = 3 };
 
 // One piece of work of one key head. Query lists: the tokens q0 .. q0 + n_tok (rows of q) see the keys k0 .. of one

@@ -989,7 +989,7 @@ extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, lon
   j.plan = p.plan, j.plan_bytes = p.plan_bytes, j.N = N, j.M = M, j.Hq = Hq, j.Hkv = Hkv, j.G = p.G, j.tpt = p.tpt;
   j.part = p.part, j.part_q = p.part_q, j.scale = scale, j.status = p.status;
   j.dq = dq, j.dqt = dq_token, j.dqh = dq_head, j.dk = dk, j.dkt = dk_token, j.dkh = dk_head, j.dv = dv, j.dvt = dv_token, j.dvh = dv_head;
-  if (launch_pack_join(j, D, f16, true, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
+  if (pack_may_cut(N, M, p.tpt, true) && launch_pack_join(j, D, f16, true, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;
 }

@@ -614,7 +614,7 @@ extern "C" scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, lon
   PackJoin j = {};
   j.plan = p.plan, j.plan_bytes = p.plan_bytes, j.N = N, j.M = M, j.Hq = Hq, j.Hkv = Hkv, j.G = p.G, j.tpt = p.tpt;
   j.part = p.part, j.o = o, j.ot = o_token, j.oh = o_head, j.lse = lse, j.status = p.status;
-  if (launch_pack_join(j, D, f16, false, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
+  if (pack_may_cut(N, M, p.tpt, false) && launch_pack_join(j, D, f16, false, sms, st) != cudaSuccess) return SCFA_ERR_CUDA;
   if ((flags & SCFA_FLAG_DEBUG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return SCFA_ERR_CUDA;
   return SCFA_OK;
 }

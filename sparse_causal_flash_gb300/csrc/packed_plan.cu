@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   const int longest = max(1, s_most);
   const long long per_sm = (static_cast<long long>(s_units) * p.Hkv + p.sms - 1) / p.sms;
   auto candidate = [&](int c) -> int {  // the last one: no cut
-    if (c == kCandidates - 1) return longest;
+    if (c == kCandidates - 1 || longest <= kPackNeverCut) return longest;
     return static_cast<int>(min(static_cast<long long>(longest), max(2ll, (per_sm * (c + 2) + 7) / 8)));
   };
   int big[kCandidates], cut[kCandidates];
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   if (tid == 0) {
     const long long room = static_cast<long long>(kPackSlotsPerSm) * p.sms, all = static_cast<long long>(s_units) * p.Hkv;
     const long long n = static_cast<long long>(s_big[kCandidates - 1]) * p.Hkv, over = n % p.sms;
-    if (s_limit >= longest && n > p.sms && over > 0 && 8 * (all - static_cast<long long>(s_work[kCandidates - 1]) * p.Hkv) < all) {
+    if (s_limit >= longest && longest > kPackNeverCut && n > p.sms && over > 0 && 8 * (all - static_cast<long long>(s_work[kCandidates - 1]) * p.Hkv) < all) {
       // the items beyond whole rounds, cut to a share of an SM each
       const long long cut_tiles = (over + p.Hkv - 1) / p.Hkv, share = max(2ll, (cut_tiles * p.Hkv * longest + p.sms - 1) / p.sms);
       const long long chunks = cut_tiles * p.Hkv * ((longest + share - 1) / share);

@@ -289,6 +289,13 @@ def test_a_window_wider_than_the_keys_hides_none(scfa, window):
     assert all(torch.equal(getattr(p, key), getattr(r, key)) for key in ("o", "lse", "dq", "dk", "dv"))
 
 
+@pytest.mark.parametrize("lens", [[(5, 384)], [(5, 385)], [(384, 384)], [(385, 380)], [(1, 100), (2, 284)], [(200, 2000)]])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1)])
+def test_on_either_side_of_what_is_never_cut(scfa, lens, Hq, Hkv):
+    """Calls on at most three tiles of keys (backward: and of queries) have no join behind them."""
+    Problem(scfa, lens, Hq, Hkv, 64, seed=13).all()
+
+
 def test_many_sequences(scfa):
     """More sequences than the plan has threads, most of them short or empty."""
     g = np.random.default_rng(0)
