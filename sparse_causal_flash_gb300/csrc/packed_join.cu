@@ -1,6 +1,7 @@
 // Joins what chunks of cut work left behind (packed_plan.cu): one row by a warp (128 channels) or half a warp (64), its
-// chunks in their order, so that results are the same bits on every run. Bounded by L2: every share is read once. (The last
-// chunk to arrive joining for all took 27 us for eight chunks on its one SM, at the end of the kernel.)
+// chunks in their order, so that results are the same bits on every run. Bounded by L2: every share is read once (12 us,
+// alone and with cold caches, for the 17 MB of three chunks over 12,000 keys). The last chunk to arrive joining for all
+// took 27 us for eight chunks on its one SM, at the end of the kernel.
 #include "packed.cuh"
 
 namespace scfa {
