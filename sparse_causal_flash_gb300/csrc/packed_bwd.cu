@@ -39,7 +39,7 @@ constexpr int kSlots = 3;                      // items known ahead
 struct PBwdParams {
   const char* plan;
   long long plan_bytes;
-  int N, M, Hq, Hkv, G, tpt, D;
+  int N, M, Hq, Hkv, G, tpt;
   float scale, scale_log2;
   const uint16_t *o, *dO;
   long long ot, oh, dot, doh;
@@ -968,7 +968,7 @@ extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, lon
   if (N == 0 && M == 0) return cudaMemsetAsync(c, 0, w.clear, st) == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
   PBwdParams p = {};
   p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
-  p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.D = D, p.scale = scale, p.scale_log2 = factor;
+  p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.scale = scale, p.scale_log2 = factor;
   p.o = o, p.ot = o_token, p.oh = o_head, p.dO = dO, p.dot = do_token, p.doh = do_head, p.lse = lse;
   p.dq = dq, p.dqt = dq_token, p.dqh = dq_head, p.dk = dk, p.dkt = dk_token, p.dkh = dk_head, p.dv = dv, p.dvt = dv_token, p.dvh = dv_head;
   p.counter = reinterpret_cast<int*>(c + w.counters);
