@@ -386,3 +386,39 @@ def test_cache_steps_with_rope_and_norm(scfa):
     with pytest.raises(ValueError, match="positions"):
         b.step(q, k, v, n, 0.125, pos=pos)
     assert torch.equal(a.len, b.len)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("N,H", [(6, 3), (9000, 5)])
+@pytest.mark.parametrize("D,rot,il", [(64, 0, False), (64, 32, False), (128, 96, False), (64, 20, False), (128, 126, False),
+                                      (64, 0, True), (64, 32, True), (128, 22, True)])
+def test_channels_that_do_not_turn_pass_as_they_are(scfa, D, rot, il, N, H, dt):
+    """Bit for bit, whatever stands in the channels beside them: infinities, NaN, zeros with a sign."""
+    x = rand(rot + H, (N, H, D), dt)
+    x[..., rot:] = torch.tensor([float("inf"), 1.5, -0.0, float("nan"), -2.0, 0.0, float("-inf"), 3.0], dtype=dt,
+                                device="cuda").repeat(D // 8)[rot:]
+    x[1::2, :, rot:] = x[1::2, :, rot:].flip(-1)
+    x[-1, :, rot:] = torch.roll(x[0, :, rot:], 1, -1)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 3 + 1
+    f, table = freqs(rot), scfa.rope_table(freqs(rot))
+    for call, sign in ((scfa.scfa_rope_fwd, 1), (scfa.scfa_rope_bwd, -1)):
+        y = torch.zeros_like(x)
+        call(x, None, pos, table, y, None, il, 1.3)
+        was, got = x[..., rot:], y[..., rot:]
+        assert torch.equal(torch.isnan(was), torch.isnan(got))
+        same = ~torch.isnan(was)
+        assert torch.equal(was.view(torch.int16)[same], got.view(torch.int16)[same])
+        if rot:
+            check_fwd(y[..., :rot], dbl(x[..., :rot]), sign * pos.cpu().numpy().astype(np.float64), f, il, 1.3, None, dt)
+
+
+@pytest.mark.parametrize("D,rot,il", [(64, 32, False), (128, 126, False), (64, 22, True)])
+def test_a_channel_that_does_not_turn_spoils_no_other_weight(scfa, D, rot, il):
+    """An infinite gradient in a channel behind `rot`: that channel's dw is not finite, every other is."""
+    N, H = 70, 3
+    x, dy = rand(1, (N, H, D), BF), rand(2, (N, H, D), BF)
+    dy[11, 2, D - 2] = float("inf")
+    pos, dw = torch.arange(N, dtype=torch.int32, device="cuda"), torch.empty(D, device="cuda")
+    scfa.scfa_rope_bwd(dy, None, pos, scfa.rope_table(freqs(rot)), torch.empty_like(x), None, il, q=x,
+                       wq=torch.ones(D, device="cuda"), eps=EPS, dwq=dw, ws=scfa.workspace(scfa.rope_workspace_size(N, H, 0, D)))
+    assert torch.isfinite(dw).tolist() == [c != D - 2 for c in range(D)]
