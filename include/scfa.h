@@ -511,7 +511,12 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  * nothing from call to call; a plan for other
  * sizes raises SCFA_ERR_INVALID in its status word. Results are the same bits on
  * every run. A row of q, k or v that is not finite may reach any row of its own
- * sequence and key head, and no other. flags: SCFA_FLAG_DEBUG_SYNC,
+ * sequence and key head, and no other. Weights and their gradients dS are
+ * rounded to the rows' type for their products, in fp16 times powers of two that
+ * are taken out again, so that gradients of any size keep their digits; results
+ * that fp16 cannot hold (above 65,504, below 2^-24) are infinite or zero. The
+ * forward's weights below 2^-24 of the largest of their row are zero in fp16
+ * (its lse has them). flags: SCFA_FLAG_DEBUG_SYNC,
  * SCFA_FLAG_DEBUG_STALL.
  * ------------------------------------------------------------------------- */
 size_t scfa_packed_plan_size(int N, int M, int R, int Hq, int Hkv);

@@ -42,7 +42,8 @@ struct PackEntry {
   int slot;    // first partial slot of the cut entry (per key head); -1: not cut
   int chunk, chunks;
   int head;    // (in shared memory) key head, -1: no more work
-  int pad[3];
+  int seq;     // number of the sequence
+  int pad[2];
 };
 static_assert(sizeof(PackEntry) == 64, "entries are copied as 16 words");
 
@@ -104,7 +105,8 @@ struct PackWs {
   size_t counters = 0;          // ints: next item of each kernel
   size_t part = 0, part_q = 0;  // fp32, [slot][Hkv]: two tiles of D + 2 columns, or dV and dK; (backward) dQ
   size_t forward = 0;           // what a forward needs
-  size_t stats = 0;             // backward: [2][query tiles][Hkv][128]
+  size_t stats = 0;             // backward: [2][query tiles][Hkv][128] floats, then for fp16 the largest rows (packed_bwd.cu):
+                                // [query tiles][Hkv][16] of dO, [key tiles][Hkv][8] of V
   size_t clear = 0;             // bytes from the start that a call clears
 };
 // A backward's workspace serves a forward too.
@@ -118,7 +120,13 @@ inline PackWs pack_ws(int D, int sms) {
   w.stats = align_up(w.part_q + slots * row * D, 256);
   return w;
 }
-inline long long pack_stats_tile_bytes(int Hkv) { return 2ll * Hkv * kTile * sizeof(float); }
+constexpr int kDoUnits = 16, kVUnits = 8;  // a tile's pieces of 8 and 16 rows
+__host__ __device__ __forceinline__ long long pack_stats_bytes(long long q_tiles, int M, int R, int Hkv) {
+  return (q_tiles * (2 * kTile + kDoUnits) + (static_cast<long long>(M / kTile) + R) * kVUnits) * Hkv * static_cast<long long>(sizeof(float));
+}
+// Number of key tile i (of the sequence seq, whose keys start at row k0) among less than M / 128 + R: sequences of m keys
+// leave room for as many tiles as they may have.
+__device__ __forceinline__ long long pack_key_tile(int k0, int seq, int i) { return static_cast<long long>(k0 / kTile) + seq + i; }
 
 // The join of what the chunks left, behind the kernel that left it: o and lse (forward), or dV, dK and dQ.
 struct PackJoin {
@@ -276,16 +284,16 @@ __device__ __forceinline__ void quad_store(uint16_t* row, bool live, const uint3
   const uint4 v = t & 2 ? make_uint4(y0, y1, p2, p3) : make_uint4(p0, p1, y0, y1);
   if (live) *reinterpret_cast<uint4*>(row + 8 * t) = v;
 }
-// Leave 32 columns of an accumulator (rows of D) as a chunk's share.
-template <int D>
-__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[16], int row) {
+// Leave 32 columns of an accumulator (rows of D) as a chunk's share; TIMES: the quad's two rows times f.
+template <int D, bool TIMES = false>
+__device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[16], int row, const float (&f)[2] = {}) {
   const int c0 = 2 * (threadIdx.x & 3);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
-          make_float2(__uint_as_float(acc[i * 4 + 2 * u]), __uint_as_float(acc[i * 4 + 2 * u + 1]));
+          make_float2(__uint_as_float(acc[i * 4 + 2 * u]) * (TIMES ? f[u] : 1.f), __uint_as_float(acc[i * 4 + 2 * u + 1]) * (TIMES ? f[u] : 1.f));
 }
 __device__ __forceinline__ float pack_max3(float a, float b, float c) {
   float d;

@@ -41,12 +41,12 @@ struct PBwdParams {
   long long plan_bytes;
   int N, M, Hq, Hkv, G, tpt;
   float scale, scale_log2;
-  const uint16_t *o, *dO;
-  long long ot, oh, dot, doh;
+  const uint16_t *o, *dO, *v;
+  long long ot, oh, dot, doh, vt, vh;
   const float* lse;
   uint16_t *dq, *dk, *dv;
   long long dqt, dqh, dkt, dkh, dvt, dvh;
-  float* stats;             // [2][tiles][Hkv][128]
+  float* stats;             // [2][tiles][Hkv][128] and, for fp16, the largest rows
   long long stats_bytes;    // room for them
   int* counter;
   float *part, *part_q;     // chunks' shares of dV and dK, and of dQ
@@ -58,14 +58,51 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
   const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
   const int s = pack_plan_status(h, p.plan_bytes, p.N, p.M, p.Hq, p.Hkv);
   if (s != SCFA_OK) return s;
-  return 2ll * h->n_qtiles * p.Hkv * kTile * static_cast<long long>(sizeof(float)) > p.stats_bytes ? SCFA_ERR_WORKSPACE : SCFA_OK;
+  return pack_stats_bytes(h->n_qtiles, p.M, h->R, p.Hkv) > p.stats_bytes ? SCFA_ERR_WORKSPACE : SCFA_OK;
+}
+
+// ------------------------------------------------------------------ fp16: what P and dS are held times
+// A weight over n flat keys is 1 / n and dS = P (dP - delta) may be any size, while fp16 has normal numbers from 2^-14 to
+// 2^16 only: as they are, weights over 16,384 keys and dS of a dO of 0.001 over 2,000 lose their digits, and a dO of
+// thousands leaves infinities. So for fp16 P is held times 2^10 (normal from 2^-24 up; it is at most 1, and room for 2^6
+// is left to an lse that is far from zero), and dS times 2^k, with 2^10.5 <= 2^k |dO| |V| <= 2^13 for the longest rows of
+// dO and V that meet in a piece of work (dK, dV), or for a query's block of eight rows and the V that its piece meets (dQ).
+// |dP - delta| <= 2 |dO| |V|, so dS stays below 2^14, and is normal down to 2^-24.5 |dO| |V|. Both are powers of two and
+// taken out again in fp32. The statistics kernel finds the lengths, squared: of dO's blocks of eight rows, at most 2^1.5
+// above the longest row's, and of the longest of 16 rows of V. What is not finite counts as nothing there, and spoils what
+// it meets in any case. It costs 3 us of the 14 of the statistics and 1-3% of the other kernels (9 texts of 101 to 3501
+// tokens, 12 heads over 4 of 64 channels: 231 us in a graph instead of 219).
+constexpr int kPUp = 10, kDsUp = 13;
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
+// k of the squared lengths a (dO), b (V), each 0 or 2^-48 to 2^42
+__device__ __forceinline__ int ds_up(float a, float b) {
+  const int e = (__float_as_int(a * b) >> 23) - 127;  // |dO| |V| < 2^((e + 1) / 2)
+  return kDsUp - ((e + 2) >> 1);
+}
+__device__ __forceinline__ float finite_or_zero(float x) { return x < INFINITY ? x : 0.f; }
+// The largest of n groups of PER numbers (none negative), group i at base + i * stride; by a whole warp.
+template <int PER>
+__device__ __forceinline__ float warp_largest(const float* base, long long stride, int n, int lane) {
+  constexpr int L = PER / 4;
+  float m = 0.f;
+  for (int i0 = lane; i0 < n * L; i0 += 4 * 32) {
+    float4 x[4];  // (all on their way at once; the last one again where there is none)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(i0 + 32 * j, n * L - 1);
+      x[j] = __ldcg(reinterpret_cast<const float4*>(base + (i / L) * stride) + i % L);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = pack_max3(m, pack_max3(x[j].x, x[j].y, x[j].z), x[j].w);
+  }
+  return __int_as_float(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
 }
 
 // ------------------------------------------------------------------ row statistics
 // A warp takes eight rows of a tile at a time, a 16-byte piece of O and dO per lane and row, all on their way at once.
 // Bounded by HBM: both are read once (26 us for 8192 tokens of 32 heads of 128 channels, 5.2 TB/s).
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant__ PBwdParams p) {
+__global__ void __launch_bounds__(256, D == 64 ? 6 : 4) packed_stats_kernel(const __grid_constant__ PBwdParams p) {
   constexpr int L = D / 8, RW = 32 / L, kRows = 8, kSteps = kRows / RW;
   const PackHeader* h = reinterpret_cast<const PackHeader*>(p.plan);
   const int status = bwd_plan_status(p);
@@ -94,23 +131,68 @@ __global__ void __launch_bounds__(256) packed_stats_kernel(const __grid_constant
         lse[i] = p.lse[static_cast<long long>(t.x + tok) * p.Hq + qh];
       }
     }
+    float block = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-      float s = 0.f;
+      float s = 0.f, sq = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 x = c4_unpack<F16>(aw[k]), y = c4_unpack<F16>(bw[k]);
         s = fmaf(x.x, y.x, fmaf(x.y, y.y, s));
+        if (F16) sq = fmaf(y.x, y.x, fmaf(y.y, y.y, sq));
       }
 #pragma unroll
       for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (F16 && lse[i] != -INFINITY) block += finite_or_zero(sq);
       if (ch == 0) {
         const long long at = static_cast<long long>(unit) * kRows + i * RW + lane / L;
         // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
-        p.stats[at] = lse[i] == -INFINITY ? -INFINITY : -(lse[i] * kPackLog2e);
+        p.stats[at] = lse[i] == -INFINITY ? -INFINITY : F16 ? fmaf(-lse[i], kPackLog2e, static_cast<float>(kPUp)) : -(lse[i] * kPackLog2e);
         p.stats[n + at] = lse[i] == -INFINITY ? 0.f : -s;
       }
+    }
+    if (F16) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) block += __shfl_xor_sync(0xffffffffu, block, o);
+      if (lane == 0) p.stats[2 * n + unit] = block;
+    }
+  }
+  if (F16) {  // 16 rows of a key tile of V a warp at a time
+    constexpr int kVRows = kTile / kVUnits, kVSteps = kVRows / RW;
+    const PackEntry* const tiles_v = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDkv]);
+    float* const big_v = p.stats + 2 * n + units;
+    const long long n_v = static_cast<long long>(h->n_entries[kListDkv]) * p.Hkv * kVUnits;
+    // (counted from the grid's middle: in small calls by CTAs that have nothing to do above and run at the same time)
+    for (long long x = ((blockIdx.x + gridDim.x / 2) % gridDim.x) * (blockDim.x / 32) + (threadIdx.x >> 5); x < n_v; x += step) {
+      const int piece = static_cast<int>(x % kVUnits);
+      const uint32_t pair = static_cast<uint32_t>(x / kVUnits);  // (entries x heads: below 2^31)
+      const PackEntry& e = tiles_v[pair / p.Hkv];
+      const int head = static_cast<int>(pair % p.Hkv), n_tok = __ldg(&e.n_tok), k0 = __ldg(&e.k0), diag = __ldg(&e.diag);
+      if (__ldg(&e.chunk) != 0) continue;  // (the first chunk does it)
+      uint4 a[kVSteps];
+#pragma unroll
+      for (int i = 0; i < kVSteps; ++i) {
+        const int row = piece * kVRows + i * RW + lane / L;
+        a[i] = row < n_tok ? *reinterpret_cast<const uint4*>(p.v + static_cast<long long>(k0 + row) * p.vt + head * p.vh + ch * 8) : make_uint4(0, 0, 0, 0);
+      }
+      float longest = 0.f;
+#pragma unroll
+      for (int i = 0; i < kVSteps; ++i) {
+        const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+        float sq = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = c4_unpack<F16>(aw[k]);
+          sq = fmaf(y.x, y.x, fmaf(y.y, y.y, sq));
+        }
+#pragma unroll
+        for (int o = L / 2; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        longest = fmaxf(longest, finite_or_zero(sq));
+      }
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+      if (lane == 0) big_v[(pack_key_tile(k0 - diag, __ldg(&e.seq), diag / kTile) * p.Hkv + head) * kVUnits + piece] = longest;
     }
   }
   grid_release();
@@ -131,7 +213,8 @@ struct __align__(1024) DqSmem {
   PackEntry item[kSlots];
   uint64_t q_full[kQs], q_empty[kQs], k_full[kKs], k_empty[kKs], v_full[kVs], v_empty[kVs];
   uint64_t s_full, s_free, dp_full, dp_free, ds_full[2], ds_free[2], dq_full, dq_empty, tail, drain;
-  uint64_t item_full[kSlots], item_empty[kSlots];
+  uint64_t item_full[kSlots], item_empty[kSlots], v_known[kSlots];
+  float v_longest[kSlots];  // fp16: squared length of the longest V row that the item meets
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -172,7 +255,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     mbar_init(&sm.ds_full[1], kSoftWarps), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
     mbar_init(&sm.ds_free[0], 1), mbar_init(&sm.ds_free[1], 1);
     mbar_init(&sm.dq_full, 1), mbar_init(&sm.dq_empty, kSoftWarps), mbar_init(&sm.tail, 1), mbar_init(&sm.drain, 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
+    for (int s = 0; s < kSlots; ++s)
+      mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps + (F16 ? 1 : 0)), mbar_init(&sm.v_known[s], 1);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
@@ -325,6 +409,20 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_commit(&sm.drain);
         mbar_wait_drain(&sm.drain, 0, p.status);
       }
+    } else if (F16 && warp == 2) {
+      // ---------------------------------------------------------- the longest V rows, ahead of the softmax
+      const float* const big_v = p.stats + 2 * n_stats + n_stats / (kTile / kDoUnits);
+      for (int it = 0;; ++it) {
+        const int slot = it % kSlots;
+        if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+        const PackEntry& e = sm.item[slot];
+        if (e.head < 0) break;
+        const float v2 = warp_largest<kVUnits>(big_v + (pack_key_tile(e.k0, e.seq, e.a) * p.Hkv + e.head) * kVUnits,
+                                               static_cast<long long>(p.Hkv) * kVUnits, e.b - e.a, lane);
+        if (lane == 0) sm.v_longest[slot] = v2;
+        warp_arrive(&sm.v_known[slot]);
+        warp_arrive(&sm.item_empty[slot]);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -343,7 +441,14 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const bool valid = r_tok < n_tok;
       const int hi = valid ? first + r_tok : -1;
       const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
-      const float nl = p.stats[at], nd = p.stats[n_stats + at];
+      float nl = p.stats[at], down = 1.f;
+      const float nd = p.stats[n_stats + at];
+      if (F16) {  // dS is held times 2^k = 1 / down: a row's own, in its exponent, from which P's 2^10 is taken again
+        const float o2 = __ldcg(p.stats + 2 * n_stats + at / (kTile / kDoUnits));
+        if (!warp_wait(&sm.v_known[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+        const int k = ds_up(o2, sm.v_longest[slot]);
+        nl += static_cast<float>(k - kPUp), down = pow2(-k);
+      }
       auto tile = [&](auto may_mask, bool masked, int j) -> bool {
         uint32_t sr[64], dr[64];
         if (!warp_wait(&sm.dp_full, n & 1, abort_flag, p.status)) return false;
@@ -438,17 +543,22 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tc_fence_before();
         warp_arrive(&sm.dq_empty);
       }
+      float f[2] = {1.f, 1.f};
+      if (F16) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) f[u] = __shfl_sync(0xffffffffu, down, (row + 8 * u) & 31);
+      }
       if (e.slot >= 0) {  // this chunk's share, for the join behind this kernel
         float* const mine = p.part_q + (static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * kTile * D;
 #pragma unroll
-        for (int c = 0; c < D; c += 32) leave_part<D>(mine + c, acc[c / 32], row);
+        for (int c = 0; c < D; c += 32) leave_part<D, F16>(mine + c, acc[c / 32], row, f);
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int tk = (row + 8 * u) / p.G, qh = head * p.G + row + 8 * u - tk * p.G;
           uint16_t* const to = p.dq + static_cast<long long>(e.q0 + tk) * p.dqt + qh * p.dqh;
 #pragma unroll
-          for (int c = 0; c < D; c += 32) quad_store<F16>(to + c, tk < n_tok, acc[c / 32], u, p.scale);
+          for (int c = 0; c < D; c += 32) quad_store<F16>(to + c, tk < n_tok, acc[c / 32], u, p.scale * f[u]);
         }
       }
       warp_arrive(&sm.item_empty[slot]);
@@ -491,9 +601,10 @@ struct __align__(1024) DkvSmem {
   alignas(16) float nd[kStatStages][kTile];
   PackEntry item[kSlots];
   uint64_t k_full[kKs], k_empty[kKs], q_full[kQs], q_empty[kQs], do_full[kOs], do_empty[kOs];
-  uint64_t st_full[kStatStages], st_empty[kStatStages];
+  uint64_t st_full[kStatStages], st_empty[kStatStages], st_raw[kStatStages];
   uint64_t s_full, s_free, dp_full, dp_free, p_full, ds_full, pd_free, acc_full, acc_empty, tail[2], drain;
-  uint64_t item_full[kSlots], item_empty[kSlots];
+  uint64_t item_full[kSlots], item_empty[kSlots], up_known[kSlots];
+  int up[kSlots];  // fp16: k of the item
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -527,12 +638,13 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     for (int s = 0; s < kKs; ++s) mbar_init(&sm.k_full[s], 1), mbar_init(&sm.k_empty[s], 1);
     for (int s = 0; s < kQs; ++s) mbar_init(&sm.q_full[s], 1), mbar_init(&sm.q_empty[s], 1);
     for (int s = 0; s < kOs; ++s) mbar_init(&sm.do_full[s], 1), mbar_init(&sm.do_empty[s], 1);
-    for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_empty[s], kSoftWarps);
+    for (int s = 0; s < kStatStages; ++s) mbar_init(&sm.st_full[s], 1), mbar_init(&sm.st_raw[s], 1), mbar_init(&sm.st_empty[s], kSoftWarps);
     mbar_init(&sm.s_full, 1), mbar_init(&sm.s_free, kSoftWarps), mbar_init(&sm.dp_full, 1), mbar_init(&sm.dp_free, kSoftWarps);
     mbar_init(&sm.p_full, kSoftWarps), mbar_init(&sm.ds_full, kSoftWarps), mbar_init(&sm.pd_free, 1);
     mbar_init(&sm.acc_full, 1), mbar_init(&sm.acc_empty, kSoftWarps);
     mbar_init(&sm.tail[0], 1), mbar_init(&sm.tail[1], 1), mbar_init(&sm.drain, 1);
-    for (int s = 0; s < kSlots; ++s) mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps);
+    for (int s = 0; s < kSlots; ++s)
+      mbar_init(&sm.item_full[s], 1), mbar_init(&sm.item_empty[s], 1 + kSoftWarps + (F16 ? 1 : 0)), mbar_init(&sm.up_known[s], 1);
     sm.abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q), tma_prefetch_desc(&tm_k), tma_prefetch_desc(&tm_v), tma_prefetch_desc(&tm_do);
@@ -554,6 +666,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       int k_it = 0, q_it = 0, do_it = 0, st_it = 0, tails[2] = {0, 0}, unmarked[2] = {-1, -1};
+      uint64_t* const st_land = F16 ? sm.st_raw : sm.st_full;
       bool ok = true;
       // Q or dO tile of query tile i into its ring; rows behind the sequence's
       // last, up to the last MMA step's end, become zero
@@ -615,9 +728,9 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           if (!ok) break;
           if (lane == 0) {
             const float* const st = p.stats + (static_cast<long long>(e.tile0 + i) * p.Hkv + head) * kTile;
-            mbar_arrive_expect_tx(&sm.st_full[s], 2 * kTile * 4);
-            bulk_load(sm.nl[s], st, kTile * 4, &sm.st_full[s]);
-            bulk_load(sm.nd[s], st + n_stats, kTile * 4, &sm.st_full[s]);
+            mbar_arrive_expect_tx(&st_land[s], 2 * kTile * 4);
+            bulk_load(sm.nl[s], st, kTile * 4, &st_land[s]);
+            bulk_load(sm.nd[s], st + n_stats, kTile * 4, &st_land[s]);
           }
           ++st_it;
           if (i == a) work.next(p.counter, lane);  // (under the loads)
@@ -632,7 +745,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         for (int d = 1; d <= kOs && d <= do_it; ++d)
           if (do_it - d != unmarked[1]) mbar_wait_drain(&sm.do_full[(do_it - d) % kOs], ((do_it - d) / kOs) & 1, p.status);
         for (int d = 1; d <= kStatStages && d <= st_it; ++d)
-          mbar_wait_drain(&sm.st_full[(st_it - d) % kStatStages], ((st_it - d) / kStatStages) & 1, p.status);
+          mbar_wait_drain(&st_land[(st_it - d) % kStatStages], ((st_it - d) / kStatStages) & 1, p.status);
         for (int d = 1; d <= kKs && d <= k_it; ++d) mbar_wait_drain(&sm.k_full[(k_it - d) % kKs], ((k_it - d) / kKs) & 1, p.status);
       }
     } else if (warp == 1) {
@@ -714,6 +827,39 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         tc_commit(&sm.drain);
         mbar_wait_drain(&sm.drain, 0, p.status);
       }
+    } else if (F16 && warp == 2) {
+      // ---------------------------------------------------------- what dS is held times, and -delta times that, ahead of the
+      // softmax (which did both by itself at first: 244 us instead of 219 unscaled for 9 texts of 101 to 3501 tokens, 12 heads
+      // over 4 of 64 channels)
+      const float* const big_do = p.stats + 2 * n_stats;
+      const float* const big_v = big_do + n_stats / (kTile / kDoUnits);
+      int t = 0;
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        const int slot = it % kSlots;
+        if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+        const PackEntry& e = sm.item[slot];
+        if (e.head < 0) break;
+        // (a key tile's numbers come together with the first of the queries')
+        const float v = __ldcg(big_v + (pack_key_tile(e.k0 - e.diag, e.seq, e.diag / kTile) * p.Hkv + e.head) * kVUnits + lane % kVUnits);
+        const float o2 = warp_largest<kDoUnits>(big_do + (static_cast<long long>(e.tile0 + e.a) * p.Hkv + e.head) * kDoUnits,
+                                                static_cast<long long>(p.Hkv) * kDoUnits, e.b - e.a, lane);
+        const float v2 = __int_as_float(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(v))));
+        const int k = ds_up(o2, v2);
+        const float up = pow2(k - kPUp);
+        if (lane == 0) sm.up[slot] = k;
+        warp_arrive(&sm.up_known[slot]);
+        for (int i = e.a; i < e.b && ok; ++i, ++t) {
+          const int ss = t % kStatStages;
+          ok = warp_wait(&sm.st_raw[ss], (t / kStatStages) & 1, abort_flag, p.status);
+          if (!ok) break;
+          float4& d = *reinterpret_cast<float4*>(&sm.nd[ss][4 * lane]);
+          d.x *= up, d.y *= up, d.z *= up, d.w *= up;
+          fence_proxy_async_smem();  // (the next copy writes there)
+          warp_arrive(&sm.st_full[ss]);
+        }
+        warp_arrive(&sm.item_empty[slot]);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -729,6 +875,12 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       const int head = e.head;
       if (head < 0) break;
       const int a = e.a, b = e.b, n_tok = e.n_tok, key = e.diag + r;
+      float up = 1.f, down = 1.f;  // fp16: dS is held times 2^k = 1 / down, P times 2^10
+      if (F16) {
+        if (!warp_wait(&sm.up_known[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
+        const int k = sm.up[slot];
+        up = pow2(k - kPUp), down = pow2(-k);
+      }
       auto tile = [&](auto may_mask, bool masked, int i) -> bool {
         const int ss = t % kStatStages;
         const uint32_t s_at = lanes + s_col, dp_at = lanes + (s_col ^ 128u);
@@ -742,7 +894,12 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
           for (int c = 0; c < 64; c += 2) w[c >> 1] &= bit_pair(bits[c >> 5], c & 31);
         };
-        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2), up2 = f2(up, up);
+        // dP - delta, for fp16 times up (and so is -delta in nd)
+        auto centred = [&](uint32_t x0, uint32_t x1, float d0, float d1) {
+          const uint64_t x = f2(__uint_as_float(x0), __uint_as_float(x1)), d = f2(d0, d1);
+          return F16 ? fma2(x, up2, d) : add2(x, d);
+        };
         if constexpr (kOwn) {
           uint32_t x[64], y[64], ps[32], ds[32];
           if (!warp_wait(&sm.s_full, t & 1, abort_flag, p.status)) return false;
@@ -767,8 +924,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll
             for (int k = 0; k < 4; ++k) z[k] = ex2_approx(z[k]);
             ps[c >> 1] = c4_pack<F16>(z[0], z[1]), ps[(c >> 1) + 1] = c4_pack<F16>(z[2], z[3]);
-            f2_split(mul2(f2(z[0], z[1]), add2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), f2(d4.x, d4.y))), z[0], z[1]);
-            f2_split(mul2(f2(z[2], z[3]), add2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), f2(d4.z, d4.w))), z[2], z[3]);
+            f2_split(mul2(f2(z[0], z[1]), centred(y[c], y[c + 1], d4.x, d4.y)), z[0], z[1]);
+            f2_split(mul2(f2(z[2], z[3]), centred(y[c + 2], y[c + 3], d4.z, d4.w)), z[2], z[3]);
             ds[c >> 1] = c4_pack<F16>(z[0], z[1]), ds[(c >> 1) + 1] = c4_pack<F16>(z[2], z[3]);
           }
           warp_arrive(&sm.st_empty[ss]);
@@ -820,8 +977,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           for (int c = 0; c < 64; c += 4) {
             const float4 d4 = *reinterpret_cast<const float4*>(&sm.nd[ss][col0 + c]);
             float y[4];
-            f2_split(mul2(pr[c >> 1], add2(f2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2(d4.x, d4.y))), y[0], y[1]);
-            f2_split(mul2(pr[(c >> 1) + 1], add2(f2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2(d4.z, d4.w))), y[2], y[3]);
+            f2_split(mul2(pr[c >> 1], centred(x[c], x[c + 1], d4.x, d4.y)), y[0], y[1]);
+            f2_split(mul2(pr[(c >> 1) + 1], centred(x[c + 2], x[c + 3], d4.z, d4.w)), y[2], y[3]);
             pk[c >> 1] = c4_pack<F16>(y[0], y[1]), pk[(c >> 1) + 1] = c4_pack<F16>(y[2], y[3]);
           }
           warp_arrive(&sm.st_empty[ss]);
@@ -869,12 +1026,14 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // the first warpgroup writes dV, the second dK, 16 rows of a warp's 32 at a time
       const int row = quarter * 32 + (lane >> 2);
       const uint32_t from = lanes + (wg ? colDK : colDV);
+      const float back = !F16 ? 1.f : wg ? down : pow2(-kPUp);
+      const float f[2] = {back, back};
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
         const uint32_t at = from + (static_cast<uint32_t>(hf * 16) << 16);
         if (e.slot >= 0) {  // this chunk's share, for the join behind these kernels
           float* const mine = p.part + ((static_cast<long long>(e.slot + e.chunk) * p.Hkv + head) * 2 + wg) * kTile * D;
-          quad_blocks<D>(at, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D>(mine + c, acc, row + 16 * hf); });
+          quad_blocks<D>(at, a < b, [&](int c, const uint32_t(&acc)[16]) { leave_part<D, F16>(mine + c, acc, row + 16 * hf, f); });
           continue;
         }
         uint16_t* to[2];
@@ -888,7 +1047,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         quad_blocks<D>(at, a < b, [&](int c, const uint32_t(&acc)[16]) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) quad_store<F16>(to[u] + c, live[u], acc, u, wg ? p.scale : 1.f);
+          for (int u = 0; u < 2; ++u) quad_store<F16>(to[u] + c, live[u], acc, u, wg ? p.scale * back : back);
         });
       }
       if (a < b) {
@@ -970,6 +1129,7 @@ extern "C" scfa_status scfa_packed_bwd(const uint16_t* q, long long q_token, lon
   p.plan = static_cast<const char*>(plan), p.plan_bytes = static_cast<long long>(plan_bytes);
   p.N = N, p.M = M, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.tpt = kTile / p.G, p.scale = scale, p.scale_log2 = factor;
   p.o = o, p.ot = o_token, p.oh = o_head, p.dO = dO, p.dot = do_token, p.doh = do_head, p.lse = lse;
+  p.v = v, p.vt = v_token, p.vh = v_head;
   p.dq = dq, p.dqt = dq_token, p.dqh = dq_head, p.dk = dk, p.dkt = dk_token, p.dkh = dk_head, p.dv = dv, p.dvt = dv_token, p.dvh = dv_head;
   p.counter = reinterpret_cast<int*>(c + w.counters);
   p.part = reinterpret_cast<float*>(c + w.part), p.part_q = reinterpret_cast<float*>(c + w.part_q), p.stats = reinterpret_cast<float*>(c + w.stats);

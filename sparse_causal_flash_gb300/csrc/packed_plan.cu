@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     int a, b;
     tile_range(list, i, nq, m, p.tpt, p.window, a, b);
     PackEntry e = {};
-    e.shift = m - nq, e.chunks = n;
+    e.shift = m - nq, e.chunks = n, e.seq = r;
     if (list == kListDkv) {
       e.q0 = q0, e.k0 = k0 + i * kTile, e.n_tok = min(kTile, m - i * kTile), e.diag = i * kTile, e.m = nq;
       e.tile0 = pre_q[r];
@@ -306,7 +306,7 @@ size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int
   const PackWs w = pack_ws(D, sms);
   if (!backward) return w.forward;
   const int tpt = kTile / (Hq / Hkv);
-  return align_up(w.stats + static_cast<size_t>((N / tpt + static_cast<long long>(R)) * pack_stats_tile_bytes(Hkv)), 256);
+  return align_up(w.stats + static_cast<size_t>(pack_stats_bytes(N / tpt + static_cast<long long>(R), M, R, Hkv)), 256);
 }
 
 }  // extern "C"

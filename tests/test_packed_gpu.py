@@ -591,3 +591,46 @@ def test_step_refuses_what_does_not_fit(scfa):
     expanded = x[:1, :2].expand(8, 2, 64)  # rows that are one row: strides of zero
     with pytest.raises(scfa.ScfaError):
         plain.forward(expanded, k, v, 0.1)
+
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size,v_up,scale", [(4e3, 8.0, 0.5), (1e-3, 1.0, 8.0), (1e-4, 1.0, 8.0), (1e-3, 0.01, 8.0)])
+@pytest.mark.parametrize("lens,Hq,Hkv,window", [([(1500, 1500), (3, 3)], 2, 1, 0), ([(5, 9000)], 4, 1, 0),
+                                                ([(700, 700)], 3, 3, 300)])
+def test_fp16_gradients_of_any_size(scfa, monkeypatch, lens, Hq, Hkv, window, D, size, v_up, scale):
+    """Flat rows over many keys: weights times (dP - delta) lie far below fp16's smallest number, or with a large dO above
+    its largest, where the gradients themselves do not. P is held times 2^10 and dS times 2^k with 2^k |dO| |V| >= 2^10.5 for
+    the longest rows of a piece of work: a rounding below the normal numbers moves P by at most 2^-35 and dS by at most
+    2^-25 / 2^k <= 2^-35.5 |dO| |V|."""
+    p = Problem(scfa, lens, Hq, Hkv, D, HF, window, seed=22, q_scale=0.1)
+    p.k.mul_(0.1)
+    p.v.mul_(v_up)
+    p.do.copy_((p.do.float() * size).to(HF))
+    p.scale = scale
+    p.forward()
+    p.backward()
+    assert p.status() == 0
+    norms = [float(torch.linalg.vector_norm(t.double(), dim=-1).max()) for t in (p.do, p.v)]
+    monkeypatch.setitem(globals(), "tiny", lambda dt: 2.0 ** -35 + 2.0 ** -35.5 * norms[0] * norms[1])
+    p.check_backward()
+
+
+def test_fp16_gradients_beside_rows_that_are_not_finite(scfa):
+    """A row of dO or v that is not finite leaves other sequences' bits alone, and the scale of its own as it is."""
+    p, r = (Problem(scfa, same([90, 150, 33]), 4, 2, 64, HF, seed=23) for _ in range(2))
+    for x in (p, r):
+        x.do.mul_(1e-3)
+        x.forward()
+    r.do[100, 1, 5], r.do[200, 3, 0] = float("inf"), float("nan")
+    for x in (p, r):
+        x.backward()
+        assert x.status() == 0
+    for a, b in ((slice(0, 90), slice(0, 90)), (slice(240, 273), slice(240, 273))):
+        assert all(torch.equal(getattr(p, key)[a], getattr(r, key)[a]) for key in ("dq", "dk", "dv"))
+    for t, h in ((100, 1), (200, 3)):
+        assert not torch.isfinite(r.dq[t, h]).any()
+    ok = torch.ones(150, dtype=torch.bool, device="cuda")
+    ok[[10, 110]] = False
+    assert torch.isfinite(r.dq[90:240][ok]).all()
+    assert float((p.dq[90:240][ok].double() - r.dq[90:240][ok].double()).abs().max()) <= float(p.dq.abs().max()) * 2.0 ** -9
