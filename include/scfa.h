@@ -499,6 +499,10 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  *   several at once; it holds the starts itself. Starts that fall, or lie
  *   outside [0, N] or [0, M], raise SCFA_ERR_INVALID in the plan's status word,
  *   and in that of every call with the plan, which then computes nothing.
+ * scfa_packed_plan_self: the plan of a batch whose queries and keys are the same N
+ *   rows from row 0 on; start[0] other than 0 is refused as above. The int at byte
+ *   4 of the plan says how many rows belong to sequences (0 if refused): what
+ *   scfa_rope_fwd and scfa_rope_bwd take as `count`.
  * scfa_packed_fwd: o [N][Hq][D], lse [N][Hq] fp32, natural log.
  * scfa_packed_bwd: from the forward's q, k, v, o, lse and do [N][Hq][D], the
  *   gradients dq [N][Hq][D], dk, dv [M][Hkv][D]; those of a key head are the sums
@@ -524,6 +528,8 @@ size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int
 scfa_status scfa_packed_plan(const int32_t* q_start, const int32_t* k_start, int N, int M, int R,
                              int Hq, int Hkv, int window, void* plan, size_t plan_bytes,
                              void* stream);
+scfa_status scfa_packed_plan_self(const int32_t* start, int N, int R, int Hq, int Hkv, int window,
+                                  void* plan, size_t plan_bytes, void* stream);
 scfa_status scfa_packed_fwd(const uint16_t* q, long long q_token, long long q_head,
                             const uint16_t* k, long long k_token, long long k_head,
                             const uint16_t* v, long long v_token, long long v_head,

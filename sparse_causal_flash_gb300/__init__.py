@@ -85,6 +85,7 @@ _SIGS = {
     "scfa_packed_plan_size": ([_I] * 5, _S),
     "scfa_packed_workspace_size": ([_I] * 7, _S),
     "scfa_packed_plan": ([_P, _P] + [_I] * 6 + [_P, _S, _P], _I),
+    "scfa_packed_plan_self": ([_P] + [_I] * 5 + [_P, _S, _P], _I),
     "scfa_packed_bwd": ([_P, _L, _L] * 4 + [_P] + [_P, _L, _L] + [_P, _S] + [_I] * 5 + [_F, _I] + [_P, _L, _L] * 3
                         + [_P, _S, _U, _P], _I),
     "scfa_packed_fwd": ([_P, _L, _L] * 3 + [_P, _S] + [_I] * 5 + [_F, _I, _P, _L, _L, _P, _P, _S, _U, _P], _I),
@@ -567,6 +568,16 @@ def scfa_packed_plan(q_start, k_start, N, M, Hq, Hkv, window, plan, stream=None)
         _refuse("scfa_packed_plan", dev, q_start=(q_start, _i32, R + 1), k_start=(k_start, _i32, R + 1))
     _launch("scfa_packed_plan", dev, stream, q_start.data_ptr(), k_start.data_ptr(), N, M, R, Hq, Hkv, window,
             plan.data_ptr(), _ws_bytes("scfa_packed_plan", plan, dev))
+
+
+def scfa_packed_plan_self(start, N, Hq, Hkv, window, plan, stream=None):
+    """The same for sequences whose queries and keys are the same N rows, from row 0 on (start[0] is 0). plan[4:8], as int32,
+    is then the number of rows that belong to sequences, 0 for a batch that is refused: a `count` for scfa_rope_fwd."""
+    R, dev = start.numel() - 1, start.get_device()
+    if not (dev >= 0 and _is(start, _i32, dev, R + 1)):
+        _refuse("scfa_packed_plan_self", dev, start=(start, _i32, R + 1))
+    _launch("scfa_packed_plan_self", dev, stream, start.data_ptr(), N, R, Hq, Hkv, window, plan.data_ptr(),
+            _ws_bytes("scfa_packed_plan_self", plan, dev))
 
 
 def scfa_packed_fwd(q, k, v, plan, scale, o, lse, ws, flags=0, stream=None):

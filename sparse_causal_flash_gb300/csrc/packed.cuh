@@ -49,6 +49,7 @@ static_assert(sizeof(PackEntry) == 64, "entries are copied as 16 words");
 
 struct PackHeader {
   int status;  // SCFA_OK or what is wrong with the sequences
+  int rows;    // (at byte 4, as the interface says) where the last sequence's queries end; 0 for a batch that is refused
   uint32_t magic;
   int N, M, R, Hq, Hkv, window;
   int n_entries[kLists];
@@ -60,7 +61,7 @@ struct PackHeader {
   long long cuts[kLists];     // PackEntry: the first chunk of each cut one
   long long qtiles;           // int4 (first token, tokens, last key of the first token, 0) of each query tile
   long long bytes;
-  int pad[28];
+  int pad[26];
 };
 static_assert(sizeof(PackHeader) == 256, "the plan's header");
 

@@ -27,6 +27,7 @@ struct PlanArgs {
   char* plan;
   PackPlanLayout L;
   int N, M, R, Hq, Hkv, tpt, window, sms;
+  bool from_0;  // the first sequence has to start at row 0
 };
 
 // inclusive scan over the CTA; `total` is the sum
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   if (tid < kCandidates) s_big[tid] = s_cut[tid] = 0, s_work[tid] = 0;
   s_bin[tid] = 0;
   __syncthreads();
-  bool bad = false;
+  bool bad = p.from_0 && p.q_start[0] != 0;
   for (int r = tid; r < p.R; r += kPlanThreads) {
     const int a = p.q_start[r], b = p.q_start[r + 1], c = p.k_start[r], d = p.k_start[r + 1];
     bad |= a < 0 || b < a || b > p.N || c < 0 || d < c || d > p.M;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
     if (list == 0) {
       h->magic = kPackMagic, h->N = p.N, h->M = p.M, h->R = p.R, h->Hq = p.Hq, h->Hkv = p.Hkv, h->window = p.window;
       h->qtiles = static_cast<long long>(p.L.qtiles), h->bytes = static_cast<long long>(p.L.total);
-      h->status = refused ? SCFA_ERR_INVALID : SCFA_OK;
+      h->status = refused ? SCFA_ERR_INVALID : SCFA_OK, h->rows = refused ? 0 : p.q_start[p.R];
     }
     h->entries[list] = static_cast<long long>(p.L.entries[list]), h->cuts[list] = static_cast<long long>(p.L.cuts[list]);
     h->n_cuts[list] = 0;
@@ -272,6 +273,21 @@ __global__ void __launch_bounds__(kPlanThreads) pack_plan_kernel(const PlanArgs 
   }
 }
 
+scfa_status launch_plan(const int32_t* q_start, const int32_t* k_start, int N, int M, int R, int Hq, int Hkv, int window, bool from_0,
+                        void* plan, size_t plan_bytes, void* stream) {
+  if (!q_start || !k_start || !plan || N < 0 || M < 0 || R < 1 || window < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
+    return SCFA_ERR_INVALID;
+  PlanArgs p = {};
+  p.sms = num_sms();
+  if (!pack_plan_layout(N, M, R, Hq, Hkv, p.sms, &p.L)) return SCFA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < p.L.total) return SCFA_ERR_WORKSPACE;
+  p.q_start = q_start, p.k_start = k_start, p.plan = static_cast<char*>(plan);
+  p.N = N, p.M = M, p.R = R, p.Hq = Hq, p.Hkv = Hkv, p.tpt = kTile / (Hq / Hkv), p.from_0 = from_0;
+  p.window = window < M ? window : 0;  // (one as wide as all keys hides none, and sums with it might leave 32 bits)
+  pack_plan_kernel<<<kLists, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace scfa
 
@@ -286,17 +302,12 @@ size_t scfa_packed_plan_size(int N, int M, int R, int Hq, int Hkv) {
 
 scfa_status scfa_packed_plan(const int32_t* q_start, const int32_t* k_start, int N, int M, int R, int Hq, int Hkv, int window,
                              void* plan, size_t plan_bytes, void* stream) {
-  if (!q_start || !k_start || !plan || N < 0 || M < 0 || R < 1 || window < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
-    return SCFA_ERR_INVALID;
-  PlanArgs p = {};
-  p.sms = num_sms();
-  if (!pack_plan_layout(N, M, R, Hq, Hkv, p.sms, &p.L)) return SCFA_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(plan) & 255u) || plan_bytes < p.L.total) return SCFA_ERR_WORKSPACE;
-  p.q_start = q_start, p.k_start = k_start, p.plan = static_cast<char*>(plan);
-  p.N = N, p.M = M, p.R = R, p.Hq = Hq, p.Hkv = Hkv, p.tpt = kTile / (Hq / Hkv);
-  p.window = window < M ? window : 0;  // (one as wide as all keys hides none, and sums with it might leave 32 bits)
-  pack_plan_kernel<<<kLists, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SCFA_OK : SCFA_ERR_CUDA;
+  return launch_plan(q_start, k_start, N, M, R, Hq, Hkv, window, false, plan, plan_bytes, stream);
+}
+
+scfa_status scfa_packed_plan_self(const int32_t* start, int N, int R, int Hq, int Hkv, int window, void* plan, size_t plan_bytes,
+                                  void* stream) {
+  return launch_plan(start, start, N, N, R, Hq, Hkv, window, true, plan, plan_bytes, stream);
 }
 
 size_t scfa_packed_workspace_size(int backward, int N, int M, int R, int Hq, int Hkv, int D) {

@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import (packed_plan_size, packed_workspace_size, scfa_get_device_status, scfa_packed_bwd, scfa_packed_fwd,
-               scfa_packed_plan, workspace)
+               scfa_packed_plan_self, workspace)
 
 
 class PackedStep:
@@ -47,8 +47,8 @@ class PackedStep:
         if norm:
             self.dwq, self.dwk = (torch.zeros(D, dtype=torch.float32, device=dev) for _ in range(2))
             self.ws_rope = rope.workspace(N, Hq, Hkv, D)
-        self.count = torch.zeros(1, dtype=torch.int32, device=dev)  # tokens of the batch
         self.plan_buf = workspace(nbytes, dev)
+        self.count = self.plan_buf[4:8].view(torch.int32)  # tokens of the batch, by the plan; 0 if it is refused
         self.ws = workspace(nws, dev)
         for b in (self.plan_buf, self.ws):
             b[:4].zero_()  # the status word: nothing has run yet
@@ -56,12 +56,11 @@ class PackedStep:
     def plan(self, starts, stream=None):
         """The batch's sequences: starts [R + 1] int32, from 0; tokens starts[r] .. starts[r + 1] are sequence r (a shorter
         batch repeats its end). To be called before the first step and whenever `starts` changes; one plan serves any
-        number of layers' steps."""
+        number of layers' steps. Starts that fall, leave the N rows or do not begin at 0 show in status(), and steps
+        then write no row (dwq and dwk, sums over no rows, become zero)."""
         if starts.numel() != self.R + 1:
             raise ValueError(f"PackedStep.plan: {self.R + 1} starts expected, got {starts.numel()}")
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
-            self.count.copy_(starts[-1:])
-        scfa_packed_plan(starts, starts, self.N, self.N, self.Hq, self.Hkv, self.window, self.plan_buf, stream)
+        scfa_packed_plan_self(starts, self.N, self.Hq, self.Hkv, self.window, self.plan_buf, stream)
 
     def _args(self, pos, wq, wk):
         if (pos is None) != (self.rope is None):

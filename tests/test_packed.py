@@ -141,3 +141,17 @@ def test_binding_refuses_before_any_launch(scfa):
     for kw in (dict(Hq=3, Hkv=2), dict(D=96), dict(N=0), dict(R=0), dict(dtype=torch.float32), dict(norm=True)):
         with pytest.raises(ValueError):
             PackedStep(**{**dict(N=8, R=1, Hq=4, Hkv=2, D=64), **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(qs=None), 1), (dict(plan=None), 1), (dict(N=-1), 1), (dict(R=0), 1), (dict(window=-1), 1), (dict(Hkv=0), 1),
+    (dict(Hq=3), 1), (dict(Hq=258), 2), (dict(nb=100), 3), (dict(plan=ctypes.c_void_p(4160)), 3), (dict(N=2 ** 31 - 1, Hq=256), 2)])
+def test_self_plan_refusals(scfa, kw, code):
+    a = dict(qs=FAKE, N=8, R=2, Hq=4, Hkv=2, window=0, plan=FAKE, nb=1 << 26, st=None)
+    a.update(kw)
+    assert scfa._lib.scfa_packed_plan_self(*a.values()) == code
+
+
+def test_self_plan_binding_refuses_cpu_tensors(scfa):
+    with pytest.raises(ValueError, match="CUDA"):
+        scfa.scfa_packed_plan_self(torch.zeros(3, dtype=torch.int32), 4, 2, 2, 0, torch.zeros(1 << 20, dtype=torch.uint8))

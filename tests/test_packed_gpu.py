@@ -634,3 +634,34 @@ def test_fp16_gradients_beside_rows_that_are_not_finite(scfa):
     ok[[10, 110]] = False
     assert torch.isfinite(r.dq[90:240][ok]).all()
     assert float((p.dq[90:240][ok].double() - r.dq[90:240][ok].double()).abs().max()) <= float(p.dq.abs().max()) * 2.0 ** -9
+
+
+# ---------------------------------------------------------------- steps: batches that are refused, plans that are shared
+def packed_step(N=40, R=2, Hq=4, Hkv=2, D=64, **kw):
+    from sparse_causal_flash_gb300.packed import PackedStep
+    from sparse_causal_flash_gb300.rope import Rope
+    st = PackedStep(N, R, Hq, Hkv, D, rope=Rope(D), norm=True, **kw)
+    x = rand(1, (N, Hq + 2 * Hkv, D))
+    args = (x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], rand(2, (N, Hq, D)), 0.125, i32(np.arange(N)),
+            torch.ones(D, device="cuda"), torch.ones(D, device="cuda"))
+    return st, args
+
+
+@pytest.mark.parametrize("starts", [[0, 30, 20], [0, 30, 41], [-1, 20, 40], [3, 20, 40], [40, 40, 40], [2 ** 31 - 1] * 3])
+def test_step_leaves_gradients_of_a_refused_batch_alone(scfa, starts):
+    """Starts that fall or leave the rows, or do not begin at 0: the status says so, and no row is written or turned."""
+    st, args = packed_step()
+    st.plan(i32([0, 20, 40]))
+    st.run(*args)
+    assert st.status() == 0
+    first = st.dqkv.clone(), st.o.clone(), st.lse.clone()
+    st.plan(i32(starts))
+    for _ in range(2):
+        st.run(*args)
+        assert st.status() == 1
+        assert all(torch.equal(a, b) for a, b in zip(first, (st.dqkv, st.o, st.lse)))
+        assert not st.dwq.any() and not st.dwk.any()  # sums over no rows
+    st.plan(i32([0, 20, 40]))
+    st.run(*args)
+    assert st.status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(first, (st.dqkv, st.o, st.lse)))
