@@ -16,10 +16,11 @@ class PackedStep:
     """Buffers and the launch sequence of a layer's step for N token rows in up to R sequences."""
 
     def __init__(self, N: int, R: int, Hq: int, Hkv: int, D: int, window: int = 0, rope=None, norm: bool = False,
-                 eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+                 eps: float = 1e-6, dtype=torch.bfloat16, device="cuda", plan_of=None):
         """window: keys that a query sees at most (0: all before it). rope: a Rope, whose positions the calls then take.
         norm: queries and keys pass a root-mean-square norm per head first, with weights that the calls take (needs a
-        rope; Rope(0) turns nothing)."""
+        rope; Rope(0) turns nothing). plan_of: another PackedStep of the same sizes and window, another layer's, whose plan
+        this one reads: a batch is planned once, by plan() of either. Each layer's step keeps its own results and workspace."""
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"PackedStep: rows are bf16 or fp16, not {dtype}")
         if norm and rope is None:
@@ -47,16 +48,22 @@ class PackedStep:
         if norm:
             self.dwq, self.dwk = (torch.zeros(D, dtype=torch.float32, device=dev) for _ in range(2))
             self.ws_rope = rope.workspace(N, Hq, Hkv, D)
-        self.plan_buf = workspace(nbytes, dev)
+        if plan_of is not None:
+            mine = (N, R, Hq, Hkv, window, dev)
+            theirs = (plan_of.N, plan_of.R, plan_of.Hq, plan_of.Hkv, plan_of.window, plan_of.device)
+            if mine != theirs:
+                raise ValueError(f"PackedStep: a plan of (tokens, sequences, query heads, key heads, window, device) {theirs} "
+                                 f"is none of {mine}")
+        self.plan_buf = workspace(nbytes, dev) if plan_of is None else plan_of.plan_buf
         self.count = self.plan_buf[4:8].view(torch.int32)  # tokens of the batch, by the plan; 0 if it is refused
         self.ws = workspace(nws, dev)
-        for b in (self.plan_buf, self.ws):
+        for b in (self.ws,) if plan_of is not None else (self.plan_buf, self.ws):
             b[:4].zero_()  # the status word: nothing has run yet
 
     def plan(self, starts, stream=None):
         """The batch's sequences: starts [R + 1] int32, from 0; tokens starts[r] .. starts[r + 1] are sequence r (a shorter
         batch repeats its end). To be called before the first step and whenever `starts` changes; one plan serves any
-        number of layers' steps. Starts that fall, leave the N rows or do not begin at 0 show in status(), and steps
+        number of layers' steps (plan_of). Starts that fall, leave the N rows or do not begin at 0 show in status(), and steps
         then write no row (dwq and dwk, sums over no rows, become zero)."""
         if starts.numel() != self.R + 1:
             raise ValueError(f"PackedStep.plan: {self.R + 1} starts expected, got {starts.numel()}")

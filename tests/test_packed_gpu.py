@@ -665,3 +665,29 @@ def test_step_leaves_gradients_of_a_refused_batch_alone(scfa, starts):
     st.run(*args)
     assert st.status() == 0
     assert all(torch.equal(a, b) for a, b in zip(first, (st.dqkv, st.o, st.lse)))
+
+
+def test_layers_share_a_plan(scfa):
+    """Forwards of all layers, then their backwards, on one plan: the bits of steps with plans of their own; and the next
+    batch by one plan() for both."""
+    (a, args), (alone, _) = packed_step(), packed_step()
+    b, _ = packed_step(plan_of=a)
+    other = (*(t.flip(0) for t in args[:4]), *args[4:])
+    for starts in ([0, 20, 40], [0, 3, 37]):
+        a.plan(i32(starts))
+        a.forward(*args[:3], *args[4:])
+        b.forward(*other[:3], *other[4:])
+        b.backward(*other)
+        a.backward(*args)
+        assert a.status() == 0 and b.status() == 0
+        alone.plan(i32(starts))
+        for st, x in ((a, args), (b, other)):
+            alone.run(*x)
+            n = starts[-1]
+            assert all(torch.equal(getattr(st, key)[:n], getattr(alone, key)[:n]) for key in ("o", "lse", "dqkv"))
+            assert torch.equal(st.dwq, alone.dwq) and torch.equal(st.dwk, alone.dwk)
+    b.plan(i32([0, 41, 40]))
+    assert a.status() == 1
+    for kw in (dict(N=41), dict(R=3), dict(Hq=2), dict(window=7)):
+        with pytest.raises(ValueError, match="plan"):
+            packed_step(plan_of=a, **kw)
