@@ -57,14 +57,15 @@ class PackedStep:
         self.plan_buf = workspace(nbytes, dev) if plan_of is None else plan_of.plan_buf
         self.count = self.plan_buf[4:8].view(torch.int32)  # tokens of the batch, by the plan; 0 if it is refused
         self.ws = workspace(nws, dev)
-        for b in (self.ws,) if plan_of is not None else (self.plan_buf, self.ws):
-            b[:4].zero_()  # the status word: nothing has run yet
+        self.ws[:4].zero_()  # the status word: nothing has run yet
+        if plan_of is None:
+            self.plan_buf[:256].zero_()  # no plan, whatever the memory held: steps before plan() are refused
 
     def plan(self, starts, stream=None):
         """The batch's sequences: starts [R + 1] int32, from 0; tokens starts[r] .. starts[r + 1] are sequence r (a shorter
-        batch repeats its end). To be called before the first step and whenever `starts` changes; one plan serves any
-        number of layers' steps (plan_of). Starts that fall, leave the N rows or do not begin at 0 show in status(), and steps
-        then write no row (dwq and dwk, sums over no rows, become zero)."""
+        batch repeats its end). To be called before the first step, which is refused otherwise, and whenever `starts`
+        changes; one plan serves any number of layers' steps (plan_of). Starts that fall, leave the N rows or do not begin
+        at 0 show in status(), and steps then write no row (dwq and dwk, sums over no rows, become zero)."""
         if starts.numel() != self.R + 1:
             raise ValueError(f"PackedStep.plan: {self.R + 1} starts expected, got {starts.numel()}")
         scfa_packed_plan_self(starts, self.N, self.Hq, self.Hkv, self.window, self.plan_buf, stream)

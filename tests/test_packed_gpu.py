@@ -691,3 +691,21 @@ def test_layers_share_a_plan(scfa):
     for kw in (dict(N=41), dict(R=3), dict(Hq=2), dict(window=7)):
         with pytest.raises(ValueError, match="plan"):
             packed_step(plan_of=a, **kw)
+
+
+def test_step_before_its_plan_computes_nothing(scfa, monkeypatch):
+    """Also on memory that holds the plan of a step that is gone."""
+    from sparse_causal_flash_gb300 import packed
+    st, _ = packed_step()
+    st.plan(i32([0, 20, 40]))
+    plan = st.plan_buf
+    monkeypatch.setattr(packed, "workspace", lambda n, dev: plan.clone() if n == plan.numel() else scfa.workspace(n, dev))
+    st, args = packed_step()
+    assert st.status() == 0
+    for _ in range(2):
+        st.run(*args)
+        assert st.status() == 1
+        assert not st.o.any() and not st.lse.any() and not st.dqkv.any() and not st.dwq.any()
+    st.plan(i32([0, 20, 40]))
+    st.run(*args)
+    assert st.status() == 0 and bool(st.o.any())
