@@ -514,8 +514,9 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  * (scfa_packed_workspace_size; one for a backward serves a forward too) holds
  * nothing from call to call; a plan for other
  * sizes raises SCFA_ERR_INVALID in its status word. Results are the same bits on
- * every run. A row of q, k or v that is not finite may reach any row of its own
- * sequence and key head, and no other. Weights and their gradients dS are
+ * every run. A row of q, k, v, o or dO that is not finite may reach any row of its
+ * own sequence and key head, and no other; one of a query that sees nothing
+ * reaches none. Weights and their gradients dS are
  * rounded to the rows' type for their products, in fp16 times powers of two that
  * are taken out again, so that gradients of any size keep their digits; results
  * that fp16 cannot hold (above 65,504, below 2^-24) are infinite or zero. The

@@ -668,12 +668,12 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       int k_it = 0, q_it = 0, do_it = 0, st_it = 0, tails[2] = {0, 0}, unmarked[2] = {-1, -1};
       uint64_t* const st_land = F16 ? sm.st_raw : sm.st_full;
       bool ok = true;
-      // Q or dO tile of query tile i into its ring; rows behind the sequence's
-      // last, up to the last MMA step's end, become zero
+      // Q or dO tile of query tile i into its ring. Rows behind the sequence's last, up to the last MMA step's end, become
+      // zero, and those of queries that see nothing (before the first key): their P and dS are zero, 0 x NaN is not
       auto load = [&](int which, const CUtensorMap* map, uint8_t (*ring)[kSubs][kPackSub], uint64_t* full, uint64_t* empty, int& n, int stages,
-                      int head, const PackEntry& e, int i) -> bool {
+                      int head, const PackEntry& e, int i, int blind) -> bool {
         const int s = n % stages, rows = min(p.tpt, e.m - i * p.tpt) * p.G;
-        const bool cut = rows < used && (rows & 15) != 0;
+        const bool cut = (rows < used && (rows & 15) != 0) || blind > 0;
         if (!warp_wait(&empty[s], ((n / stages) & 1) ^ 1, abort_flag, p.status)) return false;
         if (lane == 0) {
           uint64_t* const bar = cut ? &sm.tail[which] : &full[s];
@@ -688,7 +688,8 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
             unmarked[which] = n - 1;
             return false;
           }
-          zero_tile_rows(ring[s][0], kSubs, rows, (rows + 15) & ~15, lane, 32);
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) zero_tile_rows(ring[s][0], kSubs, part ? 0 : rows, part ? blind : (rows + 15) & ~15, lane, 32);
           fence_proxy_async_smem();
           warp_arrive(&full[s]);
         }
@@ -718,10 +719,11 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           }
           ++k_it;
         }
-        for (int i = a; i < b && ok; ++i) {
-          ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, kQs, head, e, i);
+        int blind = max(-e.shift - a * p.tpt, 0) * p.G;  // (a piece's first tile alone may have such rows)
+        for (int i = a; i < b && ok; ++i, blind = 0) {
+          ok = load(0, &tm_q, sm.q, sm.q_full, sm.q_empty, q_it, kQs, head, e, i, blind);
           if (!ok) break;
-          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i);
+          ok = load(1, &tm_do, sm.dO, sm.do_full, sm.do_empty, do_it, kOs, head, e, i, blind);
           if (!ok) break;
           const int s = st_it % kStatStages;
           ok = warp_wait(&sm.st_empty[s], ((st_it / kStatStages) & 1) ^ 1, abort_flag, p.status);

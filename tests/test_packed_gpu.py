@@ -709,3 +709,24 @@ def test_step_before_its_plan_computes_nothing(scfa, monkeypatch):
     st.plan(i32([0, 20, 40]))
     st.run(*args)
     assert st.status() == 0 and bool(st.o.any())
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([(200, 90), (40, 40)], 3, 1), ([(150, 7), (129, 128)], 4, 2), ([(300, 20)], 1, 1),
+                                         ([(20, 3)], 8, 1)])
+def test_queries_that_see_nothing_pass_no_gradient(scfa, lens, Hq, Hkv, D, dt):
+    """Also where their rows of q and dO are not finite."""
+    p = Problem(scfa, lens, Hq, Hkv, D, dt, seed=21)
+    bad = []
+    for (n, m), (a, _) in zip(lens, p.seqs()):
+        bad.append(slice(a.start, a.start + max(0, n - m)))
+        p.q[bad[-1]], p.do[bad[-1]] = float("nan"), float("inf")
+    p.forward()
+    p.backward()
+    assert p.status() == 0
+    for b in bad:
+        assert not p.o[b].any() and bool(torch.isneginf(p.lse[b]).all()) and not p.dq[b].any()
+        p.q[b] = p.do[b] = 0.0  # what the oracle may multiply by its zeros
+    p.check_forward()
+    p.check_backward()
