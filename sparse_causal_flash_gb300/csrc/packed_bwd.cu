@@ -230,7 +230,9 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Nothing here needs the dK / dV kernel: these CTAs come as its CTAs leave, and fill its last round. They end behind it,
-  // so that what follows this kernel follows both.
+  // so that what follows this kernel follows both. What is needed is the statistics kernel's: the dK / dV kernel has waited
+  // for its end, and so for its writes in L2, before any of these CTAs could start. A kernel in between promises nothing
+  // about L1, so all that comes from there is read past it (__ldcg, and an atomic for the counter).
   grid_release();
   if (bwd_plan_status(p) != SCFA_OK) {  // (the first kernel has said so)
     grid_wait();
@@ -441,8 +443,8 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const bool valid = r_tok < n_tok;
       const int hi = valid ? first + r_tok : -1;
       const long long at = (static_cast<long long>(e.tile0) * p.Hkv + head) * kTile + r;
-      float nl = p.stats[at], down = 1.f;
-      const float nd = p.stats[n_stats + at];
+      float nl = __ldcg(p.stats + at), down = 1.f;
+      const float nd = __ldcg(p.stats + n_stats + at);
       if (F16) {  // dS is held times 2^k = 1 / down: a row's own, in its exponent, from which P's 2^10 is taken again
         const float o2 = __ldcg(p.stats + 2 * n_stats + at / (kTile / kDoUnits));
         if (!warp_wait(&sm.v_known[slot], (it / kSlots) & 1, abort_flag, p.status)) break;

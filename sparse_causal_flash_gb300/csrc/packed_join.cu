@@ -20,9 +20,9 @@ __device__ __forceinline__ void put4(uint16_t* dst, float4 a, float f) {
 template <int D, bool F16, bool BACK>
 __global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const __grid_constant__ PackJoin j) {
   constexpr int L = D / 4;  // lanes of a row
-  grid_wait();
+  grid_wait();  // (the shares of a kernel two before, and the status, are read past L1)
   const PackHeader* const h = reinterpret_cast<const PackHeader*>(j.plan);
-  if (pack_plan_status(h, j.plan_bytes, j.N, j.M, j.Hq, j.Hkv) != SCFA_OK || *j.status != SCFA_OK) return;
+  if (pack_plan_status(h, j.plan_bytes, j.N, j.M, j.Hq, j.Hkv) != SCFA_OK || __ldcg(j.status) != SCFA_OK) return;
   const int lane = threadIdx.x % L;
   const uint32_t step = gridDim.x * (kJoinThreads / L), first = blockIdx.x * (kJoinThreads / L) + threadIdx.x / L;
 #pragma unroll 1
