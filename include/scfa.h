@@ -521,7 +521,9 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  * are taken out again, so that gradients of any size keep their digits; results
  * that fp16 cannot hold (above 65,504, below 2^-24) are infinite or zero. The
  * forward's weights below 2^-24 of the largest of their row are zero in fp16
- * (its lse has them). flags: SCFA_FLAG_DEBUG_SYNC,
+ * (its lse has them). The backward recomputes weights from lse, an fp32 number:
+ * each is off by up to 2^-22 |lse| of itself, all of a row by the same (1% at
+ * |lse| = 40,000). flags: SCFA_FLAG_DEBUG_SYNC,
  * SCFA_FLAG_DEBUG_STALL.
  * ------------------------------------------------------------------------- */
 size_t scfa_packed_plan_size(int N, int M, int R, int Hq, int Hkv);

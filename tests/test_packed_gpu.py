@@ -730,3 +730,29 @@ def test_queries_that_see_nothing_pass_no_gradient(scfa, lens, Hq, Hkv, D, dt):
         p.q[b] = p.do[b] = 0.0  # what the oracle may multiply by its zeros
     p.check_forward()
     p.check_backward()
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("scale_up", [300.0, 30000.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_of_scores_far_from_zero(scfa, monkeypatch, dt, scale_up, D):
+    """The forward's test of far scores, backward. The scores are exact here (one q, keys of +-1). A weight is recomputed from
+    the stored lse: four roundings (lse from log2 units, its storage, log2(e), the way back) of at most 2^-24 |lse| each
+    are 2^-22 |lse| of the weight."""
+    n = 150
+    p = Problem(scfa, same([n]), 2, 1, D, dt, seed=6)
+    p.q.fill_(1.0)
+    p.k.copy_(torch.sign(rand(1, (n, 1, D), dt)))
+    p.k[7], p.k[3] = 1.0, 1.0
+    p.q.mul_(scale_up / 8)
+    p.forward()
+    p.backward()
+    assert p.status() == 0
+    whole = parts
+
+    def exact_scores(q, k, scale, window, lse_given):
+        w, lse, _, top = whole(q, k, scale, window, lse_given)
+        return w, lse, np.broadcast_to(2.0 ** -20 + 2.0 ** -22 * np.abs(lse)[:, None], w.shape), top
+
+    monkeypatch.setitem(globals(), "parts", exact_scores)
+    p.check_backward()
