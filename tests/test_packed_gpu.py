@@ -756,3 +756,31 @@ def test_gradients_of_scores_far_from_zero(scfa, monkeypatch, dt, scale_up, D):
 
     monkeypatch.setitem(globals(), "parts", exact_scores)
     p.check_backward()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_key_heads_are_copies_of_theirs(scfa, D):
+    """o and lse bit by bit: a row's products, maxima and sums run over the same key tiles in the same order, whatever rows
+    stand beside it (keys of tiles that it does not see add zeros). dk and dv of a shared head are the sums over its
+    query heads: each side rounds once (u), the sums differ in order by n G 2^-23 of the magnitudes."""
+    lens = same([200, 61])
+    p, r = Problem(scfa, lens, 4, 2, D, seed=10), Problem(scfa, lens, 4, 4, D, seed=10)
+    r.q.copy_(p.q), r.do.copy_(p.do)
+    r.k.copy_(p.k.repeat_interleave(2, 1)), r.v.copy_(p.v.repeat_interleave(2, 1))
+    for x in (p, r):
+        x.forward()
+        x.backward()
+        assert x.status() == 0
+    assert torch.equal(p.o, r.o) and torch.equal(p.lse, r.lse) and torch.equal(p.dq, r.dq)
+    for key in ("dk", "dv"):
+        one, two = dbl(getattr(p, key)), dbl(getattr(r, key))
+        heads = two.reshape(*two.shape[:1], 2, 2, D)
+        mags = np.zeros_like(one)
+        for a, b in p.seqs():
+            for h in range(4):
+                q, k, v, do, o = (dbl(x) for x in (p.q[a, h], p.k[b, h // 2], p.v[b, h // 2], p.do[a, h], p.o[a, h]))
+                w, _ = op.weights(q, k, p.scale)
+                ds = np.abs(w * (do @ v.T - (do * o).sum(1, keepdims=True)))
+                mags[b, h // 2] += w.T @ np.abs(do) if key == "dv" else p.scale * (ds.T @ np.abs(q))
+        bound = half_step(one, BF) + half_step(heads[:, :, 0], BF) + half_step(heads[:, :, 1], BF) + 1.01 * 400 * 2.0 ** -23 * mags
+        assert np.all(np.abs(one - heads.sum(2)) <= bound)
