@@ -62,11 +62,9 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// maximum of three. Written as two fmaxf so that the compiler picks the
-// instruction: a hand-written three-input max.f32 on scores fresh from a TMEM
-// load returned stale values in the softmax loop (a row whose every key was
-// masked got a tiny denormal instead of -inf as its tile maximum), which made
-// the low bits of O and LSE depend on the launch.
+// maximum of three, as two fmaxf, from which the compiler picks the instruction. (The three-input max.f32 written by hand is
+// as good behind tmem_ld_fence(). Before that fence was there it was scheduled above the wait for its TMEM load and took
+// values that had not arrived: a row whose every key was masked got a tiny denormal as its maximum instead of -inf.)
 __device__ __forceinline__ float max3f(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // packed pairs of f32: one instruction does two lanes' worth of FMA / add / mul

@@ -296,6 +296,8 @@ __device__ __forceinline__ void leave_part(float* mine, const uint32_t (&acc)[16
       *reinterpret_cast<float2*>(mine + (row + 8 * u) * D + 8 * i + c0) =
           make_float2(__uint_as_float(acc[i * 4 + 2 * u]) * (TIMES ? f[u] : 1.f), __uint_as_float(acc[i * 4 + 2 * u + 1]) * (TIMES ? f[u] : 1.f));
 }
+// The largest of three, one instruction. Scores from TMEM pass tmem_ld_fence() before they come here: to the compiler they are
+// there as soon as their load is issued, and it may put this asm above the wait for it.
 __device__ __forceinline__ float pack_max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));

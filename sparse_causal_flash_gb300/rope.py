@@ -7,7 +7,8 @@ cache.KVCache4 at given ones). Contexts longer than the trained one are reached 
             by `stretch`;
   "parts"   pairs that turn more than `fast` times over the trained length stay, those that turn less than `slow` times are
             divided by `stretch`, those between are blended linearly by their turns; cosines and sines times
-            0.1 ln(stretch) + 1.
+            0.1 ln(stretch) + 1. (Some models' code blends by the pair's number instead, between the pairs that turn `fast`
+            and `slow` times: their frequencies are passed as inv_freq, with the factor.)
 """
 from __future__ import annotations
 
