@@ -51,8 +51,8 @@ class Rope:
             inv_freq, f = rope_frequencies(rot, base, scaling, stretch, trained, slow, fast)
         else:
             inv_freq, f = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu"), 1.0
-            if inv_freq.shape != (rot // 2,):
-                raise ValueError(f"Rope: {rot // 2} frequencies expected, got {tuple(inv_freq.shape)}")
+            if rot < 0 or rot % 2 or inv_freq.shape != (rot // 2,):
+                raise ValueError(f"Rope: {rot} channels to turn need half as many frequencies, got {tuple(inv_freq.shape)}")
         self.rot, self.interleaved = rot, bool(interleaved)
         self.factor = float(f if factor is None else factor)
         self.inv_freq = inv_freq

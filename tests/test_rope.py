@@ -161,3 +161,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(scfa):
         scfa.rope_table([float("nan")], "cpu")
     with pytest.raises(ValueError):
         scfa.rope_table([[1.0]], "cpu")
+
+
+def test_frequencies_of_ones_own_make_pairs(scfa):
+    """Channels that turn are twice the frequencies: an odd number of channels is refused, also with frequencies given."""
+    from sparse_causal_flash_gb300.rope import Rope
+    r = Rope(4, inv_freq=[1.0, 0.5], factor=1.5, device="cpu")
+    assert (r.rot, r.factor, r.table.numel()) == (4, 1.5, 2)
+    for rot, f in ((5, [1.0, 0.5]), (1, []), (-1, [1.0]), (4, [1.0]), (4, [1.0, 0.5, 0.2])):
+        with pytest.raises(ValueError):
+            Rope(rot, inv_freq=f, device="cpu")
