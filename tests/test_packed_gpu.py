@@ -784,3 +784,13 @@ def test_shared_key_heads_are_copies_of_theirs(scfa, D):
                 mags[b, h // 2] += w.T @ np.abs(do) if key == "dv" else p.scale * (ds.T @ np.abs(q))
         bound = half_step(one, BF) + half_step(heads[:, :, 0], BF) + half_step(heads[:, :, 1], BF) + 1.01 * 400 * 2.0 ** -23 * mags
         assert np.all(np.abs(one - heads.sum(2)) <= bound)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_stalled_pipeline_ends_with_a_status_in_fp16(scfa, D):
+    """The warps that prepare dS's scale give up as the others do."""
+    p = Problem(scfa, same([300, 20]) + [(2, 5000)], 4, 2, D, HF)
+    p.forward()
+    p.backward(flags=scfa.FLAG_DEBUG_STALL)
+    assert scfa.scfa_get_device_status(p.ws) == 5
+    p.all()
