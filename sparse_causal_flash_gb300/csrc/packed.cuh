@@ -21,7 +21,9 @@ constexpr float kPackLn2 = 0.6931471805599453f;
 constexpr int kPackSlotsPerSm = 4;
 
 // Work of so many tiles is never cut, so that calls on few rows need no join (7 short texts, in a graph:
-// 9.4 us instead of 10.8 forward, 16.8 instead of 19.0 backward).
+// 9.4 us instead of 10.8 forward, 16.8 instead of 19.0 backward; other numbers were not measured). What is cut depends on the
+// longest range of a tile, which the host does not know: it goes by the rows of the whole call, and larger calls that are
+// not cut either have an empty join behind them (2 to 3.5 us).
 constexpr int kPackNeverCut = 3;
 inline bool pack_may_cut(int N, int M, int tpt, bool backward) {
   return M > kPackNeverCut * kTile || (backward && N > kPackNeverCut * tpt);

@@ -16,13 +16,14 @@
 // rows of the last MMA step zeroed in shared memory where they are summed over.
 //
 // Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
-// MMAs, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
+// MMAs, warp 2 prepares the scales of dS for fp16, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
 // thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of 460). What chunks of cut pieces
 // leave is joined by a kernel behind both, in the order of the chunks.
 //
-// Bounded at D = 128 by the tensor cores (81 and 85% busy), at D = 64 by latency inside the softmax. Measured: 1051 us for
-// 8192 tokens of 32 heads over 8 of 128 channels (1,310 TFLOP/s of useful work; dQ 450, dK and dV 612, statistics 26),
-// 1371 us for 16384 of 16 heads over 4 of 64 (1,000).
+// Bounded at D = 128 by the tensor cores (79 and 85% busy), at D = 64 by latency inside the softmax. Measured in a graph, one
+// call after another: 1,063 us for 8192 tokens of 32 heads over 8 of 128 channels (1,290 TFLOP/s of useful work; dQ 462, dK
+// and dV 611, statistics 26 alone), 1,376 us for 16384 of 16 heads over 4 of 64 (1,000). Called on inputs that change from
+// call to call the first takes 1,190 us (1,150), under the power cap.
 #include <climits>
 #include <type_traits>
 
@@ -70,8 +71,8 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
 // |dP - delta| <= 2 |dO| |V|, so dS stays below 2^14, and is normal down to 2^-24.5 |dO| |V|. Both are powers of two and
 // taken out again in fp32. The statistics kernel finds the lengths, squared: of dO's blocks of eight rows, at most 2^1.5
 // above the longest row's, and of the longest of 16 rows of V. What is not finite counts as nothing there, and spoils what
-// it meets in any case. It costs 3 us of the 14 of the statistics and 1-3% of the other kernels (9 texts of 101 to 3501
-// tokens, 12 heads over 4 of 64 channels: 231 us in a graph instead of 219).
+// it meets in any case. It costs 5 us on the statistics' 14 and 2-3% of the other kernels for 9 texts of 101 to 3501 tokens,
+// 12 heads over 4 of 64 channels (233 us in a graph, 219 unscaled), and 1% of all for 8192 tokens, 32 over 8 of 128.
 constexpr int kPUp = 10, kDsUp = 13;
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
 // k of the squared lengths a (dO), b (V), each 0 or 2^-48 to 2^42

@@ -22,8 +22,10 @@
 // order.
 //
 // Bounded at D = 128 by the chain S, softmax, P V, which two tiles take in turns (tensor cores 72% busy), at D = 64 by
-// latency inside the softmax (no unit above half). Measured: 334 us for 8192 tokens of 32 heads over 8 of 128 channels
-// (1,640 TFLOP/s of useful work), 1224 us for 16384 (1,800), 487 us for 16384 of 16 heads over 4 of 64 (1,130).
+// latency inside the softmax (no unit above half). Measured in a graph, one call after another: 335 us for 8192 tokens of 32
+// heads over 8 of 128 channels (1,640 TFLOP/s of useful work), 484 us for 16384 of 16 heads over 4 of 64 (1,140). Called on
+// inputs that change from call to call the first takes 367 us (1,500), in long runs under the power cap: 1,340 us for 16384
+// tokens (1,640; 1,224 at full clocks).
 #include <climits>
 #include <type_traits>
 
