@@ -518,7 +518,8 @@ scfa_status scfa_rope_bwd(const uint16_t* dq, long long dq_token, long long dq_h
  * own sequence and key head, and no other; one of a query that sees nothing
  * reaches none. Weights and their gradients dS are
  * rounded to the rows' type for their products, in fp16 times powers of two that
- * are taken out again, so that gradients of any size keep their digits; results
+ * are taken out again, so that gradients of any size keep their digits (a row's
+ * dq for itself, dk beside the longest rows of dO among its queries); results
  * that fp16 cannot hold (above 65,504, below 2^-24) are infinite or zero. The
  * forward's weights below 2^-24 of the largest of their row are zero in fp16
  * (its lse has them). The backward recomputes weights from lse, an fp32 number:

@@ -108,8 +108,8 @@ struct PackWs {
   size_t counters = 0;          // ints: next item of each kernel
   size_t part = 0, part_q = 0;  // fp32, [slot][Hkv]: two tiles of D + 2 columns, or dV and dK; (backward) dQ
   size_t forward = 0;           // what a forward needs
-  size_t stats = 0;             // backward: [2][query tiles][Hkv][128] floats, then for fp16 the largest rows (packed_bwd.cu):
-                                // [query tiles][Hkv][16] of dO, [key tiles][Hkv][8] of V
+  size_t stats = 0;             // backward: [2][query tiles][Hkv][128] floats, then for fp16 lengths of rows (packed_bwd.cu):
+                                // [query tiles][Hkv][128] and [..][16] of dO, [key tiles][Hkv][8] of V
   size_t clear = 0;             // bytes from the start that a call clears
 };
 // A backward's workspace serves a forward too.
@@ -125,7 +125,7 @@ inline PackWs pack_ws(int D, int sms) {
 }
 constexpr int kDoUnits = 16, kVUnits = 8;  // a tile's pieces of 8 and 16 rows
 __host__ __device__ __forceinline__ long long pack_stats_bytes(long long q_tiles, int M, int R, int Hkv) {
-  return (q_tiles * (2 * kTile + kDoUnits) + (static_cast<long long>(M / kTile) + R) * kVUnits) * Hkv * static_cast<long long>(sizeof(float));
+  return (q_tiles * (3 * kTile + kDoUnits) + (static_cast<long long>(M / kTile) + R) * kVUnits) * Hkv * static_cast<long long>(sizeof(float));
 }
 // Number of key tile i (of the sequence seq, whose keys start at row k0) among less than M / 128 + R: sequences of m keys
 // leave room for as many tiles as they may have.

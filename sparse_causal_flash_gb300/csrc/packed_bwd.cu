@@ -16,9 +16,9 @@
 // rows of the last MMA step zeroed in shared memory where they are summed over.
 //
 // Both kernels: one CTA per SM, pieces of work from a counter, longest first; warp 0 copies (TMA), warp 1 issues the
-// MMAs, warp 2 prepares the scales of dS for fp16, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread = TMEM lane; with 32 columns a
-// thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of 460). What chunks of cut pieces
-// leave is joined by a kernel behind both, in the order of the chunks.
+// MMAs, warp 2 prepares the scales of dS for fp16, warps 4-7 and 8-11 take 64 columns each of a 128 x 128 tile (thread =
+// TMEM lane; with 32 columns a thread in 16 warps the kernels issue a third more instructions: dQ took 539 us instead of
+// 460). What chunks of cut pieces leave is joined by a kernel behind both, in the order of the chunks.
 //
 // Bounded at D = 128 by the tensor cores (79 and 85% busy), at D = 64 by latency inside the softmax. Measured in a graph, one
 // call after another: 1,063 us for 8192 tokens of 32 heads over 8 of 128 channels (1,290 TFLOP/s of useful work; dQ 462, dK
@@ -47,7 +47,7 @@ struct PBwdParams {
   const float* lse;
   uint16_t *dq, *dk, *dv;
   long long dqt, dqh, dkt, dkh, dvt, dvh;
-  float* stats;             // [2][tiles][Hkv][128] and, for fp16, the largest rows
+  float* stats;             // [2][tiles][Hkv][128] and, for fp16, lengths of rows
   long long stats_bytes;    // room for them
   int* counter;
   float *part, *part_q;     // chunks' shares of dV and dK, and of dQ
@@ -66,16 +66,16 @@ __device__ __forceinline__ int bwd_plan_status(const PBwdParams& p) {
 // A weight over n flat keys is 1 / n and dS = P (dP - delta) may be any size, while fp16 has normal numbers from 2^-14 to
 // 2^16 only: as they are, weights over 16,384 keys and dS of a dO of 0.001 over 2,000 lose their digits, and a dO of
 // thousands leaves infinities. So for fp16 P is held times 2^10 (normal from 2^-24 up; it is at most 1, and room for 2^6
-// is left to an lse that is far from zero), and dS times 2^k, with 2^10.5 <= 2^k |dO| |V| <= 2^13 for the longest rows of
-// dO and V that meet in a piece of work (dK, dV), or for a query's block of eight rows and the V that its piece meets (dQ).
-// |dP - delta| <= 2 |dO| |V|, so dS stays below 2^14, and is normal down to 2^-24.5 |dO| |V|. Both are powers of two and
-// taken out again in fp32. The statistics kernel finds the lengths, squared: of dO's blocks of eight rows, at most 2^1.5
-// above the longest row's, and of the longest of 16 rows of V. What is not finite counts as nothing there, and spoils what
+// is left to an lse that is far from zero), and dS times 2^k, with 2^12 <= 2^k |dO| |V| <= 2^13 for the query's own row and
+// the longest V row that its piece of work meets (dQ), or for the longest rows of dO and V that meet in a piece (dK, dV).
+// |dP - delta| <= 2 |dO| |V|, so dS stays below 2^14, and is normal down to 2^-26 |dO| |V|. Both are powers of two and
+// taken out again in fp32. The statistics kernel finds the lengths, squared: of each row of dO, of the longest of eight, and
+// of the longest of 16 rows of V. What is not finite counts as nothing there, and spoils what
 // it meets in any case. It costs 5 us on the statistics' 14 and 2-3% of the other kernels for 9 texts of 101 to 3501 tokens,
 // 12 heads over 4 of 64 channels (233 us in a graph, 219 unscaled), and 1% of all for 8192 tokens, 32 over 8 of 128.
 constexpr int kPUp = 10, kDsUp = 13;
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
-// k of the squared lengths a (dO), b (V), each 0 or 2^-48 to 2^42
+// k of the squared lengths a (dO), b (V), each 0 or 2^-48 to 2^39
 __device__ __forceinline__ int ds_up(float a, float b) {
   const int e = (__float_as_int(a * b) >> 23) - 127;  // |dO| |V| < 2^((e + 1) / 2)
   return kDsUp - ((e + 2) >> 1);
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 6 : 4) packed_stats_kernel(cons
         lse[i] = p.lse[static_cast<long long>(t.x + tok) * p.Hq + qh];
       }
     }
-    float block = 0.f;
+    float longest = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const uint32_t aw[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
@@ -144,25 +144,29 @@ __global__ void __launch_bounds__(256, D == 64 ? 6 : 4) packed_stats_kernel(cons
         if (F16) sq = fmaf(y.x, y.x, fmaf(y.y, y.y, sq));
       }
 #pragma unroll
-      for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (F16 && lse[i] != -INFINITY) block += finite_or_zero(sq);
+      for (int o = L / 2; o; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (F16) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      }
+      if (F16) sq = lse[i] == -INFINITY ? 0.f : finite_or_zero(sq), longest = fmaxf(longest, sq);
       if (ch == 0) {
         const long long at = static_cast<long long>(unit) * kRows + i * RW + lane / L;
         // a row that sees nothing, or is none, weighs nothing: P = 2^(-inf)
         p.stats[at] = lse[i] == -INFINITY ? -INFINITY : F16 ? fmaf(-lse[i], kPackLog2e, static_cast<float>(kPUp)) : -(lse[i] * kPackLog2e);
         p.stats[n + at] = lse[i] == -INFINITY ? 0.f : -s;
+        if (F16) p.stats[2 * n + at] = sq;
       }
     }
     if (F16) {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) block += __shfl_xor_sync(0xffffffffu, block, o);
-      if (lane == 0) p.stats[2 * n + unit] = block;
+      for (int o = L; o < 32; o <<= 1) longest = fmaxf(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+      if (lane == 0) p.stats[3 * n + unit] = longest;
     }
   }
   if (F16) {  // 16 rows of a key tile of V a warp at a time
     constexpr int kVRows = kTile / kVUnits, kVSteps = kVRows / RW;
     const PackEntry* const tiles_v = reinterpret_cast<const PackEntry*>(p.plan + h->entries[kListDkv]);
-    float* const big_v = p.stats + 2 * n + units;
+    float* const big_v = p.stats + 3 * n + units;
     const long long n_v = static_cast<long long>(h->n_entries[kListDkv]) * p.Hkv * kVUnits;
     // (counted from the grid's middle: in small calls by CTAs that have nothing to do above and run at the same time)
     for (long long x = ((blockIdx.x + gridDim.x / 2) % gridDim.x) * (blockDim.x / 32) + (threadIdx.x >> 5); x < n_v; x += step) {
@@ -414,7 +418,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     } else if (F16 && warp == 2) {
       // ---------------------------------------------------------- the longest V rows, ahead of the softmax
-      const float* const big_v = p.stats + 2 * n_stats + n_stats / (kTile / kDoUnits);
+      const float* const big_v = p.stats + 3 * n_stats + n_stats / (kTile / kDoUnits);
       for (int it = 0;; ++it) {
         const int slot = it % kSlots;
         if (!warp_wait(&sm.item_full[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
@@ -447,7 +451,7 @@ packed_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       float nl = __ldcg(p.stats + at), down = 1.f;
       const float nd = __ldcg(p.stats + n_stats + at);
       if (F16) {  // dS is held times 2^k = 1 / down: a row's own, in its exponent, from which P's 2^10 is taken again
-        const float o2 = __ldcg(p.stats + 2 * n_stats + at / (kTile / kDoUnits));
+        const float o2 = __ldcg(p.stats + 2 * n_stats + at);
         if (!warp_wait(&sm.v_known[slot], (it / kSlots) & 1, abort_flag, p.status)) break;
         const int k = ds_up(o2, sm.v_longest[slot]);
         nl += static_cast<float>(k - kPUp), down = pow2(-k);
@@ -836,7 +840,7 @@ packed_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       // ---------------------------------------------------------- what dS is held times, and -delta times that, ahead of the
       // softmax (which did both by itself at first: 244 us instead of 219 unscaled for 9 texts of 101 to 3501 tokens, 12 heads
       // over 4 of 64 channels)
-      const float* const big_do = p.stats + 2 * n_stats;
+      const float* const big_do = p.stats + 3 * n_stats;
       const float* const big_v = big_do + n_stats / (kTile / kDoUnits);
       int t = 0;
       bool ok = true;

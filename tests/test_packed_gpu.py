@@ -794,3 +794,25 @@ def test_a_stalled_pipeline_ends_with_a_status_in_fp16(scfa, D):
     p.backward(flags=scfa.FLAG_DEBUG_STALL)
     assert scfa.scfa_get_device_status(p.ws) == 5
     p.all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_fp16_query_gradients_beside_far_larger_ones(scfa, monkeypatch, D):
+    """Rows of dO that are 2^20 apart, token by token and head by head, over flat rows: each row of dQ is held to its own
+    size. Its dS moves by at most 2^-25 / 2^k <= 2^-37 |dO| |V| below the normal numbers, with the row's own |dO|."""
+    p = Problem(scfa, same([1200, 5]), 4, 2, D, HF, seed=24, q_scale=0.1)
+    p.k.mul_(0.1)
+    p.scale = 8.0
+    big = torch.arange(p.N, device="cuda")[:, None] * 3 + torch.arange(4, device="cuda") * 5
+    p.do.copy_((p.do.float() * torch.where(big % 7 < 3, 1000.0, 1000.0 * 2.0 ** -20)[..., None]).to(HF))
+    p.forward()
+    p.backward()
+    assert p.status() == 0
+    v_long = float(torch.linalg.vector_norm(p.v.double(), dim=-1).max())
+    monkeypatch.setitem(globals(), "tiny", lambda dt: 0.0)
+    for a, b in p.seqs():
+        for h in range(4):
+            k, v, do = dbl(p.k[b, h // 2]), dbl(p.v[b, h // 2]), dbl(p.do[a, h])
+            (ref, size), _, _ = grad_bounds(dbl(p.q[a, h]), k, v, do, dbl(p.o[a, h]), p.scale, 0, HF)
+            low = 2.0 ** -37 * v_long * np.linalg.norm(do, axis=1)[:, None] * p.scale * (op.mask(len(do), len(k)) @ np.abs(k))
+            check("dq", dbl(p.dq[a, h]), ref, (size + low) * 1.01 + half_step(ref, HF))
